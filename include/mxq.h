@@ -61,9 +61,12 @@ typedef enum mxq_status {
 #define MXQ_DEVERR_SCALE 0x2     /* an FP32 scale that is not a power of two in range */
 #define MXQ_DEVERR_SLOT 0x4      /* a KV-cache slot at or beyond the number of cache rows */
 
-/* Cache element types of mxq_rope_kv_insert. */
+#define MXQ_DEVERR_LENGTH 0x8    /* a sequence length outside the block table's reach */
+
+/* Cache element types of mxq_rope_kv_insert and mxq_attn. */
 #define MXQ_CACHE_E4M3 0 /* OCP E4M3 bytes with one per-tensor FP32 scale */
 #define MXQ_CACHE_BF16 1 /* BF16 */
+#define MXQ_CACHE_E2M1 2 /* 4 bits (mxq_attn only): written by mxq_rope_kv4_insert */
 
 /* Human-readable name of a status code.  Never NULL. */
 const char* mxq_status_string(int status);
@@ -285,6 +288,99 @@ int mxq_rope_kv_insert(const void* q_bf16, void* q_out_bf16, int64_t T, int32_t 
                        const int64_t* slot_mapping, void* kv_cache, int64_t num_slots,
                        int32_t cache_dtype, const float* kv_scale, int32_t* err_flag,
                        mxq_stream_t stream);
+
+/*
+ * mxq_rope_kv_insert with a KV cache held in 4 bits (the pages have no
+ * counterpart).  The rotation, the query output, pos/cos/sin, slot_mapping
+ * and err_flag are those of mxq_rope_kv_insert; only what a KV row is stored
+ * as differs:
+ *
+ *  cache      [num_slots, Dk/2] bytes: E2M1 codes, element 2i in the low and
+ *             2i+1 in the high nibble of byte i (values 0, 0.5, 1, 1.5, 2, 3,
+ *             4, 6 and their negatives).
+ *  cache_sf   [num_slots, Dk/32] E8M0 bytes, one per 32 consecutive values.
+ *
+ * Per 32 values (amax over the fp32 rotated values): e = smallest integer
+ * with amax <= 6 * 2^e, clamped to [-127, 127] (amax == 0 gives -127); scale
+ * byte e + 127; code = E2M1 round-to-nearest-even, saturating, of y * 2^-e.
+ * A block with a NaN or an infinity gets scale byte 0xFF (NaN).
+ * Dk % 32 == 0, Dk >= 32; cache 16-byte aligned.  Other limits as
+ * mxq_rope_kv_insert.
+ */
+int mxq_rope_kv4_insert(const void* q_bf16, void* q_out_bf16, int64_t T, int32_t H, int32_t Dq,
+                        const void* kv_bf16, int32_t Dk, const int64_t* pos, const void* cos_bf16,
+                        const void* sin_bf16, int64_t cs_ld, int64_t max_pos, int32_t R,
+                        const int64_t* slot_mapping, uint8_t* cache, uint8_t* cache_sf,
+                        int64_t num_slots, int32_t* err_flag, mxq_stream_t stream);
+
+/*
+ * Rows of a 4-bit cache as BF16: out[i] = the Dk values of cache row
+ * slots[i], exact (a magnitude past BF16's largest becomes infinity, scale
+ * byte 0xFF NaN).  slots [n] int64; a negative slot gives a row of zeros, and
+ * so does one at or beyond num_slots, which also sets MXQ_DEVERR_SLOT.
+ * n == 0 is a no-op; n*Dk/8 >= 2^31 returns MXQ_ERR_UNSUPPORTED.
+ */
+int mxq_kv4_gather(const uint8_t* cache, const uint8_t* cache_sf, int64_t num_slots, int32_t Dk,
+                   const int64_t* slots, int64_t n, void* out_bf16, int32_t* err_flag,
+                   mxq_stream_t stream);
+
+/* Workspace bytes mxq_attn needs for these sizes (0 when the keys are not
+ * split over CTAs).  Depends on the sizes alone, not on the device data. */
+size_t mxq_attn_workspace_bytes(int64_t T, int32_t B, int32_t H, int32_t D, int32_t max_pages,
+                                int32_t page_size, int32_t window, int32_t sinks);
+
+/*
+ * Attention over the paged KV cache that mxq_rope_kv_insert or
+ * mxq_rope_kv4_insert fills: causal, with a sliding window and a few first
+ * keys that stay visible.  The pages have no counterpart; it is the step
+ * between the insertion and mxq_wo_a.  A token's key and value are the same
+ * cache row, shared by all H query heads.
+ *
+ *  q_bf16      [T, H, D] BF16: the new tokens of B sequences, one sequence
+ *              after the other, rotated and already inserted in the cache.
+ *  q_start     [B+1] int32, non-decreasing, from 0 to T: sequence b owns the
+ *              tokens q_start[b] .. q_start[b+1]-1 (n_b of them, 0 allowed).
+ *              NULL: one token per sequence (then T == B).  Tokens that no
+ *              sequence owns are not written.
+ *  seq_lens    [B] int32: keys of sequence b, its new tokens included.  The
+ *              i-th new token has position p = seq_lens[b] - n_b + i.
+ *  block_table [B, max_pages] int32: key j of sequence b is cache row
+ *              block_table[b][j / page_size] * page_size + j % page_size.
+ *              page_size % 16 == 0.
+ *  kv_cache    [num_slots, D]: BF16 (MXQ_CACHE_BF16), E4M3 bytes standing for
+ *              code * *kv_scale (MXQ_CACHE_E4M3), or E2M1 codes
+ *              [num_slots, D/2] with cache_sf [num_slots, D/32]
+ *              (MXQ_CACHE_E2M1).  kv_scale / cache_sf are unused (may be
+ *              NULL) for the other types.
+ *  window, sinks
+ *              key j is visible to position p iff j <= p and (window == 0 or
+ *              j > p - window or j < sinks).
+ *  out_bf16    [T, H, D]: sum_j exp(s_j - lse) * k_j over the visible keys,
+ *              s_j = sm_scale * (q . k_j); rounded once to BF16.  The two
+ *              products run on the tensor cores with FP32 accumulation; the
+ *              exponentials are rounded to 16 bits before the second one.
+ *  lse         optional [T, H] FP32: log(sum_j exp(s_j)).
+ *  err_flag    optional int32 device word: MXQ_DEVERR_SLOT when a block-table
+ *              entry that is read lies outside the cache (its keys are
+ *              invisible), MXQ_DEVERR_LENGTH for a length outside
+ *              [0, max_pages * page_size] (it is clamped to that range).
+ *  ws          mxq_attn_workspace_bytes() bytes, 16-byte aligned; calls that
+ *              may run at the same time need distinct workspaces.
+ *
+ * A row that sees no key gets out = 0 and lse = -infinity.  What masked keys
+ * hold (NaN and infinities included) never reaches an output; a visible key
+ * row with a NaN or an infinity makes the rows that see it NaN.  Results do
+ * not depend on timing: no atomics are used on them.
+ * D % 64 == 0, 64 <= D <= 512, 1 <= H <= 4096, B >= 1, sm_scale finite,
+ * window, sinks >= 0.  T == 0 is a no-op.  T*H >= 2^31, max_pages*page_size
+ * >= 2^31 or num_slots >= 2^40 returns MXQ_ERR_UNSUPPORTED.
+ */
+int mxq_attn(const void* q_bf16, int64_t T, int32_t H, int32_t D, const int32_t* q_start,
+             const int32_t* seq_lens, int32_t B, const int32_t* block_table, int32_t max_pages,
+             int32_t page_size, const void* kv_cache, int64_t num_slots, int32_t cache_dtype,
+             const float* kv_scale, const uint8_t* cache_sf, int32_t window, int32_t sinks,
+             float sm_scale, void* out_bf16, float* lse, int32_t* err_flag, void* ws,
+             size_t ws_bytes, mxq_stream_t stream);
 
 /* Size in bytes of the fixed device scratch array behind
  * mxq_linear_noalloc (4 MiB). */

@@ -23,6 +23,7 @@ __all__ = [
     "mxq_dequant_bf16", "mxq_scales_f32_to_e8m0", "mxq_watchdog_read", "mxq_watchdog_selftest",
     "mxq_arch_supported",
     "mxq_version", "mxq_wo_a_workspace_bytes", "mxq_wo_a", "wo_a", "mxq_rope_kv_insert",
+    "mxq_rope_kv4_insert", "mxq_kv4_gather", "mxq_attn_workspace_bytes", "mxq_attn",
     "mxq_debug_set_pair_limit", "mxq_debug_set_lazy_pairs", "mxq_debug_takeovers",
 ]
 
@@ -32,8 +33,10 @@ library_path = os.path.join(HERE, "libmxq.so")
 MXQ_DEVERR_POSITION = 0x1
 MXQ_DEVERR_SCALE = 0x2
 MXQ_DEVERR_SLOT = 0x4
+MXQ_DEVERR_LENGTH = 0x8
 MXQ_CACHE_E4M3 = 0
 MXQ_CACHE_BF16 = 1
+MXQ_CACHE_E2M1 = 2
 
 
 class MxqLibraryError(RuntimeError):
@@ -76,6 +79,12 @@ _SIGNATURES = {
     "mxq_wo_a_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32]),
     "mxq_rope_kv_insert": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _i64,
                                           _i64, _i32, _vp, _vp, _i64, _i32, _vp, _vp, _vp]),
+    "mxq_rope_kv4_insert": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _i64,
+                                           _i64, _i32, _vp, _vp, _vp, _i64, _vp, _vp]),
+    "mxq_kv4_gather": (ctypes.c_int, [_vp, _vp, _i64, _i32, _vp, _i64, _vp, _vp, _vp]),
+    "mxq_attn_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32]),
+    "mxq_attn": (ctypes.c_int, [_vp, _i64, _i32, _i32, _vp, _vp, _i32, _vp, _i32, _i32, _vp, _i64, _i32,
+                                _vp, _vp, _i32, _i32, ctypes.c_float, _vp, _vp, _vp, _vp, _sz, _vp]),
     "mxq_wo_a": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32,
                                 _i32, _vp, _vp, _sz, _vp]),
 }
@@ -333,3 +342,112 @@ def mxq_rope_kv_insert(q, kv, pos, cos, sin, R, slot_mapping, cache, scale=None,
                                   cache.shape[0], dtype, _ptr(scale), _ptr(err_flag), _stream(stream))
     _check("mxq_rope_kv_insert", st)
     return q_out
+
+
+def _tensor(fn, name, t, dtype, shape=None):
+    """Refuses a tensor that is not a contiguous CUDA tensor of this dtype (and shape, None = any size)."""
+    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous()):
+        raise MxqError(fn, 2, f"{name} must be a contiguous CUDA tensor of {dtype}")
+    if shape is not None and (t.dim() != len(shape)
+                              or any(w is not None and w != n for n, w in zip(t.shape, shape))):
+        raise MxqError(fn, 2, f"{name} has shape {tuple(t.shape)}, not {shape}")
+
+
+def mxq_rope_kv4_insert(q, kv, pos, cos, sin, R, slot_mapping, cache, cache_sf, q_out=None,
+                        err_flag=None, stream=None):
+    """mxq_rope_kv_insert with a 4-bit cache: kv bf16 [T, Dk] goes, rotated, to row slot_mapping[t] of
+    cache uint8 [num_slots, Dk/2] (E2M1 codes, two per byte) and cache_sf uint8 [num_slots, Dk/32]
+    (E8M0 scale of each 32 values).  q (or None) and q_out as in mxq_rope_kv_insert; returns q_out."""
+    fn = "mxq_rope_kv4_insert"
+    T, Dk = kv.shape
+    _tensor(fn, "kv", kv, torch.bfloat16)
+    _tensor(fn, "slot_mapping", slot_mapping, torch.int64, (T,))
+    _tensor(fn, "cache", cache, torch.uint8, (None, Dk // 2))
+    _tensor(fn, "cache_sf", cache_sf, torch.uint8, (cache.shape[0], Dk // 32))
+    H = Dq = 0
+    if q is not None:
+        _, H, Dq = q.shape
+        _tensor(fn, "q", q, torch.bfloat16, (T, None, None))
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        _tensor(fn, "q_out", q_out, torch.bfloat16, (T, H, Dq))
+    cs_ld = max_pos = 0
+    if R > 0:
+        _tensor(fn, "pos", pos, torch.int64, (T,))
+        if cos.dtype != torch.bfloat16 or sin.dtype != torch.bfloat16 or cos.stride() != sin.stride() \
+                or cos.stride(1) != 1 or cos.shape != sin.shape or cos.shape[1] < R // 2:
+            raise MxqError(fn, 2, "cos and sin must be bf16 [max_pos, >= R/2] with the same strides")
+        cs_ld, max_pos = cos.stride(0), cos.shape[0]
+    st = lib().mxq_rope_kv4_insert(_ptr(q), _ptr(q_out), T, H, Dq, _ptr(kv), Dk, _ptr(pos), _ptr(cos),
+                                   _ptr(sin), cs_ld, max_pos, R, _ptr(slot_mapping), _ptr(cache),
+                                   _ptr(cache_sf), cache.shape[0], _ptr(err_flag), _stream(stream))
+    _check(fn, st)
+    return q_out
+
+
+def mxq_kv4_gather(cache, cache_sf, slots, out=None, err_flag=None, stream=None):
+    """Rows `slots` (int64 [n]) of a 4-bit cache as bf16 [n, Dk] (zeros for a negative slot)."""
+    fn = "mxq_kv4_gather"
+    Dk, n = cache.shape[1] * 2, slots.numel()
+    _tensor(fn, "cache", cache, torch.uint8)
+    _tensor(fn, "cache_sf", cache_sf, torch.uint8, (cache.shape[0], Dk // 32))
+    _tensor(fn, "slots", slots, torch.int64, (n,))
+    if out is None:
+        out = torch.empty((n, Dk), dtype=torch.bfloat16, device=cache.device)
+    _tensor(fn, "out", out, torch.bfloat16, (n, Dk))
+    _check(fn, lib().mxq_kv4_gather(_ptr(cache), _ptr(cache_sf), cache.shape[0], Dk, _ptr(slots), n,
+                                    _ptr(out), _ptr(err_flag), _stream(stream)))
+    return out
+
+
+def mxq_attn_workspace_bytes(T, B, H, D, max_pages, page_size, window=0, sinks=0):
+    """Workspace bytes of mxq_attn (0 when the keys of a row are not split over CTAs)."""
+    return lib().mxq_attn_workspace_bytes(T, B, H, D, max_pages, page_size, window, sinks)
+
+
+def mxq_attn(q, cache, block_table, seq_lens, q_start=None, page_size=64, window=0, sinks=0,
+             sm_scale=None, kv_scale=None, cache_sf=None, out=None, lse=None, ws=None, err_flag=None,
+             stream=None):
+    """Causal attention of q bf16 [T, H, D] over the paged cache whose rows are key and value at once.
+
+    block_table int32 [B, max_pages], seq_lens int32 [B], q_start int32 [B+1] (None: one token per
+    sequence).  cache: bf16 [num_slots, D]; uint8 [num_slots, D] = E4M3 codes times `kv_scale`
+    (float32 device tensor of one element); uint8 [num_slots, D/2] = E2M1 codes with `cache_sf`
+    uint8 [num_slots, D/32].  A key is visible within `window` positions (0: all) or below `sinks`.
+    sm_scale defaults to D ** -0.5; `lse`, a float32 [T, H] tensor, receives the log of the softmax
+    denominators; `ws` (mxq_attn_workspace_bytes) is allocated when not given.  Returns out bf16 [T, H, D]."""
+    fn = "mxq_attn"
+    T, H, D = q.shape
+    B, max_pages = block_table.shape
+    _tensor(fn, "q", q, torch.bfloat16)
+    _tensor(fn, "block_table", block_table, torch.int32)
+    _tensor(fn, "seq_lens", seq_lens, torch.int32, (B,))
+    if q_start is not None:
+        _tensor(fn, "q_start", q_start, torch.int32, (B + 1,))
+    if cache_sf is not None:
+        dtype = MXQ_CACHE_E2M1
+        _tensor(fn, "cache", cache, torch.uint8, (None, D // 2))
+        _tensor(fn, "cache_sf", cache_sf, torch.uint8, (cache.shape[0], D // 32))
+    elif cache.dtype == torch.uint8:
+        dtype = MXQ_CACHE_E4M3
+        _tensor(fn, "cache", cache, torch.uint8, (None, D))
+        if kv_scale is not None:
+            _tensor(fn, "kv_scale", kv_scale, torch.float32)
+    else:
+        dtype = MXQ_CACHE_BF16
+        _tensor(fn, "cache", cache, torch.bfloat16, (None, D))
+    if out is None:
+        out = torch.empty_like(q)
+    _tensor(fn, "out", out, torch.bfloat16, (T, H, D))
+    if lse is not None:
+        _tensor(fn, "lse", lse, torch.float32, (T, H))
+    if ws is None:
+        need = mxq_attn_workspace_bytes(T, B, H, D, max_pages, page_size, window, sinks)
+        if need > 0:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    st = lib().mxq_attn(_ptr(q), T, H, D, _ptr(q_start), _ptr(seq_lens), B, _ptr(block_table), max_pages,
+                        page_size, _ptr(cache), cache.shape[0], dtype, _ptr(kv_scale), _ptr(cache_sf),
+                        window, sinks, D ** -0.5 if sm_scale is None else sm_scale, _ptr(out), _ptr(lse),
+                        _ptr(err_flag), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream))
+    _check(fn, st)
+    return out

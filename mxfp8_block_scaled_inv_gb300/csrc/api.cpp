@@ -420,6 +420,172 @@ int mxq_rope_kv_insert(const void* q_bf16, void* q_out_bf16, int64_t T, int32_t 
       "rope_kv_insert launch");
 }
 
+int mxq_rope_kv4_insert(const void* q_bf16, void* q_out_bf16, int64_t T, int32_t H, int32_t Dq,
+                        const void* kv_bf16, int32_t Dk, const int64_t* pos, const void* cos_bf16,
+                        const void* sin_bf16, int64_t cs_ld, int64_t max_pos, int32_t R,
+                        const int64_t* slot_mapping, uint8_t* cache, uint8_t* cache_sf,
+                        int64_t num_slots, int32_t* err_flag, mxq_stream_t stream) {
+  if (T < 0 || H < 0 || Dk < 32 || R < 0 || num_slots < 0 || (H > 0 && Dq < 16))
+    return fail(MXQ_ERR_SHAPE, "need T >= 0, H >= 0, Dk >= 32, R >= 0, num_slots >= 0, "
+                               "Dq >= 16 when H > 0 (T=%lld H=%d Dq=%d Dk=%d R=%d)",
+                (long long)T, H, Dq, Dk, R);
+  if (Dk % 32 != 0 || (H > 0 && Dq % 16 != 0))
+    return fail(MXQ_ERR_SHAPE, "need Dk %% 32 == 0 and Dq %% 16 == 0 (Dq=%d Dk=%d)", Dq, Dk);
+  if (R % 16 != 0 || R > Dk || (H > 0 && R > Dq))
+    return fail(MXQ_ERR_UNSUPPORTED, "R must be a multiple of 16, <= Dk and <= Dq (R=%d)", R);
+  if (T >= ((int64_t)1 << 31) ||
+      T * ((int64_t)H * (Dq / 8) + Dk / 8) >= ((int64_t)1 << 31))
+    return fail(MXQ_ERR_UNSUPPORTED, "T*H*Dq/8 + T*Dk/8 must be < 2^31");
+  if (T == 0) return ok();
+  if (R > 0) {
+    if (max_pos < 1 || cs_ld < R / 2)
+      return fail(MXQ_ERR_SHAPE, "need max_pos >= 1 and cs_ld >= R/2 (max_pos=%lld cs_ld=%lld)",
+                  (long long)max_pos, (long long)cs_ld);
+    if (cs_ld % 8 != 0) return fail(MXQ_ERR_ALIGN, "cs_ld %% 8 != 0 (cs_ld=%lld)", (long long)cs_ld);
+    if (!pos || !cos_bf16 || !sin_bf16) return fail(MXQ_ERR_NULL, "pos/cos/sin is NULL with R > 0");
+    if (!aligned16(cos_bf16) || !aligned16(sin_bf16) || (reinterpret_cast<uintptr_t>(pos) & 7u))
+      return fail(MXQ_ERR_ALIGN, "cos/sin must be 16-byte aligned and pos 8-byte aligned");
+  }
+  if (!kv_bf16 || !slot_mapping || !cache || !cache_sf)
+    return fail(MXQ_ERR_NULL, "kv, slot_mapping, cache or cache_sf is NULL");
+  if (H > 0 && (!q_bf16 || !q_out_bf16)) return fail(MXQ_ERR_NULL, "q or q_out is NULL with H > 0");
+  if (!aligned16(kv_bf16) || !aligned16(cache) ||
+      (H > 0 && (!aligned16(q_bf16) || !aligned16(q_out_bf16))))
+    return fail(MXQ_ERR_ALIGN, "q, q_out, kv and cache must be 16-byte aligned");
+  if (H > 0 && q_bf16 != q_out_bf16) {
+    // Distinct query buffers must not overlap (in place is q_out == q exactly).
+    const uintptr_t a = reinterpret_cast<uintptr_t>(q_bf16), b = reinterpret_cast<uintptr_t>(q_out_bf16);
+    const uintptr_t n = (uintptr_t)T * (uintptr_t)H * (uintptr_t)Dq * 2u;
+    if (a < b + n && b < a + n)
+      return fail(MXQ_ERR_SHAPE, "q_out overlaps q without being q itself");
+  }
+  if ((reinterpret_cast<uintptr_t>(slot_mapping) & 7u) ||
+      (err_flag && (reinterpret_cast<uintptr_t>(err_flag) & 3u)))
+    return fail(MXQ_ERR_ALIGN, "slot_mapping must be 8-byte aligned, err_flag 4-byte aligned");
+  int sms = 0;
+  if (int st = device_check(&sms)) return st;
+  return cuda_status(
+      mxq::launch_rope_kv4_insert(q_bf16, q_out_bf16, T, H, Dq, kv_bf16, Dk, pos, cos_bf16, sin_bf16,
+                                  cs_ld, max_pos, R, slot_mapping, cache, cache_sf, num_slots, err_flag,
+                                  sms, static_cast<cudaStream_t>(stream)),
+      "rope_kv4_insert launch");
+}
+
+int mxq_kv4_gather(const uint8_t* cache, const uint8_t* cache_sf, int64_t num_slots, int32_t Dk,
+                   const int64_t* slots, int64_t n, void* out_bf16, int32_t* err_flag,
+                   mxq_stream_t stream) {
+  if (n < 0 || num_slots < 0 || Dk < 32 || Dk % 32 != 0)
+    return fail(MXQ_ERR_SHAPE, "need n >= 0, num_slots >= 0, Dk >= 32, Dk %% 32 == 0 (n=%lld Dk=%d)",
+                (long long)n, Dk);
+  if (n >= ((int64_t)1 << 31) || n * (Dk / 8) >= ((int64_t)1 << 31))
+    return fail(MXQ_ERR_UNSUPPORTED, "n*Dk/8 must be < 2^31");
+  if (n == 0) return ok();
+  if (!cache || !cache_sf || !slots || !out_bf16)
+    return fail(MXQ_ERR_NULL, "cache, cache_sf, slots or out is NULL");
+  if (!aligned16(cache) || !aligned16(out_bf16) || (reinterpret_cast<uintptr_t>(slots) & 7u) ||
+      (err_flag && (reinterpret_cast<uintptr_t>(err_flag) & 3u)))
+    return fail(MXQ_ERR_ALIGN, "cache and out must be 16-byte aligned, slots 8-byte, err_flag 4-byte");
+  int sms = 0;
+  if (int st = device_check(&sms)) return st;
+  return cuda_status(mxq::launch_kv4_gather(cache, cache_sf, slots, n, Dk, num_slots, out_bf16, err_flag,
+                                            sms, static_cast<cudaStream_t>(stream)),
+                     "kv4_gather launch");
+}
+
+// Sizes of mxq_attn; MXQ_OK when they are accepted.
+static int validate_attn_sizes(int64_t T, int32_t B, int32_t H, int32_t D, int32_t max_pages,
+                               int32_t page_size, int32_t window, int32_t sinks) {
+  if (T < 0 || B < 1 || H < 1 || D < 64 || max_pages < 1 || page_size < 1 || window < 0 || sinks < 0)
+    return fail(MXQ_ERR_SHAPE, "need T >= 0, B >= 1, H >= 1, D >= 64, max_pages >= 1, page_size >= 1, "
+                               "window >= 0, sinks >= 0 (T=%lld B=%d H=%d D=%d max_pages=%d "
+                               "page_size=%d window=%d sinks=%d)",
+                (long long)T, B, H, D, max_pages, page_size, window, sinks);
+  if (page_size % 16 != 0) return fail(MXQ_ERR_SHAPE, "page_size %% 16 != 0 (page_size=%d)", page_size);
+  if (D % 64 != 0 || D > 512) return fail(MXQ_ERR_UNSUPPORTED, "D must be a multiple of 64, <= 512 (D=%d)", D);
+  if (H > 4096) return fail(MXQ_ERR_UNSUPPORTED, "H > 4096");
+  if (T >= ((int64_t)1 << 31) || T * H >= ((int64_t)1 << 31))
+    return fail(MXQ_ERR_UNSUPPORTED, "T*H must be < 2^31");
+  if ((int64_t)max_pages * page_size >= ((int64_t)1 << 31))
+    return fail(MXQ_ERR_UNSUPPORTED, "max_pages*page_size must be < 2^31");
+  return MXQ_OK;
+}
+
+size_t mxq_attn_workspace_bytes(int64_t T, int32_t B, int32_t H, int32_t D, int32_t max_pages,
+                                int32_t page_size, int32_t window, int32_t sinks) {
+  if (validate_attn_sizes(T, B, H, D, max_pages, page_size, window, sinks)) return 0;
+  mxq::AttnArgs a = {};
+  a.T = T;
+  a.B = B;
+  a.H = H;
+  a.D = D;
+  a.max_pages = max_pages;
+  a.page_size = page_size;
+  a.window = window;
+  a.sinks = sinks;
+  return mxq::attn_workspace_bytes(a);
+}
+
+int mxq_attn(const void* q_bf16, int64_t T, int32_t H, int32_t D, const int32_t* q_start,
+             const int32_t* seq_lens, int32_t B, const int32_t* block_table, int32_t max_pages,
+             int32_t page_size, const void* kv_cache, int64_t num_slots, int32_t cache_dtype,
+             const float* kv_scale, const uint8_t* cache_sf, int32_t window, int32_t sinks,
+             float sm_scale, void* out_bf16, float* lse, int32_t* err_flag, void* ws,
+             size_t ws_bytes, mxq_stream_t stream) {
+  if (int st = validate_attn_sizes(T, B, H, D, max_pages, page_size, window, sinks)) return st;
+  if (num_slots < 1) return fail(MXQ_ERR_SHAPE, "num_slots < 1");
+  if (num_slots >= ((int64_t)1 << 40)) return fail(MXQ_ERR_UNSUPPORTED, "num_slots >= 2^40");
+  if (!q_start && T != B)
+    return fail(MXQ_ERR_SHAPE, "without q_start T must equal B (T=%lld B=%d)", (long long)T, B);
+  if (cache_dtype != MXQ_CACHE_E4M3 && cache_dtype != MXQ_CACHE_BF16 && cache_dtype != MXQ_CACHE_E2M1)
+    return fail(MXQ_ERR_UNSUPPORTED, "cache_dtype must be MXQ_CACHE_E4M3, _BF16 or _E2M1");
+  if (!(sm_scale - sm_scale == 0.0f)) return fail(MXQ_ERR_SHAPE, "sm_scale is not finite");
+  if (T == 0) return ok();
+  if (!q_bf16 || !seq_lens || !block_table || !kv_cache || !out_bf16)
+    return fail(MXQ_ERR_NULL, "q, seq_lens, block_table, kv_cache or out is NULL");
+  if (cache_dtype == MXQ_CACHE_E4M3 && !kv_scale) return fail(MXQ_ERR_NULL, "kv_scale is NULL for an E4M3 cache");
+  if (cache_dtype == MXQ_CACHE_E2M1 && !cache_sf) return fail(MXQ_ERR_NULL, "cache_sf is NULL for a 4-bit cache");
+  if (!aligned16(q_bf16) || !aligned16(kv_cache) || !aligned16(out_bf16))
+    return fail(MXQ_ERR_ALIGN, "q, kv_cache and out must be 16-byte aligned");
+  const uintptr_t words = reinterpret_cast<uintptr_t>(q_start) | reinterpret_cast<uintptr_t>(seq_lens) |
+                          reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(kv_scale) |
+                          reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(err_flag);
+  if (words & 3u)
+    return fail(MXQ_ERR_ALIGN, "q_start, seq_lens, block_table, kv_scale, lse and err_flag must be "
+                               "4-byte aligned");
+  mxq::AttnArgs a = {};
+  a.q = q_bf16;
+  a.q_start = q_start;
+  a.seq_lens = seq_lens;
+  a.block_table = block_table;
+  a.cache = kv_cache;
+  a.cache_sf = cache_sf;
+  a.kv_scale = kv_scale;
+  a.out = out_bf16;
+  a.lse = lse;
+  a.err_flag = err_flag;
+  a.T = T;
+  a.num_slots = num_slots;
+  a.B = B;
+  a.H = H;
+  a.D = D;
+  a.max_pages = max_pages;
+  a.page_size = page_size;
+  a.dtype = cache_dtype;
+  a.window = window;
+  a.sinks = sinks;
+  a.sm_scale = sm_scale;
+  const size_t need = mxq::attn_workspace_bytes(a);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(MXQ_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, ws_bytes);
+  if (need > 0 && !aligned16(ws)) return fail(MXQ_ERR_ALIGN, "workspace must be 16-byte aligned");
+  int sms = 0;
+  if (int st = device_check(&sms)) return st;
+  const char* why = nullptr;
+  cudaError_t e = mxq::launch_attn(a, ws, sms, static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess && why) return fail(MXQ_ERR_CUDA, "attn: %s", why);
+  return cuda_status(e, "attn launch");
+}
+
 int mxq_debug_set_pair_limit(int pairs) { return mxq::set_pair_limit(pairs); }
 
 int mxq_debug_set_lazy_pairs(int from) {

@@ -33,6 +33,7 @@
 #include "mxq.h"
 #include "mxq_internal.h"
 #include "mxq_ptx.cuh"
+#include "kv_common.cuh"
 #include "quant_common.cuh"
 
 namespace mxq {
@@ -74,15 +75,6 @@ struct KvArgs {
   int fp8;                    // 1: E4M3 cache, 0: BF16 cache
 };
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&r);
-}
-
-__device__ __forceinline__ uint4 to_bf16x8(const float (&y)[8]) {
-  return make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
-}
-
 __device__ __forceinline__ uint2 to_e4m3x8(const float (&y)[8], float scale) {
   float v[8];
 #pragma unroll
@@ -100,23 +92,6 @@ __device__ __forceinline__ void store_cache(const KvArgs& a, uint8_t* dst, int c
     *reinterpret_cast<uint2*>(dst + (size_t)c * 8) = to_e4m3x8(y, scale);
   else
     *reinterpret_cast<uint4*>(dst + (size_t)c * 16) = to_bf16x8(y);
-}
-
-// Forward rotation of one rotate-half pair of chunks (x0 in the lower half,
-// x1 in the upper) with the cos/sin entries j..j+7 of position p: one
-// rounding per value, as the oracle.
-__device__ __forceinline__ void rope_pair(const uint4& va, const uint4& vb, const uint4& cw,
-                                          const uint4& sw, float (&y0)[8], float (&y1)[8]) {
-  float x0[8], x1[8], c8[8], s8[8];
-  unpack8(va, x0);
-  unpack8(vb, x1);
-  unpack8(cw, c8);
-  unpack8(sw, s8);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    y0[e] = __fsub_rn(__fmul_rn(x0[e], c8[e]), __fmul_rn(x1[e], s8[e]));
-    y1[e] = __fadd_rn(__fmul_rn(x1[e], c8[e]), __fmul_rn(x0[e], s8[e]));
-  }
 }
 
 // One work item of the row kernels (see the top of the file).
@@ -330,6 +305,11 @@ cudaError_t launch_rope_q_bulk(QBulkArgs b, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
+bool rope_q_streams(const void* q, const void* q_out, int64_t T, int H, int Dq) {
+  return H > 0 && q != q_out && T * H * (int64_t)Dq * 2 >= kBulkMinBytes &&
+         Dq * 2 <= kBulkStageBytes;
+}
+
 cudaError_t launch_rope_kv_insert(const void* q, void* q_out, int64_t T, int H, int Dq,
                                   const void* kv, int Dk, const int64_t* pos, const void* cos,
                                   const void* sin, int64_t cs_ld, int64_t max_pos, int R,
@@ -355,8 +335,7 @@ cudaError_t launch_rope_kv_insert(const void* q, void* q_out, int64_t T, int H, 
   a.Dk = Dk;
   a.R = R;
   a.fp8 = fp8;
-  const bool streamed = H > 0 && q != q_out && T * H * (int64_t)Dq * 2 >= kBulkMinBytes &&
-                        Dq * 2 <= kBulkStageBytes;
+  const bool streamed = rope_q_streams(q, q_out, T, H, Dq);
   // The item kernel's query part (none when the query is streamed; in place,
   // the query's chunks outside the slice stay where they are).
   const int hq = streamed ? 0 : H;
@@ -365,7 +344,8 @@ cudaError_t launch_rope_kv_insert(const void* q, void* q_out, int64_t T, int H, 
   a.iq = a.pq + (uint32_t)(R / 16);
   a.ik = a.pk + (uint32_t)(R / 16);
   a.q_items = (uint32_t)(T * hq) * a.iq;
-  a.n_items = a.q_items + (uint32_t)T * a.ik;
+  // Without KV rows (kv == nullptr) only the query is rotated.
+  a.n_items = a.q_items + (kv != nullptr ? (uint32_t)T * a.ik : 0u);
   if (streamed) {
     // A large query out of place: the streaming kernel, then the KV rows.
     QBulkArgs b = {};

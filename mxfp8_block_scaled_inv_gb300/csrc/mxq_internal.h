@@ -78,13 +78,50 @@ inline WoaPrefillLayout woa_prefill_layout(int64_t T, int G, int K) {
 
 // Forward RoPE of q [T][H][Dq] into q_out (may equal q) and of kv [T][Dk],
 // whose rows go to cache rows slot[t] (E4M3 of fl32(y / *scale) when fp8,
-// else BF16).
+// else BF16).  kv may be NULL: the query alone.
 cudaError_t launch_rope_kv_insert(const void* q, void* q_out, int64_t T, int H, int Dq,
                                   const void* kv, int Dk, const int64_t* pos, const void* cos,
                                   const void* sin, int64_t cs_ld, int64_t max_pos, int R,
                                   const int64_t* slot, void* cache, int64_t num_slots, int fp8,
                                   const float* scale, int32_t* err_flag, int num_sms,
                                   cudaStream_t s);
+
+// Whether launch_rope_kv_insert moves this query with the streaming kernel.
+bool rope_q_streams(const void* q, const void* q_out, int64_t T, int H, int Dq);
+
+// As launch_rope_kv_insert, the KV rows going to a 4-bit cache: E2M1 codes
+// [num_slots][Dk/2] and E8M0 bytes [num_slots][Dk/32].
+cudaError_t launch_rope_kv4_insert(const void* q, void* q_out, int64_t T, int H, int Dq,
+                                   const void* kv, int Dk, const int64_t* pos, const void* cos,
+                                   const void* sin, int64_t cs_ld, int64_t max_pos, int R,
+                                   const int64_t* slot, uint8_t* cache, uint8_t* cache_sf,
+                                   int64_t num_slots, int32_t* err_flag, int num_sms,
+                                   cudaStream_t s);
+
+// BF16 values of the rows slots[0..n) of a 4-bit cache (zeros for a slot
+// outside it).
+cudaError_t launch_kv4_gather(const uint8_t* cache, const uint8_t* cache_sf, const int64_t* slots,
+                              int64_t n, int Dk, int64_t num_slots, void* out, int32_t* err_flag,
+                              int num_sms, cudaStream_t s);
+
+// Attention over the paged cache (see mxq_attn).
+struct AttnArgs {
+  const void* q;             // [T][H][D] BF16
+  const int32_t* q_start;    // [B+1], or NULL: one token per sequence
+  const int32_t* seq_lens;   // [B]
+  const int32_t* block_table;  // [B][max_pages]
+  const void* cache;
+  const uint8_t* cache_sf;   // E2M1 cache: scale bytes
+  const float* kv_scale;     // E4M3 cache: per-tensor scale
+  void* out;                 // [T][H][D] BF16
+  float* lse;                // [T][H] or NULL
+  int32_t* err_flag;
+  int64_t T, num_slots;
+  int B, H, D, max_pages, page_size, dtype, window, sinks;
+  float sm_scale;
+};
+size_t attn_workspace_bytes(const AttnArgs& a);
+cudaError_t launch_attn(const AttnArgs& a, void* ws, int num_sms, cudaStream_t s, const char** why);
 
 // Caps the CTA pairs of the pair-form GEMM launches (0 = no cap); returns
 // the previous cap.
