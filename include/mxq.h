@@ -373,7 +373,7 @@ size_t mxq_attn_workspace_bytes(int64_t T, int32_t B, int32_t H, int32_t D, int3
  * not depend on timing: no atomics are used on them.
  * D % 64 == 0, 64 <= D <= 512, 1 <= H <= 4096, B >= 1, sm_scale finite,
  * window, sinks >= 0.  T == 0 is a no-op.  T*H >= 2^31, max_pages*page_size
- * >= 2^31 or num_slots >= 2^40 returns MXQ_ERR_UNSUPPORTED.
+ * >= 2^31 or num_slots >= 2^31 returns MXQ_ERR_UNSUPPORTED.
  */
 int mxq_attn(const void* q_bf16, int64_t T, int32_t H, int32_t D, const int32_t* q_start,
              const int32_t* seq_lens, int32_t B, const int32_t* block_table, int32_t max_pages,

@@ -533,7 +533,7 @@ int mxq_attn(const void* q_bf16, int64_t T, int32_t H, int32_t D, const int32_t*
              size_t ws_bytes, mxq_stream_t stream) {
   if (int st = validate_attn_sizes(T, B, H, D, max_pages, page_size, window, sinks)) return st;
   if (num_slots < 1) return fail(MXQ_ERR_SHAPE, "num_slots < 1");
-  if (num_slots >= ((int64_t)1 << 40)) return fail(MXQ_ERR_UNSUPPORTED, "num_slots >= 2^40");
+  if (num_slots >= ((int64_t)1 << 31)) return fail(MXQ_ERR_UNSUPPORTED, "num_slots >= 2^31");
   if (!q_start && T != B)
     return fail(MXQ_ERR_SHAPE, "without q_start T must equal B (T=%lld B=%d)", (long long)T, B);
   if (cache_dtype != MXQ_CACHE_E4M3 && cache_dtype != MXQ_CACHE_BF16 && cache_dtype != MXQ_CACHE_E2M1)
