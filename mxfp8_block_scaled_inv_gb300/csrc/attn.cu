@@ -24,8 +24,9 @@
 //
 // Warps: 0-7 softmax and epilogue (a lane is a key, then a column; the two
 // groups of four own half of the tile's rows each and never wait for one
-// another), 8 issues the matrix instructions, 9-16 fetch Q and the cache rows
-// and widen them to 16 bits in the 128-byte-swizzled layout.
+// another), 8 issues the matrix instructions, 9 the TMA copies of BF16 rows, 10
+// decodes the work items, 12-15 fetch Q and the cache rows that are widened to
+// 16 bits, into the 128-byte-swizzled layout.
 //
 // E4M3 rows are widened to FP16 (exact), with the query scaled per row by a
 // power of two into FP16's range (exact for all values within 2^24 of the
@@ -68,14 +69,16 @@ constexpr int kUnit = 16;            // keys of a unit
 constexpr int kUnits = kKeys / kUnit;
 constexpr int kChunkBytes = kKeys * 128;   // 128 keys x 64 columns of 16 bits
 constexpr int kStageBytes = 2 * kChunkBytes;
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kLoadWarp0 = 12, kLoadWarps = 8;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kItemWarp = 10,
+              kLoadWarp0 = 12, kLoadWarps = 4;
 constexpr int kThreads = (kLoadWarp0 + kLoadWarps) * 32;
-// Registers per thread: 96 at launch; softmax 144, the issuing warps 40, the
-// loading warps 72.
-constexpr int kRegsSoft = 144, kRegsIssue = 40, kRegsLoad = 72;
-static_assert(256 * kRegsSoft + 128 * kRegsIssue + 256 * kRegsLoad <= kThreads * 96, "register pool");
+// Registers per thread: 128 at launch; softmax 168, the issuing warps 40, the
+// loading warps 136.  Nothing spills: with 227 KB of shared memory in use the
+// L1 cache is too small for local memory.
+constexpr int kRegsSoft = 168, kRegsIssue = 40, kRegsLoad = 136;
+static_assert(256 * kRegsSoft + 128 * kRegsIssue + 128 * kRegsLoad <= kThreads * 128, "register pool");
 constexpr int kLoadThreads = kLoadWarps * 32;
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 6;
 constexpr uint32_t kTmemCols = 512, kTmemS = 256;
 constexpr float kNoKey = 1e30f;      // negm of a row that has seen no key
 constexpr float kSlack = 8.0f;       // log2 of how far a score may pass the maximum
@@ -91,11 +94,25 @@ struct KernelArgs {
 
 __host__ __device__ constexpr int q_bytes(int NR, int D) { return NR * D * 2; }
 
+// What one work item (a tile and a share of its key blocks) covers.
+struct alignas(16) Item {
+  int b, r0, nrows, pos0;  // sequence, first row in it, rows, position of its first new token
+  int p0, p1;              // positions of the tile's first and last row
+  int u_lo, ns;            // first unit of the window, units of the sinks
+  int units, blk0, blk1;   // units in all; this item's blocks of 8
+  int tile, split, pad;
+  int64_t qrow;            // first row of the tile in [T*H]
+};
+static_assert(sizeof(Item) == 64, "four 16-byte words");
+constexpr int kItems = 4;  // items handed out ahead
+
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages], s_full[2], p_full, pv_done, q_full[4], q_empty, drain;
+  uint64_t item_full[kItems], item_empty[kItems];
   uint32_t tmem;
   int abort;
-  float crow[4][64];
+  alignas(16) Item items[kItems];
+  float crow[3][64];
   float negm[64];
   float scale[64];  // the rescale factors of a block; in the epilogue 1 / sum
   int rowp[64];
@@ -114,13 +131,6 @@ inline int stages_for(int NR, int D) {
   return n < kMaxStages ? n : kMaxStages;
 }
 static_assert(smem_fixed(64, 512) + 4 * kStageBytes <= kSmemBudget, "a block of the widest rows fits");
-
-// What one work item (a tile and a share of its key blocks) covers.
-struct Item {
-  int b, r0, nrows, n, len, p0, p1, u_lo, ns, units, blk0, blk1;
-  int64_t qrow;  // first row of the tile in [T*H]
-  int tile, split;
-};
 
 __device__ __forceinline__ int seq_start(const AttnArgs& a, int b) {
   return a.q_start != nullptr ? __ldg(a.q_start + b) : b;
@@ -158,19 +168,21 @@ __device__ __forceinline__ Item get_item(const KernelArgs& k, int item) {
   it.b = b;
   const int start = max(seq_start(a, b), 0);
   const int end = (int)min((int64_t)seq_start(a, b + 1), a.T);
-  it.n = max(end - start, 0);
+  const int n = max(end - start, 0);
   const int cap = a.max_pages * a.page_size;
-  it.len = min(max(__ldg(a.seq_lens + b), 0), cap);
+  const int said = __ldg(a.seq_lens + b), len = min(max(said, 0), cap);
   const int64_t r0 = ((int64_t)it.tile - b - ((int64_t)start * a.H) / NR) * NR;
-  const int64_t rows = (int64_t)it.n * a.H;
+  const int64_t rows = (int64_t)n * a.H;
+  it.pos0 = len - n;
+  it.pad = said != len;
   it.nrows = r0 >= 0 && r0 < rows ? (int)min((int64_t)NR, rows - r0) : 0;
   it.r0 = (int)r0;
   it.qrow = (int64_t)start * a.H + r0;
   it.units = it.ns = it.u_lo = it.blk0 = it.blk1 = 0;
   it.p0 = it.p1 = -1;
   if (it.nrows > 0) {
-    it.p0 = it.len - it.n + it.r0 / a.H;
-    it.p1 = it.len - it.n + (it.r0 + it.nrows - 1) / a.H;
+    it.p0 = it.pos0 + it.r0 / a.H;
+    it.p1 = it.pos0 + (it.r0 + it.nrows - 1) / a.H;
     if (it.p1 >= 0) {
       const int lo = a.window > 0 ? max(0, it.p0 - a.window + 1) : 0;
       it.u_lo = lo / kUnit;
@@ -192,15 +204,27 @@ __device__ __forceinline__ int unit_key(const Item& it, int x) {
 }
 
 // ------------------------------------------------------------- instructions
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t accumulate) {
+// D[tmem] (+)= A B^T with 16-bit operands.  The descriptors come as their low
+// words (address, leading offset) and constant high words, so that stepping
+// through a tile is one 32-bit addition each: a single thread issues all of
+// the CTA's products, 64 to 96 in a block, and 64-bit descriptor arithmetic
+// in front of each took as long as the product (80 cycles).
+__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                        uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n.reg .pred p;\n"
-      "setp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n.reg .pred p;\n.reg .b64 a, b;\n"
+      "mov.b64 a, {%1, %2};\nmov.b64 b, {%3, %4};\n"
+      "setp.ne.b32 p, %6, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// Low and high words of a descriptor with 128-byte swizzle: address and
+// leading offset; stride offset 1024 (eight 128-byte rows).
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (ptx::kSwizzle128B << 29);
 
 // Instruction descriptor of kind::f16: FP32 accumulation, both operands BF16
 // (1) or FP16 (0), M = 128, N, and whether A and B are stored with M / N
@@ -241,6 +265,64 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Maximum that is NaN if either operand is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+// Maximum (or sum) over the 32 lanes of N values each, by halving exchanges:
+// lane c < N ends with value c.  31 shuffles for 32 values.
+template <int N, bool MAX>
+__device__ __forceinline__ float lanes_reduce(float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    if (off >= N) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float o = __shfl_xor_sync(0xffffffffu, v[i], off);
+        v[i] = MAX ? fmaxf(v[i], o) : v[i] + o;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < off; ++i) {
+        const bool up = lane & off;
+        const float o = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + off], off);
+        const float mine = up ? v[i + off] : v[i];
+        v[i] = MAX ? fmaxf(mine, o) : mine + o;
+      }
+    }
+  }
+  return v[0];
+}
+// 16 lanes x N columns of TMEM: per 8 columns, registers 0-1 hold lane t / 4,
+// columns 2 (t % 4) and + 1; registers 2-3 the same of lane t / 4 + 8.
+template <int N>
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t addr, uint32_t (&r)[N / 2]) {
+  static_assert(N == 8 || N == 16 || N == 32, "");
+  if constexpr (N == 8)
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+  if constexpr (N == 16)
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr));
+  if constexpr (N == 32)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+// Two 8 x 8 matrices of 16-bit values, transposed on the way to shared memory.
+__device__ __forceinline__ void stmatrix_x2_trans(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b)
+               : "memory");
+}
+__device__ __forceinline__ float out_of(bool has, uint32_t v) { return has ? __uint_as_float(v) : 0.0f; }
 __device__ __forceinline__ float warp_max(float x) {
   float y;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
@@ -327,7 +409,7 @@ __device__ __forceinline__ uint2 widen_e2m1x4(uint32_t w, const E2m1Table& t) {
 
 // Cache rows that a loading thread handles in every block.
 template <int DT>
-constexpr int kRowsPerThread = DT == MXQ_CACHE_E4M3 ? 4 : 2;
+constexpr int kRowsPerThread = DT == MXQ_CACHE_E4M3 ? 8 : 4;
 
 // ------------------------------------------------------------------ kernel
 template <int NR, int DT>
@@ -360,6 +442,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 4; ++s) ptx::mbar_init(&sh.q_full[s], kLoadThreads);
     ptx::mbar_init(&sh.q_empty, 1);
     ptx::mbar_init(&sh.drain, 1);
+    for (int i = 0; i < kItems; ++i) {
+      ptx::mbar_init(&sh.item_full[i], 1);
+      // Readers: the softmax, loading and issuing warps, and the TMA warp.
+      ptx::mbar_init(&sh.item_empty[i], kSoftWarps + kLoadWarps + 1 + (DT == MXQ_CACHE_BF16 ? 1 : 0));
+    }
     ptx::fence_barrier_init();
   }
   if (warp == kMmaWarp) {
@@ -386,68 +473,86 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, wait(bar, parity));
   };
-  // Non-blocking test by one lane for the warp.
-  auto test_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __shfl_sync(0xffffffffu, lane == 0 ? (int)ptx::mbar_test(bar, parity) : 0, 0) != 0;
+  // Non-blocking test, agreed on by the warp.
+  auto ready = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __any_sync(0xffffffffu, ptx::mbar_test(bar, parity));
+  };
+  // The i-th item of this CTA, from the item warp; false after the last (or
+  // after an abort).
+  auto read_item = [&](uint32_t i, Item& it) -> bool {
+    if (!wait_warp(&sh.item_full[i % kItems], (i / kItems) & 1u)) return false;
+    const int4* src = reinterpret_cast<const int4*>(&sh.items[i % kItems]);
+    int4* dst = reinterpret_cast<int4*>(&it);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) dst[w] = src[w];
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&sh.item_empty[i % kItems]);
+    return it.b >= 0;
   };
 
   if (warp >= kLoadWarp0) {
     // ------------------------------------- the query, and rows to be widened
-    regs_down<kRegsLoad>();
+    regs_up<kRegsLoad>();
     const int lt = tid - kLoadWarp0 * 32, lw = lt >> 5;
     const float kvs = DT == MXQ_CACHE_E4M3 ? __ldg(a.kv_scale) : 1.0f;
     int nq = 0;                // items with blocks so far
     uint32_t st = 0, stp = 0;  // stage and its phase
     bool ok = true;
-    for (int item = blockIdx.x; item < k.items && ok; item += gridDim.x) {
-      const Item it = get_item<NR>(k, item);
+    Item it;
+    for (uint32_t ni = 0; ok && read_item(ni, it); ++ni) {
       if (it.blk0 >= it.blk1) continue;
       // Q rows, one per warp and step; rows past the tile's are zeros.
       if (nq > 0 && !(ok = wait_warp(&sh.q_empty, (uint32_t)(nq - 1) & 1u))) break;
-      for (int r = lw; r < NR; r += kLoadWarps) {
-        uint4 v[2];
+      for (int r0 = lw; r0 < NR; r0 += 4 * kLoadWarps) {
+        uint4 v[4][2];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          v[c] = make_uint4(0, 0, 0, 0);
-          const int pc = c * 32 + lane;
-          if (pc < nch * 8 && r < it.nrows)
-            v[c] = __ldg(reinterpret_cast<const uint4*>(a.q) + (it.qrow + r) * (nch * 8) + pc);
-        }
-        if constexpr (!BF) {
-          // Largest magnitude of the row -> the power of two that brings it
-          // to [2^10, 2^11).
-          uint32_t mx = 0;
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+            v[i][c] = make_uint4(0, 0, 0, 0);
+            const int pc = c * 32 + lane, r = r0 + i * kLoadWarps;
+            if (pc < nch * 8 && r < it.nrows)
+              v[i][c] = __ldg(reinterpret_cast<const uint4*>(a.q) + (it.qrow + r) * (nch * 8) + pc);
+          }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              mx = max(mx, w[e] & 0x7FFFu);
-              mx = max(mx, (w[e] >> 16) & 0x7FFFu);
+        for (int i = 0; i < 4; ++i) {
+          const int r = r0 + i * kLoadWarps;
+          if constexpr (!BF) {
+            // Largest magnitude of the row -> the power of two that brings it
+            // to [2^10, 2^11).
+            uint32_t mx = 0;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t w[4] = {v[i][c].x, v[i][c].y, v[i][c].z, v[i][c].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                mx = max(mx, w[e] & 0x7FFFu);
+                mx = max(mx, (w[e] >> 16) & 0x7FFFu);
+              }
+            }
+            mx = __reduce_max_sync(0xffffffffu, mx);
+            const int ex = (int)(mx >> 7);
+            int sft = ex == 255 || mx == 0 ? 0 : 137 - ex;
+            sft = min(sft, 120);
+            const float f = __uint_as_float((uint32_t)(127 + sft) << 23);
+            if (lane == 0) {
+              const float inv = __uint_as_float((uint32_t)(127 - sft) << 23);
+              sh.crow[nq % 3][r] = r < it.nrows ? a.sm_scale * kLog2e * kvs * inv : 0.0f;
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float y[8];
+              unpack8(v[i][c], y);
+              v[i][c] = make_uint4(pack16(false, y[0] * f, y[1] * f), pack16(false, y[2] * f, y[3] * f),
+                                   pack16(false, y[4] * f, y[5] * f), pack16(false, y[6] * f, y[7] * f));
             }
           }
-          mx = __reduce_max_sync(0xffffffffu, mx);
-          const int ex = (int)(mx >> 7);
-          int sft = ex == 255 || mx == 0 ? 0 : 137 - ex;
-          sft = min(sft, 120);
-          const float f = __uint_as_float((uint32_t)(127 + sft) << 23);
-          if (lane == 0) {
-            const float inv = __uint_as_float((uint32_t)(127 - sft) << 23);
-            sh.crow[nq & 3][r] = r < it.nrows ? a.sm_scale * kLog2e * kvs * inv : 0.0f;
-          }
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float y[8];
-            unpack8(v[c], y);
-            v[c] = make_uint4(pack16(false, y[0] * f, y[1] * f), pack16(false, y[2] * f, y[3] * f),
-                              pack16(false, y[4] * f, y[5] * f), pack16(false, y[6] * f, y[7] * f));
+            const int pc = c * 32 + lane;
+            if (pc < nch * 8)
+              *reinterpret_cast<uint4*>(sm_q + (pc >> 3) * (NR * 128) + r * 128 + (((pc & 7) ^ (r & 7)) << 4)) = v[i][c];
           }
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int pc = c * 32 + lane;
-          if (pc < nch * 8)
-            *reinterpret_cast<uint4*>(sm_q + (pc >> 3) * (NR * 128) + r * 128 + (((pc & 7) ^ (r & 7)) << 4)) = v[c];
         }
       }
       ptx::fence_proxy_async_smem();
@@ -457,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (DT != MXQ_CACHE_BF16) {
         constexpr int RPT = kRowsPerThread<DT>;          // cache rows of this thread per block
         constexpr int TPR = kLoadThreads * RPT / kKeys;  // threads per row: 8, 4
-        constexpr int KSTEP = kKeys / RPT;               // key step between its rows: 32, 64
+        constexpr int KSTEP = kKeys / RPT;               // key step between its rows: 16, 32
         constexpr int PIECE_COLS = 128 / TPR;            // columns of a 16-byte piece: 16, 32
         const int key0 = lt / TPR, piece = lt % TPR;
         const uint32_t row_bytes = DT == MXQ_CACHE_E4M3 ? (uint32_t)D : (uint32_t)D / 2;
@@ -563,8 +668,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // per chunk.
       uint32_t st = 0, stp = 0;
       bool ok = true;
-      for (int item = blockIdx.x; item < k.items && ok; item += gridDim.x) {
-        const Item it = get_item<NR>(k, item);
+      Item it;
+      for (uint32_t ni = 0; ok && read_item(ni, it); ++ni) {
         for (int blk = it.blk0; blk < it.blk1 && ok; ++blk) {
           const int x = blk * kUnits + lane;
           int row = -1;
@@ -605,96 +710,116 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ahead of the second by as much as the stages hold, two blocks at most
     // (the two S buffers).  Whatever is ready is issued, the second product
     // first, because it frees stages.
-    const uint32_t stage0 = ptx::smem_u32(sm_stage), p0 = ptx::smem_u32(sm_p), q0 = ptx::smem_u32(sm_q);
+    const uint32_t dk0 = desc_lo(ptx::smem_u32(sm_stage), 16), dv0 = desc_lo(ptx::smem_u32(sm_stage), kChunkBytes);
+    const uint32_t dp0 = desc_lo(ptx::smem_u32(sm_p), kChunkBytes), dq0 = desc_lo(ptx::smem_u32(sm_q), 16);
     constexpr uint32_t idesc_s = idesc_f16(BF, NR, false, false);
     constexpr uint32_t idesc_o = idesc_f16(BF, NV, true, true);
-    struct Cursor {
-      int item;
-      Item it;
-      int blk;
-    } cq, cp;
-    auto seek = [&](Cursor& c) {  // to the next item that has blocks
-      while (c.item < k.items) {
-        c.it = get_item<NR>(k, c.item);
-        if (c.it.blk0 < c.it.blk1) {
-          c.blk = c.it.blk0;
-          return;
-        }
-        c.item += gridDim.x;
-      }
-    };
-    cq.item = cp.item = blockIdx.x;
-    seek(cq);
-    cp = cq;
+    // Items are read without blocking: those that see no key have nothing for
+    // this warp, and the others may only move on once it has issued what is ready.
+    uint32_t ni = 0;
+    bool more = true;                 // the last item has not been read
+    int qleft = 0, pleft = 0;         // blocks left of the two cursors' items
+    int punits = 0, nwait = 0;        // units left of the second's; items it still has to begin,
+    int wl0 = 0, wu0 = 0, wl1 = 0, wu1 = 0;  // at most two: it is two blocks behind at most
+    bool pfirst = true;
     uint32_t gq = 0, gp = 0, nqi = 0;     // blocks issued by each, items begun
     uint32_t qs = 0, qsp = 0, ps = 0;     // stages of the two cursors
     int qpair = 0;
     bool q_ready = false;
-    uint64_t t0 = ptx::globaltimer();
+    uint64_t t0 = 0;
     uint32_t idle = 0;
-    while (cp.item < k.items) {
+    while (more || qleft > 0 || pleft > 0) {
       bool did = false;
-      if (gp < gq && test_warp(&sh.p_full, gp & 1u)) {
+      if (more && qleft == 0 && nwait < 2 && ready(&sh.item_full[ni % kItems], (ni / kItems) & 1u)) {
+        Item it;
+        more = read_item(ni, it);
+        ++ni;
+        did = true;
+        if (more && it.blk0 < it.blk1) {
+          qleft = it.blk1 - it.blk0;
+          const int u = it.units - it.blk0 * kUnits;
+          if (pleft == 0) {
+            pleft = qleft;
+            punits = u;
+          } else {
+            if (nwait == 0) {
+              wl0 = qleft;
+              wu0 = u;
+            } else {
+              wl1 = qleft;
+              wu1 = u;
+            }
+            ++nwait;
+          }
+        }
+      }
+      if (gp < gq && ready(&sh.p_full, gp & 1u)) {
         ptx::tc_fence_after();
-        const int kk = min(kUnits, cp.it.units - cp.blk * kUnits);  // units in use
-        const bool first = cp.blk == cp.it.blk0;
+        const int kk = min(kUnits, punits);  // units in use
         for (int m = 0; m < np; ++m) {
-          if (lane == 0) {
-            const uint32_t sa = stage0 + ps * kStageBytes;
-            for (int u = 0; u < kk; ++u) {
-              const uint64_t da = ptx::smem_desc(sa + u * 2048, kChunkBytes, 1024, ptx::kSwizzle128B);
-              mma_f16(tmem + m * NV, da, ptx::smem_desc(p0 + u * 2048, kChunkBytes, 1024, ptx::kSwizzle128B),
-                      idesc_o, (first && u == 0) ? 0u : 1u);
+          if (ptx::elect_one()) {
+            const uint32_t da = dv0 + ps * (kStageBytes >> 4);
+            const uint32_t dd = tmem + m * NV;
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+              if (u >= kk) break;
+              mma_f16(dd, da + u * 128, kDescHi, dp0 + u * 128, kDescHi, idesc_o, (pfirst && u == 0) ? 0u : 1u);
               if (NR == 64)  // the low parts, a buffer of their own
-                mma_f16(tmem + m * NV, da,
-                        ptx::smem_desc(p0 + kKeys * 128 + u * 2048, kChunkBytes, 1024, ptx::kSwizzle128B),
-                        idesc_o, 1u);
+                mma_f16(dd, da + u * 128, kDescHi, dp0 + (kKeys * 8) + u * 128, kDescHi, idesc_o, 1u);
             }
             ptx::tc_commit(&sh.empty[ps]);
           }
+          __syncwarp();
           if (++ps == (uint32_t)k.stages) ps = 0;
         }
-        if (lane == 0) ptx::tc_commit(&sh.pv_done);
+        if (ptx::elect_one()) ptx::tc_commit(&sh.pv_done);
         ++gp;
-        if (++cp.blk == cp.it.blk1) {
-          cp.item += gridDim.x;
-          seek(cp);
+        pfirst = false;
+        punits -= kUnits;
+        if (--pleft == 0) {
+          pfirst = true;
+          if (nwait > 0) {
+            pleft = wl0;
+            punits = wu0;
+            wl0 = wl1;
+            wu0 = wu1;
+            --nwait;
+          }
         }
         did = true;
-      } else if (cq.item < k.items && gq < gp + 2) {
-        if (!q_ready && test_warp(&sh.q_full[nqi & 3u], (nqi >> 2) & 1u)) q_ready = true;
-        if (q_ready && test_warp(&sh.full[qs], qsp)) {
+      } else if (qleft > 0 && gq < gp + 2) {
+        if (!q_ready) q_ready = ready(&sh.q_full[nqi & 3u], (nqi >> 2) & 1u);
+        while (q_ready && ready(&sh.full[qs], qsp)) {
           ptx::tc_fence_after();
-          if (lane == 0) {
-            const uint32_t sa = stage0 + qs * kStageBytes;
+          if (ptx::elect_one()) {
+            const uint32_t da = dk0 + qs * (kStageBytes >> 4), db = dq0 + qpair * (NR * 256 >> 4);
             const uint32_t ds = tmem + kTmemS + (gq & 1u) * 64;
-            const int chunks = min(2, nch - qpair * 2);
-            for (int c = 0; c < chunks; ++c)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if (qpair * 2 + c >= nch) break;
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                mma_f16(ds,
-                        ptx::smem_desc(sa + c * kChunkBytes + e * 32, 16, 1024, ptx::kSwizzle128B),
-                        ptx::smem_desc(q0 + (qpair * 2 + c) * (NR * 128) + e * 32, 16, 1024,
-                                       ptx::kSwizzle128B),
+                mma_f16(ds, da + c * (kChunkBytes >> 4) + e * 2, kDescHi, db + c * (NR * 128 >> 4) + e * 2, kDescHi,
                         idesc_s, (qpair | c | e) ? 1u : 0u);
+            }
           }
+          __syncwarp();
+          did = true;
           if (++qs == (uint32_t)k.stages) {
             qs = 0;
             qsp ^= 1u;
           }
           if (++qpair == np) {
             qpair = 0;
-            if (lane == 0) ptx::tc_commit(&sh.s_full[gq & 1u]);
+            if (ptx::elect_one()) ptx::tc_commit(&sh.s_full[gq & 1u]);
             ++gq;
-            if (++cq.blk == cq.it.blk1) {
-              if (lane == 0) ptx::tc_commit(&sh.q_empty);
+            if (--qleft == 0) {
+              if (ptx::elect_one()) ptx::tc_commit(&sh.q_empty);
               ++nqi;
               q_ready = false;
-              cq.item += gridDim.x;
-              seek(cq);
             }
+            break;
           }
-          did = true;
         }
       }
       if (did) {
@@ -711,14 +836,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (__any_sync(0xffffffffu, stop)) break;
       }
-      __syncwarp();
     }
     // Everything issued has completed before TMEM and shared memory go away.
-    if (lane == 0) ptx::tc_commit(&sh.drain);
+    if (ptx::elect_one()) ptx::tc_commit(&sh.drain);
     __syncwarp();
     if (!ptx::mbar_wait(&sh.drain, 0, kWaitNs) && lane == 0) atomicOr(k.watchdog, kWdAttn);
+  } else if (warp == kItemWarp) {
+    // ------------------------------------------------------- work items
+    // Decoded here once for all roles, up to four ahead.
+    regs_down<kRegsIssue>();
+    uint32_t i = 0;
+    for (int item = blockIdx.x;; item += gridDim.x) {
+      Item it;
+      const bool end = item >= k.items;
+      if (end) {
+        it.b = -1;
+      } else {
+        it = get_item<NR>(k, item);
+        if (it.nrows == 0) continue;
+        if (lane == 0 && it.pad && a.err_flag != nullptr) atomicOr(a.err_flag, MXQ_DEVERR_LENGTH);
+        // Without blocks: a row that sees nothing (written by split 0), or a
+        // share of the keys that is empty.
+        if (it.blk0 >= it.blk1 && (it.units > 0 || it.split > 0)) continue;
+      }
+      if (!wait_warp(&sh.item_empty[i % kItems], ((i / kItems) & 1u) ^ 1u)) break;
+      if (lane == 0) {
+        sh.items[i % kItems] = it;
+        ptx::mbar_arrive(&sh.item_full[i % kItems]);
+      }
+      __syncwarp();
+      if (end) break;
+      ++i;
+    }
   } else if (warp >= kSoftWarps) {
-    regs_down<kRegsIssue>();  // two idle warps of the issuing group
+    regs_down<kRegsIssue>();  // an idle warp of the issuing group
   } else {
     // ------------------------------------------------- softmax and epilogue
     regs_up<kRegsSoft>();
@@ -728,30 +879,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int c0 = h * NC;
     const uint32_t bar = 1 + h;
     const float c_all = a.sm_scale * kLog2e;
+    const float4* negm4 = reinterpret_cast<const float4*>(sh.negm + c0);
     uint32_t g = 0;   // blocks so far
-    int nq = 0;
+    int nq = 0;       // items with blocks so far
     uint32_t st = 0;  // first stage of the current block
     // A wait that gives up does not leave the loops by itself: the group's
     // next vote takes all of its threads out together.
     bool ok = true, dead = false;
-    for (int item = blockIdx.x; item < k.items && !dead; item += gridDim.x) {
-      const Item it = get_item<NR>(k, item);
-      if (it.nrows == 0) continue;
+    for (uint32_t ni = 0; !dead; ++ni) {
+      Item it;
+      const bool more = read_item(ni, it);
+      if (named_any(bar, 128, !more)) break;
       const bool has = it.blk0 < it.blk1;
-      if (!has && (it.units > 0 || it.split > 0)) continue;  // other splits hold the keys
       // Rows of this group.
       if (quad == 0 && lane < NC) {
         const int r = c0 + lane;
         sh.negm[r] = r < it.nrows ? kNoKey : 0.0f;
-        sh.rowp[r] = r < it.nrows ? it.len - it.n + (it.r0 + r) / a.H : -1;
+        sh.rowp[r] = r < it.nrows ? it.pos0 + (it.r0 + r) / a.H : -1;
       }
-      if (a.err_flag != nullptr && h == 0 && quad == 0 && lane == 0 && it.len != __ldg(a.seq_lens + it.b))
-        atomicOr(a.err_flag, MXQ_DEVERR_LENGTH);
       ptx::named_sync(bar, 128);
       float l[NC];
 #pragma unroll
       for (int c = 0; c < NC; ++c) l[c] = 0.0f;
-      const float* crow = sh.crow[nq & 3] + c0;
+      const float4* crow4 = reinterpret_cast<const float4*>(sh.crow[nq % 3] + c0);
       if (has) {
         // The row scales come with the query.
         if (!BF) ok = wait(&sh.q_full[nq & 3], (uint32_t)(nq >> 2) & 1u) && ok;
@@ -782,19 +932,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t s[NC];
         tmem_ld<NC>(tq + kTmemS + (g & 1u) * 64 + c0, s);
         ptx::tmem_ld_wait();
-        // Scores past the running maximum, and scores that are not finite.
-        float top = -INFINITY, odd = 0.0f;
+        // The largest score over the running maxima, NaN if there is one: a
+        // cache row with a NaN or an infinity has no finite score at all.
+        float top = -INFINITY, seen = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const float v = __uint_as_float(s[c]);
-          const float cr = BF ? c_all : crow[c];
-          odd = fmaf(v, 0.0f, odd);
-          float d = fmaf(v, cr, sh.negm[c0 + c]);
-          if (mixed) d = sees(c) ? d : -INFINITY;
-          top = fmaxf(top, d);
+        for (int q = 0; q < NC / 4; ++q) {
+          const float4 n = negm4[q];
+          const float4 cr = BF ? make_float4(c_all, c_all, c_all, c_all) : crow4[q];
+          const float d[4] = {fmaf(__uint_as_float(s[4 * q]), cr.x, n.x), fmaf(__uint_as_float(s[4 * q + 1]), cr.y, n.y),
+                              fmaf(__uint_as_float(s[4 * q + 2]), cr.z, n.z),
+                              fmaf(__uint_as_float(s[4 * q + 3]), cr.w, n.w)};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max_nan(top, d[e]);
+          if (mixed) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) seen = fmaxf(seen, sees(4 * q + e) ? d[e] : -INFINITY);
+          }
         }
-        const bool bad = in && !(odd == 0.0f);
-        const bool raise = bad || (some && top > kSlack + kShift);
+        const bool bad = in && !(fabsf(top) <= 3.4028234e38f);
+        const bool raise = bad || (some && (mixed ? seen : top) > kSlack + kShift);
         if (named_any(bar, 128, raise || !ok)) {
           // ---- some maximum moves, something is not finite, or a wait gave up
           if (named_any(bar, 128, !ok)) {
@@ -806,11 +962,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             // that do not see it through 0 * NaN: it is cleared here, and the
             // rows that see it become NaN through their sums.
             bool rowbad = false;
-            for (int pr = 0; pr < np; ++pr) {
-              const uint32_t sidx = (st + pr) % (uint32_t)k.stages;
-              for (int ch = 0; ch < min(2, nch - pr * 2); ++ch) {
-                uint4* rp = reinterpret_cast<uint4*>(sm_stage + sidx * kStageBytes + ch * kChunkBytes + key * 128);
+            for (int pass = 0; pass < 2; ++pass)
+              for (int ch = 0; ch < nch; ++ch) {
+                const uint32_t sidx = (st + (ch >> 1)) % (uint32_t)k.stages;
+                uint4* rp = reinterpret_cast<uint4*>(sm_stage + sidx * kStageBytes + (ch & 1) * kChunkBytes + key * 128);
                 for (int e = 0; e < 8; ++e) {
+                  if (pass == 1) {
+                    if (rowbad) rp[e] = make_uint4(0, 0, 0, 0);
+                    continue;
+                  }
                   const uint4 w = rp[e];
                   const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
                   const uint32_t m = BF ? 0x7F80u : 0x7C00u;
@@ -818,29 +978,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     rowbad |= (ws[q] & m) == m || ((ws[q] >> 16) & m) == m;
                 }
               }
-            }
-            if (rowbad)
-              for (int pr = 0; pr < np; ++pr) {
-                const uint32_t sidx = (st + pr) % (uint32_t)k.stages;
-                for (int ch = 0; ch < min(2, nch - pr * 2); ++ch) {
-                  uint4* rp = reinterpret_cast<uint4*>(sm_stage + sidx * kStageBytes + ch * kChunkBytes + key * 128);
-                  for (int e = 0; e < 8; ++e) rp[e] = make_uint4(0, 0, 0, 0);
-                }
-              }
           }
+          float mx[NC];
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const float v = __uint_as_float(s[c]);
-            const bool fin = fabsf(v) <= 3.4028234e38f;
-            const bool see = mixed ? sees(c) : all;
-            if (bad && !fin) {
-              if (see) l[c] = NAN;
-              s[c] = 0xFF800000u;  // weight 0 below
+          for (int q = 0; q < NC / 4; ++q) {
+            const float4 cr4 = BF ? make_float4(c_all, c_all, c_all, c_all) : crow4[q];
+            const float cr[4] = {cr4.x, cr4.y, cr4.z, cr4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int c = 4 * q + e;
+              const float v = __uint_as_float(s[c]);
+              const bool fin = fabsf(v) <= 3.4028234e38f;
+              const bool see = mixed ? sees(c) : all;
+              if (bad && !fin) {
+                if (see) l[c] = NAN;
+                s[c] = __float_as_uint(copysignf(INFINITY, -cr[e]));  // weight 0 below
+              }
+              mx[c] = see && fin ? v * cr[e] : -INFINITY;
             }
-            const float cr = BF ? c_all : crow[c];
-            const float m = warp_max(see && fin ? v * cr : -INFINITY);
-            if (lane == c) sh.red[h][quad][c] = m;
           }
+          const float m = lanes_reduce<NC, true>(mx);
+          if (lane < NC) sh.red[h][quad][lane] = m;
           ptx::named_sync(bar, 128);
           if (quad == 0 && lane < NC) {
             const int r = c0 + lane;
@@ -858,14 +1016,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             sh.scale[r] = f;
           }
           ptx::named_sync(bar, 128);
-          bool moved = false;
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const float f = sh.scale[c0 + c];
-            l[c] *= f;
-            moved |= f != 1.0f;
-          }
           if (blk > it.blk0) {
+            bool moved = false;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              const float f = sh.scale[c0 + c];
+              l[c] *= f;
+              moved |= f != 1.0f;
+            }
             ok = wait(&sh.pv_done, (g - 1) & 1u);
             __syncwarp();
             if (moved) {
@@ -894,19 +1052,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < NC / 8; ++q) {
           uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float p[2];
+          for (int e = 0; e < 4; e += 2) {
+            const float4 n4 = negm4[q * 2 + e / 2];
+            const float4 cr4 = BF ? make_float4(c_all, c_all, c_all, c_all) : crow4[q * 2 + e / 2];
+            const float n[4] = {n4.x, n4.y, n4.z, n4.w}, cr[4] = {cr4.x, cr4.y, cr4.z, cr4.w};
+            float p[4];
 #pragma unroll
-            for (int f = 0; f < 2; ++f) {
+            for (int f = 0; f < 4; ++f) {
               const int c = q * 8 + e * 2 + f;
-              const float cr = BF ? c_all : crow[c];
-              p[f] = ex2(fmaf(__uint_as_float(s[c]), cr, sh.negm[c0 + c]));
+              p[f] = ex2(fmaf(__uint_as_float(s[c]), cr[f], n[f]));
               const bool see = mixed ? sees(c) : all;
-              p[f] = see && s[c] != 0xFF800000u ? p[f] : 0.0f;
+              p[f] = see ? p[f] : 0.0f;
               l[c] += p[f];
             }
             hi[e] = pack16(BF, p[0], p[1]);
+            hi[e + 1] = pack16(BF, p[2], p[3]);
             lo[e] = pack16_rest(BF, p[0], p[1], hi[e]);
+            lo[e + 1] = pack16_rest(BF, p[2], p[3], hi[e + 1]);
           }
           const int col = (c0 >> 3) + q;
           uint8_t* row = sm_p + key * 128;
@@ -923,22 +1085,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (dead) break;
       // ---- row sums over the 128 keys, then the output
+      const float sum32 = lanes_reduce<NC, false>(l);
+      if (lane < NC) sh.red[h][quad][lane] = sum32;
       if (has) {
         ok = wait(&sh.pv_done, (g - 1) & 1u) && ok;
         if (named_any(bar, 128, !ok)) {
           dead = true;
           break;
         }
+      } else {
+        ptx::named_sync(bar, 128);
       }
       ptx::tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        float v = l[c];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == c) sh.red[h][quad][c] = v;
-      }
-      ptx::named_sync(bar, 128);
       if (quad == 0 && lane < NC) {
         const int r = c0 + lane;
         const float sum = (sh.red[h][0][lane] + sh.red[h][1][lane]) + (sh.red[h][2][lane] + sh.red[h][3][lane]);
@@ -953,56 +1111,79 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       ptx::named_sync(bar, 128);
-      // The tile's columns m * 128 + key of this group's rows.
-      auto load_o = [&](int m, uint32_t (&o)[NC]) {
-        tmem_ld<NC>(tq + m * NV + c0, o);
-        if constexpr (NR < 64) {
-          uint32_t lo[NC];
-          tmem_ld<NC>(tq + m * NV + NR + c0, lo);
-          ptx::tmem_ld_wait();
-#pragma unroll
-          for (int c = 0; c < NC; ++c)
-            o[c] = __float_as_uint(__uint_as_float(o[c]) + __uint_as_float(lo[c]));
-        } else {
-          ptx::tmem_ld_wait();
-        }
-      };
       if (k.splits > 1 && has) {
-        float* dst = k.part + (((int64_t)it.tile * k.splits + it.split) * NR) * D;
+        // Partial sums as they are: a warp stores 32 consecutive columns of a row.
+        float* dst = k.part + (((int64_t)it.tile * k.splits + it.split) * NR + c0) * D + key;
         for (int m = 0; m < np; ++m) {
           uint32_t o[NC];
-          load_o(m, o);
-          const int d = m * 128 + key;
-          if (d < D) {
+          tmem_ld<NC>(tq + m * NV + c0, o);
+          if constexpr (NR < 64) {
+            uint32_t lo[NC];
+            tmem_ld<NC>(tq + m * NV + NR + c0, lo);
+            ptx::tmem_ld_wait();
 #pragma unroll
             for (int c = 0; c < NC; ++c)
-              if (c0 + c < it.nrows) dst[(int64_t)(c0 + c) * D + d] = __uint_as_float(o[c]);
+              o[c] = __float_as_uint(__uint_as_float(o[c]) + __uint_as_float(lo[c]));
+          } else {
+            ptx::tmem_ld_wait();
+          }
+          if (m * 128 + key < D) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              if (c0 + c < it.nrows) dst[(int64_t)c * D + m * 128] = __uint_as_float(o[c]);
           }
         }
       } else {
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + it.qrow * D;
-        for (int m = 0; m < np; ++m) {
-          uint32_t o[NC];
-          if (has) {
-            load_o(m, o);
-          } else {
+        // The output is turned around in shared memory (the group's half of
+        // the P buffers), 256 columns at a time: 16-lane TMEM fragments,
+        // rounded to BF16 pairs of rows, stored as transposed 8 x 8 matrices
+        // into rows of 512 bytes whose 16-byte words are swizzled by row; then
+        // whole rows go out with 16-byte stores.
+        uint8_t* stage = sm_p + h * (p_bytes(NR) / 2);
+        const uint32_t stage_a = ptx::smem_u32(stage);
+        float2 sc[NC / 8];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) o[c] = 0;
-          }
-          const int d = (m * 128 + key) & ~1;
+        for (int q = 0; q < NC / 8; ++q)
+          sc[q] = *reinterpret_cast<const float2*>(&sh.scale[c0 + q * 8 + (lane & 3) * 2]);
+        uint8_t* dst = static_cast<uint8_t*>(a.out) + (it.qrow + c0) * D * 2;
+        for (int m0 = 0; m0 < np; m0 += 2) {
+          for (int m = m0; m < min(m0 + 2, np); ++m)
 #pragma unroll
-          for (int c = 0; c < NC; c += 2) {
-            // Neighbouring lanes hold neighbouring columns: the even lane
-            // stores both of row c, the odd one both of row c + 1.
-            const float v0 = __uint_as_float(o[c]) * sh.scale[c0 + c];
-            const float v1 = __uint_as_float(o[c + 1]) * sh.scale[c0 + c + 1];
-            const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v0 : v1, 1);
-            const int r = c0 + c + (lane & 1);
-            if (r < it.nrows && d < D)
-              *reinterpret_cast<uint32_t*>(dst + (int64_t)r * D + d) =
-                  (lane & 1) ? pack16(true, got, v1) : pack16(true, v0, got);
+            for (int hf = 0; hf < 2; ++hf) {
+              uint32_t o[NC / 2];
+              const uint32_t ad = tq + ((uint32_t)(hf * 16) << 16) + m * NV + c0;
+              tmem_ld_16x256b<NC>(ad, o);
+              if constexpr (NR < 64) {
+                uint32_t lo[NC / 2];
+                tmem_ld_16x256b<NC>(ad + NR, lo);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < NC / 2; ++c)
+                  o[c] = __float_as_uint(__uint_as_float(o[c]) + __uint_as_float(lo[c]));
+              } else {
+                ptx::tmem_ld_wait();
+              }
+#pragma unroll
+              for (int q = 0; q < NC / 8; ++q) {
+                const uint32_t w0 = pack16(true, out_of(has, o[4 * q]) * sc[q].x, out_of(has, o[4 * q + 1]) * sc[q].y);
+                const uint32_t w1 = pack16(true, out_of(has, o[4 * q + 2]) * sc[q].x, out_of(has, o[4 * q + 3]) * sc[q].y);
+                // Lanes 0-7 name the rows of the first matrix, 8-15 of the second.
+                const int row = q * 8 + (lane & 7);
+                const int word = (m - m0) * 16 + quad * 4 + hf * 2 + ((lane >> 3) & 1);
+                stmatrix_x2_trans(stage_a + row * 512 + ((word ^ (row & 7)) << 4), w0, w1);
+              }
+            }
+          ptx::named_sync(bar, 128);
+          for (int i = quad; i < NC; i += 4) {
+            const int col = m0 * 128 + lane * 8;
+            if (c0 + i < it.nrows && col < D)
+              *reinterpret_cast<uint4*>(dst + ((int64_t)i * D + col) * 2) =
+                  *reinterpret_cast<const uint4*>(stage + i * 512 + ((lane ^ (i & 7)) << 4));
           }
+          ptx::named_sync(bar, 128);
         }
+        // Both groups are done with the P buffers.
+        ptx::named_sync(3, 256);
       }
       ptx::tc_fence_before();
     }
