@@ -69,7 +69,7 @@ constexpr int kUnit = 16;            // keys of a unit
 constexpr int kUnits = kKeys / kUnit;
 constexpr int kChunkBytes = kKeys * 128;   // 128 keys x 64 columns of 16 bits
 constexpr int kStageBytes = 2 * kChunkBytes;
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kItemWarp = 10,
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kItemWarp = 10, kUnitWarp = 11,
               kLoadWarp0 = 12, kLoadWarps = 4;
 constexpr int kThreads = (kLoadWarp0 + kLoadWarps) * 32;
 // Registers per thread: 128 at launch; softmax 168, the issuing warps 40, the
@@ -105,17 +105,19 @@ struct alignas(16) Item {
 };
 static_assert(sizeof(Item) == 64, "four 16-byte words");
 constexpr int kItems = 4;  // items handed out ahead
+constexpr int kSlots = 4;  // blocks whose units are looked up ahead
 
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages], s_full[2], p_full, pv_done, q_full[4], q_empty, drain;
-  uint64_t item_full[kItems], item_empty[kItems];
+  uint64_t item_full[kItems], item_empty[kItems], slot_full[kSlots], slot_empty[kSlots];
   uint32_t tmem;
   int abort;
   alignas(16) Item items[kItems];
+  int slots[kSlots][kUnits];  // cache row of each unit's first key, -1: none
   float crow[3][64];
   float negm[64];
   float scale[64];  // the rescale factors of a block; in the epilogue 1 / sum
-  int rowp[64];
+  uint8_t rowt[64];  // a row's token, counted from the tile's first
   float red[2][4][32];
 };
 
@@ -199,7 +201,8 @@ __device__ __forceinline__ Item get_item(const KernelArgs& k, int item) {
 }
 
 // First key of unit x of the item.
-__device__ __forceinline__ int unit_key(const Item& it, int x) {
+template <typename I>
+__device__ __forceinline__ int unit_key(const I& it, int x) {
   return (x < it.ns ? x : it.u_lo + (x - it.ns)) * kUnit;
 }
 
@@ -444,8 +447,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(&sh.drain, 1);
     for (int i = 0; i < kItems; ++i) {
       ptx::mbar_init(&sh.item_full[i], 1);
-      // Readers: the softmax, loading and issuing warps, and the TMA warp.
-      ptx::mbar_init(&sh.item_empty[i], kSoftWarps + kLoadWarps + 1 + (DT == MXQ_CACHE_BF16 ? 1 : 0));
+      // Readers: the softmax, loading, issuing and unit warps, and the TMA warp.
+      ptx::mbar_init(&sh.item_empty[i], kSoftWarps + kLoadWarps + 2 + (DT == MXQ_CACHE_BF16 ? 1 : 0));
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      ptx::mbar_init(&sh.slot_full[i], 1);
+      ptx::mbar_init(&sh.slot_empty[i], kSoftWarps + (DT == MXQ_CACHE_BF16 ? 1 : kLoadWarps));
     }
     ptx::fence_barrier_init();
   }
@@ -496,7 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lt = tid - kLoadWarp0 * 32, lw = lt >> 5;
     const float kvs = DT == MXQ_CACHE_E4M3 ? __ldg(a.kv_scale) : 1.0f;
     int nq = 0;                // items with blocks so far
-    uint32_t st = 0, stp = 0;  // stage and its phase
+    [[maybe_unused]] uint32_t nb = 0;  // blocks so far
+    [[maybe_unused]] uint32_t st = 0, stp = 0;  // stage and its phase
     bool ok = true;
     Item it;
     for (uint32_t ni = 0; ok && read_item(ni, it); ++ni) {
@@ -566,33 +574,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int PIECE_COLS = 128 / TPR;            // columns of a 16-byte piece: 16, 32
         const int key0 = lt / TPR, piece = lt % TPR;
         const uint32_t row_bytes = DT == MXQ_CACHE_E4M3 ? (uint32_t)D : (uint32_t)D / 2;
-        // Rows key0 + i * KSTEP of a block: their slot, or -1.
-        auto slots_of = [&](int blk, int (&slot)[RPT]) {
+        // Rows key0 + i * KSTEP of a block (unit i * KSTEP / 16 + key0 / 16).
+        const uint8_t* row[RPT];
+        const uint8_t* sf[RPT];
+        auto open_block = [&]() -> bool {
+          if (!wait_warp(&sh.slot_full[nb % kSlots], (nb / kSlots) & 1u)) return false;
+          const int* su = sh.slots[nb % kSlots] + (key0 >> 4);
 #pragma unroll
           for (int i = 0; i < RPT; ++i) {
-            const int key = key0 + i * KSTEP;
-            const int x = blk * kUnits + (key >> 4);
-            slot[i] = -1;
-            if (x < it.units) {
-              const int j = unit_key(it, x) + (key & 15);
-              const int pg = j / a.page_size;
-              const int page = __ldg(a.block_table + (int64_t)it.b * a.max_pages + pg);
-              const int64_t sl = (int64_t)page * a.page_size + (j - pg * a.page_size);
-              if (page >= 0 && sl < a.num_slots) slot[i] = (int)sl;
-            }
+            const int u = su[i * (KSTEP / 16)];
+            const int64_t slot = (int64_t)u + (key0 & 15);
+            const bool in = u >= 0 && slot < a.num_slots;
+            row[i] = in ? static_cast<const uint8_t*>(a.cache) + slot * row_bytes + piece * 16 : nullptr;
+            if (DT == MXQ_CACHE_E2M1) sf[i] = a.cache_sf + (in ? slot : 0) * (D >> 5) + piece;
           }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sh.slot_empty[nb % kSlots]);
+          ++nb;
+          return true;
         };
         // The 16-byte pieces of one pair of chunks (and their scale bytes).
-        auto fetch = [&](const int (&slot)[RPT], int pr, uint4 (&v)[RPT], uint32_t (&sb)[RPT]) {
+        auto fetch = [&](int pr, uint4 (&v)[RPT], uint32_t (&sb)[RPT]) {
           const bool in = pr * 128 + piece * PIECE_COLS < D;  // an odd last chunk: half a pair
 #pragma unroll
           for (int i = 0; i < RPT; ++i) {
             v[i] = make_uint4(0, 0, 0, 0);
             sb[i] = 0;
-            if (in && slot[i] >= 0) {
-              v[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.cache) +
-                                                          (int64_t)slot[i] * row_bytes + (pr * TPR + piece) * 16));
-              if (DT == MXQ_CACHE_E2M1) sb[i] = __ldg(a.cache_sf + (int64_t)slot[i] * (D >> 5) + pr * 4 + piece);
+            if (in && row[i] != nullptr) {
+              v[i] = __ldg(reinterpret_cast<const uint4*>(row[i] + pr * (TPR * 16)));
+              if (DT == MXQ_CACHE_E2M1) sb[i] = __ldg(sf[i] + pr * 4);
             }
           }
         };
@@ -634,27 +644,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             stp ^= 1u;
           }
         };
-        // The next pair is fetched before the current one is stored, and the
-        // block table entries of the next block a block ahead.
-        int slot[RPT], next[RPT];
+        // The next pair is fetched before the current one is stored.
         uint4 v[2][RPT];
         uint32_t sb[2][RPT];
-        int blk = it.blk0, pr = 0;
-        slots_of(blk, slot);
-        fetch(slot, 0, v[0], sb[0]);
-        slots_of(min(blk + 1, it.blk1 - 1), next);
+        int left = it.blk1 - it.blk0, pr = 0;
+        if (!(ok = open_block())) break;
+        fetch(0, v[0], sb[0]);
         auto step = [&](uint4 (&vc)[RPT], uint32_t (&sc)[RPT], uint4 (&vn)[RPT], uint32_t (&sn)[RPT]) -> bool {
           if (++pr == np) {
             pr = 0;
-            ++blk;
-#pragma unroll
-            for (int i = 0; i < RPT; ++i) slot[i] = next[i];
-            if (blk + 1 < it.blk1) slots_of(blk + 1, next);
+            if (--left > 0 && !(ok = open_block())) return false;
           }
-          if (blk < it.blk1) fetch(slot, pr, vn, sn);
+          if (left > 0) fetch(pr, vn, sn);
           if (!(ok = wait_warp(&sh.empty[st], stp ^ 1u))) return false;
           store(vc, sc);
-          return blk < it.blk1;
+          return left > 0;
         };
         while (step(v[0], sb[0], v[1], sb[1]) && step(v[1], sb[1], v[0], sb[0])) {
         }
@@ -666,20 +670,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // --------------------------------- BF16 rows: copied as they are by TMA
       // Lane u < 8 copies unit u of the block, one box of 16 rows x 64 columns
       // per chunk.
-      uint32_t st = 0, stp = 0;
+      uint32_t st = 0, stp = 0, nb = 0;
       bool ok = true;
       Item it;
       for (uint32_t ni = 0; ok && read_item(ni, it); ++ni) {
         for (int blk = it.blk0; blk < it.blk1 && ok; ++blk) {
-          const int x = blk * kUnits + lane;
-          int row = -1;
-          if (lane < kUnits && x < it.units) {
-            const int j = unit_key(it, x);
-            const int pg = j / a.page_size;
-            const int page = __ldg(a.block_table + (int64_t)it.b * a.max_pages + pg);
-            const int64_t slot = (int64_t)page * a.page_size + (j - pg * a.page_size);
-            if (page >= 0 && slot < a.num_slots) row = (int)slot;
-          }
+          if (!(ok = wait_warp(&sh.slot_full[nb % kSlots], (nb / kSlots) & 1u))) break;
+          const int row = lane < kUnits ? sh.slots[nb % kSlots][lane] : -1;
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sh.slot_empty[nb % kSlots]);
+          ++nb;
           const uint32_t boxes = (uint32_t)__popc(__ballot_sync(0xffffffffu, row >= 0));
           for (int pr = 0; pr < np; ++pr) {
             if (!(ok = wait_warp(&sh.empty[st], stp ^ 1u))) break;
@@ -868,8 +868,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (end) break;
       ++i;
     }
-  } else if (warp >= kSoftWarps) {
-    regs_down<kRegsIssue>();  // an idle warp of the issuing group
+  } else if (warp == kUnitWarp) {
+    // ------------------------------------- where the units of a block lie
+    // Lane u < 8 looks up unit u, a few blocks ahead of their use: the block
+    // table's latency and the divisions stay out of the other warps' way.
+    regs_down<kRegsIssue>();
+    uint32_t nb = 0;
+    bool ok = true;
+    Item it;
+    for (uint32_t ni = 0; ok && read_item(ni, it); ++ni) {
+      for (int blk = it.blk0; blk < it.blk1; ++blk, ++nb) {
+        const int x = blk * kUnits + lane;
+        int slot = -1;
+        if (lane < kUnits && x < it.units) {
+          const int j = unit_key(it, x);
+          const int pg = j / a.page_size;
+          const int page = __ldg(a.block_table + (int64_t)it.b * a.max_pages + pg);
+          const int64_t first = (int64_t)page * a.page_size + (j - pg * a.page_size);
+          if (page >= 0 && first < a.num_slots) slot = (int)first;
+          // A page outside the cache, or one that ends past it, hides keys.
+          if (a.err_flag != nullptr && (slot < 0 || first + min(kUnit, it.p1 + 1 - j) > a.num_slots))
+            atomicOr(a.err_flag, MXQ_DEVERR_SLOT);
+        }
+        if (!(ok = wait_warp(&sh.slot_empty[nb % kSlots], ((nb / kSlots) & 1u) ^ 1u))) break;
+        if (lane < kUnits) sh.slots[nb % kSlots][lane] = slot;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.slot_full[nb % kSlots]);
+      }
+    }
   } else {
     // ------------------------------------------------- softmax and epilogue
     regs_up<kRegsSoft>();
@@ -887,15 +913,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     // next vote takes all of its threads out together.
     bool ok = true, dead = false;
     for (uint32_t ni = 0; !dead; ++ni) {
-      Item it;
-      const bool more = read_item(ni, it);
+      // The item stays in shared memory until its output is on its way: only
+      // what every block needs is held in registers.
+      const volatile Item& held = sh.items[ni % kItems];
+      const bool more = wait_warp(&sh.item_full[ni % kItems], (ni / kItems) & 1u) && held.b >= 0;
       if (named_any(bar, 128, !more)) break;
+      struct {
+        int nrows, p0, p1, u_lo, ns, units, blk0, blk1;
+      } it = {held.nrows, held.p0, held.p1, held.u_lo, held.ns, held.units, held.blk0, held.blk1};
       const bool has = it.blk0 < it.blk1;
       // Rows of this group.
       if (quad == 0 && lane < NC) {
         const int r = c0 + lane;
         sh.negm[r] = r < it.nrows ? kNoKey : 0.0f;
-        sh.rowp[r] = r < it.nrows ? it.pos0 + (it.r0 + r) / a.H : -1;
+        sh.rowt[r] = (uint8_t)((held.r0 + r) / a.H - held.r0 / a.H);
       }
       ptx::named_sync(bar, 128);
       float l[NC];
@@ -913,18 +944,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool in = x < it.units;
         const int j = unit_key(it, in ? x : 0) + (key & 15);
         const int weff = (a.window == 0 || j < a.sinks) ? 0x7fffffff : a.window;
-        bool some = in && j <= it.p1 && it.p0 - j < weff;
-        if (some) {
-          const int pg = j / a.page_size;
-          const int page = __ldg(a.block_table + (int64_t)it.b * a.max_pages + pg);
-          if (page < 0 || (int64_t)page * a.page_size + (j - pg * a.page_size) >= a.num_slots) {
-            some = false;
-            if (a.err_flag != nullptr && h == 0) atomicOr(a.err_flag, MXQ_DEVERR_SLOT);
-          }
-        }
+        ok = wait(&sh.slot_full[g % kSlots], (g / kSlots) & 1u) && ok;
+        const int unit_slot = sh.slots[g % kSlots][key >> 4];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.slot_empty[g % kSlots]);
+        const bool some = in && j <= it.p1 && it.p0 - j < weff && unit_slot >= 0 &&
+                          (int64_t)unit_slot + (key & 15) < a.num_slots;
         const bool all = some && j <= it.p0 && it.p1 - j < weff;
         const bool mixed = __any_sync(0xffffffffu, some && !all);
-        auto sees = [&](int c) { return some && (uint32_t)(sh.rowp[c0 + c] - j) < (uint32_t)weff; };
+        auto sees = [&](int c) { return some && (uint32_t)(it.p0 + sh.rowt[c0 + c] - j) < (uint32_t)weff; };
 
         ok = wait(&sh.s_full[g & 1u], (g >> 1) & 1u) && ok;
         __syncwarp();
@@ -932,23 +960,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t s[NC];
         tmem_ld<NC>(tq + kTmemS + (g & 1u) * 64 + c0, s);
         ptx::tmem_ld_wait();
-        // The largest score over the running maxima, NaN if there is one: a
-        // cache row with a NaN or an infinity has no finite score at all.
-        float top = -INFINITY, seen = -INFINITY;
+        // Exponents d = s + negm in place of the scores.  Their largest is NaN
+        // if one is: a cache row with a NaN or an infinity has no finite score.
+        float d[NC], top, seen = -INFINITY;
+        auto exponents = [&]() {
+          top = -INFINITY;
 #pragma unroll
-        for (int q = 0; q < NC / 4; ++q) {
-          const float4 n = negm4[q];
-          const float4 cr = BF ? make_float4(c_all, c_all, c_all, c_all) : crow4[q];
-          const float d[4] = {fmaf(__uint_as_float(s[4 * q]), cr.x, n.x), fmaf(__uint_as_float(s[4 * q + 1]), cr.y, n.y),
-                              fmaf(__uint_as_float(s[4 * q + 2]), cr.z, n.z),
-                              fmaf(__uint_as_float(s[4 * q + 3]), cr.w, n.w)};
+          for (int q = 0; q < NC / 4; ++q) {
+            const float4 n = negm4[q];
+            const float4 cr = BF ? make_float4(c_all, c_all, c_all, c_all) : crow4[q];
+            d[4 * q] = fmaf(__uint_as_float(s[4 * q]), cr.x, n.x);
+            d[4 * q + 1] = fmaf(__uint_as_float(s[4 * q + 1]), cr.y, n.y);
+            d[4 * q + 2] = fmaf(__uint_as_float(s[4 * q + 2]), cr.z, n.z);
+            d[4 * q + 3] = fmaf(__uint_as_float(s[4 * q + 3]), cr.w, n.w);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top = max_nan(top, d[e]);
-          if (mixed) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) seen = fmaxf(seen, sees(4 * q + e) ? d[e] : -INFINITY);
+            for (int e = 0; e < 4; ++e) top = max_nan(top, d[4 * q + e]);
           }
-        }
+        };
+        exponents();
+        if (mixed)
+#pragma unroll
+          for (int c = 0; c < NC; ++c) seen = fmaxf(seen, sees(c) ? d[c] : -INFINITY);
         const bool bad = in && !(fabsf(top) <= 3.4028234e38f);
         const bool raise = bad || (some && (mixed ? seen : top) > kSlack + kShift);
         if (named_any(bar, 128, raise || !ok)) {
@@ -979,7 +1011,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
           }
-          float mx[NC];
+          // The scores again (s is not kept: registers), and their maxima.
+          tmem_ld<NC>(tq + kTmemS + (g & 1u) * 64 + c0, s);
+          ptx::tmem_ld_wait();
 #pragma unroll
           for (int q = 0; q < NC / 4; ++q) {
             const float4 cr4 = BF ? make_float4(c_all, c_all, c_all, c_all) : crow4[q];
@@ -990,14 +1024,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float v = __uint_as_float(s[c]);
               const bool fin = fabsf(v) <= 3.4028234e38f;
               const bool see = mixed ? sees(c) : all;
-              if (bad && !fin) {
-                if (see) l[c] = NAN;
-                s[c] = __float_as_uint(copysignf(INFINITY, -cr[e]));  // weight 0 below
-              }
-              mx[c] = see && fin ? v * cr[e] : -INFINITY;
+              if (bad && !fin && see) l[c] = NAN;
+              d[c] = see && fin ? v * cr[e] : -INFINITY;
             }
           }
-          const float m = lanes_reduce<NC, true>(mx);
+          const float m = lanes_reduce<NC, true>(d);
           if (lane < NC) sh.red[h][quad][lane] = m;
           ptx::named_sync(bar, 128);
           if (quad == 0 && lane < NC) {
@@ -1016,6 +1047,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             sh.scale[r] = f;
           }
           ptx::named_sync(bar, 128);
+          exponents();
+          if (bad)
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              if (!(fabsf(__uint_as_float(s[c])) <= 3.4028234e38f)) d[c] = -INFINITY;
           if (blk > it.blk0) {
             bool moved = false;
 #pragma unroll
@@ -1052,23 +1088,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < NC / 8; ++q) {
           uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            const float4 n4 = negm4[q * 2 + e / 2];
-            const float4 cr4 = BF ? make_float4(c_all, c_all, c_all, c_all) : crow4[q * 2 + e / 2];
-            const float n[4] = {n4.x, n4.y, n4.z, n4.w}, cr[4] = {cr4.x, cr4.y, cr4.z, cr4.w};
-            float p[4];
+          for (int e = 0; e < 4; ++e) {
+            float p[2];
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
+            for (int f = 0; f < 2; ++f) {
               const int c = q * 8 + e * 2 + f;
-              p[f] = ex2(fmaf(__uint_as_float(s[c]), cr[f], n[f]));
               const bool see = mixed ? sees(c) : all;
-              p[f] = see ? p[f] : 0.0f;
+              p[f] = see ? ex2(d[c]) : 0.0f;
               l[c] += p[f];
             }
             hi[e] = pack16(BF, p[0], p[1]);
-            hi[e + 1] = pack16(BF, p[2], p[3]);
             lo[e] = pack16_rest(BF, p[0], p[1], hi[e]);
-            lo[e + 1] = pack16_rest(BF, p[2], p[3], hi[e + 1]);
           }
           const int col = (c0 >> 3) + q;
           uint8_t* row = sm_p + key * 128;
@@ -1102,18 +1132,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sum = (sh.red[h][0][lane] + sh.red[h][1][lane]) + (sh.red[h][2][lane] + sh.red[h][3][lane]);
         const float nm = sh.negm[r];
         if (k.splits > 1 && has) {
-          k.part_ml[((int64_t)it.tile * k.splits + it.split) * NR + r] = make_float2(-nm, sum);
+          k.part_ml[((int64_t)held.tile * k.splits + held.split) * NR + r] = make_float2(-nm, sum);
         } else {
           const float vs = DT == MXQ_CACHE_E4M3 ? __ldg(a.kv_scale) : 1.0f;
           sh.scale[r] = sum == 0.0f ? 0.0f : vs / sum;
           if (r < it.nrows && a.lse != nullptr)
-            a.lse[it.qrow + r] = sum == 0.0f ? -INFINITY : (log2f(sum) - nm) * 0.6931471805599453f;
+            a.lse[held.qrow + r] = sum == 0.0f ? -INFINITY : (log2f(sum) - nm) * 0.6931471805599453f;
         }
       }
       ptx::named_sync(bar, 128);
       if (k.splits > 1 && has) {
         // Partial sums as they are: a warp stores 32 consecutive columns of a row.
-        float* dst = k.part + (((int64_t)it.tile * k.splits + it.split) * NR + c0) * D + key;
+        float* dst = k.part + (((int64_t)held.tile * k.splits + held.split) * NR + c0) * D + key;
         for (int m = 0; m < np; ++m) {
           uint32_t o[NC];
           tmem_ld<NC>(tq + m * NV + c0, o);
@@ -1145,7 +1175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int q = 0; q < NC / 8; ++q)
           sc[q] = *reinterpret_cast<const float2*>(&sh.scale[c0 + q * 8 + (lane & 3) * 2]);
-        uint8_t* dst = static_cast<uint8_t*>(a.out) + (it.qrow + c0) * D * 2;
+        uint8_t* dst = static_cast<uint8_t*>(a.out) + (held.qrow + c0) * D * 2;
         for (int m0 = 0; m0 < np; m0 += 2) {
           for (int m = m0; m < min(m0 + 2, np); ++m)
 #pragma unroll
@@ -1185,6 +1215,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Both groups are done with the P buffers.
         ptx::named_sync(3, 256);
       }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sh.item_empty[ni % kItems]);
       ptx::tc_fence_before();
     }
   }
