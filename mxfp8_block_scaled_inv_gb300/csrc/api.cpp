@@ -581,7 +581,7 @@ int mxq_attn(const void* q_bf16, int64_t T, int32_t H, int32_t D, const int32_t*
   int sms = 0;
   if (int st = device_check(&sms)) return st;
   const char* why = nullptr;
-  cudaError_t e = mxq::launch_attn(a, ws, sms, static_cast<cudaStream_t>(stream), &why);
+  cudaError_t e = mxq::launch_attn(a, ws, static_cast<cudaStream_t>(stream), &why);
   if (e != cudaSuccess && why) return fail(MXQ_ERR_CUDA, "attn: %s", why);
   return cuda_status(e, "attn launch");
 }

@@ -22,20 +22,28 @@
 // that most blocks need neither a cross-lane maximum nor a rescale of O.
 // Row sums are kept per thread (one key each) in FP32 and joined at the end.
 //
-// Warps: 0-7 softmax and epilogue (a lane is a key, then a column; the two
-// groups of four own half of the tile's rows each and never wait for one
-// another), 8 issues the matrix instructions, 9 the TMA copies of BF16 rows, 10
-// decodes the work items, 12-15 fetch Q and the cache rows that are widened to
-// 16 bits, into the 128-byte-swizzled layout.
+// Warps: NR / 4 for the softmax and the epilogue (a lane is a key, then a
+// column; each group of four owns 16 of the tile's rows and never waits for
+// another), one that issues the matrix instructions, one for the TMA copies of
+// BF16 rows, one that hands out the work items, one that looks up the block
+// table, and the loading warps, which fetch Q and the cache rows that are
+// widened to 16 bits, into the 128-byte-swizzled layout.
 //
-// E4M3 rows are widened to FP16 (exact), with the query scaled per row by a
-// power of two into FP16's range (exact for all values within 2^24 of the
-// row's largest) and P shifted by 2^6; BF16 and E2M1 rows and their P are
-// BF16 (E2M1 times its scale is exact in BF16).  P's rounding (2^-9 in BF16)
-// is of the order of the output's own.
+// All operands of the products are BF16: E4M3 and E2M1 rows are widened exactly
+// (E2M1 with its scale, E4M3 without: its per-tensor scale goes into the scores
+// and the output).
 //
-// When there are fewer tiles than SMs the keys of a tile are split over
-// several CTAs, whose FP32 partial sums a second kernel joins in a fixed order.
+// P would lose to its rounding as much as the output to its own.  So what is
+// left of a weight after rounding multiplies its row too, as a second 16-bit
+// part, wherever the weight is at least 1/16 of its row's sum so far; below
+// that it is rounded once (by 2^-8 of 1/16 of the sum at most).  An item's first
+// two blocks, whose sums are not known yet, have second parts throughout.
+//
+// Work: with many tiles per SM, whole tiles are dealt out, those with the most
+// keys first.  Else the key blocks of all tiles, in one line, are cut into
+// equal shares, one per CTA; a tile that is cut leaves FP32 partial sums, which
+// a second kernel joins in the order of the keys.  Both follow from the
+// lengths on the device, so ragged batches stay balanced.
 //
 // Every wait is bounded in wall time; on expiry the kernel sets a watchdog
 // bit, stops, waits for the matrix instructions in flight, frees TMEM and
@@ -69,16 +77,23 @@ constexpr int kUnit = 16;            // keys of a unit
 constexpr int kUnits = kKeys / kUnit;
 constexpr int kChunkBytes = kKeys * 128;   // 128 keys x 64 columns of 16 bits
 constexpr int kStageBytes = 2 * kChunkBytes;
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kItemWarp = 10, kUnitWarp = 11,
-              kLoadWarp0 = 12, kLoadWarps = 4;
-constexpr int kThreads = (kLoadWarp0 + kLoadWarps) * 32;
-// Registers per thread: 128 at launch; softmax 168, the issuing warps 40, the
-// loading warps 136.  Nothing spills: with 227 KB of shared memory in use the
+// Thread layout and registers (launch registers x threads is what setmaxnreg
+// deals out again).  Nothing spills: with 227 KB of shared memory in use the
 // L1 cache is too small for local memory.
-constexpr int kRegsSoft = 168, kRegsIssue = 40, kRegsLoad = 136;
-static_assert(256 * kRegsSoft + 128 * kRegsIssue + 128 * kRegsLoad <= kThreads * 128, "register pool");
-constexpr int kLoadThreads = kLoadWarps * 32;
-constexpr int kMaxStages = 6;
+template <int NR>
+struct Roles {
+  static constexpr int GROUPS = NR / 16;         // softmax groups of 4 warps, 16 rows each
+  static constexpr int SOFT = 4 * GROUPS;        // their warps
+  static constexpr int MMA = SOFT, TMA = SOFT + 1, ITEM = SOFT + 2, UNIT = SOFT + 3;
+  static constexpr int LOAD0 = SOFT + 4, LOADS = 8;
+  static constexpr int THREADS = (LOAD0 + LOADS) * 32;
+  static constexpr int REGS = 65536 / THREADS / 8 * 8;
+  static constexpr int REGS_SOFT = NR == 64 ? 88 : 112, REGS_ISSUE = NR == 64 ? 56 : 64,
+                       REGS_LOAD = NR == 64 ? 48 : NR == 32 ? 88 : 128;
+  static_assert(SOFT * 32 * REGS_SOFT + 128 * REGS_ISSUE + LOADS * 32 * REGS_LOAD <= THREADS * REGS, "register pool");
+};
+constexpr int kLoadThreads = 256;
+constexpr int kMaxStages = 5;
 constexpr uint32_t kTmemCols = 512, kTmemS = 256;
 constexpr float kNoKey = 1e30f;      // negm of a row that has seen no key
 constexpr float kSlack = 8.0f;       // log2 of how far a score may pass the maximum
@@ -86,25 +101,29 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 struct KernelArgs {
   AttnArgs a;
-  float* part;      // split form: [tiles][splits][NR][D] partial sums
-  float2* part_ml;  // [tiles][splits][NR] (maximum, sum)
+  float* part;      // [2 * gridDim][NR][D] partial sums of tiles that are cut
+  float2* part_ml;  // [2 * gridDim][NR] (maximum, sum)
+  int4* desc;       // [2 * gridDim]: first row (low, high), rows, flags
   uint32_t* watchdog;
-  int tiles, splits, stages, items;
+  int shares;       // 1: blocks in equal shares; 0: whole tiles
+  int stages;
 };
+constexpr int kPieceUsed = 1, kPieceEnds = 2;  // flags of a piece
 
 __host__ __device__ constexpr int q_bytes(int NR, int D) { return NR * D * 2; }
 
-// What one work item (a tile and a share of its key blocks) covers.
+// What one work item (a tile, or a piece of its key blocks) covers.
 struct alignas(16) Item {
   int b, r0, nrows, pos0;  // sequence, first row in it, rows, position of its first new token
   int p0, p1;              // positions of the tile's first and last row
   int u_lo, ns;            // first unit of the window, units of the sinks
   int units, blk0, blk1;   // units in all; this item's blocks of 8
-  int tile, split, pad;
+  int piece;               // its slot among the partial sums, or -1: the whole tile
   int64_t qrow;            // first row of the tile in [T*H]
+  int64_t pad;
 };
 static_assert(sizeof(Item) == 64, "four 16-byte words");
-constexpr int kItems = 4;  // items handed out ahead
+constexpr int kItems = 3;  // items handed out ahead
 constexpr int kSlots = 4;  // blocks whose units are looked up ahead
 
 struct Shared {
@@ -114,11 +133,12 @@ struct Shared {
   int abort;
   alignas(16) Item items[kItems];
   int slots[kSlots][kUnits];  // cache row of each unit's first key, -1: none
-  float crow[3][64];
-  float negm[64];
+  alignas(16) float negm[64];
+  float lthr[64];   // log2 of the weight from which the second part counts
   float scale[64];  // the rescale factors of a block; in the epilogue 1 / sum
   uint8_t rowt[64];  // a row's token, counted from the tile's first
-  float red[2][4][32];
+  uint8_t hot[4][4];  // per group and quarter: units with such a weight (2 bits)
+  float red[4][4][16];
 };
 
 // The weights P are held as two 16-bit parts, hi + lo: for NR <= 32 side by
@@ -134,70 +154,185 @@ inline int stages_for(int NR, int D) {
 }
 static_assert(smem_fixed(64, 512) + 4 * kStageBytes <= kSmemBudget, "a block of the widest rows fits");
 
-__device__ __forceinline__ int seq_start(const AttnArgs& a, int b) {
-  return a.q_start != nullptr ? __ldg(a.q_start + b) : b;
-}
-
-// Called by whole warps.
+// A sequence: its first token, new tokens and keys.  Up to 32 at a time, one per lane.
+struct Seq {
+  int start, n, len, tiles;
+  bool clamped;
+};
 template <int NR>
-__device__ __forceinline__ Item get_item(const KernelArgs& k, int item) {
-  const AttnArgs& a = k.a;
+__device__ __forceinline__ Seq get_seq(const AttnArgs& a, int b) {
+  Seq s = {0, 0, 0, 0, false};
+  if (b < 0 || b >= a.B) return s;
+  s.start = a.q_start != nullptr ? max(__ldg(a.q_start + b), 0) : b;
+  const int end = a.q_start != nullptr ? (int)min((int64_t)__ldg(a.q_start + b + 1), a.T) : b + 1;
+  s.n = max(end - s.start, 0);
+  const int said = __ldg(a.seq_lens + b);
+  s.len = min(max(said, 0), a.max_pages * a.page_size);
+  s.clamped = said != s.len;
+  s.tiles = (int)(((int64_t)s.n * a.H + NR - 1) / NR);
+  return s;
+}
+__device__ __forceinline__ Seq lane_seq(const Seq& s, int lane) {
+  Seq r;
+  r.start = __shfl_sync(0xffffffffu, s.start, lane);
+  r.n = __shfl_sync(0xffffffffu, s.n, lane);
+  r.len = __shfl_sync(0xffffffffu, s.len, lane);
+  r.tiles = __shfl_sync(0xffffffffu, s.tiles, lane);
+  r.clamped = __shfl_sync(0xffffffffu, (int)s.clamped, lane) != 0;
+  return r;
+}
+// Tile t of a sequence: everything but its blocks and its piece.
+template <int NR>
+__device__ __forceinline__ Item get_tile(const AttnArgs& a, const Seq& s, int b, int t) {
   Item it;
-  it.split = item / k.tiles;
-  // Later tiles of a chunk see more keys: they go first.
-  it.tile = k.tiles - 1 - (item - it.split * k.tiles);
-  // Tiles are numbered so that sequence b begins at floor(start_b * H / NR) + b:
-  // each has at least as many numbers as tiles, without a prefix sum.
-  const int lane = threadIdx.x & 31;
-  int b = 0;
-  if (a.q_start == nullptr && NR >= 1) {
-    // start_b = b: the number of b's whose first tile is at or before this one.
-    const int64_t t = it.tile;
-    b = (int)min((int64_t)a.B - 1, t * NR / (a.H + NR));
-    while (b + 1 < a.B && ((int64_t)(b + 1) * a.H) / NR + b + 1 <= t) ++b;
-    while (b > 0 && ((int64_t)b * a.H) / NR + b > t) --b;
-  } else {
-    for (int base = 0; base < a.B; base += 32) {
-      const int i = base + lane;
-      const bool before =
-          i < a.B && ((int64_t)max(__ldg(a.q_start + min(i, a.B - 1)), 0) * a.H) / NR + i <= it.tile;
-      const int c = __popc(__ballot_sync(0xffffffffu, before));
-      if (c == 0) break;
-      b = base + c - 1;
-      if (c < 32) break;
-    }
-  }
   it.b = b;
-  const int start = max(seq_start(a, b), 0);
-  const int end = (int)min((int64_t)seq_start(a, b + 1), a.T);
-  const int n = max(end - start, 0);
-  const int cap = a.max_pages * a.page_size;
-  const int said = __ldg(a.seq_lens + b), len = min(max(said, 0), cap);
-  const int64_t r0 = ((int64_t)it.tile - b - ((int64_t)start * a.H) / NR) * NR;
-  const int64_t rows = (int64_t)n * a.H;
-  it.pos0 = len - n;
-  it.pad = said != len;
-  it.nrows = r0 >= 0 && r0 < rows ? (int)min((int64_t)NR, rows - r0) : 0;
-  it.r0 = (int)r0;
-  it.qrow = (int64_t)start * a.H + r0;
+  it.pos0 = s.len - s.n;
+  it.r0 = t * NR;
+  it.nrows = min(NR, s.n * a.H - it.r0);
+  it.qrow = (int64_t)s.start * a.H + it.r0;
+  it.p0 = it.pos0 + it.r0 / a.H;
+  it.p1 = it.pos0 + (it.r0 + it.nrows - 1) / a.H;
   it.units = it.ns = it.u_lo = it.blk0 = it.blk1 = 0;
-  it.p0 = it.p1 = -1;
-  if (it.nrows > 0) {
-    it.p0 = it.pos0 + it.r0 / a.H;
-    it.p1 = it.pos0 + (it.r0 + it.nrows - 1) / a.H;
-    if (it.p1 >= 0) {
-      const int lo = a.window > 0 ? max(0, it.p0 - a.window + 1) : 0;
-      it.u_lo = lo / kUnit;
-      const int sink_end = a.window > 0 ? min(a.sinks, lo) : 0;
-      it.ns = min((sink_end + kUnit - 1) / kUnit, it.u_lo);
-      it.units = it.ns + it.p1 / kUnit + 1 - it.u_lo;
-      const int nb = (it.units + kUnits - 1) / kUnits;
-      const int per = (nb + k.splits - 1) / k.splits;
-      it.blk0 = min(nb, it.split * per);
-      it.blk1 = min(nb, it.blk0 + per);
-    }
+  it.piece = -1;
+  it.pad = 0;
+  if (it.p1 >= 0) {
+    const int lo = a.window > 0 ? max(0, it.p0 - a.window + 1) : 0;
+    it.u_lo = lo / kUnit;
+    const int sink_end = a.window > 0 ? min(a.sinks, lo) : 0;
+    it.ns = min((sink_end + kUnit - 1) / kUnit, it.u_lo);
+    it.units = it.ns + it.p1 / kUnit + 1 - it.u_lo;
   }
   return it;
+}
+__device__ __forceinline__ int blocks_of(const Item& it) { return (it.units + kUnits - 1) / kUnits; }
+// What a tile weighs in the shares: its blocks; one that sees no key still has
+// its rows to write.
+template <int NR>
+__device__ __forceinline__ int tile_weight(const AttnArgs& a, const Seq& s, int t) {
+  return max(1, blocks_of(get_tile<NR>(a, s, 0, t)));
+}
+__device__ __forceinline__ int warp_sum(int v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// Weight of each lane's sequence.  Lanes work side by side on their own
+// sequence, or, when one has many tiles, together on one after the other.
+template <int NR>
+__device__ __forceinline__ int seq_weight(const AttnArgs& a, const Seq& s) {
+  const int lane = threadIdx.x & 31;
+  int w = 0;
+  if (__reduce_max_sync(0xffffffffu, s.tiles) <= 16) {
+    for (int t = 0; t < s.tiles; ++t) w += tile_weight<NR>(a, s, t);
+    __syncwarp();
+  } else {
+    for (int l = 0; l < 32; ++l) {
+      const Seq o = lane_seq(s, l);
+      int part = 0;
+      for (int t = lane; t < o.tiles; t += 32) part += tile_weight<NR>(a, o, t);
+      __syncwarp();
+      part = warp_sum(part);
+      if (lane == l) w = part;
+    }
+  }
+  return w;
+}
+
+// The work items of this CTA, in order, given to `emit` (whole warp).
+template <int NR, typename Emit>
+__device__ __forceinline__ void walk_items(const KernelArgs& k, Emit emit) {
+  const AttnArgs& a = k.a;
+  const int lane = threadIdx.x & 31;
+  if (!k.shares) {
+    // Tiles counted from the last: later tiles of a chunk see more keys.
+    int before = 0, id = blockIdx.x;
+    for (int base = (a.B - 1) & ~31; base >= 0; base -= 32) {
+      const Seq s = get_seq<NR>(a, base + lane);
+      // Tiles of this and the later sequences of the group.
+      int upto = s.tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_down_sync(0xffffffffu, upto, o);
+        if (lane + o < 32) upto += v;
+      }
+      const int group = __shfl_sync(0xffffffffu, upto, 0);
+      for (; id < before + group; id += gridDim.x) {
+        // The last sequence whose count passes the number sought.
+        const int l = 31 - __clz((int)__ballot_sync(0xffffffffu, upto > id - before));
+        const Seq o = lane_seq(s, l);
+        const int u = __shfl_sync(0xffffffffu, upto, l);
+        Item it = get_tile<NR>(a, o, base + l, u - 1 - (id - before));
+        it.blk1 = blocks_of(it);
+        it.pad = o.clamped;
+        if (!emit(it)) return;
+      }
+      before += group;
+    }
+    return;
+  }
+  // Equal shares of all blocks; two at least, since a cut costs about one.
+    Seq s = get_seq<NR>(a, lane);
+  int mine = seq_weight<NR>(a, s);
+  int total = warp_sum(mine);
+  for (int base = 32; base < a.B; base += 32) total += warp_sum(seq_weight<NR>(a, get_seq<NR>(a, base + lane)));
+  int share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+  if (share < 2) share = 2;
+  int pos = (int)min((int64_t)share * blockIdx.x, (int64_t)total);
+  const int end = pos + min(share, total - pos);
+  if (lane < 2) k.desc[2 * blockIdx.x + lane] = make_int4(0, 0, 0, 0);
+  __syncwarp();
+  int run = 0;  // weight of the sequences before the group
+  for (int base = 0; base < a.B && pos < end; base += 32) {
+    if (base > 0) {
+      s = get_seq<NR>(a, base + lane);
+      mine = seq_weight<NR>(a, s);
+    }
+    const int group = warp_sum(mine);
+    if (pos >= run + group) {
+      run += group;
+      continue;
+    }
+    for (int l = 0; l < 32 && pos < end; ++l) {
+      const int w = __shfl_sync(0xffffffffu, mine, l);
+      if (pos >= run + w) {
+        run += w;
+        continue;
+      }
+      const Seq o = lane_seq(s, l);
+      // Skip tiles before pos, 32 at a time.
+      int t = 0;
+      int at = run;  // weight before tile t
+      while (true) {
+        const int tw = t + lane < o.tiles ? tile_weight<NR>(a, o, t + lane) : 0;
+        const int sum = warp_sum(tw);
+        if (at + sum > pos || t + 32 >= o.tiles) break;
+        at += sum;
+        t += 32;
+      }
+      for (; t < o.tiles && pos < end; ++t) {
+        Item it = get_tile<NR>(a, o, base + l, t);
+        const int nb = blocks_of(it), tw = max(nb, 1);
+        if (pos < at + tw) {
+          const int lo = pos - at, hi = min(tw, end - at);
+          it.blk0 = min(lo, nb);
+          it.blk1 = min(hi, nb);
+          it.pad = o.clamped;
+          if (lo > 0 || hi < tw) {
+            // Slot 2c: the rest of a tile that an earlier CTA began; slot
+            // 2c + 1: the beginning of one that the next CTA goes on with.
+            it.piece = 2 * blockIdx.x + (lo == 0 ? 1 : 0);
+            if (lane == 0)
+              k.desc[it.piece] = make_int4((int)(uint32_t)it.qrow, (int)(it.qrow >> 32), it.nrows,
+                                           kPieceUsed | (hi == tw ? kPieceEnds : 0));
+          }
+          if (!emit(it)) return;
+          pos = at + hi;
+        }
+        at += tw;
+      }
+      run += w;
+    }
+  }
 }
 
 // First key of unit x of the item.
@@ -229,11 +364,10 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
 }
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (ptx::kSwizzle128B << 29);
 
-// Instruction descriptor of kind::f16: FP32 accumulation, both operands BF16
-// (1) or FP16 (0), M = 128, N, and whether A and B are stored with M / N
-// running fastest.
-__host__ __device__ constexpr uint32_t idesc_f16(bool bf16, int N, bool a_mn, bool b_mn) {
-  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+// Instruction descriptor of kind::f16: FP32 accumulation, both operands BF16,
+// M = 128, N, and whether A and B are stored with M / N running fastest.
+__host__ __device__ constexpr uint32_t idesc_bf16(int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) |
          ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
 }
 
@@ -331,27 +465,19 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t pack16(bool bf16, float lo, float hi) {
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
-  if (bf16)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// What is left of two values after pack16, packed the same way.
-__device__ __forceinline__ uint32_t pack16_rest(bool bf16, float lo, float hi, uint32_t w) {
-  if (bf16) return pack16(true, lo - bf16_lo(w), hi - bf16_hi(w));
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-  return pack16(false, lo - f.x, hi - f.y);
+// What is left of two values after pack2, packed the same way.
+__device__ __forceinline__ uint32_t pack2_rest(float lo, float hi, uint32_t w) {
+  return pack2(lo - bf16_lo(w), hi - bf16_hi(w));
 }
-template <int N>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+template <int N, int LAUNCH>
+__device__ __forceinline__ void regs_set() {
+  if constexpr (N > LAUNCH) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  if constexpr (N < LAUNCH) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1) {
   asm volatile(
@@ -362,17 +488,31 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uin
 }
 
 // --------------------------------------------------------------- widening
-// 16 E4M3 codes -> 16 FP16 values (exact).
-__device__ __forceinline__ void widen_e4m3(const uint4& v, uint4& lo, uint4& hi) {
-  uint32_t o[8];
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// 8 E4M3 codes -> 8 BF16 values (exact), without the conversion unit, whose 16
+// results a cycle would bound the kernel: a code's exponent and significand,
+// moved to BF16's places, stand for the value times 2^-120 (subnormals too).
+// NaN codes are the caller's (e4m3_has_nan).
+__device__ __forceinline__ uint4 widen_e4m3(uint32_t a, uint32_t b) {
+  uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o[2 * i]) : "h"((uint16_t)(w[i] & 0xFFFFu)));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o[2 * i + 1]) : "h"((uint16_t)(w[i] >> 16)));
+    const uint32_t r = __byte_perm(i < 2 ? a : b, 0, (i & 1) ? 0x3424 : 0x1404);  // codes in the high bytes
+    const uint32_t m = ((r >> 4) & 0x07F007F0u) | (r & 0x80008000u);
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(m), "r"(0x7B807B80u));  // 2^120
   }
-  lo = make_uint4(o[0], o[1], o[2], o[3]);
-  hi = make_uint4(o[4], o[5], o[6], o[7]);
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ bool e4m3_has_nan(const uint4& v) {
+  const uint32_t k = 0x7F7F7F7Fu, one = 0x01010101u;
+  return ((((v.x & k) + one) | ((v.y & k) + one) | ((v.z & k) + one) | ((v.w & k) + one)) & 0x80808080u) != 0;
+}
+// BF16 NaNs in the places of NaN codes.
+__device__ __forceinline__ uint4 put_nans(uint4 o, uint32_t a, uint32_t b) {
+  uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if ((((i < 4 ? a : b) >> (8 * (i & 3))) & 0x7Fu) == 0x7Fu) w[i >> 1] |= 0x7FFFu << (16 * (i & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Table of the eight magnitudes times 2^(sb - 127) as BF16, split into low and
@@ -412,16 +552,14 @@ __device__ __forceinline__ uint2 widen_e2m1x4(uint32_t w, const E2m1Table& t) {
 
 // Cache rows that a loading thread handles in every block.
 template <int DT>
-constexpr int kRowsPerThread = DT == MXQ_CACHE_E4M3 ? 8 : 4;
+constexpr int kRowsPerThread = DT == MXQ_CACHE_E4M3 ? 4 : 2;
 
 // ------------------------------------------------------------------ kernel
 template <int NR, int DT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const KernelArgs k) {
-  constexpr bool BF = DT != MXQ_CACHE_E4M3;  // operand type: BF16, else FP16
-  constexpr int NC = NR / 2;                 // rows of a softmax group
-  constexpr int NV = NR == 64 ? 64 : 2 * NR; // N of the second product
-  constexpr float kShift = BF ? 0.0f : 6.0f;
+  using R = Roles<NR>;
+  constexpr int NC = 16;                     // rows of a softmax group
   extern __shared__ __align__(1024) uint8_t base[];
   const AttnArgs& a = k.a;
   const int D = a.D, nch = D >> 6, np = (nch + 1) >> 1;
@@ -440,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ptx::mbar_init(&sh.s_full[0], 1);
     ptx::mbar_init(&sh.s_full[1], 1);
-    ptx::mbar_init(&sh.p_full, kSoftWarps * 32);
+    ptx::mbar_init(&sh.p_full, R::SOFT * 32);
     ptx::mbar_init(&sh.pv_done, 1);
     for (int s = 0; s < 4; ++s) ptx::mbar_init(&sh.q_full[s], kLoadThreads);
     ptx::mbar_init(&sh.q_empty, 1);
@@ -448,15 +586,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kItems; ++i) {
       ptx::mbar_init(&sh.item_full[i], 1);
       // Readers: the softmax, loading, issuing and unit warps, and the TMA warp.
-      ptx::mbar_init(&sh.item_empty[i], kSoftWarps + kLoadWarps + 2 + (DT == MXQ_CACHE_BF16 ? 1 : 0));
+      ptx::mbar_init(&sh.item_empty[i], R::SOFT + R::LOADS + 2 + (DT == MXQ_CACHE_BF16 ? 1 : 0));
     }
     for (int i = 0; i < kSlots; ++i) {
       ptx::mbar_init(&sh.slot_full[i], 1);
-      ptx::mbar_init(&sh.slot_empty[i], kSoftWarps + (DT == MXQ_CACHE_BF16 ? 1 : kLoadWarps));
+      ptx::mbar_init(&sh.slot_empty[i], R::SOFT + (DT == MXQ_CACHE_BF16 ? 1 : R::LOADS));
     }
     ptx::fence_barrier_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == R::MMA) {
     ptx::tmem_alloc(&sh.tmem, kTmemCols);
     ptx::tmem_relinquish();
   }
@@ -497,11 +635,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     return it.b >= 0;
   };
 
-  if (warp >= kLoadWarp0) {
+  if (warp >= R::LOAD0) {
     // ------------------------------------- the query, and rows to be widened
-    regs_up<kRegsLoad>();
-    const int lt = tid - kLoadWarp0 * 32, lw = lt >> 5;
-    const float kvs = DT == MXQ_CACHE_E4M3 ? __ldg(a.kv_scale) : 1.0f;
+    regs_set<R::REGS_LOAD, R::REGS>();
+    const int lt = tid - R::LOAD0 * 32, lw = lt >> 5;
     int nq = 0;                // items with blocks so far
     [[maybe_unused]] uint32_t nb = 0;  // blocks so far
     [[maybe_unused]] uint32_t st = 0, stp = 0;  // stage and its phase
@@ -511,54 +648,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it.blk0 >= it.blk1) continue;
       // Q rows, one per warp and step; rows past the tile's are zeros.
       if (nq > 0 && !(ok = wait_warp(&sh.q_empty, (uint32_t)(nq - 1) & 1u))) break;
-      for (int r0 = lw; r0 < NR; r0 += 4 * kLoadWarps) {
-        uint4 v[4][2];
+      for (int r0 = lw; r0 < NR; r0 += 2 * R::LOADS) {
+        uint4 v[2][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             v[i][c] = make_uint4(0, 0, 0, 0);
-            const int pc = c * 32 + lane, r = r0 + i * kLoadWarps;
+            const int pc = c * 32 + lane, r = r0 + i * R::LOADS;
             if (pc < nch * 8 && r < it.nrows)
               v[i][c] = __ldg(reinterpret_cast<const uint4*>(a.q) + (it.qrow + r) * (nch * 8) + pc);
           }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = r0 + i * kLoadWarps;
-          if constexpr (!BF) {
-            // Largest magnitude of the row -> the power of two that brings it
-            // to [2^10, 2^11).
-            uint32_t mx = 0;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint32_t w[4] = {v[i][c].x, v[i][c].y, v[i][c].z, v[i][c].w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                mx = max(mx, w[e] & 0x7FFFu);
-                mx = max(mx, (w[e] >> 16) & 0x7FFFu);
-              }
-            }
-            mx = __reduce_max_sync(0xffffffffu, mx);
-            const int ex = (int)(mx >> 7);
-            int sft = ex == 255 || mx == 0 ? 0 : 137 - ex;
-            sft = min(sft, 120);
-            const float f = __uint_as_float((uint32_t)(127 + sft) << 23);
-            if (lane == 0) {
-              const float inv = __uint_as_float((uint32_t)(127 - sft) << 23);
-              sh.crow[nq % 3][r] = r < it.nrows ? a.sm_scale * kLog2e * kvs * inv : 0.0f;
-            }
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float y[8];
-              unpack8(v[i][c], y);
-              v[i][c] = make_uint4(pack16(false, y[0] * f, y[1] * f), pack16(false, y[2] * f, y[3] * f),
-                                   pack16(false, y[4] * f, y[5] * f), pack16(false, y[6] * f, y[7] * f));
-            }
-          }
+        for (int i = 0; i < 2; ++i) {
+          const int r = r0 + i * R::LOADS;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int pc = c * 32 + lane;
-            if (pc < nch * 8)
+            if (pc < nch * 8 && r < NR)
               *reinterpret_cast<uint4*>(sm_q + (pc >> 3) * (NR * 128) + r * 128 + (((pc & 7) ^ (r & 7)) << 4)) = v[i][c];
           }
         }
@@ -570,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (DT != MXQ_CACHE_BF16) {
         constexpr int RPT = kRowsPerThread<DT>;          // cache rows of this thread per block
         constexpr int TPR = kLoadThreads * RPT / kKeys;  // threads per row: 8, 4
-        constexpr int KSTEP = kKeys / RPT;               // key step between its rows: 16, 32
+        constexpr int KSTEP = kKeys / RPT;               // key step between its rows: 32, 64
         constexpr int PIECE_COLS = 128 / TPR;            // columns of a 16-byte piece: 16, 32
         const int key0 = lt / TPR, piece = lt % TPR;
         const uint32_t row_bytes = DT == MXQ_CACHE_E4M3 ? (uint32_t)D : (uint32_t)D / 2;
@@ -614,14 +721,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* d = dst + key * 128;
             const int sw = key & 7;
             if constexpr (DT == MXQ_CACHE_E4M3) {
-              uint4 lo, hi;
-              widen_e4m3(v[i], lo, hi);
               // The two chunks store their halves in opposite order, so that
               // eight lanes always cover eight different 16-byte columns.
               const int ch = piece >> 2, c0 = (piece & 3) * 2;
               d += ch * kChunkBytes;
-              *reinterpret_cast<uint4*>(d + (((c0 + ch) ^ sw) << 4)) = ch ? hi : lo;
-              *reinterpret_cast<uint4*>(d + (((c0 + 1 - ch) ^ sw) << 4)) = ch ? lo : hi;
+              uint4 x = widen_e4m3(v[i].x, v[i].y), y = widen_e4m3(v[i].z, v[i].w);
+              if (e4m3_has_nan(v[i])) {
+                x = put_nans(x, v[i].x, v[i].y);
+                y = put_nans(y, v[i].z, v[i].w);
+              }
+              *reinterpret_cast<uint4*>(d + (((c0 + ch) ^ sw) << 4)) = ch ? y : x;
+              *reinterpret_cast<uint4*>(d + (((c0 + 1 - ch) ^ sw) << 4)) = ch ? x : y;
             } else {
               const E2m1Table t = e2m1_table(sb[i]);
               const int ch = piece >> 1, c0 = (piece & 1) * 4;
@@ -644,28 +754,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             stp ^= 1u;
           }
         };
-        // The next pair is fetched before the current one is stored.
-        uint4 v[2][RPT];
-        uint32_t sb[2][RPT];
-        int left = it.blk1 - it.blk0, pr = 0;
-        if (!(ok = open_block())) break;
-        fetch(0, v[0], sb[0]);
-        auto step = [&](uint4 (&vc)[RPT], uint32_t (&sc)[RPT], uint4 (&vn)[RPT], uint32_t (&sn)[RPT]) -> bool {
-          if (++pr == np) {
-            pr = 0;
-            if (--left > 0 && !(ok = open_block())) return false;
+        // A pair is fetched as soon as the one before it has been stored; its
+        // rows are in L2 by then (the unit warp's prefetch).
+        uint4 v[RPT];
+        uint32_t sb[RPT];
+        for (int left = it.blk1 - it.blk0; left > 0 && ok; --left) {
+          if (!(ok = open_block())) break;
+          fetch(0, v, sb);
+          for (int pr = 0; pr < np; ++pr) {
+            if (!(ok = wait_warp(&sh.empty[st], stp ^ 1u))) break;
+            store(v, sb);
+            if (pr + 1 < np) fetch(pr + 1, v, sb);
           }
-          if (left > 0) fetch(pr, vn, sn);
-          if (!(ok = wait_warp(&sh.empty[st], stp ^ 1u))) return false;
-          store(vc, sc);
-          return left > 0;
-        };
-        while (step(v[0], sb[0], v[1], sb[1]) && step(v[1], sb[1], v[0], sb[0])) {
         }
       }
     }
-  } else if (warp == kTmaWarp) {
-    regs_down<kRegsIssue>();
+  } else if (warp == R::TMA) {
+    regs_set<R::REGS_ISSUE, R::REGS>();
     if constexpr (DT == MXQ_CACHE_BF16) {
       // --------------------------------- BF16 rows: copied as they are by TMA
       // Lane u < 8 copies unit u of the block, one box of 16 rows x 64 columns
@@ -703,17 +808,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < k.stages; ++s)
           if (!ptx::mbar_wait(&sh.full[s], (uint32_t)s < st ? stp : stp ^ 1u, kWaitNs / 8)) break;
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == R::MMA) {
     // ------------------------------------------------------------ products
-    regs_down<kRegsIssue>();
+    regs_set<R::REGS_ISSUE, R::REGS>();
     // Two cursors over the same sequence of blocks: the first product runs
     // ahead of the second by as much as the stages hold, two blocks at most
     // (the two S buffers).  Whatever is ready is issued, the second product
     // first, because it frees stages.
     const uint32_t dk0 = desc_lo(ptx::smem_u32(sm_stage), 16), dv0 = desc_lo(ptx::smem_u32(sm_stage), kChunkBytes);
     const uint32_t dp0 = desc_lo(ptx::smem_u32(sm_p), kChunkBytes), dq0 = desc_lo(ptx::smem_u32(sm_q), 16);
-    constexpr uint32_t idesc_s = idesc_f16(BF, NR, false, false);
-    constexpr uint32_t idesc_o = idesc_f16(BF, NV, true, true);
+    constexpr uint32_t kLoPart = (NR == 64 ? kKeys * 128 : NR * 2) >> 4;  // of P, in 16 bytes
+    constexpr uint32_t idesc_s = idesc_bf16(NR, false, false);
+    constexpr uint32_t idesc_o = idesc_bf16(NR, true, true), idesc_lo = idesc_bf16(NC, true, true);
     // Items are read without blocking: those that see no key have nothing for
     // this warp, and the others may only move on once it has issued what is ready.
     uint32_t ni = 0;
@@ -721,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int qleft = 0, pleft = 0;         // blocks left of the two cursors' items
     int punits = 0, nwait = 0;        // units left of the second's; items it still has to begin,
     int wl0 = 0, wu0 = 0, wl1 = 0, wu1 = 0;  // at most two: it is two blocks behind at most
-    bool pfirst = true;
+    int pdone = 0;                    // blocks of the second cursor's item that are behind it
     uint32_t gq = 0, gp = 0, nqi = 0;     // blocks issued by each, items begun
     uint32_t qs = 0, qsp = 0, ps = 0;     // stages of the two cursors
     int qpair = 0;
@@ -756,16 +862,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (gp < gq && ready(&sh.p_full, gp & 1u)) {
         ptx::tc_fence_after();
         const int kk = min(kUnits, punits);  // units in use
+        // Read before the products are issued: behind them a load waits for
+        // the tensor pipe (measured: 7500 instead of 1700 cycles a block).
+        uint32_t hot = 0;  // bit 8 q + u: group q, unit u
+        if (pdone >= 2)
+#pragma unroll
+          for (int q = 0; q < R::GROUPS; ++q) {
+            // Byte i holds the units 2i and 2i + 1 in its low bits.
+            const uint32_t w = *reinterpret_cast<const volatile uint32_t*>(sh.hot[q]);
+            hot |= ((w | (w >> 6) | (w >> 12) | (w >> 18)) & 0xFFu) << (8 * q);
+          }
+        hot &= 0x01010101u * ((1u << kk) - 1u);
         for (int m = 0; m < np; ++m) {
           if (ptx::elect_one()) {
             const uint32_t da = dv0 + ps * (kStageBytes >> 4);
-            const uint32_t dd = tmem + m * NV;
+            const uint32_t dd = tmem + m * NR;
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) {
               if (u >= kk) break;
-              mma_f16(dd, da + u * 128, kDescHi, dp0 + u * 128, kDescHi, idesc_o, (pfirst && u == 0) ? 0u : 1u);
-              if (NR == 64)  // the low parts, a buffer of their own
-                mma_f16(dd, da + u * 128, kDescHi, dp0 + (kKeys * 8) + u * 128, kDescHi, idesc_o, 1u);
+              mma_f16(dd, da + u * 128, kDescHi, dp0 + u * 128, kDescHi, idesc_o, (pdone == 0 && u == 0) ? 0u : 1u);
+            }
+            // The second parts: of all rows in the first two blocks, then 16
+            // rows at a time where there are any.
+            if (pdone < 2) {
+#pragma unroll
+              for (int u = 0; u < kUnits; ++u) {
+                if (u >= kk) break;
+                mma_f16(dd, da + u * 128, kDescHi, dp0 + kLoPart + u * 128, kDescHi, idesc_o, 1u);
+              }
+            } else {
+#pragma unroll 1
+              for (uint32_t w = hot; w != 0; w &= w - 1) {
+                const uint32_t bit = (uint32_t)__ffs((int)w) - 1u, q = bit >> 3, u = bit & 7u;
+                mma_f16(dd + q * NC, da + u * 128, kDescHi, dp0 + kLoPart + u * 128 + q * 2, kDescHi, idesc_lo, 1u);
+              }
             }
             ptx::tc_commit(&sh.empty[ps]);
           }
@@ -774,10 +904,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ptx::elect_one()) ptx::tc_commit(&sh.pv_done);
         ++gp;
-        pfirst = false;
+        ++pdone;
         punits -= kUnits;
         if (--pleft == 0) {
-          pfirst = true;
+          pdone = 0;
           if (nwait > 0) {
             pleft = wl0;
             punits = wu0;
@@ -841,38 +971,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ptx::elect_one()) ptx::tc_commit(&sh.drain);
     __syncwarp();
     if (!ptx::mbar_wait(&sh.drain, 0, kWaitNs) && lane == 0) atomicOr(k.watchdog, kWdAttn);
-  } else if (warp == kItemWarp) {
+  } else if (warp == R::ITEM) {
     // ------------------------------------------------------- work items
-    // Decoded here once for all roles, up to four ahead.
-    regs_down<kRegsIssue>();
+    // Decoded here once for all roles, up to three ahead.
+    regs_set<R::REGS_ISSUE, R::REGS>();
     uint32_t i = 0;
-    for (int item = blockIdx.x;; item += gridDim.x) {
-      Item it;
-      const bool end = item >= k.items;
-      if (end) {
-        it.b = -1;
-      } else {
-        it = get_item<NR>(k, item);
-        if (it.nrows == 0) continue;
-        if (lane == 0 && it.pad && a.err_flag != nullptr) atomicOr(a.err_flag, MXQ_DEVERR_LENGTH);
-        // Without blocks: a row that sees nothing (written by split 0), or a
-        // share of the keys that is empty.
-        if (it.blk0 >= it.blk1 && (it.units > 0 || it.split > 0)) continue;
-      }
-      if (!wait_warp(&sh.item_empty[i % kItems], ((i / kItems) & 1u) ^ 1u)) break;
+    auto hand_out = [&](const Item& it) -> bool {
+      if (!wait_warp(&sh.item_empty[i % kItems], ((i / kItems) & 1u) ^ 1u)) return false;
       if (lane == 0) {
         sh.items[i % kItems] = it;
         ptx::mbar_arrive(&sh.item_full[i % kItems]);
       }
       __syncwarp();
-      if (end) break;
       ++i;
-    }
-  } else if (warp == kUnitWarp) {
+      return true;
+    };
+    walk_items<NR>(k, [&](const Item& it) -> bool {
+      if (lane == 0 && it.pad && a.err_flag != nullptr) atomicOr(a.err_flag, MXQ_DEVERR_LENGTH);
+      return hand_out(it);
+    });
+    Item last = {};
+    last.b = -1;
+    hand_out(last);
+  } else if (warp == R::UNIT) {
     // ------------------------------------- where the units of a block lie
     // Lane u < 8 looks up unit u, a few blocks ahead of their use: the block
     // table's latency and the divisions stay out of the other warps' way.
-    regs_down<kRegsIssue>();
+    regs_set<R::REGS_ISSUE, R::REGS>();
     uint32_t nb = 0;
     bool ok = true;
     Item it;
@@ -890,6 +1015,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (a.err_flag != nullptr && (slot < 0 || first + min(kUnit, it.p1 + 1 - j) > a.num_slots))
             atomicOr(a.err_flag, MXQ_DEVERR_SLOT);
         }
+        // The unit's rows lie one after the other: into L2, blocks ahead.
+        if (DT != MXQ_CACHE_BF16 && slot >= 0) {
+          const uint32_t row_bytes = DT == MXQ_CACHE_E4M3 ? (uint32_t)D : (uint32_t)D / 2;
+          const uint32_t rows = (uint32_t)min((int64_t)kUnit, a.num_slots - slot);
+          ptx::prefetch_l2_bulk(static_cast<const uint8_t*>(a.cache) + (int64_t)slot * row_bytes, rows * row_bytes);
+        }
         if (!(ok = wait_warp(&sh.slot_empty[nb % kSlots], ((nb / kSlots) & 1u) ^ 1u))) break;
         if (lane < kUnits) sh.slots[nb % kSlots][lane] = slot;
         __syncwarp();
@@ -898,16 +1029,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------- softmax and epilogue
-    regs_up<kRegsSoft>();
-    const int h = warp >> 2, quad = warp & 3;      // row half, TMEM lane quadrant
+    regs_set<R::REGS_SOFT, R::REGS>();
+    const int h = warp >> 2, quad = warp & 3;      // group, TMEM lane quadrant
     const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16);
     const int key = quad * 32 + lane;              // this thread's key of a block
     const int c0 = h * NC;
     const uint32_t bar = 1 + h;
-    const float c_all = a.sm_scale * kLog2e;
+    const float vs = DT == MXQ_CACHE_E4M3 ? __ldg(a.kv_scale) : 1.0f;
+    const float c_all = a.sm_scale * kLog2e * vs;
     const float4* negm4 = reinterpret_cast<const float4*>(sh.negm + c0);
+    const float4* lthr4 = reinterpret_cast<const float4*>(sh.lthr + c0);
     uint32_t g = 0;   // blocks so far
-    int nq = 0;       // items with blocks so far
     uint32_t st = 0;  // first stage of the current block
     // A wait that gives up does not leave the loops by itself: the group's
     // next vote takes all of its threads out together.
@@ -926,18 +1058,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (quad == 0 && lane < NC) {
         const int r = c0 + lane;
         sh.negm[r] = r < it.nrows ? kNoKey : 0.0f;
+        sh.lthr[r] = INFINITY;  // set before the third block
         sh.rowt[r] = (uint8_t)((held.r0 + r) / a.H - held.r0 / a.H);
       }
       ptx::named_sync(bar, 128);
       float l[NC];
 #pragma unroll
       for (int c = 0; c < NC; ++c) l[c] = 0.0f;
-      const float4* crow4 = reinterpret_cast<const float4*>(sh.crow[nq % 3] + c0);
-      if (has) {
-        // The row scales come with the query.
-        if (!BF) ok = wait(&sh.q_full[nq & 3], (uint32_t)(nq >> 2) & 1u) && ok;
-        ++nq;
-      }
       for (int blk = it.blk0; blk < it.blk1; ++blk) {
         // Which rows see this thread's key: all, none or some.
         const int x = blk * kUnits + (key >> 4);
@@ -954,6 +1081,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool mixed = __any_sync(0xffffffffu, some && !all);
         auto sees = [&](int c) { return some && (uint32_t)(it.p0 + sh.rowt[c0 + c] - j) < (uint32_t)weff; };
 
+        // Now and then, the sums so far: what a weight is measured against.
+        const int done = blk - it.blk0;
+        if (done >= 2 && (done & (done - 1)) == 0) {
+          float v[NC];
+#pragma unroll
+          for (int c = 0; c < NC; ++c) v[c] = l[c];
+          const float part = lanes_reduce<NC, false>(v);
+          if (lane < NC) sh.red[h][quad][lane] = part;
+          ptx::named_sync(bar, 128);
+          if (quad == 0 && lane < NC && c0 + lane < it.nrows)
+            sh.lthr[c0 + lane] = log2f((sh.red[h][0][lane] + sh.red[h][1][lane]) +
+                                       (sh.red[h][2][lane] + sh.red[h][3][lane])) - 4.0f;
+          ptx::named_sync(bar, 128);
+        }
         ok = wait(&sh.s_full[g & 1u], (g >> 1) & 1u) && ok;
         __syncwarp();
         ptx::tc_fence_after();
@@ -968,11 +1109,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < NC / 4; ++q) {
             const float4 n = negm4[q];
-            const float4 cr = BF ? make_float4(c_all, c_all, c_all, c_all) : crow4[q];
-            d[4 * q] = fmaf(__uint_as_float(s[4 * q]), cr.x, n.x);
-            d[4 * q + 1] = fmaf(__uint_as_float(s[4 * q + 1]), cr.y, n.y);
-            d[4 * q + 2] = fmaf(__uint_as_float(s[4 * q + 2]), cr.z, n.z);
-            d[4 * q + 3] = fmaf(__uint_as_float(s[4 * q + 3]), cr.w, n.w);
+            d[4 * q] = fmaf(__uint_as_float(s[4 * q]), c_all, n.x);
+            d[4 * q + 1] = fmaf(__uint_as_float(s[4 * q + 1]), c_all, n.y);
+            d[4 * q + 2] = fmaf(__uint_as_float(s[4 * q + 2]), c_all, n.z);
+            d[4 * q + 3] = fmaf(__uint_as_float(s[4 * q + 3]), c_all, n.w);
 #pragma unroll
             for (int e = 0; e < 4; ++e) top = max_nan(top, d[4 * q + e]);
           }
@@ -982,7 +1122,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < NC; ++c) seen = fmaxf(seen, sees(c) ? d[c] : -INFINITY);
         const bool bad = in && !(fabsf(top) <= 3.4028234e38f);
-        const bool raise = bad || (some && (mixed ? seen : top) > kSlack + kShift);
+        const bool raise = bad || (some && (mixed ? seen : top) > kSlack);
         if (named_any(bar, 128, raise || !ok)) {
           // ---- some maximum moves, something is not finite, or a wait gave up
           if (named_any(bar, 128, !ok)) {
@@ -1005,7 +1145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   }
                   const uint4 w = rp[e];
                   const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-                  const uint32_t m = BF ? 0x7F80u : 0x7C00u;
+                  const uint32_t m = 0x7F80u;
                   for (int q = 0; q < 4; ++q)
                     rowbad |= (ws[q] & m) == m || ((ws[q] >> 16) & m) == m;
                 }
@@ -1015,18 +1155,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld<NC>(tq + kTmemS + (g & 1u) * 64 + c0, s);
           ptx::tmem_ld_wait();
 #pragma unroll
-          for (int q = 0; q < NC / 4; ++q) {
-            const float4 cr4 = BF ? make_float4(c_all, c_all, c_all, c_all) : crow4[q];
-            const float cr[4] = {cr4.x, cr4.y, cr4.z, cr4.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int c = 4 * q + e;
-              const float v = __uint_as_float(s[c]);
-              const bool fin = fabsf(v) <= 3.4028234e38f;
-              const bool see = mixed ? sees(c) : all;
-              if (bad && !fin && see) l[c] = NAN;
-              d[c] = see && fin ? v * cr[e] : -INFINITY;
-            }
+          for (int c = 0; c < NC; ++c) {
+            const float v = __uint_as_float(s[c]);
+            const bool fin = fabsf(v) <= 3.4028234e38f;
+            const bool see = mixed ? sees(c) : all;
+            if (bad && !fin && see) l[c] = NAN;
+            d[c] = see && fin ? v * c_all : -INFINITY;
           }
           const float m = lanes_reduce<NC, true>(d);
           if (lane < NC) sh.red[h][quad][lane] = m;
@@ -1038,13 +1172,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float old = sh.negm[r];
             float f = 1.0f;
             if (r < it.nrows && mb > -INFINITY) {
-              const float cur = old >= kNoKey ? -INFINITY : kShift - old;
+              const float cur = old >= kNoKey ? -INFINITY : -old;
               if (mb > cur) {
                 if (old < kNoKey) f = ex2(cur - mb);
-                sh.negm[r] = kShift - mb;
+                sh.negm[r] = -mb;
               }
             }
             sh.scale[r] = f;
+            if (f != 1.0f) sh.lthr[r] += log2f(f);  // stays infinite while it is
           }
           ptx::named_sync(bar, 128);
           exponents();
@@ -1064,7 +1199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (moved) {
               ptx::tc_fence_after();
-              for (int m = 0; m < np * (NV / NR); ++m)
+              for (int m = 0; m < np; ++m)
 #pragma unroll
                 for (int c = 0; c < NC; c += 8) {
                   uint32_t o[8];
@@ -1084,6 +1219,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         // ---- weights
+        // Units in which some weight is large against its row's sum so far.
+        bool big = false;
+#pragma unroll
+        for (int q = 0; q < NC / 4; ++q) {
+          const float4 t = lthr4[q];
+          const float th[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) big |= d[4 * q + e] > th[e];
+        }
+        uint32_t hot = __ballot_sync(0xffffffffu, some && big);
+        if (done < 2) hot = ~0u;
+        if (lane == 0) sh.hot[h][quad] = (uint8_t)(((hot & 0xFFFFu) ? 1 : 0) | ((hot >> 16) ? 2 : 0));
 #pragma unroll
         for (int q = 0; q < NC / 8; ++q) {
           uint32_t hi[4], lo[4];
@@ -1097,15 +1244,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               p[f] = see ? ex2(d[c]) : 0.0f;
               l[c] += p[f];
             }
-            hi[e] = pack16(BF, p[0], p[1]);
-            lo[e] = pack16_rest(BF, p[0], p[1], hi[e]);
+            hi[e] = pack2(p[0], p[1]);
+            if (hot != 0) lo[e] = pack2_rest(p[0], p[1], hi[e]);
           }
           const int col = (c0 >> 3) + q;
           uint8_t* row = sm_p + key * 128;
           *reinterpret_cast<uint4*>(row + ((col ^ (key & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           const int lcol = NR == 64 ? col : col + NR / 8;
-          *reinterpret_cast<uint4*>(row + (NR == 64 ? kKeys * 128 : 0) + ((lcol ^ (key & 7)) << 4)) =
-              make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          if (hot != 0)
+            *reinterpret_cast<uint4*>(row + (NR == 64 ? kKeys * 128 : 0) + ((lcol ^ (key & 7)) << 4)) =
+                make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
@@ -1131,32 +1279,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = c0 + lane;
         const float sum = (sh.red[h][0][lane] + sh.red[h][1][lane]) + (sh.red[h][2][lane] + sh.red[h][3][lane]);
         const float nm = sh.negm[r];
-        if (k.splits > 1 && has) {
-          k.part_ml[((int64_t)held.tile * k.splits + held.split) * NR + r] = make_float2(-nm, sum);
+        if (held.piece >= 0) {
+          k.part_ml[(int64_t)held.piece * NR + r] = make_float2(-nm, sum);
         } else {
-          const float vs = DT == MXQ_CACHE_E4M3 ? __ldg(a.kv_scale) : 1.0f;
           sh.scale[r] = sum == 0.0f ? 0.0f : vs / sum;
           if (r < it.nrows && a.lse != nullptr)
             a.lse[held.qrow + r] = sum == 0.0f ? -INFINITY : (log2f(sum) - nm) * 0.6931471805599453f;
         }
       }
       ptx::named_sync(bar, 128);
-      if (k.splits > 1 && has) {
+      if (held.piece >= 0) {
         // Partial sums as they are: a warp stores 32 consecutive columns of a row.
-        float* dst = k.part + (((int64_t)held.tile * k.splits + held.split) * NR + c0) * D + key;
+        float* dst = k.part + ((int64_t)held.piece * NR + c0) * D + key;
         for (int m = 0; m < np; ++m) {
           uint32_t o[NC];
-          tmem_ld<NC>(tq + m * NV + c0, o);
-          if constexpr (NR < 64) {
-            uint32_t lo[NC];
-            tmem_ld<NC>(tq + m * NV + NR + c0, lo);
-            ptx::tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-              o[c] = __float_as_uint(__uint_as_float(o[c]) + __uint_as_float(lo[c]));
-          } else {
-            ptx::tmem_ld_wait();
-          }
+          tmem_ld<NC>(tq + m * NR + c0, o);
+          ptx::tmem_ld_wait();
           if (m * 128 + key < D) {
 #pragma unroll
             for (int c = 0; c < NC; ++c)
@@ -1169,7 +1307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // rounded to BF16 pairs of rows, stored as transposed 8 x 8 matrices
         // into rows of 512 bytes whose 16-byte words are swizzled by row; then
         // whole rows go out with 16-byte stores.
-        uint8_t* stage = sm_p + h * (p_bytes(NR) / 2);
+        uint8_t* stage = sm_p + h * (NC * 512);
         const uint32_t stage_a = ptx::smem_u32(stage);
         float2 sc[NC / 8];
 #pragma unroll
@@ -1181,22 +1319,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               uint32_t o[NC / 2];
-              const uint32_t ad = tq + ((uint32_t)(hf * 16) << 16) + m * NV + c0;
-              tmem_ld_16x256b<NC>(ad, o);
-              if constexpr (NR < 64) {
-                uint32_t lo[NC / 2];
-                tmem_ld_16x256b<NC>(ad + NR, lo);
-                ptx::tmem_ld_wait();
-#pragma unroll
-                for (int c = 0; c < NC / 2; ++c)
-                  o[c] = __float_as_uint(__uint_as_float(o[c]) + __uint_as_float(lo[c]));
-              } else {
-                ptx::tmem_ld_wait();
-              }
+              tmem_ld_16x256b<NC>(tq + ((uint32_t)(hf * 16) << 16) + m * NR + c0, o);
+              ptx::tmem_ld_wait();
 #pragma unroll
               for (int q = 0; q < NC / 8; ++q) {
-                const uint32_t w0 = pack16(true, out_of(has, o[4 * q]) * sc[q].x, out_of(has, o[4 * q + 1]) * sc[q].y);
-                const uint32_t w1 = pack16(true, out_of(has, o[4 * q + 2]) * sc[q].x, out_of(has, o[4 * q + 3]) * sc[q].y);
+                const uint32_t w0 = pack2(out_of(has, o[4 * q]) * sc[q].x, out_of(has, o[4 * q + 1]) * sc[q].y);
+                const uint32_t w1 = pack2(out_of(has, o[4 * q + 2]) * sc[q].x, out_of(has, o[4 * q + 3]) * sc[q].y);
                 // Lanes 0-7 name the rows of the first matrix, 8-15 of the second.
                 const int row = q * 8 + (lane & 7);
                 const int word = (m - m0) * 16 + quad * 4 + hf * 2 + ((lane >> 3) & 1);
@@ -1212,8 +1340,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ptx::named_sync(bar, 128);
         }
-        // Both groups are done with the P buffers.
-        ptx::named_sync(3, 256);
+        // All groups are done with the P buffers.
+        ptx::named_sync(1 + R::GROUPS, R::SOFT * 32);
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sh.item_empty[ni % kItems]);
@@ -1221,46 +1349,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, kTmemCols);
+  if (warp == R::MMA) ptx::tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the partial sums of a tile's splits, one warp per row: the splits in
-// index order, each weighted by 2^(its maximum - the largest).
+// Joins the partial sums of the tiles that are cut: CTA (c, y) the one that
+// begins in share c, if any, one warp per row.  Its pieces lie in the slots
+// 2c + 1, 2(c + 1), 2(c + 2), ...; they are added in this order, each weighted
+// by 2^(its maximum - the largest).
+constexpr int kJoinWarps = 4;
 template <int NR>
-__global__ void __launch_bounds__(128) attn_join_kernel(const KernelArgs k) {
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const KernelArgs k) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const AttnArgs& a = k.a;
   const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (w >= (int64_t)k.tiles * NR) return;
-  const int r = (int)(w % NR);
-  // Item number of split 0 of this tile.
-  const int tile = (int)(w / NR);
-  const Item it = get_item<NR>(k, k.tiles - 1 - tile);
-  if (r >= it.nrows || it.units == 0) return;
-  const int nb = (it.units + kUnits - 1) / kUnits;
-  const int per = (nb + k.splits - 1) / k.splits;
-  const int used = (nb + per - 1) / per;
-  const float2* ml = k.part_ml + ((int64_t)tile * k.splits) * NR + r;
+  const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  const int first = 2 * blockIdx.x + 1;
+  const int4 d = k.desc[first];
+  if (!(d.w & kPieceUsed) || r >= d.z) return;
+  int used = 1;
+  // Every CTA has a slot, and the last piece of a tile is marked: the bound
+  // only keeps a broken chain from running out of the table.
+  while (2 * (blockIdx.x + used) < 2 * gridDim.x) {
+    const int f = k.desc[2 * (blockIdx.x + used)].w;
+    if (!(f & kPieceUsed)) break;
+    ++used;
+    if (f & kPieceEnds) break;
+  }
+  auto slot = [&](int i) { return i == 0 ? first : 2 * ((int)blockIdx.x + i); };
   float mx = -INFINITY;
-  for (int s = lane; s < used; s += 32) mx = fmaxf(mx, ml[(int64_t)s * NR].x);
+  for (int i = lane; i < used; i += 32) mx = fmaxf(mx, k.part_ml[(int64_t)slot(i) * NR + r].x);
   mx = warp_max(mx);
   float o[16];
 #pragma unroll
   for (int c = 0; c < 16; ++c) o[c] = 0.0f;
   float sum = 0.0f;
-  const float* p = k.part + ((int64_t)tile * k.splits * NR + r) * a.D;
-  for (int s = 0; s < used; ++s) {
-    const float2 v = ml[(int64_t)s * NR];
+#pragma unroll 4
+  for (int i = 0; i < used; ++i) {
+    const int64_t at = (int64_t)slot(i) * NR + r;
+    const float2 v = k.part_ml[at];
     const float f = ex2(v.x - mx);
     sum += f * v.y;
-    const float* ps = p + (int64_t)s * NR * a.D;
+    const float* ps = k.part + at * a.D;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const int d = c * 128 + lane * 4;
-      if (d < a.D) {
-        const float4 x = *reinterpret_cast<const float4*>(ps + d);
+      const int col = c * 128 + lane * 4;
+      if (col < a.D) {
+        const float4 x = *reinterpret_cast<const float4*>(ps + col);
         o[4 * c] += f * x.x;
         o[4 * c + 1] += f * x.y;
         o[4 * c + 2] += f * x.z;
@@ -1270,48 +1405,54 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const KernelArgs k) {
   }
   const float vs = a.dtype == MXQ_CACHE_E4M3 ? __ldg(a.kv_scale) : 1.0f;
   const float inv = sum == 0.0f ? 0.0f : vs / sum;
-  uint8_t* dst = static_cast<uint8_t*>(a.out) + (it.qrow + r) * a.D * 2;
+  const int64_t row = (int64_t)(((uint64_t)(uint32_t)d.y << 32) | (uint32_t)d.x) + r;
+  uint8_t* dst = static_cast<uint8_t*>(a.out) + row * a.D * 2;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const int d = c * 128 + lane * 4;
-    if (d < a.D)
-      *reinterpret_cast<uint2*>(dst + d * 2) = make_uint2(pack16(true, o[4 * c] * inv, o[4 * c + 1] * inv),
-                                                          pack16(true, o[4 * c + 2] * inv, o[4 * c + 3] * inv));
+    const int col = c * 128 + lane * 4;
+    if (col < a.D)
+      *reinterpret_cast<uint2*>(dst + col * 2) = make_uint2(pack2(o[4 * c] * inv, o[4 * c + 1] * inv),
+                                                            pack2(o[4 * c + 2] * inv, o[4 * c + 3] * inv));
   }
   if (lane == 0 && a.lse != nullptr)
-    a.lse[it.qrow + r] = sum == 0.0f ? -INFINITY : (log2f(sum) + mx) * 0.6931471805599453f;
+    a.lse[row] = sum == 0.0f ? -INFINITY : (log2f(sum) + mx) * 0.6931471805599453f;
 }
 
 // ---------------------------------------------------------------- host side
 struct Plan {
-  int NR, tiles, splits, stages;
-  size_t part_bytes, bytes;
+  int NR, grid, stages;
+  bool shares;
+  size_t part_bytes, ml_bytes, bytes;
 };
 
-constexpr int kSms = 152;  // the plan must not depend on the device: workspace sizes come from it
+// CTAs of the share form.  Workspace sizes come from the plan, which must not
+// depend on the device; a device with fewer SMs runs them in turns.
+constexpr int kShares = 152;
 
 Plan make_plan(const AttnArgs& a) {
   Plan p;
-  const int64_t per_seq = a.T * a.H / a.B;
+  const int64_t rows = a.T * a.H, per_seq = rows / a.B;
   p.NR = per_seq > 32 ? 64 : per_seq > 16 ? 32 : 16;
-  p.tiles = (int)(a.T * a.H / p.NR + a.B);
-  // Key blocks of a tile, at most.
+  p.stages = stages_for(p.NR, a.D);
+  // Tiles, at most, and key blocks of a tile, at most.
+  const int64_t tiles = rows / p.NR + (a.B < rows ? a.B : rows);
   const int64_t cap = (int64_t)a.max_pages * a.page_size;
   int64_t keys = cap;
   if (a.window > 0) {
     const int64_t w = (int64_t)a.window + a.sinks + 2 * kUnit + (p.NR + a.H - 1) / a.H;
     keys = keys < w ? keys : w;
   }
-  const int64_t nb = ceil_div(keys, kKeys);
-  // Tiles that exist: the numbering above leaves gaps.
-  const int64_t real = a.B * ceil_div(ceil_div(a.T * a.H, a.B), p.NR);
-  int64_t splits = kSms / (real > 0 ? real : 1);
-  if (splits > nb / 2) splits = nb / 2;  // two blocks at least: a join costs about one
-  p.splits = splits < 1 ? 1 : (int)splits;
-  p.stages = stages_for(p.NR, a.D);
-  const size_t rows = (size_t)p.tiles * p.splits * p.NR;
-  p.part_bytes = p.splits > 1 ? round_up_256(rows * a.D * 4) : 0;
-  p.bytes = p.splits > 1 ? p.part_bytes + round_up_256(rows * 8) : 0;
+  // Whole tiles when each CTA gets at least eight (what the last ones leave
+  // idle is then an eighth of a tile's time) or when no tile has more than two
+  // blocks (a cut costs about one).
+  // (Weights are 32-bit numbers on the device.)
+  const int64_t nb = ceil_div(keys, kKeys) + 1;
+  p.shares = rows / p.NR < 8 * kShares && nb > 3 && tiles * nb < (int64_t)1 << 31;
+  p.grid = p.shares || tiles > kShares ? kShares : (int)tiles;
+  const size_t pieces = 2 * (size_t)p.grid;
+  p.part_bytes = p.shares ? round_up_256(pieces * p.NR * a.D * 4) : 0;
+  p.ml_bytes = p.shares ? round_up_256(pieces * p.NR * 8) : 0;
+  p.bytes = p.shares ? p.part_bytes + p.ml_bytes + round_up_256(pieces * 16) : 0;
   return p;
 }
 
@@ -1330,7 +1471,7 @@ bool encode_rows(CUtensorMap* m, const void* base, uint64_t D, uint64_t rows) {
 }
 
 template <int NR, int DT>
-cudaError_t launch_one(const KernelArgs& k, int num_sms, cudaStream_t s, const char** why) {
+cudaError_t launch_one(const KernelArgs& k, int grid, cudaStream_t s, const char** why) {
   auto kern = attn_kernel<NR, DT>;
   const int smem = smem_fixed(NR, k.a.D) + k.stages * kStageBytes;
   int dev = 0;
@@ -1350,8 +1491,8 @@ cudaError_t launch_one(const KernelArgs& k, int num_sms, cudaStream_t s, const c
     return cudaErrorInvalidValue;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(k.items < num_sms ? k.items : num_sms), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(Roles<NR>::THREADS, 1, 1);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -1360,38 +1501,34 @@ cudaError_t launch_one(const KernelArgs& k, int num_sms, cudaStream_t s, const c
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, tm, k);
-  if (e != cudaSuccess || k.splits == 1) return e;
-  cfg.gridDim = dim3((unsigned)ceil_div((int64_t)k.tiles * NR, 4), 1, 1);
-  cfg.blockDim = dim3(128, 1, 1);
+  if (e != cudaSuccess || !k.shares) return e;
+  cfg.gridDim = dim3((unsigned)grid, NR / kJoinWarps, 1);
+  cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attn_join_kernel<NR>, k);
 }
 
 template <int NR>
-cudaError_t launch_nr(const KernelArgs& k, int num_sms, cudaStream_t s, const char** why) {
-  if (k.a.dtype == MXQ_CACHE_BF16) return launch_one<NR, MXQ_CACHE_BF16>(k, num_sms, s, why);
-  if (k.a.dtype == MXQ_CACHE_E4M3) return launch_one<NR, MXQ_CACHE_E4M3>(k, num_sms, s, why);
-  return launch_one<NR, MXQ_CACHE_E2M1>(k, num_sms, s, why);
+cudaError_t launch_nr(const KernelArgs& k, int grid, cudaStream_t s, const char** why) {
+  if (k.a.dtype == MXQ_CACHE_BF16) return launch_one<NR, MXQ_CACHE_BF16>(k, grid, s, why);
+  if (k.a.dtype == MXQ_CACHE_E4M3) return launch_one<NR, MXQ_CACHE_E4M3>(k, grid, s, why);
+  return launch_one<NR, MXQ_CACHE_E2M1>(k, grid, s, why);
 }
 
 }  // namespace
 
 size_t attn_workspace_bytes(const AttnArgs& a) { return a.T > 0 ? make_plan(a).bytes : 0; }
 
-cudaError_t launch_attn(const AttnArgs& a, void* ws, int num_sms, cudaStream_t s, const char** why) {
+cudaError_t launch_attn(const AttnArgs& a, void* ws, cudaStream_t s, const char** why) {
   const Plan p = make_plan(a);
   KernelArgs k = {};
   k.a = a;
-  k.tiles = p.tiles;
-  k.splits = p.splits;
+  k.shares = p.shares;
   k.stages = p.stages;
-  if ((int64_t)p.tiles * p.splits >= (int64_t)1 << 31) {
-    *why = "too many tiles";
-    return cudaErrorInvalidValue;
-  }
-  k.items = p.tiles * p.splits;
-  k.part = static_cast<float*>(ws);
-  k.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + p.part_bytes);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  k.part = reinterpret_cast<float*>(w);
+  k.part_ml = reinterpret_cast<float2*>(w + p.part_bytes);
+  k.desc = reinterpret_cast<int4*>(w + p.part_bytes + p.ml_bytes);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1405,9 +1542,9 @@ cudaError_t launch_attn(const AttnArgs& a, void* ws, int num_sms, cudaStream_t s
     ready.fetch_or(bit, std::memory_order_acq_rel);
   }
   k.watchdog = wd[dev & 63];
-  if (p.NR == 64) return launch_nr<64>(k, num_sms, s, why);
-  if (p.NR == 32) return launch_nr<32>(k, num_sms, s, why);
-  return launch_nr<16>(k, num_sms, s, why);
+  if (p.NR == 64) return launch_nr<64>(k, p.grid, s, why);
+  if (p.NR == 32) return launch_nr<32>(k, p.grid, s, why);
+  return launch_nr<16>(k, p.grid, s, why);
 }
 
 }  // namespace mxq

@@ -121,7 +121,7 @@ struct AttnArgs {
   float sm_scale;
 };
 size_t attn_workspace_bytes(const AttnArgs& a);
-cudaError_t launch_attn(const AttnArgs& a, void* ws, int num_sms, cudaStream_t s, const char** why);
+cudaError_t launch_attn(const AttnArgs& a, void* ws, cudaStream_t s, const char** why);
 
 // Caps the CTA pairs of the pair-form GEMM launches (0 = no cap); returns
 // the previous cap.
