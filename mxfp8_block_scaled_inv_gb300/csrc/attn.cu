@@ -86,6 +86,7 @@ struct Roles {
   static constexpr int SOFT = 4 * GROUPS;        // their warps
   static constexpr int MMA = SOFT, TMA = SOFT + 1, ITEM = SOFT + 2, UNIT = SOFT + 3;
   static constexpr int LOAD0 = SOFT + 4, LOADS = 8;
+  static constexpr int FULL = SOFT > LOADS ? SOFT : LOADS;  // arrivals that fill a stage
   static constexpr int THREADS = (LOAD0 + LOADS) * 32;
   static constexpr int REGS = 65536 / THREADS / 8 * 8;
   static constexpr int REGS_SOFT = NR == 64 ? 88 : 112, REGS_ISSUE = NR == 64 ? 56 : 64,
@@ -135,6 +136,7 @@ struct Shared {
   int slots[kSlots][kUnits];  // cache row of each unit's first key, -1: none
   alignas(16) float negm[64];
   float lthr[64];   // log2 of the weight from which the second part counts
+  float lmin[4];    // the least of each group
   float scale[64];  // the rescale factors of a block; in the epilogue 1 / sum
   uint8_t rowt[64];  // a row's token, counted from the tile's first
   uint8_t hot[4][4];  // per group and quarter: units with such a weight (2 bits)
@@ -386,6 +388,21 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* r) {
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(ptx::smem_u32(bar)), "r"(n) : "memory");
+}
+// One try of a barrier wait, asleep for at most kHintNs.
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      "selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(kHintNs)
+      : "memory");
+  return ok != 0;
+}
 // Barrier of `count` threads that also tells whether any of them passed true.
 __device__ __forceinline__ bool named_any(uint32_t id, uint32_t count, bool v) {
   uint32_t r;
@@ -550,9 +567,79 @@ __device__ __forceinline__ uint2 widen_e2m1x4(uint32_t w, const E2m1Table& t) {
   return make_uint2(__byte_perm(lo, hi, 0x5140), __byte_perm(lo, hi, 0x7362));
 }
 
-// Cache rows that a loading thread handles in every block.
-template <int DT>
-constexpr int kRowsPerThread = DT == MXQ_CACHE_E4M3 ? 4 : 2;
+// Widening of a stage (128 keys x 128 columns) by NT threads: 16-byte pieces
+// of the stored rows, TPR to a row, RPT to a thread.
+template <int DT, int NT>
+struct Widen {
+  static constexpr int TPR = DT == MXQ_CACHE_E4M3 ? 8 : 4;
+  static constexpr int RPT = kKeys * TPR / NT;
+  static constexpr int KSTEP = NT / TPR;     // key step between a thread's rows
+  static constexpr int COLS = 128 / TPR;     // columns of a piece
+  static_assert(KSTEP % 16 == 0 && RPT >= 1, "a thread's rows keep their place in a unit");
+  const uint8_t* row[RPT];
+  const uint8_t* sf[RPT];
+  uint4 v[RPT];
+  uint32_t sb[RPT];
+
+  // Rows t / TPR + i * KSTEP of a block whose units lie at su[0..7].
+  __device__ __forceinline__ void open(const AttnArgs& a, const int* su, int t) {
+    const int key0 = t / TPR, piece = t % TPR;
+    const uint32_t row_bytes = DT == MXQ_CACHE_E4M3 ? (uint32_t)a.D : (uint32_t)a.D / 2;
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int u = su[(key0 + i * KSTEP) >> 4];
+      const int64_t slot = (int64_t)u + (key0 & 15);
+      const bool in = u >= 0 && slot < a.num_slots;
+      row[i] = in ? static_cast<const uint8_t*>(a.cache) + slot * row_bytes + piece * 16 : nullptr;
+      if (DT == MXQ_CACHE_E2M1) sf[i] = a.cache_sf + (in ? slot : 0) * (a.D >> 5) + piece;
+    }
+  }
+  // The pieces (and scale bytes) of stage pr of the block.
+  __device__ __forceinline__ void fetch(int D, int pr, int t) {
+    const bool in = pr * 128 + (t % TPR) * COLS < D;  // an odd last chunk: half a stage
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      v[i] = make_uint4(0, 0, 0, 0);
+      sb[i] = 0;
+      if (in && row[i] != nullptr) {
+        v[i] = __ldg(reinterpret_cast<const uint4*>(row[i] + pr * (TPR * 16)));
+        if (DT == MXQ_CACHE_E2M1) sb[i] = __ldg(sf[i] + pr * 4);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(uint8_t* dst, int t) const {
+    const int key0 = t / TPR, piece = t % TPR, sw = key0 & 7;
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      uint8_t* d = dst + (key0 + i * KSTEP) * 128;
+      if constexpr (DT == MXQ_CACHE_E4M3) {
+        // The two chunks store their halves in opposite order, so that eight
+        // lanes always cover eight different 16-byte columns.
+        const int ch = piece >> 2, c0 = (piece & 3) * 2;
+        d += ch * kChunkBytes;
+        uint4 x = widen_e4m3(v[i].x, v[i].y), y = widen_e4m3(v[i].z, v[i].w);
+        if (e4m3_has_nan(v[i])) {
+          x = put_nans(x, v[i].x, v[i].y);
+          y = put_nans(y, v[i].z, v[i].w);
+        }
+        *reinterpret_cast<uint4*>(d + (((c0 + ch) ^ sw) << 4)) = ch ? y : x;
+        *reinterpret_cast<uint4*>(d + (((c0 + 1 - ch) ^ sw) << 4)) = ch ? x : y;
+      } else {
+        const E2m1Table tab = e2m1_table(sb[i]);
+        const int ch = piece >> 1, c0 = (piece & 1) * 4;
+        d += ch * kChunkBytes;
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // Column e ^ (2 * chunk): the same conflict rule as above.
+          const uint32_t we = ch ? w[e ^ 2] : w[e];
+          const uint2 x = widen_e2m1x4(we, tab), y = widen_e2m1x4(we >> 16, tab);
+          *reinterpret_cast<uint4*>(d + (((c0 + (ch ? e ^ 2 : e)) ^ sw) << 4)) = make_uint4(x.x, x.y, y.x, y.y);
+        }
+      }
+    }
+  }
+};
 
 // ------------------------------------------------------------------ kernel
 template <int NR, int DT>
@@ -563,6 +650,10 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
   extern __shared__ __align__(1024) uint8_t base[];
   const AttnArgs& a = k.a;
   const int D = a.D, nch = D >> 6, np = (nch + 1) >> 1;
+  // Stages of a block that the loading warps widen; where a block fills the
+  // ring (nothing is loaded ahead then) the softmax warps, idle until the
+  // products are done, widen the others.
+  [[maybe_unused]] const int own = NR == 64 && np > 2 ? 2 : np;
   uint8_t* sm_stage = base;
   uint8_t* sm_p = sm_stage + (size_t)k.stages * kStageBytes;
   uint8_t* sm_q = sm_p + p_bytes(NR);
@@ -573,14 +664,14 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
   if (tid == 0) {
     sh.abort = 0;
     for (int s = 0; s < k.stages; ++s) {
-      ptx::mbar_init(&sh.full[s], DT == MXQ_CACHE_BF16 ? 1 : kLoadThreads);
+      ptx::mbar_init(&sh.full[s], DT == MXQ_CACHE_BF16 ? 1 : R::FULL);
       ptx::mbar_init(&sh.empty[s], 1);
     }
     ptx::mbar_init(&sh.s_full[0], 1);
     ptx::mbar_init(&sh.s_full[1], 1);
-    ptx::mbar_init(&sh.p_full, R::SOFT * 32);
+    ptx::mbar_init(&sh.p_full, R::SOFT);
     ptx::mbar_init(&sh.pv_done, 1);
-    for (int s = 0; s < 4; ++s) ptx::mbar_init(&sh.q_full[s], kLoadThreads);
+    for (int s = 0; s < 4; ++s) ptx::mbar_init(&sh.q_full[s], R::LOADS);
     ptx::mbar_init(&sh.q_empty, 1);
     ptx::mbar_init(&sh.drain, 1);
     for (int i = 0; i < kItems; ++i) {
@@ -607,13 +698,21 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
 
   // A bounded wait; false once it or any other wait of the CTA gave up.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (*abort_flag) return false;
-    if (ptx::mbar_wait_hint(bar, parity, kWaitNs, kHintNs)) return true;
-    *abort_flag = 1;
-    atomicOr(k.watchdog, kWdAttn);
-    return false;
+    const uint32_t ad = ptx::smem_u32(bar);
+    if (try_wait(ad, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer();
+    while (true) {
+#pragma unroll 1
+      for (int i = 0; i < 32; ++i)
+        if (try_wait(ad, parity)) return true;
+      if (*abort_flag) return false;
+      if (ptx::globaltimer() - t0 > kWaitNs) {
+        *abort_flag = 1;
+        atomicOr(k.watchdog, kWdAttn);
+        return false;
+      }
+    }
   };
-
   // The same for a whole warp: its lanes agree on the outcome.
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, wait(bar, parity));
@@ -641,7 +740,6 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
     const int lt = tid - R::LOAD0 * 32, lw = lt >> 5;
     int nq = 0;                // items with blocks so far
     [[maybe_unused]] uint32_t nb = 0;  // blocks so far
-    [[maybe_unused]] uint32_t st = 0, stp = 0;  // stage and its phase
     bool ok = true;
     Item it;
     for (uint32_t ni = 0; ok && read_item(ni, it); ++ni) {
@@ -671,100 +769,28 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
         }
       }
       ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(&sh.q_full[nq & 3]);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sh.q_full[nq & 3]);
       ++nq;
 
       if constexpr (DT != MXQ_CACHE_BF16) {
-        constexpr int RPT = kRowsPerThread<DT>;          // cache rows of this thread per block
-        constexpr int TPR = kLoadThreads * RPT / kKeys;  // threads per row: 8, 4
-        constexpr int KSTEP = kKeys / RPT;               // key step between its rows: 32, 64
-        constexpr int PIECE_COLS = 128 / TPR;            // columns of a 16-byte piece: 16, 32
-        const int key0 = lt / TPR, piece = lt % TPR;
-        const uint32_t row_bytes = DT == MXQ_CACHE_E4M3 ? (uint32_t)D : (uint32_t)D / 2;
-        // Rows key0 + i * KSTEP of a block (unit i * KSTEP / 16 + key0 / 16).
-        const uint8_t* row[RPT];
-        const uint8_t* sf[RPT];
-        auto open_block = [&]() -> bool {
-          if (!wait_warp(&sh.slot_full[nb % kSlots], (nb / kSlots) & 1u)) return false;
-          const int* su = sh.slots[nb % kSlots] + (key0 >> 4);
-#pragma unroll
-          for (int i = 0; i < RPT; ++i) {
-            const int u = su[i * (KSTEP / 16)];
-            const int64_t slot = (int64_t)u + (key0 & 15);
-            const bool in = u >= 0 && slot < a.num_slots;
-            row[i] = in ? static_cast<const uint8_t*>(a.cache) + slot * row_bytes + piece * 16 : nullptr;
-            if (DT == MXQ_CACHE_E2M1) sf[i] = a.cache_sf + (in ? slot : 0) * (D >> 5) + piece;
-          }
+        // A stage is fetched as soon as the one before it has been stored; its
+        // rows are in L2 by then (the unit warp's prefetch).
+        Widen<DT, kLoadThreads> w;
+        for (int left = it.blk1 - it.blk0; left > 0 && ok; --left, ++nb) {
+          if (!(ok = wait_warp(&sh.slot_full[nb % kSlots], (nb / kSlots) & 1u))) break;
+          w.open(a, sh.slots[nb % kSlots], lt);
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&sh.slot_empty[nb % kSlots]);
-          ++nb;
-          return true;
-        };
-        // The 16-byte pieces of one pair of chunks (and their scale bytes).
-        auto fetch = [&](int pr, uint4 (&v)[RPT], uint32_t (&sb)[RPT]) {
-          const bool in = pr * 128 + piece * PIECE_COLS < D;  // an odd last chunk: half a pair
-#pragma unroll
-          for (int i = 0; i < RPT; ++i) {
-            v[i] = make_uint4(0, 0, 0, 0);
-            sb[i] = 0;
-            if (in && row[i] != nullptr) {
-              v[i] = __ldg(reinterpret_cast<const uint4*>(row[i] + pr * (TPR * 16)));
-              if (DT == MXQ_CACHE_E2M1) sb[i] = __ldg(sf[i] + pr * 4);
-            }
-          }
-        };
-        auto store = [&](const uint4 (&v)[RPT], const uint32_t (&sb)[RPT]) {
-          uint8_t* dst = sm_stage + st * kStageBytes;
-#pragma unroll
-          for (int i = 0; i < RPT; ++i) {
-            const int key = key0 + i * KSTEP;
-            uint8_t* d = dst + key * 128;
-            const int sw = key & 7;
-            if constexpr (DT == MXQ_CACHE_E4M3) {
-              // The two chunks store their halves in opposite order, so that
-              // eight lanes always cover eight different 16-byte columns.
-              const int ch = piece >> 2, c0 = (piece & 3) * 2;
-              d += ch * kChunkBytes;
-              uint4 x = widen_e4m3(v[i].x, v[i].y), y = widen_e4m3(v[i].z, v[i].w);
-              if (e4m3_has_nan(v[i])) {
-                x = put_nans(x, v[i].x, v[i].y);
-                y = put_nans(y, v[i].z, v[i].w);
-              }
-              *reinterpret_cast<uint4*>(d + (((c0 + ch) ^ sw) << 4)) = ch ? y : x;
-              *reinterpret_cast<uint4*>(d + (((c0 + 1 - ch) ^ sw) << 4)) = ch ? x : y;
-            } else {
-              const E2m1Table t = e2m1_table(sb[i]);
-              const int ch = piece >> 1, c0 = (piece & 1) * 4;
-              d += ch * kChunkBytes;
-              const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                // Column e ^ (2 * chunk): the same conflict rule as above.
-                const uint32_t we = ch ? w[e ^ 2] : w[e];
-                const uint2 x = widen_e2m1x4(we, t), y = widen_e2m1x4(we >> 16, t);
-                *reinterpret_cast<uint4*>(d + (((c0 + (ch ? e ^ 2 : e)) ^ sw) << 4)) =
-                    make_uint4(x.x, x.y, y.x, y.y);
-              }
-            }
-          }
-          ptx::fence_proxy_async_smem();
-          ptx::mbar_arrive(&sh.full[st]);
-          if (++st == (uint32_t)k.stages) {
-            st = 0;
-            stp ^= 1u;
-          }
-        };
-        // A pair is fetched as soon as the one before it has been stored; its
-        // rows are in L2 by then (the unit warp's prefetch).
-        uint4 v[RPT];
-        uint32_t sb[RPT];
-        for (int left = it.blk1 - it.blk0; left > 0 && ok; --left) {
-          if (!(ok = open_block())) break;
-          fetch(0, v, sb);
-          for (int pr = 0; pr < np; ++pr) {
-            if (!(ok = wait_warp(&sh.empty[st], stp ^ 1u))) break;
-            store(v, sb);
-            if (pr + 1 < np) fetch(pr + 1, v, sb);
+          w.fetch(D, 0, lt);
+          for (int pr = 0; pr < own; ++pr) {
+            const uint32_t n = nb * np + pr, st = n % (uint32_t)k.stages;
+            if (!(ok = wait_warp(&sh.empty[st], ((n / (uint32_t)k.stages) & 1u) ^ 1u))) break;
+            w.store(sm_stage + st * kStageBytes, lt);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_n(&sh.full[st], R::FULL / R::LOADS);
+            if (pr + 1 < own) w.fetch(D, pr + 1, lt);
           }
         }
       }
@@ -1016,8 +1042,8 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
             atomicOr(a.err_flag, MXQ_DEVERR_SLOT);
         }
         // The unit's rows lie one after the other: into L2, blocks ahead.
-        if (DT != MXQ_CACHE_BF16 && slot >= 0) {
-          const uint32_t row_bytes = DT == MXQ_CACHE_E4M3 ? (uint32_t)D : (uint32_t)D / 2;
+        if (slot >= 0) {
+          const uint32_t row_bytes = (uint32_t)D * 2 / (DT == MXQ_CACHE_BF16 ? 1 : DT == MXQ_CACHE_E4M3 ? 2 : 4);
           const uint32_t rows = (uint32_t)min((int64_t)kUnit, a.num_slots - slot);
           ptx::prefetch_l2_bulk(static_cast<const uint8_t*>(a.cache) + (int64_t)slot * row_bytes, rows * row_bytes);
         }
@@ -1059,6 +1085,7 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
         const int r = c0 + lane;
         sh.negm[r] = r < it.nrows ? kNoKey : 0.0f;
         sh.lthr[r] = INFINITY;  // set before the third block
+        sh.lmin[h] = INFINITY;
         sh.rowt[r] = (uint8_t)((held.r0 + r) / a.H - held.r0 / a.H);
       }
       ptx::named_sync(bar, 128);
@@ -1073,6 +1100,21 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
         const int weff = (a.window == 0 || j < a.sinks) ? 0x7fffffff : a.window;
         ok = wait(&sh.slot_full[g % kSlots], (g / kSlots) & 1u) && ok;
         const int unit_slot = sh.slots[g % kSlots][key >> 4];
+        if constexpr (DT != MXQ_CACHE_BF16 && NR == 64) {
+          if (own < np) {
+            Widen<DT, R::SOFT * 32> w;
+            w.open(a, sh.slots[g % kSlots], tid);
+            for (int pr = own; pr < np; ++pr) {
+              w.fetch(D, pr, tid);
+              const uint32_t n = g * np + pr, ws = n % (uint32_t)k.stages;
+              ok = wait(&sh.empty[ws], ((n / (uint32_t)k.stages) & 1u) ^ 1u) && ok;
+              w.store(sm_stage + ws * kStageBytes, tid);
+              ptx::fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) arrive_n(&sh.full[ws], R::FULL / R::SOFT);
+            }
+          }
+        }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&sh.slot_empty[g % kSlots]);
         const bool some = in && j <= it.p1 && it.p0 - j < weff && unit_slot >= 0 &&
@@ -1081,6 +1123,14 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
         const bool mixed = __any_sync(0xffffffffu, some && !all);
         auto sees = [&](int c) { return some && (uint32_t)(it.p0 + sh.rowt[c0 + c] - j) < (uint32_t)weff; };
 
+        // The least of the group's thresholds (called by its first warp, lane c
+        // and lane c + 16 with row c).
+        auto lowest = [&](int r) {
+          float t = sh.lthr[r];
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) t = fminf(t, __shfl_xor_sync(0xffffffffu, t, o));
+          if (lane == 0) sh.lmin[h] = t;
+        };
         // Now and then, the sums so far: what a weight is measured against.
         const int done = blk - it.blk0;
         if (done >= 2 && (done & (done - 1)) == 0) {
@@ -1090,9 +1140,13 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
           const float part = lanes_reduce<NC, false>(v);
           if (lane < NC) sh.red[h][quad][lane] = part;
           ptx::named_sync(bar, 128);
-          if (quad == 0 && lane < NC && c0 + lane < it.nrows)
-            sh.lthr[c0 + lane] = log2f((sh.red[h][0][lane] + sh.red[h][1][lane]) +
-                                       (sh.red[h][2][lane] + sh.red[h][3][lane])) - 4.0f;
+          if (quad == 0) {
+            const int r = c0 + (lane & 15);
+            if (r < it.nrows)
+              sh.lthr[r] = log2f((sh.red[h][0][lane & 15] + sh.red[h][1][lane & 15]) +
+                                 (sh.red[h][2][lane & 15] + sh.red[h][3][lane & 15])) - 4.0f;
+            lowest(r);
+          }
           ptx::named_sync(bar, 128);
         }
         ok = wait(&sh.s_full[g & 1u], (g >> 1) & 1u) && ok;
@@ -1123,7 +1177,49 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
           for (int c = 0; c < NC; ++c) seen = fmaxf(seen, sees(c) ? d[c] : -INFINITY);
         const bool bad = in && !(fabsf(top) <= 3.4028234e38f);
         const bool raise = bad || (some && (mixed ? seen : top) > kSlack);
-        if (named_any(bar, 128, raise || !ok)) {
+        // P's buffers are free once the previous block's second product is done.
+        if (blk > it.blk0) {
+          ok = wait(&sh.pv_done, (g - 1) & 1u) && ok;
+          __syncwarp();
+        }
+        for (bool again = false;;) {
+          // ---- weights, in place of the exponents, written before it is known
+          // whether a maximum has to move: it hardly ever has.
+          // Units in which some weight is large against its row's sum so far:
+          uint32_t hot = ~0u;
+          if (done >= 2) {
+            bool big = false;
+            if (top > sh.lmin[h]) {
+#pragma unroll
+              for (int q = 0; q < NC / 4; ++q) {
+                const float4 t = lthr4[q];
+                big |= d[4 * q] > t.x || d[4 * q + 1] > t.y || d[4 * q + 2] > t.z || d[4 * q + 3] > t.w;
+              }
+            }
+            hot = __ballot_sync(0xffffffffu, some && big);
+          }
+          if (lane == 0) sh.hot[h][quad] = (uint8_t)(((hot & 0xFFFFu) ? 1 : 0) | ((hot >> 16) ? 2 : 0));
+#pragma unroll
+          for (int c = 0; c < NC; ++c) d[c] = (mixed ? sees(c) : all) ? ex2(d[c]) : 0.0f;
+#pragma unroll
+          for (int q = 0; q < NC / 8; ++q) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              hi[e] = pack2(d[8 * q + 2 * e], d[8 * q + 2 * e + 1]);
+              if (hot != 0) lo[e] = pack2_rest(d[8 * q + 2 * e], d[8 * q + 2 * e + 1], hi[e]);
+            }
+            const int col = (c0 >> 3) + q;
+            uint8_t* row = sm_p + key * 128;
+            *reinterpret_cast<uint4*>(row + ((col ^ (key & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            const int lcol = NR == 64 ? col : col + NR / 8;
+            if (hot != 0)
+              *reinterpret_cast<uint4*>(row + (NR == 64 ? kKeys * 128 : 0) + ((lcol ^ (key & 7)) << 4)) =
+                  make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+          ptx::fence_proxy_async_smem();
+          if (again || !named_any(bar, 128, raise || !ok)) break;
+          again = true;
           // ---- some maximum moves, something is not finite, or a wait gave up
           if (named_any(bar, 128, !ok)) {
             dead = true;
@@ -1181,6 +1277,10 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
             sh.scale[r] = f;
             if (f != 1.0f) sh.lthr[r] += log2f(f);  // stays infinite while it is
           }
+          if (quad == 0) {
+            __syncwarp();
+            lowest(c0 + (lane & 15));
+          }
           ptx::named_sync(bar, 128);
           exponents();
           if (bad)
@@ -1195,8 +1295,6 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
               l[c] *= f;
               moved |= f != 1.0f;
             }
-            ok = wait(&sh.pv_done, (g - 1) & 1u);
-            __syncwarp();
             if (moved) {
               ptx::tc_fence_after();
               for (int m = 0; m < np; ++m)
@@ -1214,50 +1312,13 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
               tmem_st_wait();
             }
           }
-        } else if (blk > it.blk0) {
-          ok = wait(&sh.pv_done, (g - 1) & 1u);
-          __syncwarp();
         }
-        // ---- weights
-        // Units in which some weight is large against its row's sum so far.
-        bool big = false;
+        if (dead) break;
 #pragma unroll
-        for (int q = 0; q < NC / 4; ++q) {
-          const float4 t = lthr4[q];
-          const float th[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) big |= d[4 * q + e] > th[e];
-        }
-        uint32_t hot = __ballot_sync(0xffffffffu, some && big);
-        if (done < 2) hot = ~0u;
-        if (lane == 0) sh.hot[h][quad] = (uint8_t)(((hot & 0xFFFFu) ? 1 : 0) | ((hot >> 16) ? 2 : 0));
-#pragma unroll
-        for (int q = 0; q < NC / 8; ++q) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float p[2];
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-              const int c = q * 8 + e * 2 + f;
-              const bool see = mixed ? sees(c) : all;
-              p[f] = see ? ex2(d[c]) : 0.0f;
-              l[c] += p[f];
-            }
-            hi[e] = pack2(p[0], p[1]);
-            if (hot != 0) lo[e] = pack2_rest(p[0], p[1], hi[e]);
-          }
-          const int col = (c0 >> 3) + q;
-          uint8_t* row = sm_p + key * 128;
-          *reinterpret_cast<uint4*>(row + ((col ^ (key & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          const int lcol = NR == 64 ? col : col + NR / 8;
-          if (hot != 0)
-            *reinterpret_cast<uint4*>(row + (NR == 64 ? kKeys * 128 : 0) + ((lcol ^ (key & 7)) << 4)) =
-                make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-        ptx::fence_proxy_async_smem();
+        for (int c = 0; c < NC; ++c) l[c] += d[c];
         ptx::tc_fence_before();
-        ptx::mbar_arrive(&sh.p_full);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.p_full);
         ++g;
         st = (st + np) % (uint32_t)k.stages;
       }
