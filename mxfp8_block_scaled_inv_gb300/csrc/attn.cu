@@ -17,10 +17,18 @@
 //                                                   rows, read transposed)
 //
 // so a cache row is fetched once for both products and for all rows of the
-// tile.  P = 2^(x + negm), x = s * log2(e): negm is minus a running maximum
-// per row that is only moved when some score passes it by more than 2^8, so
-// that most blocks need neither a cross-lane maximum nor a rescale of O.
-// Row sums are kept per thread (one key each) in FP32 and joined at the end.
+// tile.  P = 2^(x + negm), x = s * log2(e).  BF16 has FP32's exponent range, so
+// negm need not be minus the row's maximum: it is minus the score of one key
+// of the item's first block that (nearly) all rows see, and moves only when a
+// score passes it by more than 2^40, so that blocks need neither a maximum
+// over the keys nor a rescale of O.  (O and the sums then reach 2^40 times the
+// values they stand for.)  Row sums are kept per thread (one key each) in FP32
+// and joined at the end.
+//
+// The kernel is built for a small instruction footprint (about 40 KB; at 140
+// KB every role missed the instruction cache on every block, which made all of
+// them two to three times slower): one copy of each piece of work, loops over
+// unrolling wherever latency does not matter.
 //
 // Warps: NR / 4 for the softmax and the epilogue (a lane is a key, then a
 // column; each group of four owns 16 of the tile's rows and never waits for
@@ -69,6 +77,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint32_t kWaitTries = 100000000u;
 constexpr uint32_t kHintNs = 20;
 constexpr uint32_t kWdAttn = 64;  // watchdog bit of this kernel
 
@@ -86,7 +95,6 @@ struct Roles {
   static constexpr int SOFT = 4 * GROUPS;        // their warps
   static constexpr int MMA = SOFT, TMA = SOFT + 1, ITEM = SOFT + 2, UNIT = SOFT + 3;
   static constexpr int LOAD0 = SOFT + 4, LOADS = 8;
-  static constexpr int FULL = SOFT > LOADS ? SOFT : LOADS;  // arrivals that fill a stage
   static constexpr int THREADS = (LOAD0 + LOADS) * 32;
   static constexpr int REGS = 65536 / THREADS / 8 * 8;
   static constexpr int REGS_SOFT = NR == 64 ? 88 : 112, REGS_ISSUE = NR == 64 ? 56 : 64,
@@ -97,7 +105,7 @@ constexpr int kLoadThreads = 256;
 constexpr int kMaxStages = 5;
 constexpr uint32_t kTmemCols = 512, kTmemS = 256;
 constexpr float kNoKey = 1e30f;      // negm of a row that has seen no key
-constexpr float kSlack = 8.0f;       // log2 of how far a score may pass the maximum
+constexpr float kSlack = 40.0f;      // log2 of how far a score may pass the reference
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct KernelArgs {
@@ -174,15 +182,6 @@ __device__ __forceinline__ Seq get_seq(const AttnArgs& a, int b) {
   s.tiles = (int)(((int64_t)s.n * a.H + NR - 1) / NR);
   return s;
 }
-__device__ __forceinline__ Seq lane_seq(const Seq& s, int lane) {
-  Seq r;
-  r.start = __shfl_sync(0xffffffffu, s.start, lane);
-  r.n = __shfl_sync(0xffffffffu, s.n, lane);
-  r.len = __shfl_sync(0xffffffffu, s.len, lane);
-  r.tiles = __shfl_sync(0xffffffffu, s.tiles, lane);
-  r.clamped = __shfl_sync(0xffffffffu, (int)s.clamped, lane) != 0;
-  return r;
-}
 // Tile t of a sequence: everything but its blocks and its piece.
 template <int NR>
 __device__ __forceinline__ Item get_tile(const AttnArgs& a, const Seq& s, int b, int t) {
@@ -206,133 +205,93 @@ __device__ __forceinline__ Item get_tile(const AttnArgs& a, const Seq& s, int b,
   }
   return it;
 }
-__device__ __forceinline__ int blocks_of(const Item& it) { return (it.units + kUnits - 1) / kUnits; }
-// What a tile weighs in the shares: its blocks; one that sees no key still has
-// its rows to write.
-template <int NR>
-__device__ __forceinline__ int tile_weight(const AttnArgs& a, const Seq& s, int t) {
-  return max(1, blocks_of(get_tile<NR>(a, s, 0, t)));
-}
-__device__ __forceinline__ int warp_sum(int v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-// Weight of each lane's sequence.  Lanes work side by side on their own
-// sequence, or, when one has many tiles, together on one after the other.
-template <int NR>
-__device__ __forceinline__ int seq_weight(const AttnArgs& a, const Seq& s) {
-  const int lane = threadIdx.x & 31;
-  int w = 0;
-  if (__reduce_max_sync(0xffffffffu, s.tiles) <= 16) {
-    for (int t = 0; t < s.tiles; ++t) w += tile_weight<NR>(a, s, t);
-    __syncwarp();
-  } else {
-    for (int l = 0; l < 32; ++l) {
-      const Seq o = lane_seq(s, l);
-      int part = 0;
-      for (int t = lane; t < o.tiles; t += 32) part += tile_weight<NR>(a, o, t);
-      __syncwarp();
-      part = warp_sum(part);
-      if (lane == l) w = part;
-    }
-  }
-  return w;
-}
-
-// The work items of this CTA, in order, given to `emit` (whole warp).
+// The work items of this CTA, in order; the lane that holds one gives it to
+// `emit(item, lane)` (all lanes call it).  Tiles are walked from the last to
+// the first, 32 at a time, one per lane: later tiles of a chunk see more keys.
 template <int NR, typename Emit>
 __device__ __forceinline__ void walk_items(const KernelArgs& k, Emit emit) {
   const AttnArgs& a = k.a;
   const int lane = threadIdx.x & 31;
-  if (!k.shares) {
-    // Tiles counted from the last: later tiles of a chunk see more keys.
-    int before = 0, id = blockIdx.x;
+  const int grid = (int)gridDim.x, cta = (int)blockIdx.x;
+  if (k.shares && lane < 2) k.desc[2 * cta + lane] = make_int4(0, 0, 0, 0);
+  // Pass 0 (shares only) adds up the weights, pass 1 hands out the items.
+  int pos = 0, end = 0;  // this CTA's share of the line of all blocks
+#pragma unroll 1
+  for (int pass = k.shares ? 0 : 1; pass < 2; ++pass) {
+    int run = 0;  // weight of the tiles so far; whole tiles: their number
+#pragma unroll 1
     for (int base = (a.B - 1) & ~31; base >= 0; base -= 32) {
       const Seq s = get_seq<NR>(a, base + lane);
-      // Tiles of this and the later sequences of the group.
-      int upto = s.tiles;
+      int upto = s.tiles;  // tiles of this and the earlier sequences of the group
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_down_sync(0xffffffffu, upto, o);
-        if (lane + o < 32) upto += v;
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
       }
-      const int group = __shfl_sync(0xffffffffu, upto, 0);
-      for (; id < before + group; id += gridDim.x) {
-        // The last sequence whose count passes the number sought.
-        const int l = 31 - __clz((int)__ballot_sync(0xffffffffu, upto > id - before));
-        const Seq o = lane_seq(s, l);
-        const int u = __shfl_sync(0xffffffffu, upto, l);
-        Item it = get_tile<NR>(a, o, base + l, u - 1 - (id - before));
-        it.blk1 = blocks_of(it);
-        it.pad = o.clamped;
-        if (!emit(it)) return;
-      }
-      before += group;
-    }
-    return;
-  }
-  // Equal shares of all blocks; two at least, since a cut costs about one.
-    Seq s = get_seq<NR>(a, lane);
-  int mine = seq_weight<NR>(a, s);
-  int total = warp_sum(mine);
-  for (int base = 32; base < a.B; base += 32) total += warp_sum(seq_weight<NR>(a, get_seq<NR>(a, base + lane)));
-  int share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
-  if (share < 2) share = 2;
-  int pos = (int)min((int64_t)share * blockIdx.x, (int64_t)total);
-  const int end = pos + min(share, total - pos);
-  if (lane < 2) k.desc[2 * blockIdx.x + lane] = make_int4(0, 0, 0, 0);
-  __syncwarp();
-  int run = 0;  // weight of the sequences before the group
-  for (int base = 0; base < a.B && pos < end; base += 32) {
-    if (base > 0) {
-      s = get_seq<NR>(a, base + lane);
-      mine = seq_weight<NR>(a, s);
-    }
-    const int group = warp_sum(mine);
-    if (pos >= run + group) {
-      run += group;
-      continue;
-    }
-    for (int l = 0; l < 32 && pos < end; ++l) {
-      const int w = __shfl_sync(0xffffffffu, mine, l);
-      if (pos >= run + w) {
-        run += w;
-        continue;
-      }
-      const Seq o = lane_seq(s, l);
-      // Skip tiles before pos, 32 at a time.
-      int t = 0;
-      int at = run;  // weight before tile t
-      while (true) {
-        const int tw = t + lane < o.tiles ? tile_weight<NR>(a, o, t + lane) : 0;
-        const int sum = warp_sum(tw);
-        if (at + sum > pos || t + 32 >= o.tiles) break;
-        at += sum;
-        t += 32;
-      }
-      for (; t < o.tiles && pos < end; ++t) {
-        Item it = get_tile<NR>(a, o, base + l, t);
-        const int nb = blocks_of(it), tw = max(nb, 1);
-        if (pos < at + tw) {
-          const int lo = pos - at, hi = min(tw, end - at);
+#pragma unroll 1
+      for (int left = __shfl_sync(0xffffffffu, upto, 31); left > 0; left -= 32) {
+        // This lane's tile of the group, and the sequence it belongs to: the
+        // first whose count passes it.
+        const int f = left - 1 - lane;
+        int l = 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+          if (__shfl_sync(0xffffffffu, upto, l + o - 1) <= f) l += o;
+        Seq q;
+        q.start = __shfl_sync(0xffffffffu, s.start, l);
+        q.n = __shfl_sync(0xffffffffu, s.n, l);
+        q.len = __shfl_sync(0xffffffffu, s.len, l);
+        q.tiles = __shfl_sync(0xffffffffu, s.tiles, l);
+        q.clamped = __shfl_sync(0xffffffffu, (int)s.clamped, l) != 0;
+        const int t = f - (__shfl_sync(0xffffffffu, upto, l) - q.tiles);
+        Item it = {};
+        int nb = 0;
+        if (f >= 0) {
+          it = get_tile<NR>(a, q, base + l, t);
+          nb = (it.units + kUnits - 1) / kUnits;
+        }
+        it.pad = q.clamped;
+        // A tile weighs its blocks in the line; one that sees no key still has
+        // its rows to write.  Whole tiles count one each.
+        const int w = f < 0 ? 0 : k.shares ? max(nb, 1) : 1;
+        int before = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, before, o);
+          if (lane >= o) before += v;
+        }
+        const int sum = __shfl_sync(0xffffffffu, before, 31);
+        before += run - w;  // weight before this tile
+        run += sum;
+        if (pass == 0) continue;
+        bool mine;
+        if (k.shares) {
+          const int lo = max(pos - before, 0), hi = min(end - before, w);
+          mine = lo < hi;
           it.blk0 = min(lo, nb);
           it.blk1 = min(hi, nb);
-          it.pad = o.clamped;
-          if (lo > 0 || hi < tw) {
+          if (mine && (lo > 0 || hi < w)) {
             // Slot 2c: the rest of a tile that an earlier CTA began; slot
             // 2c + 1: the beginning of one that the next CTA goes on with.
-            it.piece = 2 * blockIdx.x + (lo == 0 ? 1 : 0);
-            if (lane == 0)
-              k.desc[it.piece] = make_int4((int)(uint32_t)it.qrow, (int)(it.qrow >> 32), it.nrows,
-                                           kPieceUsed | (hi == tw ? kPieceEnds : 0));
+            it.piece = 2 * cta + (lo == 0 ? 1 : 0);
+            k.desc[it.piece] = make_int4((int)(uint32_t)it.qrow, (int)(it.qrow >> 32), it.nrows,
+                                         kPieceUsed | (hi == w ? kPieceEnds : 0));
           }
-          if (!emit(it)) return;
-          pos = at + hi;
+        } else {
+          it.blk1 = nb;
+          mine = w > 0 && before % grid == cta;
         }
-        at += tw;
+        for (uint32_t m = __ballot_sync(0xffffffffu, mine); m != 0; m &= m - 1)
+          if (!emit(it, __ffs((int)m) - 1)) return;
+        if (k.shares && run >= end) return;
       }
-      run += w;
+    }
+    if (pass == 0) {
+      // Equal shares; two blocks at least, since a cut costs about one.
+      const int share = max((run + grid - 1) / grid, 2);
+      pos = (int)min((int64_t)share * cta, (int64_t)run);
+      end = pos + min(share, run - pos);
+      if (pos == end) return;
     }
   }
 }
@@ -387,9 +346,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void arrive_n(uint64_t* bar, uint32_t n) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(ptx::smem_u32(bar)), "r"(n) : "memory");
 }
 // One try of a barrier wait, asleep for at most kHintNs.
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
@@ -650,10 +606,6 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
   extern __shared__ __align__(1024) uint8_t base[];
   const AttnArgs& a = k.a;
   const int D = a.D, nch = D >> 6, np = (nch + 1) >> 1;
-  // Stages of a block that the loading warps widen; where a block fills the
-  // ring (nothing is loaded ahead then) the softmax warps, idle until the
-  // products are done, widen the others.
-  [[maybe_unused]] const int own = NR == 64 && np > 2 ? 2 : np;
   uint8_t* sm_stage = base;
   uint8_t* sm_p = sm_stage + (size_t)k.stages * kStageBytes;
   uint8_t* sm_q = sm_p + p_bytes(NR);
@@ -664,7 +616,7 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
   if (tid == 0) {
     sh.abort = 0;
     for (int s = 0; s < k.stages; ++s) {
-      ptx::mbar_init(&sh.full[s], DT == MXQ_CACHE_BF16 ? 1 : R::FULL);
+      ptx::mbar_init(&sh.full[s], DT == MXQ_CACHE_BF16 ? 1 : R::LOADS);
       ptx::mbar_init(&sh.empty[s], 1);
     }
     ptx::mbar_init(&sh.s_full[0], 1);
@@ -696,22 +648,17 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
 
-  // A bounded wait; false once it or any other wait of the CTA gave up.
+  // A bounded wait; false once it or any other wait of the CTA gave up.  A try
+  // takes 20 ns or more, so the bound is two seconds or more.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     const uint32_t ad = ptx::smem_u32(bar);
-    if (try_wait(ad, parity)) return true;
-    const uint64_t t0 = ptx::globaltimer();
-    while (true) {
 #pragma unroll 1
-      for (int i = 0; i < 32; ++i)
-        if (try_wait(ad, parity)) return true;
+    for (uint32_t n = 0; n < kWaitTries; ++n) {
+      if (try_wait(ad, parity)) return true;
       if (*abort_flag) return false;
-      if (ptx::globaltimer() - t0 > kWaitNs) {
-        *abort_flag = 1;
-        atomicOr(k.watchdog, kWdAttn);
-        return false;
-      }
     }
+    *abort_flag = 1;
+    return false;
   };
   // The same for a whole warp: its lanes agree on the outcome.
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -739,7 +686,8 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
     regs_set<R::REGS_LOAD, R::REGS>();
     const int lt = tid - R::LOAD0 * 32, lw = lt >> 5;
     int nq = 0;                // items with blocks so far
-    [[maybe_unused]] uint32_t nb = 0;  // blocks so far
+    [[maybe_unused]] uint32_t nb = 0;           // blocks so far
+    [[maybe_unused]] uint32_t st = 0, stp = 0;  // stage and its phase
     bool ok = true;
     Item it;
     for (uint32_t ni = 0; ok && read_item(ni, it); ++ni) {
@@ -783,14 +731,17 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&sh.slot_empty[nb % kSlots]);
           w.fetch(D, 0, lt);
-          for (int pr = 0; pr < own; ++pr) {
-            const uint32_t n = nb * np + pr, st = n % (uint32_t)k.stages;
-            if (!(ok = wait_warp(&sh.empty[st], ((n / (uint32_t)k.stages) & 1u) ^ 1u))) break;
+          for (int pr = 0; pr < np; ++pr) {
+            if (!(ok = wait_warp(&sh.empty[st], stp ^ 1u))) break;
             w.store(sm_stage + st * kStageBytes, lt);
             ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) arrive_n(&sh.full[st], R::FULL / R::LOADS);
-            if (pr + 1 < own) w.fetch(D, pr + 1, lt);
+            if (lane == 0) ptx::mbar_arrive(&sh.full[st]);
+            if (++st == (uint32_t)k.stages) {
+              st = 0;
+              stp ^= 1u;
+            }
+            if (pr + 1 < np) w.fetch(D, pr + 1, lt);
           }
         }
       }
@@ -985,10 +936,7 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
         int stop = *abort_flag;
         if (!stop && ptx::globaltimer() - t0 > kWaitNs) {
           stop = 1;
-          if (lane == 0) {
-            *abort_flag = 1;
-            atomicOr(k.watchdog, kWdAttn);
-          }
+          if (lane == 0) *abort_flag = 1;
         }
         if (__any_sync(0xffffffffu, stop)) break;
       }
@@ -996,29 +944,27 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
     // Everything issued has completed before TMEM and shared memory go away.
     if (ptx::elect_one()) ptx::tc_commit(&sh.drain);
     __syncwarp();
-    if (!ptx::mbar_wait(&sh.drain, 0, kWaitNs) && lane == 0) atomicOr(k.watchdog, kWdAttn);
+    if (!ptx::mbar_wait(&sh.drain, 0, kWaitNs) && lane == 0) *abort_flag = 1;
   } else if (warp == R::ITEM) {
     // ------------------------------------------------------- work items
     // Decoded here once for all roles, up to three ahead.
     regs_set<R::REGS_ISSUE, R::REGS>();
     uint32_t i = 0;
-    auto hand_out = [&](const Item& it) -> bool {
+    auto hand_out = [&](const Item& it, int owner) -> bool {
       if (!wait_warp(&sh.item_empty[i % kItems], ((i / kItems) & 1u) ^ 1u)) return false;
-      if (lane == 0) {
+      if (lane == owner) {
         sh.items[i % kItems] = it;
+        if (it.pad && a.err_flag != nullptr) atomicOr(a.err_flag, MXQ_DEVERR_LENGTH);
         ptx::mbar_arrive(&sh.item_full[i % kItems]);
       }
       __syncwarp();
       ++i;
       return true;
     };
-    walk_items<NR>(k, [&](const Item& it) -> bool {
-      if (lane == 0 && it.pad && a.err_flag != nullptr) atomicOr(a.err_flag, MXQ_DEVERR_LENGTH);
-      return hand_out(it);
-    });
+    walk_items<NR>(k, hand_out);
     Item last = {};
     last.b = -1;
-    hand_out(last);
+    hand_out(last, 0);
   } else if (warp == R::UNIT) {
     // ------------------------------------- where the units of a block lie
     // Lane u < 8 looks up unit u, a few blocks ahead of their use: the block
@@ -1067,6 +1013,13 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
     const float4* lthr4 = reinterpret_cast<const float4*>(sh.lthr + c0);
     uint32_t g = 0;   // blocks so far
     uint32_t st = 0;  // first stage of the current block
+    // The least of the group's thresholds (its first warp; lanes c and c + 16
+    // with row c).
+    auto lowest = [&](float t) {
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) t = fminf(t, __shfl_xor_sync(0xffffffffu, t, o));
+      if (lane == 0) sh.lmin[h] = t;
+    };
     // A wait that gives up does not leave the loops by itself: the group's
     // next vote takes all of its threads out together.
     bool ok = true, dead = false;
@@ -1083,54 +1036,39 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
       // Rows of this group.
       if (quad == 0 && lane < NC) {
         const int r = c0 + lane;
-        sh.negm[r] = r < it.nrows ? kNoKey : 0.0f;
+        sh.rowt[r] = (uint8_t)((held.r0 + r) / a.H - held.r0 / a.H);
         sh.lthr[r] = INFINITY;  // set before the third block
         sh.lmin[h] = INFINITY;
-        sh.rowt[r] = (uint8_t)((held.r0 + r) / a.H - held.r0 / a.H);
       }
+      // The key of the first block whose scores are the first reference: the
+      // first of those that all rows see, where there is one.
+      const int key_ref = a.window > 0 && it.ns == 0 && it.blk0 == 0
+                              ? min(max(it.p1 - a.window + 1 - it.u_lo * kUnit, 0), kKeys - 1) : 0;
       ptx::named_sync(bar, 128);
       float l[NC];
 #pragma unroll
       for (int c = 0; c < NC; ++c) l[c] = 0.0f;
       for (int blk = it.blk0; blk < it.blk1; ++blk) {
-        // Which rows see this thread's key: all, none or some.
+        // Which rows see this thread's key: bit c for the group's row c.
         const int x = blk * kUnits + (key >> 4);
         const bool in = x < it.units;
         const int j = unit_key(it, in ? x : 0) + (key & 15);
         const int weff = (a.window == 0 || j < a.sinks) ? 0x7fffffff : a.window;
         ok = wait(&sh.slot_full[g % kSlots], (g / kSlots) & 1u) && ok;
         const int unit_slot = sh.slots[g % kSlots][key >> 4];
-        if constexpr (DT != MXQ_CACHE_BF16 && NR == 64) {
-          if (own < np) {
-            Widen<DT, R::SOFT * 32> w;
-            w.open(a, sh.slots[g % kSlots], tid);
-            for (int pr = own; pr < np; ++pr) {
-              w.fetch(D, pr, tid);
-              const uint32_t n = g * np + pr, ws = n % (uint32_t)k.stages;
-              ok = wait(&sh.empty[ws], ((n / (uint32_t)k.stages) & 1u) ^ 1u) && ok;
-              w.store(sm_stage + ws * kStageBytes, tid);
-              ptx::fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) arrive_n(&sh.full[ws], R::FULL / R::SOFT);
-            }
-          }
-        }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&sh.slot_empty[g % kSlots]);
         const bool some = in && j <= it.p1 && it.p0 - j < weff && unit_slot >= 0 &&
                           (int64_t)unit_slot + (key & 15) < a.num_slots;
         const bool all = some && j <= it.p0 && it.p1 - j < weff;
-        const bool mixed = __any_sync(0xffffffffu, some && !all);
-        auto sees = [&](int c) { return some && (uint32_t)(it.p0 + sh.rowt[c0 + c] - j) < (uint32_t)weff; };
-
-        // The least of the group's thresholds (called by its first warp, lane c
-        // and lane c + 16 with row c).
-        auto lowest = [&](int r) {
-          float t = sh.lthr[r];
+        uint32_t sees = all ? 0xFFFFu : 0u;
+        if (__any_sync(0xffffffffu, some && !all)) {
+          if (some && !all)
 #pragma unroll
-          for (int o = 8; o > 0; o >>= 1) t = fminf(t, __shfl_xor_sync(0xffffffffu, t, o));
-          if (lane == 0) sh.lmin[h] = t;
-        };
+            for (int c = 0; c < NC; ++c)
+              if ((uint32_t)(it.p0 + sh.rowt[c0 + c] - j) < (uint32_t)weff) sees |= 1u << c;
+          __syncwarp();
+        }
         // Now and then, the sums so far: what a weight is measured against.
         const int done = blk - it.blk0;
         if (done >= 2 && (done & (done - 1)) == 0) {
@@ -1141,86 +1079,112 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
           if (lane < NC) sh.red[h][quad][lane] = part;
           ptx::named_sync(bar, 128);
           if (quad == 0) {
-            const int r = c0 + (lane & 15);
-            if (r < it.nrows)
-              sh.lthr[r] = log2f((sh.red[h][0][lane & 15] + sh.red[h][1][lane & 15]) +
-                                 (sh.red[h][2][lane & 15] + sh.red[h][3][lane & 15])) - 4.0f;
-            lowest(r);
+            const int r = lane & 15;
+            float t = INFINITY;
+            if (c0 + r < it.nrows)
+              t = __log2f((sh.red[h][0][r] + sh.red[h][1][r]) + (sh.red[h][2][r] + sh.red[h][3][r])) - 4.0f;
+            sh.lthr[c0 + r] = t;
+            lowest(t);
           }
           ptx::named_sync(bar, 128);
         }
         ok = wait(&sh.s_full[g & 1u], (g >> 1) & 1u) && ok;
         __syncwarp();
         ptx::tc_fence_after();
-        uint32_t s[NC];
-        tmem_ld<NC>(tq + kTmemS + (g & 1u) * 64 + c0, s);
-        ptx::tmem_ld_wait();
-        // Exponents d = s + negm in place of the scores.  Their largest is NaN
-        // if one is: a cache row with a NaN or an infinity has no finite score.
-        float d[NC], top, seen = -INFINITY;
-        auto exponents = [&]() {
-          top = -INFINITY;
+        const uint32_t ts = tq + kTmemS + (g & 1u) * 64 + c0;
+        if (done == 0) {
+          uint32_t s[NC];
+          if (quad == key_ref >> 5) {
+            tmem_ld<NC>(ts, s);
+            ptx::tmem_ld_wait();
+            if (lane == (key_ref & 31))
 #pragma unroll
-          for (int q = 0; q < NC / 4; ++q) {
-            const float4 n = negm4[q];
-            d[4 * q] = fmaf(__uint_as_float(s[4 * q]), c_all, n.x);
-            d[4 * q + 1] = fmaf(__uint_as_float(s[4 * q + 1]), c_all, n.y);
-            d[4 * q + 2] = fmaf(__uint_as_float(s[4 * q + 2]), c_all, n.z);
-            d[4 * q + 3] = fmaf(__uint_as_float(s[4 * q + 3]), c_all, n.w);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = max_nan(top, d[4 * q + e]);
+              for (int c = 0; c < NC; ++c) {
+                const float v = __uint_as_float(s[c]) * c_all;
+                sh.negm[c0 + c] = ((sees >> c) & 1u) && fabsf(v) <= 3.4028234e38f ? -v
+                                  : c0 + c < it.nrows ? kNoKey : 0.0f;
+              }
           }
-        };
-        exponents();
-        if (mixed)
-#pragma unroll
-          for (int c = 0; c < NC; ++c) seen = fmaxf(seen, sees(c) ? d[c] : -INFINITY);
-        const bool bad = in && !(fabsf(top) <= 3.4028234e38f);
-        const bool raise = bad || (some && (mixed ? seen : top) > kSlack);
+          ptx::named_sync(bar, 128);
+        }
         // P's buffers are free once the previous block's second product is done.
-        if (blk > it.blk0) {
+        if (done > 0) {
           ok = wait(&sh.pv_done, (g - 1) & 1u) && ok;
           __syncwarp();
         }
+        float d[NC];
+        bool odd = false;  // a second time: some scores are not finite
+#pragma unroll 1
         for (bool again = false;;) {
-          // ---- weights, in place of the exponents, written before it is known
-          // whether a maximum has to move: it hardly ever has.
-          // Units in which some weight is large against its row's sum so far:
+          // ---- exponents d = s + negm, and the weights in their place, written
+          // before it is known whether a reference has to move: it hardly ever has.
+          {
+            uint32_t s[NC];
+            tmem_ld<NC>(ts, s);
+            ptx::tmem_ld_wait();
+            if (odd)
+#pragma unroll
+              for (int c = 0; c < NC; ++c)
+                if (!(fabsf(__uint_as_float(s[c])) <= 3.4028234e38f)) sees &= ~(1u << c);
+#pragma unroll
+            for (int q = 0; q < NC / 4; ++q) {
+              const float4 n = negm4[q];
+              d[4 * q] = fmaf(__uint_as_float(s[4 * q]), c_all, n.x);
+              d[4 * q + 1] = fmaf(__uint_as_float(s[4 * q + 1]), c_all, n.y);
+              d[4 * q + 2] = fmaf(__uint_as_float(s[4 * q + 2]), c_all, n.z);
+              d[4 * q + 3] = fmaf(__uint_as_float(s[4 * q + 3]), c_all, n.w);
+            }
+          }
+          // The largest, NaN if one is: a cache row with a NaN or an infinity
+          // has no finite score.
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) top = max_nan(top, d[c]);
+          const bool bad = in && !(fabsf(top) <= 3.4028234e38f);
+          float most = top;  // of the rows that see the key
+          if (some && !all) {
+            most = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              if ((sees >> c) & 1u) most = fmaxf(most, d[c]);
+          }
+          const bool raise = bad || (some && most > kSlack);
+          // Units in which some weight is large against its row's sum so far.
           uint32_t hot = ~0u;
           if (done >= 2) {
             bool big = false;
-            if (top > sh.lmin[h]) {
+            if (some && top > sh.lmin[h]) {
 #pragma unroll
               for (int q = 0; q < NC / 4; ++q) {
                 const float4 t = lthr4[q];
                 big |= d[4 * q] > t.x || d[4 * q + 1] > t.y || d[4 * q + 2] > t.z || d[4 * q + 3] > t.w;
               }
             }
-            hot = __ballot_sync(0xffffffffu, some && big);
+            hot = __ballot_sync(0xffffffffu, big);
           }
           if (lane == 0) sh.hot[h][quad] = (uint8_t)(((hot & 0xFFFFu) ? 1 : 0) | ((hot >> 16) ? 2 : 0));
 #pragma unroll
-          for (int c = 0; c < NC; ++c) d[c] = (mixed ? sees(c) : all) ? ex2(d[c]) : 0.0f;
+          for (int c = 0; c < NC; ++c) d[c] = ((sees >> c) & 1u) ? ex2(d[c]) : 0.0f;
+          uint8_t* prow = sm_p + key * 128;
 #pragma unroll
           for (int q = 0; q < NC / 8; ++q) {
-            uint32_t hi[4], lo[4];
+            uint32_t hi[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              hi[e] = pack2(d[8 * q + 2 * e], d[8 * q + 2 * e + 1]);
-              if (hot != 0) lo[e] = pack2_rest(d[8 * q + 2 * e], d[8 * q + 2 * e + 1], hi[e]);
+            for (int e = 0; e < 4; ++e) hi[e] = pack2(d[8 * q + 2 * e], d[8 * q + 2 * e + 1]);
+            *reinterpret_cast<uint4*>(prow + ((((c0 >> 3) + q) ^ (key & 7)) << 4)) =
+                make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (hot != 0) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) hi[e] = pack2_rest(d[8 * q + 2 * e], d[8 * q + 2 * e + 1], hi[e]);
+              const int col = (c0 >> 3) + q + (NR == 64 ? 0 : NR / 8);
+              *reinterpret_cast<uint4*>(prow + (NR == 64 ? kKeys * 128 : 0) + ((col ^ (key & 7)) << 4)) =
+                  make_uint4(hi[0], hi[1], hi[2], hi[3]);
             }
-            const int col = (c0 >> 3) + q;
-            uint8_t* row = sm_p + key * 128;
-            *reinterpret_cast<uint4*>(row + ((col ^ (key & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            const int lcol = NR == 64 ? col : col + NR / 8;
-            if (hot != 0)
-              *reinterpret_cast<uint4*>(row + (NR == 64 ? kKeys * 128 : 0) + ((lcol ^ (key & 7)) << 4)) =
-                  make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
           ptx::fence_proxy_async_smem();
           if (again || !named_any(bar, 128, raise || !ok)) break;
           again = true;
-          // ---- some maximum moves, something is not finite, or a wait gave up
+          // ---- some reference moves, something is not finite, or a wait gave up
           if (named_any(bar, 128, !ok)) {
             dead = true;
             break;
@@ -1230,64 +1194,57 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
             // that do not see it through 0 * NaN: it is cleared here, and the
             // rows that see it become NaN through their sums.
             bool rowbad = false;
-            for (int pass = 0; pass < 2; ++pass)
-              for (int ch = 0; ch < nch; ++ch) {
-                const uint32_t sidx = (st + (ch >> 1)) % (uint32_t)k.stages;
-                uint4* rp = reinterpret_cast<uint4*>(sm_stage + sidx * kStageBytes + (ch & 1) * kChunkBytes + key * 128);
-                for (int e = 0; e < 8; ++e) {
-                  if (pass == 1) {
-                    if (rowbad) rp[e] = make_uint4(0, 0, 0, 0);
-                    continue;
-                  }
-                  const uint4 w = rp[e];
-                  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-                  const uint32_t m = 0x7F80u;
-                  for (int q = 0; q < 4; ++q)
-                    rowbad |= (ws[q] & m) == m || ((ws[q] >> 16) & m) == m;
-                }
+#pragma unroll 1
+            for (int e = 0; e < nch * 16; ++e) {  // the row's 16-byte words, twice over
+              const int w8 = e >= nch * 8 ? e - nch * 8 : e, ch = w8 >> 3;
+              const uint32_t sidx = (st + (ch >> 1)) % (uint32_t)k.stages;
+              uint4* wp = reinterpret_cast<uint4*>(sm_stage + sidx * kStageBytes + (ch & 1) * kChunkBytes + key * 128) +
+                          (w8 & 7);
+              if (e >= nch * 8) {
+                if (rowbad) *wp = make_uint4(0, 0, 0, 0);
+                continue;
               }
+              const uint4 w = *wp;
+              const uint32_t m = 0x7F807F80u;
+              // Both halves of a word at once: an exponent field of ones.
+              auto full = [&](uint32_t v) { return ((v & 0x7F80u) == 0x7F80u) || ((v & m) >> 16) == 0x7F80u; };
+              rowbad |= full(w.x) || full(w.y) || full(w.z) || full(w.w);
+            }
           }
-          // The scores again (s is not kept: registers), and their maxima.
-          tmem_ld<NC>(tq + kTmemS + (g & 1u) * 64 + c0, s);
-          ptx::tmem_ld_wait();
+          odd = bad;
+          // The scores again, and their maxima.
+          {
+            uint32_t s[NC];
+            tmem_ld<NC>(ts, s);
+            ptx::tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const float v = __uint_as_float(s[c]);
-            const bool fin = fabsf(v) <= 3.4028234e38f;
-            const bool see = mixed ? sees(c) : all;
-            if (bad && !fin && see) l[c] = NAN;
-            d[c] = see && fin ? v * c_all : -INFINITY;
+            for (int c = 0; c < NC; ++c) {
+              const float v = __uint_as_float(s[c]);
+              const bool fin = fabsf(v) <= 3.4028234e38f, see = (sees >> c) & 1u;
+              if (bad && !fin && see) l[c] = NAN;
+              d[c] = see && fin ? v * c_all : -INFINITY;
+            }
           }
           const float m = lanes_reduce<NC, true>(d);
           if (lane < NC) sh.red[h][quad][lane] = m;
           ptx::named_sync(bar, 128);
-          if (quad == 0 && lane < NC) {
-            const int r = c0 + lane;
-            const float mb = fmaxf(fmaxf(sh.red[h][0][lane], sh.red[h][1][lane]),
-                                   fmaxf(sh.red[h][2][lane], sh.red[h][3][lane]));
-            const float old = sh.negm[r];
-            float f = 1.0f;
-            if (r < it.nrows && mb > -INFINITY) {
-              const float cur = old >= kNoKey ? -INFINITY : -old;
-              if (mb > cur) {
-                if (old < kNoKey) f = ex2(cur - mb);
-                sh.negm[r] = -mb;
-              }
-            }
-            sh.scale[r] = f;
-            if (f != 1.0f) sh.lthr[r] += log2f(f);  // stays infinite while it is
-          }
           if (quad == 0) {
+            const int r = lane & 15;
+            const float mb = fmaxf(fmaxf(sh.red[h][0][r], sh.red[h][1][r]), fmaxf(sh.red[h][2][r], sh.red[h][3][r]));
+            const float old = sh.negm[c0 + r];
+            float f = 1.0f, t = sh.lthr[c0 + r];
             __syncwarp();
-            lowest(c0 + (lane & 15));
+            if (c0 + r < it.nrows && mb > -INFINITY && (old >= kNoKey || mb > -old)) {
+              if (old < kNoKey) f = ex2(-old - mb);
+              if (lane < NC) sh.negm[c0 + r] = -mb;
+              if (f != 1.0f) t += __log2f(f);  // stays infinite while it is
+            }
+            sh.scale[c0 + r] = f;
+            sh.lthr[c0 + r] = t;
+            lowest(t);
           }
           ptx::named_sync(bar, 128);
-          exponents();
-          if (bad)
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-              if (!(fabsf(__uint_as_float(s[c])) <= 3.4028234e38f)) d[c] = -INFINITY;
-          if (blk > it.blk0) {
+          if (done > 0) {
             bool moved = false;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
@@ -1296,19 +1253,18 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
               moved |= f != 1.0f;
             }
             if (moved) {
-              ptx::tc_fence_after();
-              for (int m = 0; m < np; ++m)
+#pragma unroll 1
+              for (int o8 = 0; o8 < np * (NC / 8); ++o8) {
+                uint32_t o[8];
+                const int c = (o8 % (NC / 8)) * 8;
+                const uint32_t ad = tq + (o8 / (NC / 8)) * NR + c0 + c;
+                ptx::tmem_ld_32x32b_x8(ad, o);
+                ptx::tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < NC; c += 8) {
-                  uint32_t o[8];
-                  const uint32_t ad = tq + m * NR + c0 + c;
-                  ptx::tmem_ld_32x32b_x8(ad, o);
-                  ptx::tmem_ld_wait();
-#pragma unroll
-                  for (int e = 0; e < 8; ++e)
-                    o[e] = __float_as_uint(__uint_as_float(o[e]) * sh.scale[c0 + c + e]);
-                  tmem_st8(ad, o);
-                }
+                for (int e = 0; e < 8; ++e)
+                  o[e] = __float_as_uint(__uint_as_float(o[e]) * sh.scale[c0 + c + e]);
+                tmem_st8(ad, o);
+              }
               tmem_st_wait();
             }
           }
@@ -1326,26 +1282,22 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
       // ---- row sums over the 128 keys, then the output
       const float sum32 = lanes_reduce<NC, false>(l);
       if (lane < NC) sh.red[h][quad][lane] = sum32;
-      if (has) {
-        ok = wait(&sh.pv_done, (g - 1) & 1u) && ok;
-        if (named_any(bar, 128, !ok)) {
-          dead = true;
-          break;
-        }
-      } else {
-        ptx::named_sync(bar, 128);
+      if (has) ok = wait(&sh.pv_done, (g - 1) & 1u) && ok;
+      if (named_any(bar, 128, !ok)) {
+        dead = true;
+        break;
       }
       ptx::tc_fence_after();
       if (quad == 0 && lane < NC) {
         const int r = c0 + lane;
         const float sum = (sh.red[h][0][lane] + sh.red[h][1][lane]) + (sh.red[h][2][lane] + sh.red[h][3][lane]);
-        const float nm = sh.negm[r];
+        const float nm = has ? sh.negm[r] : kNoKey;
         if (held.piece >= 0) {
           k.part_ml[(int64_t)held.piece * NR + r] = make_float2(-nm, sum);
         } else {
           sh.scale[r] = sum == 0.0f ? 0.0f : vs / sum;
           if (r < it.nrows && a.lse != nullptr)
-            a.lse[held.qrow + r] = sum == 0.0f ? -INFINITY : (log2f(sum) - nm) * 0.6931471805599453f;
+            a.lse[held.qrow + r] = sum == 0.0f ? -INFINITY : (__log2f(sum) - nm) * 0.6931471805599453f;
         }
       }
       ptx::named_sync(bar, 128);
@@ -1375,22 +1327,23 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
         for (int q = 0; q < NC / 8; ++q)
           sc[q] = *reinterpret_cast<const float2*>(&sh.scale[c0 + q * 8 + (lane & 3) * 2]);
         uint8_t* dst = static_cast<uint8_t*>(a.out) + (held.qrow + c0) * D * 2;
+#pragma unroll 1
         for (int m0 = 0; m0 < np; m0 += 2) {
-          for (int m = m0; m < min(m0 + 2, np); ++m)
+          uint32_t o[4][NC / 2];
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              uint32_t o[NC / 2];
-              tmem_ld_16x256b<NC>(tq + ((uint32_t)(hf * 16) << 16) + m * NR + c0, o);
-              ptx::tmem_ld_wait();
+          for (int f = 0; f < 4; ++f)  // m0 + f / 2, lanes 16 * (f % 2) on
+            tmem_ld_16x256b<NC>(tq + ((uint32_t)((f & 1) * 16) << 16) + min(m0 + (f >> 1), np - 1) * NR + c0, o[f]);
+          ptx::tmem_ld_wait();
 #pragma unroll
-              for (int q = 0; q < NC / 8; ++q) {
-                const uint32_t w0 = pack2(out_of(has, o[4 * q]) * sc[q].x, out_of(has, o[4 * q + 1]) * sc[q].y);
-                const uint32_t w1 = pack2(out_of(has, o[4 * q + 2]) * sc[q].x, out_of(has, o[4 * q + 3]) * sc[q].y);
-                // Lanes 0-7 name the rows of the first matrix, 8-15 of the second.
-                const int row = q * 8 + (lane & 7);
-                const int word = (m - m0) * 16 + quad * 4 + hf * 2 + ((lane >> 3) & 1);
-                stmatrix_x2_trans(stage_a + row * 512 + ((word ^ (row & 7)) << 4), w0, w1);
-              }
+          for (int f = 0; f < 4; ++f)
+#pragma unroll
+            for (int q = 0; q < NC / 8; ++q) {
+              const uint32_t w0 = pack2(out_of(has, o[f][4 * q]) * sc[q].x, out_of(has, o[f][4 * q + 1]) * sc[q].y);
+              const uint32_t w1 = pack2(out_of(has, o[f][4 * q + 2]) * sc[q].x, out_of(has, o[f][4 * q + 3]) * sc[q].y);
+              // Lanes 0-7 name the rows of the first matrix, 8-15 of the second.
+              const int row = q * 8 + (lane & 7);
+              const int word = (f >> 1) * 16 + quad * 4 + (f & 1) * 2 + ((lane >> 3) & 1);
+              stmatrix_x2_trans(stage_a + row * 512 + ((word ^ (row & 7)) << 4), w0, w1);
             }
           ptx::named_sync(bar, 128);
           for (int i = quad; i < NC; i += 4) {
@@ -1410,73 +1363,81 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
     }
   }
   __syncthreads();
+  if (tid == 0 && sh.abort) atomicOr(k.watchdog, kWdAttn);
   if (warp == R::MMA) ptx::tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the partial sums of the tiles that are cut: CTA (c, y) the one that
-// begins in share c, if any, one warp per row.  Its pieces lie in the slots
-// 2c + 1, 2(c + 1), 2(c + 2), ...; they are added in this order, each weighted
-// by 2^(its maximum - the largest).
-constexpr int kJoinWarps = 4;
+// Joins the partial sums of the tiles that are cut: CTA (c, y) row y of the one
+// that begins in share c, if any.  Its pieces lie in the slots 2c + 1,
+// 2(c + 1), 2(c + 2), ...; each counts 2^(its reference - the largest).  Thread
+// (u, v) adds up every kJoinWays-th piece of columns 4u..4u+3, in order, and the
+// kJoinWays sums are added in order: the result does not depend on timing.
+constexpr int kJoinWays = 4;
 template <int NR>
-__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const KernelArgs k) {
+__global__ void __launch_bounds__(128 * kJoinWays) attn_join_kernel(const KernelArgs k) {
+  __shared__ float4 part[kJoinWays][128];
+  __shared__ float sums[kJoinWays];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const AttnArgs& a = k.a;
-  const int lane = threadIdx.x & 31;
-  const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  const int col = (threadIdx.x & 127) * 4, way = threadIdx.x >> 7, lane = threadIdx.x & 31;
+  const int r = blockIdx.y;
   const int first = 2 * blockIdx.x + 1;
   const int4 d = k.desc[first];
   if (!(d.w & kPieceUsed) || r >= d.z) return;
-  int used = 1;
-  // Every CTA has a slot, and the last piece of a tile is marked: the bound
-  // only keeps a broken chain from running out of the table.
-  while (2 * (blockIdx.x + used) < 2 * gridDim.x) {
-    const int f = k.desc[2 * (blockIdx.x + used)].w;
-    if (!(f & kPieceUsed)) break;
-    ++used;
-    if (f & kPieceEnds) break;
-  }
+  // Slot of piece i, and the number of pieces: every CTA has slots, and the
+  // last piece of a tile is marked.
   auto slot = [&](int i) { return i == 0 ? first : 2 * ((int)blockIdx.x + i); };
+  int used = 1;
+  for (int from = 1; blockIdx.x + from < gridDim.x; from += 32) {
+    const int f = blockIdx.x + from + lane < gridDim.x ? k.desc[slot(from + lane)].w : 0;
+    const uint32_t stop = __ballot_sync(0xffffffffu, !(f & kPieceUsed) || (f & kPieceEnds));
+    if (stop != 0) {
+      const int l = __ffs((int)stop) - 1;
+      used = from + l + ((__shfl_sync(0xffffffffu, f, l) & kPieceUsed) ? 1 : 0);
+      break;
+    }
+    used = from + 32;
+  }
   float mx = -INFINITY;
   for (int i = lane; i < used; i += 32) mx = fmaxf(mx, k.part_ml[(int64_t)slot(i) * NR + r].x);
   mx = warp_max(mx);
-  float o[16];
-#pragma unroll
-  for (int c = 0; c < 16; ++c) o[c] = 0.0f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < used; ++i) {
-    const int64_t at = (int64_t)slot(i) * NR + r;
-    const float2 v = k.part_ml[at];
-    const float f = ex2(v.x - mx);
-    sum += f * v.y;
-    const float* ps = k.part + at * a.D;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int col = c * 128 + lane * 4;
-      if (col < a.D) {
-        const float4 x = *reinterpret_cast<const float4*>(ps + col);
-        o[4 * c] += f * x.x;
-        o[4 * c + 1] += f * x.y;
-        o[4 * c + 2] += f * x.z;
-        o[4 * c + 3] += f * x.w;
-      }
+  if (col < a.D) {
+#pragma unroll 8
+    for (int i = way; i < used; i += kJoinWays) {
+      const int64_t at = (int64_t)slot(i) * NR + r;
+      const float2 v = k.part_ml[at];
+      const float4 x = *reinterpret_cast<const float4*>(k.part + at * a.D + col);
+      const float f = ex2(v.x - mx);
+      sum += f * v.y;
+      o.x += f * x.x;
+      o.y += f * x.y;
+      o.z += f * x.z;
+      o.w += f * x.w;
     }
+  }
+  part[way][threadIdx.x & 127] = o;
+  if (col == 0) sums[way] = sum;
+  __syncthreads();
+  if (way != 0 || col >= a.D) return;
+  sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+#pragma unroll
+  for (int w = 1; w < kJoinWays; ++w) {
+    const float4 x = part[w][threadIdx.x & 127];
+    o.x += x.x;
+    o.y += x.y;
+    o.z += x.z;
+    o.w += x.w;
   }
   const float vs = a.dtype == MXQ_CACHE_E4M3 ? __ldg(a.kv_scale) : 1.0f;
   const float inv = sum == 0.0f ? 0.0f : vs / sum;
   const int64_t row = (int64_t)(((uint64_t)(uint32_t)d.y << 32) | (uint32_t)d.x) + r;
-  uint8_t* dst = static_cast<uint8_t*>(a.out) + row * a.D * 2;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const int col = c * 128 + lane * 4;
-    if (col < a.D)
-      *reinterpret_cast<uint2*>(dst + col * 2) = make_uint2(pack2(o[4 * c] * inv, o[4 * c + 1] * inv),
-                                                            pack2(o[4 * c + 2] * inv, o[4 * c + 3] * inv));
-  }
-  if (lane == 0 && a.lse != nullptr)
-    a.lse[row] = sum == 0.0f ? -INFINITY : (log2f(sum) + mx) * 0.6931471805599453f;
+  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + (row * a.D + col) * 2) =
+      make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
+  if (col == 0 && a.lse != nullptr)
+    a.lse[row] = sum == 0.0f ? -INFINITY : (__log2f(sum) + mx) * 0.6931471805599453f;
 }
 
 // ---------------------------------------------------------------- host side
@@ -1563,8 +1524,8 @@ cudaError_t launch_one(const KernelArgs& k, int grid, cudaStream_t s, const char
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, tm, k);
   if (e != cudaSuccess || !k.shares) return e;
-  cfg.gridDim = dim3((unsigned)grid, NR / kJoinWarps, 1);
-  cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
+  cfg.gridDim = dim3((unsigned)grid, NR, 1);
+  cfg.blockDim = dim3(128 * kJoinWays, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attn_join_kernel<NR>, k);
 }
