@@ -345,12 +345,31 @@ def mxq_rope_kv_insert(q, kv, pos, cos, sin, R, slot_mapping, cache, scale=None,
 
 
 def _tensor(fn, name, t, dtype, shape=None):
-    """Refuses a tensor that is not a contiguous CUDA tensor of this dtype (and shape, None = any size)."""
-    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous()):
+    """The address of a contiguous CUDA tensor of this dtype (and shape, None = any size); refuses others."""
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         raise MxqError(fn, 2, f"{name} must be a contiguous CUDA tensor of {dtype}")
-    if shape is not None and (t.dim() != len(shape)
-                              or any(w is not None and w != n for n, w in zip(t.shape, shape))):
-        raise MxqError(fn, 2, f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if shape is not None:
+        got = t.shape
+        if len(got) != len(shape) or any(w is not None and w != n for n, w in zip(got, shape)):
+            raise MxqError(fn, 2, f"{name} has shape {tuple(got)}, not {shape}")
+    return t.data_ptr()
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+# The current stream's handle without a Stream object around it, where torch has it (a decode step makes
+# several calls of a few microseconds each).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def mxq_rope_kv4_insert(q, kv, pos, cos, sin, R, slot_mapping, cache, cache_sf, q_out=None,
@@ -360,43 +379,55 @@ def mxq_rope_kv4_insert(q, kv, pos, cos, sin, R, slot_mapping, cache, cache_sf, 
     (E8M0 scale of each 32 values).  q (or None) and q_out as in mxq_rope_kv_insert; returns q_out."""
     fn = "mxq_rope_kv4_insert"
     T, Dk = kv.shape
-    _tensor(fn, "kv", kv, torch.bfloat16)
-    _tensor(fn, "slot_mapping", slot_mapping, torch.int64, (T,))
-    _tensor(fn, "cache", cache, torch.uint8, (None, Dk // 2))
-    _tensor(fn, "cache_sf", cache_sf, torch.uint8, (cache.shape[0], Dk // 32))
+    num_slots = cache.shape[0]
+    pkv = _tensor(fn, "kv", kv, torch.bfloat16)
+    pslot = _tensor(fn, "slot_mapping", slot_mapping, torch.int64, (T,))
+    pcache = _tensor(fn, "cache", cache, torch.uint8, (None, Dk // 2))
+    psf = _tensor(fn, "cache_sf", cache_sf, torch.uint8, (num_slots, Dk // 32))
     H = Dq = 0
+    pq = pout = ppos = pcos = psin = None
     if q is not None:
         _, H, Dq = q.shape
-        _tensor(fn, "q", q, torch.bfloat16, (T, None, None))
+        pq = _tensor(fn, "q", q, torch.bfloat16, (T, None, None))
         if q_out is None:
             q_out = torch.empty_like(q)
-        _tensor(fn, "q_out", q_out, torch.bfloat16, (T, H, Dq))
+            pout = q_out.data_ptr()
+        else:
+            pout = _tensor(fn, "q_out", q_out, torch.bfloat16, (T, H, Dq))
     cs_ld = max_pos = 0
     if R > 0:
-        _tensor(fn, "pos", pos, torch.int64, (T,))
-        if cos.dtype != torch.bfloat16 or sin.dtype != torch.bfloat16 or cos.stride() != sin.stride() \
-                or cos.stride(1) != 1 or cos.shape != sin.shape or cos.shape[1] < R // 2:
-            raise MxqError(fn, 2, "cos and sin must be bf16 [max_pos, >= R/2] with the same strides")
-        cs_ld, max_pos = cos.stride(0), cos.shape[0]
-    st = lib().mxq_rope_kv4_insert(_ptr(q), _ptr(q_out), T, H, Dq, _ptr(kv), Dk, _ptr(pos), _ptr(cos),
-                                   _ptr(sin), cs_ld, max_pos, R, _ptr(slot_mapping), _ptr(cache),
-                                   _ptr(cache_sf), cache.shape[0], _ptr(err_flag), _stream(stream))
-    _check(fn, st)
+        ppos = _tensor(fn, "pos", pos, torch.int64, (T,))
+        max_pos, width = cos.shape
+        cs_ld = cos.stride(0)
+        if cos.dtype is not torch.bfloat16 or sin.dtype is not torch.bfloat16 or not cos.is_cuda \
+                or not sin.is_cuda or cos.stride() != sin.stride() or cos.stride(1) != 1 \
+                or cos.shape != sin.shape or width < R // 2:
+            raise MxqError(fn, 2, "cos and sin must be CUDA bf16 [max_pos, >= R/2] with the same strides")
+        pcos, psin = cos.data_ptr(), sin.data_ptr()
+    st = lib().mxq_rope_kv4_insert(pq, pout, T, H, Dq, pkv, Dk, ppos, pcos, psin, cs_ld, max_pos, R, pslot,
+                                   pcache, psf, num_slots, _addr(err_flag), _stream_of(stream, kv.device))
+    if st:
+        _check(fn, st)
     return q_out
 
 
 def mxq_kv4_gather(cache, cache_sf, slots, out=None, err_flag=None, stream=None):
     """Rows `slots` (int64 [n]) of a 4-bit cache as bf16 [n, Dk] (zeros for a negative slot)."""
     fn = "mxq_kv4_gather"
-    Dk, n = cache.shape[1] * 2, slots.numel()
-    _tensor(fn, "cache", cache, torch.uint8)
-    _tensor(fn, "cache_sf", cache_sf, torch.uint8, (cache.shape[0], Dk // 32))
-    _tensor(fn, "slots", slots, torch.int64, (n,))
+    num_slots, half = cache.shape
+    Dk, n = half * 2, slots.numel()
+    pcache = _tensor(fn, "cache", cache, torch.uint8)
+    psf = _tensor(fn, "cache_sf", cache_sf, torch.uint8, (num_slots, Dk // 32))
+    pslots = _tensor(fn, "slots", slots, torch.int64, (n,))
     if out is None:
         out = torch.empty((n, Dk), dtype=torch.bfloat16, device=cache.device)
-    _tensor(fn, "out", out, torch.bfloat16, (n, Dk))
-    _check(fn, lib().mxq_kv4_gather(_ptr(cache), _ptr(cache_sf), cache.shape[0], Dk, _ptr(slots), n,
-                                    _ptr(out), _ptr(err_flag), _stream(stream)))
+        pout = out.data_ptr()
+    else:
+        pout = _tensor(fn, "out", out, torch.bfloat16, (n, Dk))
+    st = lib().mxq_kv4_gather(pcache, psf, num_slots, Dk, pslots, n, pout, _addr(err_flag),
+                              _stream_of(stream, cache.device))
+    if st:
+        _check(fn, st)
     return out
 
 
@@ -419,35 +450,39 @@ def mxq_attn(q, cache, block_table, seq_lens, q_start=None, page_size=64, window
     fn = "mxq_attn"
     T, H, D = q.shape
     B, max_pages = block_table.shape
-    _tensor(fn, "q", q, torch.bfloat16)
-    _tensor(fn, "block_table", block_table, torch.int32)
-    _tensor(fn, "seq_lens", seq_lens, torch.int32, (B,))
-    if q_start is not None:
-        _tensor(fn, "q_start", q_start, torch.int32, (B + 1,))
+    num_slots = cache.shape[0]
+    pq = _tensor(fn, "q", q, torch.bfloat16)
+    pbt = _tensor(fn, "block_table", block_table, torch.int32)
+    plen = _tensor(fn, "seq_lens", seq_lens, torch.int32, (B,))
+    pstart = None if q_start is None else _tensor(fn, "q_start", q_start, torch.int32, (B + 1,))
+    psf = pscale = None
     if cache_sf is not None:
         dtype = MXQ_CACHE_E2M1
-        _tensor(fn, "cache", cache, torch.uint8, (None, D // 2))
-        _tensor(fn, "cache_sf", cache_sf, torch.uint8, (cache.shape[0], D // 32))
-    elif cache.dtype == torch.uint8:
+        pcache = _tensor(fn, "cache", cache, torch.uint8, (None, D // 2))
+        psf = _tensor(fn, "cache_sf", cache_sf, torch.uint8, (num_slots, D // 32))
+    elif cache.dtype is torch.uint8:
         dtype = MXQ_CACHE_E4M3
-        _tensor(fn, "cache", cache, torch.uint8, (None, D))
+        pcache = _tensor(fn, "cache", cache, torch.uint8, (None, D))
         if kv_scale is not None:
-            _tensor(fn, "kv_scale", kv_scale, torch.float32)
+            pscale = _tensor(fn, "kv_scale", kv_scale, torch.float32)
     else:
         dtype = MXQ_CACHE_BF16
-        _tensor(fn, "cache", cache, torch.bfloat16, (None, D))
+        pcache = _tensor(fn, "cache", cache, torch.bfloat16, (None, D))
     if out is None:
         out = torch.empty_like(q)
-    _tensor(fn, "out", out, torch.bfloat16, (T, H, D))
-    if lse is not None:
-        _tensor(fn, "lse", lse, torch.float32, (T, H))
+        pout = out.data_ptr()
+    else:
+        pout = _tensor(fn, "out", out, torch.bfloat16, (T, H, D))
+    plse = None if lse is None else _tensor(fn, "lse", lse, torch.float32, (T, H))
+    L = lib()
     if ws is None:
-        need = mxq_attn_workspace_bytes(T, B, H, D, max_pages, page_size, window, sinks)
+        need = L.mxq_attn_workspace_bytes(T, B, H, D, max_pages, page_size, window, sinks)
         if need > 0:
             ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    st = lib().mxq_attn(_ptr(q), T, H, D, _ptr(q_start), _ptr(seq_lens), B, _ptr(block_table), max_pages,
-                        page_size, _ptr(cache), cache.shape[0], dtype, _ptr(kv_scale), _ptr(cache_sf),
-                        window, sinks, D ** -0.5 if sm_scale is None else sm_scale, _ptr(out), _ptr(lse),
-                        _ptr(err_flag), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream))
-    _check(fn, st)
+    pws, nws = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
+    st = L.mxq_attn(pq, T, H, D, pstart, plen, B, pbt, max_pages, page_size, pcache, num_slots, dtype, pscale, psf,
+                    window, sinks, D ** -0.5 if sm_scale is None else sm_scale, pout, plse, _addr(err_flag), pws,
+                    nws, _stream_of(stream, q.device))
+    if st:
+        _check(fn, st)
     return out

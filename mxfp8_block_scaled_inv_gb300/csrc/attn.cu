@@ -144,7 +144,6 @@ struct Shared {
   int slots[kSlots][kUnits];  // cache row of each unit's first key, -1: none
   alignas(16) float negm[64];
   float lthr[64];   // log2 of the weight from which the second part counts
-  float lmin[4];    // the least of each group
   float scale[64];  // the rescale factors of a block; in the epilogue 1 / sum
   uint8_t rowt[64];  // a row's token, counted from the tile's first
   uint8_t hot[4][4];  // per group and quarter: units with such a weight (2 bits)
@@ -380,6 +379,26 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float y;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Two FP32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
 }
 // Maximum (or sum) over the 32 lanes of N values each, by halving exchanges:
 // lane c < N ends with value c.  31 shuffles for 32 values.
@@ -1013,13 +1032,6 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
     const float4* lthr4 = reinterpret_cast<const float4*>(sh.lthr + c0);
     uint32_t g = 0;   // blocks so far
     uint32_t st = 0;  // first stage of the current block
-    // The least of the group's thresholds (its first warp; lanes c and c + 16
-    // with row c).
-    auto lowest = [&](float t) {
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) t = fminf(t, __shfl_xor_sync(0xffffffffu, t, o));
-      if (lane == 0) sh.lmin[h] = t;
-    };
     // A wait that gives up does not leave the loops by itself: the group's
     // next vote takes all of its threads out together.
     bool ok = true, dead = false;
@@ -1038,7 +1050,6 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
         const int r = c0 + lane;
         sh.rowt[r] = (uint8_t)((held.r0 + r) / a.H - held.r0 / a.H);
         sh.lthr[r] = INFINITY;  // set before the third block
-        sh.lmin[h] = INFINITY;
       }
       // The key of the first block whose scores are the first reference: the
       // first of those that all rows see, where there is one.
@@ -1084,7 +1095,6 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
             if (c0 + r < it.nrows)
               t = __log2f((sh.red[h][0][r] + sh.red[h][1][r]) + (sh.red[h][2][r] + sh.red[h][3][r])) - 4.0f;
             sh.lthr[c0 + r] = t;
-            lowest(t);
           }
           ptx::named_sync(bar, 128);
         }
@@ -1129,17 +1139,22 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
 #pragma unroll
             for (int q = 0; q < NC / 4; ++q) {
               const float4 n = negm4[q];
-              d[4 * q] = fmaf(__uint_as_float(s[4 * q]), c_all, n.x);
-              d[4 * q + 1] = fmaf(__uint_as_float(s[4 * q + 1]), c_all, n.y);
-              d[4 * q + 2] = fmaf(__uint_as_float(s[4 * q + 2]), c_all, n.z);
-              d[4 * q + 3] = fmaf(__uint_as_float(s[4 * q + 3]), c_all, n.w);
+              const float2 lo = fma2(make_float2(__uint_as_float(s[4 * q]), __uint_as_float(s[4 * q + 1])),
+                                     make_float2(c_all, c_all), make_float2(n.x, n.y));
+              const float2 hi = fma2(make_float2(__uint_as_float(s[4 * q + 2]), __uint_as_float(s[4 * q + 3])),
+                                     make_float2(c_all, c_all), make_float2(n.z, n.w));
+              d[4 * q] = lo.x;
+              d[4 * q + 1] = lo.y;
+              d[4 * q + 2] = hi.x;
+              d[4 * q + 3] = hi.y;
             }
           }
           // The largest, NaN if one is: a cache row with a NaN or an infinity
           // has no finite score.
-          float top = -INFINITY;
+          float top = d[0];
 #pragma unroll
-          for (int c = 0; c < NC; ++c) top = max_nan(top, d[c]);
+          for (int c = 1; c + 1 < NC; c += 2) top = max3_nan(top, d[c], d[c + 1]);
+          top = max_nan(top, d[NC - 1]);
           const bool bad = in && !(fabsf(top) <= 3.4028234e38f);
           float most = top;  // of the rows that see the key
           if (some && !all) {
@@ -1153,18 +1168,20 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
           uint32_t hot = ~0u;
           if (done >= 2) {
             bool big = false;
-            if (some && top > sh.lmin[h]) {
 #pragma unroll
-              for (int q = 0; q < NC / 4; ++q) {
-                const float4 t = lthr4[q];
-                big |= d[4 * q] > t.x || d[4 * q + 1] > t.y || d[4 * q + 2] > t.z || d[4 * q + 3] > t.w;
-              }
+            for (int q = 0; q < NC / 4; ++q) {
+              const float4 t = lthr4[q];
+              big |= (d[4 * q] > t.x) | (d[4 * q + 1] > t.y) | (d[4 * q + 2] > t.z) | (d[4 * q + 3] > t.w);
             }
-            hot = __ballot_sync(0xffffffffu, big);
+            hot = __ballot_sync(0xffffffffu, some && big);
           }
           if (lane == 0) sh.hot[h][quad] = (uint8_t)(((hot & 0xFFFFu) ? 1 : 0) | ((hot >> 16) ? 2 : 0));
 #pragma unroll
-          for (int c = 0; c < NC; ++c) d[c] = ((sees >> c) & 1u) ? ex2(d[c]) : 0.0f;
+          for (int c = 0; c < NC; ++c) d[c] = ex2(d[c]);
+          if (sees != 0xFFFFu)
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              if (!((sees >> c) & 1u)) d[c] = 0.0f;
           uint8_t* prow = sm_p + key * 128;
 #pragma unroll
           for (int q = 0; q < NC / 8; ++q) {
@@ -1241,7 +1258,6 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
             }
             sh.scale[c0 + r] = f;
             sh.lthr[c0 + r] = t;
-            lowest(t);
           }
           ptx::named_sync(bar, 128);
           if (done > 0) {
@@ -1271,7 +1287,11 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
         }
         if (dead) break;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) l[c] += d[c];
+        for (int c = 0; c < NC; c += 2) {
+          const float2 v = add2(make_float2(l[c], l[c + 1]), make_float2(d[c], d[c + 1]));
+          l[c] = v.x;
+          l[c + 1] = v.y;
+        }
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&sh.p_full);
