@@ -37,15 +37,21 @@
 // table, and the loading warps, which fetch Q and the cache rows that are
 // widened to 16 bits, into the 128-byte-swizzled layout.
 //
-// All operands of the products are BF16: E4M3 and E2M1 rows are widened exactly
-// (E2M1 with its scale, E4M3 without: its per-tensor scale goes into the scores
-// and the output).
+// A BF16 cache's rows are copied into shared memory as they are, E2M1 rows are
+// widened to BF16 (exactly, with their scales); both products then have BF16
+// operands.  E4M3 rows are copied as they are too and multiplied as E4M3, which
+// halves their shared memory, so that a block's rows arrive while the one before
+// is in use, and spares widening them (the integer pipe's 64 results a cycle
+// bound a kernel that did).  The other operands are then sums of 8-bit parts:
+// Q two E4M3 parts (4 + 4 significant bits, all of BF16's 8, relative to the
+// row's largest value: a row is scaled by a power of two), P three E5M2 parts
+// (9 bits) down to 2^-26 of the reference and nothing below.
 //
-// P would lose to its rounding as much as the output to its own.  So what is
-// left of a weight after rounding multiplies its row too, as a second 16-bit
-// part, wherever the weight is at least 1/16 of its row's sum so far; below
-// that it is rounded once (by 2^-8 of 1/16 of the sum at most).  An item's first
-// two blocks, whose sums are not known yet, have second parts throughout.
+// P would lose to its rounding as much as the output to its own.  So wherever a
+// weight is at least 1/16 of its row's sum so far, what is left of it after
+// rounding multiplies its row too, as a second BF16 or two more E5M2 parts;
+// below that it is rounded once (by 2^-8 of 1/16 of the sum at most).  An item's
+// first two blocks, whose sums are not known yet, have all parts throughout.
 //
 // Work: with many tiles per SM, whole tiles are dealt out, those with the most
 // keys first.  Else the key blocks of all tiles, in one line, are cut into
@@ -84,8 +90,18 @@ constexpr uint32_t kWdAttn = 64;  // watchdog bit of this kernel
 constexpr int kKeys = 128;           // keys of a block (M of the first product)
 constexpr int kUnit = 16;            // keys of a unit
 constexpr int kUnits = kKeys / kUnit;
-constexpr int kChunkBytes = kKeys * 128;   // 128 keys x 64 columns of 16 bits
-constexpr int kStageBytes = 2 * kChunkBytes;
+constexpr int kChunkBytes = kKeys * 128;   // 128 keys x 128 bytes: 64 columns of 16 bits, 128 of 8
+// A stage holds 128 columns of the block's rows.
+template <int DT>
+struct Form {
+  static constexpr bool F8 = DT == MXQ_CACHE_E4M3;
+  static constexpr int CHUNKS = F8 ? 1 : 2;  // of a stage
+  static constexpr int STAGE = CHUNKS * kChunkBytes;
+  // Parts of a weight, of which the last two are only used where it is large;
+  // log2 of what a weight equal to the reference's is held as, and of the most.
+  static constexpr int PARTS = F8 ? 5 : 2, SURE = F8 ? 3 : 1;
+  static constexpr float SHIFT = F8 ? 10.0f : 0.0f, MOST = F8 ? 15.0f : 40.0f;
+};
 // Thread layout and registers (launch registers x threads is what setmaxnreg
 // deals out again).  Nothing spills: with 227 KB of shared memory in use the
 // L1 cache is too small for local memory.
@@ -97,15 +113,14 @@ struct Roles {
   static constexpr int LOAD0 = SOFT + 4, LOADS = 8;
   static constexpr int THREADS = (LOAD0 + LOADS) * 32;
   static constexpr int REGS = 65536 / THREADS / 8 * 8;
-  static constexpr int REGS_SOFT = NR == 64 ? 88 : 112, REGS_ISSUE = NR == 64 ? 56 : 64,
-                       REGS_LOAD = NR == 64 ? 48 : NR == 32 ? 88 : 128;
+  static constexpr int REGS_SOFT = NR == 64 ? 80 : 112, REGS_ISSUE = NR == 64 ? 40 : 64,
+                       REGS_LOAD = NR == 64 ? 72 : NR == 32 ? 88 : 128;
   static_assert(SOFT * 32 * REGS_SOFT + 128 * REGS_ISSUE + LOADS * 32 * REGS_LOAD <= THREADS * REGS, "register pool");
 };
 constexpr int kLoadThreads = 256;
-constexpr int kMaxStages = 5;
+constexpr int kMaxStages = 8;
 constexpr uint32_t kTmemCols = 512, kTmemS = 256;
 constexpr float kNoKey = 1e30f;      // negm of a row that has seen no key
-constexpr float kSlack = 40.0f;      // log2 of how far a score may pass the reference
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct KernelArgs {
@@ -119,7 +134,10 @@ struct KernelArgs {
 };
 constexpr int kPieceUsed = 1, kPieceEnds = 2;  // flags of a piece
 
-__host__ __device__ constexpr int q_bytes(int NR, int D) { return NR * D * 2; }
+// The query: rows of 16 bits, or two 8-bit parts of each row.
+__host__ __device__ constexpr int q_bytes(int NR, int D, bool f8) {
+  return f8 ? 2 * NR * ((D + 127) / 128 * 128) : NR * D * 2;
+}
 
 // What one work item (a tile, or a piece of its key blocks) covers.
 struct alignas(16) Item {
@@ -137,12 +155,13 @@ constexpr int kSlots = 4;  // blocks whose units are looked up ahead
 
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages], s_full[2], p_full, pv_done, q_full[4], q_empty, drain;
-  uint64_t item_full[kItems], item_empty[kItems], slot_full[kSlots], slot_empty[kSlots];
+  uint64_t item_full[kItems], item_empty[kItems], slot_full[kSlots], slot_empty[kSlots], crow_empty[2];
   uint32_t tmem;
   int abort;
   alignas(16) Item items[kItems];
-  int slots[kSlots][kUnits];  // cache row of each unit's first key, -1: none
+  int slots[kSlots][kUnits];  // cache row of each unit's first key; -1: none, -2: not needed
   alignas(16) float negm[64];
+  float crow[2][64];  // 8-bit forms: what turns a row's products into scores
   float lthr[64];   // log2 of the weight from which the second part counts
   float scale[64];  // the rescale factors of a block; in the epilogue 1 / sum
   uint8_t rowt[64];  // a row's token, counted from the tile's first
@@ -150,18 +169,24 @@ struct Shared {
   float red[4][4][16];
 };
 
-// The weights P are held as two 16-bit parts, hi + lo: for NR <= 32 side by
-// side in one 128-byte row per key, for NR = 64 in two such buffers.
-constexpr int p_bytes(int NR) { return NR == 64 ? 2 * kKeys * 128 : kKeys * 128; }
+// The weights P: part p of a key's NR rows lies p * NR elements into its row of
+// 128 bytes, going on in further buffers of 128 such rows.
+template <int NR, int DT>
+constexpr int kPartBytes = NR * (Form<DT>::F8 ? 1 : 2);
+template <int NR, int DT>
+constexpr int kPBytes = (Form<DT>::PARTS * kPartBytes<NR, DT> + 127) / 128 * kChunkBytes;
 constexpr int kSmemBudget = 232448;
-__host__ __device__ constexpr int smem_fixed(int NR, int D) {
-  return p_bytes(NR) + q_bytes(NR, D) + (int)sizeof(Shared);
+template <int NR, int DT>
+constexpr int smem_fixed(int D) {
+  return kPBytes<NR, DT> + q_bytes(NR, D, Form<DT>::F8) + (int)sizeof(Shared);
 }
-inline int stages_for(int NR, int D) {
-  const int n = (kSmemBudget - smem_fixed(NR, D)) / kStageBytes;
+template <int NR, int DT>
+int stages_for(int D) {
+  const int n = (kSmemBudget - smem_fixed<NR, DT>(D)) / Form<DT>::STAGE;
   return n < kMaxStages ? n : kMaxStages;
 }
-static_assert(smem_fixed(64, 512) + 4 * kStageBytes <= kSmemBudget, "a block of the widest rows fits");
+static_assert(smem_fixed<64, MXQ_CACHE_BF16>(512) + 4 * Form<MXQ_CACHE_BF16>::STAGE <= kSmemBudget, "a block fits");
+static_assert(smem_fixed<64, MXQ_CACHE_E4M3>(512) + 7 * Form<MXQ_CACHE_E4M3>::STAGE <= kSmemBudget, "two blocks, but for a stage");
 
 // A sequence: its first token, new tokens and keys.  Up to 32 at a time, one per lane.
 struct Seq {
@@ -317,18 +342,37 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a_lo, uint32_t a_hi
       "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// The same with 8-bit operands.
+__device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                       uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 a, b;\n"
+      "mov.b64 a, {%1, %2};\nmov.b64 b, {%3, %4};\n"
+      "setp.ne.b32 p, %6, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 // Low and high words of a descriptor with 128-byte swizzle: address and
 // leading offset; stride offset 1024 (eight 128-byte rows).
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
   return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
 }
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (ptx::kSwizzle128B << 29);
+template <bool F8>
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (F8)
+    mma_f8(d, a_lo, kDescHi, b_lo, kDescHi, idesc, accumulate);
+  else
+    mma_f16(d, a_lo, kDescHi, b_lo, kDescHi, idesc, accumulate);
+}
 
-// Instruction descriptor of kind::f16: FP32 accumulation, both operands BF16,
-// M = 128, N, and whether A and B are stored with M / N running fastest.
-__host__ __device__ constexpr uint32_t idesc_bf16(int N, bool a_mn, bool b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) |
-         ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+// Instruction descriptor: FP32 accumulation, operand types (kind::f16: 1 BF16;
+// kind::f8f6f4: 0 E4M3, 1 E5M2), M = 128, N, and whether A and B are stored
+// with M / N running fastest.
+__host__ __device__ constexpr uint32_t idesc(uint32_t a, uint32_t b, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | (a << 7) | (b << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | (8u << 24);
 }
 
 template <int N>
@@ -466,6 +510,15 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ uint32_t pack2_rest(float lo, float hi, uint32_t w) {
   return pack2(lo - bf16_lo(w), hi - bf16_hi(w));
 }
+// Four values -> four E5M2 bytes (round to nearest even, saturating).
+__device__ __forceinline__ uint32_t pack_e5m2(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+// A value cut to the three significant bits that E5M2 holds.
+__device__ __forceinline__ float cut3(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFE00000u); }
 template <int N, int LAUNCH>
 __device__ __forceinline__ void regs_set() {
   if constexpr (N > LAUNCH) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -480,33 +533,6 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uin
 }
 
 // --------------------------------------------------------------- widening
-// 8 E4M3 codes -> 8 BF16 values (exact), without the conversion unit, whose 16
-// results a cycle would bound the kernel: a code's exponent and significand,
-// moved to BF16's places, stand for the value times 2^-120 (subnormals too).
-// NaN codes are the caller's (e4m3_has_nan).
-__device__ __forceinline__ uint4 widen_e4m3(uint32_t a, uint32_t b) {
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t r = __byte_perm(i < 2 ? a : b, 0, (i & 1) ? 0x3424 : 0x1404);  // codes in the high bytes
-    const uint32_t m = ((r >> 4) & 0x07F007F0u) | (r & 0x80008000u);
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(m), "r"(0x7B807B80u));  // 2^120
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
-__device__ __forceinline__ bool e4m3_has_nan(const uint4& v) {
-  const uint32_t k = 0x7F7F7F7Fu, one = 0x01010101u;
-  return ((((v.x & k) + one) | ((v.y & k) + one) | ((v.z & k) + one) | ((v.w & k) + one)) & 0x80808080u) != 0;
-}
-// BF16 NaNs in the places of NaN codes.
-__device__ __forceinline__ uint4 put_nans(uint4 o, uint32_t a, uint32_t b) {
-  uint32_t w[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if ((((i < 4 ? a : b) >> (8 * (i & 3))) & 0x7Fu) == 0x7Fu) w[i >> 1] |= 0x7FFFu << (16 * (i & 1));
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // Table of the eight magnitudes times 2^(sb - 127) as BF16, split into low and
 // high bytes for byte selection: BF16 holds each exactly (infinity past its
 // range, NaN for sb = 255).
@@ -542,75 +568,61 @@ __device__ __forceinline__ uint2 widen_e2m1x4(uint32_t w, const E2m1Table& t) {
   return make_uint2(__byte_perm(lo, hi, 0x5140), __byte_perm(lo, hi, 0x7362));
 }
 
-// Widening of a stage (128 keys x 128 columns) by NT threads: 16-byte pieces
-// of the stored rows, TPR to a row, RPT to a thread.
-template <int DT, int NT>
+// Widening of a stage (128 keys x 128 columns) of E2M1 rows by NT threads:
+// 16-byte pieces of the stored rows (32 codes, one scale), four to a row, RPT to a thread.
+template <int NT>
 struct Widen {
-  static constexpr int TPR = DT == MXQ_CACHE_E4M3 ? 8 : 4;
-  static constexpr int RPT = kKeys * TPR / NT;
+  static constexpr int TPR = 4, RPT = kKeys * TPR / NT;
   static constexpr int KSTEP = NT / TPR;     // key step between a thread's rows
-  static constexpr int COLS = 128 / TPR;     // columns of a piece
   static_assert(KSTEP % 16 == 0 && RPT >= 1, "a thread's rows keep their place in a unit");
   const uint8_t* row[RPT];
   const uint8_t* sf[RPT];
-  uint4 v[RPT];
-  uint32_t sb[RPT];
+  struct Piece {
+    uint4 v[RPT];
+    uint32_t sb[RPT];
+  };
 
   // Rows t / TPR + i * KSTEP of a block whose units lie at su[0..7].
   __device__ __forceinline__ void open(const AttnArgs& a, const int* su, int t) {
     const int key0 = t / TPR, piece = t % TPR;
-    const uint32_t row_bytes = DT == MXQ_CACHE_E4M3 ? (uint32_t)a.D : (uint32_t)a.D / 2;
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const int u = su[(key0 + i * KSTEP) >> 4];
       const int64_t slot = (int64_t)u + (key0 & 15);
       const bool in = u >= 0 && slot < a.num_slots;
-      row[i] = in ? static_cast<const uint8_t*>(a.cache) + slot * row_bytes + piece * 16 : nullptr;
-      if (DT == MXQ_CACHE_E2M1) sf[i] = a.cache_sf + (in ? slot : 0) * (a.D >> 5) + piece;
+      row[i] = in ? static_cast<const uint8_t*>(a.cache) + slot * ((uint32_t)a.D / 2) + piece * 16 : nullptr;
+      sf[i] = a.cache_sf + (in ? slot : 0) * (a.D >> 5) + piece;
     }
   }
   // The pieces (and scale bytes) of stage pr of the block.
-  __device__ __forceinline__ void fetch(int D, int pr, int t) {
-    const bool in = pr * 128 + (t % TPR) * COLS < D;  // an odd last chunk: half a stage
+  __device__ __forceinline__ void fetch(Piece& p, int D, int pr, int t) const {
+    const bool in = pr * 128 + (t % TPR) * 32 < D;  // an odd last chunk: half a stage
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
-      v[i] = make_uint4(0, 0, 0, 0);
-      sb[i] = 0;
+      p.v[i] = make_uint4(0, 0, 0, 0);
+      p.sb[i] = 0;
       if (in && row[i] != nullptr) {
-        v[i] = __ldg(reinterpret_cast<const uint4*>(row[i] + pr * (TPR * 16)));
-        if (DT == MXQ_CACHE_E2M1) sb[i] = __ldg(sf[i] + pr * 4);
+        p.v[i] = __ldg(reinterpret_cast<const uint4*>(row[i] + pr * (TPR * 16)));
+        p.sb[i] = __ldg(sf[i] + pr * 4);
       }
     }
   }
-  __device__ __forceinline__ void store(uint8_t* dst, int t) const {
+  static __device__ __forceinline__ void store(const Piece& p, uint8_t* dst, int t) {
     const int key0 = t / TPR, piece = t % TPR, sw = key0 & 7;
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       uint8_t* d = dst + (key0 + i * KSTEP) * 128;
-      if constexpr (DT == MXQ_CACHE_E4M3) {
-        // The two chunks store their halves in opposite order, so that eight
-        // lanes always cover eight different 16-byte columns.
-        const int ch = piece >> 2, c0 = (piece & 3) * 2;
-        d += ch * kChunkBytes;
-        uint4 x = widen_e4m3(v[i].x, v[i].y), y = widen_e4m3(v[i].z, v[i].w);
-        if (e4m3_has_nan(v[i])) {
-          x = put_nans(x, v[i].x, v[i].y);
-          y = put_nans(y, v[i].z, v[i].w);
-        }
-        *reinterpret_cast<uint4*>(d + (((c0 + ch) ^ sw) << 4)) = ch ? y : x;
-        *reinterpret_cast<uint4*>(d + (((c0 + 1 - ch) ^ sw) << 4)) = ch ? x : y;
-      } else {
-        const E2m1Table tab = e2m1_table(sb[i]);
-        const int ch = piece >> 1, c0 = (piece & 1) * 4;
-        d += ch * kChunkBytes;
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      const E2m1Table tab = e2m1_table(p.sb[i]);
+      const int ch = piece >> 1, col = (piece & 1) * 4;
+      d += ch * kChunkBytes;
+      const uint32_t w[4] = {p.v[i].x, p.v[i].y, p.v[i].z, p.v[i].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // Column e ^ (2 * chunk): the same conflict rule as above.
-          const uint32_t we = ch ? w[e ^ 2] : w[e];
-          const uint2 x = widen_e2m1x4(we, tab), y = widen_e2m1x4(we >> 16, tab);
-          *reinterpret_cast<uint4*>(d + (((c0 + (ch ? e ^ 2 : e)) ^ sw) << 4)) = make_uint4(x.x, x.y, y.x, y.y);
-        }
+      for (int e = 0; e < 4; ++e) {
+        // The second chunk's lanes take their words in another order, so that
+        // eight lanes (two rows) always cover eight different 16-byte columns.
+        const uint32_t we = ch ? w[e ^ 2] : w[e];
+        const uint2 x = widen_e2m1x4(we, tab), y = widen_e2m1x4(we >> 16, tab);
+        *reinterpret_cast<uint4*>(d + (((col + (ch ? e ^ 2 : e)) ^ sw) << 4)) = make_uint4(x.x, x.y, y.x, y.y);
       }
     }
   }
@@ -621,26 +633,31 @@ template <int NR, int DT>
 __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const KernelArgs k) {
   using R = Roles<NR>;
+  using F = Form<DT>;
+  constexpr bool F8 = F::F8;
   constexpr int NC = 16;                     // rows of a softmax group
+  constexpr int kStageBytes = F::STAGE, kPart = kPartBytes<NR, DT>;
   extern __shared__ __align__(1024) uint8_t base[];
   const AttnArgs& a = k.a;
   const int D = a.D, nch = D >> 6, np = (nch + 1) >> 1;
   uint8_t* sm_stage = base;
   uint8_t* sm_p = sm_stage + (size_t)k.stages * kStageBytes;
-  uint8_t* sm_q = sm_p + p_bytes(NR);
-  Shared& sh = *reinterpret_cast<Shared*>(sm_q + q_bytes(NR, D));
+  uint8_t* sm_q = sm_p + kPBytes<NR, DT>;
+  Shared& sh = *reinterpret_cast<Shared*>(sm_q + q_bytes(NR, D, F8));
   volatile int* abort_flag = &sh.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
     sh.abort = 0;
     for (int s = 0; s < k.stages; ++s) {
-      ptx::mbar_init(&sh.full[s], DT == MXQ_CACHE_BF16 ? 1 : R::LOADS);
+      ptx::mbar_init(&sh.full[s], DT == MXQ_CACHE_E2M1 ? R::LOADS : 1);
       ptx::mbar_init(&sh.empty[s], 1);
     }
     ptx::mbar_init(&sh.s_full[0], 1);
     ptx::mbar_init(&sh.s_full[1], 1);
     ptx::mbar_init(&sh.p_full, R::SOFT);
+    ptx::mbar_init(&sh.crow_empty[0], R::SOFT);
+    ptx::mbar_init(&sh.crow_empty[1], R::SOFT);
     ptx::mbar_init(&sh.pv_done, 1);
     for (int s = 0; s < 4; ++s) ptx::mbar_init(&sh.q_full[s], R::LOADS);
     ptx::mbar_init(&sh.q_empty, 1);
@@ -648,11 +665,11 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
     for (int i = 0; i < kItems; ++i) {
       ptx::mbar_init(&sh.item_full[i], 1);
       // Readers: the softmax, loading, issuing and unit warps, and the TMA warp.
-      ptx::mbar_init(&sh.item_empty[i], R::SOFT + R::LOADS + 2 + (DT == MXQ_CACHE_BF16 ? 1 : 0));
+      ptx::mbar_init(&sh.item_empty[i], R::SOFT + R::LOADS + 2 + (DT == MXQ_CACHE_E2M1 ? 0 : 1));
     }
     for (int i = 0; i < kSlots; ++i) {
       ptx::mbar_init(&sh.slot_full[i], 1);
-      ptx::mbar_init(&sh.slot_empty[i], R::SOFT + (DT == MXQ_CACHE_BF16 ? 1 : R::LOADS));
+      ptx::mbar_init(&sh.slot_empty[i], R::SOFT + (DT == MXQ_CACHE_E2M1 ? R::LOADS : 1));
     }
     ptx::fence_barrier_init();
   }
@@ -713,6 +730,10 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
       if (it.blk0 >= it.blk1) continue;
       // Q rows, one per warp and step; rows past the tile's are zeros.
       if (nq > 0 && !(ok = wait_warp(&sh.q_empty, (uint32_t)(nq - 1) & 1u))) break;
+      // The row scales of the item before the last are no longer read.
+      if (F8 && !(ok = wait_warp(&sh.crow_empty[nq & 1], (uint32_t)((nq >> 1) & 1) ^ 1u))) break;
+      const float kvs = DT == MXQ_CACHE_E4M3 ? __ldg(a.kv_scale) : 1.0f;
+#pragma unroll 1
       for (int r0 = lw; r0 < NR; r0 += 2 * R::LOADS) {
         uint4 v[2][2];
 #pragma unroll
@@ -727,11 +748,52 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = r0 + i * R::LOADS;
+          if (r >= NR) break;
+          float f = 1.0f;
+          if constexpr (F8) {
+            // Largest magnitude of the row -> the power of two that brings it
+            // to [2^7, 2^8).  The products with both parts make up the score.
+            uint32_t mx = 0;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t w[4] = {v[i][c].x, v[i][c].y, v[i][c].z, v[i][c].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mx = max(mx, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+            }
+            mx = __reduce_max_sync(0xffffffffu, mx);
+            const int ex = (int)(mx >> 7);
+            const int sft = mx == 0 ? 0 : min(134 - ex, 120);
+            f = __uint_as_float((uint32_t)(127 + sft) << 23);
+            // A row with a NaN or an infinity has no finite score.
+            const float inv = ex == 255 ? NAN : __uint_as_float((uint32_t)(127 - sft) << 23);
+            if (lane == 0) sh.crow[nq & 1][r] = r < it.nrows ? a.sm_scale * kLog2e * kvs * inv : 0.0f;
+          }
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int pc = c * 32 + lane;
-            if (pc < nch * 8 && r < NR)
+            if (pc >= nch * 8) continue;
+            if constexpr (!F8) {
               *reinterpret_cast<uint4*>(sm_q + (pc >> 3) * (NR * 128) + r * 128 + (((pc & 7) ^ (r & 7)) << 4)) = v[i][c];
+            } else {
+              // BF16's 8 significant bits are two parts of E4M3's 4: rounded to
+              // the nearest, and what is left, 16 times as large.
+              float y[8];
+              unpack8(v[i][c], y);
+              uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+              for (int e = 0; e < 8; e += 2) {
+                const float y0 = y[e] * f, y1 = y[e + 1] * f;
+                const uint32_t h = e4m3x2(y0, y1);
+                uint32_t b;
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"((uint16_t)h));
+                const float2 w = __half22float2(*reinterpret_cast<__half2*>(&b));
+                hi[e >> 2] |= h << (16 * ((e >> 1) & 1));
+                lo[e >> 2] |= e4m3x2((y0 - w.x) * 16.0f, (y1 - w.y) * 16.0f) << (16 * ((e >> 1) & 1));
+              }
+              uint8_t* d = sm_q + (pc >> 4) * (2 * NR * 128) + r * 128 + ((((pc >> 1) & 7) ^ (r & 7)) << 4) + (pc & 1) * 8;
+              *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
+              *reinterpret_cast<uint2*>(d + NR * 128) = make_uint2(lo[0], lo[1]);
+            }
           }
         }
       }
@@ -740,36 +802,49 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
       if (lane == 0) ptx::mbar_arrive(&sh.q_full[nq & 3]);
       ++nq;
 
-      if constexpr (DT != MXQ_CACHE_BF16) {
-        // A stage is fetched as soon as the one before it has been stored; its
-        // rows are in L2 by then (the unit warp's prefetch).
-        Widen<DT, kLoadThreads> w;
-        for (int left = it.blk1 - it.blk0; left > 0 && ok; --left, ++nb) {
-          if (!(ok = wait_warp(&sh.slot_full[nb % kSlots], (nb / kSlots) & 1u))) break;
+      if constexpr (DT == MXQ_CACHE_E2M1) {
+        // The next stage is fetched before the current one is stored; its rows
+        // are in L2 by then (the unit warp's prefetch).
+        using W = Widen<kLoadThreads>;
+        W w;
+        typename W::Piece p[2];
+        int left = it.blk1 - it.blk0, pr = 0;
+        auto open = [&]() -> bool {
+          if (!wait_warp(&sh.slot_full[nb % kSlots], (nb / kSlots) & 1u)) return false;
           w.open(a, sh.slots[nb % kSlots], lt);
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&sh.slot_empty[nb % kSlots]);
-          w.fetch(D, 0, lt);
-          for (int pr = 0; pr < np; ++pr) {
-            if (!(ok = wait_warp(&sh.empty[st], stp ^ 1u))) break;
-            w.store(sm_stage + st * kStageBytes, lt);
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&sh.full[st]);
-            if (++st == (uint32_t)k.stages) {
-              st = 0;
-              stp ^= 1u;
-            }
-            if (pr + 1 < np) w.fetch(D, pr + 1, lt);
+          ++nb;
+          return true;
+        };
+        auto step = [&](const W::Piece& now, W::Piece& next) -> bool {
+          if (++pr == np) {
+            pr = 0;
+            if (--left > 0 && !(ok = open())) return false;
           }
+          if (left > 0) w.fetch(next, D, pr, lt);
+          if (!(ok = wait_warp(&sh.empty[st], stp ^ 1u))) return false;
+          W::store(now, sm_stage + st * kStageBytes, lt);
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sh.full[st]);
+          if (++st == (uint32_t)k.stages) {
+            st = 0;
+            stp ^= 1u;
+          }
+          return left > 0;
+        };
+        if (!(ok = open())) break;
+        w.fetch(p[0], D, 0, lt);
+        while (step(p[0], p[1]) && step(p[1], p[0])) {
         }
       }
     }
   } else if (warp == R::TMA) {
     regs_set<R::REGS_ISSUE, R::REGS>();
-    if constexpr (DT == MXQ_CACHE_BF16) {
-      // --------------------------------- BF16 rows: copied as they are by TMA
-      // Lane u < 8 copies unit u of the block, one box of 16 rows x 64 columns
+    if constexpr (DT != MXQ_CACHE_E2M1) {
+      // ------------------------ BF16 and E4M3 rows: copied as they are by TMA
+      // Lane u < 8 copies unit u of the block, one box of 16 rows x 128 bytes
       // per chunk.
       uint32_t st = 0, stp = 0, nb = 0;
       bool ok = true;
@@ -777,20 +852,23 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
       for (uint32_t ni = 0; ok && read_item(ni, it); ++ni) {
         for (int blk = it.blk0; blk < it.blk1 && ok; ++blk) {
           if (!(ok = wait_warp(&sh.slot_full[nb % kSlots], (nb / kSlots) & 1u))) break;
-          const int row = lane < kUnits ? sh.slots[nb % kSlots][lane] : -1;
+          // A unit that is not in the cache is filled with its first rows (nothing
+          // sees them): what lies in the stages depends on the arguments alone.
+          int row = lane < kUnits ? sh.slots[nb % kSlots][lane] : -2;
+          row = row == -1 ? 0 : row;
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&sh.slot_empty[nb % kSlots]);
           ++nb;
           const uint32_t boxes = (uint32_t)__popc(__ballot_sync(0xffffffffu, row >= 0));
           for (int pr = 0; pr < np; ++pr) {
             if (!(ok = wait_warp(&sh.empty[st], stp ^ 1u))) break;
-            const int chunks = min(2, nch - pr * 2);
+            const int chunks = F8 ? 1 : min(2, nch - pr * 2);
             if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.full[st], boxes * (uint32_t)chunks * (kUnit * 128));
             __syncwarp();
             if (row >= 0)
               for (int c = 0; c < chunks; ++c)
                 tma_load_2d(sm_stage + st * kStageBytes + c * kChunkBytes + lane * (kUnit * 128), &tm_kv,
-                            &sh.full[st], (pr * 2 + c) * 64, row);
+                            &sh.full[st], F8 ? pr * 128 : (pr * 2 + c) * 64, row);
             if (++st == (uint32_t)k.stages) {
               st = 0;
               stp ^= 1u;
@@ -813,9 +891,15 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
     // first, because it frees stages.
     const uint32_t dk0 = desc_lo(ptx::smem_u32(sm_stage), 16), dv0 = desc_lo(ptx::smem_u32(sm_stage), kChunkBytes);
     const uint32_t dp0 = desc_lo(ptx::smem_u32(sm_p), kChunkBytes), dq0 = desc_lo(ptx::smem_u32(sm_q), 16);
-    constexpr uint32_t kLoPart = (NR == 64 ? kKeys * 128 : NR * 2) >> 4;  // of P, in 16 bytes
-    constexpr uint32_t idesc_s = idesc_bf16(NR, false, false);
-    constexpr uint32_t idesc_o = idesc_bf16(NR, true, true), idesc_lo = idesc_bf16(NC, true, true);
+    constexpr uint32_t ta = F8 ? 0u : 1u;                    // type of the rows: E4M3 or BF16
+    constexpr int kSteps = F8 ? kUnits / 2 : kUnits;         // second product: 32 or 16 keys at a time
+    constexpr uint32_t kStep = F8 ? 256u : 128u;             // of descriptors: so many rows of 128 bytes
+    constexpr uint32_t idesc_s = idesc(ta, F8 ? 0u : 1u, F8 ? 2 * NR : NR, false, false);
+    constexpr uint32_t idesc_o = idesc(ta, 1u, NR, true, true), idesc_lo = idesc(ta, 1u, NC, true, true);
+    // Where part i of the weights begins, in 16-byte units.
+    auto part_at = [](int i) {
+      return (uint32_t)((i * kPart / 128) * kChunkBytes + (i * kPart) % 128) >> 4;
+    };
     // Items are read without blocking: those that see no key have nothing for
     // this warp, and the others may only move on once it has issued what is ready.
     uint32_t ni = 0;
@@ -857,41 +941,46 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
       }
       if (gp < gq && ready(&sh.p_full, gp & 1u)) {
         ptx::tc_fence_after();
-        const int kk = min(kUnits, punits);  // units in use
+        int kk = min(kUnits, punits);  // units in use; steps
+        if (F8) kk = (kk + 1) >> 1;
         // Read before the products are issued: behind them a load waits for
         // the tensor pipe (measured: 7500 instead of 1700 cycles a block).
-        uint32_t hot = 0;  // bit 8 q + u: group q, unit u
+        uint32_t hot = 0;  // bit 8 q + i: group q, step i
         if (pdone >= 2)
 #pragma unroll
           for (int q = 0; q < R::GROUPS; ++q) {
             // Byte i holds the units 2i and 2i + 1 in its low bits.
             const uint32_t w = *reinterpret_cast<const volatile uint32_t*>(sh.hot[q]);
-            hot |= ((w | (w >> 6) | (w >> 12) | (w >> 18)) & 0xFFu) << (8 * q);
+            if constexpr (F8) {
+              const uint32_t any = w | (w >> 1);
+              hot |= ((any & 1u) | ((any >> 7) & 2u) | ((any >> 14) & 4u) | ((any >> 21) & 8u)) << (8 * q);
+            } else {
+              hot |= ((w | (w >> 6) | (w >> 12) | (w >> 18)) & 0xFFu) << (8 * q);
+            }
           }
         hot &= 0x01010101u * ((1u << kk) - 1u);
         for (int m = 0; m < np; ++m) {
           if (ptx::elect_one()) {
             const uint32_t da = dv0 + ps * (kStageBytes >> 4);
             const uint32_t dd = tmem + m * NR;
+            // The last parts: of all rows in the first two blocks, then 16 rows
+            // at a time where there are any.
+            const int parts = pdone < 2 ? F::PARTS : F::SURE;
 #pragma unroll
-            for (int u = 0; u < kUnits; ++u) {
-              if (u >= kk) break;
-              mma_f16(dd, da + u * 128, kDescHi, dp0 + u * 128, kDescHi, idesc_o, (pdone == 0 && u == 0) ? 0u : 1u);
-            }
-            // The second parts: of all rows in the first two blocks, then 16
-            // rows at a time where there are any.
-            if (pdone < 2) {
+            for (int i = 0; i < F::PARTS; ++i) {
+              if (i >= parts) break;
 #pragma unroll
-              for (int u = 0; u < kUnits; ++u) {
+              for (int u = 0; u < kSteps; ++u) {
                 if (u >= kk) break;
-                mma_f16(dd, da + u * 128, kDescHi, dp0 + kLoPart + u * 128, kDescHi, idesc_o, 1u);
+                mma<F8>(dd, da + u * kStep, dp0 + part_at(i) + u * kStep, idesc_o, (pdone | i | u) ? 1u : 0u);
               }
-            } else {
+            }
 #pragma unroll 1
-              for (uint32_t w = hot; w != 0; w &= w - 1) {
-                const uint32_t bit = (uint32_t)__ffs((int)w) - 1u, q = bit >> 3, u = bit & 7u;
-                mma_f16(dd + q * NC, da + u * 128, kDescHi, dp0 + kLoPart + u * 128 + q * 2, kDescHi, idesc_lo, 1u);
-              }
+            for (uint32_t w = hot; w != 0; w &= w - 1) {
+              const uint32_t bit = (uint32_t)__ffs((int)w) - 1u, q = bit >> 3, u = bit & 7u;
+#pragma unroll
+              for (int i = F::SURE; i < F::PARTS; ++i)
+                mma<F8>(dd + q * NC, da + u * kStep, dp0 + part_at(i) + u * kStep + q * (F8 ? 1 : 2), idesc_lo, 1u);
             }
             ptx::tc_commit(&sh.empty[ps]);
           }
@@ -919,14 +1008,13 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
           ptx::tc_fence_after();
           if (ptx::elect_one()) {
             const uint32_t da = dk0 + qs * (kStageBytes >> 4), db = dq0 + qpair * (NR * 256 >> 4);
-            const uint32_t ds = tmem + kTmemS + (gq & 1u) * 64;
+            const uint32_t ds = tmem + kTmemS + (gq & 1u) * (F8 ? 2 * NR : 64);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              if (qpair * 2 + c >= nch) break;
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                mma_f16(ds, da + c * (kChunkBytes >> 4) + e * 2, kDescHi, db + c * (NR * 128 >> 4) + e * 2, kDescHi,
-                        idesc_s, (qpair | c | e) ? 1u : 0u);
+            for (int e = 0; e < 4 * F::CHUNKS; ++e) {
+              // 32 bytes of columns at a time; a chunk of 64 columns is 4 (2 of 8-bit ones).
+              if (qpair * 2 + (F8 ? e >> 1 : e >> 2) >= nch) break;
+              mma<F8>(ds, da + (e >> 2) * (kChunkBytes >> 4) + (e & 3) * 2, db + (e >> 2) * (NR * 128 >> 4) + (e & 3) * 2,
+                      idesc_s, (qpair | e) ? 1u : 0u);
             }
           }
           __syncwarp();
@@ -995,7 +1083,8 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
     for (uint32_t ni = 0; ok && read_item(ni, it); ++ni) {
       for (int blk = it.blk0; blk < it.blk1; ++blk, ++nb) {
         const int x = blk * kUnits + lane;
-        int slot = -1;
+        // The last 32 keys of an 8-bit form's product may end with a unit that is not there.
+        int slot = x < (F8 ? (it.units + 1) & ~1 : it.units) ? -1 : -2;
         if (lane < kUnits && x < it.units) {
           const int j = unit_key(it, x);
           const int pg = j / a.page_size;
@@ -1027,11 +1116,12 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
     const int c0 = h * NC;
     const uint32_t bar = 1 + h;
     const float vs = DT == MXQ_CACHE_E4M3 ? __ldg(a.kv_scale) : 1.0f;
-    const float c_all = a.sm_scale * kLog2e * vs;
+    const float c_all = a.sm_scale * kLog2e;  // of a 16-bit form's products
     const float4* negm4 = reinterpret_cast<const float4*>(sh.negm + c0);
     const float4* lthr4 = reinterpret_cast<const float4*>(sh.lthr + c0);
     uint32_t g = 0;   // blocks so far
     uint32_t st = 0;  // first stage of the current block
+    int nq = 0;       // items with blocks so far
     // A wait that gives up does not leave the loops by itself: the group's
     // next vote takes all of its threads out together.
     bool ok = true, dead = false;
@@ -1050,12 +1140,19 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
         const int r = c0 + lane;
         sh.rowt[r] = (uint8_t)((held.r0 + r) / a.H - held.r0 / a.H);
         sh.lthr[r] = INFINITY;  // set before the third block
+        if (F8) sh.negm[r] = r < it.nrows ? kNoKey : 0.0f;
       }
       // The key of the first block whose scores are the first reference: the
       // first of those that all rows see, where there is one.
       const int key_ref = a.window > 0 && it.ns == 0 && it.blk0 == 0
                               ? min(max(it.p1 - a.window + 1 - it.u_lo * kUnit, 0), kKeys - 1) : 0;
       ptx::named_sync(bar, 128);
+      if (F8 && has) {
+        // The row scales come with the query.
+        ok = wait(&sh.q_full[nq & 3], (uint32_t)(nq >> 2) & 1u) && ok;
+      }
+      const float4* crow4 = reinterpret_cast<const float4*>(sh.crow[nq & 1] + c0);
+      if (has) ++nq;
       float l[NC];
 #pragma unroll
       for (int c = 0; c < NC; ++c) l[c] = 0.0f;
@@ -1063,6 +1160,8 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
         // Which rows see this thread's key: bit c for the group's row c.
         const int x = blk * kUnits + (key >> 4);
         const bool in = x < it.units;
+        // Keys that the second product reaches (its steps may end with a unit that is not there).
+        const bool live = F8 ? x < ((it.units + 1) & ~1) : in;
         const int j = unit_key(it, in ? x : 0) + (key & 15);
         const int weff = (a.window == 0 || j < a.sinks) ? 0x7fffffff : a.window;
         ok = wait(&sh.slot_full[g % kSlots], (g / kSlots) & 1u) && ok;
@@ -1101,8 +1200,50 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
         ok = wait(&sh.s_full[g & 1u], (g >> 1) & 1u) && ok;
         __syncwarp();
         ptx::tc_fence_after();
-        const uint32_t ts = tq + kTmemS + (g & 1u) * 64 + c0;
-        if (done == 0) {
+        const uint32_t ts = tq + kTmemS + (g & 1u) * (F8 ? 2 * NR : 64) + c0;
+        // The scores of this thread's key, times log2(e), each plus add[c].
+        auto scores = [&](float (&x)[NC], const float4* add) {
+          uint32_t s[NC];
+          if constexpr (F8) {
+            uint32_t lo[NC];
+            tmem_ld<NC>(ts, s);
+            tmem_ld<NC>(ts + NR, lo);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < NC / 4; ++q) {
+              const float4 cr = crow4[q], n = add != nullptr ? add[q] : make_float4(0.f, 0.f, 0.f, 0.f);
+              const float2 ca = make_float2(cr.x, cr.y), cb = make_float2(cr.z, cr.w);
+              const float2 sixteenth = make_float2(0.0625f, 0.0625f), zero = make_float2(0.f, 0.f);
+              const float2 a0 = fma2(make_float2(__uint_as_float(lo[4 * q]), __uint_as_float(lo[4 * q + 1])), sixteenth,
+                                     make_float2(__uint_as_float(s[4 * q]), __uint_as_float(s[4 * q + 1])));
+              const float2 a1 = fma2(make_float2(__uint_as_float(lo[4 * q + 2]), __uint_as_float(lo[4 * q + 3])), sixteenth,
+                                     make_float2(__uint_as_float(s[4 * q + 2]), __uint_as_float(s[4 * q + 3])));
+              const float2 lo2 = fma2(a0, ca, add != nullptr ? make_float2(n.x, n.y) : zero);
+              const float2 hi2 = fma2(a1, cb, add != nullptr ? make_float2(n.z, n.w) : zero);
+              x[4 * q] = lo2.x;
+              x[4 * q + 1] = lo2.y;
+              x[4 * q + 2] = hi2.x;
+              x[4 * q + 3] = hi2.y;
+            }
+          } else {
+            tmem_ld<NC>(ts, s);
+            ptx::tmem_ld_wait();
+            const float2 cc = make_float2(c_all, c_all);
+#pragma unroll
+            for (int q = 0; q < NC / 4; ++q) {
+              const float4 n = add != nullptr ? add[q] : make_float4(0.f, 0.f, 0.f, 0.f);
+              const float2 lo2 = fma2(make_float2(__uint_as_float(s[4 * q]), __uint_as_float(s[4 * q + 1])), cc,
+                                      make_float2(n.x, n.y));
+              const float2 hi2 = fma2(make_float2(__uint_as_float(s[4 * q + 2]), __uint_as_float(s[4 * q + 3])), cc,
+                                      make_float2(n.z, n.w));
+              x[4 * q] = lo2.x;
+              x[4 * q + 1] = lo2.y;
+              x[4 * q + 2] = hi2.x;
+              x[4 * q + 3] = hi2.y;
+            }
+          }
+        };
+        if (!F8 && done == 0) {
           uint32_t s[NC];
           if (quad == key_ref >> 5) {
             tmem_ld<NC>(ts, s);
@@ -1123,39 +1264,29 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
           __syncwarp();
         }
         float d[NC];
-        bool odd = false;  // a second time: some scores are not finite
+        // The 8-bit forms' weights have to stay near the reference, which is the
+        // first block's maximum: there the weights are left for the second time.
+        const bool skip = F8 && done == 0;
 #pragma unroll 1
         for (bool again = false;;) {
+          bool bad, raise = false;
+          if (again || !skip) {
           // ---- exponents d = s + negm, and the weights in their place, written
           // before it is known whether a reference has to move: it hardly ever has.
-          {
-            uint32_t s[NC];
-            tmem_ld<NC>(ts, s);
-            ptx::tmem_ld_wait();
-            if (odd)
-#pragma unroll
-              for (int c = 0; c < NC; ++c)
-                if (!(fabsf(__uint_as_float(s[c])) <= 3.4028234e38f)) sees &= ~(1u << c);
-#pragma unroll
-            for (int q = 0; q < NC / 4; ++q) {
-              const float4 n = negm4[q];
-              const float2 lo = fma2(make_float2(__uint_as_float(s[4 * q]), __uint_as_float(s[4 * q + 1])),
-                                     make_float2(c_all, c_all), make_float2(n.x, n.y));
-              const float2 hi = fma2(make_float2(__uint_as_float(s[4 * q + 2]), __uint_as_float(s[4 * q + 3])),
-                                     make_float2(c_all, c_all), make_float2(n.z, n.w));
-              d[4 * q] = lo.x;
-              d[4 * q + 1] = lo.y;
-              d[4 * q + 2] = hi.x;
-              d[4 * q + 3] = hi.y;
-            }
-          }
+          scores(d, negm4);
           // The largest, NaN if one is: a cache row with a NaN or an infinity
           // has no finite score.
           float top = d[0];
 #pragma unroll
           for (int c = 1; c + 1 < NC; c += 2) top = max3_nan(top, d[c], d[c + 1]);
           top = max_nan(top, d[NC - 1]);
-          const bool bad = in && !(fabsf(top) <= 3.4028234e38f);
+          bad = live && !(fabsf(top) <= 3.4028234e38f);
+          if (again && bad) {
+            // A second time: what is not finite has no weight.
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              if (!(fabsf(d[c]) <= 3.4028234e38f)) d[c] = -INFINITY;
+          }
           float most = top;  // of the rows that see the key
           if (some && !all) {
             most = -INFINITY;
@@ -1163,7 +1294,7 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
             for (int c = 0; c < NC; ++c)
               if ((sees >> c) & 1u) most = fmaxf(most, d[c]);
           }
-          const bool raise = bad || (some && most > kSlack);
+          raise = bad || (some && most > F::MOST);
           // Units in which some weight is large against its row's sum so far.
           uint32_t hot = ~0u;
           if (done >= 2) {
@@ -1183,64 +1314,92 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
             for (int c = 0; c < NC; ++c)
               if (!((sees >> c) & 1u)) d[c] = 0.0f;
           uint8_t* prow = sm_p + key * 128;
+          if constexpr (!F8) {
 #pragma unroll
-          for (int q = 0; q < NC / 8; ++q) {
-            uint32_t hi[4];
+            for (int q = 0; q < NC / 8; ++q) {
+              uint32_t hi[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) hi[e] = pack2(d[8 * q + 2 * e], d[8 * q + 2 * e + 1]);
-            *reinterpret_cast<uint4*>(prow + ((((c0 >> 3) + q) ^ (key & 7)) << 4)) =
-                make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if (hot != 0) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) hi[e] = pack2_rest(d[8 * q + 2 * e], d[8 * q + 2 * e + 1], hi[e]);
-              const int col = (c0 >> 3) + q + (NR == 64 ? 0 : NR / 8);
-              *reinterpret_cast<uint4*>(prow + (NR == 64 ? kKeys * 128 : 0) + ((col ^ (key & 7)) << 4)) =
+              for (int e = 0; e < 4; ++e) hi[e] = pack2(d[8 * q + 2 * e], d[8 * q + 2 * e + 1]);
+              *reinterpret_cast<uint4*>(prow + ((((c0 >> 3) + q) ^ (key & 7)) << 4)) =
                   make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              if (hot != 0) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) hi[e] = pack2_rest(d[8 * q + 2 * e], d[8 * q + 2 * e + 1], hi[e]);
+                const int at = kPart + c0 * 2 + q * 16;
+                *reinterpret_cast<uint4*>(prow + (at / 128) * kChunkBytes + (((at % 128) >> 4 ^ (key & 7)) << 4)) =
+                    make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              }
+            }
+          } else {
+            // Three significant bits at a time; the last part is rounded.
+            float r[NC];
+#pragma unroll
+            for (int c = 0; c < NC; ++c) r[c] = d[c];
+            const int parts = hot != 0 ? F::PARTS : F::SURE;
+#pragma unroll 1
+            for (int i = 0; i < parts; ++i) {
+              uint32_t w[NC / 4];
+#pragma unroll
+              for (int q = 0; q < NC / 4; ++q) {
+                float t[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  t[e] = i + 1 < parts ? cut3(r[4 * q + e]) : r[4 * q + e];
+                  r[4 * q + e] -= t[e];
+                }
+                w[q] = pack_e5m2(t[0], t[1], t[2], t[3]);
+              }
+              const int at = i * kPart + c0;
+              *reinterpret_cast<uint4*>(prow + (at / 128) * kChunkBytes + (((at % 128) >> 4 ^ (key & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
           ptx::fence_proxy_async_smem();
           if (again || !named_any(bar, 128, raise || !ok)) break;
+          }
           again = true;
           // ---- some reference moves, something is not finite, or a wait gave up
           if (named_any(bar, 128, !ok)) {
             dead = true;
             break;
           }
+          // The scores again, and their maxima.
+          scores(d, nullptr);
+          bad = false;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) bad |= !(fabsf(d[c]) <= 3.4028234e38f);
+          bad = bad && live;
           if (bad) {
             // A row that holds a NaN or an infinity must not reach the rows
             // that do not see it through 0 * NaN: it is cleared here, and the
             // rows that see it become NaN through their sums.
             bool rowbad = false;
+            const int words = F8 ? np * 8 : nch * 8;
 #pragma unroll 1
-            for (int e = 0; e < nch * 16; ++e) {  // the row's 16-byte words, twice over
-              const int w8 = e >= nch * 8 ? e - nch * 8 : e, ch = w8 >> 3;
-              const uint32_t sidx = (st + (ch >> 1)) % (uint32_t)k.stages;
-              uint4* wp = reinterpret_cast<uint4*>(sm_stage + sidx * kStageBytes + (ch & 1) * kChunkBytes + key * 128) +
-                          (w8 & 7);
-              if (e >= nch * 8) {
+            for (int e = 0; e < 2 * words; ++e) {  // the row's 16-byte words, twice over
+              const int w8 = e >= words ? e - words : e, ch = w8 >> 3;
+              const uint32_t sidx = (st + ch / F::CHUNKS) % (uint32_t)k.stages;
+              uint4* wp = reinterpret_cast<uint4*>(sm_stage + sidx * kStageBytes + (ch % F::CHUNKS) * kChunkBytes +
+                                                   key * 128) + (w8 & 7);
+              if (e >= words) {
                 if (rowbad) *wp = make_uint4(0, 0, 0, 0);
                 continue;
               }
               const uint4 w = *wp;
-              const uint32_t m = 0x7F807F80u;
-              // Both halves of a word at once: an exponent field of ones.
-              auto full = [&](uint32_t v) { return ((v & 0x7F80u) == 0x7F80u) || ((v & m) >> 16) == 0x7F80u; };
-              rowbad |= full(w.x) || full(w.y) || full(w.z) || full(w.w);
+              const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll 1
+              for (int b = 0; b < 16; b += F8 ? 1 : 2) {
+                // An exponent field of ones (E4M3: the one NaN code).
+                const uint32_t v = ws[b >> 2] >> (8 * (b & 3));
+                rowbad |= F8 ? (v & 0x7Fu) == 0x7Fu : (v & 0x7F80u) == 0x7F80u;
+              }
             }
           }
-          odd = bad;
-          // The scores again, and their maxima.
-          {
-            uint32_t s[NC];
-            tmem_ld<NC>(ts, s);
-            ptx::tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              const float v = __uint_as_float(s[c]);
-              const bool fin = fabsf(v) <= 3.4028234e38f, see = (sees >> c) & 1u;
-              if (bad && !fin && see) l[c] = NAN;
-              d[c] = see && fin ? v * c_all : -INFINITY;
-            }
+          for (int c = 0; c < NC; ++c) {
+            const bool fin = fabsf(d[c]) <= 3.4028234e38f, see = (sees >> c) & 1u;
+            if (bad && !fin && see) l[c] = NAN;
+            d[c] = see && fin ? d[c] : -INFINITY;
           }
           const float m = lanes_reduce<NC, true>(d);
           if (lane < NC) sh.red[h][quad][lane] = m;
@@ -1251,9 +1410,9 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
             const float old = sh.negm[c0 + r];
             float f = 1.0f, t = sh.lthr[c0 + r];
             __syncwarp();
-            if (c0 + r < it.nrows && mb > -INFINITY && (old >= kNoKey || mb > -old)) {
-              if (old < kNoKey) f = ex2(-old - mb);
-              if (lane < NC) sh.negm[c0 + r] = -mb;
+            if (c0 + r < it.nrows && mb > -INFINITY && (old >= kNoKey || F::SHIFT - mb < old)) {
+              if (old < kNoKey) f = ex2(F::SHIFT - mb - old);
+              if (lane < NC) sh.negm[c0 + r] = F::SHIFT - mb;
               if (f != 1.0f) t += __log2f(f);  // stays infinite while it is
             }
             sh.scale[c0 + r] = f;
@@ -1299,6 +1458,10 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
         st = (st + np) % (uint32_t)k.stages;
       }
       if (dead) break;
+      if (F8 && has) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.crow_empty[(nq - 1) & 1]);
+      }
       // ---- row sums over the 128 keys, then the output
       const float sum32 = lanes_reduce<NC, false>(l);
       if (lane < NC) sh.red[h][quad][lane] = sum32;
@@ -1462,7 +1625,7 @@ __global__ void __launch_bounds__(128 * kJoinWays) attn_join_kernel(const Kernel
 
 // ---------------------------------------------------------------- host side
 struct Plan {
-  int NR, grid, stages;
+  int NR, grid;
   bool shares;
   size_t part_bytes, ml_bytes, bytes;
 };
@@ -1475,7 +1638,6 @@ Plan make_plan(const AttnArgs& a) {
   Plan p;
   const int64_t rows = a.T * a.H, per_seq = rows / a.B;
   p.NR = per_seq > 32 ? 64 : per_seq > 16 ? 32 : 16;
-  p.stages = stages_for(p.NR, a.D);
   // Tiles, at most, and key blocks of a tile, at most.
   const int64_t tiles = rows / p.NR + (a.B < rows ? a.B : rows);
   const int64_t cap = (int64_t)a.max_pages * a.page_size;
@@ -1498,24 +1660,25 @@ Plan make_plan(const AttnArgs& a) {
   return p;
 }
 
-// BF16 cache rows as a 2-D map: boxes of 16 rows x 64 columns, 128-byte rows
-// swizzled, zeros past the last row.
-bool encode_rows(CUtensorMap* m, const void* base, uint64_t D, uint64_t rows) {
+// BF16 or E4M3 cache rows as a 2-D map: boxes of 16 rows x 128 bytes, swizzled,
+// zeros outside.
+bool encode_rows(CUtensorMap* m, const void* base, bool f8, uint64_t D, uint64_t rows) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[2] = {D, rows};
-  cuuint64_t strides[1] = {D * 2};
-  cuuint32_t box[2] = {64, kUnit};
+  cuuint64_t strides[1] = {f8 ? D : D * 2};
+  cuuint32_t box[2] = {f8 ? 128u : 64u, kUnit};
   cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return enc(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int NR, int DT>
-cudaError_t launch_one(const KernelArgs& k, int grid, cudaStream_t s, const char** why) {
+cudaError_t launch_one(KernelArgs k, int grid, cudaStream_t s, const char** why) {
+  k.stages = stages_for<NR, DT>(k.a.D);
   auto kern = attn_kernel<NR, DT>;
-  const int smem = smem_fixed(NR, k.a.D) + k.stages * kStageBytes;
+  const int smem = smem_fixed<NR, DT>(k.a.D) + k.stages * Form<DT>::STAGE;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1528,7 +1691,7 @@ cudaError_t launch_one(const KernelArgs& k, int grid, cudaStream_t s, const char
     ready.fetch_or(bit, std::memory_order_acq_rel);
   }
   CUtensorMap tm = {};
-  if (DT == MXQ_CACHE_BF16 && !encode_rows(&tm, k.a.cache, (uint64_t)k.a.D, (uint64_t)k.a.num_slots)) {
+  if (DT != MXQ_CACHE_E2M1 && !encode_rows(&tm, k.a.cache, Form<DT>::F8, (uint64_t)k.a.D, (uint64_t)k.a.num_slots)) {
     *why = "cuTensorMapEncodeTiled failed (driver entry point missing or arguments rejected)";
     return cudaErrorInvalidValue;
   }
@@ -1566,7 +1729,6 @@ cudaError_t launch_attn(const AttnArgs& a, void* ws, cudaStream_t s, const char*
   KernelArgs k = {};
   k.a = a;
   k.shares = p.shares;
-  k.stages = p.stages;
   uint8_t* w = static_cast<uint8_t*>(ws);
   k.part = reinterpret_cast<float*>(w);
   k.part_ml = reinterpret_cast<float2*>(w + p.part_bytes);
