@@ -151,7 +151,7 @@ struct alignas(16) Item {
 };
 static_assert(sizeof(Item) == 64, "four 16-byte words");
 constexpr int kItems = 3;  // items handed out ahead
-constexpr int kSlots = 4;  // blocks whose units are looked up ahead
+constexpr int kSlots = 2;  // blocks whose units are looked up, and fetched into L2, ahead
 
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages], s_full[2], p_full, pv_done, q_full[4], q_empty, drain;
@@ -734,10 +734,10 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
       if (F8 && !(ok = wait_warp(&sh.crow_empty[nq & 1], (uint32_t)((nq >> 1) & 1) ^ 1u))) break;
       const float kvs = DT == MXQ_CACHE_E4M3 ? __ldg(a.kv_scale) : 1.0f;
 #pragma unroll 1
-      for (int r0 = lw; r0 < NR; r0 += 2 * R::LOADS) {
-        uint4 v[2][2];
+      for (int r0 = lw; r0 < NR; r0 += 4 * R::LOADS) {
+        uint4 v[4][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             v[i][c] = make_uint4(0, 0, 0, 0);
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
               v[i][c] = __ldg(reinterpret_cast<const uint4*>(a.q) + (it.qrow + r) * (nch * 8) + pc);
           }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const int r = r0 + i * R::LOADS;
           if (r >= NR) break;
           float f = 1.0f;
@@ -1485,18 +1485,32 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
       }
       ptx::named_sync(bar, 128);
       if (held.piece >= 0) {
-        // Partial sums as they are: a warp stores 32 consecutive columns of a row.
-        float* dst = k.part + ((int64_t)held.piece * NR + c0) * D + key;
+        // Partial sums as they are, 128 columns at a time: through the group's
+        // share of the P buffers (a lane holds a column), then whole rows of
+        // 512 bytes by bulk copies.
+        float* stage = reinterpret_cast<float*>(sm_p + h * (NC * 512));
+        float* dst = k.part + ((int64_t)held.piece * NR + c0) * D;
+#pragma unroll 1
         for (int m = 0; m < np; ++m) {
           uint32_t o[NC];
           tmem_ld<NC>(tq + m * NR + c0, o);
           ptx::tmem_ld_wait();
-          if (m * 128 + key < D) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-              if (c0 + c < it.nrows) dst[(int64_t)c * D + m * 128] = __uint_as_float(o[c]);
+          for (int c = 0; c < NC; ++c) stage[c * 128 + key] = __uint_as_float(o[c]);
+          ptx::fence_proxy_async_smem();
+          ptx::named_sync(bar, 128);
+          if (quad == 0) {
+            if (lane < NC && c0 + lane < it.nrows)
+              ptx::bulk_store(dst + (int64_t)lane * D + m * 128, stage + lane * 128,
+                              (uint32_t)min(128, D - m * 128) * 4);
+            ptx::bulk_commit_group();
+            ptx::bulk_wait_read<0>();
           }
+          ptx::named_sync(bar, 128);
         }
+        if (quad == 0) ptx::bulk_wait_all();
+        // All groups are done with the P buffers.
+        ptx::named_sync(1 + R::GROUPS, R::SOFT * 32);
       } else {
         // The output is turned around in shared memory (the group's half of
         // the P buffers), 256 columns at a time: 16-lane TMEM fragments,
@@ -1550,30 +1564,41 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
   if (warp == R::MMA) ptx::tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the partial sums of the tiles that are cut: CTA (c, y) row y of the one
-// that begins in share c, if any.  Its pieces lie in the slots 2c + 1,
-// 2(c + 1), 2(c + 2), ...; each counts 2^(its reference - the largest).  Thread
-// (u, v) adds up every kJoinWays-th piece of columns 4u..4u+3, in order, and the
-// kJoinWays sums are added in order: the result does not depend on timing.
-constexpr int kJoinWays = 4;
-template <int NR>
-__global__ void __launch_bounds__(128 * kJoinWays) attn_join_kernel(const KernelArgs k) {
-  __shared__ float4 part[kJoinWays][128];
-  __shared__ float sums[kJoinWays];
+// Joins the partial sums of the tiles that are cut: CTA (x, y) row y of the x-th
+// of them, the one that begins in the x-th share c that has such a beginning.
+// Its pieces lie in the slots 2c + 1, 2(c + 1), 2(c + 2), ...; each counts
+// 2^(its reference - the largest).  Thread (u, v) adds up every WAYS-th piece of
+// columns 4u..4u+3, in order, and the WAYS sums are added in order: the result
+// does not depend on timing.
+template <int NR, int WAYS>
+__global__ void __launch_bounds__(128 * WAYS) attn_join_kernel(const KernelArgs k, const int shares) {
+  __shared__ float4 part[WAYS][128];
+  __shared__ float sums[WAYS];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const AttnArgs& a = k.a;
   const int col = (threadIdx.x & 127) * 4, way = threadIdx.x >> 7, lane = threadIdx.x & 31;
   const int r = blockIdx.y;
-  const int first = 2 * blockIdx.x + 1;
+  int c = -1;
+  for (int base = 0, skip = blockIdx.x; base < shares && c < 0; base += 32) {
+    uint32_t m = __ballot_sync(0xffffffffu, base + lane < shares && (k.desc[2 * (base + lane) + 1].w & kPieceUsed));
+    if (skip >= __popc(m)) {
+      skip -= __popc(m);
+      continue;
+    }
+    for (; skip > 0; --skip) m &= m - 1;
+    c = base + __ffs((int)m) - 1;
+  }
+  if (c < 0) return;
+  const int first = 2 * c + 1;
   const int4 d = k.desc[first];
-  if (!(d.w & kPieceUsed) || r >= d.z) return;
+  if (r >= d.z) return;
   // Slot of piece i, and the number of pieces: every CTA has slots, and the
   // last piece of a tile is marked.
-  auto slot = [&](int i) { return i == 0 ? first : 2 * ((int)blockIdx.x + i); };
+  auto slot = [&](int i) { return i == 0 ? first : 2 * (c + i); };
   int used = 1;
-  for (int from = 1; blockIdx.x + from < gridDim.x; from += 32) {
-    const int f = blockIdx.x + from + lane < gridDim.x ? k.desc[slot(from + lane)].w : 0;
+  for (int from = 1; c + from < shares; from += 32) {
+    const int f = c + from + lane < shares ? k.desc[slot(from + lane)].w : 0;
     const uint32_t stop = __ballot_sync(0xffffffffu, !(f & kPieceUsed) || (f & kPieceEnds));
     if (stop != 0) {
       const int l = __ffs((int)stop) - 1;
@@ -1589,7 +1614,7 @@ __global__ void __launch_bounds__(128 * kJoinWays) attn_join_kernel(const Kernel
   float sum = 0.0f;
   if (col < a.D) {
 #pragma unroll 8
-    for (int i = way; i < used; i += kJoinWays) {
+    for (int i = way; i < used; i += WAYS) {
       const int64_t at = (int64_t)slot(i) * NR + r;
       const float2 v = k.part_ml[at];
       const float4 x = *reinterpret_cast<const float4*>(k.part + at * a.D + col);
@@ -1605,9 +1630,10 @@ __global__ void __launch_bounds__(128 * kJoinWays) attn_join_kernel(const Kernel
   if (col == 0) sums[way] = sum;
   __syncthreads();
   if (way != 0 || col >= a.D) return;
-  sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+  sum = sums[0];
 #pragma unroll
-  for (int w = 1; w < kJoinWays; ++w) {
+  for (int w = 1; w < WAYS; ++w) {
+    sum += sums[w];
     const float4 x = part[w][threadIdx.x & 127];
     o.x += x.x;
     o.y += x.y;
@@ -1626,6 +1652,7 @@ __global__ void __launch_bounds__(128 * kJoinWays) attn_join_kernel(const Kernel
 // ---------------------------------------------------------------- host side
 struct Plan {
   int NR, grid;
+  int64_t tiles;  // at most
   bool shares;
   size_t part_bytes, ml_bytes, bytes;
 };
@@ -1638,8 +1665,10 @@ Plan make_plan(const AttnArgs& a) {
   Plan p;
   const int64_t rows = a.T * a.H, per_seq = rows / a.B;
   p.NR = per_seq > 32 ? 64 : per_seq > 16 ? 32 : 16;
-  // Tiles, at most, and key blocks of a tile, at most.
-  const int64_t tiles = rows / p.NR + (a.B < rows ? a.B : rows);
+  // Tiles, and key blocks of a tile, at most.
+  const int64_t tiles = a.q_start == nullptr && a.T == a.B ? a.B * ceil_div(a.H, p.NR)
+                                                           : rows / p.NR + (a.B < rows ? a.B : rows);
+  p.tiles = tiles;
   const int64_t cap = (int64_t)a.max_pages * a.page_size;
   int64_t keys = cap;
   if (a.window > 0) {
@@ -1675,7 +1704,7 @@ bool encode_rows(CUtensorMap* m, const void* base, bool f8, uint64_t D, uint64_t
 }
 
 template <int NR, int DT>
-cudaError_t launch_one(KernelArgs k, int grid, cudaStream_t s, const char** why) {
+cudaError_t launch_one(KernelArgs k, int grid, int64_t tiles, cudaStream_t s, const char** why) {
   k.stages = stages_for<NR, DT>(k.a.D);
   auto kern = attn_kernel<NR, DT>;
   const int smem = smem_fixed<NR, DT>(k.a.D) + k.stages * Form<DT>::STAGE;
@@ -1707,17 +1736,23 @@ cudaError_t launch_one(KernelArgs k, int grid, cudaStream_t s, const char** why)
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, tm, k);
   if (e != cudaSuccess || !k.shares) return e;
-  cfg.gridDim = dim3((unsigned)grid, NR, 1);
-  cfg.blockDim = dim3(128 * kJoinWays, 1, 1);
+  // Fewer tiles than a quarter of the shares are cut into more than four pieces
+  // each, and more threads share a row then.
+  cfg.gridDim = dim3((unsigned)(tiles < grid ? tiles : grid), NR, 1);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<NR>, k);
+  if (tiles * 4 < grid) {
+    cfg.blockDim = dim3(512, 1, 1);
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<NR, 4>, k, grid);
+  }
+  cfg.blockDim = dim3(128, 1, 1);
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel<NR, 1>, k, grid);
 }
 
 template <int NR>
-cudaError_t launch_nr(const KernelArgs& k, int grid, cudaStream_t s, const char** why) {
-  if (k.a.dtype == MXQ_CACHE_BF16) return launch_one<NR, MXQ_CACHE_BF16>(k, grid, s, why);
-  if (k.a.dtype == MXQ_CACHE_E4M3) return launch_one<NR, MXQ_CACHE_E4M3>(k, grid, s, why);
-  return launch_one<NR, MXQ_CACHE_E2M1>(k, grid, s, why);
+cudaError_t launch_nr(const KernelArgs& k, int grid, int64_t tiles, cudaStream_t s, const char** why) {
+  if (k.a.dtype == MXQ_CACHE_BF16) return launch_one<NR, MXQ_CACHE_BF16>(k, grid, tiles, s, why);
+  if (k.a.dtype == MXQ_CACHE_E4M3) return launch_one<NR, MXQ_CACHE_E4M3>(k, grid, tiles, s, why);
+  return launch_one<NR, MXQ_CACHE_E2M1>(k, grid, tiles, s, why);
 }
 
 }  // namespace
@@ -1746,9 +1781,9 @@ cudaError_t launch_attn(const AttnArgs& a, void* ws, cudaStream_t s, const char*
     ready.fetch_or(bit, std::memory_order_acq_rel);
   }
   k.watchdog = wd[dev & 63];
-  if (p.NR == 64) return launch_nr<64>(k, p.grid, s, why);
-  if (p.NR == 32) return launch_nr<32>(k, p.grid, s, why);
-  return launch_nr<16>(k, p.grid, s, why);
+  if (p.NR == 64) return launch_nr<64>(k, p.grid, p.tiles, s, why);
+  if (p.NR == 32) return launch_nr<32>(k, p.grid, p.tiles, s, why);
+  return launch_nr<16>(k, p.grid, p.tiles, s, why);
 }
 
 }  // namespace mxq
