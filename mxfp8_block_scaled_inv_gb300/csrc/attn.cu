@@ -44,12 +44,12 @@
 // is in use, and spares widening them (the integer pipe's 64 results a cycle
 // bound a kernel that did).  The other operands are then sums of 8-bit parts:
 // Q two E4M3 parts (4 + 4 significant bits, all of BF16's 8, relative to the
-// row's largest value: a row is scaled by a power of two), P three E5M2 parts
-// (9 bits) down to 2^-26 of the reference and nothing below.
+// row's largest value: a row is scaled by a power of two), P an E5M2, an E4M3
+// and an E5M2 part (10 bits) down to 2^-26 of the reference and nothing below.
 //
 // P would lose to its rounding as much as the output to its own.  So wherever a
 // weight is at least 1/16 of its row's sum so far, what is left of it after
-// rounding multiplies its row too, as a second BF16 or two more E5M2 parts;
+// rounding multiplies its row too, as a second BF16 or a fourth 8-bit part;
 // below that it is rounded once (by 2^-8 of 1/16 of the sum at most).  An item's
 // first two blocks, whose sums are not known yet, have all parts throughout.
 //
@@ -69,6 +69,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "mxq.h"
 #include "mxq_internal.h"
@@ -97,10 +98,13 @@ struct Form {
   static constexpr bool F8 = DT == MXQ_CACHE_E4M3;
   static constexpr int CHUNKS = F8 ? 1 : 2;  // of a stage
   static constexpr int STAGE = CHUNKS * kChunkBytes;
-  // Parts of a weight, of which the last two are only used where it is large;
-  // log2 of what a weight equal to the reference's is held as, and of the most.
-  static constexpr int PARTS = F8 ? 5 : 2, SURE = F8 ? 3 : 1;
-  static constexpr float SHIFT = F8 ? 10.0f : 0.0f, MOST = F8 ? 15.0f : 40.0f;
+  // Parts of a weight, of which the last is only used where it is large; log2
+  // of what a weight equal to the reference's is held as, and of the most (8
+  // bits: what the first part leaves has to fit E4M3).
+  static constexpr int PARTS = F8 ? 4 : 2, SURE = F8 ? 3 : 1;
+  static constexpr float SHIFT = F8 ? 9.0f : 0.0f, MOST = F8 ? 11.0f : 40.0f;
+  // Type of part i in an instruction descriptor: E5M2, E4M3, E5M2, E4M3, or BF16.
+  static constexpr uint32_t part_type(int i) { return F8 ? (i & 1 ? 0u : 1u) : 1u; }
 };
 // Thread layout and registers (launch registers x threads is what setmaxnreg
 // deals out again).  Nothing spills: with 227 KB of shared memory in use the
@@ -186,7 +190,7 @@ int stages_for(int D) {
   return n < kMaxStages ? n : kMaxStages;
 }
 static_assert(smem_fixed<64, MXQ_CACHE_BF16>(512) + 4 * Form<MXQ_CACHE_BF16>::STAGE <= kSmemBudget, "a block fits");
-static_assert(smem_fixed<64, MXQ_CACHE_E4M3>(512) + 7 * Form<MXQ_CACHE_E4M3>::STAGE <= kSmemBudget, "two blocks, but for a stage");
+static_assert(smem_fixed<64, MXQ_CACHE_E4M3>(512) + 8 * Form<MXQ_CACHE_E4M3>::STAGE <= kSmemBudget, "two blocks fit");
 
 // A sequence: its first token, new tokens and keys.  Up to 32 at a time, one per lane.
 struct Seq {
@@ -517,8 +521,15 @@ __device__ __forceinline__ uint32_t pack_e5m2(float a, float b, float c, float d
   asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
-// A value cut to the three significant bits that E5M2 holds.
-__device__ __forceinline__ float cut3(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFE00000u); }
+// Four values -> four E4M3 bytes.
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
+  return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+}
+// A value cut to the three (E5M2) or four (E4M3) significant bits of a part.
+template <uint32_t TYPE>
+__device__ __forceinline__ float cut_part(float x) {
+  return __uint_as_float(__float_as_uint(x) & (TYPE ? 0xFFE00000u : 0xFFF00000u));
+}
 template <int N, int LAUNCH>
 __device__ __forceinline__ void regs_set() {
   if constexpr (N > LAUNCH) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -895,7 +906,7 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
     constexpr int kSteps = F8 ? kUnits / 2 : kUnits;         // second product: 32 or 16 keys at a time
     constexpr uint32_t kStep = F8 ? 256u : 128u;             // of descriptors: so many rows of 128 bytes
     constexpr uint32_t idesc_s = idesc(ta, F8 ? 0u : 1u, F8 ? 2 * NR : NR, false, false);
-    constexpr uint32_t idesc_o = idesc(ta, 1u, NR, true, true), idesc_lo = idesc(ta, 1u, NC, true, true);
+    constexpr uint32_t idesc_o = idesc(ta, 0u, NR, true, true), idesc_lo = idesc(ta, 0u, NC, true, true);
     // Where part i of the weights begins, in 16-byte units.
     auto part_at = [](int i) {
       return (uint32_t)((i * kPart / 128) * kChunkBytes + (i * kPart) % 128) >> 4;
@@ -972,7 +983,8 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
 #pragma unroll
               for (int u = 0; u < kSteps; ++u) {
                 if (u >= kk) break;
-                mma<F8>(dd, da + u * kStep, dp0 + part_at(i) + u * kStep, idesc_o, (pdone | i | u) ? 1u : 0u);
+                mma<F8>(dd, da + u * kStep, dp0 + part_at(i) + u * kStep, idesc_o | (F::part_type(i) << 10),
+                        (pdone | i | u) ? 1u : 0u);
               }
             }
 #pragma unroll 1
@@ -980,7 +992,8 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
               const uint32_t bit = (uint32_t)__ffs((int)w) - 1u, q = bit >> 3, u = bit & 7u;
 #pragma unroll
               for (int i = F::SURE; i < F::PARTS; ++i)
-                mma<F8>(dd + q * NC, da + u * kStep, dp0 + part_at(i) + u * kStep + q * (F8 ? 1 : 2), idesc_lo, 1u);
+                mma<F8>(dd + q * NC, da + u * kStep, dp0 + part_at(i) + u * kStep + q * (F8 ? 1 : 2),
+                        idesc_lo | (F::part_type(i) << 10), 1u);
             }
             ptx::tc_commit(&sh.empty[ps]);
           }
@@ -1263,7 +1276,7 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
           ok = wait(&sh.pv_done, (g - 1) & 1u) && ok;
           __syncwarp();
         }
-        float d[NC];
+        float d[NC], p[NC];  // 8-bit forms: the weights, while d is split up
         // The 8-bit forms' weights have to stay near the reference, which is the
         // first block's maximum: there the weights are left for the second time.
         const bool skip = F8 && done == 0;
@@ -1331,28 +1344,33 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
               }
             }
           } else {
-            // Three significant bits at a time; the last part is rounded.
-            float r[NC];
-#pragma unroll
-            for (int c = 0; c < NC; ++c) r[c] = d[c];
-            const int parts = hot != 0 ? F::PARTS : F::SURE;
-#pragma unroll 1
-            for (int i = 0; i < parts; ++i) {
+            // 3 + 4 + 3 significant bits and, where some weight is large, 4 more.
+            // All but the last part are cut, not rounded, so that what is left
+            // of the weight is exact and positive.
+            auto part = [&](auto index, bool last) {
+              constexpr int i = decltype(index)::value;
               uint32_t w[NC / 4];
 #pragma unroll
               for (int q = 0; q < NC / 4; ++q) {
                 float t[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  t[e] = i + 1 < parts ? cut3(r[4 * q + e]) : r[4 * q + e];
-                  r[4 * q + e] -= t[e];
+                  t[e] = last ? d[4 * q + e] : cut_part<F::part_type(i)>(d[4 * q + e]);
+                  if (!last) d[4 * q + e] -= t[e];
                 }
-                w[q] = pack_e5m2(t[0], t[1], t[2], t[3]);
+                w[q] = F::part_type(i) ? pack_e5m2(t[0], t[1], t[2], t[3]) : pack_e4m3(t[0], t[1], t[2], t[3]);
               }
-              const int at = i * kPart + c0;
-              *reinterpret_cast<uint4*>(prow + (at / 128) * kChunkBytes + (((at % 128) >> 4 ^ (key & 7)) << 4)) =
+              constexpr int at = i * kPart;
+              const int b = at % 128 + c0;
+              *reinterpret_cast<uint4*>(prow + (at / 128) * kChunkBytes + ((b >> 4 ^ (key & 7)) << 4)) =
                   make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            };
+#pragma unroll
+            for (int c = 0; c < NC; ++c) p[c] = d[c];
+            part(std::integral_constant<int, 0>(), false);
+            part(std::integral_constant<int, 1>(), false);
+            part(std::integral_constant<int, 2>(), hot == 0);
+            if (hot != 0) part(std::integral_constant<int, 3>(), true);
           }
           ptx::fence_proxy_async_smem();
           if (again || !named_any(bar, 128, raise || !ok)) break;
@@ -1447,7 +1465,7 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
         if (dead) break;
 #pragma unroll
         for (int c = 0; c < NC; c += 2) {
-          const float2 v = add2(make_float2(l[c], l[c + 1]), make_float2(d[c], d[c + 1]));
+          const float2 v = add2(make_float2(l[c], l[c + 1]), F8 ? make_float2(p[c], p[c + 1]) : make_float2(d[c], d[c + 1]));
           l[c] = v.x;
           l[c + 1] = v.y;
         }
