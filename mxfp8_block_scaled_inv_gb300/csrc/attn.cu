@@ -544,39 +544,57 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uin
 }
 
 // --------------------------------------------------------------- widening
-// Table of the eight magnitudes times 2^(sb - 127) as BF16, split into low and
-// high bytes for byte selection: BF16 holds each exactly (infinity past its
-// range, NaN for sb = 255).
-struct E2m1Table {
-  uint32_t lo0, lo1, hi0, hi1;
+// A code's sign and its three magnitude bits, moved to BF16's sign and to the
+// lowest two bits of its exponent and the highest of its fraction, are the code's
+// value times 2^-126 (the code without exponent bits a subnormal one); a product
+// with a power of two is then exact wherever the result is in BF16's range.  Two
+// codes are moved by one multiplication: 2^a for the magnitudes and 2^b for the
+// signs, which do not meet.  The codes that share a register are four apart: the
+// stages hold the columns 0..7 in the order 0 4 1 5 2 6 3 7, as does Q, and the
+// output is put back in order (1.1 operations of the half-rate pipe a value; a
+// table by byte selection took 2.1, and the decode step of 32 sequences 193 us).
+struct E2m1Scale {
+  uint32_t m, past;  // 2^(sb - 1), or 2^127 and what is missing to it
 };
-__device__ __forceinline__ E2m1Table e2m1_table(uint32_t sb) {
-  // 2^(sb-127) as BF16; sb = 0 is the subnormal 2^-127.
-  const uint32_t s1 = sb == 255u ? 0x7FFFu : sb == 0u ? 0x0040u : sb << 7;
-  const uint32_t s = s1 | (s1 << 16);
-  uint32_t t01, t23, t45, t67;  // (0, .5), (1, 1.5), (2, 3), (4, 6)
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(t01) : "r"(s), "r"(0x3F000000u));
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(t23) : "r"(s), "r"(0x3FC03F80u));
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(t45) : "r"(s), "r"(0x40404000u));
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(t67) : "r"(s), "r"(0x40C04080u));
-  E2m1Table t;
-  t.lo0 = __byte_perm(t01, t23, 0x6420);
-  t.lo1 = __byte_perm(t45, t67, 0x6420);
-  t.hi0 = __byte_perm(t01, t23, 0x7531);
-  t.hi1 = __byte_perm(t45, t67, 0x7531);
-  return t;
+__device__ __forceinline__ E2m1Scale e2m1_scale(uint32_t sb) {
+  const uint32_t m = sb == 255u ? 0x7FFFu : (min(sb, 128u) + 126u) << 7, past = (max(sb, 128u) - 1u) << 7;
+  return {m | (m << 16), past | (past << 16)};
 }
-// Four codes (the low 16 bits of w) -> four BF16 values.
-__device__ __forceinline__ uint2 widen_e2m1x4(uint32_t w, const E2m1Table& t) {
-  const uint32_t sel = w & 0x7777u;
-  const uint32_t lo = __byte_perm(t.lo0, t.lo1, sel);
-  uint32_t hi = __byte_perm(t.hi0, t.hi1, sel);
-  // The code's sign bit is the selector's replicate-the-top-bit flag: 0x80
-  // becomes 0xFF for a negative code, whose lowest bit is then the sign.
-  uint32_t sg;
-  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(sg) : "r"(0x80808080u), "r"(w));
-  hi |= (sg << 7) & 0x80808080u;
-  return make_uint2(__byte_perm(lo, hi, 0x5140), __byte_perm(lo, hi, 0x7362));
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Eight codes -> eight BF16 values, in the order above.
+__device__ __forceinline__ uint4 widen_e2m1x8(uint32_t w, const E2m1Scale& t, bool any_past) {
+  constexpr uint32_t kKeep = 0x81C081C0u;
+  const uint32_t v = w >> 8;
+  uint32_t r[4] = {((w & 0x000F000Fu) * 0x1040u) & kKeep, ((w & 0x00F000F0u) * 0x104u) & kKeep,
+                   ((v & 0x000F000Fu) * 0x1040u) & kKeep, ((v & 0x00F000F0u) * 0x104u) & kKeep};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) r[e] = mul_bf16x2(r[e], t.m);
+  if (any_past)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = mul_bf16x2(r[e], t.past);
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+// Eight BF16 values (E2M1: from the columns' order to the stages', and back).
+template <int DT>
+__device__ __forceinline__ uint4 to_stage_order(const uint4 v) {
+  if constexpr (DT != MXQ_CACHE_E2M1) return v;
+  return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                    __byte_perm(v.y, v.w, 0x7632));
+}
+template <int DT>
+__device__ __forceinline__ uint4 from_stage_order(const uint4 v) {
+  if constexpr (DT != MXQ_CACHE_E2M1) return v;
+  return make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.x, v.y, 0x7632),
+                    __byte_perm(v.z, v.w, 0x7632));
+}
+// The column that place p of a stage holds.
+template <int DT>
+__device__ __forceinline__ int stage_column(int p) {
+  return DT == MXQ_CACHE_E2M1 ? (p & ~7) | ((p >> 1) & 3) | ((p & 1) << 2) : p;
 }
 
 // Widening of a stage (128 keys x 128 columns) of E2M1 rows by NT threads:
@@ -623,7 +641,8 @@ struct Widen {
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       uint8_t* d = dst + (key0 + i * KSTEP) * 128;
-      const E2m1Table tab = e2m1_table(p.sb[i]);
+      const E2m1Scale scale = e2m1_scale(p.sb[i]);
+      const bool any_past = __any_sync(0xffffffffu, p.sb[i] > 128u);
       const int ch = piece >> 1, col = (piece & 1) * 4;
       d += ch * kChunkBytes;
       const uint32_t w[4] = {p.v[i].x, p.v[i].y, p.v[i].z, p.v[i].w};
@@ -632,8 +651,7 @@ struct Widen {
         // The second chunk's lanes take their words in another order, so that
         // eight lanes (two rows) always cover eight different 16-byte columns.
         const uint32_t we = ch ? w[e ^ 2] : w[e];
-        const uint2 x = widen_e2m1x4(we, tab), y = widen_e2m1x4(we >> 16, tab);
-        *reinterpret_cast<uint4*>(d + (((col + (ch ? e ^ 2 : e)) ^ sw) << 4)) = make_uint4(x.x, x.y, y.x, y.y);
+        *reinterpret_cast<uint4*>(d + (((col + (ch ? e ^ 2 : e)) ^ sw) << 4)) = widen_e2m1x8(we, scale, any_past);
       }
     }
   }
@@ -784,7 +802,8 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
             const int pc = c * 32 + lane;
             if (pc >= nch * 8) continue;
             if constexpr (!F8) {
-              *reinterpret_cast<uint4*>(sm_q + (pc >> 3) * (NR * 128) + r * 128 + (((pc & 7) ^ (r & 7)) << 4)) = v[i][c];
+              *reinterpret_cast<uint4*>(sm_q + (pc >> 3) * (NR * 128) + r * 128 + (((pc & 7) ^ (r & 7)) << 4)) =
+                  to_stage_order<DT>(v[i][c]);
             } else {
               // BF16's 8 significant bits are two parts of E4M3's 4: rounded to
               // the nearest, and what is left, 16 times as large.
@@ -1271,12 +1290,9 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
           }
           ptx::named_sync(bar, 128);
         }
-        // P's buffers are free once the previous block's second product is done.
-        if (done > 0) {
-          ok = wait(&sh.pv_done, (g - 1) & 1u) && ok;
-          __syncwarp();
-        }
-        float d[NC], p[NC];  // 8-bit forms: the weights, while d is split up
+        float d[NC];
+        // Units in which some weight is large against its row's sum so far.
+        uint32_t hot = ~0u;
         // The 8-bit forms' weights have to stay near the reference, which is the
         // first block's maximum: there the weights are left for the second time.
         const bool skip = F8 && done == 0;
@@ -1284,98 +1300,51 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
         for (bool again = false;;) {
           bool bad, raise = false;
           if (again || !skip) {
-          // ---- exponents d = s + negm, and the weights in their place, written
-          // before it is known whether a reference has to move: it hardly ever has.
-          scores(d, negm4);
-          // The largest, NaN if one is: a cache row with a NaN or an infinity
-          // has no finite score.
-          float top = d[0];
+            // ---- exponents d = s + negm, and the weights in their place, before it
+            // is known whether a reference has to move: it hardly ever has.
+            scores(d, negm4);
+            // The largest, NaN if one is: a cache row with a NaN or an infinity
+            // has no finite score.
+            float top = d[0];
 #pragma unroll
-          for (int c = 1; c + 1 < NC; c += 2) top = max3_nan(top, d[c], d[c + 1]);
-          top = max_nan(top, d[NC - 1]);
-          bad = live && !(fabsf(top) <= 3.4028234e38f);
-          if (again && bad) {
-            // A second time: what is not finite has no weight.
+            for (int c = 1; c + 1 < NC; c += 2) top = max3_nan(top, d[c], d[c + 1]);
+            top = max_nan(top, d[NC - 1]);
+            bad = live && !(fabsf(top) <= 3.4028234e38f);
+            if (again && bad) {
+              // A second time: what is not finite has no weight.
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-              if (!(fabsf(d[c]) <= 3.4028234e38f)) d[c] = -INFINITY;
-          }
-          float most = top;  // of the rows that see the key
-          if (some && !all) {
-            most = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-              if ((sees >> c) & 1u) most = fmaxf(most, d[c]);
-          }
-          raise = bad || (some && most > F::MOST);
-          // Units in which some weight is large against its row's sum so far.
-          uint32_t hot = ~0u;
-          if (done >= 2) {
-            bool big = false;
-#pragma unroll
-            for (int q = 0; q < NC / 4; ++q) {
-              const float4 t = lthr4[q];
-              big |= (d[4 * q] > t.x) | (d[4 * q + 1] > t.y) | (d[4 * q + 2] > t.z) | (d[4 * q + 3] > t.w);
+              for (int c = 0; c < NC; ++c)
+                if (!(fabsf(d[c]) <= 3.4028234e38f)) d[c] = -INFINITY;
             }
-            hot = __ballot_sync(0xffffffffu, some && big);
-          }
-          if (lane == 0) sh.hot[h][quad] = (uint8_t)(((hot & 0xFFFFu) ? 1 : 0) | ((hot >> 16) ? 2 : 0));
+            float most = top;  // of the rows that see the key
+            if (some && !all) {
+              most = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < NC; ++c) d[c] = ex2(d[c]);
-          if (sees != 0xFFFFu)
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-              if (!((sees >> c) & 1u)) d[c] = 0.0f;
-          uint8_t* prow = sm_p + key * 128;
-          if constexpr (!F8) {
-#pragma unroll
-            for (int q = 0; q < NC / 8; ++q) {
-              uint32_t hi[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) hi[e] = pack2(d[8 * q + 2 * e], d[8 * q + 2 * e + 1]);
-              *reinterpret_cast<uint4*>(prow + ((((c0 >> 3) + q) ^ (key & 7)) << 4)) =
-                  make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              if (hot != 0) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) hi[e] = pack2_rest(d[8 * q + 2 * e], d[8 * q + 2 * e + 1], hi[e]);
-                const int at = kPart + c0 * 2 + q * 16;
-                *reinterpret_cast<uint4*>(prow + (at / 128) * kChunkBytes + (((at % 128) >> 4 ^ (key & 7)) << 4)) =
-                    make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              }
+              for (int c = 0; c < NC; ++c)
+                if ((sees >> c) & 1u) most = fmaxf(most, d[c]);
             }
-          } else {
-            // 3 + 4 + 3 significant bits and, where some weight is large, 4 more.
-            // All but the last part are cut, not rounded, so that what is left
-            // of the weight is exact and positive.
-            auto part = [&](auto index, bool last) {
-              constexpr int i = decltype(index)::value;
-              uint32_t w[NC / 4];
+            raise = bad || (some && most > F::MOST);
+            if (done >= 2) {
+              bool big = false;
 #pragma unroll
               for (int q = 0; q < NC / 4; ++q) {
-                float t[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  t[e] = last ? d[4 * q + e] : cut_part<F::part_type(i)>(d[4 * q + e]);
-                  if (!last) d[4 * q + e] -= t[e];
-                }
-                w[q] = F::part_type(i) ? pack_e5m2(t[0], t[1], t[2], t[3]) : pack_e4m3(t[0], t[1], t[2], t[3]);
+                const float4 t = lthr4[q];
+                big |= (d[4 * q] > t.x) | (d[4 * q + 1] > t.y) | (d[4 * q + 2] > t.z) | (d[4 * q + 3] > t.w);
               }
-              constexpr int at = i * kPart;
-              const int b = at % 128 + c0;
-              *reinterpret_cast<uint4*>(prow + (at / 128) * kChunkBytes + ((b >> 4 ^ (key & 7)) << 4)) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
-            };
+              hot = __ballot_sync(0xffffffffu, some && big);
+            }
 #pragma unroll
-            for (int c = 0; c < NC; ++c) p[c] = d[c];
-            part(std::integral_constant<int, 0>(), false);
-            part(std::integral_constant<int, 1>(), false);
-            part(std::integral_constant<int, 2>(), hot == 0);
-            if (hot != 0) part(std::integral_constant<int, 3>(), true);
-          }
-          ptx::fence_proxy_async_smem();
-          if (again || !named_any(bar, 128, raise || !ok)) break;
+            for (int c = 0; c < NC; ++c) d[c] = ex2(d[c]);
+            if (sees != 0xFFFFu)
+#pragma unroll
+              for (int c = 0; c < NC; ++c)
+                if (!((sees >> c) & 1u)) d[c] = 0.0f;
+            if (again || !named_any(bar, 128, raise || !ok)) break;
           }
           again = true;
+          // O is at rest once the previous block's second product is done.
+          if (done > 0 && !wait(&sh.pv_done, (g - 1) & 1u)) ok = false;
+          ptx::tc_fence_after();
           // ---- some reference moves, something is not finite, or a wait gave up
           if (named_any(bar, 128, !ok)) {
             dead = true;
@@ -1465,10 +1434,73 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
         if (dead) break;
 #pragma unroll
         for (int c = 0; c < NC; c += 2) {
-          const float2 v = add2(make_float2(l[c], l[c + 1]), F8 ? make_float2(p[c], p[c + 1]) : make_float2(d[c], d[c + 1]));
+          const float2 v = add2(make_float2(l[c], l[c + 1]), make_float2(d[c], d[c + 1]));
           l[c] = v.x;
           l[c + 1] = v.y;
         }
+        // ---- P, held back until the previous block's second product has read it
+        auto free_p = [&]() {
+          if (done > 0) {
+            ok = wait(&sh.pv_done, (g - 1) & 1u) && ok;
+            __syncwarp();
+          }
+          if (lane == 0) sh.hot[h][quad] = (uint8_t)(((hot & 0xFFFFu) ? 1 : 0) | ((hot >> 16) ? 2 : 0));
+        };
+        uint8_t* prow = sm_p + key * 128;
+        // The 16 bytes of part i's row that begin `at` bytes into this group's.
+        auto put = [&](int i, int at, const uint32_t* w) {
+          const int b = i * kPart + c0 * (F8 ? 1 : 2) + at;
+          *reinterpret_cast<uint4*>(prow + (b / 128) * kChunkBytes + (((b % 128) >> 4 ^ (key & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        };
+        if constexpr (!F8) {
+          free_p();
+          uint32_t hi[NC / 2];
+#pragma unroll
+          for (int e = 0; e < NC / 2; ++e) hi[e] = pack2(d[2 * e], d[2 * e + 1]);
+          put(0, 0, hi);
+          put(0, 16, hi + 4);
+          if (hot != 0) {
+#pragma unroll
+            for (int e = 0; e < NC / 2; ++e) hi[e] = pack2_rest(d[2 * e], d[2 * e + 1], hi[e]);
+            put(1, 0, hi);
+            put(1, 16, hi + 4);
+          }
+        } else {
+          // 3 + 4 + 3 significant bits and, where some weight is large, 4 more.
+          // All but the last part are cut, not rounded, so that what is left of
+          // the weight is exact and positive.
+          uint32_t w[3][NC / 4], more[NC / 4];
+          auto split = [&](auto type, bool last, uint32_t* out) {
+            constexpr uint32_t T = decltype(type)::value;
+#pragma unroll
+            for (int q = 0; q < NC / 4; ++q) {
+              float t[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                t[e] = last ? d[4 * q + e] : cut_part<T>(d[4 * q + e]);
+                d[4 * q + e] -= t[e];
+              }
+              out[q] = T ? pack_e5m2(t[0], t[1], t[2], t[3]) : pack_e4m3(t[0], t[1], t[2], t[3]);
+            }
+          };
+          using E5M2 = std::integral_constant<uint32_t, 1>;
+          using E4M3 = std::integral_constant<uint32_t, 0>;
+          split(E5M2(), false, w[0]);
+          split(E4M3(), false, w[1]);
+          if (hot == 0) {
+            split(E5M2(), true, w[2]);
+          } else {
+            split(E5M2(), false, w[2]);
+            split(E4M3(), true, more);
+          }
+          free_p();
+          put(0, 0, w[0]);
+          put(1, 0, w[1]);
+          put(2, 0, w[2]);
+          if (hot != 0) put(3, 0, more);
+        }
+        ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&sh.p_full);
@@ -1514,7 +1546,7 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
           tmem_ld<NC>(tq + m * NR + c0, o);
           ptx::tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < NC; ++c) stage[c * 128 + key] = __uint_as_float(o[c]);
+          for (int c = 0; c < NC; ++c) stage[c * 128 + stage_column<DT>(key)] = __uint_as_float(o[c]);
           ptx::fence_proxy_async_smem();
           ptx::named_sync(bar, 128);
           if (quad == 0) {
@@ -1565,7 +1597,7 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
             const int col = m0 * 128 + lane * 8;
             if (c0 + i < it.nrows && col < D)
               *reinterpret_cast<uint4*>(dst + ((int64_t)i * D + col) * 2) =
-                  *reinterpret_cast<const uint4*>(stage + i * 512 + ((lane ^ (i & 7)) << 4));
+                  from_stage_order<DT>(*reinterpret_cast<const uint4*>(stage + i * 512 + ((lane ^ (i & 7)) << 4)));
           }
           ptx::named_sync(bar, 128);
         }
