@@ -131,12 +131,11 @@ struct KernelArgs {
   AttnArgs a;
   float* part;      // [2 * gridDim][NR][D] partial sums of tiles that are cut
   float2* part_ml;  // [2 * gridDim][NR] (maximum, sum)
-  int4* desc;       // [2 * gridDim]: first row (low, high), rows, flags
+  int4* desc;       // [gridDim]: first row (low, high), rows, pieces of the tile that begins there and is cut
   uint32_t* watchdog;
   int shares;       // 1: blocks in equal shares; 0: whole tiles
   int stages;
 };
-constexpr int kPieceUsed = 1, kPieceEnds = 2;  // flags of a piece
 
 // The query: rows of 16 bits, or two 8-bit parts of each row.
 __host__ __device__ constexpr int q_bytes(int NR, int D, bool f8) {
@@ -241,9 +240,10 @@ __device__ __forceinline__ void walk_items(const KernelArgs& k, Emit emit) {
   const AttnArgs& a = k.a;
   const int lane = threadIdx.x & 31;
   const int grid = (int)gridDim.x, cta = (int)blockIdx.x;
-  if (k.shares && lane < 2) k.desc[2 * cta + lane] = make_int4(0, 0, 0, 0);
+  if (k.shares && lane == 0) k.desc[cta] = make_int4(0, 0, 0, 0);
+  __syncwarp();
   // Pass 0 (shares only) adds up the weights, pass 1 hands out the items.
-  int pos = 0, end = 0;  // this CTA's share of the line of all blocks
+  int share = 0, pos = 0, end = 0;  // this CTA's share of the line of all blocks
 #pragma unroll 1
   for (int pass = k.shares ? 0 : 1; pass < 2; ++pass) {
     int run = 0;  // weight of the tiles so far; whole tiles: their number
@@ -302,8 +302,9 @@ __device__ __forceinline__ void walk_items(const KernelArgs& k, Emit emit) {
             // Slot 2c: the rest of a tile that an earlier CTA began; slot
             // 2c + 1: the beginning of one that the next CTA goes on with.
             it.piece = 2 * cta + (lo == 0 ? 1 : 0);
-            k.desc[it.piece] = make_int4((int)(uint32_t)it.qrow, (int)(it.qrow >> 32), it.nrows,
-                                         kPieceUsed | (hi == w ? kPieceEnds : 0));
+            if (lo == 0)
+              k.desc[cta] = make_int4((int)(uint32_t)it.qrow, (int)(it.qrow >> 32), it.nrows,
+                                      (before + w - 1) / share - cta + 1);
           }
         } else {
           it.blk1 = nb;
@@ -316,7 +317,7 @@ __device__ __forceinline__ void walk_items(const KernelArgs& k, Emit emit) {
     }
     if (pass == 0) {
       // Equal shares; two blocks at least, since a cut costs about one.
-      const int share = max((run + grid - 1) / grid, 2);
+      share = max((run + grid - 1) / grid, 2);
       pos = (int)min((int64_t)share * cta, (int64_t)run);
       end = pos + min(share, run - pos);
       if (pos == end) return;
@@ -500,11 +501,6 @@ __device__ __forceinline__ void stmatrix_x2_trans(uint32_t addr, uint32_t a, uin
                : "memory");
 }
 __device__ __forceinline__ float out_of(bool has, uint32_t v) { return has ? __uint_as_float(v) : 0.0f; }
-__device__ __forceinline__ float warp_max(float x) {
-  float y;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -1614,82 +1610,95 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
   if (warp == R::MMA) ptx::tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the partial sums of the tiles that are cut: CTA (x, y) row y of the x-th
-// of them, the one that begins in the x-th share c that has such a beginning.
-// Its pieces lie in the slots 2c + 1, 2(c + 1), 2(c + 2), ...; each counts
-// 2^(its reference - the largest).  Thread (u, v) adds up every WAYS-th piece of
-// columns 4u..4u+3, in order, and the WAYS sums are added in order: the result
-// does not depend on timing.
+// Joins the partial sums of the tiles that are cut: CTA (x, y) of the x-th of
+// them, the one that begins in the x-th share c that has such a beginning.  Its
+// pieces lie in the slots 2c + 1, 2(c + 1), 2(c + 2), ...; each counts
+// 2^(its reference - the largest).  128 threads, of four columns each, add up
+// every WAYS-th piece of a row, in order and four at a time, so that their loads
+// are under way together; the WAYS sums are added in order too: the result does
+// not depend on timing.
+constexpr int kJoinThreads = 512;
 template <int NR, int WAYS>
-__global__ void __launch_bounds__(128 * WAYS) attn_join_kernel(const KernelArgs k, const int shares) {
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const KernelArgs k, const int shares) {
+  constexpr int ROWS = kJoinThreads / 128 / WAYS;  // of a CTA
+  __shared__ int pieces[kJoinThreads];
+  __shared__ uint32_t begins[kJoinThreads / 32];
   __shared__ float4 part[WAYS][128];
-  __shared__ float sums[WAYS];
+  __shared__ float2 ml[WAYS];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const AttnArgs& a = k.a;
-  const int col = (threadIdx.x & 127) * 4, way = threadIdx.x >> 7, lane = threadIdx.x & 31;
-  const int r = blockIdx.y;
+  const int tid = threadIdx.x, col = (tid & 127) * 4, sub = tid >> 7;
+  const int way = WAYS > 1 ? sub : 0, r = blockIdx.y * ROWS + (WAYS > 1 ? 0 : sub);
+  pieces[tid] = tid < shares ? k.desc[tid].w : 0;
+  const uint32_t b = __ballot_sync(0xffffffffu, pieces[tid] != 0);
+  if ((tid & 31) == 0) begins[tid >> 5] = b;
+  __syncthreads();
   int c = -1;
-  for (int base = 0, skip = blockIdx.x; base < shares && c < 0; base += 32) {
-    uint32_t m = __ballot_sync(0xffffffffu, base + lane < shares && (k.desc[2 * (base + lane) + 1].w & kPieceUsed));
-    if (skip >= __popc(m)) {
-      skip -= __popc(m);
-      continue;
-    }
-    for (; skip > 0; --skip) m &= m - 1;
-    c = base + __ffs((int)m) - 1;
-  }
-  if (c < 0) return;
-  const int first = 2 * c + 1;
-  const int4 d = k.desc[first];
-  if (r >= d.z) return;
-  // Slot of piece i, and the number of pieces: every CTA has slots, and the
-  // last piece of a tile is marked.
-  auto slot = [&](int i) { return i == 0 ? first : 2 * (c + i); };
-  int used = 1;
-  for (int from = 1; c + from < shares; from += 32) {
-    const int f = c + from + lane < shares ? k.desc[slot(from + lane)].w : 0;
-    const uint32_t stop = __ballot_sync(0xffffffffu, !(f & kPieceUsed) || (f & kPieceEnds));
-    if (stop != 0) {
-      const int l = __ffs((int)stop) - 1;
-      used = from + l + ((__shfl_sync(0xffffffffu, f, l) & kPieceUsed) ? 1 : 0);
+  for (int w = 0, skip = blockIdx.x; w * 32 < shares; ++w) {
+    uint32_t m = begins[w];
+    if (skip < __popc(m)) {
+      for (; skip > 0; --skip) m &= m - 1;
+      c = w * 32 + __ffs((int)m) - 1;
       break;
     }
-    used = from + 32;
+    skip -= __popc(m);
   }
-  float mx = -INFINITY;
-  for (int i = lane; i < used; i += 32) mx = fmaxf(mx, k.part_ml[(int64_t)slot(i) * NR + r].x);
-  mx = warp_max(mx);
+  if (c < 0) return;
+  const int4 d = k.desc[c];
+  if (ROWS == 1 && r >= d.z) return;
+  const int used = pieces[c];
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.0f;
-  if (col < a.D) {
-#pragma unroll 8
-    for (int i = way; i < used; i += WAYS) {
-      const int64_t at = (int64_t)slot(i) * NR + r;
-      const float2 v = k.part_ml[at];
-      const float4 x = *reinterpret_cast<const float4*>(k.part + at * a.D + col);
-      const float f = ex2(v.x - mx);
-      sum += f * v.y;
+  float mx = -INFINITY, sum = 0.0f;
+  if (col < a.D && r < d.z) {
+#pragma unroll 1
+    for (int i0 = way; i0 < used; i0 += 4 * WAYS) {
+      float2 v[4];
+      float4 x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = i0 + e * WAYS;
+        const int64_t at = (int64_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * NR + r;
+        v[e] = i < used ? k.part_ml[at] : make_float2(-INFINITY, 0.f);
+        x[e] = i < used ? *reinterpret_cast<const float4*>(k.part + at * a.D + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      const float top = fmaxf(fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x)), mx);
+      const float old = ex2(mx - top);
+      mx = top;
+      sum *= old;
+      o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float f = ex2(v[e].x - mx);
+        sum += f * v[e].y;
+        o.x += f * x[e].x;
+        o.y += f * x[e].y;
+        o.z += f * x[e].z;
+        o.w += f * x[e].w;
+      }
+    }
+  }
+  if constexpr (WAYS > 1) {
+    part[way][tid & 127] = o;
+    if (col == 0) ml[way] = make_float2(mx, sum);
+    __syncthreads();
+    if (way != 0) return;
+#pragma unroll
+    for (int w = 1; w < WAYS; ++w) mx = fmaxf(mx, ml[w].x);
+    sum = 0.0f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < WAYS; ++w) {
+      const float f = ex2(ml[w].x - mx);
+      const float4 x = part[w][tid & 127];
+      sum += f * ml[w].y;
       o.x += f * x.x;
       o.y += f * x.y;
       o.z += f * x.z;
       o.w += f * x.w;
     }
   }
-  part[way][threadIdx.x & 127] = o;
-  if (col == 0) sums[way] = sum;
-  __syncthreads();
-  if (way != 0 || col >= a.D) return;
-  sum = sums[0];
-#pragma unroll
-  for (int w = 1; w < WAYS; ++w) {
-    sum += sums[w];
-    const float4 x = part[w][threadIdx.x & 127];
-    o.x += x.x;
-    o.y += x.y;
-    o.z += x.z;
-    o.w += x.w;
-  }
+  if (col >= a.D || r >= d.z) return;
   const float vs = a.dtype == MXQ_CACHE_E4M3 ? __ldg(a.kv_scale) : 1.0f;
   const float inv = sum == 0.0f ? 0.0f : vs / sum;
   const int64_t row = (int64_t)(((uint64_t)(uint32_t)d.y << 32) | (uint32_t)d.x) + r;
@@ -1710,6 +1719,7 @@ struct Plan {
 // CTAs of the share form.  Workspace sizes come from the plan, which must not
 // depend on the device; a device with fewer SMs runs them in turns.
 constexpr int kShares = 152;
+static_assert(kShares <= kJoinThreads, "a thread of the join looks at one share");
 
 Plan make_plan(const AttnArgs& a) {
   Plan p;
@@ -1735,7 +1745,7 @@ Plan make_plan(const AttnArgs& a) {
   const size_t pieces = 2 * (size_t)p.grid;
   p.part_bytes = p.shares ? round_up_256(pieces * p.NR * a.D * 4) : 0;
   p.ml_bytes = p.shares ? round_up_256(pieces * p.NR * 8) : 0;
-  p.bytes = p.shares ? p.part_bytes + p.ml_bytes + round_up_256(pieces * 16) : 0;
+  p.bytes = p.shares ? p.part_bytes + p.ml_bytes + round_up_256((size_t)p.grid * 16) : 0;
   return p;
 }
 
@@ -1789,12 +1799,10 @@ cudaError_t launch_one(KernelArgs k, int grid, int64_t tiles, cudaStream_t s, co
   // Fewer tiles than a quarter of the shares are cut into more than four pieces
   // each, and more threads share a row then.
   cfg.gridDim = dim3((unsigned)(tiles < grid ? tiles : grid), NR, 1);
+  cfg.blockDim = dim3(kJoinThreads, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  if (tiles * 4 < grid) {
-    cfg.blockDim = dim3(512, 1, 1);
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<NR, 4>, k, grid);
-  }
-  cfg.blockDim = dim3(128, 1, 1);
+  if (tiles * 4 < grid) return cudaLaunchKernelEx(&cfg, attn_join_kernel<NR, 4>, k, grid);
+  cfg.gridDim.y = NR / (kJoinThreads / 128);
   return cudaLaunchKernelEx(&cfg, attn_join_kernel<NR, 1>, k, grid);
 }
 
