@@ -1531,32 +1531,21 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
       }
       ptx::named_sync(bar, 128);
       if (held.piece >= 0) {
-        // Partial sums as they are, 128 columns at a time: through the group's
-        // share of the P buffers (a lane holds a column), then whole rows of
-        // 512 bytes by bulk copies.
-        float* stage = reinterpret_cast<float*>(sm_p + h * (NC * 512));
-        float* dst = k.part + ((int64_t)held.piece * NR + c0) * D;
+        // Partial sums as they are: a lane holds a column, a warp stores 128
+        // bytes of a row at a time.
+        float* dst = k.part + ((int64_t)held.piece * NR + c0) * D + stage_column<DT>(key);
 #pragma unroll 1
-        for (int m = 0; m < np; ++m) {
+        for (int m = 0; m < np; ++m, dst += 128) {
           uint32_t o[NC];
           tmem_ld<NC>(tq + m * NR + c0, o);
           ptx::tmem_ld_wait();
+          if (m * 128 + key < D) {
 #pragma unroll
-          for (int c = 0; c < NC; ++c) stage[c * 128 + stage_column<DT>(key)] = __uint_as_float(o[c]);
-          ptx::fence_proxy_async_smem();
-          ptx::named_sync(bar, 128);
-          if (quad == 0) {
-            if (lane < NC && c0 + lane < it.nrows)
-              ptx::bulk_store(dst + (int64_t)lane * D + m * 128, stage + lane * 128,
-                              (uint32_t)min(128, D - m * 128) * 4);
-            ptx::bulk_commit_group();
-            ptx::bulk_wait_read<0>();
+            for (int c = 0; c < NC; ++c)
+              if (c0 + c < held.nrows) dst[(int64_t)c * D] = __uint_as_float(o[c]);
           }
-          ptx::named_sync(bar, 128);
+          __syncwarp();
         }
-        if (quad == 0) ptx::bulk_wait_all();
-        // All groups are done with the P buffers.
-        ptx::named_sync(1 + R::GROUPS, R::SOFT * 32);
       } else {
         // The output is turned around in shared memory (the group's half of
         // the P buffers), 256 columns at a time: 16-lane TMEM fragments,
