@@ -474,32 +474,6 @@ __device__ __forceinline__ float lanes_reduce(float (&v)[N]) {
   }
   return v[0];
 }
-// 16 lanes x N columns of TMEM: per 8 columns, registers 0-1 hold lane t / 4,
-// columns 2 (t % 4) and + 1; registers 2-3 the same of lane t / 4 + 8.
-template <int N>
-__device__ __forceinline__ void tmem_ld_16x256b(uint32_t addr, uint32_t (&r)[N / 2]) {
-  static_assert(N == 8 || N == 16 || N == 32, "");
-  if constexpr (N == 8)
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-  if constexpr (N == 16)
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(addr));
-  if constexpr (N == 32)
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-        "%14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(addr));
-}
-// Two 8 x 8 matrices of 16-bit values, transposed on the way to shared memory.
-__device__ __forceinline__ void stmatrix_x2_trans(uint32_t addr, uint32_t a, uint32_t b) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b)
-               : "memory");
-}
 __device__ __forceinline__ float out_of(bool has, uint32_t v) { return has ? __uint_as_float(v) : 0.0f; }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
@@ -574,18 +548,12 @@ __device__ __forceinline__ uint4 widen_e2m1x8(uint32_t w, const E2m1Scale& t, bo
     for (int e = 0; e < 4; ++e) r[e] = mul_bf16x2(r[e], t.past);
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
-// Eight BF16 values (E2M1: from the columns' order to the stages', and back).
+// Eight BF16 values, from the columns' order to the stages'.
 template <int DT>
 __device__ __forceinline__ uint4 to_stage_order(const uint4 v) {
   if constexpr (DT != MXQ_CACHE_E2M1) return v;
   return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
                     __byte_perm(v.y, v.w, 0x7632));
-}
-template <int DT>
-__device__ __forceinline__ uint4 from_stage_order(const uint4 v) {
-  if constexpr (DT != MXQ_CACHE_E2M1) return v;
-  return make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.x, v.y, 0x7632),
-                    __byte_perm(v.z, v.w, 0x7632));
 }
 // The column that place p of a stage holds.
 template <int DT>
@@ -1547,47 +1515,37 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
           __syncwarp();
         }
       } else {
-        // The output is turned around in shared memory (the group's half of
-        // the P buffers), 256 columns at a time: 16-lane TMEM fragments,
-        // rounded to BF16 pairs of rows, stored as transposed 8 x 8 matrices
-        // into rows of 512 bytes whose 16-byte words are swizzled by row; then
-        // whole rows go out with 16-byte stores.
-        uint8_t* stage = sm_p + h * (NC * 512);
-        const uint32_t stage_a = ptx::smem_u32(stage);
-        float2 sc[NC / 8];
-#pragma unroll
-        for (int q = 0; q < NC / 8; ++q)
-          sc[q] = *reinterpret_cast<const float2*>(&sh.scale[c0 + q * 8 + (lane & 3) * 2]);
-        uint8_t* dst = static_cast<uint8_t*>(a.out) + (held.qrow + c0) * D * 2;
+        // The output: a lane holds a column, and the lanes of two neighbouring
+        // columns swap halves of their rows, so that each stores pairs of columns
+        // of eight rows.
+        constexpr int kNext = DT == MXQ_CACHE_E2M1 ? 2 : 1;  // lane bit that is the column's lowest
+        const bool odd = lane & kNext;
+        const uint32_t pick = odd ? 0x3276u : 0x5410u;
+        const int col = stage_column<DT>(key) & ~1, row = odd ? NC / 2 : 0;
+        uint8_t* dst = static_cast<uint8_t*>(a.out) + ((held.qrow + c0 + row) * D + col) * 2;
+        const int left = held.nrows - c0 - row;
+        const float4* sc4 = reinterpret_cast<const float4*>(sh.scale + c0);
 #pragma unroll 1
-        for (int m0 = 0; m0 < np; m0 += 2) {
-          uint32_t o[4][NC / 2];
-#pragma unroll
-          for (int f = 0; f < 4; ++f)  // m0 + f / 2, lanes 16 * (f % 2) on
-            tmem_ld_16x256b<NC>(tq + ((uint32_t)((f & 1) * 16) << 16) + min(m0 + (f >> 1), np - 1) * NR + c0, o[f]);
+        for (int m = 0; m * 128 + col < D; ++m, dst += 256) {
+          uint32_t o[NC];
+          tmem_ld<NC>(tq + m * NR + c0, o);
           ptx::tmem_ld_wait();
+          float v[NC];
 #pragma unroll
-          for (int f = 0; f < 4; ++f)
-#pragma unroll
-            for (int q = 0; q < NC / 8; ++q) {
-              const uint32_t w0 = pack2(out_of(has, o[f][4 * q]) * sc[q].x, out_of(has, o[f][4 * q + 1]) * sc[q].y);
-              const uint32_t w1 = pack2(out_of(has, o[f][4 * q + 2]) * sc[q].x, out_of(has, o[f][4 * q + 3]) * sc[q].y);
-              // Lanes 0-7 name the rows of the first matrix, 8-15 of the second.
-              const int row = q * 8 + (lane & 7);
-              const int word = (f >> 1) * 16 + quad * 4 + (f & 1) * 2 + ((lane >> 3) & 1);
-              stmatrix_x2_trans(stage_a + row * 512 + ((word ^ (row & 7)) << 4), w0, w1);
-            }
-          ptx::named_sync(bar, 128);
-          for (int i = quad; i < NC; i += 4) {
-            const int col = m0 * 128 + lane * 8;
-            if (c0 + i < it.nrows && col < D)
-              *reinterpret_cast<uint4*>(dst + ((int64_t)i * D + col) * 2) =
-                  from_stage_order<DT>(*reinterpret_cast<const uint4*>(stage + i * 512 + ((lane ^ (i & 7)) << 4)));
+          for (int q = 0; q < NC / 4; ++q) {
+            const float4 sc = sc4[q];
+            v[4 * q] = out_of(has, o[4 * q]) * sc.x;
+            v[4 * q + 1] = out_of(has, o[4 * q + 1]) * sc.y;
+            v[4 * q + 2] = out_of(has, o[4 * q + 2]) * sc.z;
+            v[4 * q + 3] = out_of(has, o[4 * q + 3]) * sc.w;
           }
-          ptx::named_sync(bar, 128);
+#pragma unroll
+          for (int c = 0; c < NC / 2; ++c) {
+            const uint32_t mine = pack2(v[c], v[c + NC / 2]);
+            const uint32_t next = __shfl_xor_sync(0xffffffffu, mine, kNext);
+            if (c < left) *reinterpret_cast<uint32_t*>(dst + (int64_t)c * D * 2) = __byte_perm(mine, next, pick);
+          }
         }
-        // All groups are done with the P buffers.
-        ptx::named_sync(1 + R::GROUPS, R::SOFT * 32);
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sh.item_empty[ni % kItems]);
