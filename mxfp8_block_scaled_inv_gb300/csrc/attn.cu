@@ -1682,12 +1682,17 @@ Plan make_plan(const AttnArgs& a) {
     const int64_t w = (int64_t)a.window + a.sinks + 2 * kUnit + (p.NR + a.H - 1) / a.H;
     keys = keys < w ? keys : w;
   }
-  // Whole tiles when each CTA gets at least eight (what the last ones leave
-  // idle is then an eighth of a tile's time) or when no tile has more than two
-  // blocks (a cut costs about one).
+  // Shares are even, but a cut costs about a block, and the pieces' sums and
+  // their join about 16 stages (128 keys x 128 columns) of every CTA.  So whole
+  // tiles where none has more than two blocks; where they leave fewer stages idle
+  // in the last round of a few (301 tokens of each of 7 sequences, 12 heads of 192
+  // columns, window 777: 53 us whole, 60 in shares; 500 of each of 2, 32 heads of
+  // 256 columns over 4001 keys: 237 and 222); and from eight tiles a CTA, since
+  // each CTA walks the line of all tiles before it begins its share.
   // (Weights are 32-bit numbers on the device.)
-  const int64_t nb = ceil_div(keys, kKeys) + 1;
-  p.shares = rows / p.NR < 8 * kShares && nb > 3 && tiles * nb < (int64_t)1 << 31;
+  const int64_t nb = ceil_div(keys, kKeys) + 1, idle = ceil_div(tiles, kShares) * kShares - tiles;
+  p.shares = rows / p.NR < 8 * kShares && nb > 3 && tiles * nb < (int64_t)1 << 31 &&
+             (tiles <= kShares || idle * nb * ceil_div(a.D, 128) > 16 * kShares);
   p.grid = p.shares || tiles > kShares ? kShares : (int)tiles;
   const size_t pieces = 2 * (size_t)p.grid;
   p.part_bytes = p.shares ? round_up_256(pieces * p.NR * a.D * 4) : 0;
