@@ -357,8 +357,13 @@ size_t mxq_attn_workspace_bytes(int64_t T, int32_t B, int32_t H, int32_t D, int3
  *              j > p - window or j < sinks).
  *  out_bf16    [T, H, D]: sum_j exp(s_j - lse) * k_j over the visible keys,
  *              s_j = sm_scale * (q . k_j); rounded once to BF16.  The two
- *              products run on the tensor cores with FP32 accumulation; the
- *              exponentials are rounded to 16 bits before the second one.
+ *              products run on the tensor cores with FP32 accumulation.
+ *              Before the second one the exponentials are rounded to BF16,
+ *              or (MXQ_CACHE_E4M3) to 10 significant bits, those below 2^-26
+ *              of a reference near the largest to zero; where one is 1/16 of
+ *              its row's sum or more, what the rounding left is added too.
+ *              The scores' query is exact in BF16's 8 bits (MXQ_CACHE_E4M3:
+ *              relative to its row's largest value).
  *  lse         optional [T, H] FP32: log(sum_j exp(s_j)).
  *  err_flag    optional int32 device word: MXQ_DEVERR_SLOT when a block-table
  *              entry that is read lies outside the cache (its keys are
@@ -449,8 +454,8 @@ int mxq_debug_set_lazy_pairs(int from);
 int mxq_debug_takeovers(uint32_t* host_value, int clear);
 
 /*
- * Watchdog word of the GEMM kernels and of the streamed query copy of
- * mxq_rope_kv_insert on the current device (host call, synchronous).  Every
+ * Watchdog word of the GEMM kernels, of the streamed query copy of the
+ * insertions and of mxq_attn on the current device (host call, synchronous).  Every
  * wait inside those kernels is bounded; a wait that runs out sets a bit here
  * and the kernel returns early instead of hanging.  0 means no wait ever ran
  * out.  With clear != 0 the word is reset after reading.

@@ -25,15 +25,15 @@
 // values they stand for.)  Row sums are kept per thread (one key each) in FP32
 // and joined at the end.
 //
-// The kernel is built for a small instruction footprint (about 40 KB; at 140
-// KB every role missed the instruction cache on every block, which made all of
-// them two to three times slower): one copy of each piece of work, loops over
-// unrolling wherever latency does not matter.
+// The kernel is built for a small instruction footprint (70 to 90 KB; at 140 KB
+// the roles missed the instruction cache on every block, and 8192 queries with a
+// window of 128 took 681 us where half the code took 600): one copy of each
+// piece of work, loops over unrolling wherever latency does not matter.
 //
 // Warps: NR / 4 for the softmax and the epilogue (a lane is a key, then a
 // column; each group of four owns 16 of the tile's rows and never waits for
 // another), one that issues the matrix instructions, one for the TMA copies of
-// BF16 rows, one that hands out the work items, one that looks up the block
+// BF16 and E4M3 rows, one that hands out the work items, one that looks up the block
 // table, and the loading warps, which fetch Q and the cache rows that are
 // widened to 16 bits, into the 128-byte-swizzled layout.
 //
@@ -42,22 +42,43 @@
 // operands.  E4M3 rows are copied as they are too and multiplied as E4M3, which
 // halves their shared memory, so that a block's rows arrive while the one before
 // is in use, and spares widening them (the integer pipe's 64 results a cycle
-// bound a kernel that did).  The other operands are then sums of 8-bit parts:
-// Q two E4M3 parts (4 + 4 significant bits, all of BF16's 8, relative to the
-// row's largest value: a row is scaled by a power of two), P an E5M2, an E4M3
-// and an E5M2 part (10 bits) down to 2^-26 of the reference and nothing below.
+// bound a kernel that did: 2048 queries with a window of 4096 took 2350 us).  The
+// other operands are then sums of 8-bit parts: Q two E4M3 parts (4 + 4 significant
+// bits, all of BF16's 8, relative to the row's largest value: a row is scaled by a
+// power of two), P an E5M2, an E4M3 and an E5M2 part (10 bits) down to 2^-26 of
+// the reference and nothing below.
 //
 // P would lose to its rounding as much as the output to its own.  So wherever a
 // weight is at least 1/16 of its row's sum so far, what is left of it after
 // rounding multiplies its row too, as a second BF16 or a fourth 8-bit part;
-// below that it is rounded once (by 2^-8 of 1/16 of the sum at most).  An item's
-// first two blocks, whose sums are not known yet, have all parts throughout.
+// below that it is rounded once (BF16: by half an ulp, 2^-8 of itself at most,
+// to either side).  An item's first two blocks, whose sums are not known yet,
+// have all parts throughout.
 //
 // Work: with many tiles per SM, whole tiles are dealt out, those with the most
 // keys first.  Else the key blocks of all tiles, in one line, are cut into
 // equal shares, one per CTA; a tile that is cut leaves FP32 partial sums, which
 // a second kernel joins in the order of the keys.  Both follow from the
 // lengths on the device, so ragged batches stay balanced.
+//
+// What bounds it, and what it measured (GB300, rows of 512 columns, 64 heads;
+// products and bytes counted once):
+//   2048 queries, window 4096, E4M3     1.36 ms   0.81 PFLOP/s
+//   8192 queries, window 128, BF16      526 us    2.1 TB/s
+//   16 x 1 query, window 8192, BF16     67 us     2.0 TB/s
+//   32 x 1 query, 32768 keys, E2M1      182 us    1.0 TB/s, 0.46 PFLOP/s
+//   1 query, 131072 keys, E2M1          56 us     0.64 TB/s
+// E4M3: the matrix pipe and the shared memory that feeds it, 80 % busy: at 64
+// rows an instruction takes what its operands take to read (128 x 32 and 64 x 32
+// bytes, 50 of 40 cycles), and the weights' three parts read the rows three
+// times.  BF16 and E2M1 of 512 columns: one block of 128 keys fills the stages, so
+// that the next one's copies and first product wait for the second product to
+// free them; that chain takes 9000 cycles a block (2500 second product, 2000
+// copies, 800 first product, 2700 softmax, the rest handing over).  Blocks of 64
+// keys, of which two fit, were no faster (67 us in BF16) or slower (215 us in
+// E2M1): the first product's rows past the block are read all the same.  Few
+// keys: what a CTA does once, 20 to 25 thousand cycles of item decoding, first
+// loads and output, and the join (8 us).
 //
 // Every wait is bounded in wall time; on expiry the kernel sets a watchdog
 // bit, stops, waits for the matrix instructions in flight, frees TMEM and
@@ -107,8 +128,8 @@ struct Form {
   static constexpr uint32_t part_type(int i) { return F8 ? (i & 1 ? 0u : 1u) : 1u; }
 };
 // Thread layout and registers (launch registers x threads is what setmaxnreg
-// deals out again).  Nothing spills: with 227 KB of shared memory in use the
-// L1 cache is too small for local memory.
+// deals out again).  Next to nothing spills: with 227 KB of shared memory in use
+// the L1 cache is too small for local memory.
 template <int NR>
 struct Roles {
   static constexpr int GROUPS = NR / 16;         // softmax groups of 4 warps, 16 rows each
