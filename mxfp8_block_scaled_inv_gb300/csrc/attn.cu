@@ -68,17 +68,17 @@
 //   16 x 1 query, window 8192, BF16     67 us     2.0 TB/s
 //   32 x 1 query, 32768 keys, E2M1      182 us    1.0 TB/s, 0.46 PFLOP/s
 //   1 query, 131072 keys, E2M1          56 us     0.64 TB/s
-// E4M3: the matrix pipe and the shared memory that feeds it, 80 % busy: at 64
-// rows an instruction takes what its operands take to read (128 x 32 and 64 x 32
-// bytes, 50 of 40 cycles), and the weights' three parts read the rows three
-// times.  BF16 and E2M1 of 512 columns: one block of 128 keys fills the stages, so
-// that the next one's copies and first product wait for the second product to
-// free them; that chain takes 9000 cycles a block (2500 second product, 2000
-// copies, 800 first product, 2700 softmax, the rest handing over).  Blocks of 64
-// keys, of which two fit, were no faster (67 us in BF16) or slower (215 us in
-// E2M1): the first product's rows past the block are read all the same.  Few
-// keys: what a CTA does once, 20 to 25 thousand cycles of item decoding, first
-// loads and output, and the join (8 us).
+// E4M3: the products, which are being issued 80 % of the time: at 64 rows an
+// instruction takes 55 to 60 cycles, 48 of them to read its operands (128 x 32
+// and 64 x 32 bytes), where the arithmetic takes 32, and the three parts of the
+// weights read the rows three times.  BF16 and E2M1 of 512 columns: one block of
+// 128 keys fills the stages, so that the next one's copies and first product
+// wait for the second product to free them; that chain takes 9000 cycles a block
+// (2500 second product, 2000 copies, 800 first product, 2700 softmax, the rest
+// handing over).  Blocks of 64 keys, of which two fit, were no faster (67 us in
+// BF16) or slower (215 us in E2M1): the first product's rows past the block are
+// read all the same.  Few keys: what a CTA does once, 20 to 25 thousand cycles of
+// item decoding, first loads and output, and the join (8 us).
 //
 // Every wait is bounded in wall time; on expiry the kernel sets a watchdog
 // bit, stops, waits for the matrix instructions in flight, frees TMEM and
