@@ -374,8 +374,9 @@ size_t mxq_attn_workspace_bytes(int64_t T, int32_t B, int32_t H, int32_t D, int3
  *
  * A row that sees no key gets out = 0 and lse = -infinity.  What masked keys
  * hold (NaN and infinities included) never reaches an output; a visible key
- * row with a NaN or an infinity makes the rows that see it NaN.  Results do
- * not depend on timing: no atomics are used on them.
+ * row with a NaN or an infinity makes the rows that see it NaN.  Values of
+ * 2^70 and more may overflow the FP32 sums.  Results do not depend on timing:
+ * no atomics are used on them.
  * D % 64 == 0, 64 <= D <= 512, 1 <= H <= 4096, B >= 1, sm_scale finite,
  * window, sinks >= 0.  T == 0 is a no-op.  T*H >= 2^31, max_pages*page_size
  * >= 2^31 or num_slots >= 2^31 returns MXQ_ERR_UNSUPPORTED.

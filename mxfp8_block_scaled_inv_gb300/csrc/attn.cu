@@ -22,7 +22,7 @@
 // of the item's first block that (nearly) all rows see, and moves only when a
 // score passes it by more than 2^40, so that blocks need neither a maximum
 // over the keys nor a rescale of O.  (O and the sums then reach 2^40 times the
-// values they stand for.)  Row sums are kept per thread (one key each) in FP32
+// values they stand for, times the number of keys: 2^57 of them leave 2^70.)  Row sums are kept per thread (one key each) in FP32
 // and joined at the end.
 //
 // The kernel is built for a small instruction footprint (70 to 90 KB; at 140 KB
