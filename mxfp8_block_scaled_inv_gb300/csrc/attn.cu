@@ -1581,26 +1581,28 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
 // Joins the partial sums of the tiles that are cut: CTA (x, y) of the x-th of
 // them, the one that begins in the x-th share c that has such a beginning.  Its
 // pieces lie in the slots 2c + 1, 2(c + 1), 2(c + 2), ...; each counts
-// 2^(its reference - the largest).  128 threads, of four columns each, add up
-// every WAYS-th piece of a row, in order and four at a time, so that their loads
-// are under way together; the WAYS sums are added in order too: the result does
-// not depend on timing.
-constexpr int kJoinThreads = 512;
+// 2^(its reference - the largest).  A warp adds up every WAYS-th piece of 128
+// columns of a row, in order, BATCH at a time, so that their loads are under way
+// together; the WAYS sums are added in order too: the result does not depend on
+// timing.  Bound by latency: about 10 us of a call (152 to 215 pieces of 64 rows
+// x 512 columns, 20 to 28 MB from L2); at most two rounds of CTAs, since each
+// begins with the search (four rounds took 1 to 5 us more).
+constexpr int kJoinThreads = 256, kJoinCtas = 1520;  // CTAs, about two to a place on the device
 template <int NR, int WAYS>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const KernelArgs k, const int shares) {
-  constexpr int ROWS = kJoinThreads / 128 / WAYS;  // of a CTA
+__global__ void __launch_bounds__(kJoinThreads, WAYS == 8 ? 3 : 5) attn_join_kernel(const KernelArgs k, const int shares) {
+  constexpr int WARPS = kJoinThreads / 32, ITEMS = WARPS / WAYS, BATCH = WAYS == 8 ? 8 : 4;
   __shared__ int pieces[kJoinThreads];
-  __shared__ uint32_t begins[kJoinThreads / 32];
-  __shared__ float4 part[WAYS][128];
-  __shared__ float2 ml[WAYS];
+  __shared__ uint32_t begins[WARPS];
+  __shared__ float4 part[WARPS][32];
+  __shared__ float2 ml[WARPS];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const AttnArgs& a = k.a;
-  const int tid = threadIdx.x, col = (tid & 127) * 4, sub = tid >> 7;
-  const int way = WAYS > 1 ? sub : 0, r = blockIdx.y * ROWS + (WAYS > 1 ? 0 : sub);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, way = warp % WAYS;
+  const int np = (a.D + 127) >> 7;
   pieces[tid] = tid < shares ? k.desc[tid].w : 0;
   const uint32_t b = __ballot_sync(0xffffffffu, pieces[tid] != 0);
-  if ((tid & 31) == 0) begins[tid >> 5] = b;
+  if (lane == 0) begins[warp] = b;
   __syncthreads();
   int c = -1;
   for (int w = 0, skip = blockIdx.x; w * 32 < shares; ++w) {
@@ -1614,66 +1616,73 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const KernelArg
   }
   if (c < 0) return;
   const int4 d = k.desc[c];
-  if (ROWS == 1 && r >= d.z) return;
   const int used = pieces[c];
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float mx = -INFINITY, sum = 0.0f;
-  if (col < a.D && r < d.z) {
+  // (NR rows of np parts are a whole number of rounds for every warp.)
 #pragma unroll 1
-    for (int i0 = way; i0 < used; i0 += 4 * WAYS) {
-      float2 v[4];
-      float4 x[4];
+  for (int item = blockIdx.y * ITEMS + warp / WAYS; item < NR * np; item += gridDim.y * ITEMS) {
+    const int r = item / np, col = (item - r * np) * 128 + lane * 4;
+    const bool here = r < d.z && col < a.D;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float mx = -INFINITY, sum = 0.0f;
+    if (here) {
+#pragma unroll 1
+      for (int i0 = way; i0 < used; i0 += BATCH * WAYS) {
+        float2 v[BATCH];
+        float4 x[BATCH];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = i0 + e * WAYS;
-        const int64_t at = (int64_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * NR + r;
-        v[e] = i < used ? k.part_ml[at] : make_float2(-INFINITY, 0.f);
-        x[e] = i < used ? *reinterpret_cast<const float4*>(k.part + at * a.D + col) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      const float top = fmaxf(fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x)), mx);
-      const float old = ex2(mx - top);
-      mx = top;
-      sum *= old;
-      o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
+        for (int e = 0; e < BATCH; ++e) {
+          const int i = i0 + e * WAYS;
+          const int64_t at = (int64_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * NR + r;
+          v[e] = i < used ? k.part_ml[at] : make_float2(-INFINITY, 0.f);
+          x[e] = i < used ? *reinterpret_cast<const float4*>(k.part + at * a.D + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        const float before = mx;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float f = ex2(v[e].x - mx);
-        sum += f * v[e].y;
-        o.x += f * x[e].x;
-        o.y += f * x[e].y;
-        o.z += f * x[e].z;
-        o.w += f * x[e].w;
+        for (int e = 0; e < BATCH; ++e) mx = fmaxf(mx, v[e].x);
+        const float old = ex2(before - mx);
+        sum *= old;
+        o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
+#pragma unroll
+        for (int e = 0; e < BATCH; ++e) {
+          const float f = ex2(v[e].x - mx);
+          sum += f * v[e].y;
+          o.x += f * x[e].x;
+          o.y += f * x[e].y;
+          o.z += f * x[e].z;
+          o.w += f * x[e].w;
+        }
       }
     }
-  }
-  if constexpr (WAYS > 1) {
-    part[way][tid & 127] = o;
-    if (col == 0) ml[way] = make_float2(mx, sum);
-    __syncthreads();
-    if (way != 0) return;
+    if constexpr (WAYS > 1) {
+      __syncthreads();  // the last ones have been read
+      part[warp][lane] = o;
+      if (lane == 0) ml[warp] = make_float2(mx, sum);
+      __syncthreads();
+      if (way != 0) continue;
 #pragma unroll
-    for (int w = 1; w < WAYS; ++w) mx = fmaxf(mx, ml[w].x);
-    sum = 0.0f;
-    o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 1; w < WAYS; ++w) mx = fmaxf(mx, ml[warp + w].x);
+      sum = 0.0f;
+      o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < WAYS; ++w) {
-      const float f = ex2(ml[w].x - mx);
-      const float4 x = part[w][tid & 127];
-      sum += f * ml[w].y;
-      o.x += f * x.x;
-      o.y += f * x.y;
-      o.z += f * x.z;
-      o.w += f * x.w;
+      for (int w = 0; w < WAYS; ++w) {
+        const float f = ex2(ml[warp + w].x - mx);
+        const float4 x = part[warp + w][lane];
+        sum += f * ml[warp + w].y;
+        o.x += f * x.x;
+        o.y += f * x.y;
+        o.z += f * x.z;
+        o.w += f * x.w;
+      }
     }
+    if (!here) continue;
+    const float vs = a.dtype == MXQ_CACHE_E4M3 ? __ldg(a.kv_scale) : 1.0f;
+    const float inv = sum == 0.0f ? 0.0f : vs / sum;
+    const int64_t row = (int64_t)(((uint64_t)(uint32_t)d.y << 32) | (uint32_t)d.x) + r;
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + (row * a.D + col) * 2) =
+        make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
+    if (col == 0 && a.lse != nullptr)
+      a.lse[row] = sum == 0.0f ? -INFINITY : (__log2f(sum) + mx) * 0.6931471805599453f;
   }
-  if (col >= a.D || r >= d.z) return;
-  const float vs = a.dtype == MXQ_CACHE_E4M3 ? __ldg(a.kv_scale) : 1.0f;
-  const float inv = sum == 0.0f ? 0.0f : vs / sum;
-  const int64_t row = (int64_t)(((uint64_t)(uint32_t)d.y << 32) | (uint32_t)d.x) + r;
-  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + (row * a.D + col) * 2) =
-      make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
-  if (col == 0 && a.lse != nullptr)
-    a.lse[row] = sum == 0.0f ? -INFINITY : (__log2f(sum) + mx) * 0.6931471805599453f;
 }
 
 // ---------------------------------------------------------------- host side
@@ -1769,14 +1778,19 @@ cudaError_t launch_one(KernelArgs k, int grid, int64_t tiles, cudaStream_t s, co
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, tm, k);
   if (e != cudaSuccess || !k.shares) return e;
-  // Fewer tiles than a quarter of the shares are cut into more than four pieces
-  // each, and more threads share a row then.
-  cfg.gridDim = dim3((unsigned)(tiles < grid ? tiles : grid), NR, 1);
-  cfg.blockDim = dim3(kJoinThreads, 1, 1);
-  cfg.dynamicSmemBytes = 0;
-  if (tiles * 4 < grid) return cudaLaunchKernelEx(&cfg, attn_join_kernel<NR, 4>, k, grid);
-  cfg.gridDim.y = NR / (kJoinThreads / 128);
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<NR, 1>, k, grid);
+  // As many warps to a sum as a tile has a few pieces each for (shares over
+  // tiles, at least).
+  auto join = [&](auto join_kernel, int ways) {
+    const int64_t rounds = NR * ceil_div(k.a.D, 128) * ways / (kJoinThreads / 32), x = tiles < grid ? tiles : grid;
+    const int64_t y = ceil_div(kJoinCtas, x);
+    cfg.gridDim = dim3((unsigned)x, (unsigned)(y < rounds ? y : rounds), 1);
+    cfg.blockDim = dim3(kJoinThreads, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, join_kernel, k, grid);
+  };
+  if (tiles * 16 <= grid) return join(attn_join_kernel<NR, 8>, 8);
+  if (tiles * 4 <= grid) return join(attn_join_kernel<NR, 4>, 4);
+  return join(attn_join_kernel<NR, 1>, 1);
 }
 
 template <int NR>
