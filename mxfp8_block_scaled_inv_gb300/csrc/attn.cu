@@ -65,9 +65,9 @@
 // products and bytes counted once):
 //   2048 queries, window 4096, E4M3     1.36 ms   0.81 PFLOP/s
 //   8192 queries, window 128, BF16      526 us    2.1 TB/s
-//   16 x 1 query, window 8192, BF16     67 us     2.0 TB/s
+//   16 x 1 query, window 8192, BF16     65 us     2.1 TB/s
 //   32 x 1 query, 32768 keys, E2M1      182 us    1.0 TB/s, 0.46 PFLOP/s
-//   1 query, 131072 keys, E2M1          56 us     0.64 TB/s
+//   1 query, 131072 keys, E2M1          52 us     0.69 TB/s
 // E4M3: the products, which are being issued 80 % of the time: at 64 rows an
 // instruction takes 55 to 60 cycles, 48 of them to read its operands (128 x 32
 // and 64 x 32 bytes), where the arithmetic takes 32, and the three parts of the
@@ -78,7 +78,7 @@
 // handing over).  Blocks of 64 keys, of which two fit, were no faster (67 us in
 // BF16) or slower (215 us in E2M1): the first product's rows past the block are
 // read all the same.  Few keys: what a CTA does once, 20 to 25 thousand cycles of
-// item decoding, first loads and output, and the join (8 us).
+// item decoding, first loads and output, and the join (10 us).
 //
 // Every wait is bounded in wall time; on expiry the kernel sets a watchdog
 // bit, stops, waits for the matrix instructions in flight, frees TMEM and
