@@ -358,12 +358,13 @@ size_t mxq_attn_workspace_bytes(int64_t T, int32_t B, int32_t H, int32_t D, int3
  *  out_bf16    [T, H, D]: sum_j exp(s_j - lse) * k_j over the visible keys,
  *              s_j = sm_scale * (q . k_j); rounded once to BF16.  The two
  *              products run on the tensor cores with FP32 accumulation.
- *              Before the second one the exponentials are rounded to BF16,
- *              or (MXQ_CACHE_E4M3) to 10 significant bits, those below 2^-26
- *              of a reference near the largest to zero; where one is 1/16 of
- *              its row's sum or more, what the rounding left is added too.
- *              The scores' query is exact in BF16's 8 bits (MXQ_CACHE_E4M3:
- *              relative to its row's largest value).
+ *              Before the second one the exponentials are rounded to BF16
+ *              (by 2^-8 of themselves at most), or (MXQ_CACHE_E4M3) by 2^-8.8
+ *              of themselves or 2^-30 of their row's largest, whichever is
+ *              more; where one is 1/16 of its row's sum or more, what the
+ *              rounding left is added too.  lse counts them unrounded.  The
+ *              scores' query is exact (MXQ_CACHE_E4M3: to 2^-21 of its row's
+ *              largest value).
  *  lse         optional [T, H] FP32: log(sum_j exp(s_j)).
  *  err_flag    optional int32 device word: MXQ_DEVERR_SLOT when a block-table
  *              entry that is read lies outside the cache (its keys are

@@ -45,8 +45,14 @@
 // bound a kernel that did: 2048 queries with a window of 4096 took 2350 us).  The
 // other operands are then sums of 8-bit parts: Q two E4M3 parts (4 + 4 significant
 // bits, all of BF16's 8, relative to the row's largest value: a row is scaled by a
-// power of two), P an E5M2, an E4M3 and an E5M2 part (10 bits) down to 2^-26 of
-// the reference and nothing below.
+// power of two; half a step of the second part is 2^-21 of that value), P three
+// E5M2 parts.  E5M2 is FP16's upper byte, so that a part is the upper byte of
+// what the parts before it left, an FP16 number that holds it exactly: nothing is
+// lost between the parts, whatever the weight.  A weight is off by 2^-8.8 of
+// itself at most, or by half of E5M2's smallest step where that is more: the
+// reference is held as 2^13, so that this is 2^-30 of it, met by weights below
+// 2^-21 of it.  (E4M3 as the second part has a bit more, but ends seven octaves
+// before E5M2: weights below 2^-16 of the reference lost 8 % of themselves.)
 //
 // P would lose to its rounding as much as the output to its own.  So wherever a
 // weight is at least 1/16 of its row's sum so far, what is left of it after
@@ -121,11 +127,12 @@ struct Form {
   static constexpr int STAGE = CHUNKS * kChunkBytes;
   // Parts of a weight, of which the last is only used where it is large; log2
   // of what a weight equal to the reference's is held as, and of the most (8
-  // bits: what the first part leaves has to fit E4M3).
+  // bits: FP16 and E5M2 end below 2^16).
   static constexpr int PARTS = F8 ? 4 : 2, SURE = F8 ? 3 : 1;
-  static constexpr float SHIFT = F8 ? 9.0f : 0.0f, MOST = F8 ? 11.0f : 40.0f;
-  // Type of part i in an instruction descriptor: E5M2, E4M3, E5M2, E4M3, or BF16.
-  static constexpr uint32_t part_type(int i) { return F8 ? (i & 1 ? 0u : 1u) : 1u; }
+  static constexpr float SHIFT = F8 ? 13.0f : 0.0f, MOST = F8 ? 15.0f : 40.0f;
+  // Type of part i in an instruction descriptor: E5M2 three times and E4M3 (a
+  // large weight's fourth part is in its range and has a bit more), or BF16.
+  static constexpr uint32_t part_type(int i) { return F8 && i == 3 ? 0u : 1u; }
 };
 // Thread layout and registers (launch registers x threads is what setmaxnreg
 // deals out again).  Next to nothing spills: with 227 KB of shared memory in use
@@ -505,21 +512,36 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ uint32_t pack2_rest(float lo, float hi, uint32_t w) {
   return pack2(lo - bf16_lo(w), hi - bf16_hi(w));
 }
-// Four values -> four E5M2 bytes (round to nearest even, saturating).
-__device__ __forceinline__ uint32_t pack_e5m2(float a, float b, float c, float d) {
+// Two values -> FP16, the first in the low half.
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t v) { return __half22float2(*reinterpret_cast<__half2*>(&v)); }
+__device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Four FP16 values -> four bytes: E5M2 cut, E5M2 and E4M3 to the nearest.
+__device__ __forceinline__ uint32_t cut_e5m2(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7531); }
+__device__ __forceinline__ uint32_t round_e5m2(uint32_t a, uint32_t b) {
   uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(lo) : "r"(a));
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(hi) : "r"(b));
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
-// Four values -> four E4M3 bytes.
-__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
-  return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
-}
-// A value cut to the three (E5M2) or four (E4M3) significant bits of a part.
-template <uint32_t TYPE>
-__device__ __forceinline__ float cut_part(float x) {
-  return __uint_as_float(__float_as_uint(x) & (TYPE ? 0xFFE00000u : 0xFFF00000u));
+__device__ __forceinline__ uint32_t round_e4m3(uint32_t a, uint32_t b) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(b));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 template <int N, int LAUNCH>
 __device__ __forceinline__ void regs_set() {
@@ -1452,38 +1474,42 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
             put(1, 16, hi + 4);
           }
         } else {
-          // 3 + 4 + 3 significant bits and, where some weight is large, 4 more.
-          // All but the last part are cut, not rounded, so that what is left of
-          // the weight is exact and positive.
-          uint32_t w[3][NC / 4], more[NC / 4];
-          auto split = [&](auto type, bool last, uint32_t* out) {
-            constexpr uint32_t T = decltype(type)::value;
+          // The weights in FP16, whose upper bytes are the first parts; where some
+          // weight is large, with what FP16 left of it, which joins the rest
+          // before the third part is taken.
+          uint32_t h[NC / 2], left[NC / 2], w[4][NC / 4];
+#pragma unroll
+          for (int e = 0; e < NC / 2; ++e) h[e] = pack_f16(d[2 * e], d[2 * e + 1]);
+          if (hot != 0)
+#pragma unroll
+            for (int e = 0; e < NC / 2; ++e) {
+              const float2 v = unpack_f16(h[e]);
+              left[e] = pack_f16(d[2 * e] - v.x, d[2 * e + 1] - v.y);
+            }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int q = 0; q < NC / 4; ++q) w[i][q] = cut_e5m2(h[2 * q], h[2 * q + 1]);
+#pragma unroll
+            for (int e = 0; e < NC / 2; ++e) h[e] = sub_f16x2(h[e], h[e] & 0xFF00FF00u);
+          }
+          if (hot == 0) {
+#pragma unroll
+            for (int q = 0; q < NC / 4; ++q) w[2][q] = round_e5m2(h[2 * q], h[2 * q + 1]);
+          } else {
 #pragma unroll
             for (int q = 0; q < NC / 4; ++q) {
-              float t[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                t[e] = last ? d[4 * q + e] : cut_part<T>(d[4 * q + e]);
-                d[4 * q + e] -= t[e];
-              }
-              out[q] = T ? pack_e5m2(t[0], t[1], t[2], t[3]) : pack_e4m3(t[0], t[1], t[2], t[3]);
+              const uint32_t a0 = add_f16x2(h[2 * q], left[2 * q]), a1 = add_f16x2(h[2 * q + 1], left[2 * q + 1]);
+              w[2][q] = round_e5m2(a0, a1);
+              w[3][q] = round_e4m3(sub_f16x2(a0, __byte_perm(w[2][q], 0, 0x1404)),
+                                   sub_f16x2(a1, __byte_perm(w[2][q], 0, 0x3424)));
             }
-          };
-          using E5M2 = std::integral_constant<uint32_t, 1>;
-          using E4M3 = std::integral_constant<uint32_t, 0>;
-          split(E5M2(), false, w[0]);
-          split(E4M3(), false, w[1]);
-          if (hot == 0) {
-            split(E5M2(), true, w[2]);
-          } else {
-            split(E5M2(), false, w[2]);
-            split(E4M3(), true, more);
           }
           free_p();
           put(0, 0, w[0]);
           put(1, 0, w[1]);
           put(2, 0, w[2]);
-          if (hot != 0) put(3, 0, more);
+          if (hot != 0) put(3, 0, w[3]);
         }
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
