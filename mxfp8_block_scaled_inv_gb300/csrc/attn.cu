@@ -1714,7 +1714,7 @@ __global__ void __launch_bounds__(kJoinThreads, WAYS == 8 ? 3 : 5) attn_join_ker
 // ---------------------------------------------------------------- host side
 struct Plan {
   int NR, grid;
-  int64_t tiles;  // at most
+  int64_t tiles;  // at most, of this call
   bool shares;
   size_t part_bytes, ml_bytes, bytes;
 };
@@ -1724,14 +1724,17 @@ struct Plan {
 constexpr int kShares = 152;
 static_assert(kShares <= kJoinThreads, "a thread of the join looks at one share");
 
+// Everything but `tiles` follows from what the workspace query takes, which is not
+// told whether there is a q_start.
 Plan make_plan(const AttnArgs& a) {
   Plan p;
   const int64_t rows = a.T * a.H, per_seq = rows / a.B;
   p.NR = per_seq > 32 ? 64 : per_seq > 16 ? 32 : 16;
-  // Tiles, and key blocks of a tile, at most.
-  const int64_t tiles = a.q_start == nullptr && a.T == a.B ? a.B * ceil_div(a.H, p.NR)
-                                                           : rows / p.NR + (a.B < rows ? a.B : rows);
-  p.tiles = tiles;
+  // Tiles, and key blocks of a tile, at most; T == B is taken as one token per
+  // sequence, which a q_start need not bear out.
+  const int64_t most = rows / p.NR + (a.B < rows ? a.B : rows);
+  const int64_t tiles = a.T == a.B ? a.B * ceil_div(a.H, p.NR) : most;
+  p.tiles = a.q_start == nullptr ? tiles : most;
   const int64_t cap = (int64_t)a.max_pages * a.page_size;
   int64_t keys = cap;
   if (a.window > 0) {
@@ -1747,7 +1750,7 @@ Plan make_plan(const AttnArgs& a) {
   // each CTA walks the line of all tiles before it begins its share.
   // (Weights are 32-bit numbers on the device.)
   const int64_t nb = ceil_div(keys, kKeys) + 1, idle = ceil_div(tiles, kShares) * kShares - tiles;
-  p.shares = rows / p.NR < 8 * kShares && nb > 3 && tiles * nb < (int64_t)1 << 31 &&
+  p.shares = rows / p.NR < 8 * kShares && nb > 3 && most * nb < (int64_t)1 << 31 &&
              (tiles <= kShares || idle * nb * ceil_div(a.D, 128) > 16 * kShares);
   p.grid = p.shares || tiles > kShares ? kShares : (int)tiles;
   const size_t pieces = 2 * (size_t)p.grid;
