@@ -133,6 +133,22 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(stream, shape, dtype, device):
+    """A tensor that the call allocates itself, from the pool of the stream that it runs on: memory of another
+    stream's pool may be in use there, or be handed out again before the call's kernels are done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _empty_like(stream, t):
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
+
+
 def mxq_version():
     """Library ABI version, major*10000 + minor*100 + patch (100 = 0.1.0)."""
     return lib().mxq_version()
@@ -151,9 +167,9 @@ def mxq_inv_rope_group_quant(x, pos=None, cos=None, sin=None, R=0, q=None, sc=No
     T, G, D = x.shape
     KG = (D + 127) // 128
     if q is None:
-        q = torch.empty((T, G, D), dtype=torch.uint8, device=x.device)
+        q = _empty(stream, (T, G, D), torch.uint8, x.device)
     if sc is None:
-        sc = torch.empty((T, G, KG), dtype=torch.uint8, device=x.device)
+        sc = _empty(stream, (T, G, KG), torch.uint8, x.device)
     cs_ld = cos.stride(0) if cos is not None else 0
     max_pos = cos.shape[0] if cos is not None else 0
     st = lib().mxq_inv_rope_group_quant(_ptr(x), T, G, D, R, _ptr(pos), _ptr(cos), _ptr(sin),
@@ -172,7 +188,7 @@ def mxq_prepare_weight_scales(w_e8m0, K, out=None, stream=None):
     """w_e8m0 uint8 [B, N, ceil(K/128)] -> prepared scale bytes for mxq_bmm_a8w8."""
     B, N, _ = w_e8m0.shape
     if out is None:
-        out = torch.empty(mxq_weight_scale_bytes(B, N, K), dtype=torch.uint8, device=w_e8m0.device)
+        out = _empty(stream, mxq_weight_scale_bytes(B, N, K), torch.uint8, w_e8m0.device)
     st = lib().mxq_prepare_weight_scales(_ptr(w_e8m0), B, N, K, _ptr(out), _stream(stream))
     _check("mxq_prepare_weight_scales", st)
     return out
@@ -189,10 +205,10 @@ def mxq_bmm_a8w8(a, a_sf, w, w_sf, out=None, ws=None, stream=None):
     T, G, K = a.shape
     N = w.shape[1]
     if out is None:
-        out = torch.empty((T, G, N), dtype=torch.bfloat16, device=a.device)
+        out = _empty(stream, (T, G, N), torch.bfloat16, a.device)
     need = mxq_bmm_workspace_bytes(T, G, N, K)
     if ws is None and need > 0:
-        ws = torch.empty(need, dtype=torch.uint8, device=a.device)
+        ws = _empty(stream, need, torch.uint8, a.device)
     st = lib().mxq_bmm_a8w8(_ptr(a), _ptr(a_sf), _ptr(w), _ptr(w_sf), _ptr(out), T, G, N, K,
                             _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream))
     _check("mxq_bmm_a8w8", st)
@@ -210,10 +226,10 @@ def mxq_linear(x, w, w_sf, out=None, ws=None, stream=None):
     M, K = x.shape
     N = w.shape[-2]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        out = _empty(stream, (M, N), torch.bfloat16, x.device)
     need = mxq_linear_workspace_bytes(M, N, K)
     if ws is None and need > 0:
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+        ws = _empty(stream, need, torch.uint8, x.device)
     st = lib().mxq_linear(_ptr(x), _ptr(w), _ptr(w_sf), _ptr(out), M, N, K, _ptr(ws),
                           0 if ws is None else ws.numel(), _stream(stream))
     _check("mxq_linear", st)
@@ -227,7 +243,7 @@ def mxq_linear_noalloc(x, w, w_sf, out=None, stream=None):
     M, K = x.shape
     N = w.shape[-2]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        out = _empty(stream, (M, N), torch.bfloat16, x.device)
     st = lib().mxq_linear_noalloc(_ptr(x), _ptr(w), _ptr(w_sf), _ptr(out), M, N, K, _stream(stream))
     _check("mxq_linear_noalloc", st)
     return out
@@ -237,7 +253,7 @@ def mxq_dequant_bf16(w, w_e8m0, out=None, stream=None):
     """w uint8 [B, N, K], w_e8m0 uint8 [B, N, ceil(K/128)] -> bf16 [B, N, K]."""
     B, N, K = w.shape
     if out is None:
-        out = torch.empty((B, N, K), dtype=torch.bfloat16, device=w.device)
+        out = _empty(stream, (B, N, K), torch.bfloat16, w.device)
     st = lib().mxq_dequant_bf16(_ptr(w), _ptr(w_e8m0), _ptr(out), B, N, K, _stream(stream))
     _check("mxq_dequant_bf16", st)
     return out
@@ -250,7 +266,7 @@ def mxq_scales_f32_to_e8m0(s, out=None, err_flag=None, stream=None):
     0xFF and sets MXQ_DEVERR_SCALE in the optional int32 `err_flag`."""
     n = s.numel()
     if out is None:
-        out = torch.empty(s.shape, dtype=torch.uint8, device=s.device)
+        out = _empty(stream, s.shape, torch.uint8, s.device)
     st = lib().mxq_scales_f32_to_e8m0(_ptr(s), n, _ptr(out), _ptr(err_flag), _stream(stream))
     _check("mxq_scales_f32_to_e8m0", st)
     return out
@@ -302,10 +318,10 @@ def mxq_wo_a(x, pos, cos, sin, w, w_sf, R=64, out=None, ws=None, err_flag=None, 
     T, G, D = x.shape
     N = w.shape[1]
     if out is None:
-        out = torch.empty((T, G, N), dtype=torch.bfloat16, device=x.device)
+        out = _empty(stream, (T, G, N), torch.bfloat16, x.device)
     need = mxq_wo_a_workspace_bytes(T, G, D, N)
     if ws is None and need > 0:
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+        ws = _empty(stream, need, torch.uint8, x.device)
     cs_ld = cos.stride(0) if cos is not None else 0
     max_pos = cos.shape[0] if cos is not None else 0
     st = lib().mxq_wo_a(_ptr(x), _ptr(pos), _ptr(cos), _ptr(sin), cs_ld, max_pos, _ptr(w), _ptr(w_sf),
@@ -328,7 +344,7 @@ def mxq_rope_kv_insert(q, kv, pos, cos, sin, R, slot_mapping, cache, scale=None,
     T, H, Dq = q.shape if q is not None else (kv.shape[0], 0, 0)
     Dk = kv.shape[1]
     if q is not None and q_out is None:
-        q_out = torch.empty_like(q)
+        q_out = _empty_like(stream, q)
     if cache.dtype == torch.uint8:
         dtype = MXQ_CACHE_E4M3
     elif cache.dtype == torch.bfloat16:
@@ -390,7 +406,7 @@ def mxq_rope_kv4_insert(q, kv, pos, cos, sin, R, slot_mapping, cache, cache_sf, 
         _, H, Dq = q.shape
         pq = _tensor(fn, "q", q, torch.bfloat16, (T, None, None))
         if q_out is None:
-            q_out = torch.empty_like(q)
+            q_out = _empty_like(stream, q)
             pout = q_out.data_ptr()
         else:
             pout = _tensor(fn, "q_out", q_out, torch.bfloat16, (T, H, Dq))
@@ -420,7 +436,7 @@ def mxq_kv4_gather(cache, cache_sf, slots, out=None, err_flag=None, stream=None)
     psf = _tensor(fn, "cache_sf", cache_sf, torch.uint8, (num_slots, Dk // 32))
     pslots = _tensor(fn, "slots", slots, torch.int64, (n,))
     if out is None:
-        out = torch.empty((n, Dk), dtype=torch.bfloat16, device=cache.device)
+        out = _empty(stream, (n, Dk), torch.bfloat16, cache.device)
         pout = out.data_ptr()
     else:
         pout = _tensor(fn, "out", out, torch.bfloat16, (n, Dk))
@@ -469,7 +485,7 @@ def mxq_attn(q, cache, block_table, seq_lens, q_start=None, page_size=64, window
         dtype = MXQ_CACHE_BF16
         pcache = _tensor(fn, "cache", cache, torch.bfloat16, (None, D))
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(stream, q)
         pout = out.data_ptr()
     else:
         pout = _tensor(fn, "out", out, torch.bfloat16, (T, H, D))
@@ -478,7 +494,7 @@ def mxq_attn(q, cache, block_table, seq_lens, q_start=None, page_size=64, window
     if ws is None:
         need = L.mxq_attn_workspace_bytes(T, B, H, D, max_pages, page_size, window, sinks)
         if need > 0:
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+            ws = _empty(stream, need, torch.uint8, q.device)
     pws, nws = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
     st = L.mxq_attn(pq, T, H, D, pstart, plen, B, pbt, max_pages, page_size, pcache, num_slots, dtype, pscale, psf,
                     window, sinks, D ** -0.5 if sm_scale is None else sm_scale, pout, plse, _addr(err_flag), pws,
