@@ -252,7 +252,8 @@ __device__ __forceinline__ Item get_tile(const AttnArgs& a, const Seq& s, int b,
   it.piece = -1;
   it.pad = 0;
   if (it.p1 >= 0) {
-    const int lo = a.window > 0 ? max(0, it.p0 - a.window + 1) : 0;
+    // (A tile may begin before its first key: p0 < 0, and the window be INT_MAX.)
+    const int lo = a.window > 0 ? max(0, max(it.p0, 0) - a.window + 1) : 0;
     it.u_lo = lo / kUnit;
     const int sink_end = a.window > 0 ? min(a.sinks, lo) : 0;
     it.ns = min((sink_end + kUnit - 1) / kUnit, it.u_lo);
@@ -1183,7 +1184,7 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
       }
       // The key of the first block whose scores are the first reference: the
       // first of those that all rows see, where there is one.
-      const int key_ref = a.window > 0 && it.ns == 0 && it.blk0 == 0
+      const int key_ref = has && a.window > 0 && it.ns == 0 && it.blk0 == 0
                               ? min(max(it.p1 - a.window + 1 - it.u_lo * kUnit, 0), kKeys - 1) : 0;
       ptx::named_sync(bar, 128);
       if (F8 && has) {
