@@ -754,6 +754,7 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
     return it.b >= 0;
   };
 
+  uint32_t tma_st = 0, tma_stp = 0;  // the copying warp: the stage after its last, and that one's phase
   if (warp >= R::LOAD0) {
     // ------------------------------------- the query, and rows to be widened
     regs_set<R::REGS_LOAD, R::REGS>();
@@ -914,11 +915,8 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
           }
         }
       }
-      // Copies in flight land before the shared memory goes away: every stage
-      // that was filled is waited for (after an abort nobody else does).
-      if (*abort_flag && lane == 0)
-        for (int s = 0; s < k.stages; ++s)
-          if (!ptx::mbar_wait(&sh.full[s], (uint32_t)s < st ? stp : stp ^ 1u, kWaitNs / 8)) break;
+      tma_st = st;
+      tma_stp = stp;
     }
   } else if (warp == R::MMA) {
     // ------------------------------------------------------------ products
@@ -1601,6 +1599,12 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
     }
   }
   __syncthreads();
+  // After an abort, copies may be in flight that nobody has waited for: they land
+  // before the shared memory goes away.  (Only here is it certain that no role
+  // gives up any more: one may after the copying warp has issued its last copy.)
+  if (DT != MXQ_CACHE_E2M1 && sh.abort && warp == R::TMA && lane == 0)
+    for (int s = 0; s < k.stages; ++s)
+      if (!ptx::mbar_wait(&sh.full[s], (uint32_t)s < tma_st ? tma_stp : tma_stp ^ 1u, kWaitNs / 8)) break;
   if (tid == 0 && sh.abort) atomicOr(k.watchdog, kWdAttn);
   if (warp == R::MMA) ptx::tmem_dealloc(tmem, kTmemCols);
 }
