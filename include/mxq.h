@@ -427,7 +427,7 @@ int mxq_linear_noalloc(const void* x_bf16, const uint8_t* w_e4m3, const uint8_t*
 
 /*
  * Testing aids (the pages have no counterpart), process-wide settings that
- * change no result.
+ * change no result (but for the last).
  *
  * mxq_debug_set_pair_limit caps the number of CTA pairs that the many-token
  * GEMM forms launch -- mxq_bmm_a8w8, mxq_wo_a and mxq_linear above 128
@@ -450,10 +450,17 @@ int mxq_linear_noalloc(const void* x_bf16, const uint8_t* w_e4m3, const uint8_t*
  * pair instead of their owner since the last clear (host call, synchronous;
  * with clear != 0 the count is reset after reading).  0 after a call means
  * no pair ever waited 50 us for a job.  MXQ_ERR_NULL for a NULL host_value.
+ *
+ * mxq_debug_set_attn_wait bounds the waits inside mxq_attn's kernel to ns
+ * nanoseconds (0, the default, and values above 2e9: 2e9).  A wait that runs
+ * out ends the kernel as mxq_watchdog_read describes: a bound of a few
+ * microseconds exercises that path, and leaves the call's outputs undefined.
+ * Returns the previous bound.
  */
 int mxq_debug_set_pair_limit(int pairs);
 int mxq_debug_set_lazy_pairs(int from);
 int mxq_debug_takeovers(uint32_t* host_value, int clear);
+uint32_t mxq_debug_set_attn_wait(uint32_t ns);
 
 /*
  * Watchdog word of the GEMM kernels, of the streamed query copy of the

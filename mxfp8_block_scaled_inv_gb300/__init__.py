@@ -25,6 +25,7 @@ __all__ = [
     "mxq_version", "mxq_wo_a_workspace_bytes", "mxq_wo_a", "wo_a", "mxq_rope_kv_insert",
     "mxq_rope_kv4_insert", "mxq_kv4_gather", "mxq_attn_workspace_bytes", "mxq_attn",
     "mxq_debug_set_pair_limit", "mxq_debug_set_lazy_pairs", "mxq_debug_takeovers",
+    "mxq_debug_set_attn_wait",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -76,6 +77,7 @@ _SIGNATURES = {
     "mxq_debug_set_pair_limit": (ctypes.c_int, [ctypes.c_int]),
     "mxq_debug_set_lazy_pairs": (ctypes.c_int, [ctypes.c_int]),
     "mxq_debug_takeovers": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]),
+    "mxq_debug_set_attn_wait": (ctypes.c_uint32, [ctypes.c_uint32]),
     "mxq_wo_a_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32]),
     "mxq_rope_kv_insert": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _i64,
                                           _i64, _i32, _vp, _vp, _i64, _i32, _vp, _vp, _vp]),
@@ -297,6 +299,13 @@ def mxq_debug_takeovers(clear=False):
     v = ctypes.c_uint32(0)
     _check("mxq_debug_takeovers", lib().mxq_debug_takeovers(ctypes.byref(v), 1 if clear else 0))
     return v.value
+
+
+def mxq_debug_set_attn_wait(ns):
+    """Testing aid: bound the waits inside mxq_attn's kernel to `ns` nanoseconds (0: the default, two
+    seconds); returns the previous bound.  A wait that runs out sets bit 0x40 of the watchdog word and
+    leaves the call's outputs undefined."""
+    return lib().mxq_debug_set_attn_wait(int(ns))
 
 
 def mxq_watchdog_selftest(limit_ns=1_000_000, stream=None):

@@ -86,9 +86,9 @@
 // read all the same.  Few keys: what a CTA does once, 20 to 25 thousand cycles of
 // item decoding, first loads and output, and the join (10 us).
 //
-// Every wait is bounded in wall time; on expiry the kernel sets a watchdog
-// bit, stops, waits for the matrix instructions in flight, frees TMEM and
-// returns.
+// Every wait is bounded in wall time (two seconds); on expiry the kernel sets a
+// watchdog bit, stops, waits for the matrix instructions and the copies in
+// flight, frees TMEM and returns.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -110,9 +110,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 namespace {
 
-constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr uint32_t kWaitTries = 100000000u;
-constexpr uint32_t kHintNs = 20;
+constexpr uint32_t kWaitNs = 2000000000u;
 constexpr uint32_t kWdAttn = 64;  // watchdog bit of this kernel
 
 constexpr int kKeys = 128;           // keys of a block (M of the first product)
@@ -161,6 +159,7 @@ struct KernelArgs {
   float2* part_ml;  // [2 * gridDim][NR] (maximum, sum)
   int4* desc;       // [gridDim]: first row (low, high), rows, pieces of the tile that begins there and is cut
   uint32_t* watchdog;
+  uint32_t wait_ns;  // the longest wait
   int shares;       // 1: blocks in equal shares; 0: whole tiles
   int stages;
 };
@@ -424,15 +423,16 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* r) {
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// One try of a barrier wait, asleep for at most kHintNs.
+// One try of a barrier wait.  It returns as soon as the phase is over, and after
+// 4 us if it is not (measured; a suspension hint of 20 ns to 2 us changes nothing).
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n.reg .pred p;\n"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
       "selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(kHintNs)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
@@ -721,17 +721,23 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
 
-  // A bounded wait; false once it or any other wait of the CTA gave up.  A try
-  // takes 20 ns or more, so the bound is two seconds or more.
+  // A bounded wait; false once it or any other wait of the CTA gave up.  The
+  // clock is read after a try that failed (its low word, whose differences have a
+  // sign up to 2.1 s).
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     const uint32_t ad = ptx::smem_u32(bar);
+    uint32_t end = 0;  // 0: no try has failed so far
 #pragma unroll 1
-    for (uint32_t n = 0; n < kWaitTries; ++n) {
-      if (try_wait(ad, parity)) return true;
+    while (!try_wait(ad, parity)) {
       if (*abort_flag) return false;
+      const uint32_t now = (uint32_t)ptx::globaltimer();
+      if (end == 0) end = (now + k.wait_ns) | 1u;
+      if ((int)(now - end) > 0) {
+        *abort_flag = 1;
+        return false;
+      }
     }
-    *abort_flag = 1;
-    return false;
+    return true;
   };
   // The same for a whole warp: its lanes agree on the outcome.
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -1079,7 +1085,7 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
       } else if ((++idle & 63u) == 0) {
         if (idle == 64) t0 = ptx::globaltimer();
         int stop = *abort_flag;
-        if (!stop && ptx::globaltimer() - t0 > kWaitNs) {
+        if (!stop && ptx::globaltimer() - t0 > k.wait_ns) {
           stop = 1;
           if (lane == 0) *abort_flag = 1;
         }
@@ -1836,6 +1842,10 @@ cudaError_t launch_nr(const KernelArgs& k, int grid, int64_t tiles, cudaStream_t
 
 }  // namespace
 
+static std::atomic<uint32_t> g_wait_ns{kWaitNs};
+
+uint32_t set_attn_wait(uint32_t ns) { return g_wait_ns.exchange(ns == 0 || ns > kWaitNs ? kWaitNs : ns); }
+
 size_t attn_workspace_bytes(const AttnArgs& a) { return a.T > 0 ? make_plan(a).bytes : 0; }
 
 cudaError_t launch_attn(const AttnArgs& a, void* ws, cudaStream_t s, const char** why) {
@@ -1843,6 +1853,7 @@ cudaError_t launch_attn(const AttnArgs& a, void* ws, cudaStream_t s, const char*
   KernelArgs k = {};
   k.a = a;
   k.shares = p.shares;
+  k.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
   uint8_t* w = static_cast<uint8_t*>(ws);
   k.part = reinterpret_cast<float*>(w);
   k.part_ml = reinterpret_cast<float2*>(w + p.part_bytes);

@@ -122,6 +122,9 @@ struct AttnArgs {
 };
 size_t attn_workspace_bytes(const AttnArgs& a);
 cudaError_t launch_attn(const AttnArgs& a, void* ws, cudaStream_t s, const char** why);
+// Bounds the attention's waits (0: the default, two seconds, which is also the
+// most); returns the previous bound.
+uint32_t set_attn_wait(uint32_t ns);
 
 // Caps the CTA pairs of the pair-form GEMM launches (0 = no cap); returns
 // the previous cap.

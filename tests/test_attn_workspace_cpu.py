@@ -37,3 +37,9 @@ def test_queried_size_is_accepted(L, H, D):
                                         0.1, Q, None, None, P if need else None, need, None)
                         assert st == 7, (B, T, pages, window, q_start, need, L.mxq_last_error())
     assert some > 100
+
+
+def test_wait_bound_is_a_plain_setting(L):
+    assert L.mxq_debug_set_attn_wait(5000) == 2_000_000_000
+    assert L.mxq_debug_set_attn_wait(3_000_000_000) == 5000  # above the most: the default
+    assert L.mxq_debug_set_attn_wait(0) == 2_000_000_000
