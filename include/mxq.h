@@ -365,6 +365,9 @@ size_t mxq_attn_workspace_bytes(int64_t T, int32_t B, int32_t H, int32_t D, int3
  *              rounding left is added too.  lse counts them unrounded.  The
  *              scores' query is exact (MXQ_CACHE_E4M3: to 2^-21 of its row's
  *              largest value).
+ *              out_bf16 may be q_bf16 (in place); a partial overlap with it,
+ *              an overlap with the cache, and one of lse with any of the three
+ *              return MXQ_ERR_SHAPE.
  *  lse         optional [T, H] FP32: log(sum_j exp(s_j)).
  *  err_flag    optional int32 device word: MXQ_DEVERR_SLOT when a block-table
  *              entry that is read lies outside the cache (its keys are

@@ -492,6 +492,12 @@ int mxq_kv4_gather(const uint8_t* cache, const uint8_t* cache_sf, int64_t num_sl
                      "kv4_gather launch");
 }
 
+// Whether two buffers of these sizes in bytes share any.
+static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
 // Sizes of mxq_attn; MXQ_OK when they are accepted.
 static int validate_attn_sizes(int64_t T, int32_t B, int32_t H, int32_t D, int32_t max_pages,
                                int32_t page_size, int32_t window, int32_t sinks) {
@@ -552,6 +558,17 @@ int mxq_attn(const void* q_bf16, int64_t T, int32_t H, int32_t D, const int32_t*
   if (words & 3u)
     return fail(MXQ_ERR_ALIGN, "q_start, seq_lens, block_table, kv_scale, lse and err_flag must be "
                                "4-byte aligned");
+  // Rows are written while others are read; a row itself is read first (out == q).
+  const size_t rows = (size_t)T * H, row_bytes = (size_t)D * 2;
+  const size_t cache_row = cache_dtype == MXQ_CACHE_BF16   ? row_bytes
+                           : cache_dtype == MXQ_CACHE_E4M3 ? row_bytes / 2
+                                                           : row_bytes / 4;
+  if ((out_bf16 != q_bf16 && overlap(out_bf16, rows * row_bytes, q_bf16, rows * row_bytes)) ||
+      overlap(out_bf16, rows * row_bytes, kv_cache, (size_t)num_slots * cache_row))
+    return fail(MXQ_ERR_SHAPE, "out overlaps q without being q itself, or overlaps the cache");
+  if (lse && (overlap(lse, rows * 4, out_bf16, rows * row_bytes) || overlap(lse, rows * 4, q_bf16, rows * row_bytes) ||
+              overlap(lse, rows * 4, kv_cache, (size_t)num_slots * cache_row)))
+    return fail(MXQ_ERR_SHAPE, "lse overlaps out, q or the cache");
   mxq::AttnArgs a = {};
   a.q = q_bf16;
   a.q_start = q_start;
