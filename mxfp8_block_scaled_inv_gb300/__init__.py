@@ -1,9 +1,11 @@
 """Python binding of libmxq (the MX-scaled FP8 ``wo_a`` path for GB300).
 
-Argument marshalling only: every function here checks nothing that the C
-ABI does not check itself, allocates output tensors with torch when the
-caller passes none, and forwards raw device pointers plus the current
-torch CUDA stream to the entry point of the same name in ``libmxq.so``.
+Argument marshalling only: every function here allocates output tensors with
+torch when the caller passes none, and forwards raw device pointers plus the
+current torch CUDA stream to the entry point of the same name in
+``libmxq.so``, which checks sizes, alignment and missing pointers.  The
+attention and 4-bit cache functions also check what an address does not tell
+(type, shape, device, contiguity); the others leave that to the caller.
 All arithmetic runs in the library's CUDA kernels; there is no other path.
 A missing or unbuilt library raises ``MxqLibraryError`` on first use.
 """
@@ -370,7 +372,10 @@ def mxq_rope_kv_insert(q, kv, pos, cos, sin, R, slot_mapping, cache, scale=None,
 
 
 def _tensor(fn, name, t, dtype, shape=None):
-    """The address of a contiguous CUDA tensor of this dtype (and shape, None = any size); refuses others."""
+    """The address of a contiguous CUDA tensor of this dtype (and shape, None = any size); refuses others.
+    No tensor is no address: the library knows whether it needs one."""
+    if t is None:
+        return None
     if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         raise MxqError(fn, 2, f"{name} must be a contiguous CUDA tensor of {dtype}")
     if shape is not None:
@@ -380,8 +385,11 @@ def _tensor(fn, name, t, dtype, shape=None):
     return t.data_ptr()
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
+def _word(fn, name, t, dtype):
+    """The address of a tensor of one element at least, or None."""
+    if t is not None and t.numel() < 1:
+        raise MxqError(fn, 2, f"{name} has no element")
+    return _tensor(fn, name, t, dtype)
 
 
 # The current stream's handle without a Stream object around it, where torch has it (a decode step makes
@@ -422,6 +430,7 @@ def mxq_rope_kv4_insert(q, kv, pos, cos, sin, R, slot_mapping, cache, cache_sf, 
     cs_ld = max_pos = 0
     if R > 0:
         ppos = _tensor(fn, "pos", pos, torch.int64, (T,))
+    if R > 0 and cos is not None and sin is not None:
         max_pos, width = cos.shape
         cs_ld = cos.stride(0)
         if cos.dtype is not torch.bfloat16 or sin.dtype is not torch.bfloat16 or not cos.is_cuda \
@@ -430,7 +439,8 @@ def mxq_rope_kv4_insert(q, kv, pos, cos, sin, R, slot_mapping, cache, cache_sf, 
             raise MxqError(fn, 2, "cos and sin must be CUDA bf16 [max_pos, >= R/2] with the same strides")
         pcos, psin = cos.data_ptr(), sin.data_ptr()
     st = lib().mxq_rope_kv4_insert(pq, pout, T, H, Dq, pkv, Dk, ppos, pcos, psin, cs_ld, max_pos, R, pslot,
-                                   pcache, psf, num_slots, _addr(err_flag), _stream_of(stream, kv.device))
+                                   pcache, psf, num_slots, _word(fn, "err_flag", err_flag, torch.int32),
+                                   _stream_of(stream, kv.device))
     if st:
         _check(fn, st)
     return q_out
@@ -449,8 +459,8 @@ def mxq_kv4_gather(cache, cache_sf, slots, out=None, err_flag=None, stream=None)
         pout = out.data_ptr()
     else:
         pout = _tensor(fn, "out", out, torch.bfloat16, (n, Dk))
-    st = lib().mxq_kv4_gather(pcache, psf, num_slots, Dk, pslots, n, pout, _addr(err_flag),
-                              _stream_of(stream, cache.device))
+    st = lib().mxq_kv4_gather(pcache, psf, num_slots, Dk, pslots, n, pout,
+                              _word(fn, "err_flag", err_flag, torch.int32), _stream_of(stream, cache.device))
     if st:
         _check(fn, st)
     return out
@@ -488,8 +498,7 @@ def mxq_attn(q, cache, block_table, seq_lens, q_start=None, page_size=64, window
     elif cache.dtype is torch.uint8:
         dtype = MXQ_CACHE_E4M3
         pcache = _tensor(fn, "cache", cache, torch.uint8, (None, D))
-        if kv_scale is not None:
-            pscale = _tensor(fn, "kv_scale", kv_scale, torch.float32)
+        pscale = _word(fn, "kv_scale", kv_scale, torch.float32)
     else:
         dtype = MXQ_CACHE_BF16
         pcache = _tensor(fn, "cache", cache, torch.bfloat16, (None, D))
@@ -504,10 +513,11 @@ def mxq_attn(q, cache, block_table, seq_lens, q_start=None, page_size=64, window
         need = L.mxq_attn_workspace_bytes(T, B, H, D, max_pages, page_size, window, sinks)
         if need > 0:
             ws = _empty(stream, need, torch.uint8, q.device)
-    pws, nws = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
+    pws, nws = (None, 0) if ws is None else (_tensor(fn, "ws", ws, torch.uint8), ws.numel())
+    perr = _word(fn, "err_flag", err_flag, torch.int32)
     st = L.mxq_attn(pq, T, H, D, pstart, plen, B, pbt, max_pages, page_size, pcache, num_slots, dtype, pscale, psf,
-                    window, sinks, D ** -0.5 if sm_scale is None else sm_scale, pout, plse, _addr(err_flag), pws,
-                    nws, _stream_of(stream, q.device))
+                    window, sinks, D ** -0.5 if sm_scale is None else sm_scale, pout, plse, perr, pws, nws,
+                    _stream_of(stream, q.device))
     if st:
         _check(fn, st)
     return out
