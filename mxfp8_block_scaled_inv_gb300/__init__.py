@@ -386,8 +386,8 @@ def _tensor(fn, name, t, dtype, shape=None):
 
 
 def _word(fn, name, t, dtype):
-    """The address of a tensor of one element at least, or None."""
-    if t is not None and t.numel() < 1:
+    """The address of a tensor of one element at least."""
+    if t.numel() < 1:
         raise MxqError(fn, 2, f"{name} has no element")
     return _tensor(fn, name, t, dtype)
 
@@ -423,7 +423,7 @@ def mxq_rope_kv4_insert(q, kv, pos, cos, sin, R, slot_mapping, cache, cache_sf, 
         _, H, Dq = q.shape
         pq = _tensor(fn, "q", q, torch.bfloat16, (T, None, None))
         if q_out is None:
-            q_out = _empty_like(stream, q)
+            q_out = torch.empty_like(q) if stream is None else _empty_like(stream, q)
             pout = q_out.data_ptr()
         else:
             pout = _tensor(fn, "q_out", q_out, torch.bfloat16, (T, H, Dq))
@@ -438,9 +438,9 @@ def mxq_rope_kv4_insert(q, kv, pos, cos, sin, R, slot_mapping, cache, cache_sf, 
                 or cos.shape != sin.shape or width < R // 2:
             raise MxqError(fn, 2, "cos and sin must be CUDA bf16 [max_pos, >= R/2] with the same strides")
         pcos, psin = cos.data_ptr(), sin.data_ptr()
+    perr = None if err_flag is None else _word(fn, "err_flag", err_flag, torch.int32)
     st = lib().mxq_rope_kv4_insert(pq, pout, T, H, Dq, pkv, Dk, ppos, pcos, psin, cs_ld, max_pos, R, pslot,
-                                   pcache, psf, num_slots, _word(fn, "err_flag", err_flag, torch.int32),
-                                   _stream_of(stream, kv.device))
+                                   pcache, psf, num_slots, perr, _stream_of(stream, kv.device))
     if st:
         _check(fn, st)
     return q_out
@@ -459,8 +459,9 @@ def mxq_kv4_gather(cache, cache_sf, slots, out=None, err_flag=None, stream=None)
         pout = out.data_ptr()
     else:
         pout = _tensor(fn, "out", out, torch.bfloat16, (n, Dk))
-    st = lib().mxq_kv4_gather(pcache, psf, num_slots, Dk, pslots, n, pout,
-                              _word(fn, "err_flag", err_flag, torch.int32), _stream_of(stream, cache.device))
+    perr = None if err_flag is None else _word(fn, "err_flag", err_flag, torch.int32)
+    st = lib().mxq_kv4_gather(pcache, psf, num_slots, Dk, pslots, n, pout, perr,
+                              _stream_of(stream, cache.device))
     if st:
         _check(fn, st)
     return out
@@ -498,12 +499,12 @@ def mxq_attn(q, cache, block_table, seq_lens, q_start=None, page_size=64, window
     elif cache.dtype is torch.uint8:
         dtype = MXQ_CACHE_E4M3
         pcache = _tensor(fn, "cache", cache, torch.uint8, (None, D))
-        pscale = _word(fn, "kv_scale", kv_scale, torch.float32)
+        pscale = None if kv_scale is None else _word(fn, "kv_scale", kv_scale, torch.float32)
     else:
         dtype = MXQ_CACHE_BF16
         pcache = _tensor(fn, "cache", cache, torch.bfloat16, (None, D))
     if out is None:
-        out = _empty_like(stream, q)
+        out = torch.empty_like(q) if stream is None else _empty_like(stream, q)
         pout = out.data_ptr()
     else:
         pout = _tensor(fn, "out", out, torch.bfloat16, (T, H, D))
@@ -514,7 +515,7 @@ def mxq_attn(q, cache, block_table, seq_lens, q_start=None, page_size=64, window
         if need > 0:
             ws = _empty(stream, need, torch.uint8, q.device)
     pws, nws = (None, 0) if ws is None else (_tensor(fn, "ws", ws, torch.uint8), ws.numel())
-    perr = _word(fn, "err_flag", err_flag, torch.int32)
+    perr = None if err_flag is None else _word(fn, "err_flag", err_flag, torch.int32)
     st = L.mxq_attn(pq, T, H, D, pstart, plen, B, pbt, max_pages, page_size, pcache, num_slots, dtype, pscale, psf,
                     window, sinks, D ** -0.5 if sm_scale is None else sm_scale, pout, plse, perr, pws, nws,
                     _stream_of(stream, q.device))
