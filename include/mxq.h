@@ -381,8 +381,9 @@ size_t mxq_attn_workspace_bytes(int64_t T, int32_t B, int32_t H, int32_t D, int3
  * row with a NaN or an infinity makes the rows that see it NaN.  Values of
  * 2^70 and more may overflow the FP32 sums.  Results do not depend on timing:
  * no atomics are used on them.
- * D % 64 == 0, 64 <= D <= 512, 1 <= H <= 4096, B >= 1, sm_scale finite,
- * window, sinks >= 0.  T == 0 is a no-op.  T*H >= 2^31, max_pages*page_size
+ * D % 64 == 0, 64 <= D <= 512 (the insertions take other row lengths too,
+ * such as 576 or 96: caches of those cannot be attended to), 1 <= H <= 4096,
+ * B >= 1, sm_scale finite, window, sinks >= 0.  T == 0 is a no-op.  T*H >= 2^31, max_pages*page_size
  * >= 2^31 or num_slots >= 2^31 returns MXQ_ERR_UNSUPPORTED.
  */
 int mxq_attn(const void* q_bf16, int64_t T, int32_t H, int32_t D, const int32_t* q_start,

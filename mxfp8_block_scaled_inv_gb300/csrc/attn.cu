@@ -61,19 +61,22 @@
 // to either side).  An item's first two blocks, whose sums are not known yet,
 // have all parts throughout.
 //
-// Work: with many tiles per SM, whole tiles are dealt out, those with the most
-// keys first.  Else the key blocks of all tiles, in one line, are cut into
-// equal shares, one per CTA; a tile that is cut leaves FP32 partial sums, which
-// a second kernel joins in the order of the keys.  Both follow from the
-// lengths on the device, so ragged batches stay balanced.
+// Work: with many tiles per SM, whole tiles are dealt out in turn, the last
+// sequence's last tile first (in a sequence, those with the most keys).  Else the
+// key blocks of all tiles, in one line, are cut into equal shares, one per CTA; a
+// tile that is cut leaves FP32 partial sums, which a second kernel joins in the
+// order of the keys.  Equal shares follow from the lengths on the device and stay
+// balanced in ragged batches.  Whole tiles do not: a chunk of 1216 tiles or more
+// together with a decode over many more keys leaves the latter's blocks, 5 us
+// each, to one CTA.
 //
 // What bounds it, and what it measured (GB300, rows of 512 columns, 64 heads;
 // products and bytes counted once):
 //   2048 queries, window 4096, E4M3     1.36 ms   0.81 PFLOP/s
 //   8192 queries, window 128, BF16      526 us    2.1 TB/s
-//   16 x 1 query, window 8192, BF16     65 us     2.1 TB/s
-//   32 x 1 query, 32768 keys, E2M1      182 us    1.0 TB/s, 0.46 PFLOP/s
-//   1 query, 131072 keys, E2M1          52 us     0.69 TB/s
+//   16 x 1 query, window 8192, BF16     63 us     2.1 TB/s
+//   32 x 1 query, 32768 keys, E2M1      179 us    1.0 TB/s, 0.47 PFLOP/s
+//   1 query, 131072 keys, E2M1          51 us     0.70 TB/s
 // E4M3: the products, which are being issued 80 % of the time: at 64 rows an
 // instruction takes 55 to 60 cycles, 48 of them to read its operands (128 x 32
 // and 64 x 32 bytes), where the arithmetic takes 32, and the three parts of the
@@ -1621,9 +1624,10 @@ __global__ void __launch_bounds__(Roles<NR>::THREADS, 1)
 // 2^(its reference - the largest).  A warp adds up every WAYS-th piece of 128
 // columns of a row, in order, BATCH at a time, so that their loads are under way
 // together; the WAYS sums are added in order too: the result does not depend on
-// timing.  Bound by latency: about 10 us of a call (152 to 215 pieces of 64 rows
-// x 512 columns, 20 to 28 MB from L2); at most two rounds of CTAs, since each
-// begins with the search (four rounds took 1 to 5 us more).
+// timing.  Bound by latency: 9 to 12 us for 152 to 215 pieces of 64 rows x 512
+// columns (20 to 28 MB from L2), 4 us for pieces of 16 rows, each by itself under
+// the profiler; at most two rounds of CTAs, since each begins with the search
+// (four rounds took 1 to 5 us more).
 constexpr int kJoinThreads = 256, kJoinCtas = 1520;  // CTAs, about two to a place on the device
 template <int NR, int WAYS>
 __global__ void __launch_bounds__(kJoinThreads, WAYS == 8 ? 3 : 5) attn_join_kernel(const KernelArgs k, const int shares) {
