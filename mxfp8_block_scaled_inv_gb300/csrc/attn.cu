@@ -67,8 +67,9 @@
 // tile that is cut leaves FP32 partial sums, which a second kernel joins in the
 // order of the keys.  Equal shares follow from the lengths on the device and stay
 // balanced in ragged batches.  Whole tiles do not: a chunk of 1216 tiles or more
-// together with a decode over many more keys leaves the latter's blocks, 5 us
-// each, to one CTA.
+// together with a decode over many more keys leaves the latter's blocks to one CTA
+// (64 heads, E4M3: 2048 tokens over 2048 keys and 8 tokens over 131072 keys each
+// take 3.2 ms in one call, 0.41 and 0.19 ms in two).
 //
 // What bounds it, and what it measured (GB300, rows of 512 columns, 64 heads;
 // products and bytes counted once):
