@@ -62,11 +62,21 @@ typedef enum mxq_status {
 #define MXQ_DEVERR_SLOT 0x4      /* a KV-cache slot at or beyond the number of cache rows */
 
 #define MXQ_DEVERR_LENGTH 0x8    /* a sequence length outside the block table's reach */
+#define MXQ_DEVERR_EXPERT 0x10   /* an expert index that is neither -1 nor below E */
 
 /* Cache element types of mxq_rope_kv_insert and mxq_attn. */
 #define MXQ_CACHE_E4M3 0 /* OCP E4M3 bytes with one per-tensor FP32 scale */
 #define MXQ_CACHE_BF16 1 /* BF16 */
 #define MXQ_CACHE_E2M1 2 /* 4 bits (mxq_attn only): written by mxq_rope_kv4_insert */
+
+/* Element types of the logits of mxq_route. */
+#define MXQ_LOGITS_F32 0
+#define MXQ_LOGITS_BF16 1
+
+/* Scores of mxq_route. */
+#define MXQ_SCORE_SOFTMAX 0      /* exp(l) / sum exp(l) */
+#define MXQ_SCORE_SIGMOID 1      /* 1 / (1 + exp(-l)) */
+#define MXQ_SCORE_SQRTSOFTPLUS 2 /* sqrt(log(1 + exp(l))) */
 
 /* Human-readable name of a status code.  Never NULL. */
 const char* mxq_status_string(int status);
@@ -393,6 +403,143 @@ int mxq_attn(const void* q_bf16, int64_t T, int32_t H, int32_t D, const int32_t*
              float sm_scale, void* out_bf16, float* lse, int32_t* err_flag, void* ws,
              size_t ws_bytes, mxq_stream_t stream);
 
+/*
+ * Residual addition, root-mean-square norm and quantisation in one pass: what
+ * lies between one projection and the next (the pages have no counterpart).
+ *
+ *  x_bf16        [T, D] BF16.
+ *  residual_bf16 [T, D] BF16, or NULL: nothing is added.
+ *  residual_out_bf16
+ *                [T, D] BF16 out: s = bf16(x + residual).  NULL if and only if
+ *                residual is NULL (then s = x).
+ *  weight_bf16   [D] BF16, or NULL: ones.
+ *  y_bf16        [T, D] BF16 out: y = bf16(s * weight / sqrt(m + eps)), m the
+ *                mean of the squares of the row's s, summed in FP32; or NULL.
+ *  q_e4m3, q_e8m0
+ *                [T, D] codes and [T, ceil(D/128)] scale bytes of y, as
+ *                mxq_inv_rope_group_quant with R = 0 makes them of that BF16
+ *                y (whether y is stored or not); or both NULL.
+ * At least one of y and the codes must be asked for.  residual_out may be
+ * residual or x itself, and y may be x or residual itself; other overlaps
+ * between an output and any other buffer return MXQ_ERR_SHAPE.  A row with an
+ * infinity or a NaN gives NaN values in y, and codes as
+ * mxq_inv_rope_group_quant gives them; a row whose sum of squares overflows
+ * FP32 gives zeros.
+ * D % 16 == 0, 16 <= D <= 65536; eps positive and finite.  T == 0 is a no-op.
+ * T >= 2^31 returns MXQ_ERR_UNSUPPORTED.
+ */
+int mxq_add_rms_norm(const void* x_bf16, const void* residual_bf16, void* residual_out_bf16,
+                     const void* weight_bf16, int64_t T, int32_t D, float eps, void* y_bf16,
+                     uint8_t* q_e4m3, uint8_t* q_e8m0, mxq_stream_t stream);
+
+/*
+ * Routing of tokens to experts (the pages have no counterpart).
+ *
+ *  logits    [T, E] FP32 (MXQ_LOGITS_F32) or BF16 (MXQ_LOGITS_BF16).  An
+ *            expert whose logit is -infinity or NaN is masked for the token: it
+ *            is not chosen and adds nothing to the softmax.  +infinity counts
+ *            as FP32's largest value.
+ *  bias      [E] FP32 or NULL (zeros).  Added to the scores for the choice
+ *            only.  -infinity or NaN masks the expert's choice (it still counts
+ *            in the softmax); values above 1e30 count as 1e30.
+ *  k         experts per token, 1 <= k <= 32, k <= E.
+ *  scoring   MXQ_SCORE_*: p_e = score of logit e; c_e = p_e + bias_e.
+ *  groups, topk_groups, group_top
+ *            the experts form `groups` groups of E/groups neighbours; a group's
+ *            value is the sum of its group_top (1 or 2) largest c (of one, where
+ *            only one of its experts is not masked), and only the topk_groups
+ *            groups of largest value take part.  groups == topk_groups: no
+ *            selection.  1 <= topk_groups <= groups <= 32, E % groups == 0.
+ *  renormalise, scale
+ *            w_j = scale * p_j, or with renormalise != 0
+ *            w_j = scale * p_j / (sum of the chosen p + 1e-20).
+ *  ids       [T, k] int32 out: the chosen experts, largest c first; -1 where
+ *            there are no more.
+ *  weights   [T, k] FP32 out: w_j; 0 beside an id of -1.
+ *
+ * Ties go to the lowest index.  Without a bias, experts are ordered by their
+ * logits; with one by c, and groups by their values, both compared as 64-bit
+ * sums of 64-bit scores.
+ * 1 <= E <= 1024.  T == 0 is a no-op.  T >= 2^31 returns MXQ_ERR_UNSUPPORTED.
+ */
+int mxq_route(const void* logits, int32_t logits_dtype, int64_t T, int32_t E, const float* bias,
+              int32_t k, int32_t scoring, int32_t groups, int32_t topk_groups, int32_t group_top,
+              int32_t renormalise, float scale, int32_t* ids, float* weights, mxq_stream_t stream);
+
+/* Size in bytes of B prepared 4-bit weights of N rows and K columns: 8704 for
+ * each 128 x 128 block, padded up.  Returns 0 for invalid sizes. */
+size_t mxq_w4_bytes(int32_t B, int32_t N, int32_t K);
+
+/*
+ * Load-time layout of 4-bit weights (OCP MXFP4 blocks) for mxq_linear_a8w4 and
+ * mxq_experts_a8w4 (the pages name an FP4 expert backend; they do not
+ * describe it).
+ *
+ *  w_e2m1   [B, N, K/2]: E2M1 codes, element 2i in the low and 2i+1 in the
+ *           high nibble of byte i (values 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ *           negatives).
+ *  w_e8m0   [B, N, K/32]: E8M0 bytes, one per 32 consecutive values; 0xFF
+ *           makes the products of its row NaN.
+ *  out      mxq_w4_bytes(B, N, K) bytes, 32-byte aligned.  For each matrix,
+ *           block of 128 rows and block of 128 columns, in that order: 128 rows
+ *           of 64 code bytes, then a 512-byte scale atom in which row
+ *           r = 32*j + i owns the four bytes at 16*i + 4*j, one per 32 columns.
+ *           Rows and columns past the matrix are codes 0 with byte 127.
+ * N >= 1, K % 32 == 0, 32 <= K <= 65536; w_e2m1 16-byte aligned.  Larger than
+ * 2^31 rows of 64 bytes in all returns MXQ_ERR_UNSUPPORTED.
+ */
+int mxq_prepare_w4(const uint8_t* w_e2m1, const uint8_t* w_e8m0, int32_t B, int32_t N, int32_t K,
+                   uint8_t* out, mxq_stream_t stream);
+
+/*
+ * Product of quantised activations with a 4-bit weight:
+ * out[t, n] = bf16_rne( sum_k A[t,k] * W[n,k] ).
+ *
+ *  a_e4m3, a_e8m0  [T, K] codes and [T, ceil(K/128)] scale bytes, as
+ *                  mxq_add_rms_norm and mxq_inv_rope_group_quant write them.
+ *  w4              mxq_prepare_w4(.., B = 1, N, K).
+ *  out_bf16        [T, N]; must not overlap an input.
+ * A = E4M3(code) * 2^(byte-127), W = E2M1(code) * 2^(byte-127); products are
+ * exact and summed in FP32 on the tensor cores.
+ * N % 16 == 0, N >= 16, K % 32 == 0, 32 <= K <= 65536.  T == 0 is a no-op.
+ * T >= 2^31 or N*K >= 2^37 returns MXQ_ERR_UNSUPPORTED.
+ */
+int mxq_linear_a8w4(const uint8_t* a_e4m3, const uint8_t* a_e8m0, const uint8_t* w4, void* out_bf16,
+                    int64_t T, int32_t N, int32_t K, mxq_stream_t stream);
+
+/* Workspace bytes mxq_experts_a8w4 needs (0 for invalid sizes). */
+size_t mxq_experts_workspace_bytes(int64_t T, int32_t k, int32_t E, int32_t I, int32_t N);
+
+/*
+ * Routed experts with 4-bit weights: out[t] = sum_j weights[t,j] * F_e(x_t),
+ * e = ids[t,j], with F_e(x) = W2_e * q8( silu(G_e x) * (U_e x) ), G_e and U_e
+ * the two halves of W13_e, silu(v) = v / (1 + exp(-v)) and q8 the group-128
+ * quantisation of mxq_inv_rope_group_quant (of the FP32 products).
+ *
+ *  a_e4m3, a_e8m0  [T, K] and [T, ceil(K/128)]: the quantised x.
+ *  ids             [T, k] int32, weights [T, k] FP32 (mxq_route's).  An id of
+ *                  -1 is no expert; any other id outside [0, E) is none either
+ *                  and sets MXQ_DEVERR_EXPERT.  An id may occur more than once.
+ *  w13             mxq_prepare_w4(.., B = 2*E, N = I, K) of a weight
+ *                  [E, 2, I, K]: gate rows, then up rows, of each expert.
+ *  w2              mxq_prepare_w4(.., B = E, N, K = I) of a weight [E, N, I].
+ *  out_bf16        [T, N]: FP32 sums over j in the order of the ids, rounded
+ *                  once.  A token without experts gets zeros.  Must not
+ *                  overlap an input or the workspace.
+ *  err_flag        optional int32 device word.
+ *  ws              mxq_experts_workspace_bytes() bytes, 16-byte aligned; calls
+ *                  that may run at the same time need distinct workspaces.
+ * Results do not depend on timing: atomics only choose where a row's sums are
+ * kept meanwhile.
+ * 1 <= k <= 32, 1 <= E <= 1024, K and I multiples of 32 up to 65536, N % 16 ==
+ * 0, N >= 16.  T == 0 is a no-op.  T*k >= 2^24, or a weight of more than 2^31
+ * rows of 64 bytes, returns MXQ_ERR_UNSUPPORTED.
+ */
+int mxq_experts_a8w4(const uint8_t* a_e4m3, const uint8_t* a_e8m0, const int32_t* ids,
+                     const float* weights, const uint8_t* w13, const uint8_t* w2, void* out_bf16,
+                     int64_t T, int32_t k, int32_t E, int32_t K, int32_t I, int32_t N,
+                     int32_t* err_flag, void* ws, size_t ws_bytes, mxq_stream_t stream);
+
 /* Size in bytes of the fixed device scratch array behind
  * mxq_linear_noalloc (4 MiB). */
 #define MXQ_NOALLOC_SCRATCH_BYTES (4u * 1024u * 1024u)
@@ -468,7 +615,7 @@ uint32_t mxq_debug_set_attn_wait(uint32_t ns);
 
 /*
  * Watchdog word of the GEMM kernels, of the streamed query copy of the
- * insertions and of mxq_attn on the current device (host call, synchronous).  Every
+ * insertions, of mxq_attn and of the 4-bit products on the current device (host call, synchronous).  Every
  * wait inside those kernels is bounded; a wait that runs out sets a bit here
  * and the kernel returns early instead of hanging.  0 means no wait ever ran
  * out.  With clear != 0 the word is reset after reading.

@@ -4,7 +4,7 @@ Argument marshalling only: every function here allocates output tensors with
 torch when the caller passes none, and forwards raw device pointers plus the
 current torch CUDA stream to the entry point of the same name in
 ``libmxq.so``, which checks sizes, alignment and missing pointers.  The
-attention and 4-bit cache functions also check what an address does not tell
+attention, norm, routing and 4-bit functions also check what an address does not tell
 (type, shape, device, contiguity); the others leave that to the caller.
 All arithmetic runs in the library's CUDA kernels; there is no other path.
 A missing or unbuilt library raises ``MxqLibraryError`` on first use.
@@ -26,6 +26,8 @@ __all__ = [
     "mxq_arch_supported",
     "mxq_version", "mxq_wo_a_workspace_bytes", "mxq_wo_a", "wo_a", "mxq_rope_kv_insert",
     "mxq_rope_kv4_insert", "mxq_kv4_gather", "mxq_attn_workspace_bytes", "mxq_attn",
+    "mxq_add_rms_norm", "mxq_route", "mxq_w4_bytes", "mxq_prepare_w4", "mxq_linear_a8w4",
+    "mxq_experts_workspace_bytes", "mxq_experts_a8w4",
     "mxq_debug_set_pair_limit", "mxq_debug_set_lazy_pairs", "mxq_debug_takeovers",
     "mxq_debug_set_attn_wait",
 ]
@@ -37,6 +39,10 @@ MXQ_DEVERR_POSITION = 0x1
 MXQ_DEVERR_SCALE = 0x2
 MXQ_DEVERR_SLOT = 0x4
 MXQ_DEVERR_LENGTH = 0x8
+MXQ_DEVERR_EXPERT = 0x10
+MXQ_LOGITS_F32 = 0
+MXQ_LOGITS_BF16 = 1
+MXQ_SCORES = {"softmax": 0, "sigmoid": 1, "sqrtsoftplus": 2}
 MXQ_CACHE_E4M3 = 0
 MXQ_CACHE_BF16 = 1
 MXQ_CACHE_E2M1 = 2
@@ -89,6 +95,15 @@ _SIGNATURES = {
     "mxq_attn_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32]),
     "mxq_attn": (ctypes.c_int, [_vp, _i64, _i32, _i32, _vp, _vp, _i32, _vp, _i32, _i32, _vp, _i64, _i32,
                                 _vp, _vp, _i32, _i32, ctypes.c_float, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "mxq_add_rms_norm": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i32, ctypes.c_float, _vp, _vp, _vp, _vp]),
+    "mxq_route": (ctypes.c_int, [_vp, _i32, _i64, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+                                 ctypes.c_float, _vp, _vp, _vp]),
+    "mxq_w4_bytes": (_sz, [_i32, _i32, _i32]),
+    "mxq_prepare_w4": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _vp, _vp]),
+    "mxq_linear_a8w4": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _vp]),
+    "mxq_experts_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i32]),
+    "mxq_experts_a8w4": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32,
+                                        _i32, _vp, _vp, _sz, _vp]),
     "mxq_wo_a": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32,
                                 _i32, _vp, _vp, _sz, _vp]),
 }
@@ -519,6 +534,175 @@ def mxq_attn(q, cache, block_table, seq_lens, q_start=None, page_size=64, window
     st = L.mxq_attn(pq, T, H, D, pstart, plen, B, pbt, max_pages, page_size, pcache, num_slots, dtype, pscale, psf,
                     window, sinks, D ** -0.5 if sm_scale is None else sm_scale, pout, plse, perr, pws, nws,
                     _stream_of(stream, q.device))
+    if st:
+        _check(fn, st)
+    return out
+
+
+def _same_device(fn, first, *others):
+    """Refuses tensors of different devices, and a device that is not the current one (the library launches there)."""
+    i = first.device.index
+    for t in others:
+        if t is not None and t.device.index != i:
+            raise MxqError(fn, 2, "tensors of different devices")
+    if i != torch.cuda.current_device():
+        raise MxqError(fn, 2, f"the tensors are on cuda:{i}, the current device is another")
+
+
+def mxq_add_rms_norm(x, weight=None, eps=1e-6, residual=None, residual_out=None, y=None, q=None, sc=None,
+                     want_y=True, want_codes=True, stream=None):
+    """RMS norm of x bf16 [..., D], or of s = bf16(x + residual), with `weight` bf16 [D] (None: ones).
+
+    Returns (s, y, codes, scales): s (None without a residual) in residual_out, by default a new tensor
+    (residual_out=residual adds in place); y bf16 [..., D] unless want_y is false; E4M3 codes uint8
+    [..., D] and E8M0 scales uint8 [..., ceil(D/128)] of y, as mxq_inv_rope_group_quant's, unless
+    want_codes is false.  y, q and sc, where given, receive them."""
+    fn = "mxq_add_rms_norm"
+    px = _tensor(fn, "x", x, torch.bfloat16)
+    shape = tuple(x.shape)
+    if not shape:
+        raise MxqError(fn, 2, "x has no dimension")
+    D = shape[-1]
+    T = x.numel() // D if D else 0
+    _same_device(fn, x, weight, residual, residual_out, y, q, sc)
+    pw = _tensor(fn, "weight", weight, torch.bfloat16, (D,))
+    pres = pout = None
+    if residual is not None:
+        pres = _tensor(fn, "residual", residual, torch.bfloat16, shape)
+        if residual_out is None:
+            residual_out = _empty(stream, shape, torch.bfloat16, x.device)
+        pout = _tensor(fn, "residual_out", residual_out, torch.bfloat16, shape)
+    elif residual_out is not None:
+        raise MxqError(fn, 2, "residual_out without residual")
+    if want_y and y is None:
+        y = _empty(stream, shape, torch.bfloat16, x.device)
+    py = _tensor(fn, "y", y, torch.bfloat16, shape)
+    pq = psc = None
+    if want_codes or q is not None or sc is not None:
+        sshape = (*shape[:-1], (D + 127) // 128)
+        if q is None:
+            q = _empty(stream, shape, torch.uint8, x.device)
+        if sc is None:
+            sc = _empty(stream, sshape, torch.uint8, x.device)
+        pq = _tensor(fn, "q", q, torch.uint8, shape)
+        psc = _tensor(fn, "sc", sc, torch.uint8, sshape)
+    st = lib().mxq_add_rms_norm(px, pres, pout, pw, T, D, eps, py, pq, psc, _stream_of(stream, x.device))
+    if st:
+        _check(fn, st)
+    return residual_out, y, q, sc
+
+
+def mxq_route(logits, k, scoring="softmax", bias=None, groups=1, topk_groups=1, group_top=2, renormalise=True,
+              scale=1.0, ids=None, weights=None, stream=None):
+    """The k experts of each token: logits float32 or bf16 [T, E] -> (ids int32 [T, k], weights float32 [T, k]).
+
+    scoring: "softmax", "sigmoid" or "sqrtsoftplus"; bias float32 [E] is added to the scores for the choice
+    only; with topk_groups < groups only the experts of the best groups (by the sum of their group_top best)
+    take part.  Ids run from the best down, -1 where masked logits (-infinity, NaN) leave none."""
+    fn = "mxq_route"
+    T, E = logits.shape
+    dtype = MXQ_LOGITS_BF16 if logits.dtype is torch.bfloat16 else MXQ_LOGITS_F32
+    pl = _tensor(fn, "logits", logits, torch.bfloat16 if dtype else torch.float32)
+    _same_device(fn, logits, bias, ids, weights)
+    if scoring not in MXQ_SCORES:
+        raise MxqError(fn, 4, f"scoring must be one of {sorted(MXQ_SCORES)}")
+    pb = _tensor(fn, "bias", bias, torch.float32, (E,))
+    if ids is None:
+        ids = _empty(stream, (T, max(k, 0)), torch.int32, logits.device)
+    if weights is None:
+        weights = _empty(stream, (T, max(k, 0)), torch.float32, logits.device)
+    pi = _tensor(fn, "ids", ids, torch.int32, (T, k))
+    pw = _tensor(fn, "weights", weights, torch.float32, (T, k))
+    st = lib().mxq_route(pl, dtype, T, E, pb, k, MXQ_SCORES[scoring], groups, topk_groups, group_top,
+                         1 if renormalise else 0, scale, pi, pw, _stream_of(stream, logits.device))
+    if st:
+        _check(fn, st)
+    return ids, weights
+
+
+def mxq_w4_bytes(B, N, K):
+    """Bytes of B prepared 4-bit weights [N, K] (0 for invalid sizes)."""
+    return lib().mxq_w4_bytes(B, N, K)
+
+
+def mxq_prepare_w4(w, w_e8m0, out=None, stream=None):
+    """Load-time layout of 4-bit weights: w uint8 [B, N, K/2] or [N, K/2] (E2M1 codes, two per byte) with
+    w_e8m0 uint8 [.., N, K/32] -> the bytes that mxq_linear_a8w4 (B = 1) and mxq_experts_a8w4 read."""
+    fn = "mxq_prepare_w4"
+    if w.dim() not in (2, 3):
+        raise MxqError(fn, 2, f"w has shape {tuple(w.shape)}, not [B, N, K/2] or [N, K/2]")
+    *lead, N, half = w.shape
+    B, K = (lead[0] if lead else 1), 2 * half
+    pw = _tensor(fn, "w", w, torch.uint8)
+    ps = _tensor(fn, "w_e8m0", w_e8m0, torch.uint8, (*lead, N, K // 32))
+    _same_device(fn, w, w_e8m0, out)
+    need = mxq_w4_bytes(B, N, K)
+    if out is None:
+        out = _empty(stream, need, torch.uint8, w.device)
+    po = _tensor(fn, "out", out, torch.uint8, (need,))
+    st = lib().mxq_prepare_w4(pw, ps, B, N, K, po, _stream_of(stream, w.device))
+    if st:
+        _check(fn, st)
+    return out
+
+
+def mxq_linear_a8w4(a, a_sf, w4, N, out=None, stream=None):
+    """a uint8 [T, K] E4M3 codes, a_sf uint8 [T, ceil(K/128)], w4 from mxq_prepare_w4 of a weight [N, K]
+    -> out bf16 [T, N]."""
+    fn = "mxq_linear_a8w4"
+    T, K = a.shape
+    pa = _tensor(fn, "a", a, torch.uint8)
+    ps = _tensor(fn, "a_sf", a_sf, torch.uint8, (T, (K + 127) // 128))
+    L = lib()
+    pw = _tensor(fn, "w4", w4, torch.uint8, (L.mxq_w4_bytes(1, N, K),))
+    _same_device(fn, a, a_sf, w4, out)
+    if out is None:
+        out = _empty(stream, (T, N), torch.bfloat16, a.device)
+    po = _tensor(fn, "out", out, torch.bfloat16, (T, N))
+    st = L.mxq_linear_a8w4(pa, ps, pw, po, T, N, K, _stream_of(stream, a.device))
+    if st:
+        _check(fn, st)
+    return out
+
+
+def mxq_experts_workspace_bytes(T, k, E, I, N):
+    """Workspace bytes of mxq_experts_a8w4 (0 for invalid sizes)."""
+    return lib().mxq_experts_workspace_bytes(T, k, E, I, N)
+
+
+def mxq_experts_a8w4(a, a_sf, ids, weights, w13, w2, I, N=None, out=None, ws=None, err_flag=None, stream=None):
+    """Routed experts: a uint8 [T, K] and a_sf uint8 [T, ceil(K/128)] (the quantised rows), ids int32 [T, k] and
+    weights float32 [T, k] (mxq_route's; -1: no expert), w13 from mxq_prepare_w4 of [2*E, I, K] (each expert's gate
+    rows, then its up rows), w2 from mxq_prepare_w4 of [E, N, I] -> out bf16 [T, N] (N: K unless given).
+    `ws` (mxq_experts_workspace_bytes) is allocated when not given; concurrent calls need distinct workspaces."""
+    fn = "mxq_experts_a8w4"
+    T, K = a.shape
+    k = ids.shape[-1]
+    if N is None:
+        N = K
+    pa = _tensor(fn, "a", a, torch.uint8)
+    ps = _tensor(fn, "a_sf", a_sf, torch.uint8, (T, (K + 127) // 128))
+    pi = _tensor(fn, "ids", ids, torch.int32, (T, k))
+    pwt = _tensor(fn, "weights", weights, torch.float32, (T, k))
+    L = lib()
+    one13, one2 = L.mxq_w4_bytes(2, I, K), L.mxq_w4_bytes(1, N, I)
+    if not one13 or not one2:
+        raise MxqError(fn, 2, f"no expert weights of K={K}, I={I}, N={N}: K and I must be multiples of 32")
+    E = w2.numel() // one2
+    p13 = _tensor(fn, "w13", w13, torch.uint8, (E * one13,))
+    p2 = _tensor(fn, "w2", w2, torch.uint8, (E * one2,))
+    _same_device(fn, a, a_sf, ids, weights, w13, w2, out, ws, err_flag)
+    if out is None:
+        out = _empty(stream, (T, N), torch.bfloat16, a.device)
+    po = _tensor(fn, "out", out, torch.bfloat16, (T, N))
+    if ws is None:
+        need = L.mxq_experts_workspace_bytes(T, k, E, I, N)
+        if need > 0:
+            ws = _empty(stream, need, torch.uint8, a.device)
+    pws, nws = (None, 0) if ws is None else (_tensor(fn, "ws", ws, torch.uint8), ws.numel())
+    perr = None if err_flag is None else _word(fn, "err_flag", err_flag, torch.int32)
+    st = L.mxq_experts_a8w4(pa, ps, pi, pwt, p13, p2, po, T, k, E, K, I, N, perr, pws, nws,
+                            _stream_of(stream, a.device))
     if st:
         _check(fn, st)
     return out

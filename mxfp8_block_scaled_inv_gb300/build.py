@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(HERE, "libmxq.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CU_SOURCES = ["quant.cu", "misc.cu", "bmm.cu", "linear_noalloc.cu", "kv_insert.cu", "kv4.cu",
-              "attn.cu"]
+              "attn.cu", "norm.cu", "route.cu", "w4.cu"]
 CXX_SOURCES = ["api.cpp"]
 
 

@@ -603,6 +603,208 @@ int mxq_attn(const void* q_bf16, int64_t T, int32_t H, int32_t D, const int32_t*
   return cuda_status(e, "attn launch");
 }
 
+int mxq_add_rms_norm(const void* x_bf16, const void* residual_bf16, void* residual_out_bf16,
+                     const void* weight_bf16, int64_t T, int32_t D, float eps, void* y_bf16,
+                     uint8_t* q_e4m3, uint8_t* q_e8m0, mxq_stream_t stream) {
+  if (T < 0 || D < 16 || D % 16 != 0)
+    return fail(MXQ_ERR_SHAPE, "need T >= 0, D >= 16, D %% 16 == 0 (T=%lld D=%d)", (long long)T, D);
+  if (D > 65536) return fail(MXQ_ERR_UNSUPPORTED, "D > 65536");
+  if (T >= ((int64_t)1 << 31)) return fail(MXQ_ERR_UNSUPPORTED, "T must be < 2^31");
+  if (!(eps > 0.0f) || !(eps - eps == 0.0f))
+    return fail(MXQ_ERR_SHAPE, "eps must be positive and finite");
+  if (T == 0) return ok();
+  if (!x_bf16) return fail(MXQ_ERR_NULL, "x is NULL");
+  if (!residual_bf16 != !residual_out_bf16)
+    return fail(MXQ_ERR_NULL, "residual and residual_out go together");
+  if (!q_e4m3 != !q_e8m0) return fail(MXQ_ERR_NULL, "q_e4m3 and q_e8m0 go together");
+  if (!y_bf16 && !q_e4m3) return fail(MXQ_ERR_NULL, "neither y nor the codes are asked for");
+  if (!aligned16(x_bf16) || !aligned16(residual_bf16) || !aligned16(residual_out_bf16) ||
+      !aligned16(weight_bf16) || !aligned16(y_bf16) || !aligned16(q_e4m3))
+    return fail(MXQ_ERR_ALIGN, "x, residual, residual_out, weight, y and q_e4m3 must be 16-byte aligned");
+  // A row's inputs are read before its outputs are written; rows run at once.
+  const size_t n = (size_t)T * D, sn = (size_t)T * (size_t)kgroups(D);
+  struct Buf {
+    const void* p;
+    size_t bytes;
+  };
+  const Buf in[3] = {{x_bf16, n * 2}, {residual_bf16, n * 2}, {weight_bf16, (size_t)D * 2}};
+  const Buf out[4] = {{residual_out_bf16, n * 2}, {y_bf16, n * 2}, {q_e4m3, n}, {q_e8m0, sn}};
+  for (int i = 0; i < 4; ++i) {
+    if (!out[i].p) continue;
+    for (int j = 0; j < 3; ++j) {
+      if (!in[j].p || (i < 2 && j < 2 && in[j].p == out[i].p)) continue;
+      if (overlap(out[i].p, out[i].bytes, in[j].p, in[j].bytes))
+        return fail(MXQ_ERR_SHAPE, "an output overlaps an input without being it");
+    }
+    for (int j = 0; j < i; ++j)
+      if (out[j].p && overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+        return fail(MXQ_ERR_SHAPE, "two outputs overlap");
+  }
+  int sms = 0;
+  if (int st = device_check(&sms)) return st;
+  return cuda_status(mxq::launch_add_rms_norm(x_bf16, residual_bf16, residual_out_bf16, weight_bf16, T,
+                                              D, eps, y_bf16, q_e4m3, q_e8m0,
+                                              static_cast<cudaStream_t>(stream)),
+                     "add_rms_norm launch");
+}
+
+int mxq_route(const void* logits, int32_t logits_dtype, int64_t T, int32_t E, const float* bias,
+              int32_t k, int32_t scoring, int32_t groups, int32_t topk_groups, int32_t group_top,
+              int32_t renormalise, float scale, int32_t* ids, float* weights, mxq_stream_t stream) {
+  if (T < 0 || E < 1 || k < 1 || k > E || groups < 1 || topk_groups < 1 || topk_groups > groups)
+    return fail(MXQ_ERR_SHAPE, "need T >= 0, 1 <= k <= E, 1 <= topk_groups <= groups (T=%lld E=%d "
+                               "k=%d groups=%d topk_groups=%d)",
+                (long long)T, E, k, groups, topk_groups);
+  if (E % groups != 0) return fail(MXQ_ERR_SHAPE, "E %% groups != 0 (E=%d groups=%d)", E, groups);
+  if (group_top != 1 && group_top != 2) return fail(MXQ_ERR_UNSUPPORTED, "group_top must be 1 or 2");
+  if (E > mxq::kMaxExperts || k > 32 || groups > 32)
+    return fail(MXQ_ERR_UNSUPPORTED, "need E <= %d, k <= 32, groups <= 32 (E=%d k=%d groups=%d)",
+                mxq::kMaxExperts, E, k, groups);
+  if (logits_dtype != MXQ_LOGITS_F32 && logits_dtype != MXQ_LOGITS_BF16)
+    return fail(MXQ_ERR_UNSUPPORTED, "logits_dtype must be MXQ_LOGITS_F32 or _BF16");
+  if (scoring != MXQ_SCORE_SOFTMAX && scoring != MXQ_SCORE_SIGMOID && scoring != MXQ_SCORE_SQRTSOFTPLUS)
+    return fail(MXQ_ERR_UNSUPPORTED, "scoring must be MXQ_SCORE_SOFTMAX, _SIGMOID or _SQRTSOFTPLUS");
+  if (!(scale - scale == 0.0f)) return fail(MXQ_ERR_SHAPE, "scale is not finite");
+  if (T >= ((int64_t)1 << 31)) return fail(MXQ_ERR_UNSUPPORTED, "T must be < 2^31");
+  if (T == 0) return ok();
+  if (!logits || !ids || !weights) return fail(MXQ_ERR_NULL, "logits, ids or weights is NULL");
+  if (!aligned16(logits)) return fail(MXQ_ERR_ALIGN, "logits must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(bias) | reinterpret_cast<uintptr_t>(ids) |
+       reinterpret_cast<uintptr_t>(weights)) & 3u)
+    return fail(MXQ_ERR_ALIGN, "bias, ids and weights must be 4-byte aligned");
+  const size_t in = (size_t)T * E * (logits_dtype == MXQ_LOGITS_F32 ? 4 : 2), out = (size_t)T * k * 4;
+  if (overlap(ids, out, weights, out) || overlap(ids, out, logits, in) || overlap(weights, out, logits, in) ||
+      (bias && (overlap(ids, out, bias, (size_t)E * 4) || overlap(weights, out, bias, (size_t)E * 4))))
+    return fail(MXQ_ERR_SHAPE, "ids or weights overlaps another buffer");
+  int sms = 0;
+  if (int st = device_check(&sms)) return st;
+  return cuda_status(mxq::launch_route(logits, logits_dtype == MXQ_LOGITS_BF16, T, E, bias, k, scoring,
+                                       groups, topk_groups, group_top, renormalise != 0, scale, ids,
+                                       weights, static_cast<cudaStream_t>(stream)),
+                     "route launch");
+}
+
+// Whether the coordinates of B prepared matrices fit a copy's 32 bits.
+static bool w4_fits(int64_t B, int32_t N, int32_t K) {
+  return mxq::w4_blocks(B, N, K) < ((int64_t)1 << 31) / (mxq::kW4BlockBytes / 64);
+}
+
+size_t mxq_w4_bytes(int32_t B, int32_t N, int32_t K) {
+  if (B < 1 || N < 1 || K < 32 || K % 32 != 0 || K > 65536 || !w4_fits(B, N, K)) return 0;
+  return (size_t)mxq::w4_blocks(B, N, K) * mxq::kW4BlockBytes;
+}
+
+int mxq_prepare_w4(const uint8_t* w_e2m1, const uint8_t* w_e8m0, int32_t B, int32_t N, int32_t K,
+                   uint8_t* out, mxq_stream_t stream) {
+  if (B < 1 || N < 1 || K < 32 || K % 32 != 0)
+    return fail(MXQ_ERR_SHAPE, "need B >= 1, N >= 1, K >= 32, K %% 32 == 0 (B=%d N=%d K=%d)", B, N, K);
+  if (K > 65536 || !w4_fits(B, N, K)) return fail(MXQ_ERR_UNSUPPORTED, "K or the weight is too large");
+  if (!w_e2m1 || !w_e8m0 || !out) return fail(MXQ_ERR_NULL, "w_e2m1, w_e8m0 or out is NULL");
+  if (!aligned16(w_e2m1) || (reinterpret_cast<uintptr_t>(out) & 31u))
+    return fail(MXQ_ERR_ALIGN, "w_e2m1 must be 16-byte aligned, out 32-byte");
+  const size_t bytes = mxq_w4_bytes(B, N, K), rows = (size_t)B * N;
+  if (overlap(out, bytes, w_e2m1, rows * (K / 2)) || overlap(out, bytes, w_e8m0, rows * (K / 32)))
+    return fail(MXQ_ERR_SHAPE, "out overlaps an input");
+  int sms = 0;
+  if (int st = device_check(&sms)) return st;
+  return cuda_status(mxq::launch_prepare_w4(w_e2m1, w_e8m0, B, N, K, out,
+                                            static_cast<cudaStream_t>(stream)),
+                     "prepare_w4 launch");
+}
+
+int mxq_linear_a8w4(const uint8_t* a_e4m3, const uint8_t* a_e8m0, const uint8_t* w4, void* out_bf16,
+                    int64_t T, int32_t N, int32_t K, mxq_stream_t stream) {
+  if (T < 0 || N < 16 || K < 32 || N % 16 != 0 || K % 32 != 0)
+    return fail(MXQ_ERR_SHAPE, "need T >= 0, N >= 16, K >= 32, N %% 16 == 0, K %% 32 == 0 (T=%lld "
+                               "N=%d K=%d)", (long long)T, N, K);
+  if (K > 65536 || T >= ((int64_t)1 << 31) || (int64_t)N * K >= ((int64_t)1 << 37))
+    return fail(MXQ_ERR_UNSUPPORTED, "need K <= 65536, T < 2^31, N*K < 2^37");
+  if ((T / 16 + 1) * (N / 128 + 1) >= ((int64_t)1 << 28))
+    return fail(MXQ_ERR_UNSUPPORTED, "T*N is too large");
+  if (T == 0) return ok();
+  if (!a_e4m3 || !a_e8m0 || !w4 || !out_bf16) return fail(MXQ_ERR_NULL, "a NULL operand pointer");
+  if (!aligned16(a_e4m3) || !aligned16(out_bf16) || (reinterpret_cast<uintptr_t>(w4) & 31u))
+    return fail(MXQ_ERR_ALIGN, "a_e4m3 and out must be 16-byte aligned, w4 32-byte");
+  const size_t out = (size_t)T * N * 2;
+  if (overlap(out_bf16, out, a_e4m3, (size_t)T * K) ||
+      overlap(out_bf16, out, a_e8m0, (size_t)T * (size_t)kgroups(K)) ||
+      overlap(out_bf16, out, w4, mxq_w4_bytes(1, N, K)))
+    return fail(MXQ_ERR_SHAPE, "out overlaps an input");
+  int sms = 0;
+  if (int st = device_check(&sms)) return st;
+  const char* why = nullptr;
+  cudaError_t e = mxq::launch_linear_a8w4(a_e4m3, a_e8m0, w4, out_bf16, T, N, K, sms,
+                                          static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess && why) return fail(MXQ_ERR_CUDA, "linear_a8w4: %s", why);
+  return cuda_status(e, "linear_a8w4 launch");
+}
+
+// Sizes of mxq_experts_a8w4; MXQ_OK when they are accepted.
+static int validate_experts_sizes(int64_t T, int32_t k, int32_t E, int32_t I, int32_t N) {
+  if (T < 0 || k < 1 || E < 1 || I < 32 || I % 32 != 0 || N < 16 || N % 16 != 0)
+    return fail(MXQ_ERR_SHAPE, "need T >= 0, k >= 1, E >= 1, I >= 32, I %% 32 == 0, N >= 16, "
+                               "N %% 16 == 0 (T=%lld k=%d E=%d I=%d N=%d)", (long long)T, k, E, I, N);
+  if (k > 32 || E > mxq::kMaxExperts || I > 65536)
+    return fail(MXQ_ERR_UNSUPPORTED, "need k <= 32, E <= %d, I <= 65536", mxq::kMaxExperts);
+  // T alone first, so that the product stays in 64 bits.
+  if (T >= ((int64_t)1 << 24) || T * k >= ((int64_t)1 << 24))
+    return fail(MXQ_ERR_UNSUPPORTED, "T*k must be < 2^24");
+  if (!w4_fits(E, N, I) || (T * k / 16 + E) * ((int64_t)(N > I ? N : I) / 128 + 1) >= ((int64_t)1 << 28) ||
+      T * (N / 8) >= ((int64_t)1 << 38))
+    return fail(MXQ_ERR_UNSUPPORTED, "the weights or T*k*N are too large");
+  return MXQ_OK;
+}
+
+size_t mxq_experts_workspace_bytes(int64_t T, int32_t k, int32_t E, int32_t I, int32_t N) {
+  if (validate_experts_sizes(T, k, E, I, N)) return 0;
+  return mxq::experts_layout(T, k, E, I, N).total;
+}
+
+int mxq_experts_a8w4(const uint8_t* a_e4m3, const uint8_t* a_e8m0, const int32_t* ids,
+                     const float* weights, const uint8_t* w13, const uint8_t* w2, void* out_bf16,
+                     int64_t T, int32_t k, int32_t E, int32_t K, int32_t I, int32_t N,
+                     int32_t* err_flag, void* ws, size_t ws_bytes, mxq_stream_t stream) {
+  if (int st = validate_experts_sizes(T, k, E, I, N)) return st;
+  if (K < 32 || K % 32 != 0) return fail(MXQ_ERR_SHAPE, "need K >= 32, K %% 32 == 0 (K=%d)", K);
+  if (K > 65536 || !w4_fits(2 * (int64_t)E, I, K))
+    return fail(MXQ_ERR_UNSUPPORTED, "K or w13 is too large");
+  if (T == 0) return ok();
+  if (!a_e4m3 || !a_e8m0 || !ids || !weights || !w13 || !w2 || !out_bf16)
+    return fail(MXQ_ERR_NULL, "a NULL operand pointer");
+  if (!aligned16(a_e4m3) || !aligned16(out_bf16) ||
+      ((reinterpret_cast<uintptr_t>(w13) | reinterpret_cast<uintptr_t>(w2)) & 31u))
+    return fail(MXQ_ERR_ALIGN, "a_e4m3 and out must be 16-byte aligned, w13 and w2 32-byte");
+  if ((reinterpret_cast<uintptr_t>(ids) | reinterpret_cast<uintptr_t>(weights) |
+       reinterpret_cast<uintptr_t>(err_flag)) & 3u)
+    return fail(MXQ_ERR_ALIGN, "ids, weights and err_flag must be 4-byte aligned");
+  const size_t need = mxq::experts_layout(T, k, E, I, N).total;
+  if (!ws || ws_bytes < need)
+    return fail(MXQ_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, ws_bytes);
+  if (!aligned16(ws)) return fail(MXQ_ERR_ALIGN, "workspace must be 16-byte aligned");
+  const struct {
+    const void* p;
+    size_t bytes;
+  } in[6] = {{a_e4m3, (size_t)T * K},
+             {a_e8m0, (size_t)T * (size_t)kgroups(K)},
+             {ids, (size_t)T * k * 4},
+             {weights, (size_t)T * k * 4},
+             {w13, (size_t)mxq::w4_blocks(2 * (int64_t)E, I, K) * mxq::kW4BlockBytes},
+             {w2, (size_t)mxq::w4_blocks(E, N, I) * mxq::kW4BlockBytes}};
+  const size_t out = (size_t)T * N * 2;
+  if (overlap(out_bf16, out, ws, need)) return fail(MXQ_ERR_SHAPE, "out overlaps the workspace");
+  for (const auto& b : in)
+    if (overlap(out_bf16, out, b.p, b.bytes) || overlap(ws, need, b.p, b.bytes))
+      return fail(MXQ_ERR_SHAPE, "out or the workspace overlaps an input");
+  int sms = 0;
+  if (int st = device_check(&sms)) return st;
+  const char* why = nullptr;
+  cudaError_t e = mxq::launch_experts_a8w4(a_e4m3, a_e8m0, ids, weights, w13, w2, out_bf16, T, k, E, K,
+                                           I, N, err_flag, ws, sms, static_cast<cudaStream_t>(stream),
+                                           &why);
+  if (e != cudaSuccess && why) return fail(MXQ_ERR_CUDA, "experts_a8w4: %s", why);
+  return cuda_status(e, "experts_a8w4 launch");
+}
+
 int mxq_debug_set_pair_limit(int pairs) { return mxq::set_pair_limit(pairs); }
 
 int mxq_debug_set_lazy_pairs(int from) {

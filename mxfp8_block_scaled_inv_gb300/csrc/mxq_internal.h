@@ -126,6 +126,39 @@ cudaError_t launch_attn(const AttnArgs& a, void* ws, cudaStream_t s, const char*
 // most); returns the previous bound.
 uint32_t set_attn_wait(uint32_t ns);
 
+// Residual addition, RMS norm and quantisation (see mxq_add_rms_norm).
+cudaError_t launch_add_rms_norm(const void* x, const void* res, void* res_out, const void* w,
+                                int64_t T, int D, float eps, void* y, uint8_t* q, uint8_t* sc,
+                                cudaStream_t s);
+
+// Routing (see mxq_route).
+cudaError_t launch_route(const void* logits, bool bf16, int64_t T, int E, const float* bias, int k,
+                         int scoring, int groups, int keep, int group_top, int renorm, float scale,
+                         int32_t* ids, float* weights, cudaStream_t s);
+
+// 4-bit weights: a block is 128 x 128 codes and their scale atom.
+constexpr int kW4BlockBytes = 128 * 64 + kSfAtomBytes;
+constexpr int kMaxExperts = 1024;
+inline int64_t w4_blocks(int64_t B, int64_t N, int64_t K) {
+  return B * ceil_div(N, 128) * ceil_div(K, kGroup);
+}
+cudaError_t launch_prepare_w4(const uint8_t* w, const uint8_t* sf, int64_t B, int N, int K,
+                              uint8_t* out, cudaStream_t s);
+cudaError_t launch_linear_a8w4(const uint8_t* a, const uint8_t* a_sf, const uint8_t* w, void* out,
+                               int64_t T, int N, int K, int num_sms, cudaStream_t s,
+                               const char** why);
+// Workspace of launch_experts_a8w4: the number of tiles, the tiles, the sorted
+// rows, the activation between the two products (codes and scales, by sorted
+// row) and the weighted partial results [T*k][N] FP32.
+struct ExpertsLayout {
+  size_t tiles, perm, h, h_sf, part, total;
+};
+ExpertsLayout experts_layout(int64_t T, int k, int E, int I, int N);
+cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int32_t* ids,
+                                const float* wt, const uint8_t* w13, const uint8_t* w2, void* out,
+                                int64_t T, int k, int E, int K, int I, int N, int32_t* err_flag,
+                                void* ws, int num_sms, cudaStream_t s, const char** why);
+
 // Caps the CTA pairs of the pair-form GEMM launches (0 = no cap); returns
 // the previous cap.
 int set_pair_limit(int pairs);
