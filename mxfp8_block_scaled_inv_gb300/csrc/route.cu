@@ -7,22 +7,29 @@
 // the lowest index; w_j = scale * p_j (/ (sum p + 1e-20)).
 //
 // A warp takes a token; lane i holds the experts [i * PER, (i + 1) * PER), so
-// that lane order is index order and the lowest lane of a tie is the lowest
-// index.  Each pick is one warp-wide integer maximum over order-preserving
-// keys, one ballot, and a new maximum in the lane that lost an expert.
+// that lane order is index order, the lowest lane of a tie holds the lowest
+// index, and groups are runs of lanes (their two best are found by a butterfly
+// over the run).  Each pick is one warp-wide integer maximum over
+// order-preserving keys, one ballot, and a new maximum in the lane that lost an
+// expert; lane j keeps pick j and computes its weight.
 //
 // What is chosen is defined by 64-bit scores: fp32 scores order two experts
-// wrongly where they differ by less than their rounding.  So the fp32 pass
-// also looks one pick past the last, and where two neighbouring picks (or the
-// last kept group and the next) are nearer than the rounding bounds below, and
-// not equal in logit and bias, the row is done again with 64-bit scores.
-// Without a bias the experts are ordered by their logits, which is exact.
+// wrongly where they differ by less than their rounding.  So one pick more than
+// asked for is made, and where two neighbouring picks are nearer than the
+// rounding bounds below, and not equal in logit and bias, picking goes on to the
+// next clear gap and the lanes order their picks by 64-bit values, one for each
+// lane.  Where that does not settle it (the edge between kept groups, a softmax
+// under a bias, no gap within 32) the row is done again in 64 bits altogether.
+// The device has next to no 64-bit units: the whole row in 64 bits costs as much
+// as some tens of rows.  Without a bias the experts are ordered by their logits,
+// which is exact.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "mxq.h"
 #include "mxq_internal.h"
 #include "mxq_ptx.cuh"
+#include "quant_common.cuh"
 
 namespace mxq {
 namespace {
@@ -36,7 +43,7 @@ struct RouteArgs {
   int32_t* ids;
   float* weights;
   int64_t T;
-  int E, k, scoring, groups, keep, group_top, renorm, per_group;
+  int E, k, scoring, groups, keep, group_top, renorm, per_group, vec, lanes;
   float scale;
 };
 
@@ -50,16 +57,30 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 }
 
 // score(l); for the softmax mx is the row's maximum and z the sum of
-// exp(l - mx).
-__device__ __forceinline__ float score_of(int scoring, float l, float mx, float z) {
-  if (scoring == MXQ_SCORE_SOFTMAX) return expf(l - mx) / z;
-  if (scoring == MXQ_SCORE_SIGMOID) return 1.0f / (1.0f + expf(-l));
+// exp(l - mx), in fp32 its reciprocal.
+__device__ __forceinline__ float score_of(int scoring, float l, float mx, float inv_z) {
+  if (scoring == MXQ_SCORE_SOFTMAX) return expf(l - mx) * inv_z;
+  if (scoring == MXQ_SCORE_SIGMOID) return __fdividef(1.0f, 1.0f + expf(-l));
   return sqrtf(fmaxf(l, 0.0f) + log1pf(expf(-fabsf(l))));
 }
 __device__ __forceinline__ double score_of(int scoring, double l, double mx, double z) {
   if (scoring == MXQ_SCORE_SOFTMAX) return exp(l - mx) / z;
   if (scoring == MXQ_SCORE_SIGMOID) return 1.0 / (1.0 + exp(-l));
   return sqrt(fmax(l, 0.0) + log1p(exp(-fabs(l))));
+}
+
+
+__device__ __forceinline__ float load_logit(const RouteArgs& a, int64_t t, int e, bool bf16) {
+  const size_t at = (size_t)t * (size_t)a.E + (size_t)e;
+  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[at])
+              : static_cast<const float*>(a.logits)[at];
+}
+// Masked logits (-infinity, NaN) read -infinity, +infinity the largest number.
+__device__ __forceinline__ float clean_logit(float l) {
+  return l > -INFINITY ? fminf(l, 3.4028234e38f) : -INFINITY;
+}
+__device__ __forceinline__ float clean_bias(float b) {
+  return b > -INFINITY ? fminf(b, 1e30f) : -INFINITY;
 }
 
 template <typename R>
@@ -78,167 +99,108 @@ __device__ __forceinline__ R warp_sum(R v) {
   return v;
 }
 
-// A value that compares below every candidate.
+// The two largest of two pairs, each in order.
 template <typename R>
-__device__ __forceinline__ R lowest();
-template <>
-__device__ __forceinline__ float lowest<float>() { return -INFINITY; }
-template <>
-__device__ __forceinline__ double lowest<double>() { return -(double)INFINITY; }
-
-// The lowest lane that holds the largest `v`; -1 if every lane holds lowest().
-__device__ __forceinline__ int best_lane(float v, float* top) {
-  const uint32_t key = v == -INFINITY ? 0u : key_of(v);
-  const uint32_t m = __reduce_max_sync(kAll, key);
-  *top = m == 0u ? -INFINITY : value_of(m);
-  return m == 0u ? -1 : __ffs(__ballot_sync(kAll, key == m)) - 1;
-}
-__device__ __forceinline__ int best_lane(double v, double* top) {
-  const double m = warp_max(v);
-  *top = m;
-  return m == -(double)INFINITY ? -1 : __ffs(__ballot_sync(kAll, v == m)) - 1;
+__device__ __forceinline__ void merge2(R& a1, R& a2, R b1, R b2) {
+  const R lo = b1 < a1 ? b1 : a1, hi2 = b2 > a2 ? b2 : a2;
+  a1 = b1 > a1 ? b1 : a1;
+  a2 = lo > hi2 ? lo : hi2;
 }
 
-// One row with scores of type R.  `l`: the lane's logits, `open`: bit i set
-// where expert i of the lane may be chosen, b: its biases.  Lane j < k returns
-// the j-th expert (-1: none) and its score.  True where fp32 cannot tell.
-template <int PER, typename R>
-__device__ bool route_row(const RouteArgs& a, const float (&l)[PER], const float (&b)[PER],
-                          uint32_t open, uint32_t summed, int lane, int* expert, R* score) {
-  const bool grouped = a.keep < a.groups;
-  const bool biased = a.bias != nullptr;
-  R mx = (R)0, z = (R)1;
+// A whole row with 64-bit scores, one expert after the other: lane j < k
+// returns the j-th expert (-1: none) and its score.
+__device__ __noinline__ void route_row_64(const RouteArgs& a, int64_t t, bool bf16, int lane,
+                                          int* expert, float* score) {
+  const double none = -(double)INFINITY;
+  const int rounds = (a.E + 31) / 32;
+  double mx = 0.0, z = 1.0;
   if (a.scoring == MXQ_SCORE_SOFTMAX) {
-    R m = lowest<R>();
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if ((summed >> i) & 1u) m = (R)l[i] > m ? (R)l[i] : m;
+    double m = none;
+    for (int e = lane; e < a.E; e += 32) m = fmax(m, (double)clean_logit(load_logit(a, t, e, bf16)));
     mx = warp_max(m);
-    R s = (R)0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if ((summed >> i) & 1u) s += exp((R)l[i] - mx);
+    double s = 0.0;
+    for (int e = lane; e < a.E; e += 32) {
+      const float l = clean_logit(load_logit(a, t, e, bf16));
+      if (l > -INFINITY) s += exp((double)l - mx);
+    }
     z = warp_sum(s);
   }
-  // What orders the experts; without a bias the logits do.
-  R c[PER];
-  R pmax = (R)0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    c[i] = lowest<R>();
-    if ((open >> i) & 1u) {
-      if (biased || grouped) {
-        const R p = score_of(a.scoring, (R)l[i], mx, z);
-        pmax = p > pmax ? p : pmax;
-        c[i] = p + (R)b[i];
-      } else {
-        c[i] = (R)l[i];
-      }
+  double c[kMaxExperts / 32];  // of the experts lane, lane + 32, ...
+  for (int i = 0; i < rounds; ++i) {
+    const int e = i * 32 + lane;
+    c[i] = none;
+    if (e < a.E) {
+      const float l = clean_logit(load_logit(a, t, e, bf16));
+      const float b = a.bias != nullptr ? clean_bias(a.bias[e]) : 0.0f;
+      if (l > -INFINITY && b > -INFINITY) c[i] = score_of(a.scoring, (double)l, mx, z) + (double)b;
     }
   }
-  // Bounds on the error of an fp32 difference: the scores' relative errors
-  // (exp, sums of up to 1024 terms, a quotient: below 2e-6 each), and the
-  // rounding of the sums with the bias.
-  const R slack = sizeof(R) == 4 && (biased || grouped) ? (R)4e-6f * warp_max(pmax) : (R)0;
-  bool unsure = false;
-  if (grouped) {
-    // The two best of each group; lane g keeps group g's value.
-    R mine = lowest<R>();
+  if (a.keep < a.groups) {
+    double mine = none;  // lane g: the value of group g
     for (int g = 0; g < a.groups; ++g) {
-      R a1 = lowest<R>(), a2 = lowest<R>();
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int e = lane * PER + i - g * a.per_group;
-        if (e >= 0 && e < a.per_group) {
-          const R v = c[i];
-          if (v > a1) {
-            a2 = a1;
-            a1 = v;
-          } else if (v > a2) {
-            a2 = v;
-          }
-        }
+      double a1 = none, a2 = none;
+      for (int i = 0; i < rounds; ++i) {
+        const int e = i * 32 + lane;
+        if (e < a.E && e / a.per_group == g) merge2(a1, a2, c[i], none);
       }
-#pragma unroll
       for (int m = 16; m > 0; m >>= 1) {
-        const R o1 = __shfl_xor_sync(kAll, a1, m), o2 = __shfl_xor_sync(kAll, a2, m);
-        const R lo = o1 < a1 ? o1 : a1, hi2 = o2 > a2 ? o2 : a2;
-        a1 = o1 > a1 ? o1 : a1;
-        a2 = lo > hi2 ? lo : hi2;
+        const double o1 = __shfl_xor_sync(kAll, a1, m), o2 = __shfl_xor_sync(kAll, a2, m);
+        merge2(a1, a2, o1, o2);
       }
-      const R v = a.group_top == 2 && a2 != lowest<R>() ? a1 + a2 : a1;
-      if (lane == g) mine = v;
+      if (lane == g) mine = a.group_top == 2 && a2 > none ? a1 + a2 : a1;
     }
-    uint32_t kept = 0;
-    R last = (R)0, top;
-    for (int j = 0; j < a.keep; ++j) {
-      const int w = best_lane(mine, &top);
-      if (w < 0) break;
-      last = top;
-      kept |= 1u << w;
-      if (lane == w) mine = lowest<R>();
+    int rank = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const double v = __shfl_sync(kAll, mine, g);
+      rank += v > mine || (v == mine && g < lane) ? 1 : 0;
     }
-    if (sizeof(R) == 4) {
-      const int w = best_lane(mine, &top);
-      if (w >= 0 && !(last - top > (R)2 * slack + (R)1e-6f * (fabs(last) + fabs(top)))) unsure = true;
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (!((kept >> ((lane * PER + i) / a.per_group)) & 1u)) c[i] = lowest<R>();
-    if (!biased) {
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (c[i] != lowest<R>()) c[i] = (R)l[i];
+    const uint32_t kept = __ballot_sync(kAll, lane < a.groups && rank < a.keep);
+    for (int i = 0; i < rounds; ++i) {
+      const int e = i * 32 + lane;
+      if (e < a.E && !((kept >> (e / a.per_group)) & 1u)) c[i] = none;
     }
   }
-  int eid = -1;
-  R prev = (R)0;
-  float prev_l = 0.0f, prev_b = 0.0f, my_l = 0.0f;
-  R best = lowest<R>();
-#pragma unroll
-  for (int i = 0; i < PER; ++i) best = c[i] > best ? c[i] : best;
-  const int picks = a.k + (sizeof(R) == 4 && biased ? 1 : 0);
-  for (int j = 0; j < picks; ++j) {
-    R top;
-    const int w = best_lane(best, &top);
-    if (w < 0) break;
-    int e = 0;
-    float wl = 0.0f, wb = 0.0f;
-    if (lane == w) {
-      R next = lowest<R>();
-      bool found = false;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        if (!found && c[i] == top) {
-          found = true;
-          e = lane * PER + i;
-          wl = l[i];
-          wb = b[i];
-          c[i] = lowest<R>();
-        }
-        next = c[i] > next ? c[i] : next;
+  if (a.bias == nullptr) {
+    for (int i = 0; i < rounds; ++i)
+      if (c[i] > none) c[i] = (double)clean_logit(load_logit(a, t, i * 32 + lane, bf16));
+  }
+  *expert = -1;
+  *score = 0.0f;
+  for (int j = 0; j < a.k; ++j) {
+    double best = none;
+    int at = 0;
+    for (int i = 0; i < rounds; ++i)
+      if (c[i] > best) {
+        best = c[i];
+        at = i;
       }
-      best = next;
-    }
-    e = __shfl_sync(kAll, e, w);
-    wl = __shfl_sync(kAll, wl, w);
-    if (sizeof(R) == 4 && biased) {
-      wb = __shfl_sync(kAll, wb, w);
-      if (j > 0 && !(prev - top > slack + (R)2.5e-7f * (fabs(prev) + fabs(top))) &&
-          !(wl == prev_l && wb == prev_b))
-        unsure = true;
-      prev = top;
-      prev_l = wl;
-      prev_b = wb;
-    }
-    if (lane == j && j < a.k) {
-      eid = e;
-      my_l = wl;
+    const double top = warp_max(best);
+    if (top == none) break;
+    // The lowest index among the lanes that hold it.
+    const int e = (int)__reduce_min_sync(kAll, best == top ? (uint32_t)(at * 32 + lane) : 0xffffffffu);
+    if (lane == (e & 31)) c[e >> 5] = none;
+    if (lane == j) *expert = e;
+  }
+  if (*expert >= 0)
+    *score = (float)score_of(a.scoring, (double)clean_logit(load_logit(a, t, *expert, bf16)), mx, z);
+}
+
+// Odd-even merge sort, largest first: passes of compare-exchanges at distance K
+// inside blocks of 2 P.
+template <int PER, int P, int K>
+__device__ __forceinline__ void sort_pass(uint32_t (&v)[PER]) {
+#pragma unroll
+  for (int x = 0; x + K < PER; ++x) {
+    if (x >= K % P && (x - K % P) % (2 * K) < K && x / (2 * P) == (x + K) / (2 * P)) {
+      const uint32_t hi = max(v[x], v[x + K]), lo = min(v[x], v[x + K]);
+      v[x] = hi;
+      v[x + K] = lo;
     }
   }
-  *expert = eid;
-  *score = eid >= 0 ? score_of(a.scoring, (R)my_l, mx, z) : (R)0;
-  return unsure;
+  if constexpr (K > 1)
+    sort_pass<PER, P, K / 2>(v);
+  else if constexpr (2 * P < PER)
+    sort_pass<PER, 2 * P, 2 * P>(v);
 }
 
 template <int PER, bool BF16>
@@ -248,39 +210,273 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= a.T) return;
-  float l[PER], b[PER];
-  uint32_t open = 0, summed = 0;
+  const bool biased = a.bias != nullptr, grouped = a.keep < a.groups;
+  const int e0 = lane * PER;
+  float l[PER];
+  if (PER >= (BF16 ? 8 : 4) && a.vec && e0 + PER <= a.E) {
+    if constexpr (BF16) {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.logits) +
+                                                        (size_t)t * (size_t)a.E + (size_t)e0);
+#pragma unroll
+      for (int i = 0; i + 8 <= PER; i += 8) {
+        float v[8];
+        unpack8(src[i / 8], v);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) l[i + q] = v[q];
+      }
+    } else {
+      const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) +
+                                                          (size_t)t * (size_t)a.E + (size_t)e0);
+#pragma unroll
+      for (int i = 0; i + 4 <= PER; i += 4) {
+        const float4 v = src[i / 4];
+        l[i] = v.x;
+        l[i + 1] = v.y;
+        l[i + 2] = v.z;
+        l[i + 3] = v.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) l[i] = e0 + i < a.E ? load_logit(a, t, e0 + i, BF16) : -INFINITY;
+  }
+  float b[PER];
+  if (biased && PER >= 4 && a.vec && e0 + PER <= a.E) {
+#pragma unroll
+    for (int i = 0; i + 4 <= PER; i += 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(a.bias + e0 + i));
+      b[i] = v.x;
+      b[i + 1] = v.y;
+      b[i + 2] = v.z;
+      b[i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) b[i] = biased && e0 + i < a.E ? __ldg(a.bias + e0 + i) : 0.0f;
+  }
+  // The row's largest logit bounds the scores; the softmax needs it anyway.
+  float mx = -INFINITY, inv_z = 1.0f, pmax = 1.0f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int e = lane * PER + i;
-    l[i] = -INFINITY;
-    b[i] = 0.0f;
-    if (e < a.E) {
-      const size_t at = (size_t)t * (size_t)a.E + (size_t)e;
-      l[i] = BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[at])
-                  : static_cast<const float*>(a.logits)[at];
-      if (a.bias != nullptr) b[i] = a.bias[e];
+    l[i] = clean_logit(l[i]);
+    mx = fmaxf(mx, l[i]);
+  }
+  if (a.scoring != MXQ_SCORE_SIGMOID) {
+    const uint32_t top = __reduce_max_sync(kAll, mx == -INFINITY ? 0u : key_of(mx));
+    mx = top == 0u ? 0.0f : value_of(top);
+    if (a.scoring == MXQ_SCORE_SOFTMAX) {
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) s += expf(l[i] - mx);
+      inv_z = 1.0f / warp_sum(s);
+      pmax = inv_z;
+    } else {
+      pmax = score_of(a.scoring, mx, 0.0f, 1.0f);
     }
-    if (l[i] > -INFINITY) {  // neither -infinity nor NaN
-      l[i] = fminf(l[i], 3.4028234e38f);
-      summed |= 1u << i;
-      if (b[i] > -INFINITY) {
-        b[i] = fminf(b[i], 1e30f);
-        open |= 1u << i;
+  }
+  // Bounds on the error of an fp32 difference of two scores, relative to the
+  // largest: exp 2 ulp, log1p 1 ulp, reciprocal 1 ulp, sums of up to 37 roundings.
+  const float slack = pmax * (a.scoring == MXQ_SCORE_SIGMOID   ? 1e-6f
+                              : a.scoring == MXQ_SCORE_SOFTMAX ? 6e-6f
+                                                               : 2.5e-6f);
+  bool whole = false;  // the row needs 64 bits altogether
+  uint32_t key[PER];   // order of the lane's experts; 0: not to be chosen
+  if (!biased && !grouped) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) key[i] = l[i] > -INFINITY ? key_of(l[i]) : 0u;
+  } else {
+    float c[PER];
+    // (One loop for each score: a choice inside it is made once for each value.)
+    if (a.scoring == MXQ_SCORE_SIGMOID) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) c[i] = score_of(MXQ_SCORE_SIGMOID, l[i], mx, inv_z);
+    } else if (a.scoring == MXQ_SCORE_SOFTMAX) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) c[i] = score_of(MXQ_SCORE_SOFTMAX, l[i], mx, inv_z);
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) c[i] = score_of(MXQ_SCORE_SQRTSOFTPLUS, l[i], mx, inv_z);
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) c[i] = l[i] > -INFINITY ? c[i] + clean_bias(b[i]) : -INFINITY;
+    uint32_t in = 0xffffffffu;  // bit i: the group of expert i is kept
+    if (grouped) {
+      float v = -INFINITY;  // a group's value, and whether it is this lane's to rank
+      int g;
+      if (a.lanes > 0) {
+        // A group is a run of 2^n lanes.
+        float a1 = -INFINITY, a2 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          a2 = fmaxf(a2, fminf(a1, c[i]));
+          a1 = fmaxf(a1, c[i]);
+        }
+        for (int m = 1; m < a.lanes; m <<= 1) {
+          const float o1 = __shfl_xor_sync(kAll, a1, m), o2 = __shfl_xor_sync(kAll, a2, m);
+          merge2(a1, a2, o1, o2);
+        }
+        v = a.group_top == 2 && a2 > -INFINITY ? a1 + a2 : a1;
+        g = lane / a.lanes;
+      } else {
+        // Groups that begin or end inside a lane: one after the other.
+        for (int q = 0; q < a.groups; ++q) {
+          float a1 = -INFINITY, a2 = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const int at = e0 + i - q * a.per_group;
+            if (at >= 0 && at < a.per_group) {
+              a2 = fmaxf(a2, fminf(a1, c[i]));
+              a1 = fmaxf(a1, c[i]);
+            }
+          }
+#pragma unroll
+          for (int m = 16; m > 0; m >>= 1) {
+            const float o1 = __shfl_xor_sync(kAll, a1, m), o2 = __shfl_xor_sync(kAll, a2, m);
+            merge2(a1, a2, o1, o2);
+          }
+          if (lane == q) v = a.group_top == 2 && a2 > -INFINITY ? a1 + a2 : a1;
+        }
+        g = lane;
+      }
+      const int step = a.lanes > 0 ? a.lanes : 1;
+      int rank = 0;
+      for (int q = 0; q < a.groups; ++q) {
+        const float o = __shfl_sync(kAll, v, q * step);
+        rank += o > v || (o == v && q < g) ? 1 : 0;
+      }
+      const bool kept = rank < a.keep;
+      const uint32_t vkey = g < a.groups && v > -INFINITY ? key_of(v) : 0u;
+      const uint32_t low = __reduce_min_sync(kAll, kept && g < a.groups ? vkey : 0xffffffffu);
+      const uint32_t high = __reduce_max_sync(kAll, kept ? 0u : vkey);
+      if (low != 0u && high != 0u) {
+        const float x = value_of(low), y = value_of(high);
+        whole = !(x - y > 2.0f * slack + 2.5e-7f * (fabsf(x) + fabsf(y)));
+      }
+      if (a.lanes > 0) {
+        in = kept ? 0xffffffffu : 0u;
+      } else {
+        const uint32_t mask = __ballot_sync(kAll, kept && lane < a.groups);
+        in = 0u;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) in |= ((mask >> (min(e0 + i, a.E - 1) / a.per_group)) & 1u) << i;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      key[i] = c[i] > -INFINITY && ((in >> i) & 1u) ? key_of(biased ? c[i] : l[i]) : 0u;
+  }
+  // Each lane's keys in order, so that a pick is their head; which expert the
+  // key belongs to is looked up for all picks at once afterwards.
+  uint32_t head[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) head[i] = key[i];
+  if constexpr (PER > 1) sort_pass<PER, 1, 1>(head);
+  int expert = -1, picks = 0;
+  uint32_t my_key = 0u;  // of this lane's pick, and the lane that holds it
+  int my_lane = 0;
+  float cj = 0.0f;
+  // Takes the next expert into lane `picks`; false where none is left.
+  auto pick = [&]() {
+    const uint32_t top = __reduce_max_sync(kAll, head[0]);
+    if (top == 0u) return false;
+    const int w = __ffs(__ballot_sync(kAll, head[0] == top)) - 1;
+    if (lane == w) {
+#pragma unroll
+      for (int i = 0; i + 1 < PER; ++i) head[i] = head[i + 1];
+      head[PER - 1] = 0u;
+    }
+    if (lane == picks) {
+      my_key = top;
+      my_lane = w;
+    }
+    ++picks;
+    return true;
+  };
+  auto look_up = [&]() {
+    cj = my_key != 0u ? value_of(my_key) : 0.0f;
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      m |= (__shfl_sync(kAll, key[i], my_lane) == my_key ? 1u : 0u) << i;
+    // Equal keys of one lane are picked one behind the other.
+    const uint32_t prev = __shfl_up_sync(kAll, my_key, 1);
+    const int prev_lane = __shfl_up_sync(kAll, my_lane, 1);
+    const bool again = lane > 0 && prev == my_key && prev_lane == my_lane && my_key != 0u;
+    const uint32_t run = __ballot_sync(kAll, again);
+    if (again) {
+      // Length of the run of `again` that ends here.
+      const int skip = __clz(~(run << (31 - lane)));
+      for (int i = 0; i < skip; ++i) m &= m - 1u;
+    }
+    expert = my_key != 0u ? my_lane * PER + __ffs(m) - 1 : -1;
+  };
+  const int want = biased ? a.k + 1 : a.k;
+  while (picks < want && picks < 32 && pick()) {
+  }
+  look_up();
+  int place = lane;  // of this lane's pick in the output
+  float lj = 0.0f, bj = 0.0f;
+  auto near = [&](float hi, float lo) {
+    return !(hi - lo > slack + 1.2e-7f * (fabsf(hi) + fabsf(lo)));
+  };
+  // Whether the last pick is too near to the best expert that is left.
+  auto near_rest = [&]() {
+    const uint32_t rest = __reduce_max_sync(kAll, head[0]);
+    return rest != 0u && near(__shfl_sync(kAll, cj, picks - 1), value_of(rest));
+  };
+  if (biased && picks == 32) whole |= near_rest();
+  if (biased && !whole) {
+    // Lane j > 0: whether picks j - 1 and j are too near to call.
+    auto near_prev = [&]() {
+      const float pc = __shfl_up_sync(kAll, cj, 1);
+      return lane > 0 && lane < picks && near(pc, cj);
+    };
+    auto fetch = [&]() {
+      if (expert >= 0) {
+        lj = clean_logit(load_logit(a, t, expert, BF16));
+        bj = clean_bias(a.bias[expert]);
+      }
+    };
+    if (__any_sync(kAll, near_prev())) {
+      fetch();
+      const float pl = __shfl_up_sync(kAll, lj, 1), pb = __shfl_up_sync(kAll, bj, 1);
+      if (__any_sync(kAll, near_prev() && !(pl == lj && pb == bj))) {
+        // On to the first clear gap behind the k-th pick.
+        while (picks > a.k && picks < 32 && __shfl_sync(kAll, (int)near_prev(), picks - 1) && pick()) {
+          look_up();
+        }
+        if (a.scoring == MXQ_SCORE_SOFTMAX ||
+            (__shfl_sync(kAll, (int)near_prev(), picks - 1) && near_rest())) {
+          whole = true;
+        } else {
+          fetch();
+          const double c = expert >= 0
+                               ? score_of(a.scoring, (double)lj, 0.0, 1.0) + (double)bj
+                               : -(double)INFINITY;
+          int rank = 0;
+          for (int j = 0; j < picks; ++j) {
+            const double o = __shfl_sync(kAll, c, j);
+            const int oe = __shfl_sync(kAll, expert, j);
+            rank += o > c || (o == c && oe < expert) ? 1 : 0;
+          }
+          place = expert >= 0 ? rank : 32;
+        }
       }
     }
   }
-  int e;
-  float p;
-  if (route_row<PER, float>(a, l, b, open, summed, lane, &e, &p)) {
-    double pd;
-    route_row<PER, double>(a, l, b, open, summed, lane, &e, &pd);
-    p = (float)pd;
+  float p = 0.0f;
+  if (whole) {
+    route_row_64(a, t, BF16, lane, &expert, &p);
+    place = lane;
+  } else if (expert >= 0) {
+    p = score_of(a.scoring, clean_logit(load_logit(a, t, expert, BF16)), mx, inv_z);
   }
+  if (place >= a.k) p = 0.0f;
   if (a.renorm) p = p / (warp_sum(p) + 1e-20f);
-  if (lane < a.k) {
-    a.ids[t * a.k + lane] = e;
-    a.weights[t * a.k + lane] = e >= 0 ? p * a.scale : 0.0f;
+  if (lane < a.k && expert < 0) place = lane;  // behind the last expert
+  if (place < a.k) {
+    a.ids[t * a.k + place] = expert;
+    a.weights[t * a.k + place] = expert >= 0 ? p * a.scale : 0.0f;
   }
 }
 
@@ -319,6 +515,12 @@ cudaError_t launch_route(const void* logits, bool bf16, int64_t T, int E, const 
   a.renorm = renorm;
   a.per_group = E / groups;
   a.scale = scale;
+  // 16-byte loads of a lane's logits; groups of whole lanes, a power of two of them.
+  a.vec = E % 8 == 0;
+  int per = 1;
+  while (per * 32 < E) per *= 2;
+  const int lanes = a.per_group % per == 0 ? a.per_group / per : 0;
+  a.lanes = lanes > 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
   if (E <= 32) return launch_per<1>(a, bf16, s);
   if (E <= 64) return launch_per<2>(a, bf16, s);
   if (E <= 128) return launch_per<4>(a, bf16, s);
