@@ -508,7 +508,8 @@ int mxq_linear_a8w4(const uint8_t* a_e4m3, const uint8_t* a_e8m0, const uint8_t*
                     int64_t T, int32_t N, int32_t K, mxq_stream_t stream);
 
 /* Workspace bytes mxq_experts_a8w4 needs (0 for invalid sizes). */
-size_t mxq_experts_workspace_bytes(int64_t T, int32_t k, int32_t E, int32_t I, int32_t N);
+size_t mxq_experts_workspace_bytes(int64_t T, int32_t k, int32_t E, int32_t K, int32_t I,
+                                   int32_t N);
 
 /*
  * Routed experts with 4-bit weights: out[t] = sum_j weights[t,j] * F_e(x_t),

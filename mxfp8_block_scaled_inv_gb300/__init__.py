@@ -101,7 +101,7 @@ _SIGNATURES = {
     "mxq_w4_bytes": (_sz, [_i32, _i32, _i32]),
     "mxq_prepare_w4": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _vp, _vp]),
     "mxq_linear_a8w4": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _vp]),
-    "mxq_experts_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i32]),
+    "mxq_experts_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i32, _i32]),
     "mxq_experts_a8w4": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32,
                                         _i32, _vp, _vp, _sz, _vp]),
     "mxq_wo_a": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32,
@@ -665,9 +665,9 @@ def mxq_linear_a8w4(a, a_sf, w4, N, out=None, stream=None):
     return out
 
 
-def mxq_experts_workspace_bytes(T, k, E, I, N):
+def mxq_experts_workspace_bytes(T, k, E, K, I, N):
     """Workspace bytes of mxq_experts_a8w4 (0 for invalid sizes)."""
-    return lib().mxq_experts_workspace_bytes(T, k, E, I, N)
+    return lib().mxq_experts_workspace_bytes(T, k, E, K, I, N)
 
 
 def mxq_experts_a8w4(a, a_sf, ids, weights, w13, w2, I, N=None, out=None, ws=None, err_flag=None, stream=None):
@@ -696,7 +696,7 @@ def mxq_experts_a8w4(a, a_sf, ids, weights, w13, w2, I, N=None, out=None, ws=Non
         out = _empty(stream, (T, N), torch.bfloat16, a.device)
     po = _tensor(fn, "out", out, torch.bfloat16, (T, N))
     if ws is None:
-        need = L.mxq_experts_workspace_bytes(T, k, E, I, N)
+        need = L.mxq_experts_workspace_bytes(T, k, E, K, I, N)
         if need > 0:
             ws = _empty(stream, need, torch.uint8, a.device)
     pws, nws = (None, 0) if ws is None else (_tensor(fn, "ws", ws, torch.uint8), ws.numel())

@@ -740,34 +740,32 @@ int mxq_linear_a8w4(const uint8_t* a_e4m3, const uint8_t* a_e8m0, const uint8_t*
 }
 
 // Sizes of mxq_experts_a8w4; MXQ_OK when they are accepted.
-static int validate_experts_sizes(int64_t T, int32_t k, int32_t E, int32_t I, int32_t N) {
-  if (T < 0 || k < 1 || E < 1 || I < 32 || I % 32 != 0 || N < 16 || N % 16 != 0)
-    return fail(MXQ_ERR_SHAPE, "need T >= 0, k >= 1, E >= 1, I >= 32, I %% 32 == 0, N >= 16, "
-                               "N %% 16 == 0 (T=%lld k=%d E=%d I=%d N=%d)", (long long)T, k, E, I, N);
-  if (k > 32 || E > mxq::kMaxExperts || I > 65536)
-    return fail(MXQ_ERR_UNSUPPORTED, "need k <= 32, E <= %d, I <= 65536", mxq::kMaxExperts);
+static int validate_experts_sizes(int64_t T, int32_t k, int32_t E, int32_t K, int32_t I, int32_t N) {
+  if (T < 0 || k < 1 || E < 1 || K < 32 || K % 32 != 0 || I < 32 || I % 32 != 0 || N < 16 || N % 16 != 0)
+    return fail(MXQ_ERR_SHAPE, "need T >= 0, k >= 1, E >= 1, K and I >= 32 and multiples of 32, N >= 16, "
+                               "N %% 16 == 0 (T=%lld k=%d E=%d K=%d I=%d N=%d)",
+                (long long)T, k, E, K, I, N);
+  if (k > 32 || E > mxq::kMaxExperts || I > 65536 || K > 65536)
+    return fail(MXQ_ERR_UNSUPPORTED, "need k <= 32, E <= %d, K and I <= 65536", mxq::kMaxExperts);
   // T alone first, so that the product stays in 64 bits.
   if (T >= ((int64_t)1 << 24) || T * k >= ((int64_t)1 << 24))
     return fail(MXQ_ERR_UNSUPPORTED, "T*k must be < 2^24");
-  if (!w4_fits(E, N, I) || (T * k / 16 + E) * ((int64_t)(N > I ? N : I) / 128 + 1) >= ((int64_t)1 << 28) ||
+  if (!w4_fits(E, N, I) || !w4_fits(2 * (int64_t)E, I, K) || (T * k / 16 + E) * ((int64_t)(N > I ? N : I) / 128 + 1) >= ((int64_t)1 << 28) ||
       T * (N / 8) >= ((int64_t)1 << 38))
     return fail(MXQ_ERR_UNSUPPORTED, "the weights or T*k*N are too large");
   return MXQ_OK;
 }
 
-size_t mxq_experts_workspace_bytes(int64_t T, int32_t k, int32_t E, int32_t I, int32_t N) {
-  if (validate_experts_sizes(T, k, E, I, N)) return 0;
-  return mxq::experts_layout(T, k, E, I, N).total;
+size_t mxq_experts_workspace_bytes(int64_t T, int32_t k, int32_t E, int32_t K, int32_t I, int32_t N) {
+  if (validate_experts_sizes(T, k, E, K, I, N)) return 0;
+  return mxq::experts_layout(T, k, E, K, I, N).total;
 }
 
 int mxq_experts_a8w4(const uint8_t* a_e4m3, const uint8_t* a_e8m0, const int32_t* ids,
                      const float* weights, const uint8_t* w13, const uint8_t* w2, void* out_bf16,
                      int64_t T, int32_t k, int32_t E, int32_t K, int32_t I, int32_t N,
                      int32_t* err_flag, void* ws, size_t ws_bytes, mxq_stream_t stream) {
-  if (int st = validate_experts_sizes(T, k, E, I, N)) return st;
-  if (K < 32 || K % 32 != 0) return fail(MXQ_ERR_SHAPE, "need K >= 32, K %% 32 == 0 (K=%d)", K);
-  if (K > 65536 || !w4_fits(2 * (int64_t)E, I, K))
-    return fail(MXQ_ERR_UNSUPPORTED, "K or w13 is too large");
+  if (int st = validate_experts_sizes(T, k, E, K, I, N)) return st;
   if (T == 0) return ok();
   if (!a_e4m3 || !a_e8m0 || !ids || !weights || !w13 || !w2 || !out_bf16)
     return fail(MXQ_ERR_NULL, "a NULL operand pointer");
@@ -777,7 +775,7 @@ int mxq_experts_a8w4(const uint8_t* a_e4m3, const uint8_t* a_e8m0, const int32_t
   if ((reinterpret_cast<uintptr_t>(ids) | reinterpret_cast<uintptr_t>(weights) |
        reinterpret_cast<uintptr_t>(err_flag)) & 3u)
     return fail(MXQ_ERR_ALIGN, "ids, weights and err_flag must be 4-byte aligned");
-  const size_t need = mxq::experts_layout(T, k, E, I, N).total;
+  const size_t need = mxq::experts_layout(T, k, E, K, I, N).total;
   if (!ws || ws_bytes < need)
     return fail(MXQ_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, ws_bytes);
   if (!aligned16(ws)) return fail(MXQ_ERR_ALIGN, "workspace must be 16-byte aligned");

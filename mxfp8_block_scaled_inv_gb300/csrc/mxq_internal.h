@@ -147,13 +147,13 @@ cudaError_t launch_prepare_w4(const uint8_t* w, const uint8_t* sf, int64_t B, in
 cudaError_t launch_linear_a8w4(const uint8_t* a, const uint8_t* a_sf, const uint8_t* w, void* out,
                                int64_t T, int N, int K, int num_sms, cudaStream_t s,
                                const char** why);
-// Workspace of launch_experts_a8w4: the number of tiles, the tiles, the sorted
-// rows, the activation between the two products (codes and scales, by sorted
+// Workspace of launch_experts_a8w4: the numbers of tiles and rows, the tiles, the
+// sorted rows' indices, the rows themselves (for large tiles), the activation between the two products (codes and scales, by sorted
 // row) and the weighted partial results [T*k][N] FP32.
 struct ExpertsLayout {
-  size_t tiles, perm, h, h_sf, part, total;
+  size_t tiles, perm, rows, h, h_sf, part, total;
 };
-ExpertsLayout experts_layout(int64_t T, int k, int E, int I, int N);
+ExpertsLayout experts_layout(int64_t T, int k, int E, int K, int I, int N);
 cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int32_t* ids,
                                 const float* wt, const uint8_t* w13, const uint8_t* w2, void* out,
                                 int64_t T, int k, int E, int K, int I, int N, int32_t* err_flag,

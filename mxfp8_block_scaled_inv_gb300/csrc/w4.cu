@@ -11,29 +11,38 @@
 // of two such products, q8 being the group-128 quantisation of the other
 // operators.
 //
-// Form: weight rows on the MMA's M axis (128), tokens on N (16..256), so that
+// Form: weight rows on the MMA's M axis (128), tokens on N (16..240), so that
 // few tokens cost no padding.  The prepared weight is a sequence of 8704-byte
 // blocks, each 128 rows x 128 columns of codes (64 bytes a row) and the
 // 512-byte scale atom of those rows: one block is one pipeline stage's operand,
-// and a CTA's blocks lie one behind the other in memory.  TMA unpacks the codes
-// on the way into shared memory (16 codes in 8 bytes of a 16-byte chunk, 128-byte
-// swizzle), where the MMA reads them; no instruction touches a weight.
+// and a row block's stages lie one behind the other in memory.  TMA unpacks the
+// codes on the way into shared memory (16 codes in 8 bytes of a 16-byte chunk,
+// 128-byte swizzle; the barrier counts the 8192 bytes read), where the MMA reads
+// them; no instruction touches a weight.
 //
-// A CTA makes one unit: 128 weight rows (gate and up rows: twice 128) x NT
-// tokens over its share of K.  Warp roles in the main loop:
-//   warp 0   copies: weight codes and scale atoms, and the token tile (dense and
-//            down products).
+// A unit is 128 weight rows (gate and up rows: twice 128) x a tile of tokens.
+// Warp roles:
+//   warp 0   copies: weight codes and scale atoms, and the token tile.
 //   warp 1   TMEM owner; per stage tcgen05.cp of the scale atoms, four
-//            tcgen05.mma (K = 32 each, scale byte k of each word), commit.
-//   warp 2   token scales, one byte per row and stage, into the scale atom; in
-//            the gate and up product also the token rows themselves, gathered
-//            by index four to an instruction.
-// Then all eight warps drain the accumulator to shared memory, row-contiguous
-// per token, and a half-warp takes a token's 128 values: 16-byte stores, and
-// the abs-max of a scale group is four shuffles.  Few units: the K range is
-// split over a cluster of up to 8 CTAs, each of which owns some of the tokens,
-// receives the partial sums for them through distributed shared memory and adds
-// them in rank order.
+//            tcgen05.mma for each 128 rows (K = 32 each, scale byte k of each
+//            word), commit.  The MMA's N is the tile's own number of tokens,
+//            rounded up to 16.
+//   warp 2   token scales, one byte per row and stage, into the scale atom; for
+//            few rows of the gate and up product also the token rows themselves,
+//            gathered by index four to an instruction.
+//   warp 3   idle (the epilogue's warps begin at a multiple of four).
+//   warps 4- epilogue: groups of four warps, one for each TMEM lane quadrant, drain
+//            16 tokens at a time to shared memory, row-contiguous per token; then
+//            a half-warp takes a token's 128 values: 16-byte stores, and the
+//            abs-max of a scale group is four shuffles.
+// Two forms:
+//   streaming  CTAs walk the units with a stride of the grid; copies run ahead
+//              across units and the accumulator is doubled where TMEM allows it,
+//              so that one unit's epilogue overlaps the next one's products.
+//   split      few units: one unit for each cluster of up to 8 CTAs, which share
+//              its K range.  Each CTA owns some of the tokens, receives the partial
+//              sums for them through distributed shared memory and adds them in
+//              rank order.
 //
 // Every wait is bounded in wall time; on expiry the kernel sets a watchdog bit,
 // stops issuing, waits for its own copies and MMAs, frees TMEM and returns.
@@ -59,16 +68,17 @@ namespace {
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kHintNs = 20;
 constexpr uint32_t kWdW4 = 0x80;  // a wait of these kernels ran out
-constexpr int kThreads = 256;
 
 constexpr int kCodeBytes = 128 * 64;    // a block's codes in memory
 constexpr int kTileBytes = 128 * 128;   // the same, unpacked in shared memory
 constexpr int kBlockBytes = kW4BlockBytes;
 static_assert(kBlockBytes == kCodeBytes + kSfAtomBytes, "block layout");
+constexpr int kChunk = 16;       // tokens drained at a time
+constexpr int kMaxTokens = 240;  // of a tile: two accumulators and scale columns fit TMEM
 
 enum Mode { kLinear = 0, kGateUp = 1, kDown = 2 };
 
-// Device-side plan of a routed call: which rows each tile holds.
+// Device-side plan of a routed call: which sorted rows each tile holds.
 struct Tile {
   int32_t expert, row0, count, pad;
 };
@@ -84,58 +94,108 @@ struct W4Args {
   uint8_t* out_sf;        // kGateUp: [rows][NG]
   uint32_t* wd;           // watchdog word
   int T, N, KG, KB, NB, NG, k;
+  int per_tile, n_tiles_host;  // kLinear: tokens of a tile, tiles
   int splits, kb_per_split;
 };
 
-template <int MODE, int NT, int NSTAGE, bool SPLIT>
+// Shape of an instance.  GATHER: the token rows are fetched by index.
+template <int MODE, int NT, bool SPLIT>
 struct Cfg {
   static constexpr int NA = MODE == kGateUp ? 2 : 1;
+  static constexpr bool GATHER = MODE == kGateUp && NT <= 32;
+  // Stages and CTAs per SM: as many bytes under way as shared memory allows; two
+  // CTAs where the tile is small, so that one streams while the other turns
+  // around.
+  static constexpr int CTAS = NA == 1 && NT <= 64 ? 2 : 1;
+  static constexpr int GROUPS = NT <= 64 || SPLIT ? 1 : 2;  // epilogue groups
+  static constexpr int THREADS = 128 + 128 * GROUPS;
   static constexpr int TOK_ATOMS = (NT + 127) / 128;
   static constexpr int TOK_TILE = NT * 128;
+  static constexpr int BOX_ROWS = NT > 128 ? 80 : NT;  // rows of a copy of tokens
+  static_assert(NT % BOX_ROWS == 0 && (BOX_ROWS % 8 == 0), "token copies");
+  static constexpr int STAGE = NA * (kTileBytes + kSfAtomBytes) + TOK_TILE + TOK_ATOMS * kSfAtomBytes;
+  // Sums on their way to the epilogue, fp32: a chunk [token][accumulator][row]
+  // for each group, or with a split K what the CTA receives,
+  // [rank][owned token][accumulator][row].
+  static constexpr int SUM_BYTES = SPLIT ? NA * NT * 512 : GROUPS * kChunk * NA * 512;
+  static constexpr int LIMIT = (CTAS == 2 ? 113 * 1024 : 232448) - 1024 - 512;
+  static constexpr int FIT = (LIMIT - SUM_BYTES) / STAGE;
+  static constexpr int NSTAGE = FIT > 10 ? 10 : FIT;
   static constexpr int OFF_W = 0;
   static constexpr int OFF_TOK = NSTAGE * NA * kTileBytes;
   static constexpr int OFF_WSF = OFF_TOK + NSTAGE * TOK_TILE;
   static constexpr int OFF_TSF = OFF_WSF + NSTAGE * NA * kSfAtomBytes;
-  static constexpr int PIPE = OFF_TSF + NSTAGE * TOK_ATOMS * kSfAtomBytes;
-  // Sums on their way to the epilogue, fp32 [token][weight row] for each
-  // accumulator: over the pipeline's buffers, or with a split K, whose other
-  // CTAs may still be in their main loop, in a place of its own.
-  static constexpr int SUM_BYTES = NA * NT * 128 * 4;
-  static constexpr int OFF_SUM = SPLIT ? PIPE : 0;
-  static constexpr int OFF_BAR = SPLIT ? PIPE + SUM_BYTES : (PIPE > SUM_BYTES ? PIPE : SUM_BYTES);
-  static constexpr int SMEM = OFF_BAR + (2 * NSTAGE + 1) * 8 + 32 + 1024;
+  static constexpr int OFF_SUM = OFF_TSF + NSTAGE * TOK_ATOMS * kSfAtomBytes;
+  static constexpr int OFF_BAR = OFF_SUM + SUM_BYTES;
+  static constexpr int SMEM = OFF_BAR + (2 * NSTAGE + 5) * 8 + 32 + 1024;
+  // TMEM: accumulators, then a ring of scale columns.  A copy of scales into
+  // columns that earlier MMAs read is ordered behind them (both are issued by one
+  // thread and execute in order); the ring keeps the copy from waiting.
   static constexpr int SF_COLS = 4 * NA + 4 * TOK_ATOMS;
-  static constexpr int TMEM_USED = NA * NT + NSTAGE * SF_COLS;
-  static constexpr int TMEM_COLS = TMEM_USED <= 32    ? 32
-                                   : TMEM_USED <= 64  ? 64
-                                   : TMEM_USED <= 128 ? 128
-                                   : TMEM_USED <= 256 ? 256
-                                                      : 512;
-  // kind::mxf8f6f4: A E2M1 (format 5), B E4M3 (0), N >> 3 at bits 17-22, UE8M0
-  // scales (bit 23), M >> 4 at bits 24-28; the scale byte of each operand is
-  // chosen at bits 4-5 (B) and 29-30 (A).
-  static constexpr uint32_t IDESC =
-      (5u << 7) | (1u << 23) | ((uint32_t)(NT >> 3) << 17) | ((128u >> 4) << 24);
-  // Two CTAs share an SM where their shared memory and TMEM allow it: one
-  // streams while the other starts or finishes.
-  static constexpr int CTAS_PER_SM = SMEM <= 113 * 1024 && TMEM_COLS <= 256 ? 2 : 1;
-  static_assert(TMEM_USED <= 512 && SMEM <= 232448, "budgets");
-  static_assert(NT % 16 == 0 && NT <= 256, "MMA N");
+  static constexpr int NBUF = !SPLIT && 2 * NA * NT + 2 * SF_COLS <= 512 / CTAS ? 2 : 1;
+  static constexpr int SF_RING = (512 / CTAS - NBUF * NA * NT) / SF_COLS >= 4 ? 4 : 2;
+  static constexpr int TMEM_USED = NBUF * NA * NT + SF_RING * SF_COLS;
+  static constexpr int TMEM_COLS = TMEM_USED <= 64 ? 64 : TMEM_USED <= 128 ? 128 : TMEM_USED <= 256 ? 256 : 512;
+  // kind::mxf8f6f4: A E2M1 (format 5), B E4M3 (0), UE8M0 scales (bit 23), M >> 4
+  // at bits 24-28; N >> 3 (bits 17-22) is the tile's; the scale byte of each
+  // operand is chosen at bits 4-5 (B) and 29-30 (A).
+  static constexpr uint32_t IDESC = (5u << 7) | (1u << 23) | ((128u >> 4) << 24);
+  static_assert(NSTAGE >= 3 && SMEM <= 232448 && TMEM_COLS * CTAS <= 512, "budgets");
+  static_assert(NT % kChunk == 0 && NT <= kMaxTokens && (!SPLIT || NT <= 32), "tokens of a tile");
 };
 
-template <int MODE, int NT, int NSTAGE, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, (Cfg<MODE, NT, NSTAGE, SPLIT>::CTAS_PER_SM))
+// silu(g) * u.
+__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// What a half-warp does with 128 sums of one token: v[a] are this lane's eight,
+// from weight row n on.  All 32 lanes call it (in: the token exists).
+template <int MODE, int NA>
+__device__ __forceinline__ void finish_token(const W4Args& p, const float (&v)[NA][8], int row, int n,
+                                             int rb, int sub, bool in) {
+  const bool store = in && n < p.N;
+  if constexpr (MODE == kLinear) {
+    if (store)
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (size_t)row * p.N + n) =
+          to_bf16x8(v[0]);
+  } else if constexpr (MODE == kGateUp) {
+    float h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = swiglu(v[0][e], v[NA - 1][e]);
+    uint32_t sb;
+    const float amax = half_warp_amax(h);
+    const uint2 codes = encode8(h, amax, &sb);
+    if (store) {
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + (size_t)row * p.N + n) = codes;
+      if (sub == 0) p.out_sf[(size_t)row * p.NG + rb] = (uint8_t)sb;
+    }
+  } else {
+    if (store) {
+      const int pair = p.perm[row];
+      const float w = p.wt[pair];
+      float* o = static_cast<float*>(p.out) + (size_t)pair * p.N + n;
+      *reinterpret_cast<float4*>(o) =
+          make_float4(v[0][0] * w, v[0][1] * w, v[0][2] * w, v[0][3] * w);
+      *reinterpret_cast<float4*>(o + 4) =
+          make_float4(v[0][4] * w, v[0][5] * w, v[0][6] * w, v[0][7] * w);
+    }
+  }
+}
+
+template <int MODE, int NT, bool SPLIT>
+__global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, SPLIT>::CTAS))
     w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
               const W4Args p) {
-  using C = Cfg<MODE, NT, NSTAGE, SPLIT>;
-  constexpr int NA = C::NA;
+  using C = Cfg<MODE, NT, SPLIT>;
+  constexpr int NA = C::NA, NSTAGE = C::NSTAGE;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + NSTAGE;
-  uint64_t* acc = empty + NSTAGE;
-  uint32_t* slot = reinterpret_cast<uint32_t*>(acc + 1);
+  uint64_t* acc_full = empty + NSTAGE;  // [2]
+  uint64_t* acc_empty = acc_full + 2;   // [2]
+  uint64_t* done = acc_empty + 2;       // every MMA has completed
+  uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(slot + 1);
   volatile int* issued = reinterpret_cast<volatile int*>(slot + 2);  // [0] warp 0, [1] warp 2
 
@@ -143,31 +203,38 @@ __global__ void __launch_bounds__(kThreads, (Cfg<MODE, NT, NSTAGE, SPLIT>::CTAS_
   ptx::griddep_launch_dependents();
 
   const int split = SPLIT ? (int)ptx::cluster_rank() : 0;
-  const uint32_t unit = blockIdx.x / (uint32_t)p.splits;
-  const int tile = (int)(unit / (uint32_t)p.NB);
-  const int rb = (int)(unit - (uint32_t)tile * (uint32_t)p.NB);
-  const int kb0 = split * p.kb_per_split;
-  const int nk = max(0, min(p.KB - kb0, p.kb_per_split));
-
-  int expert = 0, row0, count;
+  const int kb0 = SPLIT ? split * p.kb_per_split : 0;
+  const int nk = SPLIT ? max(0, min(p.KB - kb0, p.kb_per_split)) : p.KB;
+  const int u_first = SPLIT ? (int)(blockIdx.x / (uint32_t)p.splits) : (int)blockIdx.x;
+  int units;
   if constexpr (MODE == kLinear) {
-    row0 = tile * NT;
-    count = min(NT, p.T - row0);
+    units = p.n_tiles_host * p.NB;
     // The weight does not depend on what runs before: bring the first blocks
     // into L2 while that finishes.
-    if (warp == 0 && lane < NSTAGE && lane < nk)
-      ptx::prefetch_l2_bulk(p.w + ((size_t)rb * p.KB + kb0 + lane) * kBlockBytes, kBlockBytes);
+    if (warp == 0 && lane < NSTAGE && lane < nk && u_first < units)
+      ptx::prefetch_l2_bulk(p.w + ((size_t)(u_first % p.NB) * p.KB + kb0 + lane) * kBlockBytes,
+                            kBlockBytes);
     ptx::griddep_wait();
   } else {
     ptx::griddep_wait();
-    // The grid covers the most tiles that there can be; the whole cluster
-    // leaves where there is none.
-    if (tile >= *p.n_tiles) return;
-    const Tile t = p.tiles[tile];
-    expert = t.expert;
-    row0 = t.row0;
-    count = t.count;
+    units = *p.n_tiles * p.NB;
   }
+  // The grid covers the most units that there can be; a CTA (the whole cluster
+  // alike) without any leaves.
+  if (u_first >= units) return;
+  const int u_step = SPLIT ? units : (int)gridDim.x;  // split: one unit
+
+  auto tile_of = [&](int u) {
+    Tile t;
+    if constexpr (MODE == kLinear) {
+      t.expert = 0;
+      t.row0 = (u / p.NB) * p.per_tile;
+      t.count = min(p.per_tile, p.T - t.row0);
+    } else {
+      t = p.tiles[u / p.NB];
+    }
+    return t;
+  };
 
   if (threadIdx.x == 0) {
     ptx::prefetch_tmap(&tm_w);
@@ -176,7 +243,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<MODE, NT, NSTAGE, SPLIT>::CTAS_
       ptx::mbar_init(&full[i], 2);
       ptx::mbar_init(&empty[i], 1);
     }
-    ptx::mbar_init(acc, 1);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&acc_full[i], 1);
+      ptx::mbar_init(&acc_empty[i], 4 * C::GROUPS);
+    }
+    ptx::mbar_init(done, 1);
     ptx::fence_barrier_init();
     *abort_flag = 0;
     issued[0] = issued[1] = 0;
@@ -191,264 +262,296 @@ __global__ void __launch_bounds__(kThreads, (Cfg<MODE, NT, NSTAGE, SPLIT>::CTAS_
   const uint32_t tmem = *slot;
   if constexpr (SPLIT) ptx::cluster_arrive();  // this CTA's shared memory may be written
 
+  // A wait of a whole warp; false once it or another role has given up.
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu,
+                   !*abort_flag && ptx::mbar_wait_hint(bar, parity, kWaitNs, kHintNs)))
+      return true;
+    if (lane == 0 && !*abort_flag) atomicOr(p.wd, kWdW4);
+    *abort_flag = 1;
+    return false;
+  };
+
   if (warp == 0) {
     // ------------------------------------------------------------- copies
-    const uint32_t mat = MODE == kGateUp ? 2u * (uint32_t)expert + (lane & 1) : (uint32_t)expert;
-    const size_t blk0 = ((size_t)mat * p.NB + rb) * p.KB + kb0;
     int it = 0;
-    for (; it < nk; ++it) {
-      const int s = it % NSTAGE;
-      if (*abort_flag ||
-          !ptx::mbar_wait_hint(&empty[s], ((uint32_t)(it / NSTAGE) & 1u) ^ 1u, kWaitNs, kHintNs)) {
-        if (lane == 0 && !*abort_flag) atomicOr(p.wd, kWdW4);
-        *abort_flag = 1;
-        break;
+    bool ok = true;
+    for (int u = u_first; u < units && ok; u += u_step) {
+      const Tile t = tile_of(u);
+      const int boxes = (t.count + C::BOX_ROWS - 1) / C::BOX_ROWS;
+      const uint32_t bytes =
+          NA * kBlockBytes + (C::GATHER ? 0u : (uint32_t)(boxes * C::BOX_ROWS * 128));
+      const int mat = MODE == kGateUp ? 2 * t.expert + (lane & 1) : t.expert;
+      const size_t blk0 = ((size_t)mat * p.NB + u % p.NB) * p.KB + kb0;
+      for (int kk = 0; kk < nk; ++kk, ++it) {
+        const int s = it % NSTAGE;
+        ok = wait(&empty[s], ((uint32_t)(it / NSTAGE) & 1u) ^ 1u);
+        if (!ok) break;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&full[s], bytes);
+        __syncwarp();
+        // Lanes 0..NA-1: codes; 2..: their scale atoms; 4..: the tokens.
+        if (lane < NA) {
+          ptx::tma_load_2d(smem + C::OFF_W + (s * NA + lane) * kTileBytes, &tm_w, &full[s], 0,
+                           (int)((blk0 + kk) * (kBlockBytes / 64)));
+        } else if (lane >= 2 && lane < 2 + NA) {
+          ptx::bulk_load(smem + C::OFF_WSF + (s * NA + lane - 2) * kSfAtomBytes,
+                         p.w + (blk0 + kk) * kBlockBytes + kCodeBytes, kSfAtomBytes, &full[s]);
+        } else if (!C::GATHER && lane >= 4 && lane < 4 + boxes) {
+          const int b = lane - 4;
+          ptx::tma_load_2d(smem + C::OFF_TOK + s * C::TOK_TILE + b * C::BOX_ROWS * 128, &tm_a,
+                           &full[s], (kb0 + kk) * 128, t.row0 + b * C::BOX_ROWS);
+        }
+        __syncwarp();
       }
-      if (lane == 0)
-        ptx::mbar_arrive_expect_tx(&full[s], NA * kBlockBytes + (MODE == kGateUp ? 0 : C::TOK_TILE));
-      __syncwarp();
-      // Lanes 0..NA-1: codes; the next NA: their scale atoms; then the tokens.
-      if (lane < NA) {
-        ptx::tma_load_2d(smem + C::OFF_W + (s * NA + lane) * kTileBytes, &tm_w, &full[s], 0,
-                         (int)((blk0 + it) * (kBlockBytes / 64)));
-      } else if (lane >= 2 && lane < 2 + NA) {
-        ptx::bulk_load(smem + C::OFF_WSF + (s * NA + lane - 2) * kSfAtomBytes,
-                       p.w + (blk0 + it) * kBlockBytes + kCodeBytes, kSfAtomBytes, &full[s]);
-      } else if (MODE != kGateUp && lane == 4) {
-        ptx::tma_load_2d(smem + C::OFF_TOK + s * C::TOK_TILE, &tm_a, &full[s], (kb0 + it) * 128,
-                         row0);
-      }
-      __syncwarp();
     }
     if (lane == 0) issued[0] = it;
   } else if (warp == 2) {
     // ------------------------------------- token scales (and gathered rows)
-    // Lane i serves the rows i, i + 32, ...: their bytes of stage `it` are
-    // fetched one stage ahead.
-    constexpr int ROWS = NT >= 32 ? NT / 32 : 1;
-    const uint8_t* src[ROWS];
-    bool live[ROWS];
-#pragma unroll
-    for (int j = 0; j < ROWS; ++j) {
-      const int r = 32 * j + lane;
-      live[j] = r < count;
-      int row = row0 + (live[j] ? r : 0);
-      if constexpr (MODE == kGateUp) row = p.perm[row] / p.k;
-      src[j] = p.a_sf + (size_t)row * p.KG + kb0;
-    }
-    int g4[4];
-    if constexpr (MODE == kGateUp) {
-      // The rows past the tile's last repeat its first.
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 4 * lane + i;
-        g4[i] = p.perm[row0 + (r < count ? r : 0)] / p.k;
-      }
-    }
-    uint32_t next[ROWS];
-#pragma unroll
-    for (int j = 0; j < ROWS; ++j) next[j] = live[j] && nk > 0 ? src[j][0] : 127u;
-    int it = 0;
-    for (; it < nk; ++it) {
-      const int s = it % NSTAGE;
-      if (*abort_flag ||
-          !ptx::mbar_wait_hint(&empty[s], ((uint32_t)(it / NSTAGE) & 1u) ^ 1u, kWaitNs, kHintNs)) {
-        if (lane == 0 && !*abort_flag) atomicOr(p.wd, kWdW4);
-        *abort_flag = 1;
-        break;
-      }
-      if constexpr (MODE == kGateUp) {
-        if (lane == 0) ptx::mbar_expect_tx(&full[s], C::TOK_TILE);
-        __syncwarp();
-        for (int i = lane; i < NT / 4; i += 32)
-          ptx::tma_gather4(smem + C::OFF_TOK + s * C::TOK_TILE + i * 512, &tm_a, &full[s],
-                           (kb0 + it) * 128, g4[0], g4[1], g4[2], g4[3]);
-        static_assert(MODE != kGateUp || NT <= 128, "one gather per lane");
-      }
-      uint32_t cur[ROWS];
+    // Lane i serves the rows i, i + 32, ...: the byte of a stage is fetched one
+    // stage ahead, and the rows of a unit one unit ahead.
+    constexpr int ROWS = (NT + 31) / 32;
+    struct Rows {
+      const uint8_t* src[ROWS];
+      uint32_t byte[ROWS];  // of the first stage
+      int g4[4];
+      int count;
+    };
+    auto rows_of = [&](int u, Rows& r) {
+      const Tile t = tile_of(u);
+      r.count = t.count;
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) {
-        cur[j] = next[j] * 0x01010101u;
-        if (live[j] && it + 1 < nk) next[j] = src[j][it + 1];
+        // Rows past the last stand for it: their columns are not stored.
+        const int i = t.row0 + min(32 * j + lane, t.count - 1);
+        r.src[j] = p.a_sf + (size_t)(MODE == kGateUp ? p.perm[i] / p.k : i) * p.KG + kb0;
       }
-      uint8_t* atom = smem + C::OFF_TSF + s * C::TOK_ATOMS * kSfAtomBytes;
-      // Row r of an atom owns word (r % 128) / 32 of line r % 32.
+      if constexpr (C::GATHER) {
 #pragma unroll
-      for (int j = 0; j < ROWS; ++j)
-        *reinterpret_cast<uint32_t*>(atom + (j >> 2) * kSfAtomBytes + lane * 16 + (j & 3) * 4) =
-            cur[j];
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&full[s]);
+        for (int i = 0; i < 4; ++i)
+          r.g4[i] = p.perm[t.row0 + min(4 * lane + i, t.count - 1)] / p.k;
+      }
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) r.byte[j] = nk > 0 ? r.src[j][0] : 127u;
+    };
+    Rows now, then;
+    rows_of(u_first, now);
+    int it = 0;
+    bool ok = true;
+    for (int u = u_first; u < units && ok; u += u_step) {
+      if (u + u_step < units) rows_of(u + u_step, then);
+      const int gathers = (now.count + 3) / 4;
+      for (int kk = 0; kk < nk; ++kk, ++it) {
+        const int s = it % NSTAGE;
+        ok = wait(&empty[s], ((uint32_t)(it / NSTAGE) & 1u) ^ 1u);
+        if (!ok) break;
+        if constexpr (C::GATHER) {
+          if (lane == 0) ptx::mbar_expect_tx(&full[s], (uint32_t)gathers * 512u);
+          __syncwarp();
+          if (lane < gathers)
+            ptx::tma_gather4(smem + C::OFF_TOK + s * C::TOK_TILE + lane * 512, &tm_a, &full[s],
+                             (kb0 + kk) * 128, now.g4[0], now.g4[1], now.g4[2], now.g4[3]);
+        }
+        // Row r of an atom owns word (r % 128) / 32 of line r % 32; a group's
+        // byte stands for its four blocks of 32.
+        uint8_t* atom = smem + C::OFF_TSF + s * C::TOK_ATOMS * kSfAtomBytes;
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) {
+          const uint32_t w = now.byte[j] * 0x01010101u;
+          if (kk + 1 < nk) now.byte[j] = now.src[j][kk + 1];
+          *reinterpret_cast<uint32_t*>(atom + (j >> 2) * kSfAtomBytes + lane * 16 + (j & 3) * 4) = w;
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&full[s]);
+      }
+      now = then;
     }
     if (lane == 0) issued[1] = it;
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA
-    for (int it = 0; it < nk; ++it) {
-      const int s = it % NSTAGE;
-      if (*abort_flag ||
-          !ptx::mbar_wait_hint(&full[s], (uint32_t)(it / NSTAGE) & 1u, kWaitNs, kHintNs)) {
-        if (lane == 0 && !*abort_flag) atomicOr(p.wd, kWdW4);
-        *abort_flag = 1;
-        break;
-      }
+    int it = 0, n = 0;
+    bool ok = true;
+    for (int u = u_first; u < units && ok; u += u_step, ++n) {
+      const int buf = C::NBUF == 2 ? n & 1 : 0;
+      const uint32_t idesc = C::IDESC | ((uint32_t)((tile_of(u).count + 15) / 16 * 2) << 17);
+      const uint32_t d = tmem + buf * NA * NT;
+      ok = wait(&acc_empty[buf], ((uint32_t)(n / C::NBUF) & 1u) ^ 1u);
+      if (!ok) break;
       ptx::tc_fence_after();
-      if (lane == 0) {
-        const uint32_t sf = tmem + NA * NT + s * C::SF_COLS;
-        const uint32_t tok_sf = sf + 4 * NA;
-        const uint64_t bdesc = ptx::smem_desc(
-            ptx::smem_u32(smem + C::OFF_TOK + s * C::TOK_TILE), 16, 1024, ptx::kSwizzle128B);
+      for (int kk = 0; kk < nk; ++kk, ++it) {
+        const int s = it % NSTAGE;
+        ok = wait(&full[s], (uint32_t)(it / NSTAGE) & 1u);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (lane == 0) {
+          const uint32_t sf = tmem + C::NBUF * NA * NT + (it % C::SF_RING) * C::SF_COLS;
+          const uint32_t tok_sf = sf + 4 * NA;
+          const uint64_t bdesc = ptx::smem_desc(
+              ptx::smem_u32(smem + C::OFF_TOK + s * C::TOK_TILE), 16, 1024, ptx::kSwizzle128B);
 #pragma unroll
-        for (int a = 0; a < NA; ++a)
-          ptx::tmem_cp_32x128b_x4(
-              sf + 4 * a, ptx::smem_desc(ptx::smem_u32(smem + C::OFF_WSF + (s * NA + a) * kSfAtomBytes),
-                                         128, 128, ptx::kSwizzleNone));
+          for (int a = 0; a < NA; ++a)
+            ptx::tmem_cp_32x128b_x4(
+                sf + 4 * a,
+                ptx::smem_desc(ptx::smem_u32(smem + C::OFF_WSF + (s * NA + a) * kSfAtomBytes), 128,
+                               128, ptx::kSwizzleNone));
 #pragma unroll
-        for (int a = 0; a < C::TOK_ATOMS; ++a)
-          ptx::tmem_cp_32x128b_x4(
-              tok_sf + 4 * a,
-              ptx::smem_desc(ptx::smem_u32(smem + C::OFF_TSF + (s * C::TOK_ATOMS + a) * kSfAtomBytes),
-                             128, 128, ptx::kSwizzleNone));
+          for (int a = 0; a < C::TOK_ATOMS; ++a)
+            ptx::tmem_cp_32x128b_x4(
+                tok_sf + 4 * a,
+                ptx::smem_desc(
+                    ptx::smem_u32(smem + C::OFF_TSF + (s * C::TOK_ATOMS + a) * kSfAtomBytes), 128,
+                    128, ptx::kSwizzleNone));
 #pragma unroll
-        for (int a = 0; a < NA; ++a) {
-          const uint64_t adesc =
-              ptx::smem_desc(ptx::smem_u32(smem + C::OFF_W + (s * NA + a) * kTileBytes), 16, 1024,
-                             ptx::kSwizzle128B);
+          for (int a = 0; a < NA; ++a) {
+            const uint64_t adesc =
+                ptx::smem_desc(ptx::smem_u32(smem + C::OFF_W + (s * NA + a) * kTileBytes), 16, 1024,
+                               ptx::kSwizzle128B);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            ptx::mma_mxf8(tmem + a * NT, adesc + 2 * k, bdesc + 2 * k,
-                          C::IDESC | ((uint32_t)k << 29) | ((uint32_t)k << 4), sf + 4 * a, tok_sf,
-                          (it > 0 || k > 0) ? 1u : 0u);
+            for (int k = 0; k < 4; ++k)
+              ptx::mma_mxf8(d + a * NT, adesc + 2 * k, bdesc + 2 * k,
+                            idesc | ((uint32_t)k << 29) | ((uint32_t)k << 4), sf + 4 * a, tok_sf,
+                            (kk > 0 || k > 0) ? 1u : 0u);
+          }
+          ptx::tc_commit(&empty[s]);
         }
-        ptx::tc_commit(&empty[s]);
+        __syncwarp();
       }
+      if (lane == 0) ptx::tc_commit(&acc_full[buf]);
       __syncwarp();
     }
-    // Everything issued completes before the accumulator is read or freed.
-    if (lane == 0) ptx::tc_commit(acc);
+    if (lane == 0) ptx::tc_commit(done);
   }
   __syncwarp();
 
   // ------------------------------------------------------------- epilogue
-  if (!ptx::mbar_wait(acc, 0, 2 * kWaitNs)) {
-    if (lane == 0) atomicOr(p.wd, kWdW4);
-    *abort_flag = 1;
-  }
-  __syncwarp();
-  ptx::tc_fence_after();
-  if constexpr (SPLIT) ptx::cluster_wait();  // every CTA of the cluster has begun
-  {
-    // Warp w drains lanes 32 (w % 4)... of half the columns.
-    constexpr int CH = NA * NT / 2;
-    constexpr int STEP = CH >= 32 ? 32 : CH;
-    constexpr int TOK_OWN = NT / 8;  // smallest share of tokens; see below
-    static_assert(TOK_OWN >= 2 && CH % STEP == 0 && STEP % 8 == 0, "drain");
-    const int row = (warp & 3) * 32 + lane;
-    const uint32_t t0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (warp >> 2) * CH;
-    float* sum = reinterpret_cast<float*>(smem + C::OFF_SUM);
-    const int own = NT / p.splits;  // tokens owned by each CTA
+  const int sub = lane & 15;
+  float* sums = reinterpret_cast<float*>(smem + C::OFF_SUM);
+  if constexpr (!SPLIT) {
+    if (warp >= 4) {
+      const int q = warp & 3, group = (warp - 4) >> 2;
+      float* sum = sums + group * kChunk * NA * 128;
+      int n = 0;
+      for (int u = u_first; u < units; u += u_step, ++n) {
+        const int buf = C::NBUF == 2 ? n & 1 : 0;
+        const Tile t = tile_of(u);
+        const int rb = u % p.NB;
+        const int chunks = (t.count + kChunk - 1) / kChunk;
+        const bool ok = wait(&acc_full[buf], (uint32_t)(n / C::NBUF) & 1u);
+        if (!ptx::named_sync_and(1 + group, 128, ok)) break;  // the group goes on, or leaves, together
+        ptx::tc_fence_after();
+        const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + buf * NA * NT;
+        for (int c = group; c < chunks; c += C::GROUPS) {
+          uint32_t v[NA][kChunk];
 #pragma unroll
-    for (int c = 0; c < CH; c += STEP) {
-      uint32_t v[STEP];
-      if constexpr (STEP == 32) {
-        ptx::tmem_ld_32x32b_x32(t0 + c, v);
-      } else {
+          for (int a = 0; a < NA; ++a) ptx::tmem_ld_32x32b_x16(t0 + a * NT + c * kChunk, v[a]);
+          ptx::tmem_ld_wait();
+          if (c + C::GROUPS >= chunks) {  // this group's last: the accumulator is free
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&acc_empty[buf]);
+          }
 #pragma unroll
-        for (int i = 0; i < STEP; i += 8) ptx::tmem_ld_32x32b_x8(t0 + c + i, v + i);
-      }
-      ptx::tmem_ld_wait();
-      const int col = (warp >> 2) * CH + c;
+          for (int i = 0; i < kChunk; ++i)
 #pragma unroll
-      for (int i = 0; i < STEP; ++i) {
-        const int a = (col + i) / NT, tok = (col + i) % NT;
-        const float f = nk > 0 ? __uint_as_float(v[i]) : 0.0f;
-        if constexpr (SPLIT) {
-          // [rank][owned token][accumulator][row] at the token's owner.
-          const int o = tok / own, tl = tok - o * own;
-          const uint32_t at =
-              ptx::smem_u32(sum + ((split * own + tl) * NA + a) * 128 + row);
-          ptx::st_shared_cluster_f32(ptx::map_shared_rank(at, (uint32_t)o), f);
-        } else {
-          sum[(tok * NA + a) * 128 + row] = f;
+            for (int a = 0; a < NA; ++a)
+              sum[(i * NA + a) * 128 + q * 32 + lane] = __uint_as_float(v[a][i]);
+          ptx::named_sync(1 + group, 128);
+#pragma unroll
+          for (int j = 0; j < kChunk; j += 8) {
+            const int i = j + 2 * q + (lane >> 4);
+            const int tok = c * kChunk + i;
+            float w[NA][8];
+#pragma unroll
+            for (int a = 0; a < NA; ++a) {
+              const float* at = sum + (i * NA + a) * 128 + 8 * sub;
+              *reinterpret_cast<float4*>(&w[a][0]) = *reinterpret_cast<const float4*>(at);
+              *reinterpret_cast<float4*>(&w[a][4]) = *reinterpret_cast<const float4*>(at + 4);
+            }
+            finish_token<MODE, NA>(p, w, t.row0 + tok, rb * 128 + 8 * sub, rb, sub, tok < t.count);
+          }
+          ptx::named_sync(1 + group, 128);
+        }
+        if (group >= chunks) {  // no chunk for this group
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&acc_empty[buf]);
         }
       }
     }
-  }
-  ptx::tc_fence_before();
-  if constexpr (SPLIT)
-    ptx::cluster_sync();  // all partial sums have arrived; nobody writes here again
-  else
     __syncthreads();
-  if (warp == 1) {
-    ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, C::TMEM_COLS);
-  }
-  if (*abort_flag) {
-    __syncthreads();
-    // Copies in flight land before the CTA's shared memory is given up: raise
-    // each issued stage's missing arrivals, then wait for its phase.
-    if (threadIdx.x == 0) {
-      const int i0 = issued[0], i2 = issued[1];
-      for (int i = min(i0, i2); i < max(i0, i2); ++i) ptx::mbar_arrive(&full[i % NSTAGE]);
-      for (int i = max(0, max(i0, i2) - NSTAGE); i < max(i0, i2); ++i)
-        ptx::mbar_wait(&full[i % NSTAGE], (uint32_t)(i / NSTAGE) & 1u, kWaitNs);
+  } else {
+    // One unit.  The four epilogue warps push each token's partial sums to the
+    // CTA that owns the token.
+    const Tile t = tile_of(u_first);
+    const int rb = u_first % p.NB;
+    const int own_log = __ffs(NT / p.splits) - 1, own = 1 << own_log;  // tokens of each CTA
+    if (warp >= 4) {
+      wait(&acc_full[0], 0);
+      __syncwarp();
+      ptx::tc_fence_after();
     }
-    __syncthreads();
-    return;
-  }
-  {
-    const float* sum = reinterpret_cast<const float*>(smem + C::OFF_SUM);
-    const int own = NT / p.splits;
-    const int first = SPLIT ? split * own : 0;
-    const int mine = min(own, count - first);  // tokens of this CTA
-    const int sub = lane & 15;
-    for (int i = 2 * warp; i < mine; i += 2 * (kThreads / 32)) {
-      const int tl = i + (lane >> 4);
-      const bool in = tl < mine;
-      float v[NA][8];
+    ptx::cluster_wait();  // every CTA of the cluster has begun
+    if (warp >= 4) {
+      const int q = warp & 3;
+      const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16);
 #pragma unroll
-      for (int a = 0; a < NA; ++a) {
-        const float* at = sum + ((in ? tl : i) * NA + a) * 128 + 8 * sub;
-        *reinterpret_cast<float4*>(&v[a][0]) = *reinterpret_cast<const float4*>(at);
-        *reinterpret_cast<float4*>(&v[a][4]) = *reinterpret_cast<const float4*>(at + 4);
-        if constexpr (SPLIT) {
+      for (int a = 0; a < NA; ++a)
+#pragma unroll
+        for (int c = 0; c < NT; c += 16) {
+          uint32_t v[16];
+          ptx::tmem_ld_32x32b_x16(t0 + a * NT + c, v);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (c + i < t.count) {
+              const int o = (c + i) >> own_log, tl = (c + i) & (own - 1);
+              const uint32_t at =
+                  ptx::smem_u32(sums + ((split * own + tl) * NA + a) * 128 + q * 32 + lane);
+              ptx::st_shared_cluster_f32(ptx::map_shared_rank(at, (uint32_t)o),
+                                         nk > 0 ? __uint_as_float(v[i]) : 0.0f);
+            }
+          }
+        }
+      ptx::tc_fence_before();
+    }
+    __syncwarp();
+    ptx::cluster_sync();  // all partial sums have arrived; nobody writes here again
+    const int first = split * own;
+    const int mine = min(own, t.count - first);
+    if (!*abort_flag) {
+      for (int i = 2 * warp; i < mine; i += 2 * (C::THREADS / 32)) {
+        const int tl = i + (lane >> 4);
+        const bool in = tl < mine;
+        float v[NA][8];
+#pragma unroll
+        for (int a = 0; a < NA; ++a) {
+          const float* at = sums + ((in ? tl : i) * NA + a) * 128 + 8 * sub;
+          *reinterpret_cast<float4*>(&v[a][0]) = *reinterpret_cast<const float4*>(at);
+          *reinterpret_cast<float4*>(&v[a][4]) = *reinterpret_cast<const float4*>(at + 4);
           for (int r = 1; r < p.splits; ++r) {
             const float* ar = at + r * own * NA * 128;
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[a][e] += ar[e];
           }
         }
-      }
-      const int n = rb * 128 + 8 * sub;
-      const int tok = first + tl;
-      if constexpr (MODE == kLinear) {
-        if (in && n < p.N)
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) +
-                                    (size_t)(row0 + tok) * p.N + n) = to_bf16x8(v[0]);
-      } else if constexpr (MODE == kGateUp) {
-        float h[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] = v[0][e] / (1.0f + expf(-v[0][e])) * v[NA - 1][e];
-        uint32_t sb;
-        const float amax = half_warp_amax(h);
-        const uint2 codes = encode8(h, amax, &sb);
-        if (in && n < p.N) {
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + (size_t)(row0 + tok) * p.N + n) =
-              codes;
-          if (sub == 0) p.out_sf[(size_t)(row0 + tok) * p.NG + rb] = (uint8_t)sb;
-        }
-      } else {
-        if (in && n < p.N) {
-          const int pair = p.perm[row0 + tok];
-          const float w = p.wt[pair];
-          float* o = static_cast<float*>(p.out) + (size_t)pair * p.N + n;
-          *reinterpret_cast<float4*>(o) =
-              make_float4(v[0][0] * w, v[0][1] * w, v[0][2] * w, v[0][3] * w);
-          *reinterpret_cast<float4*>(o + 4) =
-              make_float4(v[0][4] * w, v[0][5] * w, v[0][6] * w, v[0][7] * w);
-        }
+        finish_token<MODE, NA>(p, v, t.row0 + first + tl, rb * 128 + 8 * sub, rb, sub, in);
       }
     }
+  }
+  if (*abort_flag) {
+    // MMAs and copies in flight end before TMEM and shared memory are given up:
+    // raise each issued stage's missing arrivals, then wait for its phase.
+    if (threadIdx.x == 32) {
+      ptx::mbar_wait(done, 0, kWaitNs);
+      const int i0 = issued[0], i2 = issued[1], last = max(i0, i2);
+      for (int i = min(i0, i2); i < last; ++i) ptx::mbar_arrive(&full[i % NSTAGE]);
+      for (int i = max(0, last - NSTAGE); i < last; ++i)
+        ptx::mbar_wait(&full[i % NSTAGE], (uint32_t)(i / NSTAGE) & 1u, kWaitNs);
+    }
+    __syncthreads();
+  }
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
 
@@ -480,8 +583,11 @@ __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* id
   }
   if (bad && err_flag != nullptr) atomicOr(err_flag, MXQ_DEVERR_EXPERT);
   __syncthreads();
+  // Even tiles of at most nt rows, each a multiple of 16 but for the last.
   const int c = tid < E ? cnt[tid] : 0;
-  const int nt_e = (c + nt - 1) / nt;
+  const int even = (c + nt - 1) / nt;
+  const int rows = c > 0 ? ((c + even - 1) / even + 15) / 16 * 16 : 16;
+  const int nt_e = (c + rows - 1) / rows;
   int sc = c, st = nt_e;  // inclusive sums over the warp, then over warps
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
@@ -507,18 +613,46 @@ __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* id
     for (int i = 0; i < nt_e; ++i) {
       Tile t;
       t.expert = tid;
-      t.row0 = row0 + i * nt;
-      t.count = min(nt, c - i * nt);
+      t.row0 = row0 + i * rows;
+      t.count = min(rows, c - i * rows);
       t.pad = 0;
       tiles[tile0 + i] = t;
     }
   }
-  if (tid == kPlanThreads - 1) *n_tiles = pt + st;
+  if (tid == kPlanThreads - 1) {
+    n_tiles[0] = pt + st;
+    n_tiles[1] = pc + sc;
+  }
   __syncthreads();
   for (int i = tid; i < R; i += kPlanThreads) {
     const int e = ids[i];
     if (e >= 0 && e < E) perm[atomicAdd(&cur[e], 1)] = i;
   }
+}
+
+// The activation rows laid out by expert (one warp for each), for the plain
+// copies of large tiles: every 128 weight rows read a tile's tokens anew, and a
+// copy by index moves four rows where a plain one moves 80.
+constexpr int kRowWarps = 8;
+
+__global__ void __launch_bounds__(kRowWarps * 32) w4_rows_kernel(const uint4* a, const int32_t* perm,
+                                                                 const int32_t* n_tiles, int k,
+                                                                 int chunks, uint4* out) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int r = blockIdx.x * kRowWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (r >= n_tiles[1]) return;  // the number of sorted rows
+  const uint4* src = a + (size_t)(perm[r] / k) * chunks;
+  uint4* dst = out + (size_t)r * chunks;
+  int c = lane;
+  for (; c + 96 < chunks; c += 128) {
+    const uint4 v0 = src[c], v1 = src[c + 32], v2 = src[c + 64], v3 = src[c + 96];
+    dst[c] = v0;
+    dst[c + 32] = v1;
+    dst[c + 64] = v2;
+    dst[c + 96] = v3;
+  }
+  for (; c < chunks; c += 32) dst[c] = src[c];
 }
 
 // out[t] = sum over the token's choices, in their order.
@@ -611,17 +745,17 @@ bool encode_rows(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, ui
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, int NT, int NSTAGE, bool SPLIT>
+template <int MODE, int NT, bool SPLIT>
 cudaError_t launch_cfg(const void* a, uint64_t a_rows, uint64_t K, uint64_t blocks, W4Args args,
-                       int64_t units, cudaStream_t s, const char** why) {
-  using C = Cfg<MODE, NT, NSTAGE, SPLIT>;
+                       int64_t units, int num_sms, cudaStream_t s, const char** why) {
+  using C = Cfg<MODE, NT, SPLIT>;
   CUtensorMap tm_w, tm_a;
   if (!encode_weight(&tm_w, args.w, blocks) ||
-      !encode_rows(&tm_a, a, K, a_rows, MODE == kGateUp ? 1 : NT)) {
+      !encode_rows(&tm_a, a, K, a_rows, C::GATHER ? 1 : C::BOX_ROWS)) {
     *why = "cuTensorMapEncodeTiled failed (driver entry point missing or arguments rejected)";
     return cudaErrorInvalidValue;
   }
-  auto kern = w4_kernel<MODE, NT, NSTAGE, SPLIT>;
+  auto kern = w4_kernel<MODE, NT, SPLIT>;
   static std::atomic<uint64_t> smem_set{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -632,9 +766,10 @@ cudaError_t launch_cfg(const void* a, uint64_t a_rows, uint64_t K, uint64_t bloc
     if (e != cudaSuccess) return e;
     smem_set.fetch_or(bit, std::memory_order_acq_rel);
   }
+  const int64_t slots = (int64_t)num_sms * C::CTAS;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * args.splits), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.gridDim = dim3((unsigned)(SPLIT ? units * args.splits : units < slots ? units : slots), 1, 1);
+  cfg.blockDim = dim3(C::THREADS, 1, 1);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -652,8 +787,30 @@ cudaError_t launch_cfg(const void* a, uint64_t a_rows, uint64_t K, uint64_t bloc
   return cudaLaunchKernelEx(&cfg, kern, tm_w, tm_a, args);
 }
 
-// CTAs along K for `units` units of KB blocks each: about two CTAs for each SM,
-// powers of two up to the portable cluster size, and two blocks each at least.
+// The product for tiles of at most `nt` tokens (16, 32, 64, 128 or 240), its K
+// split where the caller chose so (16 and, dense, 32 tokens only).
+template <int MODE>
+cudaError_t launch_tokens(int nt, const void* a, uint64_t a_rows, uint64_t K, uint64_t blocks,
+                          const W4Args& g, int64_t units, int num_sms, cudaStream_t s,
+                          const char** why) {
+  if (nt <= 16)
+    return g.splits > 1 ? launch_cfg<MODE, 16, true>(a, a_rows, K, blocks, g, units, num_sms, s, why)
+                        : launch_cfg<MODE, 16, false>(a, a_rows, K, blocks, g, units, num_sms, s, why);
+  if (nt <= 32) {
+    if constexpr (MODE == kLinear) {
+      if (g.splits > 1)
+        return launch_cfg<MODE, 32, true>(a, a_rows, K, blocks, g, units, num_sms, s, why);
+    }
+    return launch_cfg<MODE, 32, false>(a, a_rows, K, blocks, g, units, num_sms, s, why);
+  }
+  if (nt <= 64) return launch_cfg<MODE, 64, false>(a, a_rows, K, blocks, g, units, num_sms, s, why);
+  if (nt <= 128) return launch_cfg<MODE, 128, false>(a, a_rows, K, blocks, g, units, num_sms, s, why);
+  return launch_cfg<MODE, kMaxTokens, false>(a, a_rows, K, blocks, g, units, num_sms, s, why);
+}
+
+// CTAs along K for `units` units of KB blocks each: powers of two up to the
+// portable cluster size that the device's slots hold at once, and two blocks each
+// at least.
 int pick_splits(int64_t units, int KB, int slots) {
   int s = 1;
   while (s < 8 && units * s * 2 <= slots && KB >= 4 * s) s *= 2;
@@ -683,41 +840,55 @@ cudaError_t launch_linear_a8w4(const uint8_t* a, const uint8_t* a_sf, const uint
   g.KG = g.KB = (int)ceil_div(K, kGroup);
   g.NB = (int)ceil_div(N, 128);
   g.splits = 1;
-  g.kb_per_split = g.KB;
   cudaError_t e = watchdog_address(&g.wd);
   if (e != cudaSuccess) return e;
-  const uint64_t blocks = (uint64_t)g.NB * g.KB;
   if (T <= 32) {
     g.splits = pick_splits(g.NB, g.KB, 2 * num_sms);
-    g.kb_per_split = (int)ceil_div(g.KB, g.splits);
+    g.per_tile = T <= 16 ? 16 : 32;
+  } else {
+    // Tiles of even size.  A stage costs about 256 + 2 n cycles of shared memory
+    // for n tokens (the weight tile's write and read, and the tokens'), so the
+    // number of tiles is the one with the least rounds x (128 + n).
+    int64_t best = -1;
+    const int64_t least = ceil_div(T, kMaxTokens);
+    for (int64_t n = least; n <= least + 8; ++n) {
+      const int64_t per = ceil_div(ceil_div(T, n), 16) * 16;
+      const int64_t cost = ceil_div(ceil_div(T, per) * g.NB, num_sms) * (128 + per);
+      if (best < 0 || cost < best) {
+        best = cost;
+        g.per_tile = (int)per;
+      }
+    }
   }
-  if (T <= 16) {
-    return g.splits > 1 ? launch_cfg<kLinear, 16, 5, true>(a, T, K, blocks, g, g.NB, s, why)
-                        : launch_cfg<kLinear, 16, 5, false>(a, T, K, blocks, g, g.NB, s, why);
-  }
-  if (T <= 32) {
-    return g.splits > 1 ? launch_cfg<kLinear, 32, 4, true>(a, T, K, blocks, g, g.NB, s, why)
-                        : launch_cfg<kLinear, 32, 4, false>(a, T, K, blocks, g, g.NB, s, why);
-  }
-  if (T <= 64) return launch_cfg<kLinear, 64, 4, false>(a, T, K, blocks, g, g.NB, s, why);
-  return launch_cfg<kLinear, 128, 3, false>(a, T, K, blocks, g, ceil_div(T, 128) * g.NB, s, why);
+  g.kb_per_split = (int)ceil_div(g.KB, g.splits);
+  g.n_tiles_host = (int)ceil_div(T, g.per_tile);
+  return launch_tokens<kLinear>(g.per_tile, a, (uint64_t)T, (uint64_t)K, (uint64_t)g.NB * g.KB, g,
+                                (int64_t)g.n_tiles_host * g.NB, num_sms, s, why);
 }
 
 namespace {
-// Tokens of a tile of the routed products.
+// Most tokens of a tile, by the rows that an expert gets on average: above that
+// some experts take two tiles, which read their weights twice (from L2).
 int expert_tile(int64_t R, int E) {
   const int64_t avg = ceil_div(R, E);
-  return avg <= 8 ? 16 : avg <= 24 ? 32 : avg <= 48 ? 64 : 128;
+  return avg <= 8 ? 16 : avg <= 16 ? 32 : avg <= 40 ? 64 : avg <= 80 ? 128 : kMaxTokens;
 }
+// An expert of c rows has ceil(c / nt) tiles at most (fewer where even tiles
+// round up to 16), that is c / nt and one more if it has any.
 int64_t most_tiles(int64_t R, int E, int nt) { return R / nt + (R < E ? R : E); }
+// Whether the rows are laid out by expert first: an indexed copy of four rows
+// takes as long as a plain one of a whole tile (see w4_rows_kernel).
+bool lays_out_rows(int nt) { return nt > 32; }
 }  // namespace
 
-ExpertsLayout experts_layout(int64_t T, int k, int E, int I, int N) {
+ExpertsLayout experts_layout(int64_t T, int k, int E, int K, int I, int N) {
   const int64_t R = T * k;
+  const int nt = expert_tile(R, E);
   ExpertsLayout l;
-  l.tiles = 256;  // the number of tiles lies before them
-  l.perm = l.tiles + round_up_256((size_t)most_tiles(R, E, expert_tile(R, E)) * sizeof(Tile));
-  l.h = l.perm + round_up_256((size_t)R * 4);
+  l.tiles = 256;  // the numbers of tiles and of rows lie before them
+  l.perm = l.tiles + round_up_256((size_t)most_tiles(R, E, nt) * sizeof(Tile));
+  l.rows = l.perm + round_up_256((size_t)R * 4);
+  l.h = l.rows + (lays_out_rows(nt) ? round_up_256((size_t)R * K) : 0);
   l.h_sf = l.h + round_up_256((size_t)R * I);
   l.part = l.h_sf + round_up_256((size_t)R * (size_t)ceil_div(I, kGroup));
   l.total = l.part + round_up_256((size_t)R * N * 4);
@@ -730,7 +901,7 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
                                 void* ws, int num_sms, cudaStream_t s, const char** why) {
   const int64_t R = T * k;
   const int nt = expert_tile(R, E);
-  const ExpertsLayout l = experts_layout(T, k, E, I, N);
+  const ExpertsLayout l = experts_layout(T, k, E, K, I, N);
   uint8_t* base = static_cast<uint8_t*>(ws);
   int32_t* n_tiles = reinterpret_cast<int32_t*>(base);
   Tile* tiles = reinterpret_cast<Tile*>(base + l.tiles);
@@ -749,6 +920,17 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   if (e != cudaSuccess) return e;
   e = cudaLaunchKernelEx(&cfg, w4_plan_kernel, ids, (int)R, E, nt, tiles, n_tiles, perm, err_flag);
   if (e != cudaSuccess) return e;
+  const uint8_t* rows = a;
+  int64_t n_rows = T;
+  if (lays_out_rows(nt)) {
+    cfg.gridDim = dim3((unsigned)ceil_div(R, kRowWarps), 1, 1);
+    cfg.blockDim = dim3(kRowWarps * 32, 1, 1);
+    e = cudaLaunchKernelEx(&cfg, w4_rows_kernel, reinterpret_cast<const uint4*>(a), perm, n_tiles, k,
+                           K / 16, reinterpret_cast<uint4*>(base + l.rows));
+    if (e != cudaSuccess) return e;
+    rows = base + l.rows;
+    n_rows = R;
+  }
 
   g.tiles = tiles;
   g.n_tiles = n_tiles;
@@ -767,18 +949,8 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   g.NB = g.NG = (int)ceil_div(I, 128);
   g.splits = nt == 16 ? pick_splits(most * g.NB, g.KB, num_sms) : 1;
   g.kb_per_split = (int)ceil_div(g.KB, g.splits);
-  uint64_t blocks = 2 * (uint64_t)E * g.NB * g.KB;
-  int64_t units = most * g.NB;
-  if (nt == 16) {
-    e = g.splits > 1 ? launch_cfg<kGateUp, 16, 5, true>(a, T, K, blocks, g, units, s, why)
-                     : launch_cfg<kGateUp, 16, 3, false>(a, T, K, blocks, g, units, s, why);
-  } else if (nt == 32) {
-    e = launch_cfg<kGateUp, 32, 5, false>(a, T, K, blocks, g, units, s, why);
-  } else if (nt == 64) {
-    e = launch_cfg<kGateUp, 64, 5, false>(a, T, K, blocks, g, units, s, why);
-  } else {
-    e = launch_cfg<kGateUp, 128, 4, false>(a, T, K, blocks, g, units, s, why);
-  }
+  e = launch_tokens<kGateUp>(nt, rows, (uint64_t)n_rows, (uint64_t)K, 2 * (uint64_t)E * g.NB * g.KB, g,
+                             most * g.NB, num_sms, s, why);
   if (e != cudaSuccess) return e;
   // Down.
   g.w = w2;
@@ -790,19 +962,8 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   g.NB = (int)ceil_div(N, 128);
   g.splits = nt == 16 ? pick_splits(most * g.NB, g.KB, 2 * num_sms) : 1;
   g.kb_per_split = (int)ceil_div(g.KB, g.splits);
-  blocks = (uint64_t)E * g.NB * g.KB;
-  units = most * g.NB;
-  const uint8_t* h = base + l.h;
-  if (nt == 16) {
-    e = g.splits > 1 ? launch_cfg<kDown, 16, 5, true>(h, R, I, blocks, g, units, s, why)
-                     : launch_cfg<kDown, 16, 5, false>(h, R, I, blocks, g, units, s, why);
-  } else if (nt == 32) {
-    e = launch_cfg<kDown, 32, 4, false>(h, R, I, blocks, g, units, s, why);
-  } else if (nt == 64) {
-    e = launch_cfg<kDown, 64, 4, false>(h, R, I, blocks, g, units, s, why);
-  } else {
-    e = launch_cfg<kDown, 128, 3, false>(h, R, I, blocks, g, units, s, why);
-  }
+  e = launch_tokens<kDown>(nt, base + l.h, (uint64_t)R, (uint64_t)I, (uint64_t)E * g.NB * g.KB, g,
+                           most * g.NB, num_sms, s, why);
   if (e != cudaSuccess) return e;
   const int chunks = N / 8;
   const int64_t items = T * chunks;

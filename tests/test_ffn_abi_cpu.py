@@ -135,7 +135,7 @@ def experts(L, a=X, s=R, ids=S, wt=W, w13=Y, w2=Q, out=C, T=4, k=8, E=16, K=576,
 def test_experts_argument_errors(L):
     for name in ("a", "s", "ids", "wt", "w13", "w2", "out"):
         assert experts(L, **{name: None}) == 1, name
-    need = L.mxq_experts_workspace_bytes(4, 8, 16, 288, 1024)
+    need = L.mxq_experts_workspace_bytes(4, 8, 16, 576, 288, 1024)
     assert need > 0
     for bad in (dict(T=-1), dict(k=0), dict(E=0), dict(K=0), dict(K=48), dict(I=0), dict(I=48), dict(N=0), dict(N=24),
                 dict(out=X), dict(out=S), dict(out=Y), dict(out=8 << 36), dict(ws=X), dict(ws=C), dict(ws=Q),
@@ -154,15 +154,16 @@ def test_experts_argument_errors(L):
 
 def test_experts_workspace(L):
     f = L.mxq_experts_workspace_bytes
-    for bad in ((-1, 8, 16, 288, 1024), (4, 0, 16, 288, 1024), (4, 33, 16, 288, 1024), (4, 8, 0, 288, 1024),
-                (4, 8, 1025, 288, 1024), (4, 8, 16, 48, 1024), (4, 8, 16, 288, 24), (1 << 21, 8, 16, 288, 1024)):
+    good = (4, 8, 16, 576, 288, 1024)
+    for at, v in ((0, -1), (1, 0), (1, 33), (2, 0), (2, 1025), (3, 48), (3, 0), (4, 48), (5, 24), (0, 1 << 21)):
+        bad = good[:at] + (v,) + good[at + 1:]
         assert f(*bad) == 0, bad
-    assert f(8, 8, 16, 288, 1024) > f(4, 8, 16, 288, 1024)
+    assert f(8, *good[1:]) > f(*good)
 
 
 @NO_GPU
 def test_valid_calls_without_device(L):
     assert prepare(L) == 7 and linear(L) == 7 and experts(L) == 7
     assert linear(L, T=8192, N=16, K=32) == 7 and linear(L, s=R + 1) == 7
-    assert experts(L, s=R + 1, err=1 << 20, nbytes=L.mxq_experts_workspace_bytes(4, 8, 16, 288, 1024)) == 7
+    assert experts(L, s=R + 1, err=1 << 20, nbytes=L.mxq_experts_workspace_bytes(4, 8, 16, 576, 288, 1024)) == 7
     assert experts(L, k=1, E=1, K=32, I=32, N=16) == 7

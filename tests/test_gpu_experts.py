@@ -65,7 +65,8 @@ SIZES = [  # T, k, E, K, I, N
     (1, 1, 1, 32, 32, 16), (1, 4, 8, 256, 128, 256), (2, 8, 64, 576, 96, 144), (3, 2, 5, 1024, 160, 1024),
     (7, 3, 4, 4096, 256, 128), (16, 8, 32, 512, 288, 512), (1, 8, 16, 2048, 512, 2048), (33, 2, 3, 384, 128, 272),
     (64, 6, 8, 320, 224, 400), (65, 4, 8, 640, 128, 640), (130, 8, 10, 256, 416, 256), (300, 2, 4, 512, 256, 512),
-    (500, 6, 12, 288, 160, 160), (40, 32, 33, 96, 64, 48), (257, 1, 1, 1024, 384, 128)]
+    (500, 6, 12, 288, 160, 160), (40, 32, 33, 96, 64, 48), (257, 1, 1, 1024, 384, 128), (24, 4, 8, 640, 192, 304),
+    (100, 2, 16, 1152, 96, 128), (90, 6, 8, 256, 512, 96), (400, 8, 64, 160, 96, 64)]
 
 
 @pytest.mark.parametrize("T,k,E,K,I,N", SIZES)
@@ -123,7 +124,7 @@ def test_nan_rows_and_stale_workspace(mxq):
         layer = Layer(mxq, 5, 256, 96, 128, seed=10)
         a, asf = unit_acts(T, 256, seed=11)
         ids, wt = choose(T, 3, 5, seed=12)
-        ws = torch.full((mxq.mxq_experts_workspace_bytes(T, 3, 5, 96, 128),), 0xFF, dtype=torch.uint8, device="cuda")
+        ws = torch.full((mxq.mxq_experts_workspace_bytes(T, 3, 5, 256, 96, 128),), 0xFF, dtype=torch.uint8, device="cuda")
         good = layer(a, asf, ids, wt, ws=ws)
         check(layer, a, asf, ids, wt, good)
         a[4, 100] = 0x7F
