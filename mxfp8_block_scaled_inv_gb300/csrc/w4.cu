@@ -79,7 +79,7 @@ constexpr int kMaxTokens = 240;  // of a tile: two accumulators and scale column
 enum Mode { kLinear = 0, kGateUp = 1, kDown = 2 };
 
 // Device-side plan of a routed call: which sorted rows each tile holds.
-struct Tile {
+struct alignas(16) Tile {
   int32_t expert, row0, count, pad;
 };
 
@@ -199,7 +199,10 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
   volatile int* abort_flag = reinterpret_cast<volatile int*>(slot + 1);
   volatile int* issued = reinterpret_cast<volatile int*>(slot + 2);  // [0] warp 0, [1] warp 2
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (Broadcast: the compiler then knows that a warp's role and what follows from
+  // it are the same in all lanes, and keeps the operands of copies and MMAs in
+  // uniform registers instead of moving them there each time.)
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   ptx::griddep_launch_dependents();
 
   const int split = SPLIT ? (int)ptx::cluster_rank() : 0;
@@ -231,7 +234,10 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
       t.row0 = (u / p.NB) * p.per_tile;
       t.count = min(p.per_tile, p.T - t.row0);
     } else {
-      t = p.tiles[u / p.NB];
+      const int4 v = *reinterpret_cast<const int4*>(p.tiles + u / p.NB);
+      t.expert = __shfl_sync(0xffffffffu, v.x, 0);
+      t.row0 = __shfl_sync(0xffffffffu, v.y, 0);
+      t.count = __shfl_sync(0xffffffffu, v.z, 0);
     }
     return t;
   };
@@ -259,7 +265,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
   }
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = *slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);
   if constexpr (SPLIT) ptx::cluster_arrive();  // this CTA's shared memory may be written
 
   // A wait of a whole warp; false once it or another role has given up.
@@ -281,25 +287,32 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
       const int boxes = (t.count + C::BOX_ROWS - 1) / C::BOX_ROWS;
       const uint32_t bytes =
           NA * kBlockBytes + (C::GATHER ? 0u : (uint32_t)(boxes * C::BOX_ROWS * 128));
-      const int mat = MODE == kGateUp ? 2 * t.expert + (lane & 1) : t.expert;
-      const size_t blk0 = ((size_t)mat * p.NB + u % p.NB) * p.KB + kb0;
+      const int rb = u % p.NB;
+      int row[NA];  // of a matrix's first block, in rows of 64 bytes
+#pragma unroll
+      for (int a = 0; a < NA; ++a)
+        row[a] = (((MODE == kGateUp ? 2 * t.expert + a : t.expert) * p.NB + rb) * p.KB + kb0) *
+                 (kBlockBytes / 64);
       for (int kk = 0; kk < nk; ++kk, ++it) {
         const int s = it % NSTAGE;
         ok = wait(&empty[s], ((uint32_t)(it / NSTAGE) & 1u) ^ 1u);
         if (!ok) break;
-        if (lane == 0) ptx::mbar_arrive_expect_tx(&full[s], bytes);
-        __syncwarp();
-        // Lanes 0..NA-1: codes; 2..: their scale atoms; 4..: the tokens.
-        if (lane < NA) {
-          ptx::tma_load_2d(smem + C::OFF_W + (s * NA + lane) * kTileBytes, &tm_w, &full[s], 0,
-                           (int)((blk0 + kk) * (kBlockBytes / 64)));
-        } else if (lane >= 2 && lane < 2 + NA) {
-          ptx::bulk_load(smem + C::OFF_WSF + (s * NA + lane - 2) * kSfAtomBytes,
-                         p.w + (blk0 + kk) * kBlockBytes + kCodeBytes, kSfAtomBytes, &full[s]);
-        } else if (!C::GATHER && lane >= 4 && lane < 4 + boxes) {
-          const int b = lane - 4;
-          ptx::tma_load_2d(smem + C::OFF_TOK + s * C::TOK_TILE + b * C::BOX_ROWS * 128, &tm_a,
-                           &full[s], (kb0 + kk) * 128, t.row0 + b * C::BOX_ROWS);
+        if (ptx::elect_one()) {
+          ptx::mbar_arrive_expect_tx(&full[s], bytes);
+#pragma unroll
+          for (int a = 0; a < NA; ++a) {
+            ptx::tma_load_2d(smem + C::OFF_W + (s * NA + a) * kTileBytes, &tm_w, &full[s], 0, row[a]);
+            ptx::bulk_load(smem + C::OFF_WSF + (s * NA + a) * kSfAtomBytes,
+                           p.w + (size_t)(uint32_t)row[a] * 64 + kCodeBytes, kSfAtomBytes, &full[s]);
+            row[a] += kBlockBytes / 64;
+          }
+          if constexpr (!C::GATHER) {
+#pragma unroll
+            for (int b = 0; b < NT / C::BOX_ROWS; ++b)
+              if (b < boxes)
+                ptx::tma_load_2d(smem + C::OFF_TOK + s * C::TOK_TILE + b * C::BOX_ROWS * 128, &tm_a,
+                                 &full[s], (kb0 + kk) * 128, t.row0 + b * C::BOX_ROWS);
+          }
         }
         __syncwarp();
       }
@@ -383,7 +396,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
         ok = wait(&full[s], (uint32_t)(it / NSTAGE) & 1u);
         if (!ok) break;
         ptx::tc_fence_after();
-        if (lane == 0) {
+        if (ptx::elect_one()) {
           const uint32_t sf = tmem + C::NBUF * NA * NT + (it % C::SF_RING) * C::SF_COLS;
           const uint32_t tok_sf = sf + 4 * NA;
           const uint64_t bdesc = ptx::smem_desc(
@@ -416,10 +429,10 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
         }
         __syncwarp();
       }
-      if (lane == 0) ptx::tc_commit(&acc_full[buf]);
+      if (ptx::elect_one()) ptx::tc_commit(&acc_full[buf]);
       __syncwarp();
     }
-    if (lane == 0) ptx::tc_commit(done);
+    if (ptx::elect_one()) ptx::tc_commit(done);
   }
   __syncwarp();
 
