@@ -22,9 +22,9 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-// Quantises one lane's 8 values of a group whose amax (over the 16 lanes of
-// the half-warp) is `amax`; returns the 8 codes and the group's scale byte.
-__device__ __forceinline__ uint2 encode8(const float (&y)[8], float amax, uint32_t* sbyte) {
+// The scale byte of a group whose abs-max is `amax`, and what its values are
+// multiplied with before they are rounded.
+__device__ __forceinline__ float group_scale(float amax, uint32_t* sbyte) {
   // Smallest e with amax <= 448 * 2^e: amax = (1+f) * 2^E and 448 = 1.75 * 2^8
   // give e = E - 8 + (f > 0.75); zero / subnormal amax clamps to e = -127.
   const uint32_t m = __float_as_uint(amax);
@@ -37,6 +37,13 @@ __device__ __forceinline__ uint2 encode8(const float (&y)[8], float amax, uint32
     *sbyte = 0xFF;
     inv = 1.0f;
   }
+  return inv;
+}
+
+// Quantises one lane's 8 values of a group whose amax (over the 16 lanes of
+// the half-warp) is `amax`; returns the 8 codes and the group's scale byte.
+__device__ __forceinline__ uint2 encode8(const float (&y)[8], float amax, uint32_t* sbyte) {
+  const float inv = group_scale(amax, sbyte);
   uint2 out;
   out.x = e4m3x2(__fmul_rn(y[0], inv), __fmul_rn(y[1], inv)) |
           (e4m3x2(__fmul_rn(y[2], inv), __fmul_rn(y[3], inv)) << 16);

@@ -31,10 +31,11 @@
 //            few rows of the gate and up product also the token rows themselves,
 //            gathered by index four to an instruction.
 //   warp 3   idle (the epilogue's warps begin at a multiple of four).
-//   warps 4- epilogue: groups of four warps, one for each TMEM lane quadrant, drain
-//            16 tokens at a time to shared memory, row-contiguous per token; then
-//            a half-warp takes a token's 128 values: 16-byte stores, and the
-//            abs-max of a scale group is four shuffles.
+//   warps 4- epilogue: groups of four warps, one for each TMEM lane quadrant, take
+//            16 tokens at a time straight from TMEM: a lane holds one weight row.
+//            Stores of a warp are contiguous along the rows; the abs-max of a
+//            scale group (128 rows of a token) is a warp-wide maximum and an
+//            exchange between the group's four warps.
 // Two forms:
 //   streaming  CTAs walk the units with a stride of the grid; copies run ahead
 //              across units and the accumulator is doubled where TMEM allows it,
@@ -107,26 +108,31 @@ struct Cfg {
   // CTAs where the tile is small, so that one streams while the other turns
   // around.
   static constexpr int CTAS = NA == 1 && NT <= 64 ? 2 : 1;
-  static constexpr int GROUPS = NT <= 64 || SPLIT ? 1 : 2;  // epilogue groups
+  static constexpr int GROUPS = NT <= 64 || SPLIT ? 1 : 3;  // epilogue groups
   static constexpr int THREADS = 128 + 128 * GROUPS;
   static constexpr int TOK_ATOMS = (NT + 127) / 128;
   static constexpr int TOK_TILE = NT * 128;
   static constexpr int BOX_ROWS = NT > 128 ? 80 : NT;  // rows of a copy of tokens
   static_assert(NT % BOX_ROWS == 0 && (BOX_ROWS % 8 == 0), "token copies");
   static constexpr int STAGE = NA * (kTileBytes + kSfAtomBytes) + TOK_TILE + TOK_ATOMS * kSfAtomBytes;
-  // Sums on their way to the epilogue, fp32: a chunk [token][accumulator][row]
-  // for each group, or with a split K what the CTA receives,
+  // Split K: the partial sums that the CTA receives, fp32
   // [rank][owned token][accumulator][row].
-  static constexpr int SUM_BYTES = SPLIT ? NA * NT * 512 : GROUPS * kChunk * NA * 512;
+  static constexpr int SUM_BYTES = SPLIT ? NA * NT * 512 : 0;
+  // For each epilogue group: the tile's places and weights in the output (down
+  // product; two units' worth), and two chunks' maxima of its four warps.
+  static constexpr int PAIR_BYTES = MODE == kDown ? GROUPS * 2 * NT * 8 : 0;
+  static constexpr int MAX_BYTES = MODE == kGateUp ? GROUPS * 2 * 4 * kChunk * 4 : 0;
   static constexpr int LIMIT = (CTAS == 2 ? 113 * 1024 : 232448) - 1024 - 512;
-  static constexpr int FIT = (LIMIT - SUM_BYTES) / STAGE;
+  static constexpr int FIT = (LIMIT - SUM_BYTES - PAIR_BYTES - MAX_BYTES) / STAGE;
   static constexpr int NSTAGE = FIT > 10 ? 10 : FIT;
   static constexpr int OFF_W = 0;
   static constexpr int OFF_TOK = NSTAGE * NA * kTileBytes;
   static constexpr int OFF_WSF = OFF_TOK + NSTAGE * TOK_TILE;
   static constexpr int OFF_TSF = OFF_WSF + NSTAGE * NA * kSfAtomBytes;
   static constexpr int OFF_SUM = OFF_TSF + NSTAGE * TOK_ATOMS * kSfAtomBytes;
-  static constexpr int OFF_BAR = OFF_SUM + SUM_BYTES;
+  static constexpr int OFF_PAIR = OFF_SUM + SUM_BYTES;
+  static constexpr int OFF_MAX = OFF_PAIR + PAIR_BYTES;
+  static constexpr int OFF_BAR = OFF_MAX + MAX_BYTES;
   static constexpr int SMEM = OFF_BAR + (2 * NSTAGE + 5) * 8 + 32 + 1024;
   // TMEM: accumulators, then a ring of scale columns.  A copy of scales into
   // columns that earlier MMAs read is ordered behind them (both are issued by one
@@ -144,39 +150,72 @@ struct Cfg {
   static_assert(NT % kChunk == 0 && NT <= kMaxTokens && (!SPLIT || NT <= 32), "tokens of a tile");
 };
 
-// silu(g) * u.
-__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+// silu(g) * u; the quotient to two units in the last place.
+__device__ __forceinline__ float swiglu(float g, float u) {
+  return __fdividef(g, 1.0f + expf(-g)) * u;
+}
 
-// What a half-warp does with 128 sums of one token: v[a] are this lane's eight,
-// from weight row n on.  All 32 lanes call it (in: the token exists).
+// Where a row's weighted result goes.
+struct Pair {
+  int32_t pair;
+  float w;
+};
+
+// What four warps do with 16 tokens: v[a][i] is token i's sum for weight row
+// n = 128 rb + 32 q + lane; `live` of them exist, the first being row `row` of the
+// output.  max_: the group's maxima (double buffered), bar its barrier.
 template <int MODE, int NA>
-__device__ __forceinline__ void finish_token(const W4Args& p, const float (&v)[NA][8], int row, int n,
-                                             int rb, int sub, bool in) {
-  const bool store = in && n < p.N;
+__device__ __forceinline__ void finish_chunk(const W4Args& p, float (&v)[NA][kChunk], int row,
+                                             int live, int rb, int q, int lane, const Pair* pairs,
+                                             float* max_, int bar) {
+  const int n = rb * 128 + q * 32 + lane;
+  const bool in = n < p.N;
   if constexpr (MODE == kLinear) {
-    if (store)
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (size_t)row * p.N + n) =
-          to_bf16x8(v[0]);
-  } else if constexpr (MODE == kGateUp) {
-    float h[8];
+    // Neighbouring lanes swap a token each, so that a lane stores two rows of one.
+    const int odd = lane & 1;
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + (size_t)(row + odd) * p.N + (n - odd);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = swiglu(v[0][e], v[NA - 1][e]);
-    uint32_t sb;
-    const float amax = half_warp_amax(h);
-    const uint2 codes = encode8(h, amax, &sb);
-    if (store) {
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + (size_t)row * p.N + n) = codes;
-      if (sub == 0) p.out_sf[(size_t)row * p.NG + rb] = (uint8_t)sb;
+    for (int i = 0; i < kChunk; i += 2) {
+      const float got = __shfl_xor_sync(0xffffffffu, odd ? v[0][i] : v[0][i + 1], 1);
+      const uint32_t w = odd ? pack2(got, v[0][i + 1]) : pack2(v[0][i], got);
+      if (in && i + odd < live) *reinterpret_cast<uint32_t*>(o + (size_t)i * p.N) = w;
+    }
+  } else if constexpr (MODE == kGateUp) {
+    float h[kChunk];
+    uint32_t mine = 0u;  // lane i: the warp's abs-max of token i, as bits
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) {
+      h[i] = swiglu(v[0][i], v[NA - 1][i]);
+      const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+      if (lane == i) mine = m;
+    }
+    if (lane < kChunk) max_[q * kChunk + lane] = __uint_as_float(mine);
+    ptx::named_sync(bar, 128);
+    float inv = 0.0f;
+    if (lane < kChunk) {
+      uint32_t m = 0u;  // (as bits: a NaN counts as the largest)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) m = max(m, __float_as_uint(max_[w * kChunk + lane]));
+      uint32_t sb;
+      inv = group_scale(__uint_as_float(m), &sb);
+      if (q == 0 && lane < live) p.out_sf[(size_t)(row + lane) * p.NG + rb] = (uint8_t)sb;
+    }
+    uint8_t* o = static_cast<uint8_t*>(p.out) + (size_t)row * p.N + n;
+#pragma unroll
+    for (int i = 0; i < kChunk; i += 2) {
+      const uint32_t c = e4m3x2(__fmul_rn(h[i], __shfl_sync(0xffffffffu, inv, i)),
+                                __fmul_rn(h[i + 1], __shfl_sync(0xffffffffu, inv, i + 1)));
+      if (in && i < live) o[(size_t)i * p.N] = (uint8_t)c;
+      if (in && i + 1 < live) o[(size_t)(i + 1) * p.N] = (uint8_t)(c >> 8);
     }
   } else {
-    if (store) {
-      const int pair = p.perm[row];
-      const float w = p.wt[pair];
-      float* o = static_cast<float*>(p.out) + (size_t)pair * p.N + n;
-      *reinterpret_cast<float4*>(o) =
-          make_float4(v[0][0] * w, v[0][1] * w, v[0][2] * w, v[0][3] * w);
-      *reinterpret_cast<float4*>(o + 4) =
-          make_float4(v[0][4] * w, v[0][5] * w, v[0][6] * w, v[0][7] * w);
+    float* o = static_cast<float*>(p.out) + n;
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) {
+      if (in && i < live) {
+        const Pair at = pairs[i];
+        o[(size_t)at.pair * p.N] = v[0][i] * at.w;
+      }
     }
   }
 }
@@ -437,52 +476,52 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
   __syncwarp();
 
   // ------------------------------------------------------------- epilogue
-  const int sub = lane & 15;
   float* sums = reinterpret_cast<float*>(smem + C::OFF_SUM);
+  const int q = warp & 3, group = warp >= 4 ? (warp - 4) >> 2 : 0;
+  Pair* pairs = reinterpret_cast<Pair*>(smem + C::OFF_PAIR) + group * 2 * NT;
+  float* max_ = reinterpret_cast<float*>(smem + C::OFF_MAX) + group * 2 * 4 * kChunk;
+  // The places and weights of a unit's rows, for the group's later use.
+  auto fetch_pairs = [&](const Tile& t, Pair* to) {
+    if constexpr (MODE == kDown) {
+      for (int i = q * 32 + lane; i < t.count; i += 128) {
+        Pair v;
+        v.pair = p.perm[t.row0 + i];
+        v.w = p.wt[v.pair];
+        to[i] = v;
+      }
+    }
+  };
   if constexpr (!SPLIT) {
     if (warp >= 4) {
-      const int q = warp & 3, group = (warp - 4) >> 2;
-      float* sum = sums + group * kChunk * NA * 128;
-      int n = 0;
+      int n = 0, chunk_no = 0;
       for (int u = u_first; u < units; u += u_step, ++n) {
         const int buf = C::NBUF == 2 ? n & 1 : 0;
         const Tile t = tile_of(u);
         const int rb = u % p.NB;
         const int chunks = (t.count + kChunk - 1) / kChunk;
+        fetch_pairs(t, pairs + (n & 1) * NT);
         const bool ok = wait(&acc_full[buf], (uint32_t)(n / C::NBUF) & 1u);
         if (!ptx::named_sync_and(1 + group, 128, ok)) break;  // the group goes on, or leaves, together
         ptx::tc_fence_after();
         const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + buf * NA * NT;
-        for (int c = group; c < chunks; c += C::GROUPS) {
-          uint32_t v[NA][kChunk];
+        for (int c = group; c < chunks; c += C::GROUPS, ++chunk_no) {
+          uint32_t r[NA][kChunk];
 #pragma unroll
-          for (int a = 0; a < NA; ++a) ptx::tmem_ld_32x32b_x16(t0 + a * NT + c * kChunk, v[a]);
+          for (int a = 0; a < NA; ++a) ptx::tmem_ld_32x32b_x16(t0 + a * NT + c * kChunk, r[a]);
           ptx::tmem_ld_wait();
           if (c + C::GROUPS >= chunks) {  // this group's last: the accumulator is free
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&acc_empty[buf]);
           }
+          float v[NA][kChunk];
 #pragma unroll
-          for (int i = 0; i < kChunk; ++i)
+          for (int a = 0; a < NA; ++a)
 #pragma unroll
-            for (int a = 0; a < NA; ++a)
-              sum[(i * NA + a) * 128 + q * 32 + lane] = __uint_as_float(v[a][i]);
-          ptx::named_sync(1 + group, 128);
-#pragma unroll
-          for (int j = 0; j < kChunk; j += 8) {
-            const int i = j + 2 * q + (lane >> 4);
-            const int tok = c * kChunk + i;
-            float w[NA][8];
-#pragma unroll
-            for (int a = 0; a < NA; ++a) {
-              const float* at = sum + (i * NA + a) * 128 + 8 * sub;
-              *reinterpret_cast<float4*>(&w[a][0]) = *reinterpret_cast<const float4*>(at);
-              *reinterpret_cast<float4*>(&w[a][4]) = *reinterpret_cast<const float4*>(at + 4);
-            }
-            finish_token<MODE, NA>(p, w, t.row0 + tok, rb * 128 + 8 * sub, rb, sub, tok < t.count);
-          }
-          ptx::named_sync(1 + group, 128);
+            for (int i = 0; i < kChunk; ++i) v[a][i] = __uint_as_float(r[a][i]);
+          finish_chunk<MODE, NA>(p, v, t.row0 + c * kChunk, t.count - c * kChunk, rb, q, lane,
+                                 pairs + (n & 1) * NT + c * kChunk,
+                                 max_ + (chunk_no & 1) * 4 * kChunk, 1 + group);
         }
         if (group >= chunks) {  // no chunk for this group
           __syncwarp();
@@ -497,14 +536,15 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
     const Tile t = tile_of(u_first);
     const int rb = u_first % p.NB;
     const int own_log = __ffs(NT / p.splits) - 1, own = 1 << own_log;  // tokens of each CTA
+    const int first = split * own;
     if (warp >= 4) {
+      fetch_pairs(t, pairs);
       wait(&acc_full[0], 0);
       __syncwarp();
       ptx::tc_fence_after();
     }
     ptx::cluster_wait();  // every CTA of the cluster has begun
     if (warp >= 4) {
-      const int q = warp & 3;
       const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16);
 #pragma unroll
       for (int a = 0; a < NA; ++a)
@@ -528,25 +568,22 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
     }
     __syncwarp();
     ptx::cluster_sync();  // all partial sums have arrived; nobody writes here again
-    const int first = split * own;
-    const int mine = min(own, t.count - first);
-    if (!*abort_flag) {
-      for (int i = 2 * warp; i < mine; i += 2 * (C::THREADS / 32)) {
-        const int tl = i + (lane >> 4);
-        const bool in = tl < mine;
-        float v[NA][8];
+    if (warp >= 4 && !*abort_flag) {
+      const int mine = min(own, t.count - first);
+      for (int c = 0; c < mine; c += kChunk) {
+        float v[NA][kChunk];
 #pragma unroll
-        for (int a = 0; a < NA; ++a) {
-          const float* at = sums + ((in ? tl : i) * NA + a) * 128 + 8 * sub;
-          *reinterpret_cast<float4*>(&v[a][0]) = *reinterpret_cast<const float4*>(at);
-          *reinterpret_cast<float4*>(&v[a][4]) = *reinterpret_cast<const float4*>(at + 4);
-          for (int r = 1; r < p.splits; ++r) {
-            const float* ar = at + r * own * NA * 128;
+        for (int a = 0; a < NA; ++a)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[a][e] += ar[e];
+          for (int i = 0; i < kChunk; ++i) {
+            v[a][i] = 0.0f;
+            if (c + i < mine) {
+              const float* at = sums + ((c + i) * NA + a) * 128 + q * 32 + lane;
+              for (int r = 0; r < p.splits; ++r) v[a][i] += at[r * own * NA * 128];
+            }
           }
-        }
-        finish_token<MODE, NA>(p, v, t.row0 + first + tl, rb * 128 + 8 * sub, rb, sub, in);
+        finish_chunk<MODE, NA>(p, v, t.row0 + first + c, mine - c, rb, q, lane, pairs + first + c,
+                               max_ + (c / kChunk & 1) * 4 * kChunk, 1);
       }
     }
   }
