@@ -90,9 +90,8 @@ struct W4Args {
   const Tile* tiles;      // routed forms
   const int32_t* n_tiles;
   const int32_t* perm;    // sorted row -> token * k + choice
-  const float* wt;        // [T][k], down product
-  void* out;              // kLinear: BF16 [T][N]; kGateUp: codes [rows][N]; kDown: fp32 [T*k][N]
-  uint8_t* out_sf;        // kGateUp: [rows][NG]
+  void* out;              // kLinear: BF16 [T][N]; kGateUp: codes [rows][N]; kDown: int16 [rows][N]
+  uint8_t* out_sf;        // kGateUp: [rows][NG]; kDown: exponents [N / 32][NG rows]
   uint32_t* wd;           // watchdog word
   int T, N, KG, KB, NB, NG, k;
   int per_tile, n_tiles_host;  // kLinear: tokens of a tile, tiles
@@ -118,20 +117,17 @@ struct Cfg {
   // Split K: the partial sums that the CTA receives, fp32
   // [rank][owned token][accumulator][row].
   static constexpr int SUM_BYTES = SPLIT ? NA * NT * 512 : 0;
-  // For each epilogue group: the tile's places and weights in the output (down
-  // product; two units' worth), and two chunks' maxima of its four warps.
-  static constexpr int PAIR_BYTES = MODE == kDown ? GROUPS * 2 * NT * 8 : 0;
+  // For each epilogue group: two chunks' maxima of its four warps.
   static constexpr int MAX_BYTES = MODE == kGateUp ? GROUPS * 2 * 4 * kChunk * 4 : 0;
   static constexpr int LIMIT = (CTAS == 2 ? 113 * 1024 : 232448) - 1024 - 512;
-  static constexpr int FIT = (LIMIT - SUM_BYTES - PAIR_BYTES - MAX_BYTES) / STAGE;
+  static constexpr int FIT = (LIMIT - SUM_BYTES - MAX_BYTES) / STAGE;
   static constexpr int NSTAGE = FIT > 10 ? 10 : FIT;
   static constexpr int OFF_W = 0;
   static constexpr int OFF_TOK = NSTAGE * NA * kTileBytes;
   static constexpr int OFF_WSF = OFF_TOK + NSTAGE * TOK_TILE;
   static constexpr int OFF_TSF = OFF_WSF + NSTAGE * NA * kSfAtomBytes;
   static constexpr int OFF_SUM = OFF_TSF + NSTAGE * TOK_ATOMS * kSfAtomBytes;
-  static constexpr int OFF_PAIR = OFF_SUM + SUM_BYTES;
-  static constexpr int OFF_MAX = OFF_PAIR + PAIR_BYTES;
+  static constexpr int OFF_MAX = OFF_SUM + SUM_BYTES;
   static constexpr int OFF_BAR = OFF_MAX + MAX_BYTES;
   static constexpr int SMEM = OFF_BAR + (2 * NSTAGE + 5) * 8 + 32 + 1024;
   // TMEM: accumulators, then a ring of scale columns.  A copy of scales into
@@ -150,24 +146,33 @@ struct Cfg {
   static_assert(NT % kChunk == 0 && NT <= kMaxTokens && (!SPLIT || NT <= 32), "tokens of a tile");
 };
 
-// silu(g) * u; the quotient to two units in the last place.
+// silu(g) * u.  The fast exponential (off by 2^-22 and 2^-23 |g| of itself) and
+// quotient (2^-22) are far inside the step of the 8-bit codes that follow; the
+// exact ones are a third of the epilogue's instructions.
 __device__ __forceinline__ float swiglu(float g, float u) {
-  return __fdividef(g, 1.0f + expf(-g)) * u;
+  return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
 
-// Where a row's weighted result goes.
-struct Pair {
-  int32_t pair;
-  float w;
-};
+// A result between the down product and the weighted sum over a token's experts
+// is held in 16 bits, as an integer with one exponent for 32 columns: the step is
+// 2^-13 to 2^-14 of the largest of the 32, which a sum rounded to BF16 does not
+// see, and half the bytes of FP32 to write and read again.  m: exponent field of
+// the largest magnitude, which is below 2^(m - 126); the value is the integer
+// times 2^(m - 140).  With an infinity or a NaN among the 32 they are BF16 values.
+constexpr uint32_t kLeastExp = 14u;  // smaller ones lose bits below 2^-126
+__device__ __forceinline__ uint32_t held16(float y, uint32_t m) {
+  const float inv = __uint_as_float((267u - max(m, kLeastExp)) << 23);  // 2^(140 - m)
+  const uint32_t bits = __float_as_uint(fmaf(y, inv, 12582912.0f));     // the integer + 1.5 * 2^23
+  return m == 255u ? pack2(y, 0.0f) : bits;
+}
 
 // What four warps do with 16 tokens: v[a][i] is token i's sum for weight row
 // n = 128 rb + 32 q + lane; `live` of them exist, the first being row `row` of the
 // output.  max_: the group's maxima (double buffered), bar its barrier.
 template <int MODE, int NA>
 __device__ __forceinline__ void finish_chunk(const W4Args& p, float (&v)[NA][kChunk], int row,
-                                             int live, int rb, int q, int lane, const Pair* pairs,
-                                             float* max_, int bar) {
+                                             int live, int rb, int q, int lane, float* max_,
+                                             int bar) {
   const int n = rb * 128 + q * 32 + lane;
   const bool in = n < p.N;
   if constexpr (MODE == kLinear) {
@@ -209,13 +214,61 @@ __device__ __forceinline__ void finish_chunk(const W4Args& p, float (&v)[NA][kCh
       if (in && i + 1 < live) o[(size_t)(i + 1) * p.N] = (uint8_t)(c >> 8);
     }
   } else {
-    float* o = static_cast<float*>(p.out) + n;
+    uint16_t* o = static_cast<uint16_t*>(p.out) + (size_t)row * p.N + n;
+    uint32_t m[kChunk], mine = 0u;
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i)
+      m[i] = __reduce_max_sync(0xffffffffu, __float_as_uint(v[0][i]) & 0x7FFFFFFFu) >> 23;
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) {
-      if (in && i < live) {
-        const Pair at = pairs[i];
-        o[(size_t)at.pair * p.N] = v[0][i] * at.w;
-      }
+      const uint32_t bits = held16(v[0][i], m[i]);
+      if (lane == i) mine = m[i];
+      if (in && i < live) o[(size_t)i * p.N] = (uint16_t)bits;
+    }
+    // (By column block first: a row's bytes of all blocks lie far apart, and single
+    // bytes to lines that nobody else writes cost as much as all the rest.)
+    if (lane < min(live, kChunk) && rb * 128 + q * 32 < p.N)
+      p.out_sf[(size_t)(rb * 4 + q) * p.NG + row + lane] = (uint8_t)max(mine, kLeastExp);
+  }
+}
+
+// The same for one token in a half-warp: v[a] are the lane's eight sums, from
+// weight row n = 128 rb + 8 sub on.  All 32 lanes call it (in: the token exists).
+template <int MODE, int NA>
+__device__ __forceinline__ void finish_token(const W4Args& p, const float (&v)[NA][8], int row,
+                                             int rb, int sub, bool in) {
+  const int n = rb * 128 + 8 * sub;
+  const bool store = in && n < p.N;
+  if constexpr (MODE == kLinear) {
+    if (store)
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (size_t)row * p.N + n) =
+          to_bf16x8(v[0]);
+  } else if constexpr (MODE == kGateUp) {
+    float h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = swiglu(v[0][e], v[NA - 1][e]);
+    uint32_t sb;
+    const float amax = half_warp_amax(h);
+    const uint2 codes = encode8(h, amax, &sb);
+    if (store) {
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + (size_t)row * p.N + n) = codes;
+      if (sub == 0) p.out_sf[(size_t)row * p.NG + rb] = (uint8_t)sb;
+    }
+  } else {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[0][e]) & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    m >>= 23;
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = (held16(v[0][2 * e], m) & 0xFFFFu) | (held16(v[0][2 * e + 1], m) << 16);
+    if (store) {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (size_t)row * p.N + n) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+      if ((sub & 3) == 0) p.out_sf[(size_t)(n >> 5) * p.NG + row] = (uint8_t)max(m, kLeastExp);
     }
   }
 }
@@ -478,19 +531,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
   // ------------------------------------------------------------- epilogue
   float* sums = reinterpret_cast<float*>(smem + C::OFF_SUM);
   const int q = warp & 3, group = warp >= 4 ? (warp - 4) >> 2 : 0;
-  Pair* pairs = reinterpret_cast<Pair*>(smem + C::OFF_PAIR) + group * 2 * NT;
   float* max_ = reinterpret_cast<float*>(smem + C::OFF_MAX) + group * 2 * 4 * kChunk;
-  // The places and weights of a unit's rows, for the group's later use.
-  auto fetch_pairs = [&](const Tile& t, Pair* to) {
-    if constexpr (MODE == kDown) {
-      for (int i = q * 32 + lane; i < t.count; i += 128) {
-        Pair v;
-        v.pair = p.perm[t.row0 + i];
-        v.w = p.wt[v.pair];
-        to[i] = v;
-      }
-    }
-  };
   if constexpr (!SPLIT) {
     if (warp >= 4) {
       int n = 0, chunk_no = 0;
@@ -499,7 +540,6 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
         const Tile t = tile_of(u);
         const int rb = u % p.NB;
         const int chunks = (t.count + kChunk - 1) / kChunk;
-        fetch_pairs(t, pairs + (n & 1) * NT);
         const bool ok = wait(&acc_full[buf], (uint32_t)(n / C::NBUF) & 1u);
         if (!ptx::named_sync_and(1 + group, 128, ok)) break;  // the group goes on, or leaves, together
         ptx::tc_fence_after();
@@ -520,7 +560,6 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
 #pragma unroll
             for (int i = 0; i < kChunk; ++i) v[a][i] = __uint_as_float(r[a][i]);
           finish_chunk<MODE, NA>(p, v, t.row0 + c * kChunk, t.count - c * kChunk, rb, q, lane,
-                                 pairs + (n & 1) * NT + c * kChunk,
                                  max_ + (chunk_no & 1) * 4 * kChunk, 1 + group);
         }
         if (group >= chunks) {  // no chunk for this group
@@ -538,7 +577,6 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
     const int own_log = __ffs(NT / p.splits) - 1, own = 1 << own_log;  // tokens of each CTA
     const int first = split * own;
     if (warp >= 4) {
-      fetch_pairs(t, pairs);
       wait(&acc_full[0], 0);
       __syncwarp();
       ptx::tc_fence_after();
@@ -568,22 +606,25 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
     }
     __syncwarp();
     ptx::cluster_sync();  // all partial sums have arrived; nobody writes here again
-    if (warp >= 4 && !*abort_flag) {
-      const int mine = min(own, t.count - first);
-      for (int c = 0; c < mine; c += kChunk) {
-        float v[NA][kChunk];
+    const int mine = min(own, t.count - first);
+    if (!*abort_flag) {
+      const int sub = lane & 15;
+      for (int i = 2 * warp; i < mine; i += 2 * (C::THREADS / 32)) {
+        const int tl = i + (lane >> 4);
+        const bool in = tl < mine;
+        float v[NA][8];
 #pragma unroll
-        for (int a = 0; a < NA; ++a)
+        for (int a = 0; a < NA; ++a) {
+          const float* at = sums + ((in ? tl : i) * NA + a) * 128 + 8 * sub;
+          *reinterpret_cast<float4*>(&v[a][0]) = *reinterpret_cast<const float4*>(at);
+          *reinterpret_cast<float4*>(&v[a][4]) = *reinterpret_cast<const float4*>(at + 4);
+          for (int r = 1; r < p.splits; ++r) {
+            const float* ar = at + r * own * NA * 128;
 #pragma unroll
-          for (int i = 0; i < kChunk; ++i) {
-            v[a][i] = 0.0f;
-            if (c + i < mine) {
-              const float* at = sums + ((c + i) * NA + a) * 128 + q * 32 + lane;
-              for (int r = 0; r < p.splits; ++r) v[a][i] += at[r * own * NA * 128];
-            }
+            for (int e = 0; e < 8; ++e) v[a][e] += ar[e];
           }
-        finish_chunk<MODE, NA>(p, v, t.row0 + first + c, mine - c, rb, q, lane, pairs + first + c,
-                               max_ + (c / kChunk & 1) * 4 * kChunk, 1);
+        }
+        finish_token<MODE, NA>(p, v, t.row0 + first + tl, rb, sub, in);
       }
     }
   }
@@ -607,14 +648,16 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
 
 // ------------------------------------------------------------ plan and join
 // One CTA counts the rows of each expert, lays out the tiles and sorts the rows
-// by expert.  The order of an expert's rows does not matter: each is summed by
+// by expert: perm gives a sorted row's token and choice, pos the other way round
+// (-1: no expert).  The order of an expert's rows does not matter: each is summed by
 // itself, and lands at its own place.
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanBatch = 8;
 
 __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* ids, int R, int E,
                                                                int nt, Tile* tiles,
                                                                int32_t* n_tiles, int32_t* perm,
-                                                               int32_t* err_flag) {
+                                                               int32_t* pos, int32_t* err_flag) {
   __shared__ int cnt[kMaxExperts], cur[kMaxExperts];
   __shared__ int wsum[32], wtile[32];
   ptx::griddep_launch_dependents();
@@ -624,12 +667,19 @@ __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* id
   if (tid < kMaxExperts) cnt[tid] = 0;
   __syncthreads();
   bool bad = false;
-  for (int i = tid; i < R; i += kPlanThreads) {
-    const int e = ids[i];
-    if (e >= 0 && e < E)
-      atomicAdd(&cnt[e], 1);
-    else
-      bad |= e != -1;
+  // (Eight loads at a time: with one after the other their latency is the time.)
+  for (int i0 = tid; i0 < R; i0 += kPlanBatch * kPlanThreads) {
+    int e[kPlanBatch];
+#pragma unroll
+    for (int j = 0; j < kPlanBatch; ++j)
+      e[j] = i0 + j * kPlanThreads < R ? ids[i0 + j * kPlanThreads] : -1;
+#pragma unroll
+    for (int j = 0; j < kPlanBatch; ++j) {
+      if (e[j] >= 0 && e[j] < E)
+        atomicAdd(&cnt[e[j]], 1);
+      else
+        bad |= e[j] != -1;
+    }
   }
   if (bad && err_flag != nullptr) atomicOr(err_flag, MXQ_DEVERR_EXPERT);
   __syncthreads();
@@ -674,9 +724,22 @@ __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* id
     n_tiles[1] = pc + sc;
   }
   __syncthreads();
-  for (int i = tid; i < R; i += kPlanThreads) {
-    const int e = ids[i];
-    if (e >= 0 && e < E) perm[atomicAdd(&cur[e], 1)] = i;
+  for (int i0 = tid; i0 < R; i0 += kPlanBatch * kPlanThreads) {
+    int e[kPlanBatch];
+#pragma unroll
+    for (int j = 0; j < kPlanBatch; ++j)
+      e[j] = i0 + j * kPlanThreads < R ? ids[i0 + j * kPlanThreads] : -1;
+#pragma unroll
+    for (int j = 0; j < kPlanBatch; ++j) {
+      const int i = i0 + j * kPlanThreads;
+      if (i >= R) break;
+      int at = -1;
+      if (e[j] >= 0 && e[j] < E) {
+        at = atomicAdd(&cur[e[j]], 1);
+        perm[at] = i;
+      }
+      pos[i] = at;
+    }
   }
 }
 
@@ -705,10 +768,12 @@ __global__ void __launch_bounds__(kRowWarps * 32) w4_rows_kernel(const uint4* a,
   for (; c < chunks; c += 32) dst[c] = src[c];
 }
 
-// out[t] = sum over the token's choices, in their order.
-__global__ void __launch_bounds__(256) w4_join_kernel(const float* part, const int32_t* ids,
+// out[t] = weighted sum over the token's choices, in their order, of the 16-bit
+// results that the down product left; eight columns to a thread.
+__global__ void __launch_bounds__(256) w4_join_kernel(const uint4* part, const uint8_t* part_sf,
+                                                      const int32_t* pos, const float* wt,
                                                       uint4* out, int64_t items, int chunks, int k,
-                                                      int E) {
+                                                      int64_t R) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -716,19 +781,30 @@ __global__ void __launch_bounds__(256) w4_join_kernel(const float* part, const i
   const int64_t t = it / chunks;
   const int c = (int)(it - t * chunks);
   float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
   for (int j = 0; j < k; ++j) {
-    const int e = ids[t * k + j];
-    if (e < 0 || e >= E) continue;
-    const float4* s = reinterpret_cast<const float4*>(part) + ((size_t)(t * k + j) * chunks + c) * 2;
-    const float4 a = s[0], b = s[1];
-    y[0] += a.x;
-    y[1] += a.y;
-    y[2] += a.z;
-    y[3] += a.w;
-    y[4] += b.x;
-    y[5] += b.y;
-    y[6] += b.z;
-    y[7] += b.w;
+    const int row = pos[t * k + j];
+    if (row < 0) continue;
+    const uint4 v = part[(size_t)row * chunks + c];
+    const uint32_t ef = part_sf[(c >> 2) * R + row];
+    const float g = wt[t * k + j];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (ef != 255u) {
+      const float s = __uint_as_float((ef - 13u) << 23);  // 2^(ef - 140)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        // The integer plus 2^15 as the low bits of 2^23.
+        const uint32_t u = w[q] ^ 0x80008000u;
+        y[2 * q] = fmaf((__uint_as_float(0x4B000000u | (u & 0xFFFFu)) - 8421376.0f) * s, g, y[2 * q]);
+        y[2 * q + 1] = fmaf((__uint_as_float(0x4B000000u | (u >> 16)) - 8421376.0f) * s, g, y[2 * q + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        y[2 * q] = fmaf(bf16_lo(w[q]), g, y[2 * q]);
+        y[2 * q + 1] = fmaf(bf16_hi(w[q]), g, y[2 * q + 1]);
+      }
+    }
   }
   out[it] = to_bf16x8(y);
 }
@@ -937,11 +1013,13 @@ ExpertsLayout experts_layout(int64_t T, int k, int E, int K, int I, int N) {
   ExpertsLayout l;
   l.tiles = 256;  // the numbers of tiles and of rows lie before them
   l.perm = l.tiles + round_up_256((size_t)most_tiles(R, E, nt) * sizeof(Tile));
-  l.rows = l.perm + round_up_256((size_t)R * 4);
+  l.pos = l.perm + round_up_256((size_t)R * 4);
+  l.rows = l.pos + round_up_256((size_t)R * 4);
   l.h = l.rows + (lays_out_rows(nt) ? round_up_256((size_t)R * K) : 0);
   l.h_sf = l.h + round_up_256((size_t)R * I);
   l.part = l.h_sf + round_up_256((size_t)R * (size_t)ceil_div(I, kGroup));
-  l.total = l.part + round_up_256((size_t)R * N * 4);
+  l.part_sf = l.part + round_up_256((size_t)R * N * 2);
+  l.total = l.part_sf + round_up_256((size_t)R * (size_t)ceil_div(N, 32));
   return l;
 }
 
@@ -956,6 +1034,7 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   int32_t* n_tiles = reinterpret_cast<int32_t*>(base);
   Tile* tiles = reinterpret_cast<Tile*>(base + l.tiles);
   int32_t* perm = reinterpret_cast<int32_t*>(base + l.perm);
+  int32_t* pos = reinterpret_cast<int32_t*>(base + l.pos);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -968,7 +1047,8 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   W4Args g = {};
   cudaError_t e = watchdog_address(&g.wd);
   if (e != cudaSuccess) return e;
-  e = cudaLaunchKernelEx(&cfg, w4_plan_kernel, ids, (int)R, E, nt, tiles, n_tiles, perm, err_flag);
+  e = cudaLaunchKernelEx(&cfg, w4_plan_kernel, ids, (int)R, E, nt, tiles, n_tiles, perm, pos,
+                         err_flag);
   if (e != cudaSuccess) return e;
   const uint8_t* rows = a;
   int64_t n_rows = T;
@@ -985,7 +1065,6 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   g.tiles = tiles;
   g.n_tiles = n_tiles;
   g.perm = perm;
-  g.wt = wt;
   g.k = k;
   const int64_t most = most_tiles(R, E, nt);
   // Gate and up.
@@ -1006,8 +1085,9 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   g.w = w2;
   g.a_sf = base + l.h_sf;
   g.out = base + l.part;
-  g.out_sf = nullptr;
+  g.out_sf = base + l.part_sf;
   g.N = N;
+  g.NG = (int)R;
   g.KG = g.KB = (int)ceil_div(I, kGroup);
   g.NB = (int)ceil_div(N, 128);
   g.splits = nt == 16 ? pick_splits(most * g.NB, g.KB, 2 * num_sms) : 1;
@@ -1019,8 +1099,9 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   const int64_t items = T * chunks;
   cfg.gridDim = dim3((unsigned)ceil_div(items, 256), 1, 1);
   cfg.blockDim = dim3(256, 1, 1);
-  return cudaLaunchKernelEx(&cfg, w4_join_kernel, reinterpret_cast<const float*>(base + l.part), ids,
-                            static_cast<uint4*>(out), items, chunks, k, E);
+  return cudaLaunchKernelEx(&cfg, w4_join_kernel, reinterpret_cast<const uint4*>(base + l.part),
+                            reinterpret_cast<const uint8_t*>(base + l.part_sf), pos, wt,
+                            static_cast<uint4*>(out), items, chunks, k, R);
 }
 
 }  // namespace mxq

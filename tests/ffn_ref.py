@@ -117,8 +117,10 @@ def quant_with_slack(h, err):
 
 def experts(a, ids, wt, w13, w2):
     """a [T, K], ids/wt [T, k], w13 [E, 2, I, K], w2 [E, N, I], all float64 -> (out, tolerance).  The tolerance
-    takes 1e-5 of the magnitudes for each product's FP32 sums, what these can move the 8-bit codes in
-    between, and half a BF16 step."""
+    takes 1e-5 of the magnitudes for each product's FP32 sums, what these and the fast exponential and quotient
+    (2^-22 + 2^-23 |g| and 2^-22, on operands that are off by 2^-24: below 2^-20 + 2^-22 |g| of h) can move the 8-bit
+    codes in between, half a step of a weighted result (a step is 2^-13 of the largest of 32 columns at most, which the
+    other errors can raise to the next power of two) and half a BF16 step."""
     T, N = a.shape[0], w2.shape[1]
     out, tol = np.zeros((T, N)), np.zeros((T, N))
     for e in range(w2.shape[0]):
@@ -129,10 +131,12 @@ def experts(a, ids, wt, w13, w2):
         u, su = linear(a[t], w13[e, 1])
         silu = g / (1 + np.exp(-g))
         h = silu * u
-        err = 1.1 * np.abs(u) * 1e-5 * sg + np.abs(silu) * 1e-5 * su + 2.0 ** -20 * np.abs(h)
+        err = 1.1 * np.abs(u) * 1e-5 * sg + np.abs(silu) * 1e-5 * su + (2.0 ** -20 + 2.0 ** -22 * np.abs(g)) * np.abs(h)
         q, slack = quant_with_slack(h, err)
         y, sy = linear(q, w2[e])
         w = wt[t, j][:, None]
+        off = 1e-5 * sy + slack @ np.abs(w2[e]).T
+        top = np.pad(np.abs(y) + off, ((0, 0), (0, -N % 32))).reshape(len(t), -1, 32).max(2)
         np.add.at(out, t, w * y)
-        np.add.at(tol, t, np.abs(w) * (1e-5 * sy + slack @ np.abs(w2[e]).T))
+        np.add.at(tol, t, np.abs(w) * (off + 2.0 ** -14 * np.repeat(top, 32, 1)[:, :N]))
     return out, tol + np.abs(out) * 2.0 ** -8 + 2.0 ** -126
