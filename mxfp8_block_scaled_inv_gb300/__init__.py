@@ -539,14 +539,40 @@ def mxq_attn(q, cache, block_table, seq_lens, q_start=None, page_size=64, window
     return out
 
 
-def _same_device(fn, first, *others):
-    """Refuses tensors of different devices, and a device that is not the current one (the library launches there)."""
-    i = first.device.index
-    for t in others:
-        if t is not None and t.device.index != i:
-            raise MxqError(fn, 2, "tensors of different devices")
-    if i != torch.cuda.current_device():
-        raise MxqError(fn, 2, f"the tensors are on cuda:{i}, the current device is another")
+# The current device, without torch's lazy-initialisation check where torch has that (a tensor on the device exists).
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _device_of(fn, t):
+    """The index of a tensor's device, which has to be the current one: the library launches there."""
+    dev = t.get_device()
+    if dev < 0:
+        raise MxqError(fn, 2, "the tensors must be CUDA tensors")
+    now = torch.cuda.current_device() if _current_device is None else _current_device()
+    if dev != now:
+        raise MxqError(fn, 2, f"the tensors are on cuda:{dev}, the current device is cuda:{now}")
+    return dev
+
+
+def _on(fn, name, t, dtype, shape, dev):
+    """The address of a contiguous tensor of exactly this dtype, shape and device; refuses others."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise MxqError(fn, 2, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, not "
+                          f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', strided'}")
+
+
+def _stream_on(stream, dev):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(dev)
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _err_on(fn, t, dev):
+    """The address of an int32 tensor of one element at least, or None."""
+    return None if t is None else _on(fn, "err_flag", t, torch.int32, t.shape if t.numel() else (1,), dev)
 
 
 def mxq_add_rms_norm(x, weight=None, eps=1e-6, residual=None, residual_out=None, y=None, q=None, sc=None,
@@ -558,35 +584,42 @@ def mxq_add_rms_norm(x, weight=None, eps=1e-6, residual=None, residual_out=None,
     [..., D] and E8M0 scales uint8 [..., ceil(D/128)] of y, as mxq_inv_rope_group_quant's, unless
     want_codes is false.  y, q and sc, where given, receive them."""
     fn = "mxq_add_rms_norm"
-    px = _tensor(fn, "x", x, torch.bfloat16)
-    shape = tuple(x.shape)
+    dev = _device_of(fn, x)
+    shape = x.shape
     if not shape:
         raise MxqError(fn, 2, "x has no dimension")
     D = shape[-1]
     T = x.numel() // D if D else 0
-    _same_device(fn, x, weight, residual, residual_out, y, q, sc)
-    pw = _tensor(fn, "weight", weight, torch.bfloat16, (D,))
-    pres = pout = None
+    px = _on(fn, "x", x, torch.bfloat16, shape, dev)
+    pw = None if weight is None else _on(fn, "weight", weight, torch.bfloat16, (D,), dev)
+    pres = pout = py = pq = psc = None
     if residual is not None:
-        pres = _tensor(fn, "residual", residual, torch.bfloat16, shape)
+        pres = _on(fn, "residual", residual, torch.bfloat16, shape, dev)
         if residual_out is None:
-            residual_out = _empty(stream, shape, torch.bfloat16, x.device)
-        pout = _tensor(fn, "residual_out", residual_out, torch.bfloat16, shape)
+            residual_out = torch.empty_like(x) if stream is None else _empty_like(stream, x)
+            pout = residual_out.data_ptr()
+        else:
+            pout = _on(fn, "residual_out", residual_out, torch.bfloat16, shape, dev)
     elif residual_out is not None:
         raise MxqError(fn, 2, "residual_out without residual")
-    if want_y and y is None:
-        y = _empty(stream, shape, torch.bfloat16, x.device)
-    py = _tensor(fn, "y", y, torch.bfloat16, shape)
-    pq = psc = None
+    if y is not None:
+        py = _on(fn, "y", y, torch.bfloat16, shape, dev)
+    elif want_y:
+        y = torch.empty_like(x) if stream is None else _empty_like(stream, x)
+        py = y.data_ptr()
     if want_codes or q is not None or sc is not None:
         sshape = (*shape[:-1], (D + 127) // 128)
         if q is None:
             q = _empty(stream, shape, torch.uint8, x.device)
+            pq = q.data_ptr()
+        else:
+            pq = _on(fn, "q", q, torch.uint8, shape, dev)
         if sc is None:
             sc = _empty(stream, sshape, torch.uint8, x.device)
-        pq = _tensor(fn, "q", q, torch.uint8, shape)
-        psc = _tensor(fn, "sc", sc, torch.uint8, sshape)
-    st = lib().mxq_add_rms_norm(px, pres, pout, pw, T, D, eps, py, pq, psc, _stream_of(stream, x.device))
+            psc = sc.data_ptr()
+        else:
+            psc = _on(fn, "sc", sc, torch.uint8, sshape, dev)
+    st = lib().mxq_add_rms_norm(px, pres, pout, pw, T, D, eps, py, pq, psc, _stream_on(stream, dev))
     if st:
         _check(fn, st)
     return residual_out, y, q, sc
@@ -600,21 +633,28 @@ def mxq_route(logits, k, scoring="softmax", bias=None, groups=1, topk_groups=1, 
     only; with topk_groups < groups only the experts of the best groups (by the sum of their group_top best)
     take part.  Ids run from the best down, -1 where masked logits (-infinity, NaN) leave none."""
     fn = "mxq_route"
-    T, E = logits.shape
+    dev = _device_of(fn, logits)
+    T, E = shape = logits.shape
     dtype = MXQ_LOGITS_BF16 if logits.dtype is torch.bfloat16 else MXQ_LOGITS_F32
-    pl = _tensor(fn, "logits", logits, torch.bfloat16 if dtype else torch.float32)
-    _same_device(fn, logits, bias, ids, weights)
-    if scoring not in MXQ_SCORES:
+    pl = _on(fn, "logits", logits, torch.bfloat16 if dtype else torch.float32, shape, dev)
+    score = MXQ_SCORES.get(scoring)
+    if score is None:
         raise MxqError(fn, 4, f"scoring must be one of {sorted(MXQ_SCORES)}")
-    pb = _tensor(fn, "bias", bias, torch.float32, (E,))
+    pb = None if bias is None else _on(fn, "bias", bias, torch.float32, (E,), dev)
+    if k < 1:
+        raise MxqError(fn, 2, f"k must be 1 at least (k={k})")
     if ids is None:
-        ids = _empty(stream, (T, max(k, 0)), torch.int32, logits.device)
+        ids = _empty(stream, (T, k), torch.int32, logits.device)
+        pi = ids.data_ptr()
+    else:
+        pi = _on(fn, "ids", ids, torch.int32, (T, k), dev)
     if weights is None:
-        weights = _empty(stream, (T, max(k, 0)), torch.float32, logits.device)
-    pi = _tensor(fn, "ids", ids, torch.int32, (T, k))
-    pw = _tensor(fn, "weights", weights, torch.float32, (T, k))
-    st = lib().mxq_route(pl, dtype, T, E, pb, k, MXQ_SCORES[scoring], groups, topk_groups, group_top,
-                         1 if renormalise else 0, scale, pi, pw, _stream_of(stream, logits.device))
+        weights = _empty(stream, (T, k), torch.float32, logits.device)
+        pw = weights.data_ptr()
+    else:
+        pw = _on(fn, "weights", weights, torch.float32, (T, k), dev)
+    st = lib().mxq_route(pl, dtype, T, E, pb, k, score, groups, topk_groups, group_top, 1 if renormalise else 0,
+                         scale, pi, pw, _stream_on(stream, dev))
     if st:
         _check(fn, st)
     return ids, weights
@@ -629,18 +669,20 @@ def mxq_prepare_w4(w, w_e8m0, out=None, stream=None):
     """Load-time layout of 4-bit weights: w uint8 [B, N, K/2] or [N, K/2] (E2M1 codes, two per byte) with
     w_e8m0 uint8 [.., N, K/32] -> the bytes that mxq_linear_a8w4 (B = 1) and mxq_experts_a8w4 read."""
     fn = "mxq_prepare_w4"
+    dev = _device_of(fn, w)
     if w.dim() not in (2, 3):
         raise MxqError(fn, 2, f"w has shape {tuple(w.shape)}, not [B, N, K/2] or [N, K/2]")
     *lead, N, half = w.shape
     B, K = (lead[0] if lead else 1), 2 * half
-    pw = _tensor(fn, "w", w, torch.uint8)
-    ps = _tensor(fn, "w_e8m0", w_e8m0, torch.uint8, (*lead, N, K // 32))
-    _same_device(fn, w, w_e8m0, out)
+    pw = _on(fn, "w", w, torch.uint8, w.shape, dev)
+    ps = _on(fn, "w_e8m0", w_e8m0, torch.uint8, (*lead, N, K // 32), dev)
     need = mxq_w4_bytes(B, N, K)
     if out is None:
         out = _empty(stream, need, torch.uint8, w.device)
-    po = _tensor(fn, "out", out, torch.uint8, (need,))
-    st = lib().mxq_prepare_w4(pw, ps, B, N, K, po, _stream_of(stream, w.device))
+        po = out.data_ptr()
+    else:
+        po = _on(fn, "out", out, torch.uint8, (need,), dev)
+    st = lib().mxq_prepare_w4(pw, ps, B, N, K, po, _stream_on(stream, dev))
     if st:
         _check(fn, st)
     return out
@@ -650,16 +692,18 @@ def mxq_linear_a8w4(a, a_sf, w4, N, out=None, stream=None):
     """a uint8 [T, K] E4M3 codes, a_sf uint8 [T, ceil(K/128)], w4 from mxq_prepare_w4 of a weight [N, K]
     -> out bf16 [T, N]."""
     fn = "mxq_linear_a8w4"
-    T, K = a.shape
-    pa = _tensor(fn, "a", a, torch.uint8)
-    ps = _tensor(fn, "a_sf", a_sf, torch.uint8, (T, (K + 127) // 128))
+    dev = _device_of(fn, a)
+    T, K = shape = a.shape
     L = lib()
-    pw = _tensor(fn, "w4", w4, torch.uint8, (L.mxq_w4_bytes(1, N, K),))
-    _same_device(fn, a, a_sf, w4, out)
+    pa = _on(fn, "a", a, torch.uint8, shape, dev)
+    ps = _on(fn, "a_sf", a_sf, torch.uint8, (T, (K + 127) // 128), dev)
+    pw = _on(fn, "w4", w4, torch.uint8, (L.mxq_w4_bytes(1, N, K),), dev)
     if out is None:
         out = _empty(stream, (T, N), torch.bfloat16, a.device)
-    po = _tensor(fn, "out", out, torch.bfloat16, (T, N))
-    st = L.mxq_linear_a8w4(pa, ps, pw, po, T, N, K, _stream_of(stream, a.device))
+        po = out.data_ptr()
+    else:
+        po = _on(fn, "out", out, torch.bfloat16, (T, N), dev)
+    st = L.mxq_linear_a8w4(pa, ps, pw, po, T, N, K, _stream_on(stream, dev))
     if st:
         _check(fn, st)
     return out
@@ -676,33 +720,37 @@ def mxq_experts_a8w4(a, a_sf, ids, weights, w13, w2, I, N=None, out=None, ws=Non
     rows, then its up rows), w2 from mxq_prepare_w4 of [E, N, I] -> out bf16 [T, N] (N: K unless given).
     `ws` (mxq_experts_workspace_bytes) is allocated when not given; concurrent calls need distinct workspaces."""
     fn = "mxq_experts_a8w4"
-    T, K = a.shape
+    dev = _device_of(fn, a)
+    T, K = shape = a.shape
     k = ids.shape[-1]
     if N is None:
         N = K
-    pa = _tensor(fn, "a", a, torch.uint8)
-    ps = _tensor(fn, "a_sf", a_sf, torch.uint8, (T, (K + 127) // 128))
-    pi = _tensor(fn, "ids", ids, torch.int32, (T, k))
-    pwt = _tensor(fn, "weights", weights, torch.float32, (T, k))
     L = lib()
     one13, one2 = L.mxq_w4_bytes(2, I, K), L.mxq_w4_bytes(1, N, I)
     if not one13 or not one2:
         raise MxqError(fn, 2, f"no expert weights of K={K}, I={I}, N={N}: K and I must be multiples of 32")
     E = w2.numel() // one2
-    p13 = _tensor(fn, "w13", w13, torch.uint8, (E * one13,))
-    p2 = _tensor(fn, "w2", w2, torch.uint8, (E * one2,))
-    _same_device(fn, a, a_sf, ids, weights, w13, w2, out, ws, err_flag)
+    pa = _on(fn, "a", a, torch.uint8, shape, dev)
+    ps = _on(fn, "a_sf", a_sf, torch.uint8, (T, (K + 127) // 128), dev)
+    pi = _on(fn, "ids", ids, torch.int32, (T, k), dev)
+    pwt = _on(fn, "weights", weights, torch.float32, (T, k), dev)
+    p13 = _on(fn, "w13", w13, torch.uint8, (E * one13,), dev)
+    p2 = _on(fn, "w2", w2, torch.uint8, (E * one2,), dev)
     if out is None:
         out = _empty(stream, (T, N), torch.bfloat16, a.device)
-    po = _tensor(fn, "out", out, torch.bfloat16, (T, N))
+        po = out.data_ptr()
+    else:
+        po = _on(fn, "out", out, torch.bfloat16, (T, N), dev)
+    pws, nws = None, 0
     if ws is None:
-        need = L.mxq_experts_workspace_bytes(T, k, E, K, I, N)
-        if need > 0:
-            ws = _empty(stream, need, torch.uint8, a.device)
-    pws, nws = (None, 0) if ws is None else (_tensor(fn, "ws", ws, torch.uint8), ws.numel())
-    perr = None if err_flag is None else _word(fn, "err_flag", err_flag, torch.int32)
-    st = L.mxq_experts_a8w4(pa, ps, pi, pwt, p13, p2, po, T, k, E, K, I, N, perr, pws, nws,
-                            _stream_of(stream, a.device))
+        nws = L.mxq_experts_workspace_bytes(T, k, E, K, I, N)
+        if nws > 0:
+            ws = _empty(stream, nws, torch.uint8, a.device)
+            pws = ws.data_ptr()
+    else:
+        pws, nws = _on(fn, "ws", ws, torch.uint8, ws.shape, dev), ws.numel()
+    st = L.mxq_experts_a8w4(pa, ps, pi, pwt, p13, p2, po, T, k, E, K, I, N, _err_on(fn, err_flag, dev), pws, nws,
+                            _stream_on(stream, dev))
     if st:
         _check(fn, st)
     return out
