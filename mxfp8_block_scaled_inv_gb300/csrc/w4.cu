@@ -81,8 +81,11 @@ enum Mode { kLinear = 0, kGateUp = 1, kDown = 2 };
 
 // Device-side plan of a routed call: which sorted rows each tile holds.
 struct alignas(16) Tile {
-  int32_t expert, row0, count, pad;
+  int32_t expert, row0, count;
+  uint32_t pairs;  // kSmall calls: bit i: pair i (token * k + choice) is one of its rows
 };
+// Pairs of a call that needs no plan: a warp sorts them in its registers.
+constexpr int kSmallPairs = 16;
 
 struct W4Args {
   const uint8_t* w;       // prepared weight
@@ -96,7 +99,84 @@ struct W4Args {
   int T, N, KG, KB, NB, NG, k;
   int per_tile, n_tiles_host;  // kLinear: tokens of a tile, tiles
   int splits, kb_per_split;
+  // kSmall calls: ids instead of a plan; the gate and up product brings w2 into L2
+  // and clears the counters (one for each 128 columns of the output), with which
+  // the down product's CTAs find the last of them, which sums their results.
+  const int32_t* ids;
+  const float* wt;
+  int32_t* err_flag;
+  const uint8_t* w2;
+  uint32_t* arrived;
+  __nv_bfloat16* y;
+  int E, KB2, NB2;
 };
+
+// The up to 16 pairs of a small call, sorted by expert in a warp's registers.
+struct Pairs {
+  int id;            // of pair `lane`
+  bool valid;
+  uint32_t peers;    // the pairs with the same expert
+  uint32_t valids, leaders;  // valid pairs; the first pair of each expert
+
+  __device__ __forceinline__ void load(const W4Args& p, int lane) {
+    const int n = p.T * p.k;
+    id = lane < n ? p.ids[lane] : -1;
+    valid = id >= 0 && id < p.E;
+    peers = __match_any_sync(0xffffffffu, valid ? id : -1 - lane);
+    valids = __ballot_sync(0xffffffffu, valid);
+    leaders = __ballot_sync(0xffffffffu, valid && (peers & ((1u << lane) - 1u)) == 0u);
+  }
+  // Pairs of the experts before the one that pair `leader` leads.
+  __device__ __forceinline__ int before(int leader) const {
+    return __popc(__ballot_sync(0xffffffffu, valid && __ffs(peers) - 1 < leader));
+  }
+  __device__ __forceinline__ Tile tile(int j) const {
+    uint32_t m = leaders;
+    for (int i = 0; i < j; ++i) m &= m - 1u;
+    const int l = __ffs(m) - 1;
+    Tile t;
+    t.expert = __shfl_sync(0xffffffffu, id, l);
+    t.pairs = __shfl_sync(0xffffffffu, peers, l);
+    t.count = __popc(t.pairs);
+    t.row0 = before(l);
+    return t;
+  }
+  static __device__ __forceinline__ int row(const Tile& t, int i) {
+    uint32_t m = t.pairs;
+    for (; i > 0; --i) m &= m - 1u;
+    return __ffs(m) - 1;
+  }
+  // The sorted row of pair `lane`.
+  __device__ __forceinline__ int place(int lane) const {
+    int r = 0;
+    for (int l = 0; l < kSmallPairs; ++l) {
+      const uint32_t o = __shfl_sync(0xffffffffu, peers, l);
+      if ((valids >> l) & 1u) r += __ffs(o) < __ffs(peers) || (o == peers && l < lane) ? 1 : 0;
+    }
+    return r;
+  }
+};
+
+// Eight results of 16 bits with their exponent, times g, added to y.
+__device__ __forceinline__ void add_held16(float (&y)[8], const uint4& v, uint32_t ef, float g) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (ef != 255u) {
+    const float s = __uint_as_float((ef - 13u) << 23);  // 2^(ef - 140)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      // The integer plus 2^15 as the low bits of 2^23.
+      const uint32_t u = w[q] ^ 0x80008000u;
+      y[2 * q] = fmaf((__uint_as_float(0x4B000000u | (u & 0xFFFFu)) - 8421376.0f) * s, g, y[2 * q]);
+      y[2 * q + 1] = fmaf((__uint_as_float(0x4B000000u | (u >> 16)) - 8421376.0f) * s, g, y[2 * q + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      y[2 * q] = fmaf(bf16_lo(w[q]), g, y[2 * q]);
+      y[2 * q + 1] = fmaf(bf16_hi(w[q]), g, y[2 * q + 1]);
+    }
+  }
+}
 
 // Shape of an instance.  GATHER: the token rows are fetched by index.
 template <int MODE, int NT, bool SPLIT>
@@ -273,7 +353,32 @@ __device__ __forceinline__ void finish_token(const W4Args& p, const float (&v)[N
   }
 }
 
-template <int MODE, int NT, bool SPLIT>
+// A small call's sum over each token's choices for 128 columns, once all of its
+// experts' results are there: called by `threads` threads (whole warps) of the CTA
+// that arrived last.
+__device__ __forceinline__ void join_small(const W4Args& p, const Pairs& pairs, int rb, int tid,
+                                           int threads) {
+  const int lane = tid & 31, place = pairs.place(lane);
+  const int items = p.T * 16;  // 8 columns of a token each
+  for (int i0 = tid - lane; i0 < items; i0 += threads) {
+    const int i = i0 + lane, t = i >> 4, n = rb * 128 + (i & 15) * 8;
+    const bool in = i < items && n < p.N;
+    float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < p.k; ++j) {
+      const int pair = min(t * p.k + j, kSmallPairs - 1);
+      const int row = __shfl_sync(0xffffffffu, place, pair);
+      if (!in || !((pairs.valids >> pair) & 1u)) continue;
+      const uint4 v = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.out) +
+                                                            (size_t)row * p.N + n));
+      const uint32_t ef = __ldcg(p.out_sf + (size_t)(n >> 5) * p.NG + row);
+      add_held16(y, v, ef, p.wt[pair]);
+    }
+    if (in) *reinterpret_cast<uint4*>(p.y + (size_t)t * p.N + n) = to_bf16x8(y);
+  }
+}
+
+// SMALL: a routed call of at most kSmallPairs rows.
+template <int MODE, int NT, bool SPLIT, bool SMALL>
 __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, SPLIT>::CTAS))
     w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
               const W4Args p) {
@@ -290,6 +395,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
   uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(slot + 1);
   volatile int* issued = reinterpret_cast<volatile int*>(slot + 2);  // [0] warp 0, [1] warp 2
+  volatile int* last = reinterpret_cast<volatile int*>(slot + 4);    // this CTA sums the results
 
   // (Broadcast: the compiler then knows that a warp's role and what follows from
   // it are the same in all lanes, and keeps the operands of copies and MMAs in
@@ -302,6 +408,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
   const int nk = SPLIT ? max(0, min(p.KB - kb0, p.kb_per_split)) : p.KB;
   const int u_first = SPLIT ? (int)(blockIdx.x / (uint32_t)p.splits) : (int)blockIdx.x;
   int units;
+  Pairs pairs;
   if constexpr (MODE == kLinear) {
     units = p.n_tiles_host * p.NB;
     // The weight does not depend on what runs before: bring the first blocks
@@ -310,6 +417,22 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
       ptx::prefetch_l2_bulk(p.w + ((size_t)(u_first % p.NB) * p.KB + kb0 + lane) * kBlockBytes,
                             kBlockBytes);
     ptx::griddep_wait();
+  } else if constexpr (SMALL) {
+    ptx::griddep_wait();
+    pairs.load(p, lane);
+    units = __popc(pairs.leaders) * p.NB;
+    if constexpr (MODE == kGateUp) {
+      if (blockIdx.x == 0) {
+        for (int i = threadIdx.x; i < p.NB2; i += C::THREADS) p.arrived[i] = 0u;
+        if (warp == 0 && p.err_flag != nullptr && !pairs.valid && pairs.id != -1)
+          atomicOr(p.err_flag, MXQ_DEVERR_EXPERT);
+      }
+    } else if (units == 0) {  // no token has an expert
+      const int64_t chunks = (int64_t)p.T * p.N / 8;
+      for (int64_t i = (int64_t)blockIdx.x * C::THREADS + threadIdx.x; i < chunks;
+           i += (int64_t)gridDim.x * C::THREADS)
+        reinterpret_cast<uint4*>(p.y)[i] = make_uint4(0, 0, 0, 0);
+    }
   } else {
     ptx::griddep_wait();
     units = *p.n_tiles * p.NB;
@@ -325,6 +448,8 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
       t.expert = 0;
       t.row0 = (u / p.NB) * p.per_tile;
       t.count = min(p.per_tile, p.T - t.row0);
+    } else if constexpr (SMALL) {
+      t = pairs.tile(u / p.NB);
     } else {
       const int4 v = *reinterpret_cast<const int4*>(p.tiles + u / p.NB);
       t.expert = __shfl_sync(0xffffffffu, v.x, 0);
@@ -332,6 +457,11 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
       t.count = __shfl_sync(0xffffffffu, v.z, 0);
     }
     return t;
+  };
+  // The pair (token * k + choice) of row i of a tile.
+  auto pair_of = [&](const Tile& t, int i) {
+    if constexpr (SMALL) return Pairs::row(t, i);
+    else return (int)p.perm[t.row0 + i];
   };
 
   if (threadIdx.x == 0) {
@@ -409,6 +539,18 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
         __syncwarp();
       }
     }
+    if constexpr (SMALL && MODE == kGateUp) {
+      // What is left to read is the experts' w2: each of an expert's CTAs brings
+      // its share into L2.
+      for (int u = u_first; u < units; u += u_step) {
+        const int64_t blocks = (int64_t)p.NB2 * p.KB2;
+        const int parts = p.NB * p.splits, part = (u % p.NB) * p.splits + split;
+        const int64_t b0 = blocks * part / parts, b1 = blocks * (part + 1) / parts;
+        const uint8_t* w2 = p.w2 + (size_t)tile_of(u).expert * blocks * kBlockBytes;
+        for (int64_t b = b0 + lane; b < b1; b += 32)
+          ptx::prefetch_l2_bulk(w2 + b * kBlockBytes, kBlockBytes);
+      }
+    }
     if (lane == 0) issued[0] = it;
   } else if (warp == 2) {
     // ------------------------------------- token scales (and gathered rows)
@@ -427,13 +569,14 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) {
         // Rows past the last stand for it: their columns are not stored.
-        const int i = t.row0 + min(32 * j + lane, t.count - 1);
-        r.src[j] = p.a_sf + (size_t)(MODE == kGateUp ? p.perm[i] / p.k : i) * p.KG + kb0;
+        const int i = min(32 * j + lane, t.count - 1);
+        r.src[j] = p.a_sf +
+                   (size_t)(MODE == kGateUp ? pair_of(t, i) / p.k : t.row0 + i) * p.KG + kb0;
       }
       if constexpr (C::GATHER) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          r.g4[i] = p.perm[t.row0 + min(4 * lane + i, t.count - 1)] / p.k;
+          r.g4[i] = pair_of(t, min(4 * lane + i, t.count - 1)) / p.k;
       }
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) r.byte[j] = nk > 0 ? r.src[j][0] : 127u;
@@ -566,6 +709,18 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&acc_empty[buf]);
         }
+        if constexpr (SMALL && MODE == kDown) {
+          static_assert(C::GROUPS == 1, "the group is the epilogue");
+          __threadfence();  // the results, before the arrival
+          ptx::named_sync(1, 128);
+          if (warp == 4 && lane == 0)
+            *last = atomicAdd(p.arrived + rb, 1u) == (uint32_t)(units / p.NB) - 1u;
+          ptx::named_sync(1, 128);
+          if (*last) {
+            __threadfence();
+            join_small(p, pairs, rb, (int)threadIdx.x - 128, 128);
+          }
+        }
       }
     }
     __syncthreads();
@@ -625,6 +780,17 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
           }
         }
         finish_token<MODE, NA>(p, v, t.row0 + first + tl, rb, sub, in);
+      }
+      if constexpr (SMALL && MODE == kDown) {
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0)
+          *last = atomicAdd(p.arrived + rb, 1u) == (uint32_t)(units / p.NB * p.splits) - 1u;
+        __syncthreads();
+        if (*last) {
+          __threadfence();
+          join_small(p, pairs, rb, (int)threadIdx.x, C::THREADS);
+        }
       }
     }
   }
@@ -715,7 +881,7 @@ __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* id
       t.expert = tid;
       t.row0 = row0 + i * rows;
       t.count = min(rows, c - i * rows);
-      t.pad = 0;
+      t.pairs = 0u;
       tiles[tile0 + i] = t;
     }
   }
@@ -788,23 +954,7 @@ __global__ void __launch_bounds__(256) w4_join_kernel(const uint4* part, const u
     const uint4 v = part[(size_t)row * chunks + c];
     const uint32_t ef = part_sf[(c >> 2) * R + row];
     const float g = wt[t * k + j];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    if (ef != 255u) {
-      const float s = __uint_as_float((ef - 13u) << 23);  // 2^(ef - 140)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        // The integer plus 2^15 as the low bits of 2^23.
-        const uint32_t u = w[q] ^ 0x80008000u;
-        y[2 * q] = fmaf((__uint_as_float(0x4B000000u | (u & 0xFFFFu)) - 8421376.0f) * s, g, y[2 * q]);
-        y[2 * q + 1] = fmaf((__uint_as_float(0x4B000000u | (u >> 16)) - 8421376.0f) * s, g, y[2 * q + 1]);
-      }
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        y[2 * q] = fmaf(bf16_lo(w[q]), g, y[2 * q]);
-        y[2 * q + 1] = fmaf(bf16_hi(w[q]), g, y[2 * q + 1]);
-      }
-    }
+    add_held16(y, v, ef, g);
   }
   out[it] = to_bf16x8(y);
 }
@@ -871,7 +1021,7 @@ bool encode_rows(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, ui
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, int NT, bool SPLIT>
+template <int MODE, int NT, bool SPLIT, bool SMALL = false>
 cudaError_t launch_cfg(const void* a, uint64_t a_rows, uint64_t K, uint64_t blocks, W4Args args,
                        int64_t units, int num_sms, cudaStream_t s, const char** why) {
   using C = Cfg<MODE, NT, SPLIT>;
@@ -881,7 +1031,7 @@ cudaError_t launch_cfg(const void* a, uint64_t a_rows, uint64_t K, uint64_t bloc
     *why = "cuTensorMapEncodeTiled failed (driver entry point missing or arguments rejected)";
     return cudaErrorInvalidValue;
   }
-  auto kern = w4_kernel<MODE, NT, SPLIT>;
+  auto kern = w4_kernel<MODE, NT, SPLIT, SMALL>;
   static std::atomic<uint64_t> smem_set{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -919,6 +1069,12 @@ template <int MODE>
 cudaError_t launch_tokens(int nt, const void* a, uint64_t a_rows, uint64_t K, uint64_t blocks,
                           const W4Args& g, int64_t units, int num_sms, cudaStream_t s,
                           const char** why) {
+  if constexpr (MODE != kLinear) {
+    if (g.ids != nullptr)
+      return g.splits > 1
+                 ? launch_cfg<MODE, 16, true, true>(a, a_rows, K, blocks, g, units, num_sms, s, why)
+                 : launch_cfg<MODE, 16, false, true>(a, a_rows, K, blocks, g, units, num_sms, s, why);
+  }
   if (nt <= 16)
     return g.splits > 1 ? launch_cfg<MODE, 16, true>(a, a_rows, K, blocks, g, units, num_sms, s, why)
                         : launch_cfg<MODE, 16, false>(a, a_rows, K, blocks, g, units, num_sms, s, why);
@@ -997,6 +1153,7 @@ namespace {
 // some experts take two tiles, which read their weights twice (from L2).
 int expert_tile(int64_t R, int E) {
   const int64_t avg = ceil_div(R, E);
+  if (R <= kSmallPairs) return 16;
   return avg <= 8 ? 16 : avg <= 16 ? 32 : avg <= 40 ? 64 : avg <= 80 ? 128 : kMaxTokens;
 }
 // An expert of c rows has ceil(c / nt) tiles at most (fewer where even tiles
@@ -1011,7 +1168,9 @@ ExpertsLayout experts_layout(int64_t T, int k, int E, int K, int I, int N) {
   const int64_t R = T * k;
   const int nt = expert_tile(R, E);
   ExpertsLayout l;
-  l.tiles = 256;  // the numbers of tiles and of rows lie before them
+  // The numbers of tiles and of rows lie first, or (a small call's) arrivals.
+  l.arrived = 0;
+  l.tiles = R <= kSmallPairs ? round_up_256((size_t)ceil_div(N, 128) * 4) : 256;
   l.perm = l.tiles + round_up_256((size_t)most_tiles(R, E, nt) * sizeof(Tile));
   l.pos = l.perm + round_up_256((size_t)R * 4);
   l.rows = l.pos + round_up_256((size_t)R * 4);
@@ -1047,7 +1206,20 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   W4Args g = {};
   cudaError_t e = watchdog_address(&g.wd);
   if (e != cudaSuccess) return e;
-  e = cudaLaunchKernelEx(&cfg, w4_plan_kernel, ids, (int)R, E, nt, tiles, n_tiles, perm, pos,
+  const bool small = R <= kSmallPairs;  // no plan, and no sum by a kernel of its own
+  if (small) {
+    g.ids = ids;
+    g.wt = wt;
+    g.err_flag = err_flag;
+    g.w2 = w2;
+    g.arrived = reinterpret_cast<uint32_t*>(base + l.arrived);
+    g.y = static_cast<__nv_bfloat16*>(out);
+    g.E = E;
+    g.KB2 = (int)ceil_div(I, kGroup);
+    g.NB2 = (int)ceil_div(N, 128);
+  }
+  if (!small)
+    e = cudaLaunchKernelEx(&cfg, w4_plan_kernel, ids, (int)R, E, nt, tiles, n_tiles, perm, pos,
                          err_flag);
   if (e != cudaSuccess) return e;
   const uint8_t* rows = a;
@@ -1094,7 +1266,7 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   g.kb_per_split = (int)ceil_div(g.KB, g.splits);
   e = launch_tokens<kDown>(nt, base + l.h, (uint64_t)R, (uint64_t)I, (uint64_t)E * g.NB * g.KB, g,
                            most * g.NB, num_sms, s, why);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || small) return e;
   const int chunks = N / 8;
   const int64_t items = T * chunks;
   cfg.gridDim = dim3((unsigned)ceil_div(items, 256), 1, 1);

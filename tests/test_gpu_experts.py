@@ -80,7 +80,25 @@ def test_against_reference(mxq, T, k, E, K, I, N):
     check(layer, a, asf, ids, wt, out)
 
 
-@pytest.mark.parametrize("T", [5, 40, 300])
+@pytest.mark.parametrize("T,k,E,K,I,N", [(1, 8, 128, 512, 256, 512), (1, 16, 16, 4096, 128, 1040), (2, 8, 3, 288, 96, 4096),
+                                         (16, 1, 2, 1024, 416, 144), (5, 3, 200, 96, 1024, 80), (3, 5, 1, 640, 32, 272),
+                                         (1, 17, 40, 256, 128, 256)])
+def test_up_to_sixteen_pairs(mxq, T, k, E, K, I, N):
+    """Calls small enough to go without a plan and a sum of their own, and the first that are not."""
+    layer = Layer(mxq, E, K, I, N, seed=T + K + E)
+    a, asf = unit_acts(T, K, seed=T + 1)
+    ids = rng(T + 2).integers(-1, E, (T, k)).astype(np.int32)
+    wt = rng(T + 3).random((T, k)).astype(np.float32)
+    ws = torch.full((mxq.mxq_experts_workspace_bytes(T, k, E, K, I, N),), 0xFF, dtype=torch.uint8, device="cuda")
+    for _ in range(2):  # the second finds the first one's arrivals
+        out = layer(a, asf, ids, wt, ws=ws)
+        check(layer, a, asf, ids, wt, out)
+        ids[0] = rng(T + 4).permutation(ids[0])
+    out = layer(a, asf, np.full_like(ids, -1), wt, ws=ws)
+    assert int(out.count_nonzero()) == 0
+
+
+@pytest.mark.parametrize("T", [2, 5, 40, 300])
 def test_padding_bad_ids_and_repeats(mxq, T):
     E, K, I, N, k = 6, 256, 160, 272, 4
     layer = Layer(mxq, E, K, I, N, seed=1)
