@@ -82,10 +82,12 @@ enum Mode { kLinear = 0, kGateUp = 1, kDown = 2 };
 // Device-side plan of a routed call: which sorted rows each tile holds.
 struct alignas(16) Tile {
   int32_t expert, row0, count;
-  uint32_t pairs;  // kSmall calls: bit i: pair i (token * k + choice) is one of its rows
+  uint32_t pairs;  // small calls: bit i: pair i (token * k + choice) is one of its rows
 };
-// Pairs of a call that needs no plan: a warp sorts them in its registers.
+// Pairs and choices of a call that needs no plan: a warp sorts the pairs in its
+// registers.
 constexpr int kSmallPairs = 16;
+constexpr int kSmallChoices = 8;  // a cluster's CTAs
 
 struct W4Args {
   const uint8_t* w;       // prepared weight
@@ -99,15 +101,11 @@ struct W4Args {
   int T, N, KG, KB, NB, NG, k;
   int per_tile, n_tiles_host;  // kLinear: tokens of a tile, tiles
   int splits, kb_per_split;
-  // kSmall calls: ids instead of a plan; the gate and up product brings w2 into L2
-  // and clears the counters (one for each 128 columns of the output), with which
-  // the down product's CTAs find the last of them, which sums their results.
+  // Small calls: ids instead of a plan; the gate and up product brings w2 into L2.
   const int32_t* ids;
   const float* wt;
   int32_t* err_flag;
   const uint8_t* w2;
-  uint32_t* arrived;
-  __nv_bfloat16* y;
   int E, KB2, NB2;
 };
 
@@ -156,6 +154,9 @@ struct Pairs {
     return r;
   }
 };
+
+constexpr uint32_t kLeastExp = 14u;  // of held results (see held16); smaller ones lose bits below 2^-126
+constexpr int kJoinBatch = 8;  // results fetched at a time: their latencies overlap
 
 // Eight results of 16 bits with their exponent, times g, added to y.
 __device__ __forceinline__ void add_held16(float (&y)[8], const uint4& v, uint32_t ef, float g) {
@@ -239,7 +240,6 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 // see, and half the bytes of FP32 to write and read again.  m: exponent field of
 // the largest magnitude, which is below 2^(m - 126); the value is the integer
 // times 2^(m - 140).  With an infinity or a NaN among the 32 they are BF16 values.
-constexpr uint32_t kLeastExp = 14u;  // smaller ones lose bits below 2^-126
 __device__ __forceinline__ uint32_t held16(float y, uint32_t m) {
   const float inv = __uint_as_float((267u - max(m, kLeastExp)) << 23);  // 2^(140 - m)
   const uint32_t bits = __float_as_uint(fmaf(y, inv, 12582912.0f));     // the integer + 1.5 * 2^23
@@ -353,31 +353,11 @@ __device__ __forceinline__ void finish_token(const W4Args& p, const float (&v)[N
   }
 }
 
-// A small call's sum over each token's choices for 128 columns, once all of its
-// experts' results are there: called by `threads` threads (whole warps) of the CTA
-// that arrived last.
-__device__ __forceinline__ void join_small(const W4Args& p, const Pairs& pairs, int rb, int tid,
-                                           int threads) {
-  const int lane = tid & 31, place = pairs.place(lane);
-  const int items = p.T * 16;  // 8 columns of a token each
-  for (int i0 = tid - lane; i0 < items; i0 += threads) {
-    const int i = i0 + lane, t = i >> 4, n = rb * 128 + (i & 15) * 8;
-    const bool in = i < items && n < p.N;
-    float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (int j = 0; j < p.k; ++j) {
-      const int pair = min(t * p.k + j, kSmallPairs - 1);
-      const int row = __shfl_sync(0xffffffffu, place, pair);
-      if (!in || !((pairs.valids >> pair) & 1u)) continue;
-      const uint4 v = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.out) +
-                                                            (size_t)row * p.N + n));
-      const uint32_t ef = __ldcg(p.out_sf + (size_t)(n >> 5) * p.NG + row);
-      add_held16(y, v, ef, p.wt[pair]);
-    }
-    if (in) *reinterpret_cast<uint4*>(p.y + (size_t)t * p.N + n) = to_bf16x8(y);
-  }
-}
-
-// SMALL: a routed call of at most kSmallPairs rows.
+// SMALL: a routed call of at most kSmallPairs rows and kSmallChoices choices, whose
+// CTAs sort the rows themselves.  Its down product takes one token's 128 columns
+// for each cluster and one of the token's experts for each CTA, and adds the
+// experts' sums as a split K adds its parts: no results of single experts, and no
+// kernel to add them.
 template <int MODE, int NT, bool SPLIT, bool SMALL>
 __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, SPLIT>::CTAS))
     w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
@@ -395,7 +375,6 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
   uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(slot + 1);
   volatile int* issued = reinterpret_cast<volatile int*>(slot + 2);  // [0] warp 0, [1] warp 2
-  volatile int* last = reinterpret_cast<volatile int*>(slot + 4);    // this CTA sums the results
 
   // (Broadcast: the compiler then knows that a warp's role and what follows from
   // it are the same in all lanes, and keeps the operands of copies and MMAs in
@@ -404,8 +383,10 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
   ptx::griddep_launch_dependents();
 
   const int split = SPLIT ? (int)ptx::cluster_rank() : 0;
-  const int kb0 = SPLIT ? split * p.kb_per_split : 0;
-  const int nk = SPLIT ? max(0, min(p.KB - kb0, p.kb_per_split)) : p.KB;
+  constexpr bool BY_CHOICE = SMALL && MODE == kDown;  // a cluster's CTAs are a token's choices
+  static_assert(!BY_CHOICE || SPLIT, "choices are summed over a cluster");
+  const int kb0 = SPLIT && !BY_CHOICE ? split * p.kb_per_split : 0;
+  int nk = SPLIT && !BY_CHOICE ? max(0, min(p.KB - kb0, p.kb_per_split)) : p.KB;
   const int u_first = SPLIT ? (int)(blockIdx.x / (uint32_t)p.splits) : (int)blockIdx.x;
   int units;
   Pairs pairs;
@@ -420,18 +401,14 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
   } else if constexpr (SMALL) {
     ptx::griddep_wait();
     pairs.load(p, lane);
-    units = __popc(pairs.leaders) * p.NB;
-    if constexpr (MODE == kGateUp) {
-      if (blockIdx.x == 0) {
-        for (int i = threadIdx.x; i < p.NB2; i += C::THREADS) p.arrived[i] = 0u;
-        if (warp == 0 && p.err_flag != nullptr && !pairs.valid && pairs.id != -1)
-          atomicOr(p.err_flag, MXQ_DEVERR_EXPERT);
-      }
-    } else if (units == 0) {  // no token has an expert
-      const int64_t chunks = (int64_t)p.T * p.N / 8;
-      for (int64_t i = (int64_t)blockIdx.x * C::THREADS + threadIdx.x; i < chunks;
-           i += (int64_t)gridDim.x * C::THREADS)
-        reinterpret_cast<uint4*>(p.y)[i] = make_uint4(0, 0, 0, 0);
+    if constexpr (BY_CHOICE) {
+      units = p.T * p.NB;
+      // A choice that is no expert adds nothing.
+      if (!((pairs.valids >> (u_first / p.NB * p.k + split)) & 1u)) nk = 0;
+    } else {
+      units = __popc(pairs.leaders) * p.NB;
+      if (blockIdx.x == 0 && warp == 0 && p.err_flag != nullptr && !pairs.valid && pairs.id != -1)
+        atomicOr(p.err_flag, MXQ_DEVERR_EXPERT);
     }
   } else {
     ptx::griddep_wait();
@@ -448,6 +425,11 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
       t.expert = 0;
       t.row0 = (u / p.NB) * p.per_tile;
       t.count = min(p.per_tile, p.T - t.row0);
+    } else if constexpr (BY_CHOICE) {
+      const int pair = u / p.NB * p.k + split;
+      t.expert = __shfl_sync(0xffffffffu, pairs.id, pair);
+      t.row0 = __shfl_sync(0xffffffffu, pairs.place(lane), pair);
+      t.count = 1;
     } else if constexpr (SMALL) {
       t = pairs.tile(u / p.NB);
     } else {
@@ -458,6 +440,16 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
     }
     return t;
   };
+  if constexpr (SMALL && MODE == kGateUp) {
+    // The first blocks on their way to L2 while barriers and TMEM are set up.
+    if (warp == 3) {
+      const Tile t = tile_of(u_first);
+      const int mat = 2 * t.expert + (lane & 1), kk = lane >> 1;
+      if (kk < nk && kk < NSTAGE)
+        ptx::prefetch_l2_bulk(
+            p.w + (((size_t)mat * p.NB + u_first % p.NB) * p.KB + kb0 + kk) * kBlockBytes, kBlockBytes);
+    }
+  }
   // The pair (token * k + choice) of row i of a tile.
   auto pair_of = [&](const Tile& t, int i) {
     if constexpr (SMALL) return Pairs::row(t, i);
@@ -709,18 +701,6 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&acc_empty[buf]);
         }
-        if constexpr (SMALL && MODE == kDown) {
-          static_assert(C::GROUPS == 1, "the group is the epilogue");
-          __threadfence();  // the results, before the arrival
-          ptx::named_sync(1, 128);
-          if (warp == 4 && lane == 0)
-            *last = atomicAdd(p.arrived + rb, 1u) == (uint32_t)(units / p.NB) - 1u;
-          ptx::named_sync(1, 128);
-          if (*last) {
-            __threadfence();
-            join_small(p, pairs, rb, (int)threadIdx.x - 128, 128);
-          }
-        }
       }
     }
     __syncthreads();
@@ -729,7 +709,9 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
     // CTA that owns the token.
     const Tile t = tile_of(u_first);
     const int rb = u_first % p.NB;
-    const int own_log = __ffs(NT / p.splits) - 1, own = 1 << own_log;  // tokens of each CTA
+    const int own_log = BY_CHOICE ? 0 : __ffs(NT / p.splits) - 1;
+    const int own = 1 << own_log;  // tokens of each CTA
+    const float weight = BY_CHOICE && nk > 0 ? p.wt[u_first / p.NB * p.k + split] : 1.0f;
     const int first = split * own;
     if (warp >= 4) {
       wait(&acc_full[0], 0);
@@ -753,7 +735,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
               const uint32_t at =
                   ptx::smem_u32(sums + ((split * own + tl) * NA + a) * 128 + q * 32 + lane);
               ptx::st_shared_cluster_f32(ptx::map_shared_rank(at, (uint32_t)o),
-                                         nk > 0 ? __uint_as_float(v[i]) : 0.0f);
+                                         nk > 0 ? __uint_as_float(v[i]) * weight : 0.0f);
             }
           }
         }
@@ -779,18 +761,8 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
             for (int e = 0; e < 8; ++e) v[a][e] += ar[e];
           }
         }
-        finish_token<MODE, NA>(p, v, t.row0 + first + tl, rb, sub, in);
-      }
-      if constexpr (SMALL && MODE == kDown) {
-        __threadfence();
-        __syncthreads();
-        if (threadIdx.x == 0)
-          *last = atomicAdd(p.arrived + rb, 1u) == (uint32_t)(units / p.NB * p.splits) - 1u;
-        __syncthreads();
-        if (*last) {
-          __threadfence();
-          join_small(p, pairs, rb, (int)threadIdx.x, C::THREADS);
-        }
+        finish_token<BY_CHOICE ? kLinear : MODE, NA>(
+            p, v, BY_CHOICE ? u_first / p.NB : t.row0 + first + tl, rb, sub, in);
       }
     }
   }
@@ -936,25 +908,40 @@ __global__ void __launch_bounds__(kRowWarps * 32) w4_rows_kernel(const uint4* a,
 
 // out[t] = weighted sum over the token's choices, in their order, of the 16-bit
 // results that the down product left; eight columns to a thread.
-__global__ void __launch_bounds__(256) w4_join_kernel(const uint4* part, const uint8_t* part_sf,
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads) w4_join_kernel(const uint4* part, const uint8_t* part_sf,
                                                       const int32_t* pos, const float* wt,
                                                       uint4* out, int64_t items, int chunks, int k,
                                                       int64_t R) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t it = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
   if (it >= items) return;
   const int64_t t = it / chunks;
   const int c = (int)(it - t * chunks);
   float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int j = 0; j < k; ++j) {
-    const int row = pos[t * k + j];
-    if (row < 0) continue;
-    const uint4 v = part[(size_t)row * chunks + c];
-    const uint32_t ef = part_sf[(c >> 2) * R + row];
-    const float g = wt[t * k + j];
-    add_held16(y, v, ef, g);
+  for (int j0 = 0; j0 < k; j0 += kJoinBatch) {
+    int row[kJoinBatch];
+    float g[kJoinBatch];
+#pragma unroll
+    for (int j = 0; j < kJoinBatch; ++j) {
+      row[j] = j0 + j < k ? pos[t * k + j0 + j] : -1;
+      g[j] = row[j] >= 0 ? wt[t * k + j0 + j] : 0.0f;
+    }
+    uint4 v[kJoinBatch];
+    uint32_t ef[kJoinBatch];
+#pragma unroll
+    for (int j = 0; j < kJoinBatch; ++j) {
+      v[j] = make_uint4(0, 0, 0, 0);
+      ef[j] = kLeastExp;  // (nothing: zeros)
+      if (row[j] >= 0) {
+        v[j] = part[(size_t)row[j] * chunks + c];
+        ef[j] = part_sf[(c >> 2) * R + row[j]];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kJoinBatch; ++j) add_held16(y, v[j], ef[j], g[j]);
   }
   out[it] = to_bf16x8(y);
 }
@@ -1070,10 +1057,13 @@ cudaError_t launch_tokens(int nt, const void* a, uint64_t a_rows, uint64_t K, ui
                           const W4Args& g, int64_t units, int num_sms, cudaStream_t s,
                           const char** why) {
   if constexpr (MODE != kLinear) {
-    if (g.ids != nullptr)
-      return g.splits > 1
-                 ? launch_cfg<MODE, 16, true, true>(a, a_rows, K, blocks, g, units, num_sms, s, why)
-                 : launch_cfg<MODE, 16, false, true>(a, a_rows, K, blocks, g, units, num_sms, s, why);
+    if (g.ids != nullptr) {
+      if constexpr (MODE == kGateUp) {
+        if (g.splits == 1)
+          return launch_cfg<MODE, 16, false, true>(a, a_rows, K, blocks, g, units, num_sms, s, why);
+      }
+      return launch_cfg<MODE, 16, true, true>(a, a_rows, K, blocks, g, units, num_sms, s, why);
+    }
   }
   if (nt <= 16)
     return g.splits > 1 ? launch_cfg<MODE, 16, true>(a, a_rows, K, blocks, g, units, num_sms, s, why)
@@ -1149,11 +1139,12 @@ cudaError_t launch_linear_a8w4(const uint8_t* a, const uint8_t* a_sf, const uint
 }
 
 namespace {
+bool small_call(int64_t R, int k) { return R <= kSmallPairs && k <= kSmallChoices; }
 // Most tokens of a tile, by the rows that an expert gets on average: above that
 // some experts take two tiles, which read their weights twice (from L2).
-int expert_tile(int64_t R, int E) {
+int expert_tile(int64_t R, int k, int E) {
   const int64_t avg = ceil_div(R, E);
-  if (R <= kSmallPairs) return 16;
+  if (small_call(R, k)) return 16;
   return avg <= 8 ? 16 : avg <= 16 ? 32 : avg <= 40 ? 64 : avg <= 80 ? 128 : kMaxTokens;
 }
 // An expert of c rows has ceil(c / nt) tiles at most (fewer where even tiles
@@ -1166,11 +1157,9 @@ bool lays_out_rows(int nt) { return nt > 32; }
 
 ExpertsLayout experts_layout(int64_t T, int k, int E, int K, int I, int N) {
   const int64_t R = T * k;
-  const int nt = expert_tile(R, E);
+  const int nt = expert_tile(R, k, E);
   ExpertsLayout l;
-  // The numbers of tiles and of rows lie first, or (a small call's) arrivals.
-  l.arrived = 0;
-  l.tiles = R <= kSmallPairs ? round_up_256((size_t)ceil_div(N, 128) * 4) : 256;
+  l.tiles = 256;  // the numbers of tiles and of rows lie before them
   l.perm = l.tiles + round_up_256((size_t)most_tiles(R, E, nt) * sizeof(Tile));
   l.pos = l.perm + round_up_256((size_t)R * 4);
   l.rows = l.pos + round_up_256((size_t)R * 4);
@@ -1187,7 +1176,7 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
                                 int64_t T, int k, int E, int K, int I, int N, int32_t* err_flag,
                                 void* ws, int num_sms, cudaStream_t s, const char** why) {
   const int64_t R = T * k;
-  const int nt = expert_tile(R, E);
+  const int nt = expert_tile(R, k, E);
   const ExpertsLayout l = experts_layout(T, k, E, K, I, N);
   uint8_t* base = static_cast<uint8_t*>(ws);
   int32_t* n_tiles = reinterpret_cast<int32_t*>(base);
@@ -1206,14 +1195,12 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   W4Args g = {};
   cudaError_t e = watchdog_address(&g.wd);
   if (e != cudaSuccess) return e;
-  const bool small = R <= kSmallPairs;  // no plan, and no sum by a kernel of its own
+  const bool small = small_call(R, k);
   if (small) {
     g.ids = ids;
     g.wt = wt;
     g.err_flag = err_flag;
     g.w2 = w2;
-    g.arrived = reinterpret_cast<uint32_t*>(base + l.arrived);
-    g.y = static_cast<__nv_bfloat16*>(out);
     g.E = E;
     g.KB2 = (int)ceil_div(I, kGroup);
     g.NB2 = (int)ceil_div(N, 128);
@@ -1262,15 +1249,22 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   g.NG = (int)R;
   g.KG = g.KB = (int)ceil_div(I, kGroup);
   g.NB = (int)ceil_div(N, 128);
-  g.splits = nt == 16 ? pick_splits(most * g.NB, g.KB, 2 * num_sms) : 1;
+  int64_t units = most * g.NB;
+  if (small) {
+    g.out = out;
+    g.splits = k;  // one CTA for each choice
+    units = T * g.NB;
+  } else {
+    g.splits = nt == 16 ? pick_splits(units, g.KB, 2 * num_sms) : 1;
+  }
   g.kb_per_split = (int)ceil_div(g.KB, g.splits);
   e = launch_tokens<kDown>(nt, base + l.h, (uint64_t)R, (uint64_t)I, (uint64_t)E * g.NB * g.KB, g,
-                           most * g.NB, num_sms, s, why);
+                           units, num_sms, s, why);
   if (e != cudaSuccess || small) return e;
   const int chunks = N / 8;
   const int64_t items = T * chunks;
-  cfg.gridDim = dim3((unsigned)ceil_div(items, 256), 1, 1);
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.gridDim = dim3((unsigned)ceil_div(items, kJoinThreads), 1, 1);
+  cfg.blockDim = dim3(kJoinThreads, 1, 1);
   return cudaLaunchKernelEx(&cfg, w4_join_kernel, reinterpret_cast<const uint4*>(base + l.part),
                             reinterpret_cast<const uint8_t*>(base + l.part_sf), pos, wt,
                             static_cast<uint4*>(out), items, chunks, k, R);
