@@ -785,7 +785,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
 }
 
 // ------------------------------------------------------------ plan and join
-// One CTA counts the rows of each expert, lays out the tiles and sorts the rows
+// One cluster counts the rows of each expert, lays out the tiles and sorts the rows
 // by expert: perm gives a sorted row's token and choice, pos the other way round
 // (-1: no expert).  The order of an expert's rows does not matter: each is summed by
 // itself, and lands at its own place.
@@ -793,7 +793,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanBatch = 8;
 
 __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* ids, int R, int E,
-                                                               int nt, Tile* tiles,
+                                                               int nt, int ctas, Tile* tiles,
                                                                int32_t* n_tiles, int32_t* perm,
                                                                int32_t* pos, int32_t* err_flag) {
   __shared__ int cnt[kMaxExperts], cur[kMaxExperts];
@@ -802,15 +802,19 @@ __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* id
   ptx::griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   static_assert(kMaxExperts <= kPlanThreads, "one expert per thread");
+  // CTA `rank` of the cluster takes the rows [first, end); shared-memory atomics
+  // of one SM alone take 19 us for 24576 rows.
+  const uint32_t rank = ptx::cluster_rank();
+  const int share = (R + ctas - 1) / ctas, first = min(R, (int)rank * share), end = min(R, first + share);
   if (tid < kMaxExperts) cnt[tid] = 0;
   __syncthreads();
   bool bad = false;
   // (Eight loads at a time: with one after the other their latency is the time.)
-  for (int i0 = tid; i0 < R; i0 += kPlanBatch * kPlanThreads) {
+  for (int i0 = first + tid; i0 < end; i0 += kPlanBatch * kPlanThreads) {
     int e[kPlanBatch];
 #pragma unroll
     for (int j = 0; j < kPlanBatch; ++j)
-      e[j] = i0 + j * kPlanThreads < R ? ids[i0 + j * kPlanThreads] : -1;
+      e[j] = i0 + j * kPlanThreads < end ? ids[i0 + j * kPlanThreads] : -1;
 #pragma unroll
     for (int j = 0; j < kPlanBatch; ++j) {
       if (e[j] >= 0 && e[j] < E)
@@ -820,9 +824,18 @@ __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* id
     }
   }
   if (bad && err_flag != nullptr) atomicOr(err_flag, MXQ_DEVERR_EXPERT);
-  __syncthreads();
+  ptx::cluster_sync();
+  // All CTAs' rows of expert `tid`, and those of the CTAs before this one.
+  int c = 0, earlier = 0;
+  if (tid < E) {
+    const uint32_t at = ptx::smem_u32(&cnt[tid]);
+    for (int r = 0; r < ctas; ++r) {
+      const int v = (int)ptx::ld_shared_cluster_u32(ptx::map_shared_rank(at, (uint32_t)r));
+      c += v;
+      earlier += r < (int)rank ? v : 0;
+    }
+  }
   // Even tiles of at most nt rows, each a multiple of 16 but for the last.
-  const int c = tid < E ? cnt[tid] : 0;
   const int even = (c + nt - 1) / nt;
   const int rows = c > 0 ? ((c + even - 1) / even + 15) / 16 * 16 : 16;
   const int nt_e = (c + rows - 1) / rows;
@@ -847,8 +860,8 @@ __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* id
   }
   const int row0 = pc + sc - c, tile0 = pt + st - nt_e;
   if (tid < E) {
-    cur[tid] = row0;
-    for (int i = 0; i < nt_e; ++i) {
+    cur[tid] = row0 + earlier;
+    for (int i = (int)rank; i < nt_e; i += ctas) {
       Tile t;
       t.expert = tid;
       t.row0 = row0 + i * rows;
@@ -857,20 +870,20 @@ __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* id
       tiles[tile0 + i] = t;
     }
   }
-  if (tid == kPlanThreads - 1) {
+  if (rank == 0 && tid == kPlanThreads - 1) {
     n_tiles[0] = pt + st;
     n_tiles[1] = pc + sc;
   }
-  __syncthreads();
-  for (int i0 = tid; i0 < R; i0 += kPlanBatch * kPlanThreads) {
+  ptx::cluster_sync();  // (also: nobody reads this CTA's counts any more)
+  for (int i0 = first + tid; i0 < end; i0 += kPlanBatch * kPlanThreads) {
     int e[kPlanBatch];
 #pragma unroll
     for (int j = 0; j < kPlanBatch; ++j)
-      e[j] = i0 + j * kPlanThreads < R ? ids[i0 + j * kPlanThreads] : -1;
+      e[j] = i0 + j * kPlanThreads < end ? ids[i0 + j * kPlanThreads] : -1;
 #pragma unroll
     for (int j = 0; j < kPlanBatch; ++j) {
       const int i = i0 + j * kPlanThreads;
-      if (i >= R) break;
+      if (i >= end) break;
       int at = -1;
       if (e[j] >= 0 && e[j] < E) {
         at = atomicAdd(&cur[e[j]], 1);
@@ -1183,7 +1196,7 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   Tile* tiles = reinterpret_cast<Tile*>(base + l.tiles);
   int32_t* perm = reinterpret_cast<int32_t*>(base + l.perm);
   int32_t* pos = reinterpret_cast<int32_t*>(base + l.pos);
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
@@ -1205,10 +1218,19 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
     g.KB2 = (int)ceil_div(I, kGroup);
     g.NB2 = (int)ceil_div(N, 128);
   }
-  if (!small)
-    e = cudaLaunchKernelEx(&cfg, w4_plan_kernel, ids, (int)R, E, nt, tiles, n_tiles, perm, pos,
-                         err_flag);
-  if (e != cudaSuccess) return e;
+  if (!small) {
+    const int ctas = R > 4 * kPlanThreads ? 8 : 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, w4_plan_kernel, ids, (int)R, E, nt, ctas, tiles, n_tiles, perm, pos,
+                           err_flag);
+    cfg.numAttrs = 1;
+    if (e != cudaSuccess) return e;
+  }
   const uint8_t* rows = a;
   int64_t n_rows = T;
   if (lays_out_rows(nt)) {

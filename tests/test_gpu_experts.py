@@ -66,7 +66,8 @@ SIZES = [  # T, k, E, K, I, N
     (7, 3, 4, 4096, 256, 128), (16, 8, 32, 512, 288, 512), (1, 8, 16, 2048, 512, 2048), (33, 2, 3, 384, 128, 272),
     (64, 6, 8, 320, 224, 400), (65, 4, 8, 640, 128, 640), (130, 8, 10, 256, 416, 256), (300, 2, 4, 512, 256, 512),
     (500, 6, 12, 288, 160, 160), (40, 32, 33, 96, 64, 48), (257, 1, 1, 1024, 384, 128), (24, 4, 8, 640, 192, 304),
-    (100, 2, 16, 1152, 96, 128), (90, 6, 8, 256, 512, 96), (400, 8, 64, 160, 96, 64)]
+    (100, 2, 16, 1152, 96, 128), (90, 6, 8, 256, 512, 96), (400, 8, 64, 160, 96, 64), (700, 8, 12, 96, 64, 48),
+    (1500, 5, 1000, 64, 32, 32)]
 
 
 @pytest.mark.parametrize("T,k,E,K,I,N", SIZES)
