@@ -751,7 +751,7 @@ static int validate_experts_sizes(int64_t T, int32_t k, int32_t E, int32_t K, in
   if (T >= ((int64_t)1 << 24) || T * k >= ((int64_t)1 << 24))
     return fail(MXQ_ERR_UNSUPPORTED, "T*k must be < 2^24");
   if (!w4_fits(E, N, I) || !w4_fits(2 * (int64_t)E, I, K) || (T * k / 16 + E) * ((int64_t)(N > I ? N : I) / 128 + 1) >= ((int64_t)1 << 28) ||
-      T * (N / 8) >= ((int64_t)1 << 38))
+      T * (N / 8) >= ((int64_t)1 << 32) - 256)
     return fail(MXQ_ERR_UNSUPPORTED, "the weights or T*k*N are too large");
   return MXQ_OK;
 }

@@ -155,27 +155,45 @@ struct Pairs {
   }
 };
 
+// Two fp32 sums at once.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n.reg .b64 a, b, r;\n"
+      "mov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\n"
+      "add.rn.f32x2 r, a, b;\nmov.b64 {%0, %1}, r;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n.reg .b64 a, b, c, r;\n"
+      "mov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
+      "fma.rn.f32x2 r, a, b, c;\nmov.b64 {%0, %1}, r;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
 constexpr uint32_t kLeastExp = 14u;  // of held results (see held16); smaller ones lose bits below 2^-126
-constexpr int kJoinBatch = 8;  // results fetched at a time: their latencies overlap
 
 // Eight results of 16 bits with their exponent, times g, added to y.
-__device__ __forceinline__ void add_held16(float (&y)[8], const uint4& v, uint32_t ef, float g) {
+__device__ __forceinline__ void add_held16(float2 (&y)[4], const uint4& v, uint32_t ef, float g) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   if (ef != 255u) {
-    const float s = __uint_as_float((ef - 13u) << 23);  // 2^(ef - 140)
+    const float s = __uint_as_float((ef - 13u) << 23) * g;  // 2^(ef - 140) g
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       // The integer plus 2^15 as the low bits of 2^23.
       const uint32_t u = w[q] ^ 0x80008000u;
-      y[2 * q] = fmaf((__uint_as_float(0x4B000000u | (u & 0xFFFFu)) - 8421376.0f) * s, g, y[2 * q]);
-      y[2 * q + 1] = fmaf((__uint_as_float(0x4B000000u | (u >> 16)) - 8421376.0f) * s, g, y[2 * q + 1]);
+      const float2 f = make_float2(__uint_as_float(__byte_perm(u, 0x4B00u, 0x5410)),
+                                   __uint_as_float(__byte_perm(u, 0x4B00u, 0x5432)));
+      y[q] = fma2(add2(f, make_float2(-8421376.0f, -8421376.0f)), make_float2(s, s), y[q]);
     }
   } else {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      y[2 * q] = fmaf(bf16_lo(w[q]), g, y[2 * q]);
-      y[2 * q + 1] = fmaf(bf16_hi(w[q]), g, y[2 * q + 1]);
-    }
+    for (int q = 0; q < 4; ++q)
+      y[q] = fma2(make_float2(bf16_lo(w[q]), bf16_hi(w[q])), make_float2(g, g), y[q]);
   }
 }
 
@@ -923,40 +941,30 @@ __global__ void __launch_bounds__(kRowWarps * 32) w4_rows_kernel(const uint4* a,
 // results that the down product left; eight columns to a thread.
 constexpr int kJoinThreads = 256;
 
-__global__ void __launch_bounds__(kJoinThreads) w4_join_kernel(const uint4* part, const uint8_t* part_sf,
-                                                      const int32_t* pos, const float* wt,
-                                                      uint4* out, int64_t items, int chunks, int k,
-                                                      int64_t R) {
+__global__ void __launch_bounds__(kJoinThreads) w4_join_kernel(const uint4* part,
+                                                               const uint8_t* part_sf,
+                                                               const int32_t* pos, const float* wt,
+                                                               uint4* out, uint32_t items,
+                                                               uint32_t chunks, int k, int64_t R) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int64_t it = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
+  const uint32_t it = blockIdx.x * kJoinThreads + threadIdx.x;
   if (it >= items) return;
-  const int64_t t = it / chunks;
-  const int c = (int)(it - t * chunks);
-  float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  for (int j0 = 0; j0 < k; j0 += kJoinBatch) {
-    int row[kJoinBatch];
-    float g[kJoinBatch];
-#pragma unroll
-    for (int j = 0; j < kJoinBatch; ++j) {
-      row[j] = j0 + j < k ? pos[t * k + j0 + j] : -1;
-      g[j] = row[j] >= 0 ? wt[t * k + j0 + j] : 0.0f;
-    }
-    uint4 v[kJoinBatch];
-    uint32_t ef[kJoinBatch];
-#pragma unroll
-    for (int j = 0; j < kJoinBatch; ++j) {
-      v[j] = make_uint4(0, 0, 0, 0);
-      ef[j] = kLeastExp;  // (nothing: zeros)
-      if (row[j] >= 0) {
-        v[j] = part[(size_t)row[j] * chunks + c];
-        ef[j] = part_sf[(c >> 2) * R + row[j]];
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kJoinBatch; ++j) add_held16(y, v[j], ef[j], g[j]);
+  const uint32_t t = it / chunks, c = it - t * chunks;
+  pos += (size_t)t * k;
+  wt += (size_t)t * k;
+  part += c;
+  part_sf += (c >> 2) * R;
+  float2 y[4] = {};
+  // (Two at a time: the other warps hide the rest, and more in flight a thread
+  // measured slower.)
+#pragma unroll 2
+  for (int j = 0; j < k; ++j) {
+    const int row = pos[j];
+    if (row >= 0) add_held16(y, part[(size_t)row * chunks], part_sf[row], wt[j]);
   }
-  out[it] = to_bf16x8(y);
+  out[it] = make_uint4(pack2(y[0].x, y[0].y), pack2(y[1].x, y[1].y), pack2(y[2].x, y[2].y),
+                       pack2(y[3].x, y[3].y));
 }
 
 // Codes and scales of B matrices [N][K] into blocks; one thread per 16 bytes.
@@ -1283,8 +1291,7 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   e = launch_tokens<kDown>(nt, base + l.h, (uint64_t)R, (uint64_t)I, (uint64_t)E * g.NB * g.KB, g,
                            units, num_sms, s, why);
   if (e != cudaSuccess || small) return e;
-  const int chunks = N / 8;
-  const int64_t items = T * chunks;
+  const uint32_t chunks = (uint32_t)(N / 8), items = (uint32_t)T * chunks;
   cfg.gridDim = dim3((unsigned)ceil_div(items, kJoinThreads), 1, 1);
   cfg.blockDim = dim3(kJoinThreads, 1, 1);
   return cudaLaunchKernelEx(&cfg, w4_join_kernel, reinterpret_cast<const uint4*>(base + l.part),
