@@ -13,6 +13,8 @@ A missing or unbuilt library raises ``MxqLibraryError`` on first use.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -539,6 +541,31 @@ def mxq_attn(q, cache, block_table, seq_lens, q_start=None, page_size=64, window
     return out
 
 
+_fast = None  # mxq_fastcall, once loaded; False where it was not built
+
+
+def _fastcall():
+    """The module that makes the common calls in C++ (checks, outputs on the current stream, the library's entry
+    point), or False.  It answers None for any other call, which then goes the way below."""
+    global _fast
+    if _fast is None:
+        _fast = False
+        path = os.path.join(HERE, "mxq_fastcall.so")
+        if os.path.exists(path):
+            L = lib()
+            loader = importlib.machinery.ExtensionFileLoader("mxq_fastcall", path)
+            try:
+                m = importlib.util.module_from_spec(importlib.util.spec_from_loader("mxq_fastcall", loader))
+                loader.exec_module(m)
+            except ImportError as e:
+                raise MxqLibraryError(f"cannot load {path}: {e}") from e
+            m.bind(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
+                "mxq_add_rms_norm", "mxq_route", "mxq_w4_bytes", "mxq_linear_a8w4", "mxq_experts_workspace_bytes",
+                "mxq_experts_a8w4")))
+            _fast = m
+    return _fast
+
+
 # The current device, without torch's lazy-initialisation check where torch has that (a tensor on the device exists).
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
 
@@ -583,6 +610,11 @@ def mxq_add_rms_norm(x, weight=None, eps=1e-6, residual=None, residual_out=None,
     (residual_out=residual adds in place); y bf16 [..., D] unless want_y is false; E4M3 codes uint8
     [..., D] and E8M0 scales uint8 [..., ceil(D/128)] of y, as mxq_inv_rope_group_quant's, unless
     want_codes is false.  y, q and sc, where given, receive them."""
+    if stream is None and residual_out is None and y is None and q is None and sc is None:
+        f = _fast or _fastcall()
+        done = f and f.norm(x, weight, eps, residual, True if want_y else False, True if want_codes else False)
+        if done:
+            return done
     fn = "mxq_add_rms_norm"
     dev = _device_of(fn, x)
     shape = x.shape
@@ -632,6 +664,12 @@ def mxq_route(logits, k, scoring="softmax", bias=None, groups=1, topk_groups=1, 
     scoring: "softmax", "sigmoid" or "sqrtsoftplus"; bias float32 [E] is added to the scores for the choice
     only; with topk_groups < groups only the experts of the best groups (by the sum of their group_top best)
     take part.  Ids run from the best down, -1 where masked logits (-infinity, NaN) leave none."""
+    if stream is None and ids is None and weights is None:
+        f = _fast or _fastcall()
+        done = f and f.route(logits, k, MXQ_SCORES.get(scoring, -1), bias, groups, topk_groups, group_top,
+                             True if renormalise else False, scale)
+        if done:
+            return done
     fn = "mxq_route"
     dev = _device_of(fn, logits)
     T, E = shape = logits.shape
@@ -691,6 +729,11 @@ def mxq_prepare_w4(w, w_e8m0, out=None, stream=None):
 def mxq_linear_a8w4(a, a_sf, w4, N, out=None, stream=None):
     """a uint8 [T, K] E4M3 codes, a_sf uint8 [T, ceil(K/128)], w4 from mxq_prepare_w4 of a weight [N, K]
     -> out bf16 [T, N]."""
+    if stream is None and out is None:
+        f = _fast or _fastcall()
+        done = f.linear(a, a_sf, w4, N) if f else None
+        if done is not None:
+            return done
     fn = "mxq_linear_a8w4"
     dev = _device_of(fn, a)
     T, K = shape = a.shape
@@ -719,6 +762,11 @@ def mxq_experts_a8w4(a, a_sf, ids, weights, w13, w2, I, N=None, out=None, ws=Non
     weights float32 [T, k] (mxq_route's; -1: no expert), w13 from mxq_prepare_w4 of [2*E, I, K] (each expert's gate
     rows, then its up rows), w2 from mxq_prepare_w4 of [E, N, I] -> out bf16 [T, N] (N: K unless given).
     `ws` (mxq_experts_workspace_bytes) is allocated when not given; concurrent calls need distinct workspaces."""
+    if stream is None and out is None and ws is None and err_flag is None:
+        f = _fast or _fastcall()
+        done = f.experts(a, a_sf, ids, weights, w13, w2, I, a.shape[1] if N is None else N) if f else None
+        if done is not None:
+            return done
     fn = "mxq_experts_a8w4"
     dev = _device_of(fn, a)
     T, K = shape = a.shape

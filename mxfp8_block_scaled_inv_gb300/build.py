@@ -3,6 +3,9 @@
 Each CUDA translation unit is compiled by nvcc in parallel with
 ``-gencode arch=compute_103a,code=sm_103a``, the C-ABI layer by the host
 compiler, and the objects are linked into ``libmxq.so`` next to this file.
+``mxq_fastcall.so``, the binding's quick way into it for common calls, is built
+beside it against the installed torch; without it (no torch or Python headers)
+the binding makes those calls through ctypes like all others.
 A build is skipped when the library is newer than every source and header.
 """
 
@@ -25,6 +28,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CU_SOURCES = ["quant.cu", "misc.cu", "bmm.cu", "linear_noalloc.cu", "kv_insert.cu", "kv4.cu",
               "attn.cu", "norm.cu", "route.cu", "w4.cu"]
 CXX_SOURCES = ["api.cpp"]
+FASTCALL_PATH = os.path.join(HERE, "mxq_fastcall.so")
 
 
 def cuda_home() -> str:
@@ -60,6 +64,29 @@ def _run(cmd, verbose):
     return r.stdout
 
 
+def _build_fastcall(cxx, inc, verbose) -> None:
+    """Compile mxq_fastcall.so; a failure leaves it out, with a message."""
+    tmp = FASTCALL_PATH + ".tmp"
+    try:
+        import sysconfig
+
+        import torch
+
+        at = os.path.dirname(torch.__file__)
+        _run([cxx, "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared",
+              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
+              "-isystem", os.path.join(at, "include"),
+              "-isystem", os.path.join(at, "include", "torch", "csrc", "api", "include"),
+              "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "fastcall.cpp"), "-o", tmp,
+              "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], verbose)
+    except (ImportError, RuntimeError) as e:
+        print(f"mxq_fastcall.so not built: {e}", file=sys.stderr, flush=True)
+        if os.path.exists(FASTCALL_PATH):
+            os.remove(FASTCALL_PATH)
+        return
+    os.replace(tmp, FASTCALL_PATH)
+
+
 def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False) -> str:
     """Compile and link libmxq.so; returns its path."""
     if not force and up_to_date():
@@ -83,9 +110,11 @@ def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False) 
                "-o", obj]
         jobs.append((cmd, obj))
     outputs = []
-    with cf.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        fast = ex.submit(_build_fastcall, cxx, inc, verbose)
         for out in ex.map(lambda j: _run(j[0], verbose), jobs):
             outputs.append(out)
+        fast.result()
     if ptxas_info:
         print("\n".join(outputs))
     tmp = LIB_PATH + ".tmp"
