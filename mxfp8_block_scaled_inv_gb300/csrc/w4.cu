@@ -809,13 +809,14 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
 // itself, and lands at its own place.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBatch = 8;
+constexpr int kSizes = kMaxTokens / 16 + 1;  // tiles of 16 i tokens and less
 
 __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* ids, int R, int E,
                                                                int nt, int ctas, Tile* tiles,
                                                                int32_t* n_tiles, int32_t* perm,
                                                                int32_t* pos, int32_t* err_flag) {
   __shared__ int cnt[kMaxExperts], cur[kMaxExperts];
-  __shared__ int wsum[32], wtile[32];
+  __shared__ int wsum[32], size_n[kSizes], size_at[kSizes];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -857,40 +858,51 @@ __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* id
   const int even = (c + nt - 1) / nt;
   const int rows = c > 0 ? ((c + even - 1) / even + 15) / 16 * 16 : 16;
   const int nt_e = (c + rows - 1) / rows;
-  int sc = c, st = nt_e;  // inclusive sums over the warp, then over warps
+  int sc = c;  // inclusive sums over the warp, then over warps
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
-    const int a = __shfl_up_sync(0xffffffffu, sc, m), b = __shfl_up_sync(0xffffffffu, st, m);
-    if (lane >= m) {
-      sc += a;
-      st += b;
-    }
+    const int a = __shfl_up_sync(0xffffffffu, sc, m);
+    if (lane >= m) sc += a;
   }
-  if (lane == 31) {
-    wsum[warp] = sc;
-    wtile[warp] = st;
-  }
+  if (lane == 31) wsum[warp] = sc;
+  // The largest tiles come first: CTAs take units in order, so the last round,
+  // which is seldom full, is one of small ones.  An expert's tiles but the last
+  // are of one size and stay together.
+  const int last = c - (nt_e - 1) * rows, full16 = rows / 16, last16 = (last + 15) / 16;
+  if (tid < kSizes) size_n[tid] = 0;
   __syncthreads();
-  int pc = 0, pt = 0;
-  for (int w = 0; w < warp; ++w) {
-    pc += wsum[w];
-    pt += wtile[w];
+  if (nt_e > 1) atomicAdd(&size_n[full16], nt_e - 1);
+  if (nt_e > 0) atomicAdd(&size_n[last16], 1);
+  __syncthreads();
+  int pc = 0;
+  for (int w = 0; w < warp; ++w) pc += wsum[w];
+  if (tid < kSizes) {
+    int before = 0;
+    for (int i = tid + 1; i < kSizes; ++i) before += size_n[i];
+    size_at[tid] = before;
   }
-  const int row0 = pc + sc - c, tile0 = pt + st - nt_e;
-  if (tid < E) {
-    cur[tid] = row0 + earlier;
-    for (int i = (int)rank; i < nt_e; i += ctas) {
-      Tile t;
-      t.expert = tid;
-      t.row0 = row0 + i * rows;
-      t.count = min(rows, c - i * rows);
-      t.pairs = 0u;
-      tiles[tile0 + i] = t;
+  const int row0 = pc + sc - c;
+  if (tid < E) cur[tid] = row0 + earlier;
+  if (rank == 0 && tid == kPlanThreads - 1) n_tiles[1] = pc + sc;
+  __syncthreads();
+  if (rank == 0) {
+    if (tid == 0) n_tiles[0] = size_at[0] + size_n[0];
+    Tile t;
+    t.expert = tid;
+    t.pairs = 0u;
+    if (nt_e > 1) {
+      const int at = atomicAdd(&size_at[full16], nt_e - 1);
+      t.count = rows;
+      for (int i = 0; i < nt_e - 1; ++i) {
+        t.row0 = row0 + i * rows;
+        tiles[at + i] = t;
+      }
     }
-  }
-  if (rank == 0 && tid == kPlanThreads - 1) {
-    n_tiles[0] = pt + st;
-    n_tiles[1] = pc + sc;
+    if (nt_e > 0) {
+      t.row0 = row0 + (nt_e - 1) * rows;
+      t.count = last;
+      tiles[atomicAdd(&size_at[last16], 1)] = t;
+    }
   }
   ptx::cluster_sync();  // (also: nobody reads this CTA's counts any more)
   for (int i0 = first + tid; i0 < end; i0 += kPlanBatch * kPlanThreads) {
