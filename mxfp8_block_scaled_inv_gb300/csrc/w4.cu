@@ -1178,7 +1178,7 @@ bool small_call(int64_t R, int k) { return R <= kSmallPairs && k <= kSmallChoice
 int expert_tile(int64_t R, int k, int E) {
   const int64_t avg = ceil_div(R, E);
   if (small_call(R, k)) return 16;
-  return avg <= 8 ? 16 : avg <= 16 ? 32 : avg <= 40 ? 64 : avg <= 80 ? 128 : kMaxTokens;
+  return avg <= 5 ? 16 : avg <= 12 ? 32 : avg <= 40 ? 64 : avg <= 80 ? 128 : kMaxTokens;
 }
 // An expert of c rows has ceil(c / nt) tiles at most (fewer where even tiles
 // round up to 16), that is c / nt and one more if it has any.
