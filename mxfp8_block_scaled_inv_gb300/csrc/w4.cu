@@ -75,7 +75,7 @@ constexpr int kTileBytes = 128 * 128;   // the same, unpacked in shared memory
 constexpr int kBlockBytes = kW4BlockBytes;
 static_assert(kBlockBytes == kCodeBytes + kSfAtomBytes, "block layout");
 constexpr int kChunk = 16;       // tokens drained at a time
-constexpr int kMaxTokens = 240;  // of a tile: two accumulators and scale columns fit TMEM
+constexpr int kMaxTokens = 240;  // of a tile (of CTA pairs): two accumulators and scale columns fit TMEM
 
 enum Mode { kLinear = 0, kGateUp = 1, kDown = 2 };
 
@@ -208,11 +208,8 @@ struct Cfg {
   static constexpr int CTAS = NA == 1 && NT <= 64 ? 2 : 1;
   static constexpr int GROUPS = NT <= 64 || SPLIT ? 1 : 3;  // epilogue groups
   static constexpr int THREADS = 128 + 128 * GROUPS;
-  static constexpr int TOK_ATOMS = (NT + 127) / 128;
   static constexpr int TOK_TILE = NT * 128;
-  static constexpr int BOX_ROWS = NT > 128 ? 80 : NT;  // rows of a copy of tokens
-  static_assert(NT % BOX_ROWS == 0 && (BOX_ROWS % 8 == 0), "token copies");
-  static constexpr int STAGE = NA * (kTileBytes + kSfAtomBytes) + TOK_TILE + TOK_ATOMS * kSfAtomBytes;
+  static constexpr int STAGE = NA * (kTileBytes + kSfAtomBytes) + TOK_TILE + kSfAtomBytes;
   // Split K: the partial sums that the CTA receives, fp32
   // [rank][owned token][accumulator][row].
   static constexpr int SUM_BYTES = SPLIT ? NA * NT * 512 : 0;
@@ -225,14 +222,14 @@ struct Cfg {
   static constexpr int OFF_TOK = NSTAGE * NA * kTileBytes;
   static constexpr int OFF_WSF = OFF_TOK + NSTAGE * TOK_TILE;
   static constexpr int OFF_TSF = OFF_WSF + NSTAGE * NA * kSfAtomBytes;
-  static constexpr int OFF_SUM = OFF_TSF + NSTAGE * TOK_ATOMS * kSfAtomBytes;
+  static constexpr int OFF_SUM = OFF_TSF + NSTAGE * kSfAtomBytes;
   static constexpr int OFF_MAX = OFF_SUM + SUM_BYTES;
   static constexpr int OFF_BAR = OFF_MAX + MAX_BYTES;
   static constexpr int SMEM = OFF_BAR + (2 * NSTAGE + 5) * 8 + 32 + 1024;
   // TMEM: accumulators, then a ring of scale columns.  A copy of scales into
   // columns that earlier MMAs read is ordered behind them (both are issued by one
   // thread and execute in order); the ring keeps the copy from waiting.
-  static constexpr int SF_COLS = 4 * NA + 4 * TOK_ATOMS;
+  static constexpr int SF_COLS = 4 * NA + 4;
   static constexpr int NBUF = !SPLIT && 2 * NA * NT + 2 * SF_COLS <= 512 / CTAS ? 2 : 1;
   static constexpr int SF_RING = (512 / CTAS - NBUF * NA * NT) / SF_COLS >= 4 ? 4 : 2;
   static constexpr int TMEM_USED = NBUF * NA * NT + SF_RING * SF_COLS;
@@ -242,7 +239,7 @@ struct Cfg {
   // operand is chosen at bits 4-5 (B) and 29-30 (A).
   static constexpr uint32_t IDESC = (5u << 7) | (1u << 23) | ((128u >> 4) << 24);
   static_assert(NSTAGE >= 3 && SMEM <= 232448 && TMEM_COLS * CTAS <= 512, "budgets");
-  static_assert(NT % kChunk == 0 && NT <= kMaxTokens && (!SPLIT || NT <= 32), "tokens of a tile");
+  static_assert(NT % kChunk == 0 && NT <= 128 && (!SPLIT || NT <= 32), "tokens of a tile");
 };
 
 // silu(g) * u.  The fast exponential (off by 2^-22 and 2^-23 |g| of itself) and
@@ -301,7 +298,7 @@ __device__ __forceinline__ void finish_chunk(const W4Args& p, float (&v)[NA][kCh
       for (int w = 0; w < 4; ++w) m = max(m, __float_as_uint(max_[w * kChunk + lane]));
       uint32_t sb;
       inv = group_scale(__uint_as_float(m), &sb);
-      if (q == 0 && lane < live) p.out_sf[(size_t)(row + lane) * p.NG + rb] = (uint8_t)sb;
+      if (q == 0 && lane < live && rb < p.NG) p.out_sf[(size_t)(row + lane) * p.NG + rb] = (uint8_t)sb;
     }
     uint8_t* o = static_cast<uint8_t*>(p.out) + (size_t)row * p.N + n;
 #pragma unroll
@@ -516,9 +513,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
     bool ok = true;
     for (int u = u_first; u < units && ok; u += u_step) {
       const Tile t = tile_of(u);
-      const int boxes = (t.count + C::BOX_ROWS - 1) / C::BOX_ROWS;
-      const uint32_t bytes =
-          NA * kBlockBytes + (C::GATHER ? 0u : (uint32_t)(boxes * C::BOX_ROWS * 128));
+      const uint32_t bytes = NA * kBlockBytes + (C::GATHER ? 0u : (uint32_t)C::TOK_TILE);
       const int rb = u % p.NB;
       int row[NA];  // of a matrix's first block, in rows of 64 bytes
 #pragma unroll
@@ -538,13 +533,9 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
                            p.w + (size_t)(uint32_t)row[a] * 64 + kCodeBytes, kSfAtomBytes, &full[s]);
             row[a] += kBlockBytes / 64;
           }
-          if constexpr (!C::GATHER) {
-#pragma unroll
-            for (int b = 0; b < NT / C::BOX_ROWS; ++b)
-              if (b < boxes)
-                ptx::tma_load_2d(smem + C::OFF_TOK + s * C::TOK_TILE + b * C::BOX_ROWS * 128, &tm_a,
-                                 &full[s], (kb0 + kk) * 128, t.row0 + b * C::BOX_ROWS);
-          }
+          if constexpr (!C::GATHER)
+            ptx::tma_load_2d(smem + C::OFF_TOK + s * C::TOK_TILE, &tm_a, &full[s], (kb0 + kk) * 128,
+                             t.row0);
         }
         __syncwarp();
       }
@@ -609,14 +600,14 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
             ptx::tma_gather4(smem + C::OFF_TOK + s * C::TOK_TILE + lane * 512, &tm_a, &full[s],
                              (kb0 + kk) * 128, now.g4[0], now.g4[1], now.g4[2], now.g4[3]);
         }
-        // Row r of an atom owns word (r % 128) / 32 of line r % 32; a group's
+        // Row r of an atom owns word r / 32 of line r % 32; a group's
         // byte stands for its four blocks of 32.
-        uint8_t* atom = smem + C::OFF_TSF + s * C::TOK_ATOMS * kSfAtomBytes;
+        uint8_t* atom = smem + C::OFF_TSF + s * kSfAtomBytes;
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
           const uint32_t w = now.byte[j] * 0x01010101u;
           if (kk + 1 < nk) now.byte[j] = now.src[j][kk + 1];
-          *reinterpret_cast<uint32_t*>(atom + (j >> 2) * kSfAtomBytes + lane * 16 + (j & 3) * 4) = w;
+          *reinterpret_cast<uint32_t*>(atom + lane * 16 + j * 4) = w;
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
@@ -652,13 +643,9 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
                 sf + 4 * a,
                 ptx::smem_desc(ptx::smem_u32(smem + C::OFF_WSF + (s * NA + a) * kSfAtomBytes), 128,
                                128, ptx::kSwizzleNone));
-#pragma unroll
-          for (int a = 0; a < C::TOK_ATOMS; ++a)
-            ptx::tmem_cp_32x128b_x4(
-                tok_sf + 4 * a,
-                ptx::smem_desc(
-                    ptx::smem_u32(smem + C::OFF_TSF + (s * C::TOK_ATOMS + a) * kSfAtomBytes), 128,
-                    128, ptx::kSwizzleNone));
+          ptx::tmem_cp_32x128b_x4(
+              tok_sf, ptx::smem_desc(ptx::smem_u32(smem + C::OFF_TSF + s * kSfAtomBytes), 128, 128,
+                                     ptx::kSwizzleNone));
 #pragma unroll
           for (int a = 0; a < NA; ++a) {
             const uint64_t adesc =
@@ -799,6 +786,320 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// The form for tiles of more than 128 tokens: CTA pairs.  One MMA (cta_group::2) takes
+// 256 weight rows, 128 of each CTA (two row blocks side by side), against the
+// tile's tokens, of which each CTA holds half.  Shared memory is what bounds the
+// streaming form (128 bytes a cycle: a stage of 240 tokens writes 46 KB and the
+// MMAs read 46 KB, 720 cycles where the products take 480; measured 712), and a
+// pair writes and reads each token once for both CTAs (30 + 31 KB).  Roles and
+// epilogue are those of the streaming form, with these differences: the even
+// CTA issues the MMAs and scale copies for both; the odd CTA's copies and scale
+// words count on the even CTA's barriers; stages and accumulators are handed
+// back to, and released by, both.  With an odd number of row blocks the last
+// pair's odd CTA repeats the last block and stores nothing.
+template <int MODE>
+struct PairCfg {
+  static constexpr int NA = MODE == kGateUp ? 2 : 1;
+  static constexpr int NT = kMaxTokens;
+  static constexpr int GROUPS = 3, THREADS = 128 + 128 * GROUPS;
+  static constexpr int TOK_ATOMS = 2;
+  static constexpr int BOX_ROWS = 40;  // rows of a copy of tokens
+  static constexpr int TOK_TILE = NT / 2 * 128;
+  static_assert((NT / 2) % BOX_ROWS == 0 && BOX_ROWS % 8 == 0, "token copies");
+  static constexpr int STAGE = NA * (kTileBytes + kSfAtomBytes) + TOK_TILE + TOK_ATOMS * kSfAtomBytes;
+  static constexpr int MAX_BYTES = MODE == kGateUp ? GROUPS * 2 * 4 * kChunk * 4 : 0;
+  static constexpr int NSTAGE = (232448 - 1024 - 512 - MAX_BYTES) / STAGE;
+  static constexpr int OFF_W = 0;
+  static constexpr int OFF_TOK = NSTAGE * NA * kTileBytes;
+  static constexpr int OFF_WSF = OFF_TOK + NSTAGE * TOK_TILE;
+  static constexpr int OFF_TSF = OFF_WSF + NSTAGE * NA * kSfAtomBytes;
+  static constexpr int OFF_MAX = OFF_TSF + NSTAGE * TOK_ATOMS * kSfAtomBytes;
+  static constexpr int OFF_BAR = OFF_MAX + MAX_BYTES;
+  static constexpr int SMEM = OFF_BAR + (2 * NSTAGE + 5) * 8 + 32 + 1024;
+  static constexpr int SF_COLS = 4 * NA + 4 * TOK_ATOMS;
+  static constexpr int NBUF = 2 * NA * NT + 2 * SF_COLS <= 512 ? 2 : 1;
+  static constexpr int SF_RING = 2;
+  static constexpr uint32_t IDESC = (5u << 7) | (1u << 23) | ((256u >> 4) << 24);
+  static_assert(NBUF * NA * NT + SF_RING * SF_COLS <= 512 && SMEM <= 232448 && TOK_TILE % 1024 == 0,
+                "budgets");
+};
+
+template <int MODE>
+__global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
+    w4_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_sf,
+                   const __grid_constant__ CUtensorMap tm_a, const W4Args p) {
+  using C = PairCfg<MODE>;
+  constexpr int NA = C::NA, NSTAGE = C::NSTAGE, NT = C::NT;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // the even CTA's count
+  uint64_t* empty = full + NSTAGE;
+  uint64_t* acc_full = empty + NSTAGE;  // [2]
+  uint64_t* acc_empty = acc_full + 2;   // [2], the even CTA's count
+  uint64_t* done = acc_empty + 2;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(slot + 1);
+
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = (int)ptx::cluster_rank();
+  ptx::griddep_launch_dependents();
+
+  const int nk = p.KB, NBP = (p.NB + 1) / 2;
+  const int u_first = (int)(blockIdx.x >> 1), u_step = (int)(gridDim.x >> 1);
+  auto block_of = [&](int u) { return 2 * (u % NBP) + rank; };  // may be NB: nothing of it is stored
+  int units;
+  if constexpr (MODE == kLinear) {
+    units = p.n_tiles_host * NBP;
+    if (warp == 0 && lane < NSTAGE && lane < nk && u_first < units)
+      ptx::prefetch_l2_bulk(
+          p.w + ((size_t)min(block_of(u_first), p.NB - 1) * p.KB + lane) * kBlockBytes, kBlockBytes);
+    ptx::griddep_wait();
+  } else {
+    ptx::griddep_wait();
+    units = *p.n_tiles * NBP;
+  }
+  if (u_first >= units) return;
+
+  auto tile_of = [&](int u) {
+    Tile t;
+    if constexpr (MODE == kLinear) {
+      t.expert = 0;
+      t.row0 = (u / NBP) * p.per_tile;
+      t.count = min(p.per_tile, p.T - t.row0);
+    } else {
+      const int4 v = *reinterpret_cast<const int4*>(p.tiles + u / NBP);
+      t.expert = __shfl_sync(0xffffffffu, v.x, 0);
+      t.row0 = __shfl_sync(0xffffffffu, v.y, 0);
+      t.count = __shfl_sync(0xffffffffu, v.z, 0);
+    }
+    return t;
+  };
+
+  if (threadIdx.x == 0) {
+    ptx::prefetch_tmap(&tm_w);
+    ptx::prefetch_tmap(&tm_sf);
+    ptx::prefetch_tmap(&tm_a);
+    for (int i = 0; i < NSTAGE; ++i) {
+      ptx::mbar_init(&full[i], 3);  // the expected bytes, and both CTAs' token scales
+      ptx::mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&acc_full[i], 1);
+      ptx::mbar_init(&acc_empty[i], 2 * 4 * C::GROUPS);
+    }
+    ptx::mbar_init(done, 1);
+    ptx::fence_barrier_init();
+    *abort_flag = 0;
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(slot, 512);
+    ptx::tmem_relinquish_pair();
+    ptx::tc_fence_before();
+  }
+  __syncthreads();
+  ptx::cluster_sync();  // both CTAs' barriers are set up
+  ptx::tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);
+  const uint32_t even_full = ptx::map_shared_rank(ptx::smem_u32(full), 0);
+  const uint32_t even_acc = ptx::map_shared_rank(ptx::smem_u32(acc_empty), 0);
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu,
+                   !*abort_flag && ptx::mbar_wait_hint(bar, parity, kWaitNs, kHintNs)))
+      return true;
+    if (lane == 0 && !*abort_flag) atomicOr(p.wd, kWdW4);
+    *abort_flag = 1;
+    return false;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- copies
+    int it = 0;
+    bool ok = true;
+    for (int u = u_first; u < units && ok; u += u_step) {
+      const Tile t = tile_of(u);
+      const int half = (t.count + 15) / 16 * 8;  // tokens held by each CTA
+      const int boxes = (half + C::BOX_ROWS - 1) / C::BOX_ROWS;
+      const uint32_t bytes = 2u * (uint32_t)(NA * kBlockBytes + boxes * C::BOX_ROWS * 128);
+      const int rb = min(block_of(u), p.NB - 1);
+      int blk[NA];
+#pragma unroll
+      for (int a = 0; a < NA; ++a)
+        blk[a] = ((MODE == kGateUp ? 2 * t.expert + a : t.expert) * p.NB + rb) * p.KB;
+      for (int kk = 0; kk < nk; ++kk, ++it) {
+        const int s = it % NSTAGE;
+        ok = wait(&empty[s], ((uint32_t)(it / NSTAGE) & 1u) ^ 1u);
+        if (!ok) break;
+        if (ptx::elect_one()) {
+          const uint32_t bar = even_full + 8u * (uint32_t)s;
+          if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], bytes);
+#pragma unroll
+          for (int a = 0; a < NA; ++a) {
+            ptx::tma_load_2d_pair(smem + C::OFF_W + (s * NA + a) * kTileBytes, &tm_w, bar, 0,
+                                  blk[a] * (kBlockBytes / 64));
+            ptx::tma_load_2d_pair(smem + C::OFF_WSF + (s * NA + a) * kSfAtomBytes, &tm_sf, bar, 0,
+                                  blk[a] * (kBlockBytes / 256) + kCodeBytes / 256);
+            ++blk[a];
+          }
+#pragma unroll
+          for (int b = 0; b < NT / 2 / C::BOX_ROWS; ++b)
+            if (b < boxes)
+              ptx::tma_load_2d_pair(smem + C::OFF_TOK + s * C::TOK_TILE + b * C::BOX_ROWS * 128, &tm_a,
+                                    bar, kk * 128, t.row0 + rank * half + b * C::BOX_ROWS);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------- token scales
+    constexpr int ROWS = (NT + 31) / 32;
+    struct Rows {
+      const uint8_t* src[ROWS];
+      uint32_t byte[ROWS];
+    };
+    auto rows_of = [&](int u, Rows& r) {
+      const Tile t = tile_of(u);
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
+        const int i = t.row0 + min(32 * j + lane, t.count - 1);
+        r.src[j] = p.a_sf + (size_t)(MODE == kGateUp ? p.perm[i] / p.k : i) * p.KG;
+      }
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) r.byte[j] = r.src[j][0];
+    };
+    Rows now, then;
+    rows_of(u_first, now);
+    int it = 0;
+    bool ok = true;
+    for (int u = u_first; u < units && ok; u += u_step) {
+      if (u + u_step < units) rows_of(u + u_step, then);
+      for (int kk = 0; kk < nk; ++kk, ++it) {
+        const int s = it % NSTAGE;
+        ok = wait(&empty[s], ((uint32_t)(it / NSTAGE) & 1u) ^ 1u);
+        if (!ok) break;
+        uint8_t* atom = smem + C::OFF_TSF + s * C::TOK_ATOMS * kSfAtomBytes;
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) {
+          const uint32_t w = now.byte[j] * 0x01010101u;
+          if (kk + 1 < nk) now.byte[j] = now.src[j][kk + 1];
+          *reinterpret_cast<uint32_t*>(atom + (j >> 2) * kSfAtomBytes + lane * 16 + (j & 3) * 4) = w;
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_remote(even_full + 8u * (uint32_t)s);
+      }
+      now = then;
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ----------------------------------------------------------------- MMA
+    int it = 0, n = 0;
+    bool ok = true;
+    for (int u = u_first; u < units && ok; u += u_step, ++n) {
+      const int buf = C::NBUF == 2 ? n & 1 : 0;
+      const uint32_t idesc = C::IDESC | ((uint32_t)((tile_of(u).count + 15) / 16 * 2) << 17);
+      const uint32_t d = tmem + buf * NA * NT;
+      ok = wait(&acc_empty[buf], ((uint32_t)(n / C::NBUF) & 1u) ^ 1u);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      for (int kk = 0; kk < nk; ++kk, ++it) {
+        const int s = it % NSTAGE;
+        ok = wait(&full[s], (uint32_t)(it / NSTAGE) & 1u);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          const uint32_t sf = tmem + C::NBUF * NA * NT + (it % C::SF_RING) * C::SF_COLS;
+          const uint32_t tok_sf = sf + 4 * NA;
+          const uint64_t bdesc = ptx::smem_desc(
+              ptx::smem_u32(smem + C::OFF_TOK + s * C::TOK_TILE), 16, 1024, ptx::kSwizzle128B);
+#pragma unroll
+          for (int a = 0; a < NA; ++a)
+            ptx::tmem_cp_32x128b_x4_pair(
+                sf + 4 * a,
+                ptx::smem_desc(ptx::smem_u32(smem + C::OFF_WSF + (s * NA + a) * kSfAtomBytes), 128,
+                               128, ptx::kSwizzleNone));
+#pragma unroll
+          for (int a = 0; a < C::TOK_ATOMS; ++a)
+            ptx::tmem_cp_32x128b_x4_pair(
+                tok_sf + 4 * a,
+                ptx::smem_desc(
+                    ptx::smem_u32(smem + C::OFF_TSF + (s * C::TOK_ATOMS + a) * kSfAtomBytes), 128,
+                    128, ptx::kSwizzleNone));
+#pragma unroll
+          for (int a = 0; a < NA; ++a) {
+            const uint64_t adesc =
+                ptx::smem_desc(ptx::smem_u32(smem + C::OFF_W + (s * NA + a) * kTileBytes), 16, 1024,
+                               ptx::kSwizzle128B);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              ptx::mma_mxf8_pair(d + a * NT, adesc + 2 * k, bdesc + 2 * k,
+                                 idesc | ((uint32_t)k << 29) | ((uint32_t)k << 4), sf + 4 * a, tok_sf,
+                                 (kk > 0 || k > 0) ? 1u : 0u);
+          }
+          ptx::tc_commit_pair_mc(&empty[s], 3);  // frees the stage in both CTAs
+        }
+        __syncwarp();
+      }
+      if (ptx::elect_one()) ptx::tc_commit_pair_mc(&acc_full[buf], 3);
+      __syncwarp();
+    }
+    if (ptx::elect_one()) ptx::tc_commit_pair_mc(done, 1);
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, group = (warp - 4) >> 2;
+    float* max_ = reinterpret_cast<float*>(smem + C::OFF_MAX) + group * 2 * 4 * kChunk;
+    int n = 0, chunk_no = 0;
+    for (int u = u_first; u < units; u += u_step, ++n) {
+      const int buf = C::NBUF == 2 ? n & 1 : 0;
+      const Tile t = tile_of(u);
+      const int rb = block_of(u);
+      const int chunks = (t.count + kChunk - 1) / kChunk;
+      const bool ok = wait(&acc_full[buf], (uint32_t)(n / C::NBUF) & 1u);
+      if (!ptx::named_sync_and(1 + group, 128, ok)) break;
+      ptx::tc_fence_after();
+      const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + buf * NA * NT;
+      for (int c = group; c < chunks; c += C::GROUPS, ++chunk_no) {
+        uint32_t r[NA][kChunk];
+#pragma unroll
+        for (int a = 0; a < NA; ++a) ptx::tmem_ld_32x32b_x16(t0 + a * NT + c * kChunk, r[a]);
+        ptx::tmem_ld_wait();
+        if (c + C::GROUPS >= chunks) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_remote(even_acc + 8u * (uint32_t)buf);
+        }
+        float v[NA][kChunk];
+#pragma unroll
+        for (int a = 0; a < NA; ++a)
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i) v[a][i] = __uint_as_float(r[a][i]);
+        finish_chunk<MODE, NA>(p, v, t.row0 + c * kChunk, t.count - c * kChunk, rb, q, lane,
+                               max_ + (chunk_no & 1) * 4 * kChunk, 1 + group);
+      }
+      if (group >= chunks) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_remote(even_acc + 8u * (uint32_t)buf);
+      }
+    }
+  }
+  __syncthreads();
+  if (*abort_flag) {
+    // What the even CTA issued completes; copies still in flight, the other CTA's
+    // too, land within this millisecond (they take a few microseconds).
+    if (threadIdx.x == 0) {
+      if (rank == 0) ptx::mbar_wait(done, 0, kWaitNs);
+      const uint64_t t0 = ptx::globaltimer();
+      while (ptx::globaltimer() - t0 < 1000000ull) __nanosleep(1000);
+    }
+    __syncthreads();
+  }
+  ptx::cluster_sync();  // neither CTA leaves while the other may still use it
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -1047,7 +1348,7 @@ cudaError_t launch_cfg(const void* a, uint64_t a_rows, uint64_t K, uint64_t bloc
   using C = Cfg<MODE, NT, SPLIT>;
   CUtensorMap tm_w, tm_a;
   if (!encode_weight(&tm_w, args.w, blocks) ||
-      !encode_rows(&tm_a, a, K, a_rows, C::GATHER ? 1 : C::BOX_ROWS)) {
+      !encode_rows(&tm_a, a, K, a_rows, C::GATHER ? 1 : NT)) {
     *why = "cuTensorMapEncodeTiled failed (driver entry point missing or arguments rejected)";
     return cudaErrorInvalidValue;
   }
@@ -1083,6 +1384,71 @@ cudaError_t launch_cfg(const void* a, uint64_t a_rows, uint64_t K, uint64_t bloc
   return cudaLaunchKernelEx(&cfg, kern, tm_w, tm_a, args);
 }
 
+// Scale atoms of the prepared weight, as two rows of 256 bytes each.
+bool encode_atoms(CUtensorMap* m, const void* base, uint64_t blocks) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {256, blocks * (kBlockBytes / 256)};
+  cuuint64_t strides[1] = {256};
+  cuuint32_t box[2] = {256, kSfAtomBytes / 256};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE>
+cudaError_t launch_pair(const void* a, uint64_t a_rows, uint64_t K, uint64_t blocks, const W4Args& args,
+                        int64_t tiles, int num_sms, cudaStream_t s, const char** why) {
+  using C = PairCfg<MODE>;
+  CUtensorMap tm_w, tm_sf, tm_a;
+  if (!encode_weight(&tm_w, args.w, blocks) || !encode_atoms(&tm_sf, args.w, blocks) ||
+      !encode_rows(&tm_a, a, K, a_rows, C::BOX_ROWS)) {
+    *why = "cuTensorMapEncodeTiled failed (driver entry point missing or arguments rejected)";
+    return cudaErrorInvalidValue;
+  }
+  auto kern = w4_pair_kernel<MODE>;
+  static std::atomic<uint64_t> smem_set{0};
+  static std::atomic<int> pair_slots[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(smem_set.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    smem_set.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(C::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  // One pair for each place that the device has for it.
+  int slots = pair_slots[dev & 63].load(std::memory_order_acquire);
+  if (slots == 0) {
+    cfg.gridDim = dim3(2u * (unsigned)(num_sms / 2), 1, 1);
+    e = cudaOccupancyMaxActiveClusters(&slots, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    if (slots <= 0) {
+      *why = "no CTA pair fits on this device";
+      return cudaErrorInvalidConfiguration;
+    }
+    pair_slots[dev & 63].store(slots, std::memory_order_release);
+  }
+  const int64_t units = tiles * ((args.NB + 1) / 2);
+  cfg.gridDim = dim3(2u * (unsigned)(units < slots ? units : slots), 1, 1);
+  return cudaLaunchKernelEx(&cfg, kern, tm_w, tm_sf, tm_a, args);
+}
+
 // The product for tiles of at most `nt` tokens (16, 32, 64, 128 or 240), its K
 // split where the caller chose so (16 and, dense, 32 tokens only).
 template <int MODE>
@@ -1110,7 +1476,7 @@ cudaError_t launch_tokens(int nt, const void* a, uint64_t a_rows, uint64_t K, ui
   }
   if (nt <= 64) return launch_cfg<MODE, 64, false>(a, a_rows, K, blocks, g, units, num_sms, s, why);
   if (nt <= 128) return launch_cfg<MODE, 128, false>(a, a_rows, K, blocks, g, units, num_sms, s, why);
-  return launch_cfg<MODE, kMaxTokens, false>(a, a_rows, K, blocks, g, units, num_sms, s, why);
+  return launch_pair<MODE>(a, a_rows, K, blocks, g, units / g.NB, num_sms, s, why);
 }
 
 // CTAs along K for `units` units of KB blocks each: powers of two up to the
@@ -1151,14 +1517,16 @@ cudaError_t launch_linear_a8w4(const uint8_t* a, const uint8_t* a_sf, const uint
     g.splits = pick_splits(g.NB, g.KB, 2 * num_sms);
     g.per_tile = T <= 16 ? 16 : 32;
   } else {
-    // Tiles of even size.  A stage costs about 256 + 2 n cycles of shared memory
-    // for n tokens (the weight tile's write and read, and the tokens'), so the
-    // number of tiles is the one with the least rounds x (128 + n).
+    // Tiles of even size.  A stage of n tokens costs about 256 + 2 n cycles of
+    // shared memory (the weight tile's write and read, and the tokens'), or, above
+    // 128 tokens, 256 + n in each CTA of a pair: the number of tiles is the one with
+    // the least rounds x that.
     int64_t best = -1;
     const int64_t least = ceil_div(T, kMaxTokens);
-    for (int64_t n = least; n <= least + 8; ++n) {
-      const int64_t per = ceil_div(ceil_div(T, n), 16) * 16;
-      const int64_t cost = ceil_div(ceil_div(T, per) * g.NB, num_sms) * (128 + per);
+    for (int64_t n = least; n <= least + 24; ++n) {
+      const int64_t per = ceil_div(ceil_div(T, n), 16) * 16, tiles = ceil_div(T, per);
+      const int64_t cost = per > 128 ? ceil_div(tiles * ((g.NB + 1) / 2), num_sms / 2) * (256 + per)
+                                     : ceil_div(tiles * g.NB, num_sms) * (256 + 2 * per);
       if (best < 0 || cost < best) {
         best = cost;
         g.per_tile = (int)per;
