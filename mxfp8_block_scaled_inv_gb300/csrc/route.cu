@@ -63,7 +63,7 @@ __device__ __forceinline__ float score_of(int scoring, float l, float mx, float 
   if (scoring == MXQ_SCORE_SIGMOID) return __fdividef(1.0f, 1.0f + expf(-l));
   return sqrtf(fmaxf(l, 0.0f) + log1pf(expf(-fabsf(l))));
 }
-__device__ __forceinline__ double score_of(int scoring, double l, double mx, double z) {
+__device__ __noinline__ double score_of(int scoring, double l, double mx, double z) {
   if (scoring == MXQ_SCORE_SOFTMAX) return exp(l - mx) / z;
   if (scoring == MXQ_SCORE_SIGMOID) return 1.0 / (1.0 + exp(-l));
   return sqrt(fmax(l, 0.0) + log1p(exp(-fabs(l))));
@@ -107,78 +107,91 @@ __device__ __forceinline__ void merge2(R& a1, R& a2, R b1, R b2) {
   a2 = lo > hi2 ? lo : hi2;
 }
 
-// A whole row with 64-bit scores, one expert after the other: lane j < k
-// returns the j-th expert (-1: none) and its score.
+// Order-preserving 64-bit key of a finite value, never 0, and back: comparisons of
+// doubles run on the few 64-bit units, those of integers do not.
+typedef unsigned long long Key64;
+__device__ __forceinline__ Key64 key64_of(double v) {
+  const Key64 u = (Key64)__double_as_longlong(v + 0.0);
+  return (u >> 63) ? ~u : (u | (1ull << 63));
+}
+__device__ __forceinline__ double value64_of(Key64 k) {
+  return __longlong_as_double((long long)((k >> 63) ? (k & ~(1ull << 63)) : ~k));
+}
+
+// A whole row with 64-bit scores: lane j < k returns the j-th expert (-1: none) and
+// its score.  Lane i holds the experts i, i + 32, ...
 __device__ __noinline__ void route_row_64(const RouteArgs& a, int64_t t, bool bf16, int lane,
                                           int* expert, float* score) {
-  const double none = -(double)INFINITY;
   const int rounds = (a.E + 31) / 32;
   double mx = 0.0, z = 1.0;
   if (a.scoring == MXQ_SCORE_SOFTMAX) {
-    double m = none;
-    for (int e = lane; e < a.E; e += 32) m = fmax(m, (double)clean_logit(load_logit(a, t, e, bf16)));
-    mx = warp_max(m);
+    float m = -INFINITY;
+    for (int e = lane; e < a.E; e += 32) m = fmaxf(m, clean_logit(load_logit(a, t, e, bf16)));
+    mx = (double)warp_max(m);
     double s = 0.0;
-    for (int e = lane; e < a.E; e += 32) {
-      const float l = clean_logit(load_logit(a, t, e, bf16));
-      if (l > -INFINITY) s += exp((double)l - mx);
+    for (int i = 0; i < rounds; ++i) {
+      const int e = i * 32 + lane;
+      const float l = e < a.E ? clean_logit(load_logit(a, t, e, bf16)) : -INFINITY;
+      if (l > -INFINITY) s += score_of(a.scoring, (double)l, mx, 1.0);
     }
     z = warp_sum(s);
   }
-  double c[kMaxExperts / 32];  // of the experts lane, lane + 32, ...
+  Key64 c[kMaxExperts / 32];  // 0: not to be chosen
   for (int i = 0; i < rounds; ++i) {
     const int e = i * 32 + lane;
-    c[i] = none;
+    c[i] = 0;
     if (e < a.E) {
       const float l = clean_logit(load_logit(a, t, e, bf16));
       const float b = a.bias != nullptr ? clean_bias(a.bias[e]) : 0.0f;
-      if (l > -INFINITY && b > -INFINITY) c[i] = score_of(a.scoring, (double)l, mx, z) + (double)b;
+      if (l > -INFINITY && b > -INFINITY)
+        c[i] = key64_of(score_of(a.scoring, (double)l, mx, z) + (double)b);
     }
   }
   if (a.keep < a.groups) {
-    double mine = none;  // lane g: the value of group g
+    Key64 mine = 0;  // lane g: the value of group g
     for (int g = 0; g < a.groups; ++g) {
-      double a1 = none, a2 = none;
+      Key64 a1 = 0, a2 = 0;
       for (int i = 0; i < rounds; ++i) {
-        const int e = i * 32 + lane;
-        if (e < a.E && e / a.per_group == g) merge2(a1, a2, c[i], none);
+        const int at = i * 32 + lane - g * a.per_group;
+        if (at >= 0 && at < a.per_group) merge2(a1, a2, c[i], (Key64)0);
       }
       for (int m = 16; m > 0; m >>= 1) {
-        const double o1 = __shfl_xor_sync(kAll, a1, m), o2 = __shfl_xor_sync(kAll, a2, m);
+        const Key64 o1 = __shfl_xor_sync(kAll, a1, m), o2 = __shfl_xor_sync(kAll, a2, m);
         merge2(a1, a2, o1, o2);
       }
-      if (lane == g) mine = a.group_top == 2 && a2 > none ? a1 + a2 : a1;
+      if (lane == g)
+        mine = a.group_top == 2 && a2 != 0 ? key64_of(value64_of(a1) + value64_of(a2)) : a1;
     }
     int rank = 0;
     for (int g = 0; g < a.groups; ++g) {
-      const double v = __shfl_sync(kAll, mine, g);
+      const Key64 v = __shfl_sync(kAll, mine, g);
       rank += v > mine || (v == mine && g < lane) ? 1 : 0;
     }
     const uint32_t kept = __ballot_sync(kAll, lane < a.groups && rank < a.keep);
     for (int i = 0; i < rounds; ++i) {
       const int e = i * 32 + lane;
-      if (e < a.E && !((kept >> (e / a.per_group)) & 1u)) c[i] = none;
+      if (e < a.E && !((kept >> (e / a.per_group)) & 1u)) c[i] = 0;
     }
   }
   if (a.bias == nullptr) {
     for (int i = 0; i < rounds; ++i)
-      if (c[i] > none) c[i] = (double)clean_logit(load_logit(a, t, i * 32 + lane, bf16));
+      if (c[i] != 0) c[i] = key_of(clean_logit(load_logit(a, t, i * 32 + lane, bf16)));
   }
   *expert = -1;
   *score = 0.0f;
   for (int j = 0; j < a.k; ++j) {
-    double best = none;
+    Key64 best = 0;
     int at = 0;
     for (int i = 0; i < rounds; ++i)
       if (c[i] > best) {
         best = c[i];
         at = i;
       }
-    const double top = warp_max(best);
-    if (top == none) break;
+    const Key64 top = warp_max(best);
+    if (top == 0) break;
     // The lowest index among the lanes that hold it.
     const int e = (int)__reduce_min_sync(kAll, best == top ? (uint32_t)(at * 32 + lane) : 0xffffffffu);
-    if (lane == (e & 31)) c[e >> 5] = none;
+    if (lane == (e & 31)) c[e >> 5] = 0;
     if (lane == j) *expert = e;
   }
   if (*expert >= 0)
@@ -203,8 +216,68 @@ __device__ __forceinline__ void sort_pass(uint32_t (&v)[PER]) {
     sort_pass<PER, 2 * P, 2 * P>(v);
 }
 
+// The rare parts that follow read the row again instead of taking the caller's
+// arrays, which stay in registers that way.
+
+// A softmax row's sum of exponentials in 64 bits; lane i holds `per` experts.
+__device__ __noinline__ double row_sum_64(const RouteArgs& a, int64_t t, bool bf16, int lane, int per,
+                                          float mx) {
+  double s = 0.0;
+  for (int e = lane * per; e < min(lane * per + per, a.E); ++e) {
+    const float l = clean_logit(load_logit(a, t, e, bf16));
+    if (l > -INFINITY) s += score_of(MXQ_SCORE_SOFTMAX, (double)l, (double)mx, 1.0);
+  }
+  return warp_sum(s);
+}
+
+// Which groups stay where the last one kept (of value x) and the first one left (y)
+// are too near to call: the groups within `edge` of them are ordered by the 64-bit
+// sums of their n best (those with an fp32 value of `least` and more), the others stay
+// where they are.  v, g: the lane's group; false in *sure where a group has more
+// than its n best that near to each other.
+__device__ __noinline__ bool keep_group_64(const RouteArgs& a, int64_t t, bool bf16, int lane, int per,
+                                           float mx, float inv_z, float v, int g, float x, float y,
+                                           float edge, float least, int n, bool* sure) {
+  const bool close = g < a.groups && v >= y - edge && v <= x + edge;
+  const double z = a.scoring == MXQ_SCORE_SOFTMAX && a.bias != nullptr
+                       ? row_sum_64(a, t, bf16, lane, per, mx) : 1.0;
+  double sum = 0.0;
+  int found = 0;
+  for (int i = 0; i < per; ++i) {
+    const int e = lane * per + i;
+    float l = -INFINITY, b = 0.0f;
+    if (close && e < a.E) {
+      l = clean_logit(load_logit(a, t, e, bf16));
+      if (a.bias != nullptr) b = clean_bias(a.bias[e]);
+    }
+    const bool counts = l > -INFINITY && b > -INFINITY && score_of(a.scoring, l, mx, inv_z) + b >= least;
+    if (__any_sync(kAll, counts)) {
+      const double s = score_of(a.scoring, (double)l, (double)mx, z) + (double)b;
+      if (counts) {
+        sum += s;
+        ++found;
+      }
+    }
+  }
+  for (int m = 1; m < a.lanes; m <<= 1) {
+    sum += __shfl_xor_sync(kAll, sum, m);
+    found += __shfl_xor_sync(kAll, found, m);
+  }
+  *sure = !__any_sync(kAll, close && found != n);
+  const Key64 mine = close ? key64_of(sum) : 0;
+  int rank = 0, above = 0;
+  for (int q = 0; q < a.groups; ++q) {
+    const Key64 o = __shfl_sync(kAll, mine, q * a.lanes);
+    rank += o > mine || (o == mine && q < g) ? 1 : 0;
+    above += __shfl_sync(kAll, v, q * a.lanes) > x + edge ? 1 : 0;
+  }
+  return v > x + edge || (close && rank < a.keep - above);
+}
+
+// (The bound on registers is what the common path needs; the rare parts, whose calls
+// would otherwise set it, keep more of theirs in memory.)
 template <int PER, bool BF16>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER == 16 ? 6 : 4) route_kernel(const RouteArgs a) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int lane = threadIdx.x & 31;
@@ -301,11 +374,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
     for (int i = 0; i < PER; ++i) c[i] = l[i] > -INFINITY ? c[i] + clean_bias(b[i]) : -INFINITY;
     uint32_t in = 0xffffffffu;  // bit i: the group of expert i is kept
     if (grouped) {
-      float v = -INFINITY;  // a group's value, and whether it is this lane's to rank
+      float v = -INFINITY;  // a group's value
+      float a1 = -INFINITY, a2 = -INFINITY;
       int g;
       if (a.lanes > 0) {
         // A group is a run of 2^n lanes.
-        float a1 = -INFINITY, a2 = -INFINITY;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
           a2 = fmaxf(a2, fminf(a1, c[i]));
@@ -320,7 +393,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
       } else {
         // Groups that begin or end inside a lane: one after the other.
         for (int q = 0; q < a.groups; ++q) {
-          float a1 = -INFINITY, a2 = -INFINITY;
+          a1 = a2 = -INFINITY;
 #pragma unroll
           for (int i = 0; i < PER; ++i) {
             const int at = e0 + i - q * a.per_group;
@@ -344,13 +417,21 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
         const float o = __shfl_sync(kAll, v, q * step);
         rank += o > v || (o == v && q < g) ? 1 : 0;
       }
-      const bool kept = rank < a.keep;
+      bool kept = rank < a.keep;
       const uint32_t vkey = g < a.groups && v > -INFINITY ? key_of(v) : 0u;
       const uint32_t low = __reduce_min_sync(kAll, kept && g < a.groups ? vkey : 0xffffffffu);
       const uint32_t high = __reduce_max_sync(kAll, kept ? 0u : vkey);
       if (low != 0u && high != 0u) {
         const float x = value_of(low), y = value_of(high);
-        whole = !(x - y > 2.0f * slack + 2.5e-7f * (fabsf(x) + fabsf(y)));
+        const float edge = 2.0f * slack + 2.5e-7f * (fabsf(x) + fabsf(y));
+        if (!(x - y > edge)) {
+          bool sure = false;  // (groups that do not lie on lanes: the whole row)
+          const bool two = a.group_top == 2 && a2 > -INFINITY;
+          if (a.lanes > 0)
+            kept = keep_group_64(a, t, BF16, lane, PER, mx, inv_z, v, g, x, y, edge,
+                                 (two ? a2 : a1) - edge, two ? 2 : 1, &sure);
+          whole = !sure;
+        }
       }
       if (a.lanes > 0) {
         in = kept ? 0xffffffffu : 0u;
@@ -445,17 +526,16 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
         while (picks > a.k && picks < 32 && __shfl_sync(kAll, (int)near_prev(), picks - 1) && pick()) {
           look_up();
         }
-        if (a.scoring == MXQ_SCORE_SOFTMAX ||
-            (__shfl_sync(kAll, (int)near_prev(), picks - 1) && near_rest())) {
+        if (__shfl_sync(kAll, (int)near_prev(), picks - 1) && near_rest()) {
           whole = true;
         } else {
           fetch();
-          const double c = expert >= 0
-                               ? score_of(a.scoring, (double)lj, 0.0, 1.0) + (double)bj
-                               : -(double)INFINITY;
+          const double z = a.scoring == MXQ_SCORE_SOFTMAX ? row_sum_64(a, t, BF16, lane, PER, mx) : 1.0;
+          const Key64 c =
+              expert >= 0 ? key64_of(score_of(a.scoring, (double)lj, (double)mx, z) + (double)bj) : 0;
           int rank = 0;
           for (int j = 0; j < picks; ++j) {
-            const double o = __shfl_sync(kAll, c, j);
+            const Key64 o = __shfl_sync(kAll, c, j);
             const int oe = __shfl_sync(kAll, expert, j);
             rank += o > c || (o == c && oe < expert) ? 1 : 0;
           }
