@@ -535,8 +535,8 @@ size_t mxq_experts_workspace_bytes(int64_t T, int32_t k, int32_t E, int32_t K, i
  * Results do not depend on timing: atomics only choose where a row's sums are
  * kept meanwhile.
  * 1 <= k <= 32, 1 <= E <= 1024, K and I multiples of 32 up to 65536, N % 16 ==
- * 0, N >= 16.  T == 0 is a no-op.  T*k >= 2^24, or a weight of more than 2^31
- * rows of 64 bytes, returns MXQ_ERR_UNSUPPORTED.
+ * 0, N >= 16.  T == 0 is a no-op.  T*k >= 2^24, T*N >= 2^35 or a weight of
+ * more than 2^31 rows of 64 bytes returns MXQ_ERR_UNSUPPORTED.
  */
 int mxq_experts_a8w4(const uint8_t* a_e4m3, const uint8_t* a_e8m0, const int32_t* ids,
                      const float* weights, const uint8_t* w13, const uint8_t* w2, void* out_bf16,
@@ -581,7 +581,7 @@ int mxq_linear_noalloc(const void* x_bf16, const uint8_t* w_e4m3, const uint8_t*
 
 /*
  * Testing aids (the pages have no counterpart), process-wide settings that
- * change no result (but for the last).
+ * change no result (but for the last two).
  *
  * mxq_debug_set_pair_limit caps the number of CTA pairs that the many-token
  * GEMM forms launch -- mxq_bmm_a8w8, mxq_wo_a and mxq_linear above 128
@@ -610,11 +610,15 @@ int mxq_linear_noalloc(const void* x_bf16, const uint8_t* w_e4m3, const uint8_t*
  * out ends the kernel as mxq_watchdog_read describes: a bound of a few
  * microseconds exercises that path, and leaves the call's outputs undefined.
  * Returns the previous bound.
+ *
+ * mxq_debug_set_w4_wait does the same for the kernels of mxq_linear_a8w4 and
+ * mxq_experts_a8w4.
  */
 int mxq_debug_set_pair_limit(int pairs);
 int mxq_debug_set_lazy_pairs(int from);
 int mxq_debug_takeovers(uint32_t* host_value, int clear);
 uint32_t mxq_debug_set_attn_wait(uint32_t ns);
+uint32_t mxq_debug_set_w4_wait(uint32_t ns);
 
 /*
  * Watchdog word of the GEMM kernels, of the streamed query copy of the

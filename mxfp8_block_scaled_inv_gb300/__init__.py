@@ -31,7 +31,7 @@ __all__ = [
     "mxq_add_rms_norm", "mxq_route", "mxq_w4_bytes", "mxq_prepare_w4", "mxq_linear_a8w4",
     "mxq_experts_workspace_bytes", "mxq_experts_a8w4",
     "mxq_debug_set_pair_limit", "mxq_debug_set_lazy_pairs", "mxq_debug_takeovers",
-    "mxq_debug_set_attn_wait",
+    "mxq_debug_set_attn_wait", "mxq_debug_set_w4_wait",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -88,6 +88,7 @@ _SIGNATURES = {
     "mxq_debug_set_lazy_pairs": (ctypes.c_int, [ctypes.c_int]),
     "mxq_debug_takeovers": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]),
     "mxq_debug_set_attn_wait": (ctypes.c_uint32, [ctypes.c_uint32]),
+    "mxq_debug_set_w4_wait": (ctypes.c_uint32, [ctypes.c_uint32]),
     "mxq_wo_a_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32]),
     "mxq_rope_kv_insert": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _i64,
                                           _i64, _i32, _vp, _vp, _i64, _i32, _vp, _vp, _vp]),
@@ -325,6 +326,12 @@ def mxq_debug_set_attn_wait(ns):
     seconds); returns the previous bound.  A wait that runs out sets bit 0x40 of the watchdog word and
     leaves the call's outputs undefined."""
     return lib().mxq_debug_set_attn_wait(int(ns))
+
+
+def mxq_debug_set_w4_wait(ns):
+    """Testing aid: mxq_debug_set_attn_wait for the kernels of mxq_linear_a8w4 and mxq_experts_a8w4, whose waits
+    set bit 0x80 of the watchdog word when they run out."""
+    return lib().mxq_debug_set_w4_wait(int(ns))
 
 
 def mxq_watchdog_selftest(limit_ns=1_000_000, stream=None):

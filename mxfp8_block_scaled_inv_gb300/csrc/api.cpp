@@ -810,6 +810,8 @@ int mxq_debug_set_lazy_pairs(int from) {
   return prev >= (1 << 30) ? -1 : prev;
 }
 
+uint32_t mxq_debug_set_w4_wait(uint32_t ns) { return mxq::set_w4_wait(ns); }
+
 uint32_t mxq_debug_set_attn_wait(uint32_t ns) { return mxq::set_attn_wait(ns); }
 
 int mxq_debug_takeovers(uint32_t* host_value, int clear) {

@@ -160,6 +160,10 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
                                 int64_t T, int k, int E, int K, int I, int N, int32_t* err_flag,
                                 void* ws, int num_sms, cudaStream_t s, const char** why);
 
+// Bounds the waits of the 4-bit products (0: the default, two seconds, which is
+// also the most); returns the previous bound.
+uint32_t set_w4_wait(uint32_t ns);
+
 // Caps the CTA pairs of the pair-form GEMM launches (0 = no cap); returns
 // the previous cap.
 int set_pair_limit(int pairs);

@@ -66,7 +66,9 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // bmm.cu
 
 namespace {
 
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint32_t kWaitNs = 2000000000u;  // default and longest bound on a wait
+constexpr uint64_t kDrainNs = 2000000000ull;  // on what ends by itself once issuing has stopped
+std::atomic<uint32_t> g_wait_ns{kWaitNs};  // see mxq_debug_set_w4_wait
 constexpr uint32_t kHintNs = 20;
 constexpr uint32_t kWdW4 = 0x80;  // a wait of these kernels ran out
 
@@ -98,6 +100,7 @@ struct W4Args {
   void* out;              // kLinear: BF16 [T][N]; kGateUp: codes [rows][N]; kDown: int16 [rows][N]
   uint8_t* out_sf;        // kGateUp: [rows][NG]; kDown: exponents [N / 32][NG rows]
   uint32_t* wd;           // watchdog word
+  uint32_t wait_ns;       // bound on a wait
   int T, N, KG, KB, NB, NG, k;
   int per_tile, n_tiles_host;  // kLinear: tokens of a tile, tiles
   int splits, kb_per_split;
@@ -500,7 +503,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
   // A wait of a whole warp; false once it or another role has given up.
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (__all_sync(0xffffffffu,
-                   !*abort_flag && ptx::mbar_wait_hint(bar, parity, kWaitNs, kHintNs)))
+                   !*abort_flag && ptx::mbar_wait_hint(bar, parity, p.wait_ns, kHintNs)))
       return true;
     if (lane == 0 && !*abort_flag) atomicOr(p.wd, kWdW4);
     *abort_flag = 1;
@@ -775,11 +778,11 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
     // MMAs and copies in flight end before TMEM and shared memory are given up:
     // raise each issued stage's missing arrivals, then wait for its phase.
     if (threadIdx.x == 32) {
-      ptx::mbar_wait(done, 0, kWaitNs);
+      ptx::mbar_wait(done, 0, kDrainNs);
       const int i0 = issued[0], i2 = issued[1], last = max(i0, i2);
       for (int i = min(i0, i2); i < last; ++i) ptx::mbar_arrive(&full[i % NSTAGE]);
       for (int i = max(0, last - NSTAGE); i < last; ++i)
-        ptx::mbar_wait(&full[i % NSTAGE], (uint32_t)(i / NSTAGE) & 1u, kWaitNs);
+        ptx::mbar_wait(&full[i % NSTAGE], (uint32_t)(i / NSTAGE) & 1u, kDrainNs);
     }
     __syncthreads();
   }
@@ -909,7 +912,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (__all_sync(0xffffffffu,
-                   !*abort_flag && ptx::mbar_wait_hint(bar, parity, kWaitNs, kHintNs)))
+                   !*abort_flag && ptx::mbar_wait_hint(bar, parity, p.wait_ns, kHintNs)))
       return true;
     if (lane == 0 && !*abort_flag) atomicOr(p.wd, kWdW4);
     *abort_flag = 1;
@@ -1090,7 +1093,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
     // What the even CTA issued completes; copies still in flight, the other CTA's
     // too, land within this millisecond (they take a few microseconds).
     if (threadIdx.x == 0) {
-      if (rank == 0) ptx::mbar_wait(done, 0, kWaitNs);
+      if (rank == 0) ptx::mbar_wait(done, 0, kDrainNs);
       const uint64_t t0 = ptx::globaltimer();
       while (ptx::globaltimer() - t0 < 1000000ull) __nanosleep(1000);
     }
@@ -1490,6 +1493,10 @@ int pick_splits(int64_t units, int KB, int slots) {
 
 }  // namespace
 
+uint32_t set_w4_wait(uint32_t ns) {
+  return g_wait_ns.exchange(ns == 0 || ns > kWaitNs ? kWaitNs : ns);
+}
+
 cudaError_t launch_prepare_w4(const uint8_t* w, const uint8_t* sf, int64_t B, int N, int K,
                               uint8_t* out, cudaStream_t s) {
   const int NB = (int)ceil_div(N, 128), KB = (int)ceil_div(K, kGroup);
@@ -1503,6 +1510,7 @@ cudaError_t launch_linear_a8w4(const uint8_t* a, const uint8_t* a_sf, const uint
                                int64_t T, int N, int K, int num_sms, cudaStream_t s,
                                const char** why) {
   W4Args g = {};
+  g.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
   g.w = w;
   g.a_sf = a_sf;
   g.out = out;
@@ -1594,6 +1602,7 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   W4Args g = {};
+  g.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
   cudaError_t e = watchdog_address(&g.wd);
   if (e != cudaSuccess) return e;
   const bool small = small_call(R, k);
