@@ -255,13 +255,20 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 // A result between the down product and the weighted sum over a token's experts
 // is held in 16 bits, as an integer with one exponent for 32 columns: the step is
 // 2^-13 to 2^-14 of the largest of the 32, which a sum rounded to BF16 does not
-// see, and half the bytes of FP32 to write and read again.  m: exponent field of
-// the largest magnitude, which is below 2^(m - 126); the value is the integer
-// times 2^(m - 140).  With an infinity or a NaN among the 32 they are BF16 values.
+// see, and half the bytes of FP32 to write and read again.  m: the exponent bits of
+// the largest magnitude, which is below 2^(e - 126) for their field e; the value is
+// the integer times 2^(e - 140).  With an infinity or a NaN among the 32 they are BF16
+// values.
+constexpr uint32_t kExpMask = 0x7F800000u;
+__device__ __forceinline__ uint32_t held16_finite(float y, uint32_t m) {
+  const float inv = __uint_as_float(0x85800000u - max(m, kLeastExp << 23));  // 2^(140 - e)
+  return __float_as_uint(fmaf(y, inv, 12582912.0f));  // the integer + 1.5 * 2^23
+}
 __device__ __forceinline__ uint32_t held16(float y, uint32_t m) {
-  const float inv = __uint_as_float((267u - max(m, kLeastExp)) << 23);  // 2^(140 - m)
-  const uint32_t bits = __float_as_uint(fmaf(y, inv, 12582912.0f));     // the integer + 1.5 * 2^23
-  return m == 255u ? pack2(y, 0.0f) : bits;
+  return m == kExpMask ? pack2(y, 0.0f) : held16_finite(y, m);
+}
+__device__ __forceinline__ uint8_t held16_exp(uint32_t m) {
+  return (uint8_t)max(m >> 23, kLeastExp);
 }
 
 // What four warps do with 16 tokens: v[a][i] is token i's sum for weight row
@@ -312,21 +319,28 @@ __device__ __forceinline__ void finish_chunk(const W4Args& p, float (&v)[NA][kCh
       if (in && i + 1 < live) o[(size_t)(i + 1) * p.N] = (uint8_t)(c >> 8);
     }
   } else {
+    // (Instructions are what this one is short of: 11 for each value now, 24 with a
+    // predicate, a shift and a choice of the non-finite form for each.)
     uint16_t* o = static_cast<uint16_t*>(p.out) + (size_t)row * p.N + n;
-    uint32_t m[kChunk], mine = 0u;
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i)
-      m[i] = __reduce_max_sync(0xffffffffu, __float_as_uint(v[0][i]) & 0x7FFFFFFFu) >> 23;
+    uint32_t m[kChunk], mine = 0u, top = 0u;
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) {
-      const uint32_t bits = held16(v[0][i], m[i]);
+      m[i] = __reduce_max_sync(0xffffffffu, __float_as_uint(v[0][i]) & kExpMask);
+      top = max(top, m[i]);
       if (lane == i) mine = m[i];
-      if (in && i < live) o[(size_t)i * p.N] = (uint16_t)bits;
+    }
+    if (top != kExpMask && live >= kChunk && rb * 128 + 128 <= p.N) {
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) o[(size_t)i * p.N] = (uint16_t)held16_finite(v[0][i], m[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i)
+        if (in && i < live) o[(size_t)i * p.N] = (uint16_t)held16(v[0][i], m[i]);
     }
     // (By column block first: a row's bytes of all blocks lie far apart, and single
     // bytes to lines that nobody else writes cost as much as all the rest.)
     if (lane < min(live, kChunk) && rb * 128 + q * 32 < p.N)
-      p.out_sf[(size_t)(rb * 4 + q) * p.NG + row + lane] = (uint8_t)max(mine, kLeastExp);
+      p.out_sf[(size_t)(rb * 4 + q) * p.NG + row + lane] = held16_exp(mine);
   }
 }
 
@@ -355,10 +369,9 @@ __device__ __forceinline__ void finish_token(const W4Args& p, const float (&v)[N
   } else {
     uint32_t m = 0u;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[0][e]) & 0x7FFFFFFFu);
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[0][e]) & kExpMask);
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    m >>= 23;
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -366,7 +379,7 @@ __device__ __forceinline__ void finish_token(const W4Args& p, const float (&v)[N
     if (store) {
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (size_t)row * p.N + n) =
           make_uint4(w[0], w[1], w[2], w[3]);
-      if ((sub & 3) == 0) p.out_sf[(size_t)(n >> 5) * p.NG + row] = (uint8_t)max(m, kLeastExp);
+      if ((sub & 3) == 0) p.out_sf[(size_t)(n >> 5) * p.NG + row] = held16_exp(m);
     }
   }
 }
