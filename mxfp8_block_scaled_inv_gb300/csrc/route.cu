@@ -43,7 +43,7 @@ struct RouteArgs {
   int32_t* ids;
   float* weights;
   int64_t T;
-  int E, k, scoring, groups, keep, group_top, renorm, per_group, vec, lanes;
+  int E, k, scoring, groups, keep, group_top, renorm, per_group, vec, bias_vec, lanes;
   float scale;
 };
 
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER == 16 ? 6 : 4)
     for (int i = 0; i < PER; ++i) l[i] = e0 + i < a.E ? load_logit(a, t, e0 + i, BF16) : -INFINITY;
   }
   float b[PER];
-  if (biased && PER >= 4 && a.vec && e0 + PER <= a.E) {
+  if (biased && PER >= 4 && a.bias_vec && e0 + PER <= a.E) {
 #pragma unroll
     for (int i = 0; i + 4 <= PER; i += 4) {
       const float4 v = __ldg(reinterpret_cast<const float4*>(a.bias + e0 + i));
@@ -595,8 +595,10 @@ cudaError_t launch_route(const void* logits, bool bf16, int64_t T, int E, const 
   a.renorm = renorm;
   a.per_group = E / groups;
   a.scale = scale;
-  // 16-byte loads of a lane's logits; groups of whole lanes, a power of two of them.
+  // 16-byte loads of a lane's logits and biases (a bias may begin at any element);
+  // groups of whole lanes, a power of two of them.
   a.vec = E % 8 == 0;
+  a.bias_vec = a.vec && (reinterpret_cast<uintptr_t>(bias) & 15u) == 0;
   int per = 1;
   while (per * 32 < E) per *= 2;
   const int lanes = a.per_group % per == 0 ? a.per_group / per : 0;

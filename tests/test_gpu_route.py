@@ -150,3 +150,14 @@ def test_many_tokens(mxq):
     wp = p.gather(1, want)
     wp = wp / wp.sum(1, keepdim=True)
     assert bool(((w.double() - wp).abs() <= 2.0 ** -18 * wp).all())
+
+
+@pytest.mark.parametrize("E", [128, 256, 512, 1024])
+def test_bias_that_begins_at_any_element(mxq, E):
+    l, b = draw(6, E, seed=E)
+    want = mxq.mxq_route(l, 5, scoring="sigmoid", bias=b, groups=8, topk_groups=3)
+    for at in (1, 2, 3):
+        room = torch.full((E + 8,), float("nan"), device="cuda")
+        room[at:at + E] = b
+        got = mxq.mxq_route(l, 5, scoring="sigmoid", bias=room[at:at + E], groups=8, topk_groups=3)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
