@@ -502,7 +502,8 @@ int mxq_prepare_w4(const uint8_t* w_e2m1, const uint8_t* w_e8m0, int32_t B, int3
  * A = E4M3(code) * 2^(byte-127), W = E2M1(code) * 2^(byte-127); products are
  * exact and summed in FP32 on the tensor cores.
  * N % 16 == 0, N >= 16, K % 32 == 0, 32 <= K <= 65536.  T == 0 is a no-op.
- * T >= 2^31 or N*K >= 2^37 returns MXQ_ERR_UNSUPPORTED.
+ * T >= 2^31, T*N of about 2^39 and more, or a weight of more than 2^31 rows of
+ * 64 bytes returns MXQ_ERR_UNSUPPORTED.
  */
 int mxq_linear_a8w4(const uint8_t* a_e4m3, const uint8_t* a_e8m0, const uint8_t* w4, void* out_bf16,
                     int64_t T, int32_t N, int32_t K, mxq_stream_t stream);
@@ -529,7 +530,7 @@ size_t mxq_experts_workspace_bytes(int64_t T, int32_t k, int32_t E, int32_t K, i
  *                  held to 2^-14 of the largest of its 32 neighbouring columns
  *                  at worst.  A token without experts gets zeros.  Must not
  *                  overlap an input or the workspace.
- *  err_flag        optional int32 device word.
+ *  err_flag        optional int32 device word, in no other buffer.
  *  ws              mxq_experts_workspace_bytes() bytes, 16-byte aligned; calls
  *                  that may run at the same time need distinct workspaces.
  * Results do not depend on timing: atomics only choose where a row's sums are

@@ -596,6 +596,13 @@ def _on(fn, name, t, dtype, shape, dev):
                           f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', strided'}")
 
 
+def _int32(fn, *sizes):
+    """Refuses sizes that the library's 32-bit arguments do not hold (ctypes would cut them off)."""
+    for v in sizes:
+        if not -0x80000000 <= v <= 0x7fffffff:
+            raise MxqError(fn, 4, f"a size of {v} does not fit 32 bits")
+
+
 def _stream_on(stream, dev):
     if stream is not None:
         return stream.cuda_stream
@@ -628,6 +635,7 @@ def mxq_add_rms_norm(x, weight=None, eps=1e-6, residual=None, residual_out=None,
     if not shape:
         raise MxqError(fn, 2, "x has no dimension")
     D = shape[-1]
+    _int32(fn, D)
     T = x.numel() // D if D else 0
     px = _on(fn, "x", x, torch.bfloat16, shape, dev)
     pw = None if weight is None else _on(fn, "weight", weight, torch.bfloat16, (D,), dev)
@@ -680,6 +688,7 @@ def mxq_route(logits, k, scoring="softmax", bias=None, groups=1, topk_groups=1, 
     fn = "mxq_route"
     dev = _device_of(fn, logits)
     T, E = shape = logits.shape
+    _int32(fn, E, k, groups, topk_groups, group_top)
     dtype = MXQ_LOGITS_BF16 if logits.dtype is torch.bfloat16 else MXQ_LOGITS_F32
     pl = _on(fn, "logits", logits, torch.bfloat16 if dtype else torch.float32, shape, dev)
     score = MXQ_SCORES.get(scoring)
@@ -707,6 +716,7 @@ def mxq_route(logits, k, scoring="softmax", bias=None, groups=1, topk_groups=1, 
 
 def mxq_w4_bytes(B, N, K):
     """Bytes of B prepared 4-bit weights [N, K] (0 for invalid sizes)."""
+    _int32("mxq_w4_bytes", B, N, K)
     return lib().mxq_w4_bytes(B, N, K)
 
 
@@ -719,6 +729,7 @@ def mxq_prepare_w4(w, w_e8m0, out=None, stream=None):
         raise MxqError(fn, 2, f"w has shape {tuple(w.shape)}, not [B, N, K/2] or [N, K/2]")
     *lead, N, half = w.shape
     B, K = (lead[0] if lead else 1), 2 * half
+    _int32(fn, B, N, K)
     pw = _on(fn, "w", w, torch.uint8, w.shape, dev)
     ps = _on(fn, "w_e8m0", w_e8m0, torch.uint8, (*lead, N, K // 32), dev)
     need = mxq_w4_bytes(B, N, K)
@@ -744,6 +755,7 @@ def mxq_linear_a8w4(a, a_sf, w4, N, out=None, stream=None):
     fn = "mxq_linear_a8w4"
     dev = _device_of(fn, a)
     T, K = shape = a.shape
+    _int32(fn, N, K)
     L = lib()
     pa = _on(fn, "a", a, torch.uint8, shape, dev)
     ps = _on(fn, "a_sf", a_sf, torch.uint8, (T, (K + 127) // 128), dev)
@@ -761,6 +773,7 @@ def mxq_linear_a8w4(a, a_sf, w4, N, out=None, stream=None):
 
 def mxq_experts_workspace_bytes(T, k, E, K, I, N):
     """Workspace bytes of mxq_experts_a8w4 (0 for invalid sizes)."""
+    _int32("mxq_experts_workspace_bytes", k, E, K, I, N)
     return lib().mxq_experts_workspace_bytes(T, k, E, K, I, N)
 
 
@@ -780,6 +793,7 @@ def mxq_experts_a8w4(a, a_sf, ids, weights, w13, w2, I, N=None, out=None, ws=Non
     k = ids.shape[-1]
     if N is None:
         N = K
+    _int32(fn, k, K, I, N)
     L = lib()
     one13, one2 = L.mxq_w4_bytes(2, I, K), L.mxq_w4_bytes(1, N, I)
     if not one13 or not one2:

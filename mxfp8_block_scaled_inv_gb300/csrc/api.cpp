@@ -717,8 +717,8 @@ int mxq_linear_a8w4(const uint8_t* a_e4m3, const uint8_t* a_e8m0, const uint8_t*
   if (T < 0 || N < 16 || K < 32 || N % 16 != 0 || K % 32 != 0)
     return fail(MXQ_ERR_SHAPE, "need T >= 0, N >= 16, K >= 32, N %% 16 == 0, K %% 32 == 0 (T=%lld "
                                "N=%d K=%d)", (long long)T, N, K);
-  if (K > 65536 || T >= ((int64_t)1 << 31) || (int64_t)N * K >= ((int64_t)1 << 37))
-    return fail(MXQ_ERR_UNSUPPORTED, "need K <= 65536, T < 2^31, N*K < 2^37");
+  if (K > 65536 || T >= ((int64_t)1 << 31) || !w4_fits(1, N, K))
+    return fail(MXQ_ERR_UNSUPPORTED, "need K <= 65536, T < 2^31 and fewer than 2^31 rows of 64 bytes of weight");
   if ((T / 16 + 1) * (N / 128 + 1) >= ((int64_t)1 << 28))
     return fail(MXQ_ERR_UNSUPPORTED, "T*N is too large");
   if (T == 0) return ok();
@@ -750,7 +750,8 @@ static int validate_experts_sizes(int64_t T, int32_t k, int32_t E, int32_t K, in
   // T alone first, so that the product stays in 64 bits.
   if (T >= ((int64_t)1 << 24) || T * k >= ((int64_t)1 << 24))
     return fail(MXQ_ERR_UNSUPPORTED, "T*k must be < 2^24");
-  if (!w4_fits(E, N, I) || !w4_fits(2 * (int64_t)E, I, K) || (T * k / 16 + E) * ((int64_t)(N > I ? N : I) / 128 + 1) >= ((int64_t)1 << 28) ||
+  if (!w4_fits(E, N, I) || !w4_fits(2 * (int64_t)E, I, K) ||
+      (T * k / 16 + E) * ((int64_t)(N > I ? N : I) / 128 + 1) >= ((int64_t)1 << 28) ||
       T * (N / 8) >= ((int64_t)1 << 32) - 256)
     return fail(MXQ_ERR_UNSUPPORTED, "the weights or T*k*N are too large");
   return MXQ_OK;
@@ -790,6 +791,8 @@ int mxq_experts_a8w4(const uint8_t* a_e4m3, const uint8_t* a_e8m0, const int32_t
              {w2, (size_t)mxq::w4_blocks(E, N, I) * mxq::kW4BlockBytes}};
   const size_t out = (size_t)T * N * 2;
   if (overlap(out_bf16, out, ws, need)) return fail(MXQ_ERR_SHAPE, "out overlaps the workspace");
+  if (err_flag && (overlap(err_flag, 4, ws, need) || overlap(err_flag, 4, out_bf16, out)))
+    return fail(MXQ_ERR_SHAPE, "err_flag lies in out or the workspace");
   for (const auto& b : in)
     if (overlap(out_bf16, out, b.p, b.bytes) || overlap(ws, need, b.p, b.bytes))
       return fail(MXQ_ERR_SHAPE, "out or the workspace overlaps an input");

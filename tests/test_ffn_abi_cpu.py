@@ -152,6 +152,13 @@ def test_experts_argument_errors(L):
     assert experts(L, T=0, a=None, out=None, ws=None) == 0
 
 
+def test_error_words_in_other_buffers_and_weights_past_the_coordinates(L):
+    """An error word in the workspace or the output; 2^24 blocks of a tall and narrow weight."""
+    for err in (8 << 36, (8 << 36) + 512, C, C + 2 * 4 * 1024 - 4):
+        assert experts(L, err=err) == 2, err
+    assert linear(L, N=(1 << 31) - 16, K=32, T=1) == 4 and prepare(L, B=1, N=(1 << 31) - 16, K=32) == 4
+
+
 def test_experts_workspace(L):
     f = L.mxq_experts_workspace_bytes
     good = (4, 8, 16, 576, 288, 1024)

@@ -141,6 +141,22 @@ def test_other_refusals(lib):
     assert not lib.calls
 
 
+def test_sizes_beyond_32_bits(lib):
+    """Sizes that 32-bit arguments would cut down to good ones."""
+    over = 1 << 32
+    for call, bad in ((norm, dict(x=Dev((4, over + 256), B16))), (route, dict(k=over + 6)), (route, dict(groups=over + 1)),
+                      (route, dict(logits=Dev((4, over + 64), F32))), (linear, dict(N=over + 128)),
+                      (experts, dict(I=over + 96)), (experts, dict(N=over + 288)),
+                      (prepare, dict(w=Dev((over + 2, 128, 64), U8)))):
+        with pytest.raises(mxq.MxqError, match="32 bits"):
+            call(**bad)
+    with pytest.raises(mxq.MxqError):
+        mxq.mxq_w4_bytes(1, over + 16, 32)
+    with pytest.raises(mxq.MxqError):
+        mxq.mxq_experts_workspace_bytes(1, 1, 1, 32, over + 32, 16)
+    assert not lib.calls
+
+
 def test_the_current_device_is_another(lib, monkeypatch):
     monkeypatch.setattr(mxq, "_current_device", lambda: 1)
     for call in CALLS:
