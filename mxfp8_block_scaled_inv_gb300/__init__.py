@@ -548,7 +548,7 @@ def mxq_attn(q, cache, block_table, seq_lens, q_start=None, page_size=64, window
     return out
 
 
-_fast = None  # mxq_fastcall, once loaded; False where it was not built
+_fast = None  # mxq_fastcall, once loaded; False where there is none for this torch
 
 
 def _fastcall():
@@ -557,7 +557,7 @@ def _fastcall():
     global _fast
     if _fast is None:
         _fast = False
-        path = os.path.join(HERE, "mxq_fastcall.so")
+        path = os.path.join(HERE, f"mxq_fastcall-{torch.__version__}{importlib.machinery.EXTENSION_SUFFIXES[0]}")
         if os.path.exists(path):
             L = lib()
             loader = importlib.machinery.ExtensionFileLoader("mxq_fastcall", path)

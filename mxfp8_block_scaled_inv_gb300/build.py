@@ -3,8 +3,9 @@
 Each CUDA translation unit is compiled by nvcc in parallel with
 ``-gencode arch=compute_103a,code=sm_103a``, the C-ABI layer by the host
 compiler, and the objects are linked into ``libmxq.so`` next to this file.
-``mxq_fastcall.so``, the binding's quick way into it for common calls, is built
-beside it against the installed torch; without it (no torch or Python headers)
+``mxq_fastcall``, the binding's quick way into it for common calls, is built beside
+it against the installed torch, and named after torch's and Python's versions;
+where there is none for them (no torch or Python headers, another torch since)
 the binding makes those calls through ctypes like all others.
 A build is skipped when the library is newer than every source and header.
 """
@@ -12,10 +13,12 @@ A build is skipped when the library is newer than every source and header.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.machinery
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -28,7 +31,11 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CU_SOURCES = ["quant.cu", "misc.cu", "bmm.cu", "linear_noalloc.cu", "kv_insert.cu", "kv4.cu",
               "attn.cu", "norm.cu", "route.cu", "w4.cu"]
 CXX_SOURCES = ["api.cpp"]
-FASTCALL_PATH = os.path.join(HERE, "mxq_fastcall.so")
+
+
+def fastcall_path(torch_version) -> str:
+    """Where the quick way in for this torch and this Python lies."""
+    return os.path.join(HERE, f"mxq_fastcall-{torch_version}{importlib.machinery.EXTENSION_SUFFIXES[0]}")
 
 
 def cuda_home() -> str:
@@ -65,13 +72,13 @@ def _run(cmd, verbose):
 
 
 def _build_fastcall(cxx, inc, verbose) -> None:
-    """Compile mxq_fastcall.so; a failure leaves it out, with a message."""
-    tmp = FASTCALL_PATH + ".tmp"
+    """Compile mxq_fastcall; a failure leaves it out, with a message."""
+    path = None
     try:
-        import sysconfig
-
         import torch
 
+        path = fastcall_path(torch.__version__)
+        tmp = path + ".tmp"
         at = os.path.dirname(torch.__file__)
         _run([cxx, "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared",
               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
@@ -80,11 +87,11 @@ def _build_fastcall(cxx, inc, verbose) -> None:
               "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "fastcall.cpp"), "-o", tmp,
               "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], verbose)
     except (ImportError, RuntimeError) as e:
-        print(f"mxq_fastcall.so not built: {e}", file=sys.stderr, flush=True)
-        if os.path.exists(FASTCALL_PATH):
-            os.remove(FASTCALL_PATH)
+        print(f"mxq_fastcall not built: {e}", file=sys.stderr, flush=True)
+        if path is not None and os.path.exists(path):
+            os.remove(path)
         return
-    os.replace(tmp, FASTCALL_PATH)
+    os.replace(tmp, path)
 
 
 def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False) -> str:

@@ -83,6 +83,20 @@ void* current_stream(int device) {
   return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
 }
 
+void* address(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+uint8_t* bytes(const at::Tensor& t) { return static_cast<uint8_t*>(address(t)); }
+
+// An entry point without the interpreter's lock.  Its arguments are values by then:
+// what can throw has been evaluated under the lock.
+template <typename F, typename... A>
+int call(F f, A... args) {
+  int st;
+  Py_BEGIN_ALLOW_THREADS
+  st = f(args...);
+  Py_END_ALLOW_THREADS
+  return st;
+}
+
 // norm(x, weight, eps, residual, want_y, want_codes) -> (s, y, q, sc)
 PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -107,14 +121,9 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     shape.back() = (D + 127) / 128;
     sc = empty(shape, at::kByte, *x);
   }
-  auto at_ = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
-  int st;
-  Py_BEGIN_ALLOW_THREADS
-  st = lib.norm(x->data_ptr(), r ? r->data_ptr() : nullptr, at_(s), w ? w->data_ptr() : nullptr, T,
-                (int32_t)D, eps, at_(y), static_cast<uint8_t*>(at_(q)), static_cast<uint8_t*>(at_(sc)),
-                current_stream(dev));
-  Py_END_ALLOW_THREADS
-  if (st) Py_RETURN_NONE;
+  if (call(lib.norm, address(*x), r ? address(*r) : nullptr, address(s), w ? address(*w) : nullptr, T,
+           (int32_t)D, eps, address(y), bytes(q), bytes(sc), current_stream(dev)))
+    Py_RETURN_NONE;
   PyObject* out = PyTuple_New(4);
   if (!out) return nullptr;
   const at::Tensor* all[4] = {&s, &y, &q, &sc};
@@ -153,13 +162,10 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor* b = nullptr;
   if (a[3] != Py_None && (!(b = tensor(a[3], at::kFloat, dev)) || !has_shape(*b, {E}))) Py_RETURN_NONE;
   at::Tensor ids = empty({T, k}, at::kInt, *l), w = empty({T, k}, at::kFloat, *l);
-  int st;
-  Py_BEGIN_ALLOW_THREADS
-  st = lib.route(l->data_ptr(), dtype, T, (int32_t)E, b ? b->data_ptr<float>() : nullptr, k, scoring,
-                 groups, keep, top, a[7] == Py_True, scale, ids.data_ptr<int32_t>(),
-                 w.data_ptr<float>(), current_stream(dev));
-  Py_END_ALLOW_THREADS
-  if (st) Py_RETURN_NONE;
+  if (call(lib.route, address(*l), dtype, T, (int32_t)E, b ? b->data_ptr<float>() : nullptr, k, scoring,
+           groups, keep, top, (int32_t)(a[7] == Py_True), scale, ids.data_ptr<int32_t>(),
+           w.data_ptr<float>(), current_stream(dev)))
+    Py_RETURN_NONE;
   return Py_BuildValue("(NN)", THPVariable_Wrap(ids), THPVariable_Wrap(w));
   END_HANDLE_TH_ERRORS
 }
@@ -175,15 +181,11 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int32_t N;
   if (!x || !s || !w || x->dim() != 2 || !small_number(a[3], &N) || x->size(1) > 65536) Py_RETURN_NONE;
   const int64_t T = x->size(0), K = x->size(1);
-  const size_t bytes = lib.w4_bytes(1, N, (int32_t)K);
-  if (!bytes || !has_shape(*s, {T, (K + 127) / 128}) || !has_shape(*w, {(int64_t)bytes})) Py_RETURN_NONE;
+  const size_t size = lib.w4_bytes(1, N, (int32_t)K);
+  if (!size || !has_shape(*s, {T, (K + 127) / 128}) || !has_shape(*w, {(int64_t)size})) Py_RETURN_NONE;
   at::Tensor out = empty({T, N}, at::kBFloat16, *x);
-  int st;
-  Py_BEGIN_ALLOW_THREADS
-  st = lib.linear(x->data_ptr<uint8_t>(), s->data_ptr<uint8_t>(), w->data_ptr<uint8_t>(), out.data_ptr(),
-                  T, N, (int32_t)K, current_stream(dev));
-  Py_END_ALLOW_THREADS
-  if (st) Py_RETURN_NONE;
+  if (call(lib.linear, bytes(*x), bytes(*s), bytes(*w), address(out), T, N, (int32_t)K, current_stream(dev)))
+    Py_RETURN_NONE;
   return THPVariable_Wrap(out);
   END_HANDLE_TH_ERRORS
 }
@@ -209,17 +211,13 @@ PyObject* experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !has_shape(*wt, {T, k}) || !has_shape(*w13, {E * (int64_t)one13}) ||
       !has_shape(*w2, {E * (int64_t)one2}))
     Py_RETURN_NONE;
-  const size_t bytes = lib.experts_ws(T, (int32_t)k, (int32_t)E, (int32_t)K, I, N);
-  if (!bytes) Py_RETURN_NONE;
-  at::Tensor out = empty({T, N}, at::kBFloat16, *x), ws = empty({(int64_t)bytes}, at::kByte, *x);
-  int st;
-  Py_BEGIN_ALLOW_THREADS
-  st = lib.experts(x->data_ptr<uint8_t>(), s->data_ptr<uint8_t>(), ids->data_ptr<int32_t>(),
-                   wt->data_ptr<float>(), w13->data_ptr<uint8_t>(), w2->data_ptr<uint8_t>(), out.data_ptr(),
-                   T, (int32_t)k, (int32_t)E, (int32_t)K, I, N, nullptr, ws.data_ptr(), bytes,
-                   current_stream(dev));
-  Py_END_ALLOW_THREADS
-  if (st) Py_RETURN_NONE;
+  const size_t need = lib.experts_ws(T, (int32_t)k, (int32_t)E, (int32_t)K, I, N);
+  if (!need) Py_RETURN_NONE;
+  at::Tensor out = empty({T, N}, at::kBFloat16, *x), ws = empty({(int64_t)need}, at::kByte, *x);
+  if (call(lib.experts, bytes(*x), bytes(*s), ids->data_ptr<int32_t>(), wt->data_ptr<float>(), bytes(*w13),
+           bytes(*w2), address(out), T, (int32_t)k, (int32_t)E, (int32_t)K, I, N, nullptr, address(ws), need,
+           current_stream(dev)))
+    Py_RETURN_NONE;
   return THPVariable_Wrap(out);
   END_HANDLE_TH_ERRORS
 }

@@ -207,12 +207,23 @@ def test_allocations_belong_to_the_stream(lib, monkeypatch, call, n):
     assert rec.allocs == ["current"] * n
 
 
+def test_the_quick_way_is_that_of_this_torch(monkeypatch, tmp_path):
+    """A module built against another torch is not loaded; the calls then go through ctypes."""
+    from importlib.machinery import EXTENSION_SUFFIXES
+
+    (tmp_path / f"mxq_fastcall-0.0{EXTENSION_SUFFIXES[0]}").write_bytes(b"not to be loaded")
+    monkeypatch.setattr(mxq, "HERE", str(tmp_path))
+    monkeypatch.setattr(mxq, "_fast", None)
+    assert mxq._fastcall() is False
+    assert build.fastcall_path(torch.__version__).endswith(f"mxq_fastcall-{torch.__version__}{EXTENSION_SUFFIXES[0]}")
+
+
 def test_the_quick_way_leaves_the_rest():
     """On the CPU nothing is the common case: each function answers None, and the errors are the Python code's."""
     build.build()
     f = mxq._fastcall()
     if not f:
-        pytest.skip("mxq_fastcall.so was not built")
+        pytest.skip("mxq_fastcall was not built")
     x, u = torch.zeros((4, 256), dtype=B16), torch.zeros((4, 256), dtype=U8)
     for call in (lambda: f.norm(x, None, 1e-6, None, True, True), lambda: f.norm(None, None, 1e-6, None, True, True),
                  lambda: f.norm(Dev((4, 256), B16), None, 1e-6, None, True, True), lambda: f.norm(x),
