@@ -411,7 +411,6 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
   // it are the same in all lanes, and keeps the operands of copies and MMAs in
   // uniform registers instead of moving them there each time.)
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  ptx::griddep_launch_dependents();
 
   const int split = SPLIT ? (int)ptx::cluster_rank() : 0;
   constexpr bool BY_CHOICE = SMALL && MODE == kDown;  // a cluster's CTAs are a token's choices
@@ -419,18 +418,43 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
   const int kb0 = SPLIT && !BY_CHOICE ? split * p.kb_per_split : 0;
   int nk = SPLIT && !BY_CHOICE ? max(0, min(p.KB - kb0, p.kb_per_split)) : p.KB;
   const int u_first = SPLIT ? (int)(blockIdx.x / (uint32_t)p.splits) : (int)blockIdx.x;
+  // The weight does not depend on what runs before: bring the first blocks into L2
+  // while that finishes.  (Everything up to the wait runs beside it.)
+  if (MODE == kLinear && warp == 3 && lane < NSTAGE && lane < nk)
+    ptx::prefetch_l2_bulk(p.w + ((size_t)(u_first % p.NB) * p.KB + kb0 + lane) * kBlockBytes, kBlockBytes);
+  if (threadIdx.x == 0) {
+    ptx::prefetch_tmap(&tm_w);
+    ptx::prefetch_tmap(&tm_a);
+    for (int i = 0; i < NSTAGE; ++i) {
+      ptx::mbar_init(&full[i], 2);
+      ptx::mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&acc_full[i], 1);
+      ptx::mbar_init(&acc_empty[i], 4 * C::GROUPS);
+    }
+    ptx::mbar_init(done, 1);
+    ptx::fence_barrier_init();
+    *abort_flag = 0;
+    issued[0] = issued[1] = 0;
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(slot, C::TMEM_COLS);
+    ptx::tmem_relinquish();
+    ptx::tc_fence_before();
+  }
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);
+  // Only now, with its TMEM in hand, may the next kernel begin: its CTAs may sit
+  // beside this one and take theirs before they wait for this grid to end.
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
   int units;
   Pairs pairs;
   if constexpr (MODE == kLinear) {
     units = p.n_tiles_host * p.NB;
-    // The weight does not depend on what runs before: bring the first blocks
-    // into L2 while that finishes.
-    if (warp == 0 && lane < NSTAGE && lane < nk && u_first < units)
-      ptx::prefetch_l2_bulk(p.w + ((size_t)(u_first % p.NB) * p.KB + kb0 + lane) * kBlockBytes,
-                            kBlockBytes);
-    ptx::griddep_wait();
   } else if constexpr (SMALL) {
-    ptx::griddep_wait();
     pairs.load(p, lane);
     if constexpr (BY_CHOICE) {
       units = p.T * p.NB;
@@ -442,12 +466,14 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
         atomicOr(p.err_flag, MXQ_DEVERR_EXPERT);
     }
   } else {
-    ptx::griddep_wait();
     units = *p.n_tiles * p.NB;
   }
   // The grid covers the most units that there can be; a CTA (the whole cluster
   // alike) without any leaves.
-  if (u_first >= units) return;
+  if (u_first >= units) {
+    if (warp == 1) ptx::tmem_dealloc(tmem, C::TMEM_COLS);
+    return;
+  }
   const int u_step = SPLIT ? units : (int)gridDim.x;  // split: one unit
 
   auto tile_of = [&](int u) {
@@ -487,30 +513,6 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
     else return (int)p.perm[t.row0 + i];
   };
 
-  if (threadIdx.x == 0) {
-    ptx::prefetch_tmap(&tm_w);
-    ptx::prefetch_tmap(&tm_a);
-    for (int i = 0; i < NSTAGE; ++i) {
-      ptx::mbar_init(&full[i], 2);
-      ptx::mbar_init(&empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&acc_full[i], 1);
-      ptx::mbar_init(&acc_empty[i], 4 * C::GROUPS);
-    }
-    ptx::mbar_init(done, 1);
-    ptx::fence_barrier_init();
-    *abort_flag = 0;
-    issued[0] = issued[1] = 0;
-  }
-  if (warp == 1) {
-    ptx::tmem_alloc(slot, C::TMEM_COLS);
-    ptx::tmem_relinquish();
-    ptx::tc_fence_before();
-  }
-  __syncthreads();
-  ptx::tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);
   if constexpr (SPLIT) ptx::cluster_arrive();  // this CTA's shared memory may be written
 
   // A wait of a whole warp; false once it or another role has given up.
@@ -862,39 +864,13 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = (int)ptx::cluster_rank();
-  ptx::griddep_launch_dependents();
 
   const int nk = p.KB, NBP = (p.NB + 1) / 2;
   const int u_first = (int)(blockIdx.x >> 1), u_step = (int)(gridDim.x >> 1);
   auto block_of = [&](int u) { return 2 * (u % NBP) + rank; };  // may be NB: nothing of it is stored
-  int units;
-  if constexpr (MODE == kLinear) {
-    units = p.n_tiles_host * NBP;
-    if (warp == 0 && lane < NSTAGE && lane < nk && u_first < units)
-      ptx::prefetch_l2_bulk(
-          p.w + ((size_t)min(block_of(u_first), p.NB - 1) * p.KB + lane) * kBlockBytes, kBlockBytes);
-    ptx::griddep_wait();
-  } else {
-    ptx::griddep_wait();
-    units = *p.n_tiles * NBP;
-  }
-  if (u_first >= units) return;
-
-  auto tile_of = [&](int u) {
-    Tile t;
-    if constexpr (MODE == kLinear) {
-      t.expert = 0;
-      t.row0 = (u / NBP) * p.per_tile;
-      t.count = min(p.per_tile, p.T - t.row0);
-    } else {
-      const int4 v = *reinterpret_cast<const int4*>(p.tiles + u / NBP);
-      t.expert = __shfl_sync(0xffffffffu, v.x, 0);
-      t.row0 = __shfl_sync(0xffffffffu, v.y, 0);
-      t.count = __shfl_sync(0xffffffffu, v.z, 0);
-    }
-    return t;
-  };
-
+  if (MODE == kLinear && warp == 3 && lane < NSTAGE && lane < nk)
+    ptx::prefetch_l2_bulk(
+        p.w + ((size_t)min(block_of(u_first), p.NB - 1) * p.KB + lane) * kBlockBytes, kBlockBytes);
   if (threadIdx.x == 0) {
     ptx::prefetch_tmap(&tm_w);
     ptx::prefetch_tmap(&tm_sf);
@@ -920,6 +896,29 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
   ptx::cluster_sync();  // both CTAs' barriers are set up
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);
+  ptx::griddep_launch_dependents();  // (TMEM in hand, as above)
+  ptx::griddep_wait();
+  const int units = (MODE == kLinear ? p.n_tiles_host : *p.n_tiles) * NBP;
+  if (u_first >= units) {  // both CTAs alike
+    if (warp == 1) ptx::tmem_dealloc_pair(tmem, 512);
+    return;
+  }
+
+  auto tile_of = [&](int u) {
+    Tile t;
+    if constexpr (MODE == kLinear) {
+      t.expert = 0;
+      t.row0 = (u / NBP) * p.per_tile;
+      t.count = min(p.per_tile, p.T - t.row0);
+    } else {
+      const int4 v = *reinterpret_cast<const int4*>(p.tiles + u / NBP);
+      t.expert = __shfl_sync(0xffffffffu, v.x, 0);
+      t.row0 = __shfl_sync(0xffffffffu, v.y, 0);
+      t.count = __shfl_sync(0xffffffffu, v.z, 0);
+    }
+    return t;
+  };
+
   const uint32_t even_full = ptx::map_shared_rank(ptx::smem_u32(full), 0);
   const uint32_t even_acc = ptx::map_shared_rank(ptx::smem_u32(acc_empty), 0);
 
