@@ -103,7 +103,8 @@ struct W4Args {
   uint32_t wait_ns;       // bound on a wait
   int T, N, KG, KB, NB, NG, k;
   int per_tile, n_tiles_host;  // kLinear: tokens of a tile, tiles
-  int splits, kb_per_split;
+  int splits, kb_per_split;  // CTAs of a cluster, K blocks of each
+  int k_parts;               // small calls, down: CTAs of each choice
   // Small calls: ids instead of a plan; the gate and up product brings w2 into L2.
   const int32_t* ids;
   const float* wt;
@@ -415,8 +416,9 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
   const int split = SPLIT ? (int)ptx::cluster_rank() : 0;
   constexpr bool BY_CHOICE = SMALL && MODE == kDown;  // a cluster's CTAs are a token's choices
   static_assert(!BY_CHOICE || SPLIT, "choices are summed over a cluster");
-  const int kb0 = SPLIT && !BY_CHOICE ? split * p.kb_per_split : 0;
-  int nk = SPLIT && !BY_CHOICE ? max(0, min(p.KB - kb0, p.kb_per_split)) : p.KB;
+  const int choice = BY_CHOICE ? split / p.k_parts : 0;
+  const int kb0 = SPLIT ? (BY_CHOICE ? split - choice * p.k_parts : split) * p.kb_per_split : 0;
+  int nk = SPLIT ? max(0, min(p.KB - kb0, p.kb_per_split)) : p.KB;
   const int u_first = SPLIT ? (int)(blockIdx.x / (uint32_t)p.splits) : (int)blockIdx.x;
   // The weight does not depend on what runs before: bring the first blocks into L2
   // while that finishes.  (Everything up to the wait runs beside it.)
@@ -459,7 +461,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
     if constexpr (BY_CHOICE) {
       units = p.T * p.NB;
       // A choice that is no expert adds nothing.
-      if (!((pairs.valids >> (u_first / p.NB * p.k + split)) & 1u)) nk = 0;
+      if (!((pairs.valids >> (u_first / p.NB * p.k + choice)) & 1u)) nk = 0;
     } else {
       units = __popc(pairs.leaders) * p.NB;
       if (blockIdx.x == 0 && warp == 0 && p.err_flag != nullptr && !pairs.valid && pairs.id != -1)
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
       t.row0 = (u / p.NB) * p.per_tile;
       t.count = min(p.per_tile, p.T - t.row0);
     } else if constexpr (BY_CHOICE) {
-      const int pair = u / p.NB * p.k + split;
+      const int pair = u / p.NB * p.k + choice;
       t.expert = __shfl_sync(0xffffffffu, pairs.id, pair);
       t.row0 = __shfl_sync(0xffffffffu, pairs.place(lane), pair);
       t.count = 1;
@@ -734,7 +736,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
     const int rb = u_first % p.NB;
     const int own_log = BY_CHOICE ? 0 : __ffs(NT / p.splits) - 1;
     const int own = 1 << own_log;  // tokens of each CTA
-    const float weight = BY_CHOICE && nk > 0 ? p.wt[u_first / p.NB * p.k + split] : 1.0f;
+    const float weight = BY_CHOICE && nk > 0 ? p.wt[u_first / p.NB * p.k + choice] : 1.0f;
     const int first = split * own;
     if (warp >= 4) {
       wait(&acc_full[0], 0);
@@ -1494,12 +1496,12 @@ cudaError_t launch_tokens(int nt, const void* a, uint64_t a_rows, uint64_t K, ui
   return launch_pair<MODE>(a, a_rows, K, blocks, g, units / g.NB, num_sms, s, why);
 }
 
-// CTAs along K for `units` units of KB blocks each: powers of two up to the
-// portable cluster size that the device's slots hold at once, and two blocks each
+// CTAs along K for `units` units of KB blocks each: powers of two up to `most` (the
+// portable cluster size) that the device's slots hold at once, and two blocks each
 // at least.
-int pick_splits(int64_t units, int KB, int slots) {
+int pick_splits(int64_t units, int KB, int slots, int most = 8) {
   int s = 1;
-  while (s < 8 && units * s * 2 <= slots && KB >= 4 * s) s *= 2;
+  while (2 * s <= most && units * s * 2 <= slots && KB >= 4 * s) s *= 2;
   return s;
 }
 
@@ -1683,12 +1685,15 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   int64_t units = most * g.NB;
   if (small) {
     g.out = out;
-    g.splits = k;  // one CTA for each choice
+    // One CTA for each choice, or several that share its K range.
     units = T * g.NB;
+    g.k_parts = pick_splits(units * k, g.KB, 2 * num_sms, kSmallChoices / k);
+    g.splits = k * g.k_parts;
   } else {
+    g.k_parts = 1;
     g.splits = nt == 16 ? pick_splits(units, g.KB, 2 * num_sms) : 1;
   }
-  g.kb_per_split = (int)ceil_div(g.KB, g.splits);
+  g.kb_per_split = (int)ceil_div(g.KB, small ? g.k_parts : g.splits);
   e = launch_tokens<kDown>(nt, base + l.h, (uint64_t)R, (uint64_t)I, (uint64_t)E * g.NB * g.KB, g,
                            units, num_sms, s, why);
   if (e != cudaSuccess || small) return e;
