@@ -201,25 +201,27 @@ __device__ __forceinline__ void add_held16(float2 (&y)[4], const uint4& v, uint3
   }
 }
 
-// Shape of an instance.  GATHER: the token rows are fetched by index.
-template <int MODE, int NT, bool SPLIT>
+// Shape of an instance.  GATHER: the token rows are fetched by index.  SMALL: see
+// w4_kernel.
+template <int MODE, int NT, bool SPLIT, int SMALL = 0>
 struct Cfg {
+  static constexpr bool BY_CHOICE = SMALL != 0 && MODE == kDown;
   static constexpr int NA = MODE == kGateUp ? 2 : 1;
   static constexpr bool GATHER = MODE == kGateUp && NT <= 32;
   // Stages and CTAs per SM: as many bytes under way as shared memory allows; two
   // CTAs where the tile is small, so that one streams while the other turns
   // around.
-  static constexpr int CTAS = NA == 1 && NT <= 64 ? 2 : 1;
+  static constexpr int CTAS = SMALL == 2 ? 4 : NA == 1 && NT <= 64 ? 2 : 1;
   static constexpr int GROUPS = NT <= 64 || SPLIT ? 1 : 3;  // epilogue groups
   static constexpr int THREADS = 128 + 128 * GROUPS;
   static constexpr int TOK_TILE = NT * 128;
   static constexpr int STAGE = NA * (kTileBytes + kSfAtomBytes) + TOK_TILE + kSfAtomBytes;
   // Split K: the partial sums that the CTA receives, fp32
   // [rank][owned token][accumulator][row].
-  static constexpr int SUM_BYTES = SPLIT ? NA * NT * 512 : 0;
+  static constexpr int SUM_BYTES = BY_CHOICE ? kSmallChoices * 512 : SPLIT ? NA * NT * 512 : 0;
   // For each epilogue group: two chunks' maxima of its four warps.
   static constexpr int MAX_BYTES = MODE == kGateUp ? GROUPS * 2 * 4 * kChunk * 4 : 0;
-  static constexpr int LIMIT = (CTAS == 2 ? 113 * 1024 : 232448) - 1024 - 512;
+  static constexpr int LIMIT = (CTAS == 4 ? 56 * 1024 : CTAS == 2 ? 113 * 1024 : 232448) - 1024 - 512;
   static constexpr int FIT = (LIMIT - SUM_BYTES - MAX_BYTES) / STAGE;
   static constexpr int NSTAGE = FIT > 10 ? 10 : FIT;
   static constexpr int OFF_W = 0;
@@ -242,7 +244,7 @@ struct Cfg {
   // at bits 24-28; N >> 3 (bits 17-22) is the tile's; the scale byte of each
   // operand is chosen at bits 4-5 (B) and 29-30 (A).
   static constexpr uint32_t IDESC = (5u << 7) | (1u << 23) | ((128u >> 4) << 24);
-  static_assert(NSTAGE >= 3 && SMEM <= 232448 && TMEM_COLS * CTAS <= 512, "budgets");
+  static_assert(NSTAGE >= 2 && SMEM <= 232448 && TMEM_COLS * CTAS <= 512, "budgets");
   static_assert(NT % kChunk == 0 && NT <= 128 && (!SPLIT || NT <= 32), "tokens of a tile");
 };
 
@@ -387,14 +389,18 @@ __device__ __forceinline__ void finish_token(const W4Args& p, const float (&v)[N
 
 // SMALL: a routed call of at most kSmallPairs rows and kSmallChoices choices, whose
 // CTAs sort the rows themselves.  Its down product takes one token's 128 columns
-// for each cluster and one of the token's experts for each CTA, and adds the
-// experts' sums as a split K adds its parts: no results of single experts, and no
-// kernel to add them.
-template <int MODE, int NT, bool SPLIT, bool SMALL>
-__global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, SPLIT>::CTAS))
+// for each cluster and one of the token's experts (or, of few, a part of one's K
+// range) for each CTA, and adds the experts' sums as a split K adds its parts: no
+// results of single experts, and no kernel to add them.  One token over 8 of 128
+// experts, 4096 x 1024: 20 us, with plan, results and sum 30.  SMALL == 2: the down
+// product with four CTAs to an SM, of two stages each instead of five, for grids
+// that fill more than two: 2 tokens over 8 of 128 (512 CTAs) 30.5 us against 34,
+// one over 2 of 8, 4096 x 14336 (256 CTAs of 28 stages) 52 against 45.5.
+template <int MODE, int NT, bool SPLIT, int SMALL>
+__global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT, SMALL>::THREADS, (Cfg<MODE, NT, SPLIT, SMALL>::CTAS))
     w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
               const W4Args p) {
-  using C = Cfg<MODE, NT, SPLIT>;
+  using C = Cfg<MODE, NT, SPLIT, SMALL>;
   constexpr int NA = C::NA, NSTAGE = C::NSTAGE;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
@@ -414,7 +420,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   const int split = SPLIT ? (int)ptx::cluster_rank() : 0;
-  constexpr bool BY_CHOICE = SMALL && MODE == kDown;  // a cluster's CTAs are a token's choices
+  constexpr bool BY_CHOICE = C::BY_CHOICE;  // a cluster's CTAs are a token's choices
   static_assert(!BY_CHOICE || SPLIT, "choices are summed over a cluster");
   const int choice = BY_CHOICE ? split / p.k_parts : 0;
   const int kb0 = SPLIT ? (BY_CHOICE ? split - choice * p.k_parts : split) * p.kb_per_split : 0;
@@ -456,7 +462,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
   Pairs pairs;
   if constexpr (MODE == kLinear) {
     units = p.n_tiles_host * p.NB;
-  } else if constexpr (SMALL) {
+  } else if constexpr (SMALL != 0) {
     pairs.load(p, lane);
     if constexpr (BY_CHOICE) {
       units = p.T * p.NB;
@@ -489,7 +495,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
       t.expert = __shfl_sync(0xffffffffu, pairs.id, pair);
       t.row0 = __shfl_sync(0xffffffffu, pairs.place(lane), pair);
       t.count = 1;
-    } else if constexpr (SMALL) {
+    } else if constexpr (SMALL != 0) {
       t = pairs.tile(u / p.NB);
     } else {
       const int4 v = *reinterpret_cast<const int4*>(p.tiles + u / p.NB);
@@ -499,7 +505,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
     }
     return t;
   };
-  if constexpr (SMALL && MODE == kGateUp) {
+  if constexpr (SMALL != 0 && MODE == kGateUp) {
     // The first blocks on their way to L2 while barriers and TMEM are set up.
     if (warp == 3) {
       const Tile t = tile_of(u_first);
@@ -511,7 +517,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
   }
   // The pair (token * k + choice) of row i of a tile.
   auto pair_of = [&](const Tile& t, int i) {
-    if constexpr (SMALL) return Pairs::row(t, i);
+    if constexpr (SMALL != 0) return Pairs::row(t, i);
     else return (int)p.perm[t.row0 + i];
   };
 
@@ -560,7 +566,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT>::THREADS, (Cfg<MODE, NT, 
         __syncwarp();
       }
     }
-    if constexpr (SMALL && MODE == kGateUp) {
+    if constexpr (SMALL != 0 && MODE == kGateUp) {
       // What is left to read is the experts' w2: each of an expert's CTAs brings
       // its share into L2.
       for (int u = u_first; u < units; u += u_step) {
@@ -1359,10 +1365,10 @@ bool encode_rows(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, ui
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, int NT, bool SPLIT, bool SMALL = false>
+template <int MODE, int NT, bool SPLIT, int SMALL = 0>
 cudaError_t launch_cfg(const void* a, uint64_t a_rows, uint64_t K, uint64_t blocks, W4Args args,
                        int64_t units, int num_sms, cudaStream_t s, const char** why) {
-  using C = Cfg<MODE, NT, SPLIT>;
+  using C = Cfg<MODE, NT, SPLIT, SMALL>;
   CUtensorMap tm_w, tm_a;
   if (!encode_weight(&tm_w, args.w, blocks) ||
       !encode_rows(&tm_a, a, K, a_rows, C::GATHER ? 1 : NT)) {
@@ -1476,9 +1482,11 @@ cudaError_t launch_tokens(int nt, const void* a, uint64_t a_rows, uint64_t K, ui
     if (g.ids != nullptr) {
       if constexpr (MODE == kGateUp) {
         if (g.splits == 1)
-          return launch_cfg<MODE, 16, false, true>(a, a_rows, K, blocks, g, units, num_sms, s, why);
+          return launch_cfg<MODE, 16, false, 1>(a, a_rows, K, blocks, g, units, num_sms, s, why);
+      } else if (units * g.splits > 2 * num_sms) {
+        return launch_cfg<MODE, 16, true, 2>(a, a_rows, K, blocks, g, units, num_sms, s, why);
       }
-      return launch_cfg<MODE, 16, true, true>(a, a_rows, K, blocks, g, units, num_sms, s, why);
+      return launch_cfg<MODE, 16, true, 1>(a, a_rows, K, blocks, g, units, num_sms, s, why);
     }
   }
   if (nt <= 16)
