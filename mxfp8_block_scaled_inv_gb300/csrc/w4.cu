@@ -84,7 +84,8 @@ enum Mode { kLinear = 0, kGateUp = 1, kDown = 2 };
 // Device-side plan of a routed call: which sorted rows each tile holds.
 struct alignas(16) Tile {
   int32_t expert, row0, count;
-  uint32_t pairs;  // small calls: bit i: pair i (token * k + choice) is one of its rows
+  uint32_t pairs;  // small calls: bit i: pair i (token * k + choice) is one of its rows;
+                   // others: whether it is its expert's only tile
 };
 // Pairs and choices of a call that needs no plan: a warp sorts the pairs in its
 // registers.
@@ -488,6 +489,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT, SMALL>::THREADS, (Cfg<MOD
     Tile t;
     if constexpr (MODE == kLinear) {
       t.expert = 0;
+      t.pairs = 0u;
       t.row0 = (u / p.NB) * p.per_tile;
       t.count = min(p.per_tile, p.T - t.row0);
     } else if constexpr (BY_CHOICE) {
@@ -502,6 +504,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT, SMALL>::THREADS, (Cfg<MOD
       t.expert = __shfl_sync(0xffffffffu, v.x, 0);
       t.row0 = __shfl_sync(0xffffffffu, v.y, 0);
       t.count = __shfl_sync(0xffffffffu, v.z, 0);
+      t.pairs = (uint32_t)__shfl_sync(0xffffffffu, v.w, 0);
     }
     return t;
   };
@@ -535,12 +538,19 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT, SMALL>::THREADS, (Cfg<MOD
 
   if (warp == 0) {
     // ------------------------------------------------------------- copies
+    // Weights that no other tile reads make way in L2 for what is read again: the rows,
+    // the activation between the products, the results (64 tokens over 128 experts
+    // 132.3 -> 128.5 us, 1024 over 64 150 -> 143; with every expert's weights marked so, 4096
+    // tokens, two tiles each, 337 -> 343).
+    constexpr bool PLANNED = MODE != kLinear && SMALL == 0;
+    const uint64_t once = ptx::policy_evict_first();
     int it = 0;
     bool ok = true;
     for (int u = u_first; u < units && ok; u += u_step) {
       const Tile t = tile_of(u);
       const uint32_t bytes = NA * kBlockBytes + (C::GATHER ? 0u : (uint32_t)C::TOK_TILE);
       const int rb = u % p.NB;
+      const uint64_t keep = PLANNED && t.pairs ? once : ptx::policy_evict_normal();
       int row[NA];  // of a matrix's first block, in rows of 64 bytes
 #pragma unroll
       for (int a = 0; a < NA; ++a)
@@ -554,7 +564,11 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT, SMALL>::THREADS, (Cfg<MOD
           ptx::mbar_arrive_expect_tx(&full[s], bytes);
 #pragma unroll
           for (int a = 0; a < NA; ++a) {
-            ptx::tma_load_2d(smem + C::OFF_W + (s * NA + a) * kTileBytes, &tm_w, &full[s], 0, row[a]);
+            if constexpr (PLANNED)
+              ptx::tma_load_2d_hint(smem + C::OFF_W + (s * NA + a) * kTileBytes, &tm_w, &full[s], 0,
+                                    row[a], keep);
+            else
+              ptx::tma_load_2d(smem + C::OFF_W + (s * NA + a) * kTileBytes, &tm_w, &full[s], 0, row[a]);
             ptx::bulk_load(smem + C::OFF_WSF + (s * NA + a) * kSfAtomBytes,
                            p.w + (size_t)(uint32_t)row[a] * 64 + kCodeBytes, kSfAtomBytes, &full[s]);
             row[a] += kBlockBytes / 64;
@@ -916,6 +930,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
     Tile t;
     if constexpr (MODE == kLinear) {
       t.expert = 0;
+      t.pairs = 0u;
       t.row0 = (u / NBP) * p.per_tile;
       t.count = min(p.per_tile, p.T - t.row0);
     } else {
@@ -923,6 +938,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
       t.expert = __shfl_sync(0xffffffffu, v.x, 0);
       t.row0 = __shfl_sync(0xffffffffu, v.y, 0);
       t.count = __shfl_sync(0xffffffffu, v.z, 0);
+      t.pairs = (uint32_t)__shfl_sync(0xffffffffu, v.w, 0);
     }
     return t;
   };
@@ -941,6 +957,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------- copies
+    const uint64_t once = ptx::policy_evict_first();  // (as above)
     int it = 0;
     bool ok = true;
     for (int u = u_first; u < units && ok; u += u_step) {
@@ -949,6 +966,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
       const int boxes = (half + C::BOX_ROWS - 1) / C::BOX_ROWS;
       const uint32_t bytes = 2u * (uint32_t)(NA * kBlockBytes + boxes * C::BOX_ROWS * 128);
       const int rb = min(block_of(u), p.NB - 1);
+      const uint64_t keep = MODE != kLinear && t.pairs ? once : ptx::policy_evict_normal();
       int blk[NA];
 #pragma unroll
       for (int a = 0; a < NA; ++a)
@@ -962,8 +980,8 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
           if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], bytes);
 #pragma unroll
           for (int a = 0; a < NA; ++a) {
-            ptx::tma_load_2d_pair(smem + C::OFF_W + (s * NA + a) * kTileBytes, &tm_w, bar, 0,
-                                  blk[a] * (kBlockBytes / 64));
+            ptx::tma_load_2d_pair_hint(smem + C::OFF_W + (s * NA + a) * kTileBytes, &tm_w, bar, 0,
+                                       blk[a] * (kBlockBytes / 64), keep);
             ptx::tma_load_2d_pair(smem + C::OFF_WSF + (s * NA + a) * kSfAtomBytes, &tm_sf, bar, 0,
                                   blk[a] * (kBlockBytes / 256) + kCodeBytes / 256);
             ++blk[a];
@@ -1213,7 +1231,7 @@ __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* id
     if (tid == 0) n_tiles[0] = size_at[0] + size_n[0];
     Tile t;
     t.expert = tid;
-    t.pairs = 0u;
+    t.pairs = nt_e == 1 ? 1u : 0u;
     if (nt_e > 1) {
       const int at = atomicAdd(&size_at[full16], nt_e - 1);
       t.count = rows;
