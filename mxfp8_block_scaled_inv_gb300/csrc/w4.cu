@@ -314,13 +314,21 @@ __device__ __forceinline__ void finish_chunk(const W4Args& p, float (&v)[NA][kCh
       inv = group_scale(__uint_as_float(m), &sb);
       if (q == 0 && lane < live && rb < p.NG) p.out_sf[(size_t)(row + lane) * p.NG + rb] = (uint8_t)sb;
     }
-    uint8_t* o = static_cast<uint8_t*>(p.out) + (size_t)row * p.N + n;
+    // Four neighbouring lanes swap the codes of four tokens, so that each stores four
+    // rows of one (64 tokens over 128 experts 127.5 us, with single bytes 128.5).
+    const int tok = lane & 3;
+    const uint32_t pick2 = lane & 2 ? 0x3276u : 0x5410u, pick1 = lane & 1 ? 0x3715u : 0x6240u;
+    uint8_t* o = static_cast<uint8_t*>(p.out) + (size_t)(row + tok) * p.N + (n - tok);
 #pragma unroll
-    for (int i = 0; i < kChunk; i += 2) {
-      const uint32_t c = e4m3x2(__fmul_rn(h[i], __shfl_sync(0xffffffffu, inv, i)),
-                                __fmul_rn(h[i + 1], __shfl_sync(0xffffffffu, inv, i + 1)));
-      if (in && i < live) o[(size_t)i * p.N] = (uint8_t)c;
-      if (in && i + 1 < live) o[(size_t)(i + 1) * p.N] = (uint8_t)(c >> 8);
+    for (int i = 0; i < kChunk; i += 4) {
+      uint32_t w = 0u;
+#pragma unroll
+      for (int j = 0; j < 4; j += 2)
+        w |= e4m3x2(__fmul_rn(h[i + j], __shfl_sync(0xffffffffu, inv, i + j)),
+                    __fmul_rn(h[i + j + 1], __shfl_sync(0xffffffffu, inv, i + j + 1))) << (8 * j);
+      w = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 2), pick2);
+      w = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 1), pick1);
+      if (in && i + tok < live) *reinterpret_cast<uint32_t*>(o + (size_t)i * p.N) = w;
     }
   } else {
     // (Instructions are what this one is short of: 11 for each value now, 24 with a
