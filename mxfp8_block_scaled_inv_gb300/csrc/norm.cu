@@ -12,8 +12,11 @@
 // Bound by memory: every byte is moved once.  A thread holds its 16-byte chunks
 // of s as packed BF16 between the two uses, and chunk c belongs to thread
 // c mod (threads of the row), so that 16 neighbouring lanes hold one scale
-// group and every access of a warp is contiguous.  Rows of up to 1024 columns
-// take one warp (no barrier, eight rows to a CTA); longer ones a CTA.
+// group and every access of a warp is contiguous.  Measured with a residual, y
+// and codes, 8192 rows: of 4096 columns 45.4 us, 6.65 TB/s (0.98 of a plain copy's
+// rate), of 512 columns 7.6 us (0.74: two rounds of CTAs, each in and out once); one
+// row of 4096 columns 2.4 us, which is its launch, one trip to memory and the sum
+// over the CTA.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -162,12 +165,20 @@ cudaError_t launch_add_rms_norm(const void* x, const void* res, void* res_out, c
   a.KG = (int)ceil_div(D, kGroup);
   a.inv_d = 1.0f / (float)D;
   a.eps = eps;
+  // Rows of up to 512 columns take one warp (no barrier, eight rows to a CTA), longer
+  // ones a CTA.  8192 rows and one row, us, this split and the next best:
+  //   512 columns   warp 7.8, 2.1       64 threads x 1 chunk 9.2, 1.9
+  //   1024          128 x 1 11.7, 2.0   warp 13.2, 2.1 (64 rows: 2.1 and 3.4)
+  //   2048          256 x 1 24.3, 2.0   128 x 2 23.9, 2.4 (2048 rows: 7.3 and 7.7)
+  //   4096          256 x 2 45.5, 2.5   512 x 1 47.0, 2.5
+  //   8192          512 x 2 88.9        1024 x 1 103, 256 x 4 89.1 (64 rows: 3.1, 3.1, 3.4)
+  //   16384         512 x 4 174         1024 x 2 213
   if (a.chunks <= 32) return launch_rows<32, 1>(a, s);
   if (a.chunks <= 64) return launch_rows<32, 2>(a, s);
-  if (a.chunks <= 128) return launch_rows<32, 4>(a, s);
-  if (a.chunks <= 256) return launch_rows<128, 2>(a, s);
+  if (a.chunks <= 128) return launch_rows<128, 1>(a, s);
+  if (a.chunks <= 256) return launch_rows<256, 1>(a, s);
   if (a.chunks <= 512) return launch_rows<256, 2>(a, s);
-  if (a.chunks <= 1024) return launch_rows<256, 4>(a, s);
+  if (a.chunks <= 1024) return launch_rows<512, 2>(a, s);
   if (a.chunks <= 2048) return launch_rows<512, 4>(a, s);
   return launch_rows<1024, 8>(a, s);
 }

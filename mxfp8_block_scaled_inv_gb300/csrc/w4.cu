@@ -90,7 +90,8 @@ struct alignas(16) Tile {
 // Pairs and choices of a call that needs no plan: a warp sorts the pairs in its
 // registers.
 constexpr int kSmallPairs = 16;
-constexpr int kSmallChoices = 8;  // a cluster's CTAs
+constexpr int kMaxCluster = 8;    // CTAs of a cluster on any device
+constexpr int kSmallChoices = kMaxCluster;
 
 struct W4Args {
   const uint8_t* w;       // prepared weight
@@ -1498,7 +1499,7 @@ cudaError_t launch_pair(const void* a, uint64_t a_rows, uint64_t K, uint64_t blo
   return cudaLaunchKernelEx(&cfg, kern, tm_w, tm_sf, tm_a, args);
 }
 
-// The product for tiles of at most `nt` tokens (16, 32, 64, 128 or 240), its K
+// The product for tiles of at most `nt` tokens (16, 32, 64, dense 128, 240), its K
 // split where the caller chose so (16 and, dense, 32 tokens only).
 template <int MODE>
 cudaError_t launch_tokens(int nt, const void* a, uint64_t a_rows, uint64_t K, uint64_t blocks,
@@ -1526,16 +1527,28 @@ cudaError_t launch_tokens(int nt, const void* a, uint64_t a_rows, uint64_t K, ui
     return launch_cfg<MODE, 32, false>(a, a_rows, K, blocks, g, units, num_sms, s, why);
   }
   if (nt <= 64) return launch_cfg<MODE, 64, false>(a, a_rows, K, blocks, g, units, num_sms, s, why);
-  if (nt <= 128) return launch_cfg<MODE, 128, false>(a, a_rows, K, blocks, g, units, num_sms, s, why);
+  if constexpr (MODE == kLinear) {
+    if (nt <= 128) return launch_cfg<MODE, 128, false>(a, a_rows, K, blocks, g, units, num_sms, s, why);
+  }
   return launch_pair<MODE>(a, a_rows, K, blocks, g, units / g.NB, num_sms, s, why);
 }
 
-// CTAs along K for `units` units of KB blocks each: powers of two up to `most` (the
-// portable cluster size) that the device's slots hold at once, and two blocks each
-// at least.
-int pick_splits(int64_t units, int KB, int slots, int most = 8) {
+// CTAs that the device holds at once in clusters of c, with one or two to an SM: a
+// cluster's SMs are neighbours, and some of their groups are short of a few (152 SMs
+// hold 36 clusters of 4 and 15 of 8, and twice 37 and 18 with two CTAs to an SM).
+int64_t held(int num_sms, int ctas, int c) {
+  const int64_t all = (int64_t)num_sms * ctas;
+  return c < 4 ? all : c > 4 && ctas == 1 ? all * 15 / 19 : all * 18 / 19;
+}
+// CTAs along K of each of a unit's `per` products of KB blocks: powers of two up to
+// the portable cluster size that the device holds at once, two blocks each at least
+// (1 x 4096 x 4096 5.6 us on 8, unsplit 11.7), and none where K has less than eight (32 x
+// 4096 x 512 3.9 us, on two 4.6; 16 x 2048 x 1024 on four 4.2, on two 4.6, unsplit 4.7).
+int pick_splits(int64_t units, int KB, int num_sms, int ctas, int per = 1) {
   int s = 1;
-  while (2 * s <= most && units * s * 2 <= slots && KB >= 4 * s) s *= 2;
+  while (2 * s * per <= kMaxCluster && units * 2 * s * per <= held(num_sms, ctas, 2 * s * per) &&
+         KB >= 8 && KB >= 4 * s)
+    s *= 2;
   return s;
 }
 
@@ -1570,7 +1583,7 @@ cudaError_t launch_linear_a8w4(const uint8_t* a, const uint8_t* a_sf, const uint
   cudaError_t e = watchdog_address(&g.wd);
   if (e != cudaSuccess) return e;
   if (T <= 32) {
-    g.splits = pick_splits(g.NB, g.KB, 2 * num_sms);
+    g.splits = pick_splits(g.NB, g.KB, num_sms, 2);
     g.per_tile = T <= 16 ? 16 : 32;
   } else {
     // Tiles of even size.  A stage of n tokens costs about 256 + 2 n cycles of
@@ -1598,11 +1611,17 @@ cudaError_t launch_linear_a8w4(const uint8_t* a, const uint8_t* a_sf, const uint
 namespace {
 bool small_call(int64_t R, int k) { return R <= kSmallPairs && k <= kSmallChoices; }
 // Most tokens of a tile, by the rows that an expert gets on average: above that
-// some experts take two tiles, which read their weights twice (from L2).
+// some experts take two tiles, which read their weights twice (from L2).  128 experts,
+// 8 choices, 4096 x 1024, us, with tiles of 16 / 32 / 64 / 128 / 240:
+//   rows an expert on average
+//    4    128 / 127 / 134 / 159 / 154      24   279 / 212 / 179 / 202 / 198
+//    5    144 / 135 / 142 / 170 / 163      40   406 / 289 / 206 / 216 / 210
+//   12    188 / 161 / 162 / 190 / 186      48   461 / 331 / 224 / 231 / 216
+//   14    206 / 176 / 166 / 194 / 189      64   586 / 409 / 268 / 252 / 228
 int expert_tile(int64_t R, int k, int E) {
   const int64_t avg = ceil_div(R, E);
   if (small_call(R, k)) return 16;
-  return avg <= 5 ? 16 : avg <= 12 ? 32 : avg <= 40 ? 64 : avg <= 80 ? 128 : kMaxTokens;
+  return avg <= 3 ? 16 : avg <= 12 ? 32 : avg <= 40 ? 64 : kMaxTokens;
 }
 // An expert of c rows has ceil(c / nt) tiles at most (fewer where even tiles
 // round up to 16), that is c / nt and one more if it has any.
@@ -1664,7 +1683,8 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
     g.NB2 = (int)ceil_div(N, 128);
   }
   if (!small) {
-    const int ctas = R > 4 * kPlanThreads ? 8 : 1;
+    // (2048 rows 1.5 us faster on eight CTAs, 24576 rows 13; 1024 rows as on one.)
+    const int ctas = R > kPlanThreads ? kMaxCluster : 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = (unsigned)ctas;
     attr[1].val.clusterDim.y = 1;
@@ -1702,7 +1722,7 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   g.N = I;
   g.KG = g.KB = (int)ceil_div(K, kGroup);
   g.NB = g.NG = (int)ceil_div(I, 128);
-  g.splits = nt == 16 ? pick_splits(most * g.NB, g.KB, num_sms) : 1;
+  g.splits = nt == 16 ? pick_splits(most * g.NB, g.KB, num_sms, 1) : 1;
   g.kb_per_split = (int)ceil_div(g.KB, g.splits);
   e = launch_tokens<kGateUp>(nt, rows, (uint64_t)n_rows, (uint64_t)K, 2 * (uint64_t)E * g.NB * g.KB, g,
                              most * g.NB, num_sms, s, why);
@@ -1721,11 +1741,11 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
     g.out = out;
     // One CTA for each choice, or several that share its K range.
     units = T * g.NB;
-    g.k_parts = pick_splits(units * k, g.KB, 2 * num_sms, kSmallChoices / k);
+    g.k_parts = pick_splits(units, g.KB, num_sms, 2, k);
     g.splits = k * g.k_parts;
   } else {
     g.k_parts = 1;
-    g.splits = nt == 16 ? pick_splits(units, g.KB, 2 * num_sms) : 1;
+    g.splits = nt == 16 ? pick_splits(units, g.KB, num_sms, 2) : 1;
   }
   g.kb_per_split = (int)ceil_div(g.KB, small ? g.k_parts : g.splits);
   e = launch_tokens<kDown>(nt, base + l.h, (uint64_t)R, (uint64_t)I, (uint64_t)E * g.NB * g.KB, g,
