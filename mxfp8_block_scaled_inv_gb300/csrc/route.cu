@@ -18,11 +18,19 @@
 // asked for is made, and where two neighbouring picks are nearer than the
 // rounding bounds below, and not equal in logit and bias, picking goes on to the
 // next clear gap and the lanes order their picks by 64-bit values, one for each
-// lane.  Where that does not settle it (the edge between kept groups, a softmax
-// under a bias, no gap within 32) the row is done again in 64 bits altogether.
-// The device has next to no 64-bit units: the whole row in 64 bits costs as much
-// as some tens of rows.  Without a bias the experts are ordered by their logits,
-// which is exact.
+// lane.  Groups whose values lie that near to the edge between those kept and
+// those left are ordered by the 64-bit sums of their best.  Where this does not
+// settle it (no gap within 32 picks, a group with more than its best that near
+// together, groups that do not lie on whole lanes) the row is done again in 64 bits
+// altogether.  The device has next to no 64-bit units: such a row takes 30 to 40 us,
+// as long as thousands of others.  Without a bias the experts are ordered by their
+// logits, which is exact.
+//
+// Bound by instructions: 1200 for a row of 256 experts with bias and groups, 63 % of
+// the issue slots, 8 of 16 warps a scheduler.  8192 rows 14.7 us (1.3 us of
+// memory; with unsorted keys, a search through the lane's experts for each
+// pick, 21; with whole rows wherever groups are near 18), without bias and groups
+// 9.9; one row 4.0 us, of which launch and one trip to memory are 2.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -30,20 +30,46 @@
 //   warp 2   token scales, one byte per row and stage, into the scale atom; for
 //            few rows of the gate and up product also the token rows themselves,
 //            gathered by index four to an instruction.
-//   warp 3   idle (the epilogue's warps begin at a multiple of four).
+//   warp 3   prefetches into L2 (the epilogue's warps begin at a multiple of four).
 //   warps 4- epilogue: groups of four warps, one for each TMEM lane quadrant, take
 //            16 tokens at a time straight from TMEM: a lane holds one weight row.
 //            Stores of a warp are contiguous along the rows; the abs-max of a
 //            scale group (128 rows of a token) is a warp-wide maximum and an
-//            exchange between the group's four warps.
-// Two forms:
-//   streaming  CTAs walk the units with a stride of the grid; copies run ahead
-//              across units and the accumulator is doubled where TMEM allows it,
-//              so that one unit's epilogue overlaps the next one's products.
+//            exchange between the group's four warps.  (By way of shared memory, a lane
+//            for eight rows: 4096 tokens over 64 experts 530 us, so 435.)
+// Roles and operands are uniform to the compiler (a warp's role is broadcast, one
+// elected lane issues): a warp that issues a copy or an MMA behind a lane's test
+// spends its time moving operands (64 tokens over 128 experts 177 us, so 132).
+// Three forms:
 //   split      few units: one unit for each cluster of up to 8 CTAs, which share
 //              its K range.  Each CTA owns some of the tokens, receives the partial
 //              sums for them through distributed shared memory and adds them in
 //              rank order.
+//   streaming  CTAs walk the units with a stride of the grid; copies run ahead
+//              across units and the accumulator is doubled where TMEM allows it,
+//              so that one unit's epilogue overlaps the next one's products.  Tiles of
+//              up to 64 tokens, 128 in the dense product.
+//   pairs      the same with two CTAs to a unit, for tiles of up to 240 tokens; see
+//              w4_pair_kernel.
+// A routed call is up to five kernels: plan (rows sorted by expert, tiles), rows
+// (laid out by expert, for large tiles), gate and up, down, join (the sum over a
+// token's experts).  Up to 16 rows take two; see w4_kernel.
+//
+// What bounds it, measured (floors: a copy's 6.78 TB/s, 3.78 PFLOP/s, twice the measured
+// BF16 rate):
+//   dense, 1 x 4096 x 4096      5.4 us (floor 1.3): launch, first copies, the sum over
+//                               the cluster, one after the other
+//   dense, 8192 x 4096 x 4096   79 us, 3.5 PFLOP/s (0.92); 2048 rows 24 us (0.76: two
+//                               rounds of pairs, and the first copies and last epilogue)
+//   64 tokens, 128 experts      127 us (0.98): HBM
+//   1 token, 8 of 128           20 us (0.38): two kernels of 35 and 18 MB, each with the
+//                               latencies of the first case
+//   4096 tokens, 64 experts     336 us (0.49): gate and up 149 us (tensor pipe 63 %
+//                               active; one accumulator, so that the epilogue's fetches
+//                               wait for the products and the other way round; without
+//                               any arithmetic or store in it 131), down 113 (copies
+//                               from L2 and 16-bit stores at once), the sum 45 and the
+//                               rows 20 (both memory), the plan 9
 //
 // Every wait is bounded in wall time; on expiry the kernel sets a watchdog bit,
 // stops issuing, waits for its own copies and MMAs, frees TMEM and returns.
@@ -252,7 +278,8 @@ struct Cfg {
 
 // silu(g) * u.  The fast exponential (off by 2^-22 and 2^-23 |g| of itself) and
 // quotient (2^-22) are far inside the step of the 8-bit codes that follow; the
-// exact ones are a third of the epilogue's instructions.
+// exact ones are a third of the epilogue's instructions.  Below g = -87, where silu(g) is
+// smaller than 2^-119, the result is zero.
 __device__ __forceinline__ float swiglu(float g, float u) {
   return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
@@ -263,7 +290,7 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 // see, and half the bytes of FP32 to write and read again.  m: the exponent bits of
 // the largest magnitude, which is below 2^(e - 126) for their field e; the value is
 // the integer times 2^(e - 140).  With an infinity or a NaN among the 32 they are BF16
-// values.
+// values.  (4096 tokens over 64 experts: FP32 results 431 us, these 384 at the time.)
 constexpr uint32_t kExpMask = 0x7F800000u;
 __device__ __forceinline__ uint32_t held16_finite(float y, uint32_t m) {
   const float inv = __uint_as_float(0x85800000u - max(m, kLeastExp << 23));  // 2^(140 - e)
@@ -838,17 +865,21 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT, SMALL>::THREADS, (Cfg<MOD
   }
 }
 
-// The form for tiles of more than 128 tokens: CTA pairs.  One MMA (cta_group::2) takes
+// The form for tiles of more than 128 tokens (routed: more than 64): CTA pairs.  One MMA
+// (cta_group::2) takes
 // 256 weight rows, 128 of each CTA (two row blocks side by side), against the
 // tile's tokens, of which each CTA holds half.  Shared memory is what bounds the
 // streaming form (128 bytes a cycle: a stage of 240 tokens writes 46 KB and the
 // MMAs read 46 KB, 720 cycles where the products take 480; measured 712), and a
-// pair writes and reads each token once for both CTAs (30 + 31 KB).  Roles and
-// epilogue are those of the streaming form, with these differences: the even
+// pair writes and reads each token once for both CTAs (30 + 31 KB): 8192 x 4096 x
+// 4096 99 us in the streaming form, 79 here; 4096 tokens over 64 experts 363 and 343.
+// Roles and epilogue are those of the streaming form, with these differences: the even
 // CTA issues the MMAs and scale copies for both; the odd CTA's copies and scale
 // words count on the even CTA's barriers; stages and accumulators are handed
 // back to, and released by, both.  With an odd number of row blocks the last
-// pair's odd CTA repeats the last block and stores nothing.
+// pair's odd CTA repeats the last block and stores nothing.  Three epilogue groups:
+// 343 us; two 349, four 350, five 355 (fewer registers each); fetching a chunk ahead of
+// its arithmetic: no faster.
 template <int MODE>
 struct PairCfg {
   static constexpr int NA = MODE == kGateUp ? 2 : 1;
@@ -1277,7 +1308,9 @@ __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* id
 
 // The activation rows laid out by expert (one warp for each), for the plain
 // copies of large tiles: every 128 weight rows read a tile's tokens anew, and a
-// copy by index moves four rows where a plain one moves 80.
+// copy by index moves four rows (in 44 ns) where a plain one moves a box of them:
+// gate and up of 4096 tokens over 64 experts 562 us by index in tiles of 128; 149 with
+// rows laid out, which takes 20.
 constexpr int kRowWarps = 8;
 
 __global__ void __launch_bounds__(kRowWarps * 32) w4_rows_kernel(const uint4* a, const int32_t* perm,
@@ -1301,7 +1334,9 @@ __global__ void __launch_bounds__(kRowWarps * 32) w4_rows_kernel(const uint4* a,
 }
 
 // out[t] = weighted sum over the token's choices, in their order, of the 16-bit
-// results that the down product left; eight columns to a thread.
+// results that the down product left; eight columns to a thread.  24576 rows of 4096
+// columns: 45 us by itself, 5.3 TB/s.  (Adding in the down product's last CTA of a
+// token instead, found by a counter, was no faster.)
 constexpr int kJoinThreads = 256;
 
 __global__ void __launch_bounds__(kJoinThreads) w4_join_kernel(const uint4* part,
@@ -1319,8 +1354,8 @@ __global__ void __launch_bounds__(kJoinThreads) w4_join_kernel(const uint4* part
   part += c;
   part_sf += (c >> 2) * R;
   float2 y[4] = {};
-  // (Two at a time: the other warps hide the rest, and more in flight a thread
-  // measured slower.)
+  // (Two at a time: the other warps hide the rest; 4096 tokens over 64 experts 365 us
+  // at the time, four at a time 368, eight 377.)
 #pragma unroll 2
   for (int j = 0; j < k; ++j) {
     const int row = pos[j];
@@ -1626,8 +1661,8 @@ int expert_tile(int64_t R, int k, int E) {
 // An expert of c rows has ceil(c / nt) tiles at most (fewer where even tiles
 // round up to 16), that is c / nt and one more if it has any.
 int64_t most_tiles(int64_t R, int E, int nt) { return R / nt + (R < E ? R : E); }
-// Whether the rows are laid out by expert first: an indexed copy of four rows
-// takes as long as a plain one of a whole tile (see w4_rows_kernel).
+// Whether the rows are laid out by expert first (see w4_rows_kernel); up to 32 tokens
+// it made no difference, and the launch and the workspace are saved.
 bool lays_out_rows(int nt) { return nt > 32; }
 }  // namespace
 
