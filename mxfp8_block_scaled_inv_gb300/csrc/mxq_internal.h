@@ -147,7 +147,7 @@ cudaError_t launch_prepare_w4(const uint8_t* w, const uint8_t* sf, int64_t B, in
 cudaError_t launch_linear_a8w4(const uint8_t* a, const uint8_t* a_sf, const uint8_t* w, void* out,
                                int64_t T, int N, int K, int num_sms, cudaStream_t s,
                                const char** why);
-// Workspace of launch_experts_a8w4: the numbers of tiles and rows, the tiles, the
+// Workspace of launch_experts_a8w4: the number of tiles, the tiles, the
 // sorted rows' indices and their inverse, the rows themselves (for large tiles),
 // the activation between the two products (codes and scales) and the results to
 // sum (16 bits each, and exponents), all by sorted row.

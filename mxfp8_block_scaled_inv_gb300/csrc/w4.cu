@@ -1248,13 +1248,12 @@ __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* id
   }
   if (lane == 31) wsum[warp] = sc;
   // The largest tiles come first: CTAs take units in order, so the last round,
-  // which is seldom full, is one of small ones.  An expert's tiles but the last
-  // are of one size and stay together.
-  const int last = c - (nt_e - 1) * rows, full16 = rows / 16, last16 = (last + 15) / 16;
+  // which is seldom full, is one of small ones.  An expert's tiles stay together, so
+  // that its weights come from HBM once (the last tile may be smaller than the others).
+  const int full16 = rows / 16;
   if (tid < kSizes) size_n[tid] = 0;
   __syncthreads();
-  if (nt_e > 1) atomicAdd(&size_n[full16], nt_e - 1);
-  if (nt_e > 0) atomicAdd(&size_n[last16], 1);
+  if (nt_e > 0) atomicAdd(&size_n[full16], nt_e);
   __syncthreads();
   int pc = 0;
   for (int w = 0; w < warp; ++w) pc += wsum[w];
@@ -1265,25 +1264,19 @@ __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* id
   }
   const int row0 = pc + sc - c;
   if (tid < E) cur[tid] = row0 + earlier;
-  if (rank == 0 && tid == kPlanThreads - 1) n_tiles[1] = pc + sc;
   __syncthreads();
   if (rank == 0) {
-    if (tid == 0) n_tiles[0] = size_at[0] + size_n[0];
+    if (tid == 0) *n_tiles = size_at[0] + size_n[0];
     Tile t;
     t.expert = tid;
     t.pairs = nt_e == 1 ? 1u : 0u;
-    if (nt_e > 1) {
-      const int at = atomicAdd(&size_at[full16], nt_e - 1);
-      t.count = rows;
-      for (int i = 0; i < nt_e - 1; ++i) {
+    if (nt_e > 0) {
+      const int at = atomicAdd(&size_at[full16], nt_e);
+      for (int i = 0; i < nt_e; ++i) {
         t.row0 = row0 + i * rows;
+        t.count = min(rows, c - i * rows);
         tiles[at + i] = t;
       }
-    }
-    if (nt_e > 0) {
-      t.row0 = row0 + (nt_e - 1) * rows;
-      t.count = last;
-      tiles[atomicAdd(&size_at[last16], 1)] = t;
     }
   }
   ptx::cluster_sync();  // (also: nobody reads this CTA's counts any more)
@@ -1306,31 +1299,36 @@ __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* id
   }
 }
 
-// The activation rows laid out by expert (one warp for each), for the plain
-// copies of large tiles: every 128 weight rows read a tile's tokens anew, and a
-// copy by index moves four rows (in 44 ns) where a plain one moves a box of them:
-// gate and up of 4096 tokens over 64 experts 562 us by index in tiles of 128; 149 with
-// rows laid out, which takes 20.
+// The activation rows laid out by expert, for the plain copies of large tiles: every
+// 128 weight rows read a tile's tokens anew, and a copy by index moves four rows (in
+// 44 ns) where a plain one moves a box of them: gate and up of 4096 tokens over 64 experts
+// 562 us by index in tiles of 128; 150 with rows laid out, which takes TODO.  A
+// warp reads 2 KB of a token's row once and writes it to each of the row's places.
 constexpr int kRowWarps = 8;
+constexpr int kRowChunks = 128;  // of 16 bytes, of a warp
 
-__global__ void __launch_bounds__(kRowWarps * 32) w4_rows_kernel(const uint4* a, const int32_t* perm,
-                                                                 const int32_t* n_tiles, int k,
+__global__ void __launch_bounds__(kRowWarps * 32) w4_rows_kernel(const uint4* a, const int32_t* pos,
+                                                                 int64_t items, int parts, int k,
                                                                  int chunks, uint4* out) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int r = blockIdx.x * kRowWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (r >= n_tiles[1]) return;  // the number of sorted rows
-  const uint4* src = a + (size_t)(perm[r] / k) * chunks;
-  uint4* dst = out + (size_t)r * chunks;
-  int c = lane;
-  for (; c + 96 < chunks; c += 128) {
-    const uint4 v0 = src[c], v1 = src[c + 32], v2 = src[c + 64], v3 = src[c + 96];
-    dst[c] = v0;
-    dst[c + 32] = v1;
-    dst[c + 64] = v2;
-    dst[c + 96] = v3;
+  const int64_t it = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (it >= items) return;
+  const int64_t t = it / parts;
+  const int c0 = (int)(it - t * parts) * kRowChunks + lane;
+  uint4 v[kRowChunks / 32];
+#pragma unroll
+  for (int i = 0; i < kRowChunks / 32; ++i)
+    if (c0 + 32 * i < chunks) v[i] = a[(size_t)t * chunks + c0 + 32 * i];
+  const int mine = lane < k ? pos[t * k + lane] : -1;  // (k is 32 at most)
+  for (int j = 0; j < k; ++j) {
+    const int row = __shfl_sync(0xffffffffu, mine, j);
+    if (row < 0) continue;
+#pragma unroll
+    for (int i = 0; i < kRowChunks / 32; ++i)
+      if (c0 + 32 * i < chunks) out[(size_t)row * chunks + c0 + 32 * i] = v[i];
   }
-  for (; c < chunks; c += 32) dst[c] = src[c];
 }
 
 // out[t] = weighted sum over the token's choices, in their order, of the 16-bit
@@ -1670,7 +1668,7 @@ ExpertsLayout experts_layout(int64_t T, int k, int E, int K, int I, int N) {
   const int64_t R = T * k;
   const int nt = expert_tile(R, k, E);
   ExpertsLayout l;
-  l.tiles = 256;  // the numbers of tiles and of rows lie before them
+  l.tiles = 256;  // their number lies before them
   l.perm = l.tiles + round_up_256((size_t)most_tiles(R, E, nt) * sizeof(Tile));
   l.pos = l.perm + round_up_256((size_t)R * 4);
   l.rows = l.pos + round_up_256((size_t)R * 4);
@@ -1734,10 +1732,12 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   const uint8_t* rows = a;
   int64_t n_rows = T;
   if (lays_out_rows(nt)) {
-    cfg.gridDim = dim3((unsigned)ceil_div(R, kRowWarps), 1, 1);
+    const int chunks = K / 16, parts = (int)ceil_div(chunks, kRowChunks);
+    cfg.gridDim = dim3((unsigned)ceil_div(T * parts, kRowWarps), 1, 1);
     cfg.blockDim = dim3(kRowWarps * 32, 1, 1);
-    e = cudaLaunchKernelEx(&cfg, w4_rows_kernel, reinterpret_cast<const uint4*>(a), perm, n_tiles, k,
-                           K / 16, reinterpret_cast<uint4*>(base + l.rows));
+    e = cudaLaunchKernelEx(&cfg, w4_rows_kernel, reinterpret_cast<const uint4*>(a),
+                           static_cast<const int32_t*>(pos), T * parts, parts, k, chunks,
+                           reinterpret_cast<uint4*>(base + l.rows));
     if (e != cudaSuccess) return e;
     rows = base + l.rows;
     n_rows = R;
