@@ -1335,32 +1335,36 @@ __global__ void __launch_bounds__(kRowWarps * 32) w4_rows_kernel(const uint4* a,
 // results that the down product left; eight columns to a thread.  24576 rows of 4096
 // columns: 45 us by itself, 5.3 TB/s.  (Adding in the down product's last CTA of a
 // token instead, found by a counter, was no faster.)
-constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = 8;
 
-__global__ void __launch_bounds__(kJoinThreads) w4_join_kernel(const uint4* part,
-                                                               const uint8_t* part_sf,
-                                                               const int32_t* pos, const float* wt,
-                                                               uint4* out, uint32_t items,
-                                                               uint32_t chunks, int k, int64_t R) {
+// One warp: 256 columns of a token.  The lanes fetch the token's rows and weights at
+// once and pass them round, so that the results' loads wait for nothing else.
+__global__ void __launch_bounds__(kJoinWarps * 32) w4_join_kernel(const uint4* part, const uint8_t* part_sf,
+                                                                  const int32_t* pos, const float* wt,
+                                                                  uint4* out, int64_t items, int segs,
+                                                                  int chunks, int k, int64_t R) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const uint32_t it = blockIdx.x * kJoinThreads + threadIdx.x;
+  const int64_t it = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
   if (it >= items) return;
-  const uint32_t t = it / chunks, c = it - t * chunks;
-  pos += (size_t)t * k;
-  wt += (size_t)t * k;
-  part += c;
-  part_sf += (c >> 2) * R;
+  const int64_t t = it / segs;
+  const int c = (int)(it - t * segs) * 32 + lane;
+  const int my_row = lane < k ? pos[t * k + lane] : -1;  // (k is 32 at most)
+  const float my_weight = lane < k ? wt[t * k + lane] : 0.0f;
+  const bool in = c < chunks;
+  part += in ? c : 0;
+  part_sf += (size_t)((in ? c : 0) >> 2) * (size_t)R;
   float2 y[4] = {};
-  // (Two at a time: the other warps hide the rest; 4096 tokens over 64 experts 365 us
-  // at the time, four at a time 368, eight 377.)
 #pragma unroll 2
   for (int j = 0; j < k; ++j) {
-    const int row = pos[j];
-    if (row >= 0) add_held16(y, part[(size_t)row * chunks], part_sf[row], wt[j]);
+    const int row = __shfl_sync(0xffffffffu, my_row, j);
+    const float weight = __shfl_sync(0xffffffffu, my_weight, j);
+    if (row >= 0) add_held16(y, part[(size_t)row * chunks], part_sf[row], weight);
   }
-  out[it] = make_uint4(pack2(y[0].x, y[0].y), pack2(y[1].x, y[1].y), pack2(y[2].x, y[2].y),
-                       pack2(y[3].x, y[3].y));
+  if (in)
+    out[t * chunks + c] = make_uint4(pack2(y[0].x, y[0].y), pack2(y[1].x, y[1].y),
+                                     pack2(y[2].x, y[2].y), pack2(y[3].x, y[3].y));
 }
 
 // Codes and scales of B matrices [N][K] into blocks; one thread per 16 bytes.
@@ -1786,12 +1790,13 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   e = launch_tokens<kDown>(nt, base + l.h, (uint64_t)R, (uint64_t)I, (uint64_t)E * g.NB * g.KB, g,
                            units, num_sms, s, why);
   if (e != cudaSuccess || small) return e;
-  const uint32_t chunks = (uint32_t)(N / 8), items = (uint32_t)T * chunks;
-  cfg.gridDim = dim3((unsigned)ceil_div(items, kJoinThreads), 1, 1);
-  cfg.blockDim = dim3(kJoinThreads, 1, 1);
+  const int chunks = N / 8, segs = (int)ceil_div(chunks, 32);
+  cfg.gridDim = dim3((unsigned)ceil_div(T * segs, kJoinWarps), 1, 1);
+  cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
   return cudaLaunchKernelEx(&cfg, w4_join_kernel, reinterpret_cast<const uint4*>(base + l.part),
-                            reinterpret_cast<const uint8_t*>(base + l.part_sf), pos, wt,
-                            static_cast<uint4*>(out), items, chunks, k, R);
+                            reinterpret_cast<const uint8_t*>(base + l.part_sf),
+                            static_cast<const int32_t*>(pos), wt, static_cast<uint4*>(out), T * segs, segs,
+                            chunks, k, R);
 }
 
 }  // namespace mxq
