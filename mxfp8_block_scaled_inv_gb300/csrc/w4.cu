@@ -64,12 +64,12 @@
 //   64 tokens, 128 experts      127 us (0.98): HBM
 //   1 token, 8 of 128           20 us (0.38): two kernels of 35 and 18 MB, each with the
 //                               latencies of the first case
-//   4096 tokens, 64 experts     336 us (0.49): gate and up 149 us (tensor pipe 63 %
+//   4096 tokens, 64 experts     323 us (0.51): gate and up 147 us (tensor pipe 64 %
 //                               active; one accumulator, so that the epilogue's fetches
 //                               wait for the products and the other way round; without
-//                               any arithmetic or store in it 131), down 113 (copies
-//                               from L2 and 16-bit stores at once), the sum 45 and the
-//                               rows 20 (both memory), the plan 9
+//                               any arithmetic or store in it 18 less), down 101 (copies
+//                               from L2 and 16-bit stores at once), the sum 40 and the
+//                               rows 17 (both memory), the plan 8
 //
 // Every wait is bounded in wall time; on expiry the kernel sets a watchdog bit,
 // stops issuing, waits for its own copies and MMAs, frees TMEM and returns.
@@ -126,7 +126,7 @@ struct W4Args {
   const int32_t* n_tiles;
   const int32_t* perm;    // sorted row -> token * k + choice
   void* out;              // kLinear: BF16 [T][N]; kGateUp: codes [rows][N]; kDown: int16 [rows][N]
-  uint8_t* out_sf;        // kGateUp: [rows][NG]; kDown: exponents [N / 32][NG rows]
+  uint8_t* out_sf;        // kGateUp: [rows][NG]; kDown: exponents [NB][NG rows][4]
   uint32_t* wd;           // watchdog word
   uint32_t wait_ns;       // bound on a wait
   int T, N, KG, KB, NB, NG, k;
@@ -377,10 +377,12 @@ __device__ __forceinline__ void finish_chunk(const W4Args& p, float (&v)[NA][kCh
       for (int i = 0; i < kChunk; ++i)
         if (in && i < live) o[(size_t)i * p.N] = (uint16_t)held16(v[0][i], m[i]);
     }
-    // (By column block first: a row's bytes of all blocks lie far apart, and single
-    // bytes to lines that nobody else writes cost as much as all the rest.)
+    // (By row block first: a row's bytes of all blocks lie far apart, and single bytes
+    // to lines that nobody else writes cost as much as all the rest.  The four of a
+    // block side by side: the sum fetches them as one, 4096 tokens over 64 experts 323
+    // us, and 328 with [N / 32][rows].)
     if (lane < min(live, kChunk) && rb * 128 + q * 32 < p.N)
-      p.out_sf[(size_t)(rb * 4 + q) * p.NG + row + lane] = held16_exp(mine);
+      p.out_sf[((size_t)rb * p.NG + row + lane) * 4 + q] = held16_exp(mine);
   }
 }
 
@@ -419,7 +421,7 @@ __device__ __forceinline__ void finish_token(const W4Args& p, const float (&v)[N
     if (store) {
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (size_t)row * p.N + n) =
           make_uint4(w[0], w[1], w[2], w[3]);
-      if ((sub & 3) == 0) p.out_sf[(size_t)(n >> 5) * p.NG + row] = held16_exp(m);
+      if ((sub & 3) == 0) p.out_sf[((size_t)rb * p.NG + row) * 4 + (sub >> 2)] = held16_exp(m);
     }
   }
 }
@@ -1302,7 +1304,7 @@ __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* id
 // The activation rows laid out by expert, for the plain copies of large tiles: every
 // 128 weight rows read a tile's tokens anew, and a copy by index moves four rows (in
 // 44 ns) where a plain one moves a box of them: gate and up of 4096 tokens over 64 experts
-// 562 us by index in tiles of 128; 150 with rows laid out, which takes TODO.  A
+// 562 us by index in tiles of 128; 147 with rows laid out, which takes 17 (and 20 where each place fetched its row anew).  A
 // warp reads 2 KB of a token's row once and writes it to each of the row's places.
 constexpr int kRowWarps = 8;
 constexpr int kRowChunks = 128;  // of 16 bytes, of a warp
@@ -1333,8 +1335,9 @@ __global__ void __launch_bounds__(kRowWarps * 32) w4_rows_kernel(const uint4* a,
 
 // out[t] = weighted sum over the token's choices, in their order, of the 16-bit
 // results that the down product left; eight columns to a thread.  24576 rows of 4096
-// columns: 45 us by itself, 5.3 TB/s.  (Adding in the down product's last CTA of a
-// token instead, found by a counter, was no faster.)
+// columns: 47 us by itself with each thread on its own, 5 TB/s; by warps the call takes
+// 329 us and not 333.  (Adding in the down product's last CTA of a token instead,
+// found by a counter, was no faster.)
 constexpr int kJoinWarps = 8;
 
 // One warp: 256 columns of a token.  The lanes fetch the token's rows and weights at
@@ -1354,13 +1357,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) w4_join_kernel(const uint4* p
   const float my_weight = lane < k ? wt[t * k + lane] : 0.0f;
   const bool in = c < chunks;
   part += in ? c : 0;
-  part_sf += (size_t)((in ? c : 0) >> 2) * (size_t)R;
+  part_sf += (size_t)((in ? c : 0) >> 4) * (size_t)R * 4 + (((in ? c : 0) >> 2) & 3);
   float2 y[4] = {};
 #pragma unroll 2
   for (int j = 0; j < k; ++j) {
     const int row = __shfl_sync(0xffffffffu, my_row, j);
     const float weight = __shfl_sync(0xffffffffu, my_weight, j);
-    if (row >= 0) add_held16(y, part[(size_t)row * chunks], part_sf[row], weight);
+    if (row >= 0) add_held16(y, part[(size_t)row * chunks], part_sf[(size_t)row * 4], weight);
   }
   if (in)
     out[t * chunks + c] = make_uint4(pack2(y[0].x, y[0].y), pack2(y[1].x, y[1].y),
@@ -1680,7 +1683,7 @@ ExpertsLayout experts_layout(int64_t T, int k, int E, int K, int I, int N) {
   l.h_sf = l.h + round_up_256((size_t)R * I);
   l.part = l.h_sf + round_up_256((size_t)R * (size_t)ceil_div(I, kGroup));
   l.part_sf = l.part + round_up_256((size_t)R * N * 2);
-  l.total = l.part_sf + round_up_256((size_t)R * (size_t)ceil_div(N, 32));
+  l.total = l.part_sf + round_up_256((size_t)R * (size_t)ceil_div(N, 128) * 4);
   return l;
 }
 
