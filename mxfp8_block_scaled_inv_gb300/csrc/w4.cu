@@ -67,9 +67,9 @@
 //   4096 tokens, 64 experts     323 us (0.51): gate and up 147 us (tensor pipe 64 %
 //                               active; one accumulator, so that the epilogue's fetches
 //                               wait for the products and the other way round; without
-//                               any arithmetic or store in it 18 less), down 101 (copies
-//                               from L2 and 16-bit stores at once), the sum 40 and the
-//                               rows 17 (both memory), the plan 8
+//                               any arithmetic or store in it 18 less), down 103 (copies
+//                               from L2 and 16-bit stores at once), the sum 46 and the
+//                               rows 18 (both memory), the plan 9, each on cold caches
 //
 // Every wait is bounded in wall time; on expiry the kernel sets a watchdog bit,
 // stops issuing, waits for its own copies and MMAs, frees TMEM and returns.
@@ -1304,7 +1304,7 @@ __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* id
 // The activation rows laid out by expert, for the plain copies of large tiles: every
 // 128 weight rows read a tile's tokens anew, and a copy by index moves four rows (in
 // 44 ns) where a plain one moves a box of them: gate and up of 4096 tokens over 64 experts
-// 562 us by index in tiles of 128; 147 with rows laid out, which takes 17 (and 20 where each place fetched its row anew).  A
+// 562 us by index in tiles of 128; 147 with rows laid out, which takes 18 (20 where each place fetched its row anew).  A
 // warp reads 2 KB of a token's row once and writes it to each of the row's places.
 constexpr int kRowWarps = 8;
 constexpr int kRowChunks = 128;  // of 16 bytes, of a warp
