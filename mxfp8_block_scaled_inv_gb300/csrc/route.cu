@@ -55,10 +55,12 @@ struct RouteArgs {
   float scale;
 };
 
-// Order-preserving 32-bit key of a finite fp32 value; never 0.
+// Order-preserving 32-bit key of an fp32 value that is no NaN; that of -infinity,
+// kNone, and what lies below stand for an expert that is not to be chosen.
+constexpr uint32_t kNone = 0x007fffffu;
 __device__ __forceinline__ uint32_t key_of(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);  // -0 becomes 0
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return u ^ (0x80000000u | (uint32_t)((int32_t)u >> 31));
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
@@ -85,10 +87,10 @@ __device__ __forceinline__ float load_logit(const RouteArgs& a, int64_t t, int e
 }
 // Masked logits (-infinity, NaN) read -infinity, +infinity the largest number.
 __device__ __forceinline__ float clean_logit(float l) {
-  return l > -INFINITY ? fminf(l, 3.4028234e38f) : -INFINITY;
+  return fminf(fmaxf(l, -INFINITY), 3.4028234e38f);
 }
 __device__ __forceinline__ float clean_bias(float b) {
-  return b > -INFINITY ? fminf(b, 1e30f) : -INFINITY;
+  return fminf(fmaxf(b, -INFINITY), 1e30f);
 }
 
 template <typename R>
@@ -338,11 +340,10 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER == 16 ? 6 : 4)
   // The row's largest logit bounds the scores; the softmax needs it anyway.
   float mx = -INFINITY, inv_z = 1.0f, pmax = 1.0f;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    l[i] = clean_logit(l[i]);
-    mx = fmaxf(mx, l[i]);
-  }
+  for (int i = 0; i < PER; ++i) l[i] = clean_logit(l[i]);
   if (a.scoring != MXQ_SCORE_SIGMOID) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) mx = fmaxf(mx, l[i]);
     const uint32_t top = __reduce_max_sync(kAll, mx == -INFINITY ? 0u : key_of(mx));
     mx = top == 0u ? 0.0f : value_of(top);
     if (a.scoring == MXQ_SCORE_SOFTMAX) {
@@ -361,12 +362,11 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER == 16 ? 6 : 4)
                               : a.scoring == MXQ_SCORE_SOFTMAX ? 6e-6f
                                                                : 2.5e-6f);
   bool whole = false;  // the row needs 64 bits altogether
-  uint32_t key[PER];   // order of the lane's experts; 0: not to be chosen
-  if (!biased && !grouped) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) key[i] = l[i] > -INFINITY ? key_of(l[i]) : 0u;
-  } else {
-    float c[PER];
+  // Order of the lane's experts.
+  uint32_t key[PER];
+  const bool spread = grouped && a.lanes == 0;  // groups begin or end inside a lane
+  float c[PER];
+  if (biased || spread) {
     // (One loop for each score: a choice inside it is made once for each value.)
     if (a.scoring == MXQ_SCORE_SIGMOID) {
 #pragma unroll
@@ -380,79 +380,66 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER == 16 ? 6 : 4)
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) c[i] = l[i] > -INFINITY ? c[i] + clean_bias(b[i]) : -INFINITY;
-    uint32_t in = 0xffffffffu;  // bit i: the group of expert i is kept
-    if (grouped) {
-      float v = -INFINITY;  // a group's value
-      float a1 = -INFINITY, a2 = -INFINITY;
-      int g;
-      if (a.lanes > 0) {
-        // A group is a run of 2^n lanes.
+  }
+  if (biased) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
+    for (int i = 0; i < PER; ++i) key[i] = key_of(c[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) key[i] = key_of(l[i]);
+  }
+  // Which groups stay: v is the value of group g, a1 and a2 its best, `step` the lanes
+  // of a group.  True where lane's group stays.
+  auto group_kept = [&](float v, int g, float a1, float a2, int step) {
+    int rank = 0;  // the lanes of a group share the comparisons
+    for (int i = 0; i < a.groups; i += step) {
+      const int q = i + (lane & (step - 1));
+      const float o = __shfl_sync(kAll, v, (q * step) & 31);
+      rank += q < a.groups && (o > v || (o == v && q < g)) ? 1 : 0;
+    }
+    for (int m = 1; m < step; m <<= 1) rank += __shfl_xor_sync(kAll, rank, m);
+    bool kept = rank < a.keep;
+    const uint32_t vkey = g < a.groups && v > -INFINITY ? key_of(v) : 0u;
+    const uint32_t low = __reduce_min_sync(kAll, kept && g < a.groups ? vkey : 0xffffffffu);
+    const uint32_t high = __reduce_max_sync(kAll, kept ? 0u : vkey);
+    if (low != 0u && high != 0u) {
+      const float x = value_of(low), y = value_of(high);
+      const float edge = 2.0f * slack + 2.5e-7f * (fabsf(x) + fabsf(y));
+      if (!(x - y > edge)) {
+        bool sure = false;  // (groups that do not lie on lanes: the whole row)
+        const bool two = a.group_top == 2 && a2 > -INFINITY;
+        if (a.lanes > 0)
+          kept = keep_group_64(a, t, BF16, lane, PER, mx, inv_z, v, g, x, y, edge,
+                               (two ? a2 : a1) - edge, two ? 2 : 1, &sure);
+        whole = !sure;
+      }
+    }
+    return kept;
+  };
+  if (spread) {
+    float v = -INFINITY;
+    for (int q = 0; q < a.groups; ++q) {
+      float a1 = -INFINITY, a2 = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int at = e0 + i - q * a.per_group;
+        if (at >= 0 && at < a.per_group) {
           a2 = fmaxf(a2, fminf(a1, c[i]));
           a1 = fmaxf(a1, c[i]);
         }
-        for (int m = 1; m < a.lanes; m <<= 1) {
-          const float o1 = __shfl_xor_sync(kAll, a1, m), o2 = __shfl_xor_sync(kAll, a2, m);
-          merge2(a1, a2, o1, o2);
-        }
-        v = a.group_top == 2 && a2 > -INFINITY ? a1 + a2 : a1;
-        g = lane / a.lanes;
-      } else {
-        // Groups that begin or end inside a lane: one after the other.
-        for (int q = 0; q < a.groups; ++q) {
-          a1 = a2 = -INFINITY;
+      }
 #pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const int at = e0 + i - q * a.per_group;
-            if (at >= 0 && at < a.per_group) {
-              a2 = fmaxf(a2, fminf(a1, c[i]));
-              a1 = fmaxf(a1, c[i]);
-            }
-          }
-#pragma unroll
-          for (int m = 16; m > 0; m >>= 1) {
-            const float o1 = __shfl_xor_sync(kAll, a1, m), o2 = __shfl_xor_sync(kAll, a2, m);
-            merge2(a1, a2, o1, o2);
-          }
-          if (lane == q) v = a.group_top == 2 && a2 > -INFINITY ? a1 + a2 : a1;
-        }
-        g = lane;
+      for (int m = 16; m > 0; m >>= 1) {
+        const float o1 = __shfl_xor_sync(kAll, a1, m), o2 = __shfl_xor_sync(kAll, a2, m);
+        merge2(a1, a2, o1, o2);
       }
-      const int step = a.lanes > 0 ? a.lanes : 1;
-      int rank = 0;
-      for (int q = 0; q < a.groups; ++q) {
-        const float o = __shfl_sync(kAll, v, q * step);
-        rank += o > v || (o == v && q < g) ? 1 : 0;
-      }
-      bool kept = rank < a.keep;
-      const uint32_t vkey = g < a.groups && v > -INFINITY ? key_of(v) : 0u;
-      const uint32_t low = __reduce_min_sync(kAll, kept && g < a.groups ? vkey : 0xffffffffu);
-      const uint32_t high = __reduce_max_sync(kAll, kept ? 0u : vkey);
-      if (low != 0u && high != 0u) {
-        const float x = value_of(low), y = value_of(high);
-        const float edge = 2.0f * slack + 2.5e-7f * (fabsf(x) + fabsf(y));
-        if (!(x - y > edge)) {
-          bool sure = false;  // (groups that do not lie on lanes: the whole row)
-          const bool two = a.group_top == 2 && a2 > -INFINITY;
-          if (a.lanes > 0)
-            kept = keep_group_64(a, t, BF16, lane, PER, mx, inv_z, v, g, x, y, edge,
-                                 (two ? a2 : a1) - edge, two ? 2 : 1, &sure);
-          whole = !sure;
-        }
-      }
-      if (a.lanes > 0) {
-        in = kept ? 0xffffffffu : 0u;
-      } else {
-        const uint32_t mask = __ballot_sync(kAll, kept && lane < a.groups);
-        in = 0u;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) in |= ((mask >> (min(e0 + i, a.E - 1) / a.per_group)) & 1u) << i;
-      }
+      if (lane == q) v = a.group_top == 2 && a2 > -INFINITY ? a1 + a2 : a1;
     }
+    const uint32_t mask =
+        __ballot_sync(kAll, group_kept(v, lane, -INFINITY, -INFINITY, 1) && lane < a.groups);
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      key[i] = c[i] > -INFINITY && ((in >> i) & 1u) ? key_of(biased ? c[i] : l[i]) : 0u;
+      if (!((mask >> (min(e0 + i, a.E - 1) / a.per_group)) & 1u)) key[i] = 0u;
   }
   // Each lane's keys in order, so that a pick is their head; which expert the
   // key belongs to is looked up for all picks at once afterwards.
@@ -460,28 +447,42 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER == 16 ? 6 : 4)
 #pragma unroll
   for (int i = 0; i < PER; ++i) head[i] = key[i];
   if constexpr (PER > 1) sort_pass<PER, 1, 1>(head);
+  if (grouped && !spread) {
+    // A group is a run of 2^n lanes, whose two best are among theirs.
+    auto value = [&](uint32_t k) {
+      if (k <= kNone) return -INFINITY;
+      return biased ? value_of(k) : score_of(a.scoring, value_of(k), mx, inv_z);
+    };
+    float a1 = value(head[0]), a2 = PER > 1 ? value(head[PER > 1 ? 1 : 0]) : -INFINITY;
+    for (int m = 1; m < a.lanes; m <<= 1) {
+      const float o1 = __shfl_xor_sync(kAll, a1, m), o2 = __shfl_xor_sync(kAll, a2, m);
+      merge2(a1, a2, o1, o2);
+    }
+    const float v = a.group_top == 2 && a2 > -INFINITY ? a1 + a2 : a1;
+    if (!group_kept(v, lane / a.lanes, a1, a2, a.lanes)) head[0] = 0u;  // hides the others
+  }
   int expert = -1, picks = 0;
-  uint32_t my_key = 0u;  // of this lane's pick, and the lane that holds it
-  int my_lane = 0;
+  uint32_t my_key = 0u, my_from = 0u;  // this lane's pick, and the bit of the lane that holds it
   float cj = 0.0f;
   // Takes the next expert into lane `picks`; false where none is left.
   auto pick = [&]() {
     const uint32_t top = __reduce_max_sync(kAll, head[0]);
-    if (top == 0u) return false;
-    const int w = __ffs(__ballot_sync(kAll, head[0] == top)) - 1;
-    if (lane == w) {
+    if (top <= kNone) return false;
+    const uint32_t at = __ballot_sync(kAll, head[0] == top), first = at & (0u - at);
+    if (first == 1u << lane) {
 #pragma unroll
       for (int i = 0; i + 1 < PER; ++i) head[i] = head[i + 1];
       head[PER - 1] = 0u;
     }
     if (lane == picks) {
       my_key = top;
-      my_lane = w;
+      my_from = first;
     }
     ++picks;
     return true;
   };
   auto look_up = [&]() {
+    const int my_lane = my_from != 0u ? __ffs(my_from) - 1 : 0;
     cj = my_key != 0u ? value_of(my_key) : 0.0f;
     uint32_t m = 0u;
 #pragma unroll
@@ -489,8 +490,8 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER == 16 ? 6 : 4)
       m |= (__shfl_sync(kAll, key[i], my_lane) == my_key ? 1u : 0u) << i;
     // Equal keys of one lane are picked one behind the other.
     const uint32_t prev = __shfl_up_sync(kAll, my_key, 1);
-    const int prev_lane = __shfl_up_sync(kAll, my_lane, 1);
-    const bool again = lane > 0 && prev == my_key && prev_lane == my_lane && my_key != 0u;
+    const uint32_t prev_from = __shfl_up_sync(kAll, my_from, 1);
+    const bool again = lane > 0 && prev == my_key && prev_from == my_from && my_key != 0u;
     const uint32_t run = __ballot_sync(kAll, again);
     if (again) {
       // Length of the run of `again` that ends here.
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER == 16 ? 6 : 4)
   // Whether the last pick is too near to the best expert that is left.
   auto near_rest = [&]() {
     const uint32_t rest = __reduce_max_sync(kAll, head[0]);
-    return rest != 0u && near(__shfl_sync(kAll, cj, picks - 1), value_of(rest));
+    return rest > kNone && near(__shfl_sync(kAll, cj, picks - 1), value_of(rest));
   };
   if (biased && picks == 32) whole |= near_rest();
   if (biased && !whole) {
