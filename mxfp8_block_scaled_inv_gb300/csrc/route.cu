@@ -6,12 +6,13 @@
 // `keep` largest stay; the experts are the k largest c of those, ties going to
 // the lowest index; w_j = scale * p_j (/ (sum p + 1e-20)).
 //
-// A warp takes a token; lane i holds the experts [i * PER, (i + 1) * PER), so
-// that lane order is index order, the lowest lane of a tie holds the lowest
-// index, and groups are runs of lanes (their two best are found by a butterfly
-// over the run).  Each pick is one warp-wide integer maximum over
-// order-preserving keys, one ballot, and a new maximum in the lane that lost an
-// expert; lane j keeps pick j and computes its weight.
+// A warp takes a token; lane i holds up to PER neighbouring experts, so that lane
+// order is index order, the lowest lane of a tie holds the lowest index, and
+// groups (a power of two of them) are runs of lanes, whose two best are found by a
+// butterfly over the run.  A lane's order-preserving keys are sorted by a network.
+// Each pick is one warp-wide integer maximum of the lanes' first keys, one ballot,
+// and a step on in the lane that lost an expert; lane j keeps pick j and computes
+// its weight.
 //
 // What is chosen is defined by 64-bit scores: fp32 scores order two experts
 // wrongly where they differ by less than their rounding.  So one pick more than
@@ -52,7 +53,13 @@ struct RouteArgs {
   float* weights;
   int64_t T;
   int E, k, scoring, groups, keep, group_top, renorm, per_group, vec, bias_vec, lanes;
+  // Lane i holds up to `count` experts from run (i >> run_log) * run_len on, at
+  // (i mod 2^run_log) * count in the run: a run is a group, or the whole row.
+  int run_log, run_len, count;
   float scale;
+  __device__ __forceinline__ int base(int lane) const {
+    return (lane >> run_log) * run_len + (lane & ((1 << run_log) - 1)) * count;
+  }
 };
 
 // Order-preserving 32-bit key of an fp32 value that is no NaN; that of -infinity,
@@ -245,7 +252,7 @@ __device__ __noinline__ double row_sum_64(const RouteArgs& a, int64_t t, bool bf
 // sums of their n best (those with an fp32 value of `least` and more), the others stay
 // where they are.  v, g: the lane's group; false in *sure where a group has more
 // than its n best that near to each other.
-__device__ __noinline__ bool keep_group_64(const RouteArgs& a, int64_t t, bool bf16, int lane, int per,
+__device__ __noinline__ bool keep_group_64(const RouteArgs& a, int64_t t, bool bf16, int lane, int per, int n_mine,
                                            float mx, float inv_z, float v, int g, float x, float y,
                                            float edge, float least, int n, bool* sure) {
   const bool close = g < a.groups && v >= y - edge && v <= x + edge;
@@ -254,9 +261,9 @@ __device__ __noinline__ bool keep_group_64(const RouteArgs& a, int64_t t, bool b
   double sum = 0.0;
   int found = 0;
   for (int i = 0; i < per; ++i) {
-    const int e = lane * per + i;
+    const int e = a.base(lane) + i;
     float l = -INFINITY, b = 0.0f;
-    if (close && e < a.E) {
+    if (close && i < n_mine) {
       l = clean_logit(load_logit(a, t, e, bf16));
       if (a.bias != nullptr) b = clean_bias(a.bias[e]);
     }
@@ -286,32 +293,46 @@ __device__ __noinline__ bool keep_group_64(const RouteArgs& a, int64_t t, bool b
 
 // (The bound on registers is what the common path needs; the rare parts, whose calls
 // would otherwise set it, keep more of theirs in memory.)
-template <int PER, bool BF16>
-__global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER == 16 ? 6 : 4) route_kernel(const RouteArgs a) {
+// EVEN: lane i begins at expert i * PER.
+template <int PER, bool BF16, bool EVEN>
+__global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER <= 16 ? 6 : 4) route_kernel(const RouteArgs a) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= a.T) return;
   const bool biased = a.bias != nullptr, grouped = a.keep < a.groups;
-  const int e0 = lane * PER;
+  const int e0 = EVEN ? lane * PER : a.base(lane);
+  // The lane's experts: what is left of its run.
+  const int n = EVEN ? min(PER, a.E - e0)
+                     : min(a.count, a.run_len - (lane & ((1 << a.run_log) - 1)) * a.count);
   float l[PER];
-  if (PER >= (BF16 ? 8 : 4) && a.vec && e0 + PER <= a.E) {
+  if (PER % 4 == 0 && a.vec && n == PER) {
+    const size_t at = (size_t)t * (size_t)a.E + (size_t)e0;
     if constexpr (BF16) {
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.logits) +
-                                                        (size_t)t * (size_t)a.E + (size_t)e0);
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.logits) + at;
+      if constexpr (PER % 8 == 0) {
 #pragma unroll
-      for (int i = 0; i + 8 <= PER; i += 8) {
-        float v[8];
-        unpack8(src[i / 8], v);
+        for (int i = 0; i < PER; i += 8) {
+          float v[8];
+          unpack8(*reinterpret_cast<const uint4*>(src + i), v);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) l[i + q] = v[q];
+          for (int q = 0; q < 8; ++q) l[i + q] = v[q];
+        }
+      } else if constexpr (PER % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < PER; i += 4) {
+          const uint2 v = *reinterpret_cast<const uint2*>(src + i);
+          l[i] = bf16_lo(v.x);
+          l[i + 1] = bf16_hi(v.x);
+          l[i + 2] = bf16_lo(v.y);
+          l[i + 3] = bf16_hi(v.y);
+        }
       }
-    } else {
-      const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) +
-                                                          (size_t)t * (size_t)a.E + (size_t)e0);
+    } else if constexpr (PER % 4 == 0) {
+      const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + at);
 #pragma unroll
-      for (int i = 0; i + 4 <= PER; i += 4) {
+      for (int i = 0; i < PER; i += 4) {
         const float4 v = src[i / 4];
         l[i] = v.x;
         l[i + 1] = v.y;
@@ -321,10 +342,10 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER == 16 ? 6 : 4)
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) l[i] = e0 + i < a.E ? load_logit(a, t, e0 + i, BF16) : -INFINITY;
+    for (int i = 0; i < PER; ++i) l[i] = i < n ? load_logit(a, t, e0 + i, BF16) : -INFINITY;
   }
   float b[PER];
-  if (biased && PER >= 4 && a.bias_vec && e0 + PER <= a.E) {
+  if (PER % 4 == 0 && biased && a.bias_vec && n == PER) {
 #pragma unroll
     for (int i = 0; i + 4 <= PER; i += 4) {
       const float4 v = __ldg(reinterpret_cast<const float4*>(a.bias + e0 + i));
@@ -335,7 +356,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER == 16 ? 6 : 4)
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) b[i] = biased && e0 + i < a.E ? __ldg(a.bias + e0 + i) : 0.0f;
+    for (int i = 0; i < PER; ++i) b[i] = biased && i < n ? __ldg(a.bias + e0 + i) : 0.0f;
   }
   // The row's largest logit bounds the scores; the softmax needs it anyway.
   float mx = -INFINITY, inv_z = 1.0f, pmax = 1.0f;
@@ -409,7 +430,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER == 16 ? 6 : 4)
         bool sure = false;  // (groups that do not lie on lanes: the whole row)
         const bool two = a.group_top == 2 && a2 > -INFINITY;
         if (a.lanes > 0)
-          kept = keep_group_64(a, t, BF16, lane, PER, mx, inv_z, v, g, x, y, edge,
+          kept = keep_group_64(a, t, BF16, lane, PER, n, mx, inv_z, v, g, x, y, edge,
                                (two ? a2 : a1) - edge, two ? 2 : 1, &sure);
         whole = !sure;
       }
@@ -459,7 +480,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER == 16 ? 6 : 4)
       merge2(a1, a2, o1, o2);
     }
     const float v = a.group_top == 2 && a2 > -INFINITY ? a1 + a2 : a1;
-    if (!group_kept(v, lane / a.lanes, a1, a2, a.lanes)) head[0] = 0u;  // hides the others
+    if (!group_kept(v, lane >> a.run_log, a1, a2, a.lanes)) head[0] = 0u;  // hides the others
   }
   int expert = -1, picks = 0;
   uint32_t my_key = 0u, my_from = 0u;  // this lane's pick, and the bit of the lane that holds it
@@ -498,7 +519,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER == 16 ? 6 : 4)
       const int skip = __clz(~(run << (31 - lane)));
       for (int i = 0; i < skip; ++i) m &= m - 1u;
     }
-    expert = my_key != 0u ? my_lane * PER + __ffs(m) - 1 : -1;
+    expert = my_key != 0u ? (EVEN ? my_lane * PER : a.base(my_lane)) + __ffs(m) - 1 : -1;
   };
   const int want = biased ? a.k + 1 : a.k;
   while (picks < want && picks < 32 && pick()) {
@@ -580,8 +601,11 @@ cudaError_t launch_per(const RouteArgs& a, bool bf16, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return bf16 ? cudaLaunchKernelEx(&cfg, route_kernel<PER, true>, a)
-              : cudaLaunchKernelEx(&cfg, route_kernel<PER, false>, a);
+  if (a.count == PER && (a.run_log == 5 || a.run_len == PER << a.run_log))
+    return bf16 ? cudaLaunchKernelEx(&cfg, route_kernel<PER, true, true>, a)
+                : cudaLaunchKernelEx(&cfg, route_kernel<PER, false, true>, a);
+  return bf16 ? cudaLaunchKernelEx(&cfg, route_kernel<PER, true, false>, a)
+              : cudaLaunchKernelEx(&cfg, route_kernel<PER, false, false>, a);
 }
 
 }  // namespace
@@ -604,19 +628,28 @@ cudaError_t launch_route(const void* logits, bool bf16, int64_t T, int E, const 
   a.renorm = renorm;
   a.per_group = E / groups;
   a.scale = scale;
-  // 16-byte loads of a lane's logits and biases (a bias may begin at any element);
-  // groups of whole lanes, a power of two of them.
-  a.vec = E % 8 == 0;
+  // Groups that are a power of two of them get equal runs of lanes; others are found
+  // by a search of all lanes for each (8192 x 160 in 8 groups 31 us, with runs 14.5).
+  // Room for 12 experts beside 8 and 16: 8192 x 384 17.5 us, and 24.2 with 16.
+  const bool select = keep < groups, runs = select && (groups & (groups - 1)) == 0;
+  a.run_log = 5;
+  while (runs && (32 >> a.run_log) < groups) --a.run_log;
+  a.run_len = runs ? a.per_group : E;
+  a.lanes = runs ? 1 << a.run_log : 0;
+  const int need = (int)ceil_div(a.run_len, 1 << a.run_log);
+  const int per = need <= 2 ? need : need <= 4 ? 4 : need <= 8 ? 8 : need <= 12 ? 12 : need <= 16 ? 16 : 32;
+  // A lane takes all it has room for where a group ends with a lane (vector loads), else
+  // an even share.
+  a.count = a.run_len % per == 0 || !runs ? per : need;
+  // Loads of four and eight logits and four biases (a bias may begin at any element).
+  a.vec = E % 8 == 0 && a.count == per && a.run_len % 4 == 0 && (a.run_len % 8 == 0 || !bf16);
   a.bias_vec = a.vec && (reinterpret_cast<uintptr_t>(bias) & 15u) == 0;
-  int per = 1;
-  while (per * 32 < E) per *= 2;
-  const int lanes = a.per_group % per == 0 ? a.per_group / per : 0;
-  a.lanes = lanes > 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
-  if (E <= 32) return launch_per<1>(a, bf16, s);
-  if (E <= 64) return launch_per<2>(a, bf16, s);
-  if (E <= 128) return launch_per<4>(a, bf16, s);
-  if (E <= 256) return launch_per<8>(a, bf16, s);
-  if (E <= 512) return launch_per<16>(a, bf16, s);
+  if (per == 1) return launch_per<1>(a, bf16, s);
+  if (per == 2) return launch_per<2>(a, bf16, s);
+  if (per == 4) return launch_per<4>(a, bf16, s);
+  if (per == 8) return launch_per<8>(a, bf16, s);
+  if (per == 12) return launch_per<12>(a, bf16, s);
+  if (per == 16) return launch_per<16>(a, bf16, s);
   return launch_per<32>(a, bf16, s);
 }
 

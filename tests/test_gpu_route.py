@@ -161,3 +161,19 @@ def test_bias_that_begins_at_any_element(mxq, E):
         room[at:at + E] = b
         got = mxq.mxq_route(l, 5, scoring="sigmoid", bias=room[at:at + E], groups=8, topk_groups=3)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("T,E,k,groups,keep", [(40, 160, 6, 8, 3), (30, 144, 8, 16, 5), (30, 352, 7, 1, 1), (30, 384, 8, 8, 4),
+                                               (30, 768, 12, 2, 1), (25, 40, 4, 4, 2), (25, 72, 5, 8, 2), (25, 1024, 9, 4, 1),
+                                               (25, 192, 6, 32, 9), (25, 320, 6, 16, 16), (30, 20, 3, 4, 2)])
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+def test_uneven_lanes(mxq, T, E, k, groups, keep, scoring):
+    """Groups that do not fill their lanes, and lanes of up to 12 experts."""
+    l, b = draw(T, E, seed=E + groups)
+    for x in (l, l.bfloat16()):
+        for bias in (None, b):
+            check(mxq, x, bias, k=k, scoring=scoring, groups=groups, topk_groups=keep)
+    room = torch.zeros((E + 1,), device="cuda")
+    room[1:] = b
+    got, want = (mxq.mxq_route(l, k, scoring, bias=v, groups=groups, topk_groups=keep) for v in (room[1:], b))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
