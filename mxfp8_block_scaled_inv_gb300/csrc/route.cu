@@ -27,11 +27,12 @@
 // as long as thousands of others.  Without a bias the experts are ordered by their
 // logits, which is exact.
 //
-// Bound by instructions: 1200 for a row of 256 experts with bias and groups, 63 % of
-// the issue slots, 8 of 16 warps a scheduler.  8192 rows 14.7 us (1.3 us of
-// memory; with unsorted keys, a search through the lane's experts for each
-// pick, 21; with whole rows wherever groups are near 18), without bias and groups
-// 9.9; one row 4.0 us, of which launch and one trip to memory are 2.
+// Bound by instructions: 1020 for a row of 256 experts with bias and groups (sigmoids
+// 7 % of the time, groups 18, nine picks 20), 55 % of the issue slots on cold caches.
+// 8192 rows 13.2 us (1.3 us of memory; with a search through the lane's experts for
+// each pick 21; with whole rows wherever groups are near 18 at the time), 65536 rows 71;
+// without bias and groups 9.5; one row 3.4 us, of which launch and one trip to memory
+// are 2.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
