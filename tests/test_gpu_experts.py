@@ -233,3 +233,29 @@ def test_half_of_a_layer(mxq):
     torch.cuda.synchronize()
     for a, b in zip((captured[7], *captured[8:]), eager):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,k,E,K,I,N", [(1, 2, 4, 256, 1024, 128), (1, 1, 3, 128, 4096, 64), (2, 3, 5, 96, 1088, 80),
+                                         (1, 3, 6, 64, 2080, 144), (4, 2, 9, 160, 4128, 48), (1, 4, 6, 1024, 1152, 400),
+                                         (16, 1, 2, 96, 2048, 272), (8, 2, 5, 128, 1056, 4112)])
+def test_few_choices_share_their_columns(mxq, T, k, E, K, I, N):
+    """Small calls whose down product gives each choice several parts of I, even and uneven ones."""
+    layer = Layer(mxq, E, K, I, N, seed=T + I)
+    a, asf = unit_acts(T, K, seed=T + 1)
+    ids, wt = choose(T, k, E, seed=T + 2)
+    check(layer, a, asf, ids, wt, layer(a, asf, ids, wt))
+    ids[0, -1], ids[-1, 0] = -1, E
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = layer(a, asf, ids, wt, err_flag=err)
+    assert int(err.item()) == mxq.MXQ_DEVERR_EXPERT and mxq.mxq_watchdog_read() == 0
+    check(layer, a, asf, np.where(ids >= E, -1, ids), wt, out)
+
+
+@pytest.mark.parametrize("T,E,k", [(60, 3, 4), (333, 4, 2), (700, 3, 3), (245, 1, 2)])
+def test_tiles_of_one_expert(mxq, T, E, k):
+    """Experts of several tiles, of which the last is smaller than the others."""
+    layer = Layer(mxq, E, 288, 160, 272, seed=T)
+    a, asf = unit_acts(T, 288, seed=T + 1)
+    ids = rng(T + 2).integers(0, E, (T, k)).astype(np.int32)
+    wt = rng(T + 3).random((T, k)).astype(np.float32)
+    check(layer, a, asf, ids, wt, layer(a, asf, ids, wt))
