@@ -125,3 +125,45 @@ def test_experts_past_32_bits(mxq):
     check(layer, a, asf, ids, wt, out[:300])
     for t0 in range(0, T, 20000):
         assert torch.equal(out[t0:t0 + 20000], out[at[t0:t0 + 20000]])
+
+
+def test_between_kernels_that_begin_early(mxq):
+    """4-bit products between a long kernel and others that begin beside them: the same results as one by one."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(70)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    long, w4 = r(16384, 4096), mxq.mxq_prepare_w4(*dev(*weight((4096,), 4096, seed=71)))
+    layer = Layer(mxq, 8, 4096, 1024, 4096, seed=72)
+    ids, wt = dev(*choose(1, 2, 8, seed=73))
+    q, cache = r(8, 16, 128), r(4096, 128)
+    table = torch.arange(64, device="cuda", dtype=torch.int32).view(8, 8)
+    lens = torch.full((8,), 500, device="cuda", dtype=torch.int32)
+    w8 = torch.randint(0, 0x38, (256, 4096), generator=g, device="cuda", dtype=torch.uint8)
+    w8_sf = mxq.mxq_prepare_weight_scales(torch.full((1, 256, 32), 121, dtype=torch.uint8, device="cuda"), 4096)
+
+    def steps(sync):
+        _, y, codes, sf = mxq.mxq_add_rms_norm(long)
+        sync()
+        out = [y[:3]]
+        for _ in range(3):
+            out.append(mxq.mxq_linear_a8w4(codes[:1], sf[:1], w4, 4096))
+            sync()
+            out.append(mxq.mxq_attn(q, cache, table, lens))
+            sync()
+            out.append(mxq.mxq_experts_a8w4(codes[:1], sf[:1], ids, wt, layer.p13, layer.p2, 1024))
+            sync()
+            out.append(mxq.mxq_linear(y[:2], w8, w8_sf))
+            sync()
+        return out
+
+    want = steps(torch.cuda.synchronize)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = steps(lambda: None)
+    for _ in range(3):
+        got = steps(lambda: None)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b, c in zip(want, got, captured):
+            assert torch.equal(a, b) and torch.equal(a, c)
+    assert mxq.mxq_watchdog_read() == 0
