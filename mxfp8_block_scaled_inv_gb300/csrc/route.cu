@@ -16,10 +16,10 @@
 //
 // What is chosen is defined by 64-bit scores: fp32 scores order two experts
 // wrongly where they differ by less than their rounding.  So one pick more than
-// asked for is made, and where two neighbouring picks are nearer than the
-// rounding bounds below, and not equal in logit and bias, picking goes on to the
-// next clear gap and the lanes order their picks by 64-bit values, one for each
-// lane.  Groups whose values lie that near to the edge between those kept and
+// asked for is made, and where two neighbouring picks, or the last one and an expert
+// that is left, are nearer than the rounding bounds below, and not equal in logit and
+// bias, picking goes on to the next clear gap and the lanes order their picks by 64-bit
+// values, one for each lane.  Groups whose values lie that near to the edge between those kept and
 // those left are ordered by the 64-bit sums of their best.  Where this does not
 // settle it (no gap within 32 picks, a group with more than its best that near
 // together, groups that do not lie on whole lanes) the row is done again in 64 bits
@@ -292,6 +292,11 @@ __device__ __noinline__ bool keep_group_64(const RouteArgs& a, int64_t t, bool b
   return v > x + edge || (close && rank < a.keep - above);
 }
 
+// Whether 64 bits have to order two fp32 values of c, the larger one first.
+__device__ __forceinline__ bool too_near(float hi, float lo, float slack) {
+  return !(hi - lo > slack + 1.2e-7f * (fabsf(hi) + fabsf(lo)));
+}
+
 // (The bound on registers is what the common path needs; the rare parts, whose calls
 // would otherwise set it, keep more of theirs in memory.)
 // EVEN: lane i begins at expert i * PER.
@@ -528,15 +533,12 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER <= 16 ? 6 : 4)
   look_up();
   int place = lane;  // of this lane's pick in the output
   float lj = 0.0f, bj = 0.0f;
-  auto near = [&](float hi, float lo) {
-    return !(hi - lo > slack + 1.2e-7f * (fabsf(hi) + fabsf(lo)));
-  };
+  auto near = [&](float hi, float lo) { return too_near(hi, lo, slack); };
   // Whether the last pick is too near to the best expert that is left.
   auto near_rest = [&]() {
     const uint32_t rest = __reduce_max_sync(kAll, head[0]);
     return rest > kNone && near(__shfl_sync(kAll, cj, picks - 1), value_of(rest));
   };
-  if (biased && picks == 32) whole |= near_rest();
   if (biased && !whole) {
     // Lane j > 0: whether picks j - 1 and j are too near to call.
     auto near_prev = [&]() {
@@ -549,15 +551,47 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER <= 16 ? 6 : 4)
         bj = clean_bias(a.bias[expert]);
       }
     };
-    if (__any_sync(kAll, near_prev())) {
+    // Whether an expert that is left is near the last pick without being the same in
+    // logit and bias.  (Among the lane's keys up to the last pick's only picks that are the
+    // same as that one are not left.)
+    auto other_near_rest = [&]() {
+      const uint32_t last = __shfl_sync(kAll, my_key, picks - 1);
+      const float ll = __shfl_sync(kAll, lj, picks - 1), lb = __shfl_sync(kAll, bj, picks - 1);
+      bool other = false;
+      uint32_t same = 0u;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (key[i] == last)
+          same |= 1u << i;
+        else if (key[i] > kNone && key[i] < last)
+          other |= near(value_of(last), value_of(key[i]));
+      }
+      if (head[0] <= kNone) {  // nothing of this lane is left, or its group is out
+        other = false;
+        same = 0u;
+      }
+      for (; same != 0u; same &= same - 1u) {
+        const int e = e0 + __ffs(same) - 1;
+        other |= clean_logit(load_logit(a, t, e, BF16)) != ll || clean_bias(a.bias[e]) != lb;
+      }
+      return __any_sync(kAll, other) != 0;
+    };
+    const uint32_t near_picks = __ballot_sync(kAll, near_prev());
+    // No room for a pick behind the k-th, and what is left may be as large.
+    const bool full = picks == a.k && picks == 32 && near_rest();
+    if (near_picks != 0u || full) {
       fetch();
+      // Equal logits and biases are ties that indices settle, among the picks and
+      // beyond the last one.
       const float pl = __shfl_up_sync(kAll, lj, 1), pb = __shfl_up_sync(kAll, bj, 1);
-      if (__any_sync(kAll, near_prev() && !(pl == lj && pb == bj))) {
+      const bool last_near = full || (picks > a.k && ((near_picks >> (picks - 1)) & 1u) && near_rest());
+      if (__any_sync(kAll, ((near_picks >> lane) & 1u) && !(pl == lj && pb == bj)) ||
+          (last_near && other_near_rest())) {
         // On to the first clear gap behind the k-th pick.
         while (picks > a.k && picks < 32 && __shfl_sync(kAll, (int)near_prev(), picks - 1) && pick()) {
           look_up();
         }
-        if (__shfl_sync(kAll, (int)near_prev(), picks - 1) && near_rest()) {
+        if ((picks == a.k || __shfl_sync(kAll, (int)near_prev(), picks - 1)) && near_rest()) {
           whole = true;
         } else {
           fetch();
