@@ -525,11 +525,9 @@ size_t mxq_experts_workspace_bytes(int64_t T, int32_t k, int32_t E, int32_t K, i
  *  w13             mxq_prepare_w4(.., B = 2*E, N = I, K) of a weight
  *                  [E, 2, I, K]: gate rows, then up rows, of each expert.
  *  w2              mxq_prepare_w4(.., B = E, N, K = I) of a weight [E, N, I].
- *  out_bf16        [T, N]: FP32 sums over j in the order of the ids, rounded
- *                  once to BF16.  Before that each F_e(x_t) is
- *                  held to 2^-14 of the largest of its 32 neighbouring columns
- *                  at worst.  A token without experts gets zeros.  Must not
- *                  overlap an input or the workspace.
+ *  out_bf16        [T, N]: FP32 sums over j in the order of the ids of FP32
+ *                  products, rounded once to BF16.  A token without experts
+ *                  gets zeros.  Must not overlap an input or the workspace.
  *  err_flag        optional int32 device word, in no other buffer.
  *  ws              mxq_experts_workspace_bytes() bytes, 16-byte aligned; calls
  *                  that may run at the same time need distinct workspaces.

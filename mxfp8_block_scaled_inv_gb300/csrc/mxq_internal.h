@@ -150,9 +150,9 @@ cudaError_t launch_linear_a8w4(const uint8_t* a, const uint8_t* a_sf, const uint
 // Workspace of launch_experts_a8w4: the number of tiles, the tiles, the
 // sorted rows' indices and their inverse, the rows themselves (for large tiles),
 // the activation between the two products (codes and scales) and the results to
-// sum (16 bits each, and exponents), all by sorted row.
+// sum (FP32), all by sorted row.
 struct ExpertsLayout {
-  size_t tiles, perm, pos, rows, h, h_sf, part, part_sf, total;
+  size_t tiles, perm, pos, rows, h, h_sf, part, total;
 };
 ExpertsLayout experts_layout(int64_t T, int k, int E, int K, int I, int N);
 cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int32_t* ids,

@@ -125,8 +125,8 @@ struct W4Args {
   const Tile* tiles;      // routed forms
   const int32_t* n_tiles;
   const int32_t* perm;    // sorted row -> token * k + choice
-  void* out;              // kLinear: BF16 [T][N]; kGateUp: codes [rows][N]; kDown: int16 [rows][N]
-  uint8_t* out_sf;        // kGateUp: [rows][NG]; kDown: exponents [NB][NG rows][4]
+  void* out;              // kLinear: BF16 [T][N]; kGateUp: codes [rows][N]; kDown: fp32 [rows][N]
+  uint8_t* out_sf;        // kGateUp: [rows][NG]
   uint32_t* wd;           // watchdog word
   uint32_t wait_ns;       // bound on a wait
   int T, N, KG, KB, NB, NG, k;
@@ -187,16 +187,7 @@ struct Pairs {
   }
 };
 
-// Two fp32 sums at once.
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n.reg .b64 a, b, r;\n"
-      "mov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\n"
-      "add.rn.f32x2 r, a, b;\nmov.b64 {%0, %1}, r;\n}\n"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
+// Two fp32 sums of a product at once.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;
   asm("{\n.reg .b64 a, b, c, r;\n"
@@ -205,28 +196,6 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "=f"(r.x), "=f"(r.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return r;
-}
-
-constexpr uint32_t kLeastExp = 14u;  // of held results (see held16); smaller ones lose bits below 2^-126
-
-// Eight results of 16 bits with their exponent, times g, added to y.
-__device__ __forceinline__ void add_held16(float2 (&y)[4], const uint4& v, uint32_t ef, float g) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  if (ef != 255u) {
-    const float s = __uint_as_float((ef - 13u) << 23) * g;  // 2^(ef - 140) g
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      // The integer plus 2^15 as the low bits of 2^23.
-      const uint32_t u = w[q] ^ 0x80008000u;
-      const float2 f = make_float2(__uint_as_float(__byte_perm(u, 0x4B00u, 0x5410)),
-                                   __uint_as_float(__byte_perm(u, 0x4B00u, 0x5432)));
-      y[q] = fma2(add2(f, make_float2(-8421376.0f, -8421376.0f)), make_float2(s, s), y[q]);
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      y[q] = fma2(make_float2(bf16_lo(w[q]), bf16_hi(w[q])), make_float2(g, g), y[q]);
-  }
 }
 
 // Shape of an instance.  GATHER: the token rows are fetched by index.  SMALL: see
@@ -282,25 +251,6 @@ struct Cfg {
 // smaller than 2^-119, the result is zero.
 __device__ __forceinline__ float swiglu(float g, float u) {
   return __fdividef(g, 1.0f + __expf(-g)) * u;
-}
-
-// A result between the down product and the weighted sum over a token's experts
-// is held in 16 bits, as an integer with one exponent for 32 columns: the step is
-// 2^-13 to 2^-14 of the largest of the 32, which a sum rounded to BF16 does not
-// see, and half the bytes of FP32 to write and read again.  m: the exponent bits of
-// the largest magnitude, which is below 2^(e - 126) for their field e; the value is
-// the integer times 2^(e - 140).  With an infinity or a NaN among the 32 they are BF16
-// values.  (4096 tokens over 64 experts: FP32 results 431 us, these 384 at the time.)
-constexpr uint32_t kExpMask = 0x7F800000u;
-__device__ __forceinline__ uint32_t held16_finite(float y, uint32_t m) {
-  const float inv = __uint_as_float(0x85800000u - max(m, kLeastExp << 23));  // 2^(140 - e)
-  return __float_as_uint(fmaf(y, inv, 12582912.0f));  // the integer + 1.5 * 2^23
-}
-__device__ __forceinline__ uint32_t held16(float y, uint32_t m) {
-  return m == kExpMask ? pack2(y, 0.0f) : held16_finite(y, m);
-}
-__device__ __forceinline__ uint8_t held16_exp(uint32_t m) {
-  return (uint8_t)max(m >> 23, kLeastExp);
 }
 
 // What four warps do with 16 tokens: v[a][i] is token i's sum for weight row
@@ -359,30 +309,17 @@ __device__ __forceinline__ void finish_chunk(const W4Args& p, float (&v)[NA][kCh
       if (in && i + tok < live) *reinterpret_cast<uint32_t*>(o + (size_t)i * p.N) = w;
     }
   } else {
-    // (Instructions are what this one is short of: 11 for each value now, 24 with a
-    // predicate, a shift and a choice of the non-finite form for each.)
-    uint16_t* o = static_cast<uint16_t*>(p.out) + (size_t)row * p.N + n;
-    uint32_t m[kChunk], mine = 0u, top = 0u;
+    // FP32, as the sum over a token's experts takes them: what a column loses must not
+    // hang on its neighbours, nor a token's result on the number of others in the call.
+    float* o = static_cast<float*>(p.out) + (size_t)row * p.N + n;
+    if (live >= kChunk && rb * 128 + 128 <= p.N) {
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-      m[i] = __reduce_max_sync(0xffffffffu, __float_as_uint(v[0][i]) & kExpMask);
-      top = max(top, m[i]);
-      if (lane == i) mine = m[i];
-    }
-    if (top != kExpMask && live >= kChunk && rb * 128 + 128 <= p.N) {
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i) o[(size_t)i * p.N] = (uint16_t)held16_finite(v[0][i], m[i]);
+      for (int i = 0; i < kChunk; ++i) o[(size_t)i * p.N] = v[0][i];
     } else {
 #pragma unroll
       for (int i = 0; i < kChunk; ++i)
-        if (in && i < live) o[(size_t)i * p.N] = (uint16_t)held16(v[0][i], m[i]);
+        if (in && i < live) o[(size_t)i * p.N] = v[0][i];
     }
-    // (By row block first: a row's bytes of all blocks lie far apart, and single bytes
-    // to lines that nobody else writes cost as much as all the rest.  The four of a
-    // block side by side: the sum fetches them as one, 4096 tokens over 64 experts 323
-    // us, and 328 with [N / 32][rows].)
-    if (lane < min(live, kChunk) && rb * 128 + q * 32 < p.N)
-      p.out_sf[((size_t)rb * p.NG + row + lane) * 4 + q] = held16_exp(mine);
   }
 }
 
@@ -409,19 +346,10 @@ __device__ __forceinline__ void finish_token(const W4Args& p, const float (&v)[N
       if (sub == 0) p.out_sf[(size_t)row * p.NG + rb] = (uint8_t)sb;
     }
   } else {
-    uint32_t m = 0u;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[0][e]) & kExpMask);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = (held16(v[0][2 * e], m) & 0xFFFFu) | (held16(v[0][2 * e + 1], m) << 16);
     if (store) {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (size_t)row * p.N + n) =
-          make_uint4(w[0], w[1], w[2], w[3]);
-      if ((sub & 3) == 0) p.out_sf[((size_t)rb * p.NG + row) * 4 + (sub >> 2)] = held16_exp(m);
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + (size_t)row * p.N + n);
+      o[0] = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+      o[1] = make_float4(v[0][4], v[0][5], v[0][6], v[0][7]);
     }
   }
 }
@@ -1333,41 +1261,47 @@ __global__ void __launch_bounds__(kRowWarps * 32) w4_rows_kernel(const uint4* a,
   }
 }
 
-// out[t] = weighted sum over the token's choices, in their order, of the 16-bit
-// results that the down product left; eight columns to a thread.  24576 rows of 4096
-// columns: 47 us by itself with each thread on its own, 5 TB/s; by warps the call takes
-// 329 us and not 333.  (Adding in the down product's last CTA of a token instead,
-// found by a counter, was no faster.)
+// out[t] = weighted sum over the token's choices, in their order, of the FP32
+// results that the down product left.  (Adding in the down product's last CTA of a token
+// instead, found by a counter, was no faster.)
 constexpr int kJoinWarps = 8;
+constexpr int kJoinCols = 256;  // of a warp
 
-// One warp: 256 columns of a token.  The lanes fetch the token's rows and weights at
-// once and pass them round, so that the results' loads wait for nothing else.
-__global__ void __launch_bounds__(kJoinWarps * 32) w4_join_kernel(const uint4* part, const uint8_t* part_sf,
-                                                                  const int32_t* pos, const float* wt,
-                                                                  uint4* out, int64_t items, int segs,
-                                                                  int chunks, int k, int64_t R) {
+// One warp: kJoinCols columns of a token, four and four to a lane.  The lanes fetch the
+// token's rows and weights at once and pass them round, so that the results' loads wait
+// for nothing else.
+__global__ void __launch_bounds__(kJoinWarps * 32) w4_join_kernel(const float* part, const int32_t* pos,
+                                                                  const float* wt, __nv_bfloat16* out,
+                                                                  int64_t items, int segs, int N, int k) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int64_t it = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (it >= items) return;
   const int64_t t = it / segs;
-  const int c = (int)(it - t * segs) * 32 + lane;
+  const int c = (int)(it - t * segs) * kJoinCols + lane * 4;
   const int my_row = lane < k ? pos[t * k + lane] : -1;  // (k is 32 at most)
   const float my_weight = lane < k ? wt[t * k + lane] : 0.0f;
-  const bool in = c < chunks;
-  part += in ? c : 0;
-  part_sf += (size_t)((in ? c : 0) >> 4) * (size_t)R * 4 + (((in ? c : 0) >> 2) & 3);
-  float2 y[4] = {};
-#pragma unroll 2
+  const bool in[2] = {c < N, c + kJoinCols / 2 < N};
+  float2 y[2][2] = {};
+#pragma unroll 4
   for (int j = 0; j < k; ++j) {
     const int row = __shfl_sync(0xffffffffu, my_row, j);
     const float weight = __shfl_sync(0xffffffffu, my_weight, j);
-    if (row >= 0) add_held16(y, part[(size_t)row * chunks], part_sf[(size_t)row * 4], weight);
+    if (row < 0) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (!in[h]) continue;
+      const float4 v = *reinterpret_cast<const float4*>(part + (size_t)row * N + c + h * (kJoinCols / 2));
+      y[h][0] = fma2(make_float2(v.x, v.y), make_float2(weight, weight), y[h][0]);
+      y[h][1] = fma2(make_float2(v.z, v.w), make_float2(weight, weight), y[h][1]);
+    }
   }
-  if (in)
-    out[t * chunks + c] = make_uint4(pack2(y[0].x, y[0].y), pack2(y[1].x, y[1].y),
-                                     pack2(y[2].x, y[2].y), pack2(y[3].x, y[3].y));
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (in[h])
+      *reinterpret_cast<uint2*>(out + (size_t)t * N + c + h * (kJoinCols / 2)) =
+          make_uint2(pack2(y[h][0].x, y[h][0].y), pack2(y[h][1].x, y[h][1].y));
 }
 
 // Codes and scales of B matrices [N][K] into blocks; one thread per 16 bytes.
@@ -1682,8 +1616,7 @@ ExpertsLayout experts_layout(int64_t T, int k, int E, int K, int I, int N) {
   l.h = l.rows + (lays_out_rows(nt) ? round_up_256((size_t)R * K) : 0);
   l.h_sf = l.h + round_up_256((size_t)R * I);
   l.part = l.h_sf + round_up_256((size_t)R * (size_t)ceil_div(I, kGroup));
-  l.part_sf = l.part + round_up_256((size_t)R * N * 2);
-  l.total = l.part_sf + round_up_256((size_t)R * (size_t)ceil_div(N, 128) * 4);
+  l.total = l.part + round_up_256((size_t)R * N * 4);
   return l;
 }
 
@@ -1773,9 +1706,7 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   g.w = w2;
   g.a_sf = base + l.h_sf;
   g.out = base + l.part;
-  g.out_sf = base + l.part_sf;
   g.N = N;
-  g.NG = (int)R;
   g.KG = g.KB = (int)ceil_div(I, kGroup);
   g.NB = (int)ceil_div(N, 128);
   int64_t units = most * g.NB;
@@ -1793,13 +1724,12 @@ cudaError_t launch_experts_a8w4(const uint8_t* a, const uint8_t* a_sf, const int
   e = launch_tokens<kDown>(nt, base + l.h, (uint64_t)R, (uint64_t)I, (uint64_t)E * g.NB * g.KB, g,
                            units, num_sms, s, why);
   if (e != cudaSuccess || small) return e;
-  const int chunks = N / 8, segs = (int)ceil_div(chunks, 32);
+  const int segs = (int)ceil_div(N, kJoinCols);
   cfg.gridDim = dim3((unsigned)ceil_div(T * segs, kJoinWarps), 1, 1);
   cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
-  return cudaLaunchKernelEx(&cfg, w4_join_kernel, reinterpret_cast<const uint4*>(base + l.part),
-                            reinterpret_cast<const uint8_t*>(base + l.part_sf),
-                            static_cast<const int32_t*>(pos), wt, static_cast<uint4*>(out), T * segs, segs,
-                            chunks, k, R);
+  return cudaLaunchKernelEx(&cfg, w4_join_kernel, reinterpret_cast<const float*>(base + l.part),
+                            static_cast<const int32_t*>(pos), wt, static_cast<__nv_bfloat16*>(out), T * segs,
+                            segs, N, k);
 }
 
 }  // namespace mxq
