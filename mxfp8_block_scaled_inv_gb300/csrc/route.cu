@@ -248,15 +248,15 @@ __device__ __noinline__ double row_sum_64(const RouteArgs& a, int64_t t, bool bf
   return warp_sum(s);
 }
 
-// Which groups stay where the last one kept (of value x) and the first one left (y)
-// are too near to call: the groups within `edge` of them are ordered by the 64-bit
-// sums of their n best (those with an fp32 value of `least` and more), the others stay
-// where they are.  v, g: the lane's group; false in *sure where a group has more
-// than its n best that near to each other.
+// Which groups stay where the bounds lo <= value <= hi of those kept and those left
+// overlap: the groups that reach between `low`, the least bound of one kept, and
+// `high`, the largest of one left, are ordered by the 64-bit sums of their n best (those
+// with an fp32 value of `least` and more), the others stay where they are.  g: the lane's
+// group; false in *sure where a group has more than its n best that near to each other.
 __device__ __noinline__ bool keep_group_64(const RouteArgs& a, int64_t t, bool bf16, int lane, int per, int n_mine,
-                                           float mx, float inv_z, float v, int g, float x, float y,
-                                           float edge, float least, int n, bool* sure) {
-  const bool close = g < a.groups && v >= y - edge && v <= x + edge;
+                                           float mx, float inv_z, int g, bool any, float lo, float hi,
+                                           float low, float high, float least, int n, bool* sure) {
+  const bool close = any && hi >= low && lo <= high, clear = any && lo > high;
   const double z = a.scoring == MXQ_SCORE_SOFTMAX && a.bias != nullptr
                        ? row_sum_64(a, t, bf16, lane, per, mx) : 1.0;
   double sum = 0.0;
@@ -283,13 +283,13 @@ __device__ __noinline__ bool keep_group_64(const RouteArgs& a, int64_t t, bool b
   }
   *sure = !__any_sync(kAll, close && found != n);
   const Key64 mine = close ? key64_of(sum) : 0;
-  int rank = 0, above = 0;
+  int rank = 0;
   for (int q = 0; q < a.groups; ++q) {
     const Key64 o = __shfl_sync(kAll, mine, q * a.lanes);
     rank += o > mine || (o == mine && q < g) ? 1 : 0;
-    above += __shfl_sync(kAll, v, q * a.lanes) > x + edge ? 1 : 0;
   }
-  return v > x + edge || (close && rank < a.keep - above);
+  const int above = __popc(__ballot_sync(kAll, clear)) / a.lanes;
+  return clear || (close && rank < a.keep - above);
 }
 
 // Whether 64 bits have to order two fp32 values of c, the larger one first.
@@ -426,25 +426,25 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER <= 16 ? 6 : 4)
     }
     for (int m = 1; m < step; m <<= 1) rank += __shfl_xor_sync(kAll, rank, m);
     bool kept = rank < a.keep;
-    const uint32_t vkey = g < a.groups && v > -INFINITY ? key_of(v) : 0u;
-    const uint32_t low = __reduce_min_sync(kAll, kept && g < a.groups ? vkey : 0xffffffffu);
-    const uint32_t high = __reduce_max_sync(kAll, kept ? 0u : vkey);
-    if (low != 0u && high != 0u) {
-      const float x = value_of(low), y = value_of(high);
-      const float edge = 2.0f * slack + 2.5e-7f * (fabsf(x) + fabsf(y));
-      if (!(x - y > edge)) {
-        bool sure = false;  // (groups that do not lie on lanes: the whole row)
-        const bool two = a.group_top == 2 && a2 > -INFINITY;
-        if (a.lanes > 0)
-          kept = keep_group_64(a, t, BF16, lane, PER, n, mx, inv_z, v, g, x, y, edge,
-                               (two ? a2 : a1) - edge, two ? 2 : 1, &sure);
-        whole = !sure;
+    // Two scores' share of the value's error, and the roundings of its terms (a score
+    // and a bias each, which may cancel) and of their sum.
+    const bool any = g < a.groups && v > -INFINITY, two = a.group_top == 2 && a2 > -INFINITY;
+    const float err = slack + 2.5e-7f * (fabsf(a1) + (two ? fabsf(a2) : 0.0f));
+    const uint32_t low = __reduce_min_sync(kAll, kept && g < a.groups ? (any ? key_of(v - err) : 0u) : 0xffffffffu);
+    const uint32_t high = __reduce_max_sync(kAll, !kept && any ? key_of(v + err) : 0u);
+    if (low != 0u && low <= high) {
+      bool sure = false;  // (groups that do not lie on lanes: the whole row)
+      if (a.lanes > 0) {
+        const float last = two ? a2 : a1;
+        kept = keep_group_64(a, t, BF16, lane, PER, n, mx, inv_z, g, any, v - err, v + err, value_of(low),
+                             value_of(high), last - (2.0f * slack + 5e-7f * fabsf(last)), two ? 2 : 1, &sure);
       }
+      whole = !sure;
     }
     return kept;
   };
   if (spread) {
-    float v = -INFINITY;
+    float v = -INFINITY, v1 = -INFINITY, v2 = -INFINITY;
     for (int q = 0; q < a.groups; ++q) {
       float a1 = -INFINITY, a2 = -INFINITY;
 #pragma unroll
@@ -460,10 +460,14 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER <= 16 ? 6 : 4)
         const float o1 = __shfl_xor_sync(kAll, a1, m), o2 = __shfl_xor_sync(kAll, a2, m);
         merge2(a1, a2, o1, o2);
       }
-      if (lane == q) v = a.group_top == 2 && a2 > -INFINITY ? a1 + a2 : a1;
+      if (lane == q) {
+        v = a.group_top == 2 && a2 > -INFINITY ? a1 + a2 : a1;
+        v1 = a1;
+        v2 = a2;
+      }
     }
     const uint32_t mask =
-        __ballot_sync(kAll, group_kept(v, lane, -INFINITY, -INFINITY, 1) && lane < a.groups);
+        __ballot_sync(kAll, group_kept(v, lane, v1, v2, 1) && lane < a.groups);
 #pragma unroll
     for (int i = 0; i < PER; ++i)
       if (!((mask >> (min(e0 + i, a.E - 1) / a.per_group)) & 1u)) key[i] = 0u;

@@ -87,3 +87,16 @@ def test_duplicated_logits_of_a_wide_row(mxq):
     l = cuda(10 + 5 * g.standard_normal((400, 256))).bfloat16().clamp_(max=26)
     check(mxq, l, cuda(np.zeros(256)), k=8, scoring="sigmoid")
     check(mxq, l, cuda(np.zeros(256)), undecided=0.01, k=8, scoring="sigmoid", groups=8, topk_groups=4)
+
+
+@pytest.mark.parametrize("E,groups,keep,top", [(64, 32, 7, 2), (64, 16, 5, 2), (60, 15, 6, 2), (256, 32, 9, 2), (96, 32, 11, 1)])
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax", "sqrtsoftplus"])
+def test_group_values_whose_terms_cancel(mxq, scoring, E, groups, keep, top):
+    """Biases of opposite sign leave sums of two that are small beside what they were rounded at."""
+    g = np.random.default_rng(E + groups)
+    n = E // groups
+    for size in (30.0, 1000.0, 2.0 ** 14):
+        b = np.full((groups, n), -5.0 * size)
+        b[:, 0], b[:, 1] = size, -size
+        l = 0.5 + 2.0 ** -10 * g.standard_normal((30, E))
+        check(mxq, cuda(l), cuda(b.reshape(-1)), k=6, scoring=scoring, groups=groups, topk_groups=keep, group_top=top)
