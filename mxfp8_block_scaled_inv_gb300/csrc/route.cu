@@ -125,6 +125,10 @@ __device__ __forceinline__ void merge2(R& a1, R& a2, R b1, R b2) {
   a2 = lo > hi2 ? lo : hi2;
 }
 
+// The value of a group of two that may be chosen: a sum past fp32's range (the lowest
+// biases) is not that of a group with none, and its bounds leave it to 64 bits.
+__device__ __forceinline__ float sum2(float a1, float a2) { return fmaxf(a1 + a2, -3.4028234e38f); }
+
 // Order-preserving 64-bit key of a finite value, never 0, and back: comparisons of
 // doubles run on the few 64-bit units, those of integers do not.
 typedef unsigned long long Key64;
@@ -461,7 +465,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER <= 16 ? 6 : 4)
         merge2(a1, a2, o1, o2);
       }
       if (lane == q) {
-        v = a.group_top == 2 && a2 > -INFINITY ? a1 + a2 : a1;
+        v = a.group_top == 2 && a2 > -INFINITY ? sum2(a1, a2) : a1;
         v1 = a1;
         v2 = a2;
       }
@@ -489,7 +493,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER <= 16 ? 6 : 4)
       const float o1 = __shfl_xor_sync(kAll, a1, m), o2 = __shfl_xor_sync(kAll, a2, m);
       merge2(a1, a2, o1, o2);
     }
-    const float v = a.group_top == 2 && a2 > -INFINITY ? a1 + a2 : a1;
+    const float v = a.group_top == 2 && a2 > -INFINITY ? sum2(a1, a2) : a1;
     if (!group_kept(v, lane >> a.run_log, a1, a2, a.lanes)) head[0] = 0u;  // hides the others
   }
   int expert = -1, picks = 0;

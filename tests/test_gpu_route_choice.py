@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+import ffn_ref as ref
 from test_gpu_route import check
 
 pytestmark = pytest.mark.gpu
@@ -100,3 +101,23 @@ def test_group_values_whose_terms_cancel(mxq, scoring, E, groups, keep, top):
         b[:, 0], b[:, 1] = size, -size
         l = 0.5 + 2.0 ** -10 * g.standard_normal((30, E))
         check(mxq, cuda(l), cuda(b.reshape(-1)), k=6, scoring=scoring, groups=groups, topk_groups=keep, group_top=top)
+
+
+@pytest.mark.parametrize("E,groups,keep", [(64, 8, 3), (64, 32, 5), (60, 5, 2), (256, 4, 1)])
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax", "sqrtsoftplus"])
+def test_biases_of_the_lowest_value(mxq, scoring, E, groups, keep):
+    """Groups whose sum of two is past FP32's range still come before those with nothing to choose, in their order."""
+    g = np.random.default_rng(E + groups)
+    lowest = torch.finfo(torch.float32).min
+    n = E // groups
+    l = 1.5 * g.standard_normal((8, E))
+    l[:, :n] = -np.inf                              # the first group has nothing
+    for seen in ([], [E - 1], [E - n, E // 2], [n + 1]):
+        for low in (lowest, -2e38, np.where(np.arange(E) % (2 * n) < n, -3e38, -2.5e38)):
+            b = np.full(E, 1.0) * low
+            b[seen] = 0.1
+            # (Such a bias is the sum in any arithmetic, so that 64 bits decide every row: ties go by index.)
+            kw = dict(k=4, scoring=scoring, groups=groups, topk_groups=keep)
+            ids, _ = mxq.mxq_route(cuda(l), bias=cuda(b), **kw)
+            want, _, _ = ref.route(cuda(l).double().cpu().numpy(), bias=cuda(b).double().cpu().numpy(), **kw)
+            assert np.array_equal(ids.cpu().numpy(), want), np.argwhere(ids.cpu().numpy() != want)[:5]
