@@ -79,7 +79,10 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 __device__ __forceinline__ float score_of(int scoring, float l, float mx, float inv_z) {
   if (scoring == MXQ_SCORE_SOFTMAX) return expf(l - mx) * inv_z;
   if (scoring == MXQ_SCORE_SIGMOID) return __fdividef(1.0f, 1.0f + expf(-l));
-  return sqrtf(fmaxf(l, 0.0f) + log1pf(expf(-fabsf(l))));
+  // Below -16 the score is exp(l / 2) to 2^-25 of itself, which fp32 holds down to l = -174;
+  // exp(l) is subnormal from -87 on.
+  const float e = expf(l < -16.0f ? 0.5f * l : -fabsf(l));
+  return l < -16.0f ? e : sqrtf(fmaxf(l, 0.0f) + log1pf(e));
 }
 __device__ __noinline__ double score_of(int scoring, double l, double mx, double z) {
   if (scoring == MXQ_SCORE_SOFTMAX) return exp(l - mx) / z;

@@ -121,3 +121,14 @@ def test_biases_of_the_lowest_value(mxq, scoring, E, groups, keep):
             ids, _ = mxq.mxq_route(cuda(l), bias=cuda(b), **kw)
             want, _, _ = ref.route(cuda(l).double().cpu().numpy(), bias=cuda(b).double().cpu().numpy(), **kw)
             assert np.array_equal(ids.cpu().numpy(), want), np.argwhere(ids.cpu().numpy() != want)[:5]
+
+
+@pytest.mark.parametrize("renormalise", [False, True])
+def test_weights_of_very_negative_logits(mxq, renormalise):
+    """sqrt(log(1 + exp(l))) is about exp(l / 2): inside FP32's range where exp(l) is not."""
+    l = np.stack([np.linspace(-170, -100, 64), np.linspace(-120, -80, 64), np.linspace(-40, 10, 64), np.linspace(-17, -15, 64)])
+    for bias in (None, cuda(np.zeros(64))):
+        check(mxq, cuda(l), bias, k=12, scoring="sqrtsoftplus", renormalise=renormalise)
+        check(mxq, cuda(l[:, ::-1].copy()), bias, k=12, scoring="sqrtsoftplus", renormalise=renormalise, groups=8, topk_groups=3)
+    for at in range(0, 64, 8):
+        check(mxq, cuda(l[:, at:at + 8]), None, k=8, scoring="sqrtsoftplus", renormalise=renormalise)
