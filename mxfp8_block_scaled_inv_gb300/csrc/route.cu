@@ -625,7 +625,15 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 8 : PER <= 16 ? 6 : 4)
     route_row_64(a, t, BF16, lane, &expert, &p);
     place = lane;
   } else if (expert >= 0) {
-    p = score_of(a.scoring, clean_logit(load_logit(a, t, expert, BF16)), mx, inv_z);
+    const float l1 = clean_logit(load_logit(a, t, expert, BF16));
+    p = score_of(a.scoring, l1, mx, inv_z);
+    if (a.scoring == MXQ_SCORE_SOFTMAX) {
+      // exp(l - mx) = exp(d) (1 + lack), lack being what the rounding of d took away: up to
+      // 2^-18 at differences of 64 and more.  (The choice does without: the bounds above
+      // go by the row's largest score, beside which such ones are nothing.)
+      const float d = l1 - mx, back = d - l1, lack = (l1 - (d - back)) - (mx + back);
+      p = p > 0.0f ? fmaf(p, lack, p) : 0.0f;
+    }
   }
   if (place >= a.k) p = 0.0f;
   if (a.renorm) p = p / (warp_sum(p) + 1e-20f);

@@ -132,3 +132,12 @@ def test_weights_of_very_negative_logits(mxq, renormalise):
         check(mxq, cuda(l[:, ::-1].copy()), bias, k=12, scoring="sqrtsoftplus", renormalise=renormalise, groups=8, topk_groups=3)
     for at in range(0, 64, 8):
         check(mxq, cuda(l[:, at:at + 8]), None, k=8, scoring="sqrtsoftplus", renormalise=renormalise)
+
+
+@pytest.mark.parametrize("renormalise", [False, True])
+def test_weights_far_from_the_largest_logit(mxq, renormalise):
+    """exp(l - max) where the difference itself is rounded: by 2^-18 at 64 and more."""
+    g = np.random.default_rng(8)
+    l = np.concatenate([-60 * g.random((200, 32)), -84 * g.random((800, 32))]) + 7 * g.random((1000, 1))
+    for bias in (None, cuda(np.zeros(32))):
+        check(mxq, cuda(l), bias, k=32, scoring="softmax", renormalise=renormalise)
