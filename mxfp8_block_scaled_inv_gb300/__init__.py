@@ -556,20 +556,21 @@ def _fastcall():
     point), or False.  It answers None for any other call, which then goes the way below."""
     global _fast
     if _fast is None:
-        _fast = False
         path = os.path.join(HERE, f"mxq_fastcall-{torch.__version__}{importlib.machinery.EXTENSION_SUFFIXES[0]}")
-        if os.path.exists(path):
-            L = lib()
-            loader = importlib.machinery.ExtensionFileLoader("mxq_fastcall", path)
-            try:
-                m = importlib.util.module_from_spec(importlib.util.spec_from_loader("mxq_fastcall", loader))
-                loader.exec_module(m)
-            except ImportError as e:
-                raise MxqLibraryError(f"cannot load {path}: {e}") from e
-            m.bind(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
-                "mxq_add_rms_norm", "mxq_route", "mxq_w4_bytes", "mxq_linear_a8w4", "mxq_experts_workspace_bytes",
-                "mxq_experts_a8w4")))
-            _fast = m
+        if not os.path.exists(path):
+            _fast = False
+            return _fast
+        L = lib()
+        loader = importlib.machinery.ExtensionFileLoader("mxq_fastcall", path)
+        try:
+            m = importlib.util.module_from_spec(importlib.util.spec_from_loader("mxq_fastcall", loader))
+            loader.exec_module(m)
+        except ImportError as e:
+            raise MxqLibraryError(f"cannot load {path}: {e}") from e
+        m.bind(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
+            "mxq_add_rms_norm", "mxq_route", "mxq_w4_bytes", "mxq_linear_a8w4", "mxq_experts_workspace_bytes",
+            "mxq_experts_a8w4")))
+        _fast = m
     return _fast
 
 
