@@ -5,9 +5,11 @@ Each CUDA translation unit is compiled by nvcc in parallel with
 compiler, and the objects are linked into ``libmxq.so`` next to this file.
 ``mxq_fastcall``, the binding's quick way into it for common calls, is built beside
 it against the installed torch, and named after torch's and Python's versions;
-where there is none for them (no torch or Python headers, another torch since)
-the binding makes those calls through ctypes like all others.
-A build is skipped when the library is newer than every source and header.
+where there is none for them (no torch or Python headers) the binding makes those
+calls through ctypes like all others.
+A build is skipped when the library is newer than every source and header; a missing
+or older ``mxq_fastcall`` for the installed torch is then built alone.  A new library
+takes away the modules that were built beside the old one, for whatever torch.
 """
 
 from __future__ import annotations
@@ -55,11 +57,15 @@ def _inputs():
     return files
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+def _current(path) -> bool:
+    if not os.path.exists(path):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = os.path.getmtime(path)
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def up_to_date() -> bool:
+    return _current(LIB_PATH)
 
 
 def _run(cmd, verbose):
@@ -71,37 +77,67 @@ def _run(cmd, verbose):
     return r.stdout
 
 
-def _build_fastcall(cxx, inc, verbose) -> None:
-    """Compile mxq_fastcall; a failure leaves it out, with a message."""
-    path = None
+_tried = set()  # modules that this process could not build
+
+
+def _fastcall_wanted(anew):
+    """Where the quick way in for the installed torch has to be built (`anew`: though it is current), or None."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    path = fastcall_path(torch.__version__)
+    return None if path in _tried or (not anew and _current(path)) else path
+
+
+def _includes():
+    return ["-I", INCLUDE, "-I", CSRC, "-I", os.path.join(cuda_home(), "include")]
+
+
+def _compile_fastcall(path, verbose):
+    """Compile mxq_fastcall beside its place; a failure leaves it out, with a message.  Returns whether it is there."""
     try:
         import torch
 
-        path = fastcall_path(torch.__version__)
-        tmp = path + ".tmp"
         at = os.path.dirname(torch.__file__)
-        _run([cxx, "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared",
-              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
+        _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared",
+              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *_includes(),
               "-isystem", os.path.join(at, "include"),
               "-isystem", os.path.join(at, "include", "torch", "csrc", "api", "include"),
-              "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "fastcall.cpp"), "-o", tmp,
+              "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "fastcall.cpp"), "-o", path + ".tmp",
               "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], verbose)
-    except (ImportError, RuntimeError) as e:
+    except (RuntimeError, OSError) as e:
         print(f"mxq_fastcall not built: {e}", file=sys.stderr, flush=True)
-        if path is not None and os.path.exists(path):
-            os.remove(path)
-        return
-    os.replace(tmp, path)
+        _tried.add(path)
+        return False
+    return True
+
+
+def _remove_fastcalls(but=None) -> None:
+    """Take away the modules for every torch and Python (but for files beginning with `but`)."""
+    for f in os.listdir(HERE):
+        if f.startswith("mxq_fastcall-") and not (but and f.startswith(os.path.basename(but))):
+            os.remove(os.path.join(HERE, f))
 
 
 def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False) -> str:
     """Compile and link libmxq.so; returns its path."""
-    if not force and up_to_date():
+    if force:
+        _tried.clear()
+    library = force or not up_to_date()
+    fast = _fastcall_wanted(anew=library)
+    if not library:
+        if fast is not None:
+            if os.path.exists(fast):  # an older one, of other arguments perhaps
+                os.remove(fast)
+            if _compile_fastcall(fast, verbose):
+                os.replace(fast + ".tmp", fast)
         return LIB_PATH
     home = cuda_home()
     nvcc = os.path.join(home, "bin", "nvcc")
+    cxx = os.environ.get("CXX", "g++")
+    inc = _includes()
     os.makedirs(BUILD_DIR, exist_ok=True)
-    inc = ["-I", INCLUDE, "-I", CSRC, "-I", os.path.join(home, "include")]
     jobs = []
     for src in CU_SOURCES:
         obj = os.path.join(BUILD_DIR, src + ".o")
@@ -110,7 +146,6 @@ def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False) 
         if ptxas_info:
             cmd.insert(1, "-Xptxas=-v")
         jobs.append((cmd, obj))
-    cxx = os.environ.get("CXX", "g++")
     for src in CXX_SOURCES:
         obj = os.path.join(BUILD_DIR, src + ".o")
         cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-Wall", *inc, "-c", os.path.join(CSRC, src),
@@ -118,16 +153,20 @@ def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False) 
         jobs.append((cmd, obj))
     outputs = []
     with cf.ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
-        fast = ex.submit(_build_fastcall, cxx, inc, verbose)
+        made = fast and ex.submit(_compile_fastcall, fast, verbose)
         for out in ex.map(lambda j: _run(j[0], verbose), jobs):
             outputs.append(out)
-        fast.result()
+        made = made and made.result()
     if ptxas_info:
         print("\n".join(outputs))
     tmp = LIB_PATH + ".tmp"
     _run([nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *[o for _, o in jobs],
           "-L", os.path.join(home, "lib64")], verbose)
+    # The modules pass their arguments by the old library's header.
+    _remove_fastcalls(but=fast + ".tmp" if made else None)
     os.replace(tmp, LIB_PATH)
+    if made:
+        os.replace(fast + ".tmp", fast)
     return LIB_PATH
 
 
