@@ -793,9 +793,12 @@ int mxq_experts_a8w4(const uint8_t* a_e4m3, const uint8_t* a_e8m0, const int32_t
   if (overlap(out_bf16, out, ws, need)) return fail(MXQ_ERR_SHAPE, "out overlaps the workspace");
   if (err_flag && (overlap(err_flag, 4, ws, need) || overlap(err_flag, 4, out_bf16, out)))
     return fail(MXQ_ERR_SHAPE, "err_flag lies in out or the workspace");
-  for (const auto& b : in)
+  for (const auto& b : in) {
     if (overlap(out_bf16, out, b.p, b.bytes) || overlap(ws, need, b.p, b.bytes))
       return fail(MXQ_ERR_SHAPE, "out or the workspace overlaps an input");
+    if (err_flag && overlap(err_flag, 4, b.p, b.bytes))
+      return fail(MXQ_ERR_SHAPE, "err_flag lies in an input");
+  }
   int sms = 0;
   if (int st = device_check(&sms)) return st;
   const char* why = nullptr;
