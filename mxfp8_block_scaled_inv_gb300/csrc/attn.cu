@@ -220,6 +220,10 @@ int stages_for(int D) {
   return n < kMaxStages ? n : kMaxStages;
 }
 static_assert(smem_fixed<64, MXQ_CACHE_BF16>(512) + 4 * Form<MXQ_CACHE_BF16>::STAGE <= kSmemBudget, "a block fits");
+// As many stages as fit, or the most there are.
+static_assert(tmem_allowed(kSmemBudget - Form<MXQ_CACHE_BF16>::STAGE) >= (int)kTmemCols &&
+                  tmem_allowed(kMaxStages * Form<MXQ_CACHE_E4M3>::STAGE + kPBytes<16, MXQ_CACHE_E4M3>) >= (int)kTmemCols,
+              "TMEM beside other kernels' CTAs");
 static_assert(smem_fixed<64, MXQ_CACHE_E4M3>(512) + 8 * Form<MXQ_CACHE_E4M3>::STAGE <= kSmemBudget, "two blocks fit");
 
 // A sequence: its first token, new tokens and keys.  Up to 32 at a time, one per lane.

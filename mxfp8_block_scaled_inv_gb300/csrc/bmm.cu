@@ -248,6 +248,9 @@ struct Cfg {
   static constexpr uint32_t IDESC =
       (1u << 23) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)((PAIR ? 2 * BM : BM) >> 4) << 24);
   static_assert(TMEM_USED <= 512, "TMEM budget");
+  // (This kernel lets the next one begin before it has its columns.)
+  static_assert(tmem_allowed(SMEM_BYTES) >= TMEM_COLS && tmem_never_short(CTAS_PER_SM, SMEM_BYTES, TMEM_COLS),
+                "TMEM beside other kernels' CTAs");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static_assert(!FUSED || (SWAP && BN <= 32), "fused activations: swapped form, <= 32 tokens");
   static_assert(BN % 16 == 0 && BN >= 16 && BN <= 256, "MMA N");

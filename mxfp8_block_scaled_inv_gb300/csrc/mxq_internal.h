@@ -14,6 +14,37 @@ constexpr int kSfRowPad = 256;     // prepared weight-scale rows are padded to t
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Tensor memory of the CTAs that share an SM.  A kernel of bmm.cu lets the next one begin
+// before its own CTAs have their columns, and the next one's CTAs take theirs before they
+// wait for it.  So what an SM's shared memory holds at once must never ask for more
+// than its 512 columns: a CTA would wait for columns of one that waits for it.  A CTA may
+// therefore have only as many columns as goes with its (dynamic) shared memory, and
+// bmm.cu checks what fits beside its own.
+constexpr int kSmSharedBytes = 228 * 1024, kCtaSharedReserve = 1024, kSmTmemCols = 512;
+constexpr int kLeastShared64 = 43 * 1024, kLeastShared256 = 100 * 1024, kLeastShared512 = 140 * 1024;
+constexpr int tmem_allowed(int shared) {
+  return shared >= kLeastShared512 ? 512 : shared >= kLeastShared256 ? 256 : shared >= kLeastShared64 ? 64 : 0;
+}
+// The most columns that CTAs in this much shared memory may have together.
+constexpr int tmem_within(int room) {
+  int most = room >= kLeastShared512 + kCtaSharedReserve
+                 ? 512 + tmem_within(room - kLeastShared512 - kCtaSharedReserve) : 0;
+  for (int n = 0; n * (kLeastShared256 + kCtaSharedReserve) <= room; ++n) {
+    const int cols = 256 * n + (room - n * (kLeastShared256 + kCtaSharedReserve)) /
+                                   (kLeastShared64 + kCtaSharedReserve) * 64;
+    if (cols > most) most = cols;
+  }
+  return most;
+}
+// Whether up to `ctas` CTAs of this much shared memory have their columns for sure.
+constexpr bool tmem_never_short(int ctas, int shared, int cols) {
+  for (int n = 1; n <= ctas; ++n) {
+    const int room = kSmSharedBytes - n * (shared + kCtaSharedReserve);
+    if (room >= 0 && n * cols + tmem_within(room) > kSmTmemCols) return false;
+  }
+  return true;
+}
+
 // Number of 128-row atoms per (b, kg) in the prepared weight-scale layout.
 inline int64_t sf_row_blocks(int64_t N) { return ceil_div(N, kSfRowPad) * (kSfRowPad / 128); }
 

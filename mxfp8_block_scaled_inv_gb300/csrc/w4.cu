@@ -242,6 +242,7 @@ struct Cfg {
   // operand is chosen at bits 4-5 (B) and 29-30 (A).
   static constexpr uint32_t IDESC = (5u << 7) | (1u << 23) | ((128u >> 4) << 24);
   static_assert(NSTAGE >= 2 && SMEM <= 232448 && TMEM_COLS * CTAS <= 512, "budgets");
+  static_assert(tmem_allowed(SMEM) >= TMEM_COLS, "TMEM beside other kernels' CTAs");
   static_assert(NT % kChunk == 0 && NT <= 128 && (!SPLIT || NT <= 32), "tokens of a tile");
 };
 
@@ -835,6 +836,7 @@ struct PairCfg {
   static constexpr uint32_t IDESC = (5u << 7) | (1u << 23) | ((256u >> 4) << 24);
   static_assert(NBUF * NA * NT + SF_RING * SF_COLS <= 512 && SMEM <= 232448 && TOK_TILE % 1024 == 0,
                 "budgets");
+  static_assert(tmem_allowed(SMEM) >= 512, "TMEM beside other kernels' CTAs");
 };
 
 template <int MODE>
