@@ -855,6 +855,9 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
   uint64_t* done = acc_empty + 2;
   uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(slot + 1);
+  volatile int* issued = reinterpret_cast<volatile int*>(slot + 2);  // [0] warp 0, [1] warp 2
+  // What the other CTA leaves here at its end: whether it gave up, and its `issued`.
+  volatile int* other = reinterpret_cast<volatile int*>(slot + 4);  // [3]
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = (int)ptx::cluster_rank();
@@ -880,6 +883,8 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
     ptx::mbar_init(done, 1);
     ptx::fence_barrier_init();
     *abort_flag = 0;
+    issued[0] = issued[1] = 0;
+    other[0] = other[1] = other[2] = 0;
   }
   if (warp == 1) {
     ptx::tmem_alloc_pair(slot, 512);
@@ -918,6 +923,10 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
   const uint32_t even_full = ptx::map_shared_rank(ptx::smem_u32(full), 0);
   const uint32_t even_acc = ptx::map_shared_rank(ptx::smem_u32(acc_empty), 0);
 
+  // Bytes of one CTA's copies of a stage of a tile.
+  auto boxes_of = [&](const Tile& t) { return ((t.count + 15) / 16 * 8 + C::BOX_ROWS - 1) / C::BOX_ROWS; };
+  auto bytes_of = [&](const Tile& t) { return (uint32_t)(NA * kBlockBytes + boxes_of(t) * C::BOX_ROWS * 128); };
+
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (__all_sync(0xffffffffu,
                    !*abort_flag && ptx::mbar_wait_hint(bar, parity, p.wait_ns, kHintNs)))
@@ -935,8 +944,8 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
     for (int u = u_first; u < units && ok; u += u_step) {
       const Tile t = tile_of(u);
       const int half = (t.count + 15) / 16 * 8;  // tokens held by each CTA
-      const int boxes = (half + C::BOX_ROWS - 1) / C::BOX_ROWS;
-      const uint32_t bytes = 2u * (uint32_t)(NA * kBlockBytes + boxes * C::BOX_ROWS * 128);
+      const int boxes = boxes_of(t);
+      const uint32_t bytes = 2u * bytes_of(t);
       const int rb = min(block_of(u), p.NB - 1);
       const uint64_t keep = MODE != kLinear && t.pairs ? once : ptx::policy_evict_normal();
       int blk[NA];
@@ -967,6 +976,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
         __syncwarp();
       }
     }
+    if (lane == 0) issued[0] = it;
   } else if (warp == 2) {
     // ------------------------------------------------------- token scales
     constexpr int ROWS = (NT + 31) / 32;
@@ -1007,6 +1017,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
       }
       now = then;
     }
+    if (lane == 0) issued[1] = it;
   } else if (warp == 1 && rank == 0) {
     // ----------------------------------------------------------------- MMA
     int it = 0, n = 0;
@@ -1099,17 +1110,39 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
     }
   }
   __syncthreads();
-  if (*abort_flag) {
-    // What the even CTA issued completes; copies still in flight, the other CTA's
-    // too, land within this millisecond (they take a few microseconds).
-    if (threadIdx.x == 0) {
-      if (rank == 0) ptx::mbar_wait(done, 0, kDrainNs);
-      const uint64_t t0 = ptx::globaltimer();
-      while (ptx::globaltimer() - t0 < 1000000ull) __nanosleep(1000);
-    }
-    __syncthreads();
+  if (threadIdx.x == 0) {
+    const int left[3] = {*abort_flag, issued[0], issued[1]};
+    for (int i = 0; i < 3; ++i)
+      ptx::st_shared_cluster_u32(
+          ptx::map_shared_rank(ptx::smem_u32(const_cast<int*>(other + i)), (uint32_t)(rank ^ 1)),
+          (uint32_t)left[i]);
   }
   ptx::cluster_sync();  // neither CTA leaves while the other may still use it
+  if (*abort_flag || other[0]) {  // (both CTAs alike)
+    // MMAs and copies in flight, all of which the even CTA's barriers count, end before TMEM
+    // and shared memory are given up: raise each issued stage's missing arrivals and
+    // bytes, then wait for its phase.
+    if (rank == 0 && warp == 0) {
+      const int i0 = issued[0], i2 = issued[1], o0 = other[1], o2 = other[2];
+      const int last = max(max(i0, i2), max(o0, o2));
+      ptx::mbar_wait(done, 0, kDrainNs);
+      for (int i = min(min(i0, i2), min(o0, o2)); i < last; ++i) {
+        const uint32_t bytes = bytes_of(tile_of(u_first + i / nk * u_step));
+        uint64_t* bar = &full[i % NSTAGE];
+        if (lane == 0) {
+          if (i >= i0 && i < o0) ptx::mbar_arrive_expect_tx(bar, bytes);
+          if (i >= i0 && i >= o0) ptx::mbar_arrive(bar);
+          if (i < i0 && i >= o0) ptx::mbar_complete_tx(bar, bytes);
+          if (i >= i2) ptx::mbar_arrive(bar);
+          if (i >= o2) ptx::mbar_arrive(bar);
+        }
+        __syncwarp();
+      }
+      for (int i = max(0, last - NSTAGE); i < last; ++i)
+        ptx::mbar_wait(&full[i % NSTAGE], (uint32_t)(i / NSTAGE) & 1u, kDrainNs);
+    }
+    ptx::cluster_sync();
+  }
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem, 512);
