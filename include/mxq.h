@@ -459,7 +459,8 @@ int mxq_add_rms_norm(const void* x_bf16, const void* residual_bf16, void* residu
  *
  * Ties go to the lowest index.  Without a bias, experts are ordered by their
  * logits; with one by c, and groups by their values, both compared as 64-bit
- * sums of 64-bit scores.
+ * sums of 64-bit scores.  Weights are within 2^-18 of those of 64-bit scores,
+ * but that scores below 2^-126 may count as zero.
  * 1 <= E <= 1024.  T == 0 is a no-op.  T >= 2^31 returns MXQ_ERR_UNSUPPORTED.
  */
 int mxq_route(const void* logits, int32_t logits_dtype, int64_t T, int32_t E, const float* bias,

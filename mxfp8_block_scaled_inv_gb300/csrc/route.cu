@@ -27,12 +27,14 @@
 // as long as thousands of others.  Without a bias the experts are ordered by their
 // logits, which is exact.
 //
-// Bound by instructions: 1020 for a row of 256 experts with bias and groups (sigmoids
-// 7 % of the time, groups 18, nine picks 20), 55 % of the issue slots on cold caches.
-// 8192 rows 13.2 us (1.3 us of memory; with a search through the lane's experts for
-// each pick 21; with whole rows wherever groups are near 18 at the time), 65536 rows 71;
-// without bias and groups 9.5; one row 3.4 us, of which launch and one trip to memory
-// are 2.
+// Bound by what one warp does in a row: 1030 instructions for a row of 256 experts with
+// bias and groups (sigmoids 7 % of the time, groups 18, nine picks 20), one behind the
+// other where picks and ranks go by shuffles; some 57 % of the issue slots are used on cold
+// caches, with the 32 warps of an SM that 64 registers leave.  8192 rows 14.5 us (1.3 us of
+// memory), without groups 10.5, without bias and groups 9.0; BF16 logits whose scores tie
+// 10.0; one row 3.0 us, of which launch and one trip to memory are 2.  What goes to whole
+// rows in 64 bits shows: 8192 rows of BF16 logits around 10 with equal biases, some of
+// which have more than 32 sigmoids next to 1, 140 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

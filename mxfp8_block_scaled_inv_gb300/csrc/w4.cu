@@ -36,10 +36,10 @@
 //            Stores of a warp are contiguous along the rows; the abs-max of a
 //            scale group (128 rows of a token) is a warp-wide maximum and an
 //            exchange between the group's four warps.  (By way of shared memory, a lane
-//            for eight rows: 4096 tokens over 64 experts 530 us, so 435.)
+//            for eight rows, a call of 4096 tokens over 64 experts took a fifth longer.)
 // Roles and operands are uniform to the compiler (a warp's role is broadcast, one
 // elected lane issues): a warp that issues a copy or an MMA behind a lane's test
-// spends its time moving operands (64 tokens over 128 experts 177 us, so 132).
+// spends its time moving operands (64 tokens over 128 experts took a third longer).
 // Three forms:
 //   split      few units: one unit for each cluster of up to 8 CTAs, which share
 //              its K range.  Each CTA owns some of the tokens, receives the partial
@@ -64,12 +64,14 @@
 //   64 tokens, 128 experts      127 us (0.98): HBM
 //   1 token, 8 of 128           20 us (0.38): two kernels of 35 and 18 MB, each with the
 //                               latencies of the first case
-//   4096 tokens, 64 experts     323 us (0.51): gate and up 147 us (tensor pipe 64 %
+//   1024 tokens, 128 experts    232 us (0.55); over 64 145 (0.45): weights of an expert read
+//                               for tiles of a few dozen rows, results written and read
+//   4096 tokens, 64 experts     351 us (0.47): gate and up 143 us (tensor pipe 62 %
 //                               active; one accumulator, so that the epilogue's fetches
-//                               wait for the products and the other way round; without
-//                               any arithmetic or store in it 18 less), down 103 (copies
-//                               from L2 and 16-bit stores at once), the sum 46 and the
-//                               rows 18 (both memory), the plan 9, each on cold caches
+//                               wait for the products and the other way round), down 116
+//                               (copies from L2 and 402 MB of results at once), the sum 63
+//                               and the rows 19 (both memory), the plan 11, each on cold
+//                               caches
 //
 // Every wait is bounded in wall time; on expiry the kernel sets a watchdog bit,
 // stops issuing, waits for its own copies and MMAs, frees TMEM and returns.
@@ -294,7 +296,7 @@ __device__ __forceinline__ void finish_chunk(const W4Args& p, float (&v)[NA][kCh
       if (q == 0 && lane < live && rb < p.NG) p.out_sf[(size_t)(row + lane) * p.NG + rb] = (uint8_t)sb;
     }
     // Four neighbouring lanes swap the codes of four tokens, so that each stores four
-    // rows of one (64 tokens over 128 experts 127.5 us, with single bytes 128.5).
+    // rows of one (64 tokens over 128 experts 1 us less than with single bytes).
     const int tok = lane & 3;
     const uint32_t pick2 = lane & 2 ? 0x3276u : 0x5410u, pick1 = lane & 1 ? 0x3715u : 0x6240u;
     uint8_t* o = static_cast<uint8_t*>(p.out) + (size_t)(row + tok) * p.N + (n - tok);
@@ -360,7 +362,7 @@ __device__ __forceinline__ void finish_token(const W4Args& p, const float (&v)[N
 // for each cluster and one of the token's experts (or, of few, a part of one's K
 // range) for each CTA, and adds the experts' sums as a split K adds its parts: no
 // results of single experts, and no kernel to add them.  One token over 8 of 128
-// experts, 4096 x 1024: 20 us, with plan, results and sum 30.  SMALL == 2: the down
+// experts, 4096 x 1024: 20 us, with plan, results and sum half as long again.  SMALL == 2: the down
 // product with four CTAs to an SM, of two stages each instead of five, for grids
 // that fill more than two: 2 tokens over 8 of 128 (512 CTAs) 30.5 us against 34,
 // one over 2 of 8, 4096 x 14336 (256 CTAs of 28 stages) 52 against 45.5.
@@ -506,9 +508,9 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT, SMALL>::THREADS, (Cfg<MOD
   if (warp == 0) {
     // ------------------------------------------------------------- copies
     // Weights that no other tile reads make way in L2 for what is read again: the rows,
-    // the activation between the products, the results (64 tokens over 128 experts
-    // 132.3 -> 128.5 us, 1024 over 64 150 -> 143; with every expert's weights marked so, 4096
-    // tokens, two tiles each, 337 -> 343).
+    // the activation between the products, the results (64 tokens over 128 experts 3 %
+    // less, 1024 over 64 5 %; with every expert's weights marked so, 4096 tokens, two tiles
+    // each, take 2 % more).
     constexpr bool PLANNED = MODE != kLinear && SMALL == 0;
     const uint64_t once = ptx::policy_evict_first();
     int it = 0;
@@ -803,14 +805,14 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, SPLIT, SMALL>::THREADS, (Cfg<MOD
 // streaming form (128 bytes a cycle: a stage of 240 tokens writes 46 KB and the
 // MMAs read 46 KB, 720 cycles where the products take 480; measured 712), and a
 // pair writes and reads each token once for both CTAs (30 + 31 KB): 8192 x 4096 x
-// 4096 99 us in the streaming form, 79 here; 4096 tokens over 64 experts 363 and 343.
+// 4096 99 us in the streaming form, 79 here; 4096 tokens over 64 experts 6 % less.
 // Roles and epilogue are those of the streaming form, with these differences: the even
 // CTA issues the MMAs and scale copies for both; the odd CTA's copies and scale
 // words count on the even CTA's barriers; stages and accumulators are handed
 // back to, and released by, both.  With an odd number of row blocks the last
-// pair's odd CTA repeats the last block and stores nothing.  Three epilogue groups:
-// 343 us; two 349, four 350, five 355 (fewer registers each); fetching a chunk ahead of
-// its arithmetic: no faster.
+// pair's odd CTA repeats the last block and stores nothing.  Three epilogue groups: with
+// two or four a call of 4096 tokens takes 2 % longer, with five 3 % (fewer registers each);
+// fetching a chunk ahead of its arithmetic: no faster.
 template <int MODE>
 struct PairCfg {
   static constexpr int NA = MODE == kGateUp ? 2 : 1;
@@ -1266,9 +1268,10 @@ __global__ void __launch_bounds__(kPlanThreads) w4_plan_kernel(const int32_t* id
 
 // The activation rows laid out by expert, for the plain copies of large tiles: every
 // 128 weight rows read a tile's tokens anew, and a copy by index moves four rows (in
-// 44 ns) where a plain one moves a box of them: gate and up of 4096 tokens over 64 experts
-// 562 us by index in tiles of 128; 147 with rows laid out, which takes 18 (20 where each place fetched its row anew).  A
-// warp reads 2 KB of a token's row once and writes it to each of the row's places.
+// 44 ns) where a plain one moves a box of them: with tiles of 128 tokens by index a call of
+// 4096 tokens over 64 experts took half as long again as with rows laid out, which takes
+// 19 us of it.  A warp reads 2 KB of a token's row once and writes it to each of the row's
+// places.
 constexpr int kRowWarps = 8;
 constexpr int kRowChunks = 128;  // of 16 bytes, of a warp
 
@@ -1622,7 +1625,8 @@ namespace {
 bool small_call(int64_t R, int k) { return R <= kSmallPairs && k <= kSmallChoices; }
 // Most tokens of a tile, by the rows that an expert gets on average: above that
 // some experts take two tiles, which read their weights twice (from L2).  128 experts,
-// 8 choices, 4096 x 1024, us, with tiles of 16 / 32 / 64 / 128 / 240:
+// 8 choices, 4096 x 1024, us, with tiles of 16 / 32 / 64 / 128 / 240 (taken with results of
+// 16 bits; FP32 ones add nothing at 4 rows, 2 us at 12 to 40 and 11 at 64, whatever the tile):
 //   rows an expert on average
 //    4    128 / 127 / 134 / 159 / 154      24   279 / 212 / 179 / 202 / 198
 //    5    144 / 135 / 142 / 170 / 163      40   406 / 289 / 206 / 216 / 210
